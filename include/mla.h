@@ -320,6 +320,108 @@ int mla_rope_append(const void* c_kv, const void* k_pe, const int32_t* pos, cons
                     int32_t n, float freq_base, float freq_scale, void* kv, int8_t* kv_q,
                     uint16_t* kv_d, int64_t ld_d, int64_t n_rows, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged latent cache
+ * ---------------------------------------------------------------------------
+ * A cache of pages shared by a batch of sequences: position p of sequence b is
+ * row p % page_size of page block_table[b][p / page_size].  The entry points
+ * below write it, read it back, and attend over it for batches in which each
+ * sequence brings any number of new tokens: a single one (decode), a chunk of
+ * a prompt, or none.  They are build choices for serving; the pages the rest
+ * of this header cites describe one contiguous cache per sequence.
+ *
+ * Row types:
+ *   MLA_PAGE_F16   576 fp16 values, latent 0..511 and RoPE key 512..575 (1152
+ *                  bytes).  fp16 is the type the tensor-core products take, so
+ *                  a page goes to them as it is; a bf16 latent becomes fp16
+ *                  exactly inside fp16's normal range.
+ *   MLA_PAGE_E4M3  656 bytes: 512 e4m3 codes (latent), then 64 fp16 values
+ *                  (RoPE key), then 16 scale bytes.  Scale byte s of block i
+ *                  (codes 32 i .. 32 i + 31) stands for 2^(s - 127): the
+ *                  smallest power of two in [2^-15, 2^7] with amax <= 448 x
+ *                  scale.  code = e4m3(x / scale), to nearest even; the value
+ *                  code x scale is exact in fp16.  Scale bytes outside
+ *                  [112, 134] and NaN codes are never written and not defined.
+ * Pages: device, [n_pages][page_size] rows, 16-byte aligned; page_size a power
+ * of two in [16, 4096]; n_pages x page_size < 2^31 - 4096.
+ * block_table: device int32, row b at block_table + b * table_stride; the
+ * first max_pages entries of a row may be read (table_stride >= max_pages when
+ * B > 1).  Only entries of pages that hold a row the call needs are used; the
+ * others may hold anything.
+ *
+ * Batches: B sequences (at most 65535) in one token array of T rows.  Sequence
+ * b's new tokens are rows cu[b] .. cu[b + 1] - 1 (cu: device int32 [B + 1], not
+ * decreasing); seq_len[b] (device int32) counts its cache rows INCLUDING the
+ * new tokens, which are its last ones: token i of n sits at position
+ * seq_len[b] - n + i.  Rows of the token array outside [cu[0], cu[B]) are
+ * padding: not read, and their outputs stay as they were.  A sequence whose
+ * new tokens leave [0, T), number more than seq_len[b], or whose seq_len[b]
+ * exceeds max_pages x page_size is skipped and recorded as MLA_ERR_INVALID_ARG
+ * in the device error word; so is a needed table entry outside [0, n_pages)
+ * (see each call).  The others are computed as usual.  These arrays are read
+ * on the device only, so a captured call follows their contents.              */
+typedef enum mla_page_type { MLA_PAGE_F16 = 0, MLA_PAGE_E4M3 = 1 } mla_page_type;
+
+typedef struct mla_paged_cache {
+  void* pages;                 /* device, rows of `type`                       */
+  const int32_t* block_table;  /* device int32 [B][table_stride]               */
+  int64_t table_stride;        /* elements between table rows                  */
+  int32_t max_pages;           /* entries of a table row that may be read      */
+  int32_t n_pages;
+  int32_t page_size;           /* rows per page: a power of two in [16, 4096]  */
+  int32_t type;                /* mla_page_type                                */
+} mla_paged_cache;
+
+/* Write the batch's new tokens into their pages (quantising them for
+ * MLA_PAGE_E4M3): row of token j <- [c_kv[j] | RoPE(k_pe[j], position)], RoPE
+ * as in mla_rope_append.
+ * c_kv device bf16 [T][512]; k_pe device bf16 [T][64] (not yet rotated).
+ * A token whose table entry is bad is skipped and recorded.  Values the row
+ * type cannot hold record MLA_ERR_RANGE: latents past fp16 (MLA_PAGE_F16) or
+ * past 57344 = 448 x 2^7 in magnitude (MLA_PAGE_E4M3; stored as the largest),
+ * RoPE values past fp16.  Two tokens of one call must not name the same row.
+ * freq_base, freq_scale and host errors as in mla_rope_append.                */
+int mla_paged_append(const mla_paged_cache* cache, const void* c_kv, const void* k_pe,
+                     const int32_t* cu_new, const int32_t* seq_len, int32_t B, int32_t T,
+                     float freq_base, float freq_scale, void* stream);
+
+/* Read rows back into the flat layout of this header (the rows a flat prefill
+ * or a copy to another cache takes): out row cu_rows[b] + i <- the values of
+ * position row0[b] + i of sequence b, for cu_rows[b] + i < cu_rows[b + 1].
+ * row0 device int32 [B] or NULL (zero); cu_rows device int32 [B + 1];
+ * out device bf16 [R][576], or fp16 with out_f16 != 0 (then exact).
+ * A row whose position is outside the table row, or whose table entry is bad,
+ * is left as it was and recorded.                                             */
+int mla_paged_gather(const mla_paged_cache* cache, const int32_t* row0, const int32_t* cu_rows,
+                     int32_t B, int32_t R, void* out, int32_t out_f16, void* stream);
+
+/* Bytes of device workspace mla_attn_paged needs on the current device: the
+ * partial results of work split over the keys.  Depends on neither the batch
+ * nor the lengths.  Returns 0 for invalid dims.                               */
+size_t mla_paged_workspace_size(const mla_dims* dims);
+
+/* Attention of the batch's new tokens over their pages (steps 2-4 of the
+ * path, as mla_attn_prefill and mla_attn_decode): for a token at position p
+ *   s[j] = scale * (q_pe . k_pe[j] + q_lat . c_kv[j])
+ *   key j visible iff j <= p and (window == 0 or j > p - window or j < n_sink)
+ *   o_lat = sum_j softmax_j(s[j]) * c_kv[j]
+ * window > 0 keeps the last `window` positions (the token's own among them)
+ * and the first n_sink (attention sinks); window == 0 keeps all.
+ * q_lat device fp16 [T][H][512]; q_pe device bf16 [T][H][64] (rotated);
+ * o_lat device fp16 [T][H][512].
+ * workspace device, ws_bytes >= mla_paged_workspace_size(dims): contents need
+ * not be kept between calls; calls that may overlap on the GPU need one each.
+ * Visible rows must hold finite values; rows that no new token of the call
+ * sees may hold anything, and a page that holds only such rows needs no valid
+ * table entry.  A needed table entry outside [0, n_pages) is recorded as
+ * MLA_ERR_INVALID_ARG and leaves that sequence's outputs undefined.
+ * The order of the sums depends on the arguments and the batch alone: the same
+ * call gives the same bits.                                                   */
+int mla_attn_paged(const mla_dims* dims, const void* q_lat, const void* q_pe,
+                   const mla_paged_cache* cache, const int32_t* cu_q, const int32_t* seq_len,
+                   int32_t B, int32_t T, int32_t window, int32_t n_sink, void* workspace,
+                   size_t ws_bytes, void* o_lat, void* stream);
+
 /* Synchronise `stream`, then return and clear the current device's error
  * word: MLA_OK, or the first device-side error recorded since the last call
  * (MLA_ERR_TIMEOUT from a bounded wait, MLA_ERR_INVALID_ARG from the slot

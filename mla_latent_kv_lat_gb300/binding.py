@@ -19,6 +19,8 @@ from . import build as _build
 
 KV_LORA_RANK, QK_ROPE, QK_NOPE, V_HEAD, ROW = 512, 64, 128, 128, 576
 Q8_BLOCKS = 18
+ROW_E4M3 = 656                    # bytes of a paged e4m3 row: 512 codes, 64 fp16, 16 scales
+PAGE_F16, PAGE_E4M3 = 0, 1
 
 STATUS = {0: "MLA_OK", -1: "MLA_ERR_INVALID_ARG", -2: "MLA_ERR_UNSUPPORTED", -3: "MLA_ERR_MISALIGNED",
           -4: "MLA_ERR_WORKSPACE", -5: "MLA_ERR_CUDA", -6: "MLA_ERR_TIMEOUT", -7: "MLA_ERR_RANGE"}
@@ -35,6 +37,12 @@ class MLADims(ctypes.Structure):
                 ("qk_nope", ctypes.c_int32), ("v_head", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class MLAPagedCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("type", ctypes.c_int32)]
+
+
 def make_dims(n_head: int, scale: Optional[float] = None) -> MLADims:
     if scale is None:
         scale = 1.0 / math.sqrt(QK_NOPE + QK_ROPE)
@@ -44,6 +52,7 @@ def make_dims(n_head: int, scale: Optional[float] = None) -> MLADims:
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _D = ctypes.POINTER(MLADims)
+_C = ctypes.POINTER(MLAPagedCache)
 
 _SIGS = {
     "mla_absorb_q": ([_D, _P, _P, _P, _I32, _P], ctypes.c_int),
@@ -66,6 +75,10 @@ _SIGS = {
     "mla_quantize_q8_0": ([_P, _P, _P, _I64, _I64, _P], ctypes.c_int),
     "mla_rope_append": ([_P, _P, _P, _P, _I32, ctypes.c_float, ctypes.c_float, _P, _P, _P, _I64, _I64, _P],
                         ctypes.c_int),
+    "mla_paged_append": ([_C, _P, _P, _P, _P, _I32, _I32, ctypes.c_float, ctypes.c_float, _P], ctypes.c_int),
+    "mla_paged_gather": ([_C, _P, _P, _I32, _I32, _P, _I32, _P], ctypes.c_int),
+    "mla_paged_workspace_size": ([_D], _SZ),
+    "mla_attn_paged": ([_D, _P, _P, _C, _P, _P, _I32, _I32, _I32, _I32, _P, _SZ, _P, _P], ctypes.c_int),
     "mla_get_device_error": ([_P], ctypes.c_int),
     "mla_selftest_wait_timeout": ([_I32, _P], ctypes.c_int),
     "mla_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -332,6 +345,96 @@ def mla_rope_append(c_kv, k_pe, pos, slot, kv=None, kv_q=None, kv_d=None, freq_b
         _need(pos, "pos", torch.int32, (n,)), _need(slot, "slot", torch.int64, (n,)), n, float(freq_base),
         float(freq_scale), kvp, kqp, kdp, ld_d, n_rows, _stream(stream))
     _check("mla_rope_append", st)
+
+
+def _paged(pages, block_table) -> MLAPagedCache:
+    """The C description of a paged cache: pages fp16 [n_pages, page_size, 576] or uint8 [n_pages, page_size, 656],
+    block_table int32 [B, max_pages] (rows may be further apart than max_pages)."""
+    if not isinstance(pages, torch.Tensor) or pages.dtype not in (torch.float16, torch.uint8):
+        raise TypeError("pages must be a torch.float16 or torch.uint8 tensor")
+    f16 = pages.dtype == torch.float16
+    if pages.dim() != 3 or pages.shape[2] != (ROW if f16 else ROW_E4M3):
+        raise ValueError(f"pages must have shape (n_pages, page_size, {ROW if f16 else ROW_E4M3}), got "
+                         f"{tuple(pages.shape)}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32:
+        raise TypeError("block_table must be a torch.int32 tensor")
+    if block_table.dim() != 2 or block_table.shape[0] < 1 or block_table.shape[1] < 1:
+        raise ValueError("block_table must have shape (B, max_pages)")
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table's rows must be contiguous")
+    if not block_table.is_cuda:
+        raise ValueError("block_table must be a CUDA tensor")
+    return MLAPagedCache(_need(pages, "pages", pages.dtype).value, block_table.data_ptr(), block_table.stride(0),
+                         block_table.shape[1], pages.shape[0], pages.shape[1], PAGE_F16 if f16 else PAGE_E4M3)
+
+
+def _one_device(**tensors):
+    """The CUDA device that all the given tensors (None skipped) share."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    return dev
+
+
+def mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base: float = 10000.0,
+                     freq_scale: float = 0.025, stream=None):
+    """New tokens' rows into their pages: token i of sequence b's n new ones (rows cu_new[b].. of c_kv, k_pe) is
+    written at position seq_len[b] - n + i, its RoPE part rotated by that position, in the pages' type."""
+    with torch.cuda.device(_one_device(c_kv=c_kv, k_pe=k_pe, pages=pages, block_table=block_table, cu_new=cu_new,
+                                       seq_len=seq_len)):
+        T, Bn = c_kv.shape[0], block_table.shape[0]
+        st = load_library().mla_paged_append(
+            ctypes.byref(_paged(pages, block_table)), _need(c_kv, "c_kv", torch.bfloat16, (T, KV_LORA_RANK)),
+            _need(k_pe, "k_pe", torch.bfloat16, (T, QK_ROPE)), _need(cu_new, "cu_new", torch.int32, (Bn + 1,)),
+            _need(seq_len, "seq_len", torch.int32, (Bn,)), Bn, T, float(freq_base), float(freq_scale),
+            _stream(stream))
+        _check("mla_paged_append", st)
+
+
+def mla_paged_gather(pages, block_table, row0, cu_rows, out, stream=None):
+    """out [R, 576] (bf16 or fp16): rows cu_rows[b].. <- positions row0[b].. of sequence b (row0 None: from 0)."""
+    with torch.cuda.device(_one_device(pages=pages, block_table=block_table, row0=row0, cu_rows=cu_rows, out=out)):
+        R, Bn = out.shape[0], block_table.shape[0]
+        if out.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"out must be torch.bfloat16 or torch.float16, got {out.dtype}")
+        st = load_library().mla_paged_gather(
+            ctypes.byref(_paged(pages, block_table)),
+            _need(row0, "row0", torch.int32, (Bn,)) if row0 is not None else None,
+            _need(cu_rows, "cu_rows", torch.int32, (Bn + 1,)), Bn, R, _need(out, "out", out.dtype, (R, ROW)),
+            int(out.dtype == torch.float16), _stream(stream))
+        _check("mla_paged_gather", st)
+
+
+def mla_paged_workspace_size(n_head: int, scale=None) -> int:
+    d = make_dims(n_head, scale)
+    return int(load_library().mla_paged_workspace_size(ctypes.byref(d)))
+
+
+def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window: int = 0, n_sink: int = 0,
+                   workspace=None, scale=None, stream=None):
+    """o_lat [T, H, 512]: attention of the batch's new tokens over their pages (one token a sequence or a chunk);
+    window > 0 keeps each token's last ``window`` positions and the first ``n_sink``.  Without a workspace a fresh
+    one is taken from PyTorch's allocator."""
+    with torch.cuda.device(_one_device(q_lat=q_lat, q_pe=q_pe, pages=pages, block_table=block_table, cu_q=cu_q,
+                                       seq_len=seq_len, o_lat=o_lat, workspace=workspace)):
+        T, H, Bn = q_lat.shape[0], q_lat.shape[1], block_table.shape[0]
+        d = make_dims(H, scale)
+        if workspace is None:
+            workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)
+        st = load_library().mla_attn_paged(
+            ctypes.byref(d), _need(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK)),
+            _need(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE)), ctypes.byref(_paged(pages, block_table)),
+            _need(cu_q, "cu_q", torch.int32, (Bn + 1,)), _need(seq_len, "seq_len", torch.int32, (Bn,)), Bn, T,
+            int(window), int(n_sink), _need(workspace, "workspace", torch.uint8), workspace.numel(),
+            _need(o_lat, "o_lat", torch.float16, (T, H, KV_LORA_RANK)), _stream(stream))
+        _check("mla_attn_paged", st)
 
 
 def mla_get_device_error(stream=None) -> int:

@@ -9,6 +9,7 @@
 
 #include "append.cuh"
 #include "kernels.cuh"
+#include "paged.cuh"
 
 namespace mla {
 namespace {
@@ -184,6 +185,51 @@ int head_gemm(const mla_dims* dims, const void* a, const void* w, void* c, int32
   if (error_word(&err) != cudaSuccess) return MLA_ERR_CUDA;
   HeadGemmArgs g = {a, w, c, T, dims->n_head, K, N, f32 ? 1 : 0, (f32 || out_f16) ? 1 : 0, out_f16 ? 1 : 0};
   return to_status(launch_head_gemm_tc(g, err, kDefaultWaitUs, static_cast<cudaStream_t>(stream)));
+}
+
+// The paged cache a caller describes (include/mla.h), checked.
+int check_paged(const mla_paged_cache* c, int32_t B, PagedCache* out) {
+  if (c == nullptr || B < 1) return MLA_ERR_INVALID_ARG;
+  if (c->type != MLA_PAGE_F16 && c->type != MLA_PAGE_E4M3) return MLA_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return MLA_ERR_UNSUPPORTED;
+  if (c->pages == nullptr || c->block_table == nullptr) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(c->pages) || (reinterpret_cast<uintptr_t>(c->block_table) & 3u)) return MLA_ERR_MISALIGNED;
+  if (c->n_pages < 1 || c->max_pages < 1 || c->table_stride < 0) return MLA_ERR_INVALID_ARG;
+  if (B > 1 && c->table_stride < c->max_pages) return MLA_ERR_INVALID_ARG;
+  // rows are 32-bit coordinates of the bulk loads
+  if (static_cast<int64_t>(c->n_pages) * c->page_size > INT32_MAX - 4096) return MLA_ERR_UNSUPPORTED;
+  if (B > 65535) return MLA_ERR_UNSUPPORTED;
+  out->pages = static_cast<uint8_t*>(c->pages);
+  out->table = c->block_table;
+  out->table_stride = c->table_stride;
+  out->max_pages = c->max_pages;
+  out->n_pages = c->n_pages;
+  out->page_shift = 0;
+  while ((1 << out->page_shift) < c->page_size) ++out->page_shift;
+  out->e4m3 = c->type == MLA_PAGE_E4M3;
+  return MLA_OK;
+}
+
+// A device int32 array (4-byte aligned).
+int check_i32(std::initializer_list<const int32_t*> ps) {
+  for (const int32_t* p : ps) {
+    if (p == nullptr) return MLA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return MLA_ERR_MISALIGNED;
+  }
+  return MLA_OK;
+}
+
+// turns per position of pair i, frac(t_i) as 0.64 fixed point: two exact
+// 32-bit halves of the double's fraction
+void rope_turns(float freq_base, float freq_scale, uint64_t* turn) {
+  const double kTwoPi = 6.283185307179586;
+  for (int i = 0; i < kRope / 2; ++i) {
+    double t = static_cast<double>(freq_scale) * pow(static_cast<double>(freq_base), -2.0 * i / kRope) / kTwoPi;
+    t -= floor(t);
+    const double hi = floor(ldexp(t, 32));
+    const double lo = nearbyint(ldexp(ldexp(t, 32) - hi, 32));
+    turn[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo);
+  }
 }
 
 }  // namespace
@@ -369,17 +415,89 @@ int mla_rope_append(const void* c_kv, const void* k_pe, const int32_t* pos, cons
   a.ld_d = ld_d;
   a.n_rows = n_rows;
   if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
-  // turns per position of pair i, frac(t_i) as 0.64 fixed point: two exact
-  // 32-bit halves of the double's fraction
-  const double kTwoPi = 6.283185307179586;
-  for (int i = 0; i < kRope / 2; ++i) {
-    double t = static_cast<double>(freq_scale) * pow(static_cast<double>(freq_base), -2.0 * i / kRope) / kTwoPi;
-    t -= floor(t);
-    const double hi = floor(ldexp(t, 32));
-    const double lo = nearbyint(ldexp(ldexp(t, 32) - hi, 32));
-    a.turn[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo);
-  }
+  rope_turns(freq_base, freq_scale, a.turn);
   return to_status(launch_rope_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_paged_append(const mla_paged_cache* cache, const void* c_kv, const void* k_pe, const int32_t* cu_new,
+                     const int32_t* seq_len, int32_t B, int32_t T, float freq_base, float freq_scale, void* stream) {
+  PagedAppendArgs a = {};
+  int s = check_paged(cache, B, &a.c);
+  if (s != MLA_OK) return s;
+  s = check_ptrs({c_kv, k_pe});
+  if (s != MLA_OK) return s;
+  s = check_i32({cu_new, seq_len});
+  if (s != MLA_OK) return s;
+  if (T < 1) return MLA_ERR_INVALID_ARG;
+  if (!(freq_base > 1.f) || !(freq_scale > 0.f) || !isfinite(freq_base) || !isfinite(freq_scale))
+    return MLA_ERR_INVALID_ARG;
+  a.c_kv = static_cast<const uint16_t*>(c_kv);
+  a.k_pe = static_cast<const uint16_t*>(k_pe);
+  a.cu = cu_new;
+  a.seq_len = seq_len;
+  a.B = B;
+  a.T = T;
+  if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
+  rope_turns(freq_base, freq_scale, a.turn);
+  return to_status(launch_paged_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_paged_gather(const mla_paged_cache* cache, const int32_t* row0, const int32_t* cu_rows, int32_t B, int32_t R,
+                     void* out, int32_t out_f16, void* stream) {
+  PagedGatherArgs a = {};
+  int s = check_paged(cache, B, &a.c);
+  if (s != MLA_OK) return s;
+  s = check_ptrs({out});
+  if (s != MLA_OK) return s;
+  s = check_i32({cu_rows});
+  if (s != MLA_OK) return s;
+  if (row0 != nullptr && (reinterpret_cast<uintptr_t>(row0) & 3u)) return MLA_ERR_MISALIGNED;
+  if (R < 1) return MLA_ERR_INVALID_ARG;
+  a.row0 = row0;
+  a.cu = cu_rows;
+  a.B = B;
+  a.R = R;
+  a.out = static_cast<uint16_t*>(out);
+  if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
+  return to_status(launch_paged_gather(a, out_f16 != 0, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_paged_workspace_size(const mla_dims* dims) {
+  if (check_dims(dims) != MLA_OK) return 0;
+  return paged_attn_workspace_bytes();
+}
+
+int mla_attn_paged(const mla_dims* dims, const void* q_lat, const void* q_pe, const mla_paged_cache* cache,
+                   const int32_t* cu_q, const int32_t* seq_len, int32_t B, int32_t T, int32_t window, int32_t n_sink,
+                   void* workspace, size_t ws_bytes, void* o_lat, void* stream) {
+  int s = check_dims(dims);
+  if (s != MLA_OK) return s;
+  PagedAttnArgs a = {};
+  s = check_paged(cache, B, &a.c);
+  if (s != MLA_OK) return s;
+  s = check_ptrs({q_lat, q_pe, o_lat});
+  if (s != MLA_OK) return s;
+  s = check_i32({cu_q, seq_len});
+  if (s != MLA_OK) return s;
+  if (T < 1 || window < 0 || n_sink < 0) return MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) * dims->n_head > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || ws_bytes < paged_attn_workspace_bytes()) return MLA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MLA_ERR_MISALIGNED;
+  a.q_lat = static_cast<const uint16_t*>(q_lat);
+  a.q_pe = static_cast<const uint16_t*>(q_pe);
+  a.cu = cu_q;
+  a.seq_len = seq_len;
+  a.B = B;
+  a.T = T;
+  a.H = dims->n_head;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.scale_log2 = dims->scale * kLog2eF;
+  a.o_lat = static_cast<uint16_t*>(o_lat);
+  a.workspace = workspace;
+  a.wait_us = kDefaultWaitUs;
+  if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
+  return to_status(launch_paged_attn(a, static_cast<cudaStream_t>(stream)));
 }
 
 int mla_get_device_error(void* stream) {

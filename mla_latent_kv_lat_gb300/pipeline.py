@@ -125,6 +125,47 @@ def mla_decode(q_nope, q_pe, wk_b, wv_b, seq_start, seq_len, max_len: int, *, kv
     return bufs
 
 
+def paged_pages(n_pages: int, page_size: int, e4m3: bool = False, device="cuda") -> torch.Tensor:
+    """The page pool of a paged cache: fp16 [n_pages, page_size, 576], or e4m3 rows as uint8 [.., 656]."""
+    if e4m3:
+        return torch.empty(n_pages, page_size, B.ROW_E4M3, dtype=torch.uint8, device=device)
+    return torch.empty(n_pages, page_size, B.ROW, dtype=torch.float16, device=device)
+
+
+@dataclass
+class PagedBuffers:
+    q_lat: torch.Tensor      # fp16 [T, H, 512]
+    o_lat: torch.Tensor      # fp16 [T, H, 512]
+    o: torch.Tensor          # fp32 [T, H, 128]
+    workspace: torch.Tensor  # uint8, mla_paged_workspace_size(H)
+
+
+def paged_buffers(T: int, H: int, device="cuda") -> PagedBuffers:
+    return PagedBuffers(
+        torch.empty(T, H, B.KV_LORA_RANK, dtype=torch.float16, device=device),
+        torch.zeros(T, H, B.KV_LORA_RANK, dtype=torch.float16, device=device),
+        torch.empty(T, H, B.V_HEAD, dtype=torch.float32, device=device),
+        torch.empty(B.mla_paged_workspace_size(H), dtype=torch.uint8, device=device))
+
+
+def mla_paged_step(q_nope, q_pe, c_kv, k_pe, wk_b, wv_b, pages, block_table, cu_q, seq_len, *, window: int = 0,
+                   n_sink: int = 0, freq_base: float = 10000.0, freq_scale: float = 0.025,
+                   bufs: Optional[PagedBuffers] = None, scale=None, stream=None) -> PagedBuffers:
+    """One step of a batch on a paged cache: the new tokens' rows into their pages, then absorb -> attention over
+    the pages -> late decompression.  A sequence may bring one token (decode), a chunk (prefill) or none; rows of
+    the token arrays behind the last sequence are padding (their ``o`` follows from what ``bufs.o_lat`` held)."""
+    T, H = q_nope.shape[0], q_nope.shape[1]
+    if bufs is None:
+        bufs = paged_buffers(T, H, q_nope.device)
+    B.mla_paged_append(c_kv, k_pe, pages, block_table, cu_q, seq_len, freq_base=freq_base, freq_scale=freq_scale,
+                       stream=stream)
+    B.mla_absorb_q(q_nope, wk_b, bufs.q_lat, scale=scale, stream=stream)
+    B.mla_attn_paged(bufs.q_lat, q_pe, pages, block_table, cu_q, seq_len, bufs.o_lat, window=window, n_sink=n_sink,
+                     workspace=bufs.workspace, scale=scale, stream=stream)
+    B.mla_late_decompress(bufs.o_lat, wv_b, bufs.o, scale=scale, stream=stream)
+    return bufs
+
+
 def mla_prefill_host(host: dict, q_pos0: int, dev: dict, bufs: PrefillBuffers, out_host: torch.Tensor,
                      stream=None) -> torch.Tensor:
     """Host-buffer prefill: copy each pinned host input into its device buffer,

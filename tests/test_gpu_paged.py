@@ -1,0 +1,355 @@
+"""The paged latent cache on the GPU: rows written and read back bit for bit against the oracle, and attention over
+pages (whole context, sliding window with sinks; one token a sequence, chunks, both mixed) against the 64-bit
+definition, with a bound per value that follows from the arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+import mla_latent_kv_lat_gb300 as mla
+from mla_latent_kv_lat_gb300 import pipeline as P
+from oracle import mla_oracle as O
+from oracle import paged_oracle as PO
+from tests.paged_util import SCALE, Batch, bf16
+
+pytestmark = pytest.mark.gpu
+
+INVALID, RANGE = -1, -7
+FB, FS = float(np.float32(10000.0)), float(np.float32(0.025))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from mla_latent_kv_lat_gb300 import build
+    build.build()
+    mla.load_library()
+    assert mla.mla_get_device_error() == 0
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x, np.int32), device="cuda")
+
+
+def run(b: Batch, d=None, out=None, **kw):
+    d = d or b.dev()
+    out = torch.full((b.T, b.H, 512), float("nan"), dtype=torch.float16, device="cuda") if out is None else out
+    mla.mla_attn_paged(d["q_lat"], d["q_pe"], d["pages"], d["block_table"], d["cu_q"], d["seq_len"], out,
+                       window=b.window, n_sink=b.n_sink, scale=SCALE, **kw)
+    return out
+
+
+def check(b: Batch, out):
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    got = out.float().cpu().numpy().astype(np.float64)
+    ref, tol = b.ref()
+    n = b.cu[-1]
+    assert np.isfinite(got[:n]).all()
+    off = np.abs(got[:n] - ref) / tol
+    assert off.max() <= 1.0, f"{off.max():.2f} of the bound at {np.unravel_index(off.argmax(), off.shape)}"
+    assert np.isnan(got[n:]).all()                      # rows behind the last sequence stay as they were
+
+
+# ---------------------------------------------------------------------------
+# writing and reading back
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("ps,news,lens,pad", [
+    (16, [1], [1], 0), (64, [1, 0, 3, 1], [700, 0, 3, 64], 2), (32, [130, 65, 1], [131, 1000, 33], 0),
+    (256, [255, 300], [5000, 300], 5)])
+def test_append_writes_rows_and_gather_reads_them(e4m3, ps, news, lens, pad):
+    b = Batch(3, e4m3, 16, ps, news, lens, pad=pad)
+    rng = np.random.default_rng(4)
+    c_kv = bf16(rng.standard_normal((b.T, 512)) * np.exp(rng.uniform(-12, 9, (b.T, 1))))
+    c_kv[0, :40] = 0.0                                   # a block of zeros and one that is half zero
+    k_pe = bf16(rng.standard_normal((b.T, 64)))
+    pages, table = b.pages_dev(), torch.from_numpy(b.table).cuda()
+    for s in range(b.B):                                 # every page of the sequence in the table
+        p = np.arange(0, b.lens[s], ps)
+        table[s, :len(p)] = torch.from_numpy((b.row_ids[s][p] // ps).astype(np.int32)).cuda()
+    mla.mla_paged_append(torch.from_numpy(c_kv).bfloat16().cuda(), torch.from_numpy(k_pe).bfloat16().cuda(), pages,
+                         table, i32(b.cu), i32(b.lens), freq_base=FB, freq_scale=FS)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    raw = pages.view(torch.uint8).reshape(b.raw.shape).cpu().numpy()
+    want = b.raw.copy()
+    for s in range(b.B):
+        lo, hi = b.cu[s], b.cu[s + 1]
+        pos = np.arange(b.lens[s] - b.news[s], b.lens[s])
+        slot = b.row_ids[s][pos]
+        rope = PO.rope_rows(k_pe[lo:hi], pos, FB, FS)
+        want[slot] = PO.pack_rows(c_kv[lo:hi], rope, e4m3)
+        o = 512 if e4m3 else 1024
+        got_rope = np.ascontiguousarray(raw[slot, o:o + 128]).view(np.float16).astype(np.float64)
+        # sine, cosine and the rotation in fp32 (a few 2^-24 of the pair's length), then one rounding to fp16
+        pair = np.repeat(np.hypot(k_pe[lo:hi, 0::2], k_pe[lo:hi, 1::2]), 2, axis=1)
+        assert (np.abs(got_rope - rope) <= 2.0 ** -11 * np.abs(rope) + 1e-6 * pair + 2.0 ** -25).all()
+        want[slot, o:o + 128] = raw[slot, o:o + 128]
+    assert np.array_equal(raw, want)                     # latents, codes, scales; no other byte touched
+    # read back: the new rows and up to 70 before them
+    back = [min(l, n + 70) for n, l in zip(b.news, b.lens)]
+    row0 = [l - k for l, k in zip(b.lens, back)]
+    cu_rows = np.concatenate([[0], np.cumsum(back)])
+    slots = np.concatenate([b.row_ids[s][row0[s]:] for s in range(b.B)]).astype(int)
+    vals = PO.row_values(want[slots], e4m3)
+    for dt in (torch.float16, torch.bfloat16):
+        out = torch.full((int(cu_rows[-1]) + 3, 576), 7.0, dtype=dt, device="cuda")
+        mla.mla_paged_gather(pages, table, i32(row0), i32(cu_rows), out)
+        torch.cuda.synchronize()
+        assert mla.mla_get_device_error() == 0
+        ref = torch.from_numpy(vals).to(torch.float32).to(dt)   # every row value is exact in fp32
+        assert torch.equal(torch.nan_to_num(out[:-3].cpu(), 9.0), torch.nan_to_num(ref, 9.0))
+        assert (out[-3:] == 7.0).all()
+
+
+def test_append_at_far_positions_and_gather_from_zero():
+    ps, L = 4096, 200001
+    n_pages = -(-L // ps)
+    pages = torch.zeros(n_pages, ps, 576, dtype=torch.float16, device="cuda")
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda").flip(0)[None].contiguous()
+    k_pe = bf16(np.random.default_rng(0).standard_normal((3, 64)))
+    mla.mla_paged_append(torch.ones(3, 512, dtype=torch.bfloat16, device="cuda"),
+                         torch.from_numpy(k_pe).bfloat16().cuda(), pages, table, i32([0, 3]), i32([L]))
+    out = torch.empty(L, 576, dtype=torch.float16, device="cuda")
+    mla.mla_paged_gather(pages, table, None, i32([0, L]), out)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    assert (out[:-3] == 0).all() and (out[-3:, :512] == 1).all()
+    ref = PO.rope_rows(k_pe, np.arange(L - 3, L), FB, FS)
+    assert np.abs(out[-3:, 512:].cpu().numpy() - ref).max() <= 2.0 ** -11 * np.abs(ref).max() + 1e-5
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_values_a_row_cannot_hold_are_reported(e4m3):
+    pages = P.paged_pages(1, 16, e4m3)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    c = torch.ones(1, 512, dtype=torch.bfloat16, device="cuda")
+    k = torch.ones(1, 64, dtype=torch.bfloat16, device="cuda")
+    call = lambda: mla.mla_paged_append(c, k, pages, table, i32([0, 1]), i32([1]))   # noqa: E731
+    call()
+    assert mla.mla_get_device_error() == 0
+    for bad in (1.0e5, float("inf"), float("nan")):
+        c[0, 100] = bad
+        call()
+        assert mla.mla_get_device_error() == RANGE
+        c[0, 100] = 57344.0                              # 448 * 2^7: the largest both types hold exactly
+        call()
+        assert mla.mla_get_device_error() == 0
+        k[0, 5] = bad
+        call()
+        assert mla.mla_get_device_error() == RANGE
+        k[0, 5] = 1.0
+
+
+def test_bad_sequences_and_pages_are_skipped_and_reported():
+    b = Batch(5, False, 16, 16, [2, 2, 2, 2], [40, 33, 20, 50])
+    c_kv = torch.ones(8, 512, dtype=torch.bfloat16, device="cuda")
+    k_pe = torch.ones(8, 64, dtype=torch.bfloat16, device="cuda")
+    d = b.dev()
+    for what in ("len", "neg", "page", "long"):
+        lens, table = i32(b.lens), d["block_table"].clone()
+        if what == "len":
+            lens[1] = 1                                  # two new tokens, one row
+        elif what == "neg":
+            lens[1] = -5
+        elif what == "long":
+            lens[1] = b.width * 16 + 1
+        else:
+            table[1, 2] = b.n_pages                      # positions 32.. of sequence 1
+        pages = d["pages"].clone()
+        mla.mla_paged_append(c_kv, k_pe, pages, table, i32(b.cu), lens)
+        assert mla.mla_get_device_error() == INVALID
+        flat = pages.reshape(-1, 576)
+        for s in (0, 2, 3):
+            rows = torch.from_numpy(b.row_ids[s][b.lens[s] - 2:b.lens[s]]).cuda()
+            assert (flat[rows, :512] == 1).all()
+        # position 31 of sequence 1 is on the page before the bad one
+        assert (flat[:, :512] == 1).all(1).sum() == (7 if what == "page" else 6)
+        out = torch.full((b.T, 16, 512), 7.0, dtype=torch.float16, device="cuda")
+        mla.mla_attn_paged(d["q_lat"], d["q_pe"], d["pages"], table, d["cu_q"], lens, out, scale=SCALE)
+        assert mla.mla_get_device_error() == INVALID
+        ref, tol = b.ref()
+        got = out.float().cpu().numpy()
+        for s in (0, 2, 3):
+            lo, hi = b.cu[s], b.cu[s + 1]
+            assert (np.abs(got[lo:hi] - ref[lo:hi]) <= tol[lo:hi]).all()
+        if what != "page":
+            assert (got[b.cu[1]:b.cu[2]] == 7.0).all()
+    cu = i32([0, 2, 4, 6, 9])                            # past the token array
+    out.fill_(7.0)
+    mla.mla_attn_paged(d["q_lat"], d["q_pe"], d["pages"], d["block_table"], cu, d["seq_len"], out, scale=SCALE)
+    assert mla.mla_get_device_error() == INVALID
+    assert (out[6:] == 7.0).all() and torch.isfinite(out[:6]).all() and (out[:6] != 7.0).any()
+    table = d["block_table"].clone()
+    table[0, 0] = -1
+    rows = torch.full((4, 576), 7.0, dtype=torch.float16, device="cuda")
+    mla.mla_paged_gather(d["pages"], table, i32([14, 0, 0, b.width * 16 - 1]), i32([0, 4, 4, 4, 4]), rows)
+    assert mla.mla_get_device_error() == INVALID         # rows 14, 15 are on the bad page
+    assert (rows[:2] == 7.0).all() and (rows[2:] != 7.0).any()
+    mla.mla_paged_gather(d["pages"], d["block_table"], i32([0, 0, 0, b.width * 16 - 1]), i32([0, 0, 0, 0, 2]), rows)
+    assert mla.mla_get_device_error() == INVALID
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+SHAPES = [                                               # heads, page, news, lens
+    (16, 16, [1], [1]), (16, 64, [1], [64]), (128, 64, [1], [65]), (48, 32, [1], [1000]),
+    (128, 16, [1, 1, 1], [17, 300, 2049]), (16, 64, [5], [5]), (16, 128, [64, 1, 0, 7], [64, 63, 9, 200]),
+    (80, 16, [33, 2], [40, 129]), (112, 64, [9, 1], [700, 513]), (32, 256, [130], [301]),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_attention_over_pages(shape, e4m3):
+    H, ps, news, lens = shape
+    b = Batch(11, e4m3, H, ps, news, lens, pad=2)
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (1, 1), (63, 0), (64, 4), (65, 64), (200, 70), (128, 1000)])
+def test_attention_in_a_window_with_sinks(window, n_sink, e4m3):
+    b = Batch(12, e4m3, 16, 16, [1, 40, 3, 0, 130], [500, 333, 3, 20, 701], window, n_sink)
+    check(b, run(b))
+    b = Batch(13, e4m3, 128, 64, [1, 2], [1000, 450], window, n_sink)
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_split_over_the_keys(e4m3):
+    b = Batch(14, e4m3, 16, 64, [1, 12], [20000, 9999])
+    check(b, run(b))
+    b = Batch(15, e4m3, 64, 16, [3], [12345], 6000, 20)
+    check(b, run(b))
+
+
+def test_sharp_and_flat_scores():
+    # nearly one key for each row; all keys alike (their mean); and all rows the same row
+    for kw in (dict(std=6.0), dict(std=1e-3), dict(same=True)):
+        b = Batch(16, False, 16, 64, [3, 1], [500, 1000], **kw)
+        if "std" in kw and kw["std"] > 1:
+            # scores reach ~60 in magnitude: fp32 sums of them move a probability by 2^-10 more
+            torch.cuda.synchronize()
+            ref, tol = b.ref()
+            got = run(b).float().cpu().numpy()
+            assert (np.abs(got - ref) <= 2 * tol).all()
+        else:
+            check(b, run(b))
+
+
+def test_strided_table_offsets_and_order_of_the_batch():
+    b = Batch(17, False, 32, 16, [4, 1, 20], [100, 77, 20])
+    d = b.dev()
+    wide = torch.full((b.B, b.width + 9), -7, dtype=torch.int32, device="cuda")
+    wide[:, :b.width] = d["block_table"]
+    want = run(b, d)
+    check(b, want)
+    d["block_table"] = wide[:, :b.width]
+    assert torch.equal(torch.nan_to_num(run(b, d)), torch.nan_to_num(want))
+    # two sequences on the same pages (a shared prefix)
+    d["block_table"] = d["block_table"][[0, 0, 2]].contiguous()
+    d["seq_len"][1] = 97
+    out = run(b, d)
+    ref, _, _ = PO.attend(np.concatenate([b.q_lat[4:5], b.q_pe[4:5]], -1).astype(np.float64), b.rows[0][:97], 96, 0, 0,
+                          SCALE)
+    assert np.abs(out[4].float().cpu().numpy() - ref[0]).max() <= 2.0 ** -9 * np.abs(ref).max()
+    assert mla.mla_get_device_error() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_same_call_same_bits_on_two_streams(e4m3):
+    b = Batch(18, e4m3, 128, 64, [1, 1, 5], [3000, 5000, 900])
+    d = b.dev()
+    first = run(b, d)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for s in streams:                                    # two calls at once, a workspace each
+        with torch.cuda.stream(s):
+            outs.append(run(b, d))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, first)
+    explicit = torch.empty_like(first)
+    run(b, d, explicit, stream=streams[0])
+    torch.cuda.synchronize()
+    assert torch.equal(explicit, first)
+    check(b, first)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_captured_step_follows_its_arrays(e4m3):
+    """One captured step (append, absorb, attention, decompression) replayed while sequences grow and swap."""
+    rng = np.random.default_rng(6)
+    H, ps, n_pages, B, T = 16, 16, 64, 3, 24
+    dev = lambda x: torch.from_numpy(np.asarray(x, np.float32)).bfloat16().cuda()    # noqa: E731
+    wk, wv = (bf16(rng.standard_normal((H, 128, 512)) / np.sqrt(128)), bf16(rng.standard_normal((H, 512, 128)) / np.sqrt(512)))
+    x = dict(q_nope=torch.zeros(T, H, 128, dtype=torch.bfloat16, device="cuda"),
+             q_pe=torch.zeros(T, H, 64, dtype=torch.bfloat16, device="cuda"),
+             c_kv=torch.zeros(T, 512, dtype=torch.bfloat16, device="cuda"),
+             k_pe=torch.zeros(T, 64, dtype=torch.bfloat16, device="cuda"))
+    cu, lens = i32([0, 20, 21, 24]), i32([20, 1, 3])
+    order = rng.permutation(n_pages).astype(np.int32)
+    table = torch.from_numpy(order[:60].reshape(3, 20).copy()).cuda()
+    pages = P.paged_pages(n_pages, ps, e4m3)
+    pages.zero_()
+    bufs = P.paged_buffers(T, H)
+    wkd, wvd = dev(wk), dev(wv)
+
+    def step():
+        P.mla_paged_step(x["q_nope"], x["q_pe"], x["c_kv"], x["k_pe"], wkd, wvd, pages, table, cu, lens, bufs=bufs,
+                         window=25, n_sink=2)
+
+    step()
+    torch.cuda.synchronize()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        step()
+    length, rows = [0, 0, 0], [np.zeros((0, 576)) for _ in range(3)]
+    for news in ([20, 1, 3], [1, 20, 0], [1, 1, 1], [3, 5, 16], [0, 0, 24]):
+        new = {k: bf16(rng.standard_normal(v.shape)) for k, v in x.items()}
+        for k in x:
+            x[k].copy_(dev(new[k]))
+        cun = np.concatenate([[0], np.cumsum(news)])
+        cu.copy_(i32(cun))
+        length = [l + n for l, n in zip(length, news)]
+        lens.copy_(i32(length))
+        g.replay()
+        torch.cuda.synchronize()
+        assert mla.mla_get_device_error() == 0
+        got = bufs.o.cpu().numpy()
+        for b in range(3):
+            lo, hi = cun[b], cun[b + 1]
+            pos = np.arange(length[b] - news[b], length[b])
+            raw = PO.pack_rows(new["c_kv"][lo:hi], PO.rope_rows(new["k_pe"][lo:hi], pos, FB, FS), e4m3)
+            rows[b] = np.concatenate([rows[b], PO.row_values(raw, e4m3)])
+            if news[b] == 0:
+                continue
+            ql = O.absorb_q(new["q_nope"][lo:hi], wk)
+            ol, _, _ = PO.attend(np.concatenate([ql, new["q_pe"][lo:hi]], -1).astype(np.float64), rows[b],
+                                 int(pos[0]), 25, 2, SCALE)
+            ref = O.late_decompress(ol, wv)
+            d = np.abs(got[lo:hi] - ref)
+            # q_lat, the probabilities and o_lat are rounded to fp16 on the way: 1e-3 in the mean
+            assert d.mean() <= 1.5e-3 * np.abs(ref).mean() and d.max() <= 1e-2 * np.abs(ref).max()
+        if cun[-1] == 2:
+            assert np.isfinite(got).all()
+
+
+def test_read_back_feeds_the_flat_prefill():
+    """A prefix in pages, read back as flat rows, gives the flat prefill the same answer as the pages give."""
+    b = Batch(19, False, 16, 64, [40], [200])
+    d = b.dev()
+    flat = torch.empty(200, 576, dtype=torch.bfloat16, device="cuda")
+    mla.mla_paged_gather(d["pages"], d["block_table"], None, i32([0, 200]), flat)
+    o = torch.empty(40, 16, 512, dtype=torch.float16, device="cuda")
+    mla.mla_attn_prefill(d["q_lat"], d["q_pe"], flat, 160, o, scale=SCALE)
+    p = run(b, d)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    a, c = o.float(), p.float()
+    assert (a - c).abs().mean() <= 2e-3 * c.abs().mean() and (a - c).abs().max() <= 1e-2 * c.abs().max()

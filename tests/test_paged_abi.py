@@ -1,0 +1,123 @@
+"""Refusals of the paged entry points, on the host (no GPU needed), and the oracle's row formats."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mla_latent_kv_lat_gb300 as mla
+from mla_latent_kv_lat_gb300 import binding, build
+from oracle import paged_oracle as PO
+from tests.paged_util import Batch
+
+P = ctypes.c_void_p
+GOOD, ODD, ODD4 = 0x100000, 0x100008, 0x100002       # never dereferenced: the checks fail first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return mla.load_library()
+
+
+def cache(**kw):
+    c = binding.MLAPagedCache(GOOD, GOOD, 8, 8, 100, 64, 0)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+BAD_CACHES = [(dict(pages=None), -1), (dict(pages=ODD), -3), (dict(block_table=None), -1), (dict(block_table=ODD4), -3),
+              (dict(table_stride=7), -1), (dict(table_stride=-1), -1), (dict(max_pages=0), -1), (dict(n_pages=0), -1),
+              (dict(page_size=8), -2), (dict(page_size=48), -2), (dict(page_size=8192), -2), (dict(type=2), -2),
+              (dict(type=-1), -2), (dict(n_pages=1 << 26, page_size=64), -2)]
+
+
+def test_bad_caches_are_refused(lib):
+    d = ctypes.byref(binding.make_dims(16))
+    ws = lib.mla_paged_workspace_size(d)
+    assert ws > 0
+    for kw, want in BAD_CACHES:
+        assert lib.mla_paged_append(cache(**kw), GOOD, GOOD, GOOD, GOOD, 2, 4, 1e4, 1.0, None) == want, kw
+        assert lib.mla_paged_gather(cache(**kw), None, GOOD, 2, 4, GOOD, 0, None) == want, kw
+        assert lib.mla_attn_paged(d, GOOD, GOOD, cache(**kw), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, GOOD, None) == want, kw
+    assert lib.mla_paged_append(None, GOOD, GOOD, GOOD, GOOD, 2, 4, 1e4, 1.0, None) == -1
+
+
+def test_bad_arguments_are_refused(lib):
+    ap, ga, at = lib.mla_paged_append, lib.mla_paged_gather, lib.mla_attn_paged
+    for a in ((None, GOOD, GOOD, GOOD, 2, 4, 1e4, 1.0), (GOOD, GOOD, None, GOOD, 2, 4, 1e4, 1.0),
+              (GOOD, GOOD, GOOD, None, 2, 4, 1e4, 1.0), (GOOD, GOOD, GOOD, GOOD, 0, 4, 1e4, 1.0),
+              (GOOD, GOOD, GOOD, GOOD, 2, 0, 1e4, 1.0), (GOOD, GOOD, GOOD, GOOD, 2, 4, 1.0, 1.0),
+              (GOOD, GOOD, GOOD, GOOD, 2, 4, 1e4, float("nan"))):
+        assert ap(cache(), *a, None) == -1
+    assert ap(cache(), ODD, GOOD, GOOD, GOOD, 2, 4, 1e4, 1.0, None) == -3
+    assert ap(cache(), GOOD, GOOD, ODD4, GOOD, 2, 4, 1e4, 1.0, None) == -3
+    assert ap(cache(table_stride=70000, max_pages=1), GOOD, GOOD, GOOD, GOOD, 65536, 4, 1e4, 1.0, None) == -2
+    assert ga(cache(), None, None, 2, 4, GOOD, 0, None) == -1
+    assert ga(cache(), ODD4, GOOD, 2, 4, GOOD, 0, None) == -3
+    assert ga(cache(), None, GOOD, 2, 4, ODD, 0, None) == -3
+    assert ga(cache(), None, GOOD, 2, 0, GOOD, 0, None) == -1
+    d = ctypes.byref(binding.make_dims(16))
+    ws = lib.mla_paged_workspace_size(d)
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, -1, 0, GOOD, ws, GOOD, None) == -1
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 8, -1, GOOD, ws, GOOD, None) == -1
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 0, 0, 0, GOOD, ws, GOOD, None) == -1
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 0, 4, 0, 0, GOOD, ws, GOOD, None) == -1
+    assert at(d, GOOD, None, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, GOOD, None) == -1
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, None, ws, GOOD, None) == -4
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws - 1, GOOD, None) == -4
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, ODD, ws, GOOD, None) == -3
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 1 << 28, 0, 0, GOOD, ws, GOOD, None) == -2
+    bad = binding.make_dims(24)
+    assert at(ctypes.byref(bad), GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, GOOD, None) == -2
+    assert lib.mla_paged_workspace_size(ctypes.byref(bad)) == 0
+
+
+def test_the_binding_refuses_what_the_library_cannot_see():
+    pages, table = torch.zeros(2, 16, 576, dtype=torch.float16), torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        mla.mla_paged_gather(pages, table, None, torch.zeros(2, dtype=torch.int32), torch.zeros(1, 576).half())
+    with pytest.raises(TypeError, match="float16 or torch.uint8"):
+        binding._paged(pages.float(), table)
+    with pytest.raises(ValueError, match="576"):
+        binding._paged(pages[..., :500], table)
+    with pytest.raises(ValueError, match="656"):
+        binding._paged(pages.view(torch.uint8), table)
+    with pytest.raises(TypeError, match="int32"):
+        binding._paged(pages, table.long())
+    with pytest.raises(ValueError, match="max_pages"):
+        binding._paged(pages, table[0])
+    with pytest.raises(ValueError, match="contiguous"):
+        binding._paged(pages, torch.zeros(4, 3, dtype=torch.int32).t())
+
+
+def test_oracle_rows():
+    v = PO.e4m3_values()
+    assert v[0x7E] == 448 and v[1] == 2.0 ** -9 and v[8] == 2.0 ** -6 and v[0x38] == 1.0 and v[0xB8] == -1.0
+    t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(np.nan_to_num(v, nan=9), np.nan_to_num(t, nan=9))
+    x = np.random.default_rng(0).uniform(-448, 448, 4000) * 2.0 ** -np.random.default_rng(1).integers(0, 17, 4000)
+    x = np.concatenate([x, v[:0x7F], (v[:0x7E] + v[1:0x7F]) / 2])       # values, and ties between them
+    assert np.array_equal(PO.e4m3_round(x), torch.from_numpy(x).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+    lat = np.random.default_rng(2).standard_normal((5, 512)) * np.exp(np.linspace(-14, 9, 5))[:, None]
+    raw = PO.pack_rows(lat, np.ones((5, 64)), True)
+    assert raw.shape == (5, 656)
+    back = PO.row_values(raw, True)
+    big = np.abs(lat.reshape(5, 16, 32)).max(-1).repeat(32, axis=1).reshape(5, 512)
+    # half a step of three mantissa bits, or of the smallest step under the block's scale
+    assert (np.abs(back[:, :512] - lat) <= np.maximum(2.0 ** -4 * np.abs(lat), 2.0 ** -25 + 2.0 ** -17 * big)).all()
+    assert (back[:, 512:] == 1).all()
+
+
+def test_oracle_attention_is_the_masked_softmax():
+    b = Batch(0, False, 16, 16, [3], [40], 9, 2)
+    o, _ = b.ref()
+    q = np.concatenate([b.q_lat, b.q_pe], -1).astype(np.float64)
+    for i in range(3):
+        p = 37 + i
+        j = np.arange(40)
+        s = (q[i] @ b.rows[0].T) * float(np.float32(1 / np.sqrt(192)))
+        s[:, (j > p) | ((j <= p - 9) & (j >= 2))] = -np.inf
+        w = np.exp(s - s.max(1, keepdims=True))
+        assert np.allclose(o[i], (w / w.sum(1, keepdims=True)) @ b.rows[0][:, :512], rtol=1e-12, atol=1e-12)

@@ -25,7 +25,10 @@ struct PagedCache {
   bool e4m3;
 
   MLA_DEVINL int64_t row_bytes() const { return e4m3 ? kRowE4m3 : kRowF16; }
-  MLA_DEVINL int64_t max_rows() const { return static_cast<int64_t>(max_pages) << page_shift; }
+  // Rows a table row can name; positions stay clear of 2^31 when they are rounded up to tiles.
+  MLA_DEVINL int64_t max_rows() const {
+    return min(static_cast<int64_t>(max_pages) << page_shift, static_cast<int64_t>(INT32_MAX - 4096));
+  }
   // Row of `pages` that holds position p (0 <= p < max_rows()) of sequence b,
   // or -1 if the table names no page of the cache there.
   MLA_DEVINL int64_t row_of(int b, int64_t p) const {
@@ -111,6 +114,30 @@ struct PagedAttnArgs {
   int* err;
   uint32_t wait_us;
 };
+
+// Two e4m3 codes (the low 16 bits of c) to two fp16 values (exact).
+MLA_DEVINL uint32_t e4m3x2_to_f16x2(uint32_t c) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(c));
+  return r;
+}
+
+// 2^(s - 127) for a scale byte s in [112, 134] as fp16 bits, in both halves.
+MLA_DEVINL uint32_t e4m3_scale_f16x2(uint32_t s) {
+  const uint32_t h = s > 112 ? (s - 112) << 10 : 0x0200u;   // 2^-15 is fp16-subnormal
+  return h | (h << 16);
+}
+
+MLA_DEVINL uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Four codes times the scale d (both halves): four fp16 values, exact.
+MLA_DEVINL void e4m3x4_to_f16x4(uint32_t c, uint32_t d, uint32_t& lo, uint32_t& hi) {
+  lo = mul_f16x2(e4m3x2_to_f16x2(c & 0xFFFFu), d);
+  hi = mul_f16x2(e4m3x2_to_f16x2(c >> 16), d);
+}
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, bool out_f16, cudaStream_t stream);

@@ -1,101 +1,1080 @@
-// Attention of a batch's new tokens over a paged latent cache.
+// Attention of a batch's new tokens over a paged latent cache, on the
+// 5th-generation tensor cores.
+//
+//   s[j] = scale * (q_lat . c_kv[j] + q_pe . k_pe[j]),  j visible to the token
+//   o_lat = sum_j softmax_j(s) c_kv[j]
+//
+// Rows are (token, head) pairs; a block is 128 consecutive rows of one
+// sequence, and its keys are walked in tiles of 64.  A CTA pair (a 2-CTA
+// cluster) works on one block at a time:
+//   * The 512-wide fp32 output of 128 rows fills a CTA's tensor memory, so the
+//     pair splits the latent dimension: CTA r holds latent columns [256 r, +256)
+//     and RoPE dimensions [32 r, +32) of queries and keys, and its 256 columns
+//     of the output.  Each CTA's score product is thus a partial sum over half
+//     the contraction, for all 128 rows.
+//   * The partial scores are reduced between the CTAs by rows: CTA r owns rows
+//     with (row / 16) % 2 == r.  Four sender warps pass the other CTA's 64 rows
+//     on to it in fp32 (st.async into distributed shared memory); four softmax
+//     warps add what arrives to their own half, so scores are full fp32 sums
+//     and each row's softmax is computed once in the pair.  P (fp16) of the
+//     owned rows is stored to both CTAs, with the factor by which the row's
+//     earlier output has to shrink if its running maximum grew.  (Exchanging
+//     all partial scores in fp16 and computing every softmax twice takes the
+//     same bytes on the wire, twice the exponentials, and rounds the scores.)
+//   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
+//   * fp16 pages come in by TMA as they are.  e4m3 pages are read, turned into
+//     fp16 (code x scale, exact) and stored in the same layout by producer
+//     warps.
+// Work split: a block costs its tiles plus `kPieceCost`; the costs of all
+// blocks form one run, which the clusters share evenly.  A cluster's piece that
+// is a whole block writes o_lat; a block cut by a cluster boundary leaves fp32
+// partials (at most two per cluster) that paged_combine_kernel merges.
+// Every wait on a barrier is bounded.
+#include <string.h>
+
 #include "kernels.cuh"
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kQ = 16, kK = 32;                  // query rows (heads of one token) and keys of a tile
-constexpr int kSmem = (kQ + kK) * kRow * 4 + kQ * kK * 4;
+constexpr int kRows = 128;                   // query rows of a block (MMA M)
+constexpr int kBK = 64;                      // keys per tile
+constexpr int kOwn = kRows / 2;              // rows whose softmax a CTA computes
+constexpr int kChunk = kBK * 128;            // 8 KB: 64 keys x 64 fp16
+constexpr int kLatStage = 4 * kChunk;        // 32 KB: 64 keys x this CTA's 256 latent dims
+constexpr int kLatStages = 4;
+constexpr int kRopeStages = 2;               // a RoPE tile is done with after its score product
+constexpr int kRopeHalf = 32;
+constexpr int kRopeChunk = kBK * kRopeHalf * 2;     // 4 KB
+constexpr int kQRopeBytes = kRows * kRopeHalf * 2;  // 8 KB
+constexpr int kPBytes = kRows * 128;         // 16 KB: 128 rows x 64 keys fp16
+constexpr int kXBytes = kOwn * kBK * 4;      // 16 KB: 64 rows x 64 keys fp32
+constexpr int kPTx = kOwn * kBK * 2 + kOwn * 4;     // bytes a CTA gets per tile: the other's P rows and factors
+constexpr int kOffLat = kQRopeBytes;
+constexpr int kOffRope = kOffLat + kLatStages * kLatStage;
+constexpr int kOffP = kOffRope + kRopeStages * kRopeChunk;
+constexpr int kOffX = kOffP + 2 * kPBytes;
+constexpr int kOffStg = kOffX + 2 * kXBytes;         // epilogue staging, 2 KB per warp
+constexpr int kOffAlpha = kOffStg + 4 * 2048;        // [2][128] output factors
+constexpr int kOffL = kOffAlpha + 2 * kRows * 4;     // [4][128] row sums
+constexpr int kOffBar = kOffL + 4 * kRows * 4;
+constexpr int kBarBytes = 512;
+constexpr int kSmem = 1024 + kOffBar + kBarBytes;
+static_assert(kSmem <= 232448, "shared memory");
 
-MLA_DEVINL float e4m3_to_f32(uint32_t c) {
-  const uint32_t e = (c >> 3) & 15u, m = c & 7u;
-  const float v = e == 0 ? static_cast<float>(m) * 0x1p-9f : __uint_as_float(((e + 120u) << 23) | (m << 20));
-  return (c & 128u) ? -v : v;
+// Warp roles: softmax 0-3, senders (and Q loads) 4-7, output 8-11, score MMAs
+// 12, P V MMAs 13, then the loader: one TMA warp, or the e4m3 producers.
+constexpr int kSendWarp = 4, kOutWarp = 8, kQkWarp = 12, kPvWarp = 13, kLoadWarp = 14;
+constexpr int kProducerWarps = 6;
+__host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kLoadWarp + (e4m3 ? kProducerWarps : 1)); }
+// 15 warps: 4 per sub-partition, 128 registers a thread; 20 warps: 5, 96.
+__host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 96 : 128; }
+
+constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
+constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
+
+constexpr int kPieceCost = 5;                // start-up of a piece, in tiles
+constexpr int kMinCost = 12;                 // least cost worth a cluster of its own
+
+struct Rec {                                 // what cluster c left unfinished
+  int32_t open_g;     // slot of the block that starts in c and ends in a later cluster (-1: none)
+  int32_t nvalid;     // its rows
+  int64_t qrow0;      // its first (token, head) row
+  int32_t cont_g;     // slot of the block that c continues from an earlier cluster (-1: none)
+  int32_t cont_open;  // and that goes on past c
+  int64_t pad;
+};
+
+struct TcArgs {
+  PagedAttnArgs p;
+  float* ws_o;        // fp32 [2 G][128][512] partials, normalised by their own sums
+  float* ws_ml;       // fp32 [2 G][128][2] running maximum (log2 units) and sum
+  Rec* rec;           // [G]
+  int32_t n_slots;
+  int32_t n_rows;     // rows of the page pool
+};
+
+// ---------------------------------------------------------------------------
+// Blocks.  Sequence b's blocks get slots cu[b] H / 128 + b, ...: these ranges
+// do not overlap (the sum of ceil(n H / 128) over earlier sequences is at most
+// floor(cu[b] H / 128) + b), so a slot's sequence is found by a search in cu
+// alone, with no prefix sums over the batch.  Slots without a block cost 0.
+// ---------------------------------------------------------------------------
+MLA_DEVINL int64_t slot_of_seq(const PagedAttnArgs& a, int b) {
+  const int32_t c = max(0, min(a.T, __ldg(a.cu + b)));
+  return static_cast<int64_t>(c) * a.H / kRows + b;
 }
 
-// A block per 16 heads of a token; keys in tiles of 32, all in fp32.
-__global__ void __launch_bounds__(256) paged_attn_kernel(PagedAttnArgs a) {
-  extern __shared__ float sm[];
-  float* q = sm;
-  float* k = q + kQ * kRow;
-  float* p = k + kK * kRow;
-  if (blockIdx.x == 0) record_bad_seqs(a.cu, a.seq_len, a.B, a.T, a.c.max_rows(), a.err);
-  const int64_t rho = static_cast<int64_t>(blockIdx.x) * kQ;
-  const int32_t tok = static_cast<int32_t>(rho / a.H);
-  const int b = find_seq(a.cu, a.B, tok);
-  bool bad;
-  const PagedSeq s = paged_seq(a.cu, a.seq_len, b, a.T, a.c.max_rows(), bad);
-  if (tok < s.q0 || tok >= s.q0 + s.n) return;
-  const int32_t pos = s.len - s.n + (tok - s.q0);
-  const int32_t wlo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  for (int i = threadIdx.x; i < kQ * kRow; i += 256) {
-    const int r = i / kRow, c = i % kRow;
-    q[i] = c < kLatent ? f16_to_f32(a.q_lat[(rho + r) * kLatent + c]) : bf16_to_f32(a.q_pe[(rho + r) * kRope + c - kLatent]);
+struct Item {
+  int32_t b, g;               // sequence, slot
+  int32_t kend, wlo;          // keys some row of the block sees: [0, n_sink) and [wlo, kend)
+  int32_t first, sink_tiles;  // tile t of the block is t < sink_tiles ? t : first + t - sink_tiles
+  int32_t t_lo, n_tiles;      // this piece: tiles [t_lo, t_lo + n_tiles)
+  int32_t nvalid;             // rows
+  int32_t pos0;               // position of the sequence's first new token
+  uint32_t row0;              // first row within the sequence's new rows
+  int64_t qrow0;              // first row in the token array
+  bool open;                  // the block goes on past this piece
+  MLA_DEVINL bool whole() const { return t_lo == 0 && !open; }
+  MLA_DEVINL int key_tile(int t) const {
+    const int x = t_lo + t;
+    return x < sink_tiles ? x : first + x - sink_tiles;
   }
-  const int row = threadIdx.x >> 4, part = threadIdx.x & 15;     // 16 threads per query row
-  float o[32], m = -INFINITY, l = 0.f;
+};
+
+// Walks the slots in order.
+struct Walker {
+  int b;                // sequence of the last slot asked for
+  int64_t s0, s1;       // its first slot, and the next sequence's
+  PagedSeq seq;
+  uint32_t rows;        // seq.n * H
+
+  MLA_DEVINL void load(const PagedAttnArgs& a) {
+    s0 = slot_of_seq(a, b);
+    s1 = b + 1 < a.B ? slot_of_seq(a, b + 1) : INT64_MAX;
+    bool bad;
+    seq = paged_seq(a.cu, a.seq_len, b, a.T, a.c.max_rows(), bad);
+    rows = static_cast<uint32_t>(seq.n) * static_cast<uint32_t>(a.H);
+  }
+  MLA_DEVINL void init(const PagedAttnArgs& a, int64_t g) {
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (slot_of_seq(a, m) <= g) lo = m; else hi = m;
+    }
+    b = lo;
+    load(a);
+  }
+  // Tiles of slot g's block (0: no block); g must not decrease between calls.
+  MLA_DEVINL int block(const PagedAttnArgs& a, int64_t g, Item& it) {
+    while (g >= s1) {
+      ++b;
+      load(a);
+    }
+    const int64_t i = g - s0;
+    if (i < 0 || i * kRows >= rows) return 0;
+    const uint32_t H = static_cast<uint32_t>(a.H), r0 = static_cast<uint32_t>(i) * kRows;
+    const uint32_t r1 = min(r0 + kRows, rows);
+    it.b = b;
+    it.g = static_cast<int32_t>(g);
+    it.nvalid = static_cast<int32_t>(r1 - r0);
+    it.row0 = r0;
+    it.qrow0 = static_cast<int64_t>(seq.q0) * a.H + r0;
+    it.pos0 = seq.len - seq.n;
+    it.kend = it.pos0 + static_cast<int32_t>((r1 - 1) / H) + 1;
+    it.wlo = a.window > 0 ? max(0, it.pos0 + static_cast<int32_t>(r0 / H) - a.window + 1) : 0;
+    it.first = it.wlo / kBK;
+    it.sink_tiles = min((min(a.n_sink, it.wlo) + kBK - 1) / kBK, it.first);
+    return it.sink_tiles + (it.kend + kBK - 1) / kBK - it.first;
+  }
+};
+
+struct Start {
+  int64_t lo, hi;     // the cluster's range in the run of costs
+  int64_t S;          // where slot g's cost starts in it
+  int32_t g;          // first slot that ends after lo (n_slots: none)
+};
+
+// This cluster's pieces in order; every role walks the same sequence.
+struct Iter {
+  Walker w;
+  int64_t lo, hi, S;
+  int32_t g;
+  MLA_DEVINL void init(const TcArgs& a, const Start& st) {
+    lo = st.lo;
+    hi = st.hi;
+    S = st.S;
+    g = st.g;
+    if (g < a.n_slots) w.init(a.p, g);
+  }
+  MLA_DEVINL bool next(const TcArgs& a, Item& it) {
+    while (g < a.n_slots && S < hi) {
+      const int n = w.block(a.p, g++, it);
+      if (n == 0) continue;
+      const int64_t r0 = S + kPieceCost;         // where the block's tiles start
+      S = r0 + n;
+      const int64_t p_lo = max(lo, r0), p_hi = min(hi, S);
+      if (p_lo >= p_hi) continue;
+      it.t_lo = static_cast<int32_t>(p_lo - r0);
+      it.n_tiles = static_cast<int32_t>(p_hi - p_lo);
+      it.open = p_hi < S;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Walks the tiles across pieces.
+struct Cursor {
+  Iter iter;
+  Item it;
+  int t;
+  bool more;
+  MLA_DEVINL void init(const TcArgs& a, const Start& st) {
+    iter.init(a, st);
+    t = 0;
+    more = iter.next(a, it);
+  }
+  MLA_DEVINL void next(const TcArgs& a) {
+    if (++t < it.n_tiles) return;
+    t = 0;
+    more = iter.next(a, it);
+  }
+};
+
+// Keys [k, k + n) hold one that some row of the block sees.
+MLA_DEVINL bool any_visible(const TcArgs& a, const Item& it, int k, int n) {
+  return k < it.kend && (k + n > it.wlo || k < a.p.n_sink);
+}
+MLA_DEVINL bool key_visible(const TcArgs& a, const Item& it, int k) {
+  return k < it.kend && (k >= it.wlo || k < a.p.n_sink);
+}
+
+// Barriers (u counts this cluster's tiles, k its pieces).
+struct Bars {
+  uint64_t lat_full[kLatStages];    // tile in its stage
+  uint64_t lat_empty[kLatStages];   // P V has read it
+  uint64_t rope_full[kRopeStages];
+  uint64_t rope_empty[kRopeStages];
+  uint64_t s_full[2];               // partial scores in TMEM
+  uint64_t s_free[2];               // both the softmax and the sender warps have read them
+  uint64_t x_full[2];               // the other CTA's partials of the owned rows have arrived
+  uint64_t x_empty[2];              // the other CTA has read what this one sent
+  uint64_t p_full[2];               // P and factors of all 128 rows
+  uint64_t pv_done[2];              // P V done in both CTAs: P buffer, factors and O of that tile
+  uint64_t q_ready;                 // piece k's queries in TMEM and shared memory
+  uint64_t o_ready;                 // piece k's last P V done
+  uint64_t l_full[4];               // piece k's row sums (slot k % 4)
+  uint64_t cmd_full, cmd_done;      // the P V warp's requests to the output warps
+  uint32_t tmem;
+  int32_t cmd;                      // -2 stop, -1 write the piece's output, else rescale O by tile cmd's factors
+  Start st;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
+
+MLA_DEVINL bool wait_all(uint64_t* bar, uint32_t parity, const TcArgs& a) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.p.wait_us, a.p.err));
+}
+MLA_DEVINL bool wait_cl(uint64_t* bar, uint32_t parity, const TcArgs& a) {
+  return __all_sync(0xffffffffu, tc::mbar_wait_cluster_bounded(bar, parity, a.p.wait_us, a.p.err));
+}
+
+// 16-byte unit u (8 halves) of a row in a 128-byte-swizzled K-major tile, and
+// in a 64-byte-swizzled one (rows of 32 halves).
+MLA_DEVINL uint32_t unit128(int row, int u) { return static_cast<uint32_t>(row * 128 + ((u ^ (row & 7)) << 4)); }
+MLA_DEVINL uint32_t unit64(int row, int u) { return static_cast<uint32_t>(row * 64 + ((u ^ ((row >> 1) & 3)) << 4)); }
+
+MLA_DEVINL void st_async_b32(uint32_t remote_addr, uint32_t v, uint32_t remote_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(remote_addr), "r"(v),
+               "r"(remote_bar)
+               : "memory");
+}
+
+// Arrive on `bar` of both CTAs of the pair when every MMA issued so far has
+// completed.  Whole warp; one lane issues.
+MLA_DEVINL void mma_commit_pair_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// 64 bytes of each of a warp's 32 rows (lane = row) to dst_row0 + row * stride,
+// through the warp's 2 KB staging slice, so that each store instruction writes
+// 8 rows x 64 contiguous bytes.  Rows >= nrows are not stored.
+MLA_DEVINL void store_rows(uint8_t* stg, int lane, const uint4 (&w)[4], uint8_t* dst_row0, int64_t stride, int nrows) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e) o[e] = 0.f;
-  for (int32_t j0 = 0; j0 <= pos; j0 += kK) {
-    if (j0 + kK <= wlo && j0 >= a.n_sink) continue;
+  for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4*>(stg + unit64(lane, v)) = w[v];
+  __syncwarp();
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int rr = (lane >> 2) + 8 * m, part = lane & 3;
+    const uint4 x = *reinterpret_cast<const uint4*>(stg + unit64(rr, part));
+    if (rr < nrows) *reinterpret_cast<uint4*>(dst_row0 + rr * stride + part * 16) = x;
+  }
+  __syncwarp();
+}
+
+MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
+  uint4 o;
+  float2 f;
+  f = bf16x2_to_f32(v.x); o.x = pack_f16x2(f.x, f.y);
+  f = bf16x2_to_f32(v.y); o.y = pack_f16x2(f.x, f.y);
+  f = bf16x2_to_f32(v.z); o.z = pack_f16x2(f.x, f.y);
+  f = bf16x2_to_f32(v.w); o.w = pack_f16x2(f.x, f.y);
+  return o;
+}
+
+// ---------------------------------------------------------------------------
+// e4m3 producer: one tile of this CTA's half of the rows into its stage.  Units
+// of 16 bytes, dealt so that a warp's load reads 4 keys x 128 contiguous codes:
+// 1024 code units (64 keys x 16), then 256 RoPE units (64 keys x 4), which are
+// fp16 already.  Rows that no row of the block sees are not read and become
+// zero.  A tile's 64 keys come from at most four pages (pages hold at least 16
+// rows): lane j < 4 of each warp holds the pool row of key 16 j.
+// ---------------------------------------------------------------------------
+struct Producer {
+  static constexpr int NT = kProducerWarps * 32;
+  static constexpr int kCodeUnits = kBK * 16, kUnits = kCodeUnits + kBK * 4;
+  static constexpr int NU = (kUnits + NT - 1) / NT;
+  uint4 v[NU];
+  uint32_t d[NU];
+
+  // Unit idx: key, byte offset in the row, scale byte offset in the row.
+  MLA_DEVINL static void unit_of(int idx, int rank, int& key, int& src, int& sc, uint32_t& dst) {
+    if (idx < kCodeUnits) {
+      key = (idx >> 3) & (kBK - 1);
+      const int cu = ((idx >> 9) << 3) + (idx & 7);
+      src = 256 * rank + 16 * cu;
+      sc = kE4m3ScaleOff + 8 * rank + (cu >> 1);
+      dst = (cu >> 2) * kChunk + unit128(key, 2 * (cu & 3));
+    } else {
+      key = (idx - kCodeUnits) >> 2;
+      const int u = idx & 3;
+      src = kE4m3RopeOff + 2 * kRopeHalf * rank + 16 * u;
+      sc = 0;
+      dst = unit64(key, u);
+    }
+  }
+
+  MLA_DEVINL void load(const TcArgs& a, const Item& it, int kt, int rank, int pt, int lane) {
+    __builtin_assume(pt >= 0 && pt < NT);
+    const int base = kt * kBK;
+    int32_t row = -1;
+    if (lane < 4 && any_visible(a, it, base + 16 * lane, 16)) {
+      row = static_cast<int32_t>(a.p.c.row_of(it.b, base + 16 * lane));
+      if (row < 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
+    }
+#pragma unroll
+    for (int t = 0; t < NU; ++t) {
+      const int idx = pt + t * NT;
+      int key, src, sc;
+      uint32_t dst;
+      unit_of(idx, rank, key, src, sc, dst);
+      const int32_t r = __shfl_sync(0xffffffffu, row, (key >> 4) & 3);
+      v[t] = make_uint4(0, 0, 0, 0);
+      d[t] = 112u;
+      if (idx < kUnits && r >= 0 && key_visible(a, it, base + key)) {
+        const uint8_t* p = a.p.c.pages + static_cast<int64_t>(r + (key & 15)) * kRowE4m3;
+        v[t] = __ldg(reinterpret_cast<const uint4*>(p + src));
+        if (idx < kCodeUnits) d[t] = __ldg(p + sc);
+      }
+    }
+  }
+
+  MLA_DEVINL void store(uint8_t* lat, uint8_t* rope, int rank, int pt) const {
+    __builtin_assume(pt >= 0 && pt < NT);
+#pragma unroll
+    for (int t = 0; t < NU; ++t) {
+      const int idx = pt + t * NT;
+      if (idx >= kUnits) break;
+      int key, src, sc;
+      uint32_t dst;
+      unit_of(idx, rank, key, src, sc, dst);
+      if (idx < kCodeUnits) {
+        const uint32_t s = e4m3_scale_f16x2(d[t]);
+        uint4 lo, hi;
+        e4m3x4_to_f16x4(v[t].x, s, lo.x, lo.y);
+        e4m3x4_to_f16x4(v[t].y, s, lo.z, lo.w);
+        e4m3x4_to_f16x4(v[t].z, s, hi.x, hi.y);
+        e4m3x4_to_f16x4(v[t].w, s, hi.z, hi.w);
+        *reinterpret_cast<uint4*>(lat + dst) = lo;
+        *reinterpret_cast<uint4*>(lat + (dst ^ 16u)) = hi;
+      } else {
+        *reinterpret_cast<uint4*>(rope + dst) = v[t];
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+template <bool kE4m3>
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
+                      const __grid_constant__ TcArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQr = sm;
+  uint8_t* sLat = sm + kOffLat;
+  uint8_t* sRope = sm + kOffRope;
+  uint8_t* sP = sm + kOffP;
+  uint8_t* sX = sm + kOffX;
+  uint8_t* sStg = sm + kOffStg;
+  float* sAlpha = reinterpret_cast<float*>(sm + kOffAlpha);
+  float* sL = reinterpret_cast<float*>(sm + kOffL);
+  Bars& B = *reinterpret_cast<Bars*>(sm + kOffBar);
+
+  const uint32_t rank = tc::cluster_ctarank(), peer = rank ^ 1u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = static_cast<int>(blockIdx.x >> 1), G = static_cast<int>(gridDim.x >> 1);
+  constexpr int NT = threads(kE4m3);
+
+  // ---- setup ---------------------------------------------------------------
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kLatStages; ++i) {
+      mbar_init(&B.lat_full[i], kE4m3 ? kProducerWarps : 1);
+      mbar_init(&B.lat_empty[i], 1);
+    }
+    for (int i = 0; i < kRopeStages; ++i) {
+      mbar_init(&B.rope_full[i], 1);
+      mbar_init(&B.rope_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.s_free[i], 8);
+      mbar_init(&B.x_full[i], 1);
+      mbar_init(&B.x_empty[i], 4);
+      mbar_init(&B.p_full[i], 5);
+      mbar_init(&B.pv_done[i], 2);
+    }
+    mbar_init(&B.q_ready, 4);
+    mbar_init(&B.o_ready, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&B.l_full[i], 5);
+    mbar_init(&B.cmd_full, 1);
+    mbar_init(&B.cmd_done, 4);
+    tc::fence_mbar_init();
+    // what the peer sends for the first use of each buffer
+    for (int i = 0; i < 2; ++i) {
+      mbar_arrive_expect_tx(&B.x_full[i], kXBytes);
+      mbar_arrive_expect_tx(&B.p_full[i], kPTx);
+    }
+    for (int i = 0; i < 4; ++i) mbar_arrive_expect_tx(&B.l_full[i], kOwn * 4);
+    B.st.g = a.n_slots;
+    B.st.lo = B.st.hi = B.st.S = 0;
+  }
+  if (warp == kQkWarp) {
+    tc::tmem_alloc(&B.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (blockIdx.x == 0) record_bad_seqs(a.p.cu, a.p.seq_len, a.p.B, a.p.T, a.p.c.max_rows(), a.p.err);
+  {
+    // The run of all blocks' costs: each thread sums a share of the slots, a
+    // scan over the block gives its start, and the thread whose share holds
+    // this cluster's first unit finds the slot.
+    long long* red = reinterpret_cast<long long*>(sStg);
+    const int per = (a.n_slots + NT - 1) / NT;
+    const int g0 = min(a.n_slots, static_cast<int>(threadIdx.x) * per), g1 = min(a.n_slots, g0 + per);
+    Walker w;
+    Item it;
+    long long sum = 0;
+    if (g0 < g1) {
+      w.init(a.p, g0);
+      for (int g = g0; g < g1; ++g) {
+        const int n = w.block(a.p, g, it);
+        sum += n > 0 ? n + kPieceCost : 0;
+      }
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) red[warp] = incl;
     __syncthreads();
-    for (int i = threadIdx.x; i < kK * kRow; i += 256) {
-      const int r = i / kRow, c = i % kRow;
-      const int32_t j = j0 + r;
-      float v = 0.f;
-      if (j <= pos && (j >= wlo || j < a.n_sink)) {
-        const int64_t cr = a.c.row_of(b, j);
-        if (cr < 0) {
-          record_error(a.err, MLA_ERR_INVALID_ARG);
-        } else {
-          const uint8_t* src = a.c.pages + cr * a.c.row_bytes();
-          if (!a.c.e4m3)
-            v = f16_to_f32(reinterpret_cast<const uint16_t*>(src)[c]);
-          else if (c >= kLatent)
-            v = f16_to_f32(reinterpret_cast<const uint16_t*>(src + kE4m3RopeOff)[c - kLatent]);
-          else
-            v = e4m3_to_f32(src[c]) * __uint_as_float(static_cast<uint32_t>(src[kE4m3ScaleOff + (c >> 5)]) << 23);
+    long long before = 0, total = 0;
+    for (int i = 0; i < NT / 32; ++i) {
+      if (i < warp) before += red[i];
+      total += red[i];
+    }
+    const long long S0 = before + incl - sum;
+    const int ge = static_cast<int>(min(static_cast<long long>(G), max(1ll, total / kMinCost)));
+    if (c < ge && sum > 0) {
+      const long long lo = total * c / ge, hi = total * (c + 1) / ge;
+      if (S0 <= lo && lo < S0 + sum) {
+        long long S = S0;
+        w.init(a.p, g0);
+        for (int g = g0; g < g1; ++g) {
+          const int n = w.block(a.p, g, it);
+          const long long e = S + (n > 0 ? n + kPieceCost : 0);
+          if (lo < e) {
+            B.st.lo = lo;
+            B.st.hi = hi;
+            B.st.S = S;
+            B.st.g = g;
+            break;
+          }
+          S = e;
         }
       }
-      k[i] = v;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kQ * kK; i += 256) {
-      const int r = i / kK, c = i % kK;
-      float x = 0.f;
-      for (int d = 0; d < kRow; ++d) x = fmaf(q[r * kRow + d], k[c * kRow + d], x);
-      const int32_t j = j0 + c;
-      p[i] = j <= pos && (j >= wlo || j < a.n_sink) ? x * a.scale_log2 : -INFINITY;
-    }
-    __syncthreads();
-    float mx = m;
-    for (int c = 0; c < kK; ++c) mx = fmaxf(mx, p[row * kK + c]);
-    const float base = mx == -INFINITY ? 0.f : mx, alpha = exp2f(m - base);
-    m = mx;
-    l *= alpha;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] *= alpha;
-    for (int c = 0; c < kK; ++c) {
-      const float w = exp2f(p[row * kK + c] - base);
-      l += w;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = fmaf(w, k[c * kRow + part + 16 * e], o[e]);
     }
   }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();                 // the peer's barriers are ready before any remote arrival
+  tc::fence_after_sync();
+  const uint32_t tmem = B.tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  Iter items;
+  items.init(a, B.st);
+  Item it;
+  bool ok = true;
+
+  if (warp < kSendWarp) {
+    // ================================ softmax ==================================
+    // Lanes l and l + 16 share row l of this warp's 16 owned rows: keys [32 hh,
+    // + 32) of every tile each.
+    const int hh = lane >> 4;
+    const int lrow = 16 * warp + (lane & 15);                                    // among the owned rows
+    const int i = 32 * warp + 16 * static_cast<int>(rank) + (lane & 15);         // row = TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(32 * warp + 16 * rank) << 16;
+    const float c2 = a.p.scale_log2;
+    const uint32_t peer_p = tc::mapa(smem_u32(sP), peer), peer_pfull = tc::mapa(smem_u32(&B.p_full[0]), peer);
+    const uint32_t peer_alpha = tc::mapa(smem_u32(sAlpha), peer), peer_l = tc::mapa(smem_u32(sL), peer);
+    const uint32_t peer_lfull = tc::mapa(smem_u32(&B.l_full[0]), peer);
+    const uint32_t peer_xempty = tc::mapa(smem_u32(&B.x_empty[0]), peer);
+    int u = 0, k = 0;
+#pragma unroll 1
+    while (ok && items.next(a, it)) {
+      const bool rvalid = i < it.nvalid;
+      // keys [wl, lim] and the sinks are visible to this row
+      const int lim = rvalid ? it.pos0 + static_cast<int>((it.row0 + i) / static_cast<uint32_t>(a.p.H)) : it.kend - 1;
+      const int wl = a.p.window > 0 ? max(0, lim - a.p.window + 1) : 0;
+      float m_run = -INFINITY, l_h = 0.f;
+#pragma unroll 1
+      for (int t = 0; t < it.n_tiles; ++t, ++u) {
+        const int sb = u & 1;
+        const uint32_t ph = (u >> 1) & 1;
+        const int base = it.key_tile(t) * kBK, k0 = base + 32 * hh;
+        ok = wait_all(&B.s_full[sb], ph, a);
+        if (!ok) break;
+        tc::fence_after_sync();
+        uint32_t r[32];
+        tc::tmem_ld16x2<32>(tmem + lanes + kTmS + sb * 64, r);
+        tc::tmem_ld_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.s_free[sb]);
+        ok = wait_cl(&B.x_full[sb], ph, a);
+        if (!ok) break;
+        float s[32];
 #pragma unroll
-  for (int e = 0; e < 32; ++e) a.o_lat[(rho + row) * kLatent + part + 16 * e] = f32_to_f16(o[e] / l);
+        for (int g = 0; g < 8; ++g) {
+          const float4 x = *reinterpret_cast<const float4*>(sX + sb * kXBytes + ((8 * hh + g) * kOwn + lrow) * 16);
+          s[4 * g] = __uint_as_float(r[4 * g]) + x.x;
+          s[4 * g + 1] = __uint_as_float(r[4 * g + 1]) + x.y;
+          s[4 * g + 2] = __uint_as_float(r[4 * g + 2]) + x.z;
+          s[4 * g + 3] = __uint_as_float(r[4 * g + 3]) + x.w;
+        }
+        if (k0 + 31 > lim || (k0 < wl && k0 + 31 >= a.p.n_sink)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (k0 + e > lim || (k0 + e < wl && k0 + e >= a.p.n_sink)) s[e] = -INFINITY;
+        }
+        float mx[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mx[e] = fmaxf(s[2 * e], s[2 * e + 1]);
+#pragma unroll
+        for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+          for (int e = 0; e < w; ++e) mx[e] = fmaxf(mx[e], mx[e + w]);
+        const float mown = mx[0] * c2;
+        const float mrow = fmaxf(mown, __shfl_xor_sync(0xffffffffu, mown, 16));
+        // Every value read from the exchange buffer went into the maximum, so
+        // the peer may refill it (and a relaxed arrival suffices).
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&B.x_full[sb], kXBytes);     // tile u + 2
+        if (lane == 0) tc::mbar_arrive_remote_relaxed(peer_xempty + sb * 8);
+        // Lazy rescale: only when the row maximum grew by more than the
+        // threshold.  A row may see none of the tile's keys (or none so far):
+        // its maximum stays -inf, its P zero.
+        float alpha = 1.f;
+        if (mrow > m_run + kRescaleThreshold) {
+          alpha = tc::exp2_approx(m_run - mrow);
+          m_run = mrow;
+          l_h *= alpha;
+        }
+        const float mb = m_run == -INFINITY ? 0.f : m_run;
+        uint32_t pk[16];
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float p0 = tc::exp2_approx(fmaf(s[2 * e], c2, -mb)), p1 = tc::exp2_approx(fmaf(s[2 * e + 1], c2, -mb));
+          ls[e & 3] += p0 + p1;
+          pk[e] = pack_f16x2(p0, p1);
+        }
+        l_h += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        // The P buffers and factors of tile u - 2 have been used in both CTAs.
+        if (u >= 2) ok = wait_cl(&B.pv_done[sb], ((u >> 1) - 1) & 1, a);
+        if (!ok) break;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint4 v = make_uint4(pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
+          const uint32_t off = sb * kPBytes + unit128(i, 4 * hh + g);
+          *reinterpret_cast<uint4*>(sP + off) = v;
+          tc::st_async_v4(peer_p + off, v, peer_pfull + sb * 8);
+        }
+        if (hh == 0) {
+          const float f = t == 0 ? 1.f : alpha;      // the piece's first P V overwrites O
+          sAlpha[sb * kRows + i] = f;
+          st_async_b32(peer_alpha + (sb * kRows + i) * 4, __float_as_uint(f), peer_pfull + sb * 8);
+        }
+        // A tile with keys that no row of the block sees: their values must
+        // not enter P V (0 x NaN).  The score product has read the tile.
+        if (!kE4m3 && (base + kBK > it.kend || (base < it.wlo && base + kBK > a.p.n_sink))) {
+          uint8_t* stage = sLat + (u % kLatStages) * kLatStage;
+          for (int q = threadIdx.x; q < kBK * 32; q += 128)
+            if (!key_visible(a, it, base + (q >> 5)))
+              *reinterpret_cast<uint4*>(stage + ((q >> 3) & 3) * kChunk + (q >> 5) * 128 + (q & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.p_full[sb]);
+      }
+      if (!ok) break;
+      // Row sums to both CTAs' output warps.  Slot k % 4 is free: the P V this
+      // warp last waited for followed the output of piece k - 3 at least.
+      const float l_row = l_h + __shfl_xor_sync(0xffffffffu, l_h, 16);
+      if (hh == 0) {
+        sL[(k & 3) * kRows + i] = l_row;
+        st_async_b32(peer_l + ((k & 3) * kRows + i) * 4, __float_as_uint(l_row), peer_lfull + (k & 3) * 8);
+        if (!it.whole() && rvalid) {
+          float* ml = a.ws_ml + 2 * ((2 * static_cast<int64_t>(c) + (it.t_lo > 0 ? 0 : 1)) * kRows + i);
+          ml[0] = m_run;
+          ml[1] = l_row;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.l_full[k & 3]);
+      ++k;
+    }
+  } else if (warp < kOutWarp) {
+    // ===================== queries, and the peer's partial scores ==============
+    const int q4 = warp - kSendWarp, hh = lane >> 4;
+    const int lrow = 16 * q4 + (lane & 15);
+    const uint32_t lanes = static_cast<uint32_t>(32 * q4 + 16 * peer) << 16;     // the peer's rows
+    const uint32_t peer_x = tc::mapa(smem_u32(sX), peer), peer_xfull = tc::mapa(smem_u32(&B.x_full[0]), peer);
+    const int i = 32 * q4 + lane;                                                // Q row of this thread
+    uint32_t qrun = 0;
+    int u = 0;
+#pragma unroll 1
+    while (ok && items.next(a, it)) {
+      // Q of the piece.  The last score product of the previous piece is
+      // complete: this warp has read its result.
+      {
+        const bool rvalid = i < it.nvalid;
+        const int64_t qrow = it.qrow0 + i;
+        const uint4* src = reinterpret_cast<const uint4*>(a.p.q_lat + qrow * kLatent + 256 * rank);
+        const uint4* qp = reinterpret_cast<const uint4*>(a.p.q_pe + qrow * kRope) + 4 * rank;
+        uint4 qpe[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) qpe[v] = rvalid ? __ldg(qp + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int h2 = 0; h2 < 2; ++h2) {
+          uint32_t r[2][32];
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const uint4 x = rvalid ? __ldg(src + (2 * h2 + cc) * 8 + v) : make_uint4(0, 0, 0, 0);
+              r[cc][4 * v] = x.x; r[cc][4 * v + 1] = x.y; r[cc][4 * v + 2] = x.z; r[cc][4 * v + 3] = x.w;
+            }
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc)
+            tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ + 32 * (2 * h2 + cc), r[cc]);
+        }
+        tc::tmem_st_wait();
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          qrun = bf16x2_absmax(bf16x2_absmax(qrun, qpe[v].x), qpe[v].y);
+          qrun = bf16x2_absmax(bf16x2_absmax(qrun, qpe[v].z), qpe[v].w);
+          *reinterpret_cast<uint4*>(sQr + unit64(i, v)) = bf16x8_to_f16x8(qpe[v]);
+        }
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.q_ready);
+      }
+#pragma unroll 1
+      for (int t = 0; t < it.n_tiles; ++t, ++u) {
+        const int sb = u & 1;
+        ok = wait_all(&B.s_full[sb], (u >> 1) & 1, a);
+        if (!ok) break;
+        tc::fence_after_sync();
+        uint32_t r[32];
+        tc::tmem_ld16x2<32>(tmem + lanes + kTmS + sb * 64, r);
+        tc::tmem_ld_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.s_free[sb]);
+        if (u >= 2) ok = wait_cl(&B.x_empty[sb], ((u >> 1) - 1) & 1, a);
+        if (!ok) break;
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+          tc::st_async_v4(peer_x + sb * kXBytes + ((8 * hh + g) * kOwn + lrow) * 16,
+                          make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]), peer_xfull + sb * 8);
+      }
+    }
+    if (bf16x2_absmax_overflows(qrun)) record_error(a.p.err, MLA_ERR_RANGE);
+  } else if (warp < kQkWarp) {
+    // ================================= output ==================================
+    // Requests of the P V warp, in order: rescale O before a P V, or write a
+    // finished piece's output.
+    const int q4 = warp - kOutWarp, i = 32 * q4 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
+    uint8_t* stg = sStg + q4 * 2048;
+    int k = 0;
+#pragma unroll 1
+    for (int n = 0; ok; ++n) {
+      ok = wait_all(&B.cmd_full, n & 1, a);
+      if (!ok) break;
+      const int u = *reinterpret_cast<volatile int32_t*>(&B.cmd);
+      if (u == -2) break;
+      if (u >= 0) {
+        const float f = sAlpha[(u & 1) * kRows + i];
+        ok = wait_cl(&B.pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, a);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            uint32_t o[32];
+            tc::tmem_ld32(tmem + lanes + kTmO + 32 * cc, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tc::tmem_st32(tmem + lanes + kTmO + 32 * cc, o);
+          }
+          tc::tmem_st_wait();
+        }
+      } else {
+        if (!items.next(a, it)) break;
+        ok = wait_all(&B.o_ready, k & 1, a) && wait_cl(&B.l_full[k & 3], (k >> 2) & 1, a);
+        if (!ok) break;
+        if (warp == kOutWarp && lane == 0) mbar_arrive_expect_tx(&B.l_full[k & 3], kOwn * 4);   // piece k + 4
+        tc::fence_after_sync();
+        const float l = sL[(k & 3) * kRows + i];
+        const float inv = l > 0.f ? 1.f / l : 0.f;     // a row that sees no key of this piece
+        const int nrows = it.nvalid - 32 * q4;
+        if (it.whole()) {
+          uint8_t* dst = reinterpret_cast<uint8_t*>(a.p.o_lat + (it.qrow0 + 32 * q4) * kLatent + 256 * rank);
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            uint32_t o[32];
+            tc::tmem_ld32(tmem + lanes + kTmO + 32 * cc, o);
+            tc::tmem_ld_wait();
+            uint4 w[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              w[v].x = pack_f16x2(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv);
+              w[v].y = pack_f16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv);
+              w[v].z = pack_f16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv);
+              w[v].w = pack_f16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv);
+            }
+            store_rows(stg, lane, w, dst + cc * 64, kLatent * 2, nrows);
+          }
+        } else {
+          const int64_t slot = 2 * static_cast<int64_t>(c) + (it.t_lo > 0 ? 0 : 1);
+          uint8_t* dst = reinterpret_cast<uint8_t*>(a.ws_o + (slot * kRows + 32 * q4) * kLatent + 256 * rank);
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            uint32_t o[32];
+            tc::tmem_ld32(tmem + lanes + kTmO + 32 * cc, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+              uint4 w[4];
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                w[v] = make_uint4(__float_as_uint(__uint_as_float(o[16 * h2 + 4 * v]) * inv),
+                                  __float_as_uint(__uint_as_float(o[16 * h2 + 4 * v + 1]) * inv),
+                                  __float_as_uint(__uint_as_float(o[16 * h2 + 4 * v + 2]) * inv),
+                                  __float_as_uint(__uint_as_float(o[16 * h2 + 4 * v + 3]) * inv));
+              store_rows(stg, lane, w, dst + (32 * cc + 16 * h2) * 4, kLatent * 4, nrows);
+            }
+          }
+        }
+        ++k;
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.cmd_done);
+    }
+  } else if (warp == kQkWarp) {
+    // ============================== score MMAs =================================
+    constexpr uint32_t idesc = tc::idesc_f16(128, kBK, false, false, false);
+    Rec rec = {-1, 0, 0, -1, 0, 0};
+    int u = 0, k = 0;
+#pragma unroll 1
+    while (ok && items.next(a, it)) {
+      if (it.t_lo > 0) {
+        rec.cont_g = it.g;
+        rec.cont_open = it.open ? 1 : 0;
+      } else if (it.open) {
+        rec.open_g = it.g;
+        rec.nvalid = it.nvalid;
+        rec.qrow0 = it.qrow0;
+      }
+      ok = wait_all(&B.q_ready, k++ & 1, a);
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int t = 0; ok && t < it.n_tiles; ++t, ++u) {
+        const int ls = u % kLatStages, rs = u % kRopeStages, sb = u & 1;
+        ok = wait_all(&B.lat_full[ls], (u / kLatStages) & 1, a);
+        if (!kE4m3) ok = ok && wait_all(&B.rope_full[rs], (u / kRopeStages) & 1, a);
+        if (u >= 2) ok = ok && wait_all(&B.s_free[sb], ((u >> 1) - 1) & 1, a);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t k0 = smem_u32(sLat + ls * kLatStage), d = tmem + kTmS + sb * 64;
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks)        // latent half: A = Q from TMEM
+          tc::mma_ts_warp(d, tmem + kTmQ + ks * 8, tc::sdesc_sw128(k0 + (ks >> 2) * kChunk + (ks & 3) * 32, 16, 1024),
+                          idesc, ks > 0 ? 1u : 0u);
+        const uint32_t q0 = smem_u32(sQr), r0 = smem_u32(sRope + rs * kRopeChunk);
+#pragma unroll
+        for (int ks = 0; ks < kRopeHalf / 16; ++ks)
+          tc::mma_ss_warp(d, tc::sdesc_sw64(q0 + ks * 32), tc::sdesc_sw64(r0 + ks * 32), idesc, 1u);
+        tc::mma_commit_warp(&B.rope_empty[rs]);
+        tc::mma_commit_warp(&B.s_full[sb]);
+      }
+    }
+    if (!ok) rec.open_g = rec.cont_g = -1;
+    if (rank == 0 && lane == 0) a.rec[c] = rec;
+  } else if (warp == kPvWarp) {
+    // =============================== P V MMAs ==================================
+    constexpr uint32_t idesc = tc::idesc_f16(128, 256, false, false, true);
+    int u = 0, n = 0;                  // tiles, requests posted to the output warps
+    auto post = [&](int cmd) {
+      if (n > 0) ok = ok && wait_all(&B.cmd_done, (n - 1) & 1, a);
+      if (!ok) return;
+      if (lane == 0) {
+        *reinterpret_cast<volatile int32_t*>(&B.cmd) = cmd;
+        mbar_arrive(&B.cmd_full);
+      }
+      ++n;
+    };
+#pragma unroll 1
+    while (ok && items.next(a, it)) {
+#pragma unroll 1
+      for (int t = 0; t < it.n_tiles; ++t, ++u) {
+        const int ls = u % kLatStages, sb = u & 1;
+        ok = wait_cl(&B.p_full[sb], (u >> 1) & 1, a);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&B.p_full[sb], kPTx);       // tile u + 2
+        if (t == 0) {
+          if (n > 0) ok = wait_all(&B.cmd_done, (n - 1) & 1, a);          // the previous output has left O
+        } else {
+          const float4 f = *reinterpret_cast<const float4*>(sAlpha + sb * kRows + 4 * lane);
+          if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f)) {
+            post(u);
+            if (ok) ok = wait_all(&B.cmd_done, (n - 1) & 1, a);
+          }
+        }
+        if (!ok) break;
+        tc::fence_proxy_async();       // the peer's P rows, written by st.async, for the MMA
+        tc::fence_after_sync();
+        const uint32_t v0 = smem_u32(sLat + ls * kLatStage), p0 = smem_u32(sP + sb * kPBytes);
+#pragma unroll
+        for (int ks = 0; ks < kBK / 16; ++ks)
+          tc::mma_ss_warp(tmem + kTmO, tc::sdesc_sw128(p0 + ks * 32, 16, 1024),
+                          tc::sdesc_sw128(v0 + ks * 2048, kChunk, 1024), idesc, (t > 0 || ks > 0) ? 1u : 0u);
+        tc::mma_commit_warp(&B.lat_empty[ls]);
+        mma_commit_pair_warp(&B.pv_done[sb]);
+      }
+      if (!ok) break;
+      tc::mma_commit_warp(&B.o_ready);
+      post(-1);
+    }
+    if (ok) post(-2);
+  } else if constexpr (!kE4m3) {
+    // ============================== TMA loader =================================
+    // Lane 5 j + c: chunk c (four of 64 latent dims, then the RoPE half) of box
+    // j, the part of the tile that lies in one page.  A box without a visible
+    // row is loaded from behind the last row, which reads as zero.
+    const int shift = min(6, a.p.c.page_shift), box = 1 << shift, nb = kBK >> shift;
+    const int j = lane / 5, ch = lane % 5;
+    const bool mine = j < nb;
+    Cursor cur;
+    cur.init(a, B.st);
+#pragma unroll 1
+    for (int u = 0; ok && cur.more; ++u, cur.next(a)) {
+      const int ls = u % kLatStages, rs = u % kRopeStages;
+      const int key = cur.it.key_tile(cur.t) * kBK + j * box;
+      int row = a.n_rows;
+      if (mine && any_visible(a, cur.it, key, box)) {
+        const int64_t x = a.p.c.row_of(cur.it.b, key);
+        if (x >= 0) {
+          row = static_cast<int>(x);
+          if (ch == 4)                 // the whole rows of the box on their way into L2
+            tc::prefetch_l2(a.p.c.pages + x * kRowF16, static_cast<uint32_t>(min(box, cur.it.kend - key)) * kRowF16);
+        } else {
+          record_error(a.p.err, MLA_ERR_INVALID_ARG);
+        }
+      }
+      if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
+      __syncwarp();
+      if (mine && ch < 4)
+        tc::tma_load_3d(sLat + ls * kLatStage + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls],
+                        256 * static_cast<int>(rank) + 64 * ch, row, 0);
+      if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
+      __syncwarp();
+      if (mine && ch == 4)
+        tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs],
+                        kLatent + kRopeHalf * static_cast<int>(rank), row, 0);
+    }
+  } else {
+    // ============================ e4m3 producers ===============================
+    const int pt = static_cast<int>(threadIdx.x) - kLoadWarp * 32;
+    Cursor cur;
+    cur.init(a, B.st);
+    Producer x;
+    if (cur.more) x.load(a, cur.it, cur.it.key_tile(cur.t), static_cast<int>(rank), pt, lane);
+#pragma unroll 1
+    for (int u = 0; cur.more; ++u) {
+      const int ls = u % kLatStages, rs = u % kRopeStages;
+      if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
+      if (u >= kRopeStages) ok = ok && wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
+      if (!ok) break;
+      x.store(sLat + ls * kLatStage, sRope + rs * kRopeChunk, static_cast<int>(rank), pt);
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.lat_full[ls]);
+      cur.next(a);
+      if (cur.more) x.load(a, cur.it, cur.it.key_tile(cur.t), static_cast<int>(rank), pt, lane);
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();                 // nothing may be sent to a CTA that has left
+  if (warp == kQkWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Merge the partials of every block that a cluster boundary cut: block (x =
+// cluster in which it starts, y = group of 8 rows), a warp per row, 16 of the
+// 512 columns a lane.  Launched as a programmatic dependent of the attention.
+// ---------------------------------------------------------------------------
+constexpr int kCombRows = 8;
+
+__global__ void __launch_bounds__(32 * kCombRows) paged_combine_kernel(const TcArgs a, int G) {
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kCombRows + warp;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Rec* rec = a.rec;
+  const int g = rec[c].open_g;
+  if (g < 0 || row >= rec[c].nvalid) return;
+  // the clusters after c that continue block g
+  int n = 1;
+  for (int x0 = c + 1; x0 < G; x0 += 32) {
+    const int x = x0 + lane;
+    const bool cont = x < G && rec[x].cont_g == g;
+    const unsigned stop = ~__ballot_sync(0xffffffffu, cont);
+    n += stop ? __ffs(stop) - 1 : 32;
+    if (stop) break;
+  }
+  auto slot = [&](int s) { return (2 * static_cast<int64_t>(c + s) + (s == 0 ? 1 : 0)) * kRows + row; };
+  float M = -INFINITY;
+  for (int s = lane; s < n; s += 32) M = fmaxf(M, a.ws_ml[2 * slot(s)]);
+  M = warp_max(M);
+  float L = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += 4) {
+    float4 v[4][4];
+    float w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + j < n) {
+        const int64_t q = slot(s0 + j);
+        const float4* src = reinterpret_cast<const float4*>(a.ws_o + q * kLatent) + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[j][k] = src[32 * k];
+        w[j] = exp2f(a.ws_ml[2 * q] - M) * a.ws_ml[2 * q + 1];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      L += w[j];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[k].x = fmaf(w[j], v[j][k].x, acc[k].x);
+        acc[k].y = fmaf(w[j], v[j][k].y, acc[k].y);
+        acc[k].z = fmaf(w[j], v[j][k].z, acc[k].z);
+        acc[k].w = fmaf(w[j], v[j][k].w, acc[k].w);
+      }
+    }
+  }
+  const float inv = 1.f / L;
+  uint2* out = reinterpret_cast<uint2*>(a.p.o_lat + (rec[c].qrow0 + row) * kLatent) + lane;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    out[32 * k] = make_uint2(pack_f16x2(acc[k].x * inv, acc[k].y * inv), pack_f16x2(acc[k].z * inv, acc[k].w * inv));
+}
+
+int clusters() { return max(1, device_sm_count() / 2); }
+
+template <bool kE4m3>
+cudaError_t launch_one(const CUtensorMap& tm, const CUtensorMap& tr, const TcArgs& a, cudaStream_t stream) {
+  auto kern = paged_attn_kernel<kE4m3>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(2 * clusters()), threads(kE4m3), kSmem, stream>>>(tm, tr, a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes() { return 256; }
+size_t paged_attn_workspace_bytes() {
+  const size_t rows = static_cast<size_t>(2 * clusters()) * kRows;
+  return rows * kLatent * sizeof(float) + rows * 2 * sizeof(float) + clusters() * sizeof(Rec);
+}
 
-cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
+  const int G = clusters();
+  const size_t rows = static_cast<size_t>(2 * G) * kRows;
+  TcArgs a = {};
+  a.p = p;
+  a.ws_o = static_cast<float*>(p.workspace);
+  a.ws_ml = a.ws_o + rows * kLatent;
+  a.rec = reinterpret_cast<Rec*>(a.ws_ml + rows * 2);
+  a.n_slots = static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
+  a.n_rows = p.c.n_pages << p.c.page_shift;
+  CUtensorMap tm, tr;
+  cudaError_t e;
+  if (p.c.e4m3) {
+    memset(&tm, 0, sizeof(tm));
+    memset(&tr, 0, sizeof(tr));
+    e = launch_one<true>(tm, tr, a, stream);
+  } else {
+    const uint32_t box = static_cast<uint32_t>(min(kBK, 1 << p.c.page_shift));
+    const uint64_t n = static_cast<uint64_t>(a.n_rows);
+    e = make_tmap_3d(&tm, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, 64, box, 1);
+    if (e != cudaSuccess) return e;
+    e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
+    if (e != cudaSuccess) return e;
+    e = launch_one<false>(tm, tr, a, stream);
+  }
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<<<static_cast<unsigned>(static_cast<int64_t>(a.T) * a.H / kQ), 256, kSmem, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(G), kRows / kCombRows);
+  cfg.blockDim = dim3(32 * kCombRows);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel, a, G);
 }
 
 }  // namespace mla

@@ -50,24 +50,6 @@ MLA_DEVINL uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Two e4m3 codes to two fp16 values (exact).
-MLA_DEVINL uint32_t e4m3x2_to_f16x2(uint32_t c) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(c));
-  return r;
-}
-
-// 2^(s - 127) for a scale byte in [112, 134] as fp16 bits, in both halves.
-MLA_DEVINL uint32_t e4m3_scale_f16x2(uint32_t s) {
-  const uint32_t h = s > 112 ? (s - 112) << 10 : 0x0200u;   // 2^-15 is fp16-subnormal
-  return h | (h << 16);
-}
-
-MLA_DEVINL uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // A warp per token: the latent values in two passes of 256 (8 per lane), then
 // the 64 RoPE values on lanes 0-7.
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a) {
@@ -157,10 +139,8 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(PagedGatherArgs a) {
       } else {
         const uint2 c = __ldg(reinterpret_cast<const uint2*>(src + 8 * u));
         const uint32_t d = e4m3_scale_f16x2(__ldg(src + kE4m3ScaleOff + (u >> 2)));
-        w[0] = mul_f16x2(e4m3x2_to_f16x2(c.x & 0xFFFFu), d);
-        w[1] = mul_f16x2(e4m3x2_to_f16x2(c.x >> 16), d);
-        w[2] = mul_f16x2(e4m3x2_to_f16x2(c.y & 0xFFFFu), d);
-        w[3] = mul_f16x2(e4m3x2_to_f16x2(c.y >> 16), d);
+        e4m3x4_to_f16x4(c.x, d, w[0], w[1]);
+        e4m3x4_to_f16x4(c.y, d, w[2], w[3]);
       }
       if (!kOutF16) {
 #pragma unroll

@@ -14,13 +14,17 @@
 //     the contraction, for all 128 rows.
 //   * The partial scores are reduced between the CTAs by rows: CTA r owns rows
 //     with (row / 16) % 2 == r.  Four sender warps pass the other CTA's 64 rows
-//     on to it in fp32 (st.async into distributed shared memory); four softmax
-//     warps add what arrives to their own half, so scores are full fp32 sums
-//     and each row's softmax is computed once in the pair.  P (fp16) of the
-//     owned rows is stored to both CTAs, with the factor by which the row's
-//     earlier output has to shrink if its running maximum grew.  (Exchanging
-//     all partial scores in fp16 and computing every softmax twice takes the
-//     same bytes on the wire, twice the exponentials, and rounds the scores.)
+//     on to it in fp32 (st.async into distributed shared memory); softmax warps
+//     add what arrives to their own half, so scores are full fp32 sums and each
+//     row's softmax is computed once in the pair.  P (fp16) of the owned rows is
+//     stored to both CTAs, with the factor by which the row's earlier output has
+//     to shrink if its running maximum grew.  (Exchanging all partial scores in
+//     fp16 and computing every softmax twice takes the same bytes on the wire,
+//     twice the exponentials, and rounds the scores.)
+//   * A tile stays in its stage from its load to its P V, so the chain of steps
+//     between them, not any unit's throughput, bounds the pace: eight warps
+//     share a tile's softmax (16 keys of a row per thread), and P goes to the
+//     peer as one bulk copy of 2 KB per 16 rows.
 //   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
 //   * fp16 pages come in by TMA as they are.  e4m3 pages are read, turned into
 //     fp16 (code x scale, exact) and stored in the same layout by producer
@@ -59,18 +63,23 @@ constexpr int kOffX = kOffP + 2 * kPBytes;
 constexpr int kOffStg = kOffX + 2 * kXBytes;         // epilogue staging, 2 KB per warp
 constexpr int kOffAlpha = kOffStg + 4 * 2048;        // [2][128] output factors
 constexpr int kOffL = kOffAlpha + 2 * kRows * 4;     // [4][128] row sums
-constexpr int kOffBar = kOffL + 4 * kRows * 4;
+constexpr int kOffM = kOffL + 4 * kRows * 4;         // [2][2][64] row maxima of the key halves, by tile parity
+constexpr int kOffBar = kOffM + 2 * 2 * kOwn * 4;
 constexpr int kBarBytes = 512;
 constexpr int kSmem = 1024 + kOffBar + kBarBytes;
 static_assert(kSmem <= 232448, "shared memory");
 
-// Warp roles: softmax 0-3, senders (and Q loads) 4-7, output 8-11, score MMAs
-// 12, P V MMAs 13, then the loader: one TMA warp, or the e4m3 producers.
-constexpr int kSendWarp = 4, kOutWarp = 8, kQkWarp = 12, kPvWarp = 13, kLoadWarp = 14;
+// Warp roles: softmax 0-3 (keys 0-31 of a tile) and 4-7 (keys 32-63), senders
+// (and Q loads) 8-11, output 12-15, score MMAs 16, P V MMAs 17, then the loader:
+// one TMA warp, or the e4m3 producers.
+constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18;
+// Named barriers of the warp pair (q, q + 4) that shares 16 rows.
+constexpr int kBarMax = 1;                   // + q: the halves' row maxima (and row sums) are in sM
+constexpr int kBarP = 5;                     // + q: both halves' P is in shared memory
 constexpr int kProducerWarps = 6;
 __host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kLoadWarp + (e4m3 ? kProducerWarps : 1)); }
-// 15 warps: 4 per sub-partition, 128 registers a thread; 20 warps: 5, 96.
-__host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 96 : 128; }
+// 19 warps: 5 per sub-partition, 96 registers a thread; 24 warps: 6, 80.
+__host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 80 : 96; }
 
 constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
@@ -272,6 +281,29 @@ MLA_DEVINL void st_async_b32(uint32_t remote_addr, uint32_t v, uint32_t remote_b
                : "memory");
 }
 
+MLA_DEVINL void named_bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// `bytes` of this CTA's shared memory to the peer's, counted on its barrier.
+MLA_DEVINL void bulk_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// 16 TMEM lanes, 16 columns per thread: threads 0-15 at columns [c, c + 16),
+// threads 16-31 the same lanes at [c + 16, c + 32).
+MLA_DEVINL void tmem_ld16x2_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // Arrive on `bar` of both CTAs of the pair when every MMA issued so far has
 // completed.  Whole warp; one lane issues.
 MLA_DEVINL void mma_commit_pair_warp(uint64_t* bar) {
@@ -409,6 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   uint8_t* sStg = sm + kOffStg;
   float* sAlpha = reinterpret_cast<float*>(sm + kOffAlpha);
   float* sL = reinterpret_cast<float*>(sm + kOffL);
+  float* sM = reinterpret_cast<float*>(sm + kOffM);
   Bars& B = *reinterpret_cast<Bars*>(sm + kOffBar);
 
   const uint32_t rank = tc::cluster_ctarank(), peer = rank ^ 1u;
@@ -428,9 +461,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.s_free[i], 8);
+      mbar_init(&B.s_free[i], 12);
       mbar_init(&B.x_full[i], 1);
-      mbar_init(&B.x_empty[i], 4);
+      mbar_init(&B.x_empty[i], 8);
       mbar_init(&B.p_full[i], 5);
       mbar_init(&B.pv_done[i], 2);
     }
@@ -520,20 +553,24 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 
   if (warp < kSendWarp) {
     // ================================ softmax ==================================
-    // Lanes l and l + 16 share row l of this warp's 16 owned rows: keys [32 hh,
-    // + 32) of every tile each.
-    const int hh = lane >> 4;
-    const int lrow = 16 * warp + (lane & 15);                                    // among the owned rows
-    const int i = 32 * warp + 16 * static_cast<int>(rank) + (lane & 15);         // row = TMEM lane
-    const uint32_t lanes = static_cast<uint32_t>(32 * warp + 16 * rank) << 16;
+    // Four threads per owned row: warps q and q + 4, lanes l and l + 16, 16 keys
+    // of every tile each.  A wait that gave up makes the warp `dead`: it goes on
+    // through the tiles with nothing but the named barriers, on which its partner
+    // waits without a limit.
+    const int half = warp >> 2, q4 = warp & 3, hh = lane >> 4;
+    const int lrow = 16 * q4 + (lane & 15);                                      // among the owned rows
+    const int i = 32 * q4 + 16 * static_cast<int>(rank) + (lane & 15);           // row = TMEM lane
+    const int col = 32 * half + 16 * hh;                                         // first key of this thread
+    const uint32_t lanes = static_cast<uint32_t>(32 * q4 + 16 * rank) << 16;
     const float c2 = a.p.scale_log2;
     const uint32_t peer_p = tc::mapa(smem_u32(sP), peer), peer_pfull = tc::mapa(smem_u32(&B.p_full[0]), peer);
     const uint32_t peer_alpha = tc::mapa(smem_u32(sAlpha), peer), peer_l = tc::mapa(smem_u32(sL), peer);
     const uint32_t peer_lfull = tc::mapa(smem_u32(&B.l_full[0]), peer);
     const uint32_t peer_xempty = tc::mapa(smem_u32(&B.x_empty[0]), peer);
+    bool dead = false;
     int u = 0, k = 0;
 #pragma unroll 1
-    while (ok && items.next(a, it)) {
+    while (items.next(a, it)) {
       const bool rvalid = i < it.nvalid;
       // keys [wl, lim] and the sinks are visible to this row
       const int lim = rvalid ? it.pos0 + static_cast<int>((it.row0 + i) / static_cast<uint32_t>(a.p.H)) : it.kend - 1;
@@ -543,107 +580,129 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int sb = u & 1;
         const uint32_t ph = (u >> 1) & 1;
-        const int base = it.key_tile(t) * kBK, k0 = base + 32 * hh;
-        ok = wait_all(&B.s_full[sb], ph, a);
-        if (!ok) break;
-        tc::fence_after_sync();
-        uint32_t r[32];
-        tc::tmem_ld16x2<32>(tmem + lanes + kTmS + sb * 64, r);
-        tc::tmem_ld_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B.s_free[sb]);
-        ok = wait_cl(&B.x_full[sb], ph, a);
-        if (!ok) break;
-        float s[32];
+        const int base = it.key_tile(t) * kBK, k0 = base + col;
+        float s[16];
+        float mrow = -INFINITY;
+        if (!dead) dead = !wait_all(&B.s_full[sb], ph, a);
+        if (!dead) {
+          tc::fence_after_sync();
+          uint32_t r[16];
+          tmem_ld16x2_16(tmem + lanes + kTmS + sb * 64 + 32 * half, r);
+          tc::tmem_ld_wait();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.s_free[sb]);
+          dead = !wait_cl(&B.x_full[sb], ph, a);
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float4 x = *reinterpret_cast<const float4*>(sX + sb * kXBytes + ((8 * hh + g) * kOwn + lrow) * 16);
-          s[4 * g] = __uint_as_float(r[4 * g]) + x.x;
-          s[4 * g + 1] = __uint_as_float(r[4 * g + 1]) + x.y;
-          s[4 * g + 2] = __uint_as_float(r[4 * g + 2]) + x.z;
-          s[4 * g + 3] = __uint_as_float(r[4 * g + 3]) + x.w;
+          for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(r[e]);
         }
-        if (k0 + 31 > lim || (k0 < wl && k0 + 31 >= a.p.n_sink)) {
+        if (!dead) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (k0 + e > lim || (k0 + e < wl && k0 + e >= a.p.n_sink)) s[e] = -INFINITY;
+          for (int g = 0; g < 4; ++g) {
+            const float4 x = *reinterpret_cast<const float4*>(sX + sb * kXBytes + ((col / 4 + g) * kOwn + lrow) * 16);
+            s[4 * g] += x.x;
+            s[4 * g + 1] += x.y;
+            s[4 * g + 2] += x.z;
+            s[4 * g + 3] += x.w;
+          }
+          if (k0 + 15 > lim || (k0 < wl && k0 + 15 >= a.p.n_sink)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (k0 + e > lim || (k0 + e < wl && k0 + e >= a.p.n_sink)) s[e] = -INFINITY;
+          }
+          float mx[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx[e] = fmaxf(s[2 * e], s[2 * e + 1]);
+#pragma unroll
+          for (int w = 4; w >= 1; w >>= 1)
+#pragma unroll
+            for (int e = 0; e < w; ++e) mx[e] = fmaxf(mx[e], mx[e + w]);
+          const float mown = mx[0] * c2;
+          mrow = fmaxf(mown, __shfl_xor_sync(0xffffffffu, mown, 16));
+          if (hh == 0) sM[(2 * sb + half) * kOwn + lrow] = mrow;
         }
-        float mx[16];
+        tc::named_bar_sync(kBarMax + q4, 64);
+        if (!dead) {
+          // Every value read from the exchange buffer went into the maximum, so
+          // the peer may refill it (and a relaxed arrival suffices).
+          if (lane == 0) tc::mbar_arrive_remote_relaxed(peer_xempty + sb * 8);
+          mrow = fmaxf(mrow, sM[(2 * sb + (half ^ 1)) * kOwn + lrow]);
+          // Lazy rescale: only when the row maximum grew by more than the
+          // threshold.  A row may see none of the tile's keys (or none so far):
+          // its maximum stays -inf, its P zero.
+          float alpha = 1.f;
+          if (mrow > m_run + kRescaleThreshold) {
+            alpha = tc::exp2_approx(m_run - mrow);
+            m_run = mrow;
+            l_h *= alpha;
+          }
+          const float mb = m_run == -INFINITY ? 0.f : m_run;
+          uint32_t pk[8];
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mx[e] = fmaxf(s[2 * e], s[2 * e + 1]);
+          for (int e = 0; e < 8; ++e) {
+            const float p0 = tc::exp2_approx(fmaf(s[2 * e], c2, -mb)), p1 = tc::exp2_approx(fmaf(s[2 * e + 1], c2, -mb));
+            ls[e & 3] += p0 + p1;
+            pk[e] = pack_f16x2(p0, p1);
+          }
+          l_h += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          // The P buffer and the factors of tile u - 2 have been used in both CTAs.
+          if (u >= 2) dead = !wait_cl(&B.pv_done[sb], ((u >> 1) - 1) & 1, a);
+          if (!dead) {
+            const uint32_t prow = sb * kPBytes + unit128(i, 0);
 #pragma unroll
-        for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-          for (int e = 0; e < w; ++e) mx[e] = fmaxf(mx[e], mx[e + w]);
-        const float mown = mx[0] * c2;
-        const float mrow = fmaxf(mown, __shfl_xor_sync(0xffffffffu, mown, 16));
-        // Every value read from the exchange buffer went into the maximum, so
-        // the peer may refill it (and a relaxed arrival suffices).
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(&B.x_full[sb], kXBytes);     // tile u + 2
-        if (lane == 0) tc::mbar_arrive_remote_relaxed(peer_xempty + sb * 8);
-        // Lazy rescale: only when the row maximum grew by more than the
-        // threshold.  A row may see none of the tile's keys (or none so far):
-        // its maximum stays -inf, its P zero.
-        float alpha = 1.f;
-        if (mrow > m_run + kRescaleThreshold) {
-          alpha = tc::exp2_approx(m_run - mrow);
-          m_run = mrow;
-          l_h *= alpha;
+            for (int g = 0; g < 2; ++g)
+              *reinterpret_cast<uint4*>(sP + (prow ^ ((col / 8 + g) << 4))) =
+                  make_uint4(pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
+            if (half == 0 && hh == 0) {
+              const float f = t == 0 ? 1.f : alpha;      // the piece's first P V overwrites O
+              st_async_b32(peer_alpha + (sb * kRows + i) * 4, __float_as_uint(f), peer_pfull + sb * 8);
+              sAlpha[sb * kRows + i] = f;
+            }
+            // A tile with keys that no row of the block sees: their values must
+            // not enter P V (0 x NaN).  The score product has read the tile.
+            if (!kE4m3 && (base + kBK > it.kend || (base < it.wlo && base + kBK > a.p.n_sink))) {
+              uint8_t* stage = sLat + (u % kLatStages) * kLatStage;
+              for (int q = threadIdx.x; q < kBK * 32; q += 256)
+                if (!key_visible(a, it, base + (q >> 5)))
+                  *reinterpret_cast<uint4*>(stage + ((q >> 3) & 3) * kChunk + (q >> 5) * 128 + (q & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async();
+          }
         }
-        const float mb = m_run == -INFINITY ? 0.f : m_run;
-        uint32_t pk[16];
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float p0 = tc::exp2_approx(fmaf(s[2 * e], c2, -mb)), p1 = tc::exp2_approx(fmaf(s[2 * e + 1], c2, -mb));
-          ls[e & 3] += p0 + p1;
-          pk[e] = pack_f16x2(p0, p1);
+        if (half == 1) {
+          named_bar_arrive(kBarP + q4, 64);
+        } else {
+          tc::named_bar_sync(kBarP + q4, 64);
+          if (!dead && lane == 0) {
+            const uint32_t off = sb * kPBytes + (32 * q4 + 16 * rank) * 128;    // the 16 rows, 128 bytes each
+            bulk_to_peer(peer_p + off, smem_u32(sP) + off, 16 * 128, peer_pfull + sb * 8);
+            mbar_arrive(&B.p_full[sb]);
+          }
         }
-        l_h += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-        // The P buffers and factors of tile u - 2 have been used in both CTAs.
-        if (u >= 2) ok = wait_cl(&B.pv_done[sb], ((u >> 1) - 1) & 1, a);
-        if (!ok) break;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint4 v = make_uint4(pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
-          const uint32_t off = sb * kPBytes + unit128(i, 4 * hh + g);
-          *reinterpret_cast<uint4*>(sP + off) = v;
-          tc::st_async_v4(peer_p + off, v, peer_pfull + sb * 8);
-        }
+      }
+      // Row sums to both CTAs' output warps.  Slot k % 4 is free: the last P V
+      // waited for followed the output of piece k - 3.
+      float l_row = l_h + __shfl_xor_sync(0xffffffffu, l_h, 16);
+      if (half == 1 && hh == 0) sM[(2 * (u & 1) + 1) * kOwn + lrow] = l_row;     // free: tile u - 2's maxima
+      tc::named_bar_sync(kBarMax + q4, 64);
+      if (half == 0 && !dead) {
         if (hh == 0) {
-          const float f = t == 0 ? 1.f : alpha;      // the piece's first P V overwrites O
-          sAlpha[sb * kRows + i] = f;
-          st_async_b32(peer_alpha + (sb * kRows + i) * 4, __float_as_uint(f), peer_pfull + sb * 8);
+          l_row += sM[(2 * (u & 1) + 1) * kOwn + lrow];
+          sL[(k & 3) * kRows + i] = l_row;
+          st_async_b32(peer_l + ((k & 3) * kRows + i) * 4, __float_as_uint(l_row), peer_lfull + (k & 3) * 8);
+          if (!it.whole() && rvalid) {
+            float* ml = a.ws_ml + 2 * ((2 * static_cast<int64_t>(c) + (it.t_lo > 0 ? 0 : 1)) * kRows + i);
+            ml[0] = m_run;
+            ml[1] = l_row;
+          }
         }
-        // A tile with keys that no row of the block sees: their values must
-        // not enter P V (0 x NaN).  The score product has read the tile.
-        if (!kE4m3 && (base + kBK > it.kend || (base < it.wlo && base + kBK > a.p.n_sink))) {
-          uint8_t* stage = sLat + (u % kLatStages) * kLatStage;
-          for (int q = threadIdx.x; q < kBK * 32; q += 128)
-            if (!key_visible(a, it, base + (q >> 5)))
-              *reinterpret_cast<uint4*>(stage + ((q >> 3) & 3) * kChunk + (q >> 5) * 128 + (q & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.p_full[sb]);
+        if (lane == 0) mbar_arrive(&B.l_full[k & 3]);
       }
-      if (!ok) break;
-      // Row sums to both CTAs' output warps.  Slot k % 4 is free: the P V this
-      // warp last waited for followed the output of piece k - 3 at least.
-      const float l_row = l_h + __shfl_xor_sync(0xffffffffu, l_h, 16);
-      if (hh == 0) {
-        sL[(k & 3) * kRows + i] = l_row;
-        st_async_b32(peer_l + ((k & 3) * kRows + i) * 4, __float_as_uint(l_row), peer_lfull + (k & 3) * 8);
-        if (!it.whole() && rvalid) {
-          float* ml = a.ws_ml + 2 * ((2 * static_cast<int64_t>(c) + (it.t_lo > 0 ? 0 : 1)) * kRows + i);
-          ml[0] = m_run;
-          ml[1] = l_row;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B.l_full[k & 3]);
+      // (The sums read above are overwritten by tile u's maxima at the earliest.)
+      tc::named_bar_sync(kBarMax + q4, 64);
       ++k;
     }
   } else if (warp < kOutWarp) {
@@ -664,9 +723,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int64_t qrow = it.qrow0 + i;
         const uint4* src = reinterpret_cast<const uint4*>(a.p.q_lat + qrow * kLatent + 256 * rank);
         const uint4* qp = reinterpret_cast<const uint4*>(a.p.q_pe + qrow * kRope) + 4 * rank;
-        uint4 qpe[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) qpe[v] = rvalid ? __ldg(qp + v) : make_uint4(0, 0, 0, 0);
 #pragma unroll 1
         for (int h2 = 0; h2 < 2; ++h2) {
           uint32_t r[2][32];
@@ -681,6 +737,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           for (int cc = 0; cc < 2; ++cc)
             tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ + 32 * (2 * h2 + cc), r[cc]);
         }
+        uint4 qpe[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) qpe[v] = rvalid ? __ldg(qp + v) : make_uint4(0, 0, 0, 0);
         tc::tmem_st_wait();
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -858,7 +917,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int ls = u % kLatStages, sb = u & 1;
         ok = wait_cl(&B.p_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&B.p_full[sb], kPTx);       // tile u + 2
+        if (lane == 0) {               // tile u + 2's P, and its scores: this tile's have been read
+          mbar_arrive_expect_tx(&B.p_full[sb], kPTx);
+          mbar_arrive_expect_tx(&B.x_full[sb], kXBytes);
+        }
         if (t == 0) {
           if (n > 0) ok = wait_all(&B.cmd_done, (n - 1) & 1, a);          // the previous output has left O
         } else {
@@ -901,13 +963,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       int row = a.n_rows;
       if (mine && any_visible(a, cur.it, key, box)) {
         const int64_t x = a.p.c.row_of(cur.it.b, key);
-        if (x >= 0) {
+        if (x >= 0)
           row = static_cast<int>(x);
-          if (ch == 4)                 // the whole rows of the box on their way into L2
-            tc::prefetch_l2(a.p.c.pages + x * kRowF16, static_cast<uint32_t>(min(box, cur.it.kend - key)) * kRowF16);
-        } else {
+        else
           record_error(a.p.err, MLA_ERR_INVALID_ARG);
-        }
       }
       if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
       if (!ok) break;

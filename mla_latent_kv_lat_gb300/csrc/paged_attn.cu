@@ -26,9 +26,9 @@
 //     share a tile's softmax (16 keys of a row per thread), and P goes to the
 //     peer as one bulk copy of 2 KB per 16 rows.
 //   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
-//   * fp16 pages come in by TMA as they are.  e4m3 pages are read, turned into
-//     fp16 (code x scale, exact) and stored in the same layout by producer
-//     warps.
+//   * fp16 pages come in by TMA as they are, and so do the RoPE parts of e4m3
+//     pages; their codes are read, turned into fp16 (code x scale, exact) and
+//     stored in the same layout by producer warps.
 // Work split: a block costs its tiles plus `kPieceCost`; the costs of all
 // blocks form one run, which the clusters share evenly.  A cluster's piece that
 // is a whole block writes o_lat; a block cut by a cluster boundary leaves fp32
@@ -70,15 +70,16 @@ constexpr int kSmem = 1024 + kOffBar + kBarBytes;
 static_assert(kSmem <= 232448, "shared memory");
 
 // Warp roles: softmax 0-3 (keys 0-31 of a tile) and 4-7 (keys 32-63), senders
-// (and Q loads) 8-11, output 12-15, score MMAs 16, P V MMAs 17, then the loader:
-// one TMA warp, or the e4m3 producers.
-constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18;
+// (and Q loads) 8-11, output 12-15, score MMAs 16, P V MMAs 17, TMA loads 18, and
+// for e4m3 pages the producers.
+constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18, kProdWarp = 19;
 // Named barriers of the warp pair (q, q + 4) that shares 16 rows.
 constexpr int kBarMax = 1;                   // + q: the halves' row maxima (and row sums) are in sM
 constexpr int kBarP = 5;                     // + q: both halves' P is in shared memory
-constexpr int kProducerWarps = 6;
-__host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kLoadWarp + (e4m3 ? kProducerWarps : 1)); }
-// 19 warps: 5 per sub-partition, 96 registers a thread; 24 warps: 6, 80.
+constexpr int kProducerWarps = 4;
+constexpr int kPrefetchTiles = 8;            // e4m3: rows on their way into L2 ahead of the producers
+__host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kProdWarp + (e4m3 ? kProducerWarps : 0)); }
+// 19 warps: 5 per sub-partition, 96 registers a thread; 23 warps: 6, 80.
 __host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 80 : 96; }
 
 constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
@@ -343,84 +344,61 @@ MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
 }
 
 // ---------------------------------------------------------------------------
-// e4m3 producer: one tile of this CTA's half of the rows into its stage.  Units
-// of 16 bytes, dealt so that a warp's load reads 4 keys x 128 contiguous codes:
-// 1024 code units (64 keys x 16), then 256 RoPE units (64 keys x 4), which are
-// fp16 already.  Rows that no row of the block sees are not read and become
-// zero.  A tile's 64 keys come from at most four pages (pages hold at least 16
-// rows): lane j < 4 of each warp holds the pool row of key 16 j.
+// e4m3 producer: this CTA's 256 codes of a tile's 64 rows into its stage, as
+// fp16.  Thread pt (of 128) takes 16 codes of key pt / 8 + 16 j, at 16 (pt % 8)
+// + 128 h, for j < 4 and h < 2: a warp's load reads 4 keys x 128 contiguous
+// codes, all offsets but the row's are constants, and group j's 16 keys lie in
+// one page (pages hold at least 16 rows).  Rows that no row of the block sees
+// are not read and become zero.
 // ---------------------------------------------------------------------------
 struct Producer {
-  static constexpr int NT = kProducerWarps * 32;
-  static constexpr int kCodeUnits = kBK * 16, kUnits = kCodeUnits + kBK * 4;
-  static constexpr int NU = (kUnits + NT - 1) / NT;
-  uint4 v[NU];
-  uint32_t d[NU];
-
-  // Unit idx: key, byte offset in the row, scale byte offset in the row.
-  MLA_DEVINL static void unit_of(int idx, int rank, int& key, int& src, int& sc, uint32_t& dst) {
-    if (idx < kCodeUnits) {
-      key = (idx >> 3) & (kBK - 1);
-      const int cu = ((idx >> 9) << 3) + (idx & 7);
-      src = 256 * rank + 16 * cu;
-      sc = kE4m3ScaleOff + 8 * rank + (cu >> 1);
-      dst = (cu >> 2) * kChunk + unit128(key, 2 * (cu & 3));
-    } else {
-      key = (idx - kCodeUnits) >> 2;
-      const int u = idx & 3;
-      src = kE4m3RopeOff + 2 * kRopeHalf * rank + 16 * u;
-      sc = 0;
-      dst = unit64(key, u);
-    }
-  }
+  uint4 v[8];
+  uint32_t d[8];
 
   MLA_DEVINL void load(const TcArgs& a, const Item& it, int kt, int rank, int pt, int lane) {
-    __builtin_assume(pt >= 0 && pt < NT);
     const int base = kt * kBK;
     int32_t row = -1;
     if (lane < 4 && any_visible(a, it, base + 16 * lane, 16)) {
       row = static_cast<int32_t>(a.p.c.row_of(it.b, base + 16 * lane));
       if (row < 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
     }
+    const int k0 = pt >> 3, c0 = pt & 7;
 #pragma unroll
-    for (int t = 0; t < NU; ++t) {
-      const int idx = pt + t * NT;
-      int key, src, sc;
-      uint32_t dst;
-      unit_of(idx, rank, key, src, sc, dst);
-      const int32_t r = __shfl_sync(0xffffffffu, row, (key >> 4) & 3);
-      v[t] = make_uint4(0, 0, 0, 0);
-      d[t] = 112u;
-      if (idx < kUnits && r >= 0 && key_visible(a, it, base + key)) {
-        const uint8_t* p = a.p.c.pages + static_cast<int64_t>(r + (key & 15)) * kRowE4m3;
-        v[t] = __ldg(reinterpret_cast<const uint4*>(p + src));
-        if (idx < kCodeUnits) d[t] = __ldg(p + sc);
+    for (int j = 0; j < 4; ++j) {
+      const int32_t r = __shfl_sync(0xffffffffu, row, j);
+      const bool see = r >= 0 && key_visible(a, it, base + 16 * j + k0);
+      const uint8_t* p = a.p.c.pages + static_cast<int64_t>(r + k0) * kRowE4m3 + 256 * rank + 16 * c0;
+      const uint8_t* sc = a.p.c.pages + static_cast<int64_t>(r + k0) * kRowE4m3 + kE4m3ScaleOff + 8 * rank + (c0 >> 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v[2 * j + h] = make_uint4(0, 0, 0, 0);
+        d[2 * j + h] = 112u;
+        if (see) {
+          v[2 * j + h] = __ldg(reinterpret_cast<const uint4*>(p + 128 * h));
+          d[2 * j + h] = __ldg(sc + 4 * h);
+        }
       }
     }
   }
 
-  MLA_DEVINL void store(uint8_t* lat, uint8_t* rope, int rank, int pt) const {
-    __builtin_assume(pt >= 0 && pt < NT);
+  MLA_DEVINL void store(uint8_t* lat, int pt) const {
+    const int k0 = pt >> 3, c0 = pt & 7;
+    const uint32_t dst = (c0 >> 2) * kChunk + unit128(k0, 2 * (c0 & 3));
 #pragma unroll
-    for (int t = 0; t < NU; ++t) {
-      const int idx = pt + t * NT;
-      if (idx >= kUnits) break;
-      int key, src, sc;
-      uint32_t dst;
-      unit_of(idx, rank, key, src, sc, dst);
-      if (idx < kCodeUnits) {
-        const uint32_t s = e4m3_scale_f16x2(d[t]);
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x = v[2 * j + h];
+        const uint32_t s = e4m3_scale_f16x2(d[2 * j + h]);
         uint4 lo, hi;
-        e4m3x4_to_f16x4(v[t].x, s, lo.x, lo.y);
-        e4m3x4_to_f16x4(v[t].y, s, lo.z, lo.w);
-        e4m3x4_to_f16x4(v[t].z, s, hi.x, hi.y);
-        e4m3x4_to_f16x4(v[t].w, s, hi.z, hi.w);
-        *reinterpret_cast<uint4*>(lat + dst) = lo;
-        *reinterpret_cast<uint4*>(lat + (dst ^ 16u)) = hi;
-      } else {
-        *reinterpret_cast<uint4*>(rope + dst) = v[t];
+        e4m3x4_to_f16x4(x.x, s, lo.x, lo.y);
+        e4m3x4_to_f16x4(x.y, s, lo.z, lo.w);
+        e4m3x4_to_f16x4(x.z, s, hi.x, hi.y);
+        e4m3x4_to_f16x4(x.w, s, hi.z, hi.w);
+        uint8_t* q = lat + 2 * kChunk * h + 16 * 128 * j;
+        *reinterpret_cast<uint4*>(q + dst) = lo;
+        *reinterpret_cast<uint4*>(q + (dst ^ 16u)) = hi;
       }
-    }
   }
 };
 
@@ -724,18 +702,14 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const uint4* src = reinterpret_cast<const uint4*>(a.p.q_lat + qrow * kLatent + 256 * rank);
         const uint4* qp = reinterpret_cast<const uint4*>(a.p.q_pe + qrow * kRope) + 4 * rank;
 #pragma unroll 1
-        for (int h2 = 0; h2 < 2; ++h2) {
-          uint32_t r[2][32];
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t r[32];
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const uint4 x = rvalid ? __ldg(src + (2 * h2 + cc) * 8 + v) : make_uint4(0, 0, 0, 0);
-              r[cc][4 * v] = x.x; r[cc][4 * v + 1] = x.y; r[cc][4 * v + 2] = x.z; r[cc][4 * v + 3] = x.w;
-            }
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
-            tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ + 32 * (2 * h2 + cc), r[cc]);
+          for (int v = 0; v < 8; ++v) {
+            const uint4 x = rvalid ? __ldg(src + cc * 8 + v) : make_uint4(0, 0, 0, 0);
+            r[4 * v] = x.x; r[4 * v + 1] = x.y; r[4 * v + 2] = x.z; r[4 * v + 3] = x.w;
+          }
+          tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ + 32 * cc, r);
         }
         uint4 qpe[4];
 #pragma unroll
@@ -878,7 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       for (int t = 0; ok && t < it.n_tiles; ++t, ++u) {
         const int ls = u % kLatStages, rs = u % kRopeStages, sb = u & 1;
         ok = wait_all(&B.lat_full[ls], (u / kLatStages) & 1, a);
-        if (!kE4m3) ok = ok && wait_all(&B.rope_full[rs], (u / kRopeStages) & 1, a);
+        ok = ok && wait_all(&B.rope_full[rs], (u / kRopeStages) & 1, a);
         if (u >= 2) ok = ok && wait_all(&B.s_free[sb], ((u >> 1) - 1) & 1, a);
         if (!ok) break;
         tc::fence_after_sync();
@@ -946,16 +920,33 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       post(-1);
     }
     if (ok) post(-2);
-  } else if constexpr (!kE4m3) {
+  } else if (warp == kLoadWarp) {
     // ============================== TMA loader =================================
     // Lane 5 j + c: chunk c (four of 64 latent dims, then the RoPE half) of box
     // j, the part of the tile that lies in one page.  A box without a visible
-    // row is loaded from behind the last row, which reads as zero.
+    // row is loaded from behind the last row, which reads as zero.  (e4m3: the
+    // RoPE boxes, and the whole rows some tiles ahead on their way into L2.)
     const int shift = min(6, a.p.c.page_shift), box = 1 << shift, nb = kBK >> shift;
     const int j = lane / 5, ch = lane % 5;
     const bool mine = j < nb;
-    Cursor cur;
+    Cursor cur, ahead;
     cur.init(a, B.st);
+    auto prefetch = [&] {
+      if (rank == 0 && lane < nb) {
+        const int key = ahead.it.key_tile(ahead.t) * kBK + lane * box;
+        if (any_visible(a, ahead.it, key, box)) {
+          const int64_t x = a.p.c.row_of(ahead.it.b, key);
+          if (x >= 0)
+            tc::prefetch_l2(a.p.c.pages + x * kRowE4m3,
+                            static_cast<uint32_t>(min(box, ahead.it.kend - key)) * kRowE4m3);
+        }
+      }
+      ahead.next(a);
+    };
+    if (kE4m3) {
+      ahead = cur;
+      for (int d = 0; d < kPrefetchTiles && ahead.more; ++d) prefetch();
+    }
 #pragma unroll 1
     for (int u = 0; ok && cur.more; ++u, cur.next(a)) {
       const int ls = u % kLatStages, rs = u % kRopeStages;
@@ -968,35 +959,38 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         else
           record_error(a.p.err, MLA_ERR_INVALID_ARG);
       }
-      if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
-      __syncwarp();
-      if (mine && ch < 4)
-        tc::tma_load_3d(sLat + ls * kLatStage + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls],
-                        256 * static_cast<int>(rank) + 64 * ch, row, 0);
+      if (kE4m3) {
+        if (ahead.more) prefetch();
+      } else {
+        if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
+        __syncwarp();
+        if (mine && ch < 4)
+          tc::tma_load_3d(sLat + ls * kLatStage + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls],
+                          256 * static_cast<int>(rank) + 64 * ch, row, 0);
+      }
       if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
       __syncwarp();
       if (mine && ch == 4)
         tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs],
-                        kLatent + kRopeHalf * static_cast<int>(rank), row, 0);
+                        (kE4m3 ? 0 : kLatent) + kRopeHalf * static_cast<int>(rank), row, 0);
     }
-  } else {
+  } else if constexpr (kE4m3) {
     // ============================ e4m3 producers ===============================
-    const int pt = static_cast<int>(threadIdx.x) - kLoadWarp * 32;
+    const int pt = static_cast<int>(threadIdx.x) - kProdWarp * 32;
     Cursor cur;
     cur.init(a, B.st);
     Producer x;
     if (cur.more) x.load(a, cur.it, cur.it.key_tile(cur.t), static_cast<int>(rank), pt, lane);
 #pragma unroll 1
     for (int u = 0; cur.more; ++u) {
-      const int ls = u % kLatStages, rs = u % kRopeStages;
+      const int ls = u % kLatStages;
       if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
-      if (u >= kRopeStages) ok = ok && wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
       if (!ok) break;
-      x.store(sLat + ls * kLatStage, sRope + rs * kRopeChunk, static_cast<int>(rank), pt);
+      x.store(sLat + ls * kLatStage, pt);
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.lat_full[ls]);
@@ -1108,15 +1102,17 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   a.rec = reinterpret_cast<Rec*>(a.ws_ml + rows * 2);
   a.n_slots = static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
   a.n_rows = p.c.n_pages << p.c.page_shift;
+  // The latent parts of fp16 pages, and the RoPE parts of either type (fp16).
   CUtensorMap tm, tr;
+  memset(&tm, 0, sizeof(tm));
+  const uint32_t box = static_cast<uint32_t>(min(kBK, 1 << p.c.page_shift));
+  const uint64_t n = static_cast<uint64_t>(a.n_rows);
   cudaError_t e;
   if (p.c.e4m3) {
-    memset(&tm, 0, sizeof(tm));
-    memset(&tr, 0, sizeof(tr));
+    e = make_tmap_3d(&tr, p.c.pages + kE4m3RopeOff, false, kRope, n, 1, kRowE4m3, n * kRowE4m3, kRopeHalf, box, 1, 64);
+    if (e != cudaSuccess) return e;
     e = launch_one<true>(tm, tr, a, stream);
   } else {
-    const uint32_t box = static_cast<uint32_t>(min(kBK, 1 << p.c.page_shift));
-    const uint64_t n = static_cast<uint64_t>(a.n_rows);
     e = make_tmap_3d(&tm, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, 64, box, 1);
     if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);

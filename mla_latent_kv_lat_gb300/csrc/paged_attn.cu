@@ -76,11 +76,11 @@ constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWar
 // Named barriers of the warp pair (q, q + 4) that shares 16 rows.
 constexpr int kBarMax = 1;                   // + q: the halves' row maxima (and row sums) are in sM
 constexpr int kBarP = 5;                     // + q: both halves' P is in shared memory
-constexpr int kProducerWarps = 4;
+constexpr int kProducerWarps = 8;
 constexpr int kPrefetchTiles = 8;            // e4m3: rows on their way into L2 ahead of the producers
 __host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kProdWarp + (e4m3 ? kProducerWarps : 0)); }
-// 19 warps: 5 per sub-partition, 96 registers a thread; 23 warps: 6, 80.
-__host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 80 : 96; }
+// 19 warps: 5 per sub-partition, 96 registers a thread; 27 warps: 7, 72.
+__host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 72 : 96; }
 
 constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
@@ -345,38 +345,38 @@ MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
 
 // ---------------------------------------------------------------------------
 // e4m3 producer: this CTA's 256 codes of a tile's 64 rows into its stage, as
-// fp16.  Thread pt (of 128) takes 16 codes of key pt / 8 + 16 j, at 16 (pt % 8)
-// + 128 h, for j < 4 and h < 2: a warp's load reads 4 keys x 128 contiguous
-// codes, all offsets but the row's are constants, and group j's 16 keys lie in
-// one page (pages hold at least 16 rows).  Rows that no row of the block sees
-// are not read and become zero.
+// fp16.  Thread pt (of 256) takes 16 codes of key pt / 8 + 32 j, at 16 (pt % 8)
+// + 128 h, for j, h < 2: a warp's load reads 4 keys x 128 contiguous codes, and
+// all offsets but the row's are constants.  The 8 scale bytes of the row's half
+// come in one load.  Keys 16 g .. 16 g + 15 lie in one page (pages hold at least
+// 16 rows); lane g < 4 of each warp looks up their first pool row, a tile ahead.
+// Rows that no row of the block sees are not read and become zero.
 // ---------------------------------------------------------------------------
 struct Producer {
-  uint4 v[8];
-  uint32_t d[8];
+  uint4 v[4];
+  uint2 d[2];
 
-  MLA_DEVINL void load(const TcArgs& a, const Item& it, int kt, int rank, int pt, int lane) {
-    const int base = kt * kBK;
+  MLA_DEVINL static int32_t lookup(const TcArgs& a, const Item& it, int kt, int lane) {
     int32_t row = -1;
-    if (lane < 4 && any_visible(a, it, base + 16 * lane, 16)) {
-      row = static_cast<int32_t>(a.p.c.row_of(it.b, base + 16 * lane));
+    if (lane < 4 && any_visible(a, it, kt * kBK + 16 * lane, 16)) {
+      row = static_cast<int32_t>(a.p.c.row_of(it.b, kt * kBK + 16 * lane));
       if (row < 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
     }
+    return row;
+  }
+
+  MLA_DEVINL void load(const TcArgs& a, const Item& it, int kt, int32_t row, int rank, int pt) {
     const int k0 = pt >> 3, c0 = pt & 7;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int32_t r = __shfl_sync(0xffffffffu, row, j);
-      const bool see = r >= 0 && key_visible(a, it, base + 16 * j + k0);
-      const uint8_t* p = a.p.c.pages + static_cast<int64_t>(r + k0) * kRowE4m3 + 256 * rank + 16 * c0;
-      const uint8_t* sc = a.p.c.pages + static_cast<int64_t>(r + k0) * kRowE4m3 + kE4m3ScaleOff + 8 * rank + (c0 >> 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v[2 * j + h] = make_uint4(0, 0, 0, 0);
-        d[2 * j + h] = 112u;
-        if (see) {
-          v[2 * j + h] = __ldg(reinterpret_cast<const uint4*>(p + 128 * h));
-          d[2 * j + h] = __ldg(sc + 4 * h);
-        }
+    for (int j = 0; j < 2; ++j) {
+      const int32_t r = __shfl_sync(0xffffffffu, row, (k0 >> 4) + 2 * j);
+      const uint8_t* p = a.p.c.pages + static_cast<int64_t>(r + (k0 & 15)) * kRowE4m3 + 256 * rank + 16 * c0;
+      v[2 * j] = v[2 * j + 1] = make_uint4(0, 0, 0, 0);
+      d[j] = make_uint2(0x70707070u, 0x70707070u);
+      if (r >= 0 && key_visible(a, it, kt * kBK + 32 * j + k0)) {
+        v[2 * j] = __ldg(reinterpret_cast<const uint4*>(p));
+        v[2 * j + 1] = __ldg(reinterpret_cast<const uint4*>(p + 128));
+        d[j] = __ldg(reinterpret_cast<const uint2*>(p + (kE4m3ScaleOff - 248 * rank - 16 * c0)));
       }
     }
   }
@@ -385,17 +385,17 @@ struct Producer {
     const int k0 = pt >> 3, c0 = pt & 7;
     const uint32_t dst = (c0 >> 2) * kChunk + unit128(k0, 2 * (c0 & 3));
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint4 x = v[2 * j + h];
-        const uint32_t s = e4m3_scale_f16x2(d[2 * j + h]);
+        const uint32_t s = e4m3_scale_f16x2(((h ? d[j].y : d[j].x) >> (8 * (c0 >> 1))) & 0xFFu);
         uint4 lo, hi;
         e4m3x4_to_f16x4(x.x, s, lo.x, lo.y);
         e4m3x4_to_f16x4(x.y, s, lo.z, lo.w);
         e4m3x4_to_f16x4(x.z, s, hi.x, hi.y);
         e4m3x4_to_f16x4(x.w, s, hi.z, hi.w);
-        uint8_t* q = lat + 2 * kChunk * h + 16 * 128 * j;
+        uint8_t* q = lat + 2 * kChunk * h + 32 * 128 * j;
         *reinterpret_cast<uint4*>(q + dst) = lo;
         *reinterpret_cast<uint4*>(q + (dst ^ 16u)) = hi;
       }
@@ -561,7 +561,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int base = it.key_tile(t) * kBK, k0 = base + col;
         float s[16];
         float mrow = -INFINITY;
-        if (!dead) dead = !wait_all(&B.s_full[sb], ph, a);
+        // The three barriers of a tile are tested together, so that their
+        // latencies overlap; one that is not complete yet is waited for where
+        // it is needed.
+        const bool s_test = mbar_test(&B.s_full[sb], ph), x_test = tc::mbar_test_cluster(&B.x_full[sb], ph);
+        const bool p_test = u < 2 || tc::mbar_test_cluster(&B.pv_done[sb], ((u >> 1) - 1) & 1);
+        if (!dead && !__all_sync(0xffffffffu, s_test)) dead = !wait_all(&B.s_full[sb], ph, a);
         if (!dead) {
           tc::fence_after_sync();
           uint32_t r[16];
@@ -570,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&B.s_free[sb]);
-          dead = !wait_cl(&B.x_full[sb], ph, a);
+          if (!__all_sync(0xffffffffu, x_test)) dead = !wait_cl(&B.x_full[sb], ph, a);
 #pragma unroll
           for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(r[e]);
         }
@@ -625,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           }
           l_h += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           // The P buffer and the factors of tile u - 2 have been used in both CTAs.
-          if (u >= 2) dead = !wait_cl(&B.pv_done[sb], ((u >> 1) - 1) & 1, a);
+          if (!__all_sync(0xffffffffu, p_test)) dead = !wait_cl(&B.pv_done[sb], ((u >> 1) - 1) & 1, a);
           if (!dead) {
             const uint32_t prow = sb * kPBytes + unit128(i, 0);
 #pragma unroll
@@ -959,6 +964,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         else
           record_error(a.p.err, MLA_ERR_INVALID_ARG);
       }
+      if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
+      __syncwarp();
+      if (mine && ch == 4)
+        tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs],
+                        (kE4m3 ? 0 : kLatent) + kRopeHalf * static_cast<int>(rank), row, 0);
       if (kE4m3) {
         if (ahead.more) prefetch();
       } else {
@@ -970,32 +982,27 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           tc::tma_load_3d(sLat + ls * kLatStage + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls],
                           256 * static_cast<int>(rank) + 64 * ch, row, 0);
       }
-      if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
-      __syncwarp();
-      if (mine && ch == 4)
-        tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs],
-                        (kE4m3 ? 0 : kLatent) + kRopeHalf * static_cast<int>(rank), row, 0);
     }
   } else if constexpr (kE4m3) {
     // ============================ e4m3 producers ===============================
     const int pt = static_cast<int>(threadIdx.x) - kProdWarp * 32;
-    Cursor cur;
-    cur.init(a, B.st);
     Producer x;
-    if (cur.more) x.load(a, cur.it, cur.it.key_tile(cur.t), static_cast<int>(rank), pt, lane);
+    int u = 0;
 #pragma unroll 1
-    for (int u = 0; cur.more; ++u) {
-      const int ls = u % kLatStages;
-      if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
-      if (!ok) break;
-      x.store(sLat + ls * kLatStage, pt);
-      tc::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B.lat_full[ls]);
-      cur.next(a);
-      if (cur.more) x.load(a, cur.it, cur.it.key_tile(cur.t), static_cast<int>(rank), pt, lane);
+    while (ok && items.next(a, it)) {
+      int32_t row = Producer::lookup(a, it, it.key_tile(0), lane);
+#pragma unroll 1
+      for (int t = 0; t < it.n_tiles; ++t, ++u) {
+        const int ls = u % kLatStages;
+        x.load(a, it, it.key_tile(t), row, static_cast<int>(rank), pt);
+        if (t + 1 < it.n_tiles) row = Producer::lookup(a, it, it.key_tile(t + 1), lane);
+        if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
+        if (!ok) break;
+        x.store(sLat + ls * kLatStage, pt);
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.lat_full[ls]);
+      }
     }
   }
 

@@ -23,8 +23,8 @@
 //     twice the exponentials, and rounds the scores.)
 //   * A tile stays in its stage from its load to its P V, so the chain of steps
 //     between them, not any unit's throughput, bounds the pace: eight warps
-//     share a tile's softmax (16 keys of a row per thread), and P goes to the
-//     peer as one bulk copy of 2 KB per 16 rows.
+//     share a tile's softmax (16 keys of a row per thread), and a warp's P goes to
+//     the peer as one bulk copy.
 //   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
 //   * fp16 pages come in by TMA as they are, and so do the RoPE parts of e4m3
 //     pages; their codes are read, turned into fp16 (code x scale, exact) and
@@ -53,7 +53,7 @@ constexpr int kRopeStages = 2;               // a RoPE tile is done with after i
 constexpr int kRopeHalf = 32;
 constexpr int kRopeChunk = kBK * kRopeHalf * 2;     // 4 KB
 constexpr int kQRopeBytes = kRows * kRopeHalf * 2;  // 8 KB
-constexpr int kPBytes = kRows * 128;         // 16 KB: 128 rows x 64 keys fp16
+constexpr int kPBytes = kRows * 128;         // 16 KB: two halves of 128 rows x 32 keys fp16
 constexpr int kXBytes = kOwn * kBK * 4;      // 16 KB: 64 rows x 64 keys fp32
 constexpr int kPTx = kOwn * kBK * 2 + kOwn * 4;     // bytes a CTA gets per tile: the other's P rows and factors
 constexpr int kOffLat = kQRopeBytes;
@@ -73,9 +73,7 @@ static_assert(kSmem <= 232448, "shared memory");
 // (and Q loads) 8-11, output 12-15, score MMAs 16, P V MMAs 17, TMA loads 18, and
 // for e4m3 pages the producers.
 constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18, kProdWarp = 19;
-// Named barriers of the warp pair (q, q + 4) that shares 16 rows.
-constexpr int kBarMax = 1;                   // + q: the halves' row maxima (and row sums) are in sM
-constexpr int kBarP = 5;                     // + q: both halves' P is in shared memory
+constexpr int kBarMax = 1;                   // + q, named: the row maxima (sums) of warps q and q + 4 are in sM
 constexpr int kProducerWarps = 8;
 constexpr int kPrefetchTiles = 8;            // e4m3: rows on their way into L2 ahead of the producers
 __host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kProdWarp + (e4m3 ? kProducerWarps : 0)); }
@@ -345,16 +343,17 @@ MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
 
 // ---------------------------------------------------------------------------
 // e4m3 producer: this CTA's 256 codes of a tile's 64 rows into its stage, as
-// fp16.  Thread pt (of 256) takes 16 codes of key pt / 8 + 32 j, at 16 (pt % 8)
-// + 128 h, for j, h < 2: a warp's load reads 4 keys x 128 contiguous codes, and
+// fp16.  Thread pt (of 8 kKeys) takes 16 codes of key pt / 8 + kKeys j, at 16 (pt
+// % 8) + 128 h, for h < 2: a warp's load reads 4 keys x 128 contiguous codes, and
 // all offsets but the row's are constants.  The 8 scale bytes of the row's half
 // come in one load.  Keys 16 g .. 16 g + 15 lie in one page (pages hold at least
 // 16 rows); lane g < 4 of each warp looks up their first pool row, a tile ahead.
 // Rows that no row of the block sees are not read and become zero.
 // ---------------------------------------------------------------------------
 struct Producer {
-  uint4 v[4];
-  uint2 d[2];
+  static constexpr int kKeys = 4 * kProducerWarps, J = kBK / kKeys;
+  uint4 v[2 * J];
+  uint2 d[J];
 
   MLA_DEVINL static int32_t lookup(const TcArgs& a, const Item& it, int kt, int lane) {
     int32_t row = -1;
@@ -368,12 +367,12 @@ struct Producer {
   MLA_DEVINL void load(const TcArgs& a, const Item& it, int kt, int32_t row, int rank, int pt) {
     const int k0 = pt >> 3, c0 = pt & 7;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int32_t r = __shfl_sync(0xffffffffu, row, (k0 >> 4) + 2 * j);
+    for (int j = 0; j < J; ++j) {
+      const int32_t r = __shfl_sync(0xffffffffu, row, (k0 + kKeys * j) >> 4);
       const uint8_t* p = a.p.c.pages + static_cast<int64_t>(r + (k0 & 15)) * kRowE4m3 + 256 * rank + 16 * c0;
       v[2 * j] = v[2 * j + 1] = make_uint4(0, 0, 0, 0);
       d[j] = make_uint2(0x70707070u, 0x70707070u);
-      if (r >= 0 && key_visible(a, it, kt * kBK + 32 * j + k0)) {
+      if (r >= 0 && key_visible(a, it, kt * kBK + kKeys * j + k0)) {
         v[2 * j] = __ldg(reinterpret_cast<const uint4*>(p));
         v[2 * j + 1] = __ldg(reinterpret_cast<const uint4*>(p + 128));
         d[j] = __ldg(reinterpret_cast<const uint2*>(p + (kE4m3ScaleOff - 248 * rank - 16 * c0)));
@@ -385,7 +384,7 @@ struct Producer {
     const int k0 = pt >> 3, c0 = pt & 7;
     const uint32_t dst = (c0 >> 2) * kChunk + unit128(k0, 2 * (c0 & 3));
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint4 x = v[2 * j + h];
@@ -395,7 +394,7 @@ struct Producer {
         e4m3x4_to_f16x4(x.y, s, lo.z, lo.w);
         e4m3x4_to_f16x4(x.z, s, hi.x, hi.y);
         e4m3x4_to_f16x4(x.w, s, hi.z, hi.w);
-        uint8_t* q = lat + 2 * kChunk * h + 32 * 128 * j;
+        uint8_t* q = lat + 2 * kChunk * h + kKeys * 128 * j;
         *reinterpret_cast<uint4*>(q + dst) = lo;
         *reinterpret_cast<uint4*>(q + (dst ^ 16u)) = hi;
       }
@@ -442,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       mbar_init(&B.s_free[i], 12);
       mbar_init(&B.x_full[i], 1);
       mbar_init(&B.x_empty[i], 8);
-      mbar_init(&B.p_full[i], 5);
+      mbar_init(&B.p_full[i], 9);
       mbar_init(&B.pv_done[i], 2);
     }
     mbar_init(&B.q_ready, 4);
@@ -561,11 +560,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int base = it.key_tile(t) * kBK, k0 = base + col;
         float s[16];
         float mrow = -INFINITY;
-        // The three barriers of a tile are tested together, so that their
-        // latencies overlap; one that is not complete yet is waited for where
-        // it is needed.
+        // Barriers are tested ahead of their use, so that their latencies
+        // overlap; one that is not complete yet is waited for there.
         const bool s_test = mbar_test(&B.s_full[sb], ph), x_test = tc::mbar_test_cluster(&B.x_full[sb], ph);
-        const bool p_test = u < 2 || tc::mbar_test_cluster(&B.pv_done[sb], ((u >> 1) - 1) & 1);
         if (!dead && !__all_sync(0xffffffffu, s_test)) dead = !wait_all(&B.s_full[sb], ph, a);
         if (!dead) {
           tc::fence_after_sync();
@@ -604,6 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           mrow = fmaxf(mown, __shfl_xor_sync(0xffffffffu, mown, 16));
           if (hh == 0) sM[(2 * sb + half) * kOwn + lrow] = mrow;
         }
+        const bool p_test = u < 2 || tc::mbar_test_cluster(&B.pv_done[sb], ((u >> 1) - 1) & 1);
         tc::named_bar_sync(kBarMax + q4, 64);
         if (!dead) {
           // Every value read from the exchange buffer went into the maximum, so
@@ -632,10 +630,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           // The P buffer and the factors of tile u - 2 have been used in both CTAs.
           if (!__all_sync(0xffffffffu, p_test)) dead = !wait_cl(&B.pv_done[sb], ((u >> 1) - 1) & 1, a);
           if (!dead) {
-            const uint32_t prow = sb * kPBytes + unit128(i, 0);
+            uint8_t* pt = sP + sb * kPBytes + half * (kPBytes / 2);
 #pragma unroll
             for (int g = 0; g < 2; ++g)
-              *reinterpret_cast<uint4*>(sP + (prow ^ ((col / 8 + g) << 4))) =
+              *reinterpret_cast<uint4*>(pt + unit64(i, 2 * hh + g)) =
                   make_uint4(pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
             if (half == 0 && hh == 0) {
               const float f = t == 0 ? 1.f : alpha;      // the piece's first P V overwrites O
@@ -652,16 +650,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
                       make_uint4(0, 0, 0, 0);
             }
             tc::fence_proxy_async();
-          }
-        }
-        if (half == 1) {
-          named_bar_arrive(kBarP + q4, 64);
-        } else {
-          tc::named_bar_sync(kBarP + q4, 64);
-          if (!dead && lane == 0) {
-            const uint32_t off = sb * kPBytes + (32 * q4 + 16 * rank) * 128;    // the 16 rows, 128 bytes each
-            bulk_to_peer(peer_p + off, smem_u32(sP) + off, 16 * 128, peer_pfull + sb * 8);
-            mbar_arrive(&B.p_full[sb]);
+            __syncwarp();
+            if (lane == 0) {                       // the warp's 16 rows x 64 bytes, to the peer too
+              const uint32_t off = sb * kPBytes + half * (kPBytes / 2) + (32 * q4 + 16 * rank) * 64;
+              bulk_to_peer(peer_p + off, smem_u32(sP) + off, 16 * 64, peer_pfull + sb * 8);
+              mbar_arrive(&B.p_full[sb]);
+            }
           }
         }
       }
@@ -734,6 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int sb = u & 1;
+        const bool x_test = u < 2 || tc::mbar_test_cluster(&B.x_empty[sb], ((u >> 1) - 1) & 1);
         ok = wait_all(&B.s_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
         tc::fence_after_sync();
@@ -743,7 +738,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.s_free[sb]);
-        if (u >= 2) ok = wait_cl(&B.x_empty[sb], ((u >> 1) - 1) & 1, a);
+        if (!__all_sync(0xffffffffu, x_test)) ok = wait_cl(&B.x_empty[sb], ((u >> 1) - 1) & 1, a);
         if (!ok) break;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
@@ -856,9 +851,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll 1
       for (int t = 0; ok && t < it.n_tiles; ++t, ++u) {
         const int ls = u % kLatStages, rs = u % kRopeStages, sb = u & 1;
+        // The last to complete is the tile, as a rule: the others are tested
+        // while it is awaited.
+        const bool r_test = mbar_test(&B.rope_full[rs], (u / kRopeStages) & 1);
+        const bool s_test = u < 2 || mbar_test(&B.s_free[sb], ((u >> 1) - 1) & 1);
         ok = wait_all(&B.lat_full[ls], (u / kLatStages) & 1, a);
-        ok = ok && wait_all(&B.rope_full[rs], (u / kRopeStages) & 1, a);
-        if (u >= 2) ok = ok && wait_all(&B.s_free[sb], ((u >> 1) - 1) & 1, a);
+        if (!__all_sync(0xffffffffu, r_test)) ok = ok && wait_all(&B.rope_full[rs], (u / kRopeStages) & 1, a);
+        if (!__all_sync(0xffffffffu, s_test)) ok = ok && wait_all(&B.s_free[sb], ((u >> 1) - 1) & 1, a);
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t k0 = smem_u32(sLat + ls * kLatStage), d = tmem + kTmS + sb * 64;
@@ -915,7 +914,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const uint32_t v0 = smem_u32(sLat + ls * kLatStage), p0 = smem_u32(sP + sb * kPBytes);
 #pragma unroll
         for (int ks = 0; ks < kBK / 16; ++ks)
-          tc::mma_ss_warp(tmem + kTmO, tc::sdesc_sw128(p0 + ks * 32, 16, 1024),
+          tc::mma_ss_warp(tmem + kTmO, tc::sdesc_sw64(p0 + (ks >> 1) * (kPBytes / 2) + (ks & 1) * 32),
                           tc::sdesc_sw128(v0 + ks * 2048, kChunk, 1024), idesc, (t > 0 || ks > 0) ? 1u : 0u);
         tc::mma_commit_warp(&B.lat_empty[ls]);
         mma_commit_pair_warp(&B.pv_done[sb]);

@@ -347,69 +347,86 @@ def mla_rope_append(c_kv, k_pe, pos, slot, kv=None, kv_q=None, kv_d=None, freq_b
     _check("mla_rope_append", st)
 
 
-def _paged(pages, block_table) -> MLAPagedCache:
+# The paged calls are made once per layer of a decode step, where their own time on the host counts: they check
+# with single comparisons and go through _need's detailed messages only when one fails.
+def _arg(t, name: str, dtype, shape, dev: int) -> int:
+    """Device address of a contiguous tensor of this type and shape on CUDA device ``dev``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, another tensor on cuda:{dev}")
+
+
+def _paged_device(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object around it
+
+
+def _stream_on(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _paged(pages, block_table, dev: int) -> MLAPagedCache:
     """The C description of a paged cache: pages fp16 [n_pages, page_size, 576] or uint8 [n_pages, page_size, 656],
     block_table int32 [B, max_pages] (rows may be further apart than max_pages)."""
     if not isinstance(pages, torch.Tensor) or pages.dtype not in (torch.float16, torch.uint8):
         raise TypeError("pages must be a torch.float16 or torch.uint8 tensor")
-    f16 = pages.dtype == torch.float16
-    if pages.dim() != 3 or pages.shape[2] != (ROW if f16 else ROW_E4M3):
-        raise ValueError(f"pages must have shape (n_pages, page_size, {ROW if f16 else ROW_E4M3}), got "
-                         f"{tuple(pages.shape)}")
-    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32:
+    f16 = pages.dtype is torch.float16
+    row = ROW if f16 else ROW_E4M3
+    if pages.dim() != 3 or pages.shape[2] != row:
+        raise ValueError(f"pages must have shape (n_pages, page_size, {row}), got {tuple(pages.shape)}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32:
         raise TypeError("block_table must be a torch.int32 tensor")
     if block_table.dim() != 2 or block_table.shape[0] < 1 or block_table.shape[1] < 1:
         raise ValueError("block_table must have shape (B, max_pages)")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    width, (stride, inner) = block_table.shape[1], block_table.stride()
+    if width > 1 and inner != 1:
         raise ValueError("block_table's rows must be contiguous")
-    if not block_table.is_cuda:
-        raise ValueError("block_table must be a CUDA tensor")
-    return MLAPagedCache(_need(pages, "pages", pages.dtype).value, block_table.data_ptr(), block_table.stride(0),
-                         block_table.shape[1], pages.shape[0], pages.shape[1], PAGE_F16 if f16 else PAGE_E4M3)
-
-
-def _one_device(**tensors):
-    """The CUDA device that all the given tensors (None skipped) share."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    return dev
+    if block_table.get_device() != dev:
+        raise ValueError(f"block_table is on {block_table.device}, another tensor on cuda:{dev}")
+    return MLAPagedCache(_arg(pages, "pages", pages.dtype, pages.shape, dev), block_table.data_ptr(), stride, width,
+                         pages.shape[0], pages.shape[1], PAGE_F16 if f16 else PAGE_E4M3)
 
 
 def mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base: float = 10000.0,
                      freq_scale: float = 0.025, stream=None):
     """New tokens' rows into their pages: token i of sequence b's n new ones (rows cu_new[b].. of c_kv, k_pe) is
     written at position seq_len[b] - n + i, its RoPE part rotated by that position, in the pages' type."""
-    with torch.cuda.device(_one_device(c_kv=c_kv, k_pe=k_pe, pages=pages, block_table=block_table, cu_new=cu_new,
-                                       seq_len=seq_len)):
-        T, Bn = c_kv.shape[0], block_table.shape[0]
-        st = load_library().mla_paged_append(
-            ctypes.byref(_paged(pages, block_table)), _need(c_kv, "c_kv", torch.bfloat16, (T, KV_LORA_RANK)),
-            _need(k_pe, "k_pe", torch.bfloat16, (T, QK_ROPE)), _need(cu_new, "cu_new", torch.int32, (Bn + 1,)),
-            _need(seq_len, "seq_len", torch.int32, (Bn,)), Bn, T, float(freq_base), float(freq_scale),
-            _stream(stream))
-        _check("mla_paged_append", st)
+    dev = _paged_device(c_kv, "c_kv")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base, freq_scale, stream)
+    cache = _paged(pages, block_table, dev)
+    T, Bn = c_kv.shape[0], block_table.shape[0]
+    st = load_library().mla_paged_append(
+        cache, _arg(c_kv, "c_kv", torch.bfloat16, (T, KV_LORA_RANK), dev),
+        _arg(k_pe, "k_pe", torch.bfloat16, (T, QK_ROPE), dev), _arg(cu_new, "cu_new", torch.int32, (Bn + 1,), dev),
+        _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn, T, freq_base, freq_scale, _stream_on(stream, dev))
+    _check("mla_paged_append", st)
 
 
 def mla_paged_gather(pages, block_table, row0, cu_rows, out, stream=None):
     """out [R, 576] (bf16 or fp16): rows cu_rows[b].. <- positions row0[b].. of sequence b (row0 None: from 0)."""
-    with torch.cuda.device(_one_device(pages=pages, block_table=block_table, row0=row0, cu_rows=cu_rows, out=out)):
-        R, Bn = out.shape[0], block_table.shape[0]
-        if out.dtype not in (torch.bfloat16, torch.float16):
-            raise TypeError(f"out must be torch.bfloat16 or torch.float16, got {out.dtype}")
-        st = load_library().mla_paged_gather(
-            ctypes.byref(_paged(pages, block_table)),
-            _need(row0, "row0", torch.int32, (Bn,)) if row0 is not None else None,
-            _need(cu_rows, "cu_rows", torch.int32, (Bn + 1,)), Bn, R, _need(out, "out", out.dtype, (R, ROW)),
-            int(out.dtype == torch.float16), _stream(stream))
-        _check("mla_paged_gather", st)
+    dev = _paged_device(out, "out")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return mla_paged_gather(pages, block_table, row0, cu_rows, out, stream)
+    cache = _paged(pages, block_table, dev)
+    R, Bn = out.shape[0], block_table.shape[0]
+    if out.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"out must be torch.bfloat16 or torch.float16, got {out.dtype}")
+    st = load_library().mla_paged_gather(
+        cache, _arg(row0, "row0", torch.int32, (Bn,), dev) if row0 is not None else None,
+        _arg(cu_rows, "cu_rows", torch.int32, (Bn + 1,), dev), Bn, R, _arg(out, "out", out.dtype, (R, ROW), dev),
+        out.dtype is torch.float16, _stream_on(stream, dev))
+    _check("mla_paged_gather", st)
 
 
 def mla_paged_workspace_size(n_head: int, scale=None) -> int:
@@ -422,19 +439,24 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
     """o_lat [T, H, 512]: attention of the batch's new tokens over their pages (one token a sequence or a chunk);
     window > 0 keeps each token's last ``window`` positions and the first ``n_sink``.  Without a workspace a fresh
     one is taken from PyTorch's allocator."""
-    with torch.cuda.device(_one_device(q_lat=q_lat, q_pe=q_pe, pages=pages, block_table=block_table, cu_q=cu_q,
-                                       seq_len=seq_len, o_lat=o_lat, workspace=workspace)):
-        T, H, Bn = q_lat.shape[0], q_lat.shape[1], block_table.shape[0]
-        d = make_dims(H, scale)
-        if workspace is None:
-            workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)
-        st = load_library().mla_attn_paged(
-            ctypes.byref(d), _need(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK)),
-            _need(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE)), ctypes.byref(_paged(pages, block_table)),
-            _need(cu_q, "cu_q", torch.int32, (Bn + 1,)), _need(seq_len, "seq_len", torch.int32, (Bn,)), Bn, T,
-            int(window), int(n_sink), _need(workspace, "workspace", torch.uint8), workspace.numel(),
-            _need(o_lat, "o_lat", torch.float16, (T, H, KV_LORA_RANK)), _stream(stream))
-        _check("mla_attn_paged", st)
+    dev = _paged_device(q_lat, "q_lat")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window, n_sink, workspace,
+                                  scale, stream)
+    cache = _paged(pages, block_table, dev)
+    if q_lat.dim() != 3:
+        raise ValueError(f"q_lat must have shape (T, H, {KV_LORA_RANK}), got {tuple(q_lat.shape)}")
+    (T, H, _), Bn = q_lat.shape, block_table.shape[0]
+    if workspace is None:
+        workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)
+    st = load_library().mla_attn_paged(
+        make_dims(H, scale), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
+        _arg(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE), dev), cache,
+        _arg(cu_q, "cu_q", torch.int32, (Bn + 1,), dev), _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn, T,
+        window, n_sink, _arg(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(),
+        _arg(o_lat, "o_lat", torch.float16, (T, H, KV_LORA_RANK), dev), _stream_on(stream, dev))
+    _check("mla_attn_paged", st)
 
 
 def mla_get_device_error(stream=None) -> int:

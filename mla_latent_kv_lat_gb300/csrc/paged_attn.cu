@@ -36,6 +36,8 @@
 // Every wait on a barrier is bounded.
 #include <string.h>
 
+#include <atomic>
+
 #include "kernels.cuh"
 #include "paged.cuh"
 #include "tc.cuh"
@@ -1085,8 +1087,16 @@ int clusters() { return max(1, device_sm_count() / 2); }
 template <bool kE4m3>
 cudaError_t launch_one(const CUtensorMap& tm, const CUtensorMap& tr, const TcArgs& a, cudaStream_t stream) {
   auto kern = paged_attn_kernel<kE4m3>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || (set.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   kern<<<dim3(2 * clusters()), threads(kE4m3), kSmem, stream>>>(tm, tr, a);
   return cudaGetLastError();
 }

@@ -79,17 +79,17 @@ def test_the_binding_refuses_what_the_library_cannot_see():
     with pytest.raises(ValueError, match="CUDA"):
         mla.mla_paged_gather(pages, table, None, torch.zeros(2, dtype=torch.int32), torch.zeros(1, 576).half())
     with pytest.raises(TypeError, match="float16 or torch.uint8"):
-        binding._paged(pages.float(), table)
+        binding._paged(pages.float(), table, -1)
     with pytest.raises(ValueError, match="576"):
-        binding._paged(pages[..., :500], table)
+        binding._paged(pages[..., :500], table, -1)
     with pytest.raises(ValueError, match="656"):
-        binding._paged(pages.view(torch.uint8), table)
+        binding._paged(pages.view(torch.uint8), table, -1)
     with pytest.raises(TypeError, match="int32"):
-        binding._paged(pages, table.long())
+        binding._paged(pages, table.long(), -1)
     with pytest.raises(ValueError, match="max_pages"):
-        binding._paged(pages, table[0])
+        binding._paged(pages, table[0], -1)
     with pytest.raises(ValueError, match="contiguous"):
-        binding._paged(pages, torch.zeros(4, 3, dtype=torch.int32).t())
+        binding._paged(pages, torch.zeros(4, 3, dtype=torch.int32).t(), -1)
 
 
 def test_oracle_rows():

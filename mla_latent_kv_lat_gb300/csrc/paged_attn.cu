@@ -28,7 +28,10 @@
 //   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
 //   * fp16 pages come in by TMA as they are, and so do the RoPE parts of e4m3
 //     pages; their codes are read, turned into fp16 (code x scale, exact) and
-//     stored in the same layout by producer warps.
+//     stored in the same layout by producer warps.  A sequence whose chunk has
+//     several blocks would have its codes converted once per block: its visible
+//     rows are converted once, before, into the workspace, and the kernel for fp16
+//     pages takes it, the e4m3 kernel the other sequences of the batch.
 // Work split: a block costs its tiles plus `kPieceCost`; the costs of all
 // blocks form one run, which the clusters share evenly.  A cluster's piece that
 // is a whole block writes o_lat; a block cut by a cluster boundary leaves fp32
@@ -73,7 +76,7 @@ static_assert(kSmem <= 232448, "shared memory");
 
 // Warp roles: softmax 0-3 (keys 0-31 of a tile) and 4-7 (keys 32-63), senders
 // (and Q loads) 8-11, output 12-15, score MMAs 16, P V MMAs 17, TMA loads 18, and
-// for e4m3 pages the producers.
+// for e4m3 pages the producers 19-26.
 constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18, kProdWarp = 19;
 constexpr int kBarMax = 1;                   // + q, named: the row maxima (sums) of warps q and q + 4 are in sM
 constexpr int kProducerWarps = 8;
@@ -97,11 +100,23 @@ struct Rec {                                 // what cluster c left unfinished
   int64_t pad;
 };
 
+// Staging of e4m3 latents as fp16 (rows of 512): up to kStageRows rows of the
+// sequences with at least kStageBlocks blocks, in batches of at most kStageSeqs.
+// Per row and visit of a block the conversion costs ~0.16 ns of the GPU's time,
+// staging a row ~0.3 ns once.
+constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 3;
+
+// Which sequences a launch takes.
+enum Take : int32_t { kTakeAll, kTakeStaged, kTakeUnstaged };
+
 struct TcArgs {
   PagedAttnArgs p;
+  Take take;
   float* ws_o;        // fp32 [2 G][128][512] partials, normalised by their own sums
   float* ws_ml;       // fp32 [2 G][128][2] running maximum (log2 units) and sum
   Rec* rec;           // [G]
+  int32_t* stage_base;   // [B] a sequence's first staged row, -1: not staged (unless take is kTakeAll)
+  uint16_t* stage;       // fp16 [kStageRows][512]
   int32_t n_slots;
   int32_t n_rows;     // rows of the page pool
 };
@@ -141,27 +156,31 @@ struct Walker {
   PagedSeq seq;
   uint32_t rows;        // seq.n * H
 
-  MLA_DEVINL void load(const PagedAttnArgs& a) {
+  MLA_DEVINL void load(const TcArgs& t) {
+    const PagedAttnArgs& a = t.p;
     s0 = slot_of_seq(a, b);
     s1 = b + 1 < a.B ? slot_of_seq(a, b + 1) : INT64_MAX;
     bool bad;
     seq = paged_seq(a.cu, a.seq_len, b, a.T, a.c.max_rows(), bad);
     rows = static_cast<uint32_t>(seq.n) * static_cast<uint32_t>(a.H);
+    if (t.take != kTakeAll && (__ldg(t.stage_base + b) >= 0) != (t.take == kTakeStaged)) rows = 0;
   }
-  MLA_DEVINL void init(const PagedAttnArgs& a, int64_t g) {
+  MLA_DEVINL void init(const TcArgs& t, int64_t g) {
+    const PagedAttnArgs& a = t.p;
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int m = (lo + hi) >> 1;
       if (slot_of_seq(a, m) <= g) lo = m; else hi = m;
     }
     b = lo;
-    load(a);
+    load(t);
   }
   // Tiles of slot g's block (0: no block); g must not decrease between calls.
-  MLA_DEVINL int block(const PagedAttnArgs& a, int64_t g, Item& it) {
+  MLA_DEVINL int block(const TcArgs& t, int64_t g, Item& it) {
+    const PagedAttnArgs& a = t.p;
     while (g >= s1) {
       ++b;
-      load(a);
+      load(t);
     }
     const int64_t i = g - s0;
     if (i < 0 || i * kRows >= rows) return 0;
@@ -197,11 +216,11 @@ struct Iter {
     hi = st.hi;
     S = st.S;
     g = st.g;
-    if (g < a.n_slots) w.init(a.p, g);
+    if (g < a.n_slots) w.init(a, g);
   }
   MLA_DEVINL bool next(const TcArgs& a, Item& it) {
     while (g < a.n_slots && S < hi) {
-      const int n = w.block(a.p, g++, it);
+      const int n = w.block(a, g++, it);
       if (n == 0) continue;
       const int64_t r0 = S + kPieceCost;         // where the block's tiles start
       S = r0 + n;
@@ -240,6 +259,21 @@ MLA_DEVINL bool any_visible(const TcArgs& a, const Item& it, int k, int n) {
 }
 MLA_DEVINL bool key_visible(const TcArgs& a, const Item& it, int k) {
   return k < it.kend && (k >= it.wlo || k < a.p.n_sink);
+}
+
+// Staging takes whole tiles of the keys that some new token of the sequence
+// sees (the first token's window starts lowest).  Staged row of key tile kt,
+// given the sequence's first staged row.
+MLA_DEVINL int32_t seq_first_tile(const PagedAttnArgs& a, int32_t pos0, int32_t& sink_tiles) {
+  const int32_t wlo = a.window > 0 ? max(0, pos0 - a.window + 1) : 0;
+  const int32_t first = wlo / kBK;
+  sink_tiles = min((min(a.n_sink, wlo) + kBK - 1) / kBK, first);
+  return first;
+}
+MLA_DEVINL int32_t staged_row(const TcArgs& a, const Item& it, int32_t base, int kt) {
+  int32_t sink;
+  const int32_t first = seq_first_tile(a.p, it.pos0, sink);
+  return base + kBK * (kt < sink ? kt : kt - first + sink);
 }
 
 // Barriers (u counts this cluster's tiles, k its pieces).
@@ -477,9 +511,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     Item it;
     long long sum = 0;
     if (g0 < g1) {
-      w.init(a.p, g0);
+      w.init(a, g0);
       for (int g = g0; g < g1; ++g) {
-        const int n = w.block(a.p, g, it);
+        const int n = w.block(a, g, it);
         sum += n > 0 ? n + kPieceCost : 0;
       }
     }
@@ -502,9 +536,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       const long long lo = total * c / ge, hi = total * (c + 1) / ge;
       if (S0 <= lo && lo < S0 + sum) {
         long long S = S0;
-        w.init(a.p, g0);
+        w.init(a, g0);
         for (int g = g0; g < g1; ++g) {
-          const int n = w.block(a.p, g, it);
+          const int n = w.block(a, g, it);
           const long long e = S + (n > 0 ? n + kPieceCost : 0);
           if (lo < e) {
             B.st.lo = lo;
@@ -929,14 +963,23 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   } else if (warp == kLoadWarp) {
     // ============================== TMA loader =================================
     // Lane 5 j + c: chunk c (four of 64 latent dims, then the RoPE half) of box
-    // j, the part of the tile that lies in one page.  A box without a visible
-    // row is loaded from behind the last row, which reads as zero.  (e4m3: the
-    // RoPE boxes, and the whole rows some tiles ahead on their way into L2.)
+    // j, the part of the tile that lies in one page, looked up a tile ahead.  A
+    // box without a visible row is loaded from behind the last row, which reads
+    // as zero.  Staged latents come as one box, on lanes 0-3.  (The e4m3 kernel's
+    // loader brings the RoPE boxes, and keeps the rows of the tiles kPrefetchTiles
+    // ahead on their way into L2.)
     const int shift = min(6, a.p.c.page_shift), box = 1 << shift, nb = kBK >> shift;
     const int j = lane / 5, ch = lane % 5;
-    const bool mine = j < nb;
-    Cursor cur, ahead;
-    cur.init(a, B.st);
+    const bool mine = j < nb, staged = !kE4m3 && a.p.c.e4m3;
+    const int rope_x = (a.p.c.e4m3 ? 0 : kLatent) + kRopeHalf * static_cast<int>(rank);
+    auto lookup = [&](int t) -> int {
+      const int key = it.key_tile(t) * kBK + j * box;
+      if (!mine || !any_visible(a, it, key, box)) return a.n_rows;
+      const int64_t x = a.p.c.row_of(it.b, key);
+      if (x < 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
+      return x >= 0 ? static_cast<int>(x) : a.n_rows;
+    };
+    Cursor ahead;
     auto prefetch = [&] {
       if (rank == 0 && lane < nb) {
         const int key = ahead.it.key_tile(ahead.t) * kBK + lane * box;
@@ -950,38 +993,39 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       ahead.next(a);
     };
     if (kE4m3) {
-      ahead = cur;
+      ahead.init(a, B.st);
       for (int d = 0; d < kPrefetchTiles && ahead.more; ++d) prefetch();
     }
+    int u = 0;
 #pragma unroll 1
-    for (int u = 0; ok && cur.more; ++u, cur.next(a)) {
-      const int ls = u % kLatStages, rs = u % kRopeStages;
-      const int key = cur.it.key_tile(cur.t) * kBK + j * box;
-      int row = a.n_rows;
-      if (mine && any_visible(a, cur.it, key, box)) {
-        const int64_t x = a.p.c.row_of(cur.it.b, key);
-        if (x >= 0)
-          row = static_cast<int>(x);
-        else
-          record_error(a.p.err, MLA_ERR_INVALID_ARG);
-      }
-      if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
-      __syncwarp();
-      if (mine && ch == 4)
-        tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs],
-                        (kE4m3 ? 0 : kLatent) + kRopeHalf * static_cast<int>(rank), row, 0);
-      if (kE4m3) {
-        if (ahead.more) prefetch();
-      } else {
+    while (ok && items.next(a, it)) {
+      const int32_t base = staged ? __ldg(a.stage_base + it.b) : 0;
+      int row_n = lookup(0);
+#pragma unroll 1
+      for (int t = 0; t < it.n_tiles; ++t, ++u) {
+        const int ls = u % kLatStages, rs = u % kRopeStages, row = row_n;
+        if (t + 1 < it.n_tiles) row_n = lookup(t + 1);
+        if (kE4m3 && ahead.more) prefetch();
+        if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
+        __syncwarp();
+        if (mine && ch == 4)
+          tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs], rope_x, row, 0);
+        if (kE4m3) continue;
         if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
         __syncwarp();
-        if (mine && ch < 4)
-          tc::tma_load_3d(sLat + ls * kLatStage + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls],
-                          256 * static_cast<int>(rank) + 64 * ch, row, 0);
+        uint8_t* dst = sLat + ls * kLatStage;
+        const int x0 = 256 * static_cast<int>(rank);
+        if (staged) {
+          if (lane < 4)
+            tc::tma_load_3d(dst + lane * kChunk, &tm_lat, &B.lat_full[ls], x0 + 64 * lane,
+                            staged_row(a, it, base, it.key_tile(t)), 0);
+        } else if (mine && ch < 4) {
+          tc::tma_load_3d(dst + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls], x0 + 64 * ch, row, 0);
+        }
       }
     }
   } else if constexpr (kE4m3) {
@@ -1082,10 +1126,121 @@ __global__ void __launch_bounds__(32 * kCombRows) paged_combine_kernel(const TcA
     out[32 * k] = make_uint2(pack_f16x2(acc[k].x * inv, acc[k].y * inv), pack_f16x2(acc[k].z * inv, acc[k].w * inv));
 }
 
+// ---------------------------------------------------------------------------
+// Staging: the latents of chosen sequences' visible rows as fp16.  Each block
+// scans the batch for the sequences' first staged rows (those that still fit
+// are staged), then the warps take four rows at a time; rows that no new token
+// sees become zero.  HBM-bound: 656 bytes in (512 + 16 used), 1024 out a row.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
+  __shared__ int32_t s_end[kStageSeqs];        // staged rows up to and with sequence b
+  __shared__ long long s_warp[8];
+  __shared__ int32_t s_total;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  long long sum = 0;
+  int32_t rows[kStageSeqs / 256];
+#pragma unroll
+  for (int q = 0; q < kStageSeqs / 256; ++q) {
+    const int b = tid * (kStageSeqs / 256) + q;
+    rows[q] = 0;
+    if (b < a.p.B) {
+      bool bad;
+      const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
+      if (static_cast<int64_t>(s.n) * a.p.H > (kStageBlocks - 1) * kRows) {
+        int32_t sink;
+        const int32_t first = seq_first_tile(a.p, s.len - s.n, sink);
+        const int64_t r = static_cast<int64_t>(sink + (s.len + kBK - 1) / kBK - first) * kBK;
+        rows[q] = static_cast<int32_t>(min(r, static_cast<int64_t>(kStageRows + 1)));
+      }
+    }
+    sum += rows[q];
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  if (tid == 0) s_total = 0;
+  __syncthreads();
+  long long end = incl - sum;
+  for (int w = 0; w < warp; ++w) end += s_warp[w];
+  // The sequences before the first that does not fit are staged.
+#pragma unroll
+  for (int q = 0; q < kStageSeqs / 256; ++q) {
+    const int b = tid * (kStageSeqs / 256) + q;
+    const long long base = end;
+    end += rows[q];
+    s_end[b] = static_cast<int32_t>(min(end, static_cast<long long>(INT32_MAX)));
+    if (end <= kStageRows) atomicMax(&s_total, static_cast<int32_t>(end));
+    if (blockIdx.x == 0 && b < a.p.B)
+      a.stage_base[b] = rows[q] > 0 && end <= kStageRows ? static_cast<int32_t>(base) : -1;
+  }
+  __syncthreads();
+  const int32_t total = s_total;
+  // Staged row r: the sequence, the position, the pool row (-1: zero).
+  auto lookup = [&](int32_t r) -> int32_t {
+    if (r >= total) return -1;
+    int lo = 0, hi = kStageSeqs - 1;           // the first sequence with s_end > r
+    while (lo < hi) {
+      const int m = (lo + hi) >> 1;
+      if (s_end[m] > r) hi = m; else lo = m + 1;
+    }
+    bool bad;
+    const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, lo, a.p.T, a.p.c.max_rows(), bad);
+    const int32_t pos0 = s.len - s.n, x = r - (lo > 0 ? s_end[lo - 1] : 0);
+    int32_t sink;
+    const int32_t first = seq_first_tile(a.p, pos0, sink);
+    const int32_t t = x / kBK, p = (t < sink ? t : t - sink + first) * kBK + x % kBK;
+    const int32_t wlo = a.p.window > 0 ? max(0, pos0 - a.p.window + 1) : 0;
+    if (p >= s.len || (p < wlo && p >= a.p.n_sink)) return -1;
+    return static_cast<int32_t>(a.p.c.row_of(lo, p));      // a bad page: recorded by the attention
+  };
+  const int32_t step = 4 * static_cast<int32_t>(gridDim.x) * 8;
+  int32_t r0 = 4 * (static_cast<int32_t>(blockIdx.x) * 8 + warp);
+  int32_t row_n = lane < 4 ? lookup(r0 + lane) : -1;
+  for (; r0 < total; r0 += step) {
+    const int32_t row_l = row_n;
+    uint2 v[8];
+    uint32_t sc = 0x70707070u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int32_t row = __shfl_sync(0xffffffffu, row_l, k >> 1);
+      v[k] = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.p.c.pages + static_cast<int64_t>(row) * kRowE4m3) + lane +
+                              32 * (k & 1))
+                      : make_uint2(0, 0);
+    }
+    const int32_t row_s = __shfl_sync(0xffffffffu, row_l, (lane >> 2) & 3);
+    if (lane < 16 && row_s >= 0)
+      sc = __ldg(reinterpret_cast<const uint32_t*>(a.p.c.pages + static_cast<int64_t>(row_s) * kRowE4m3 + kE4m3ScaleOff) +
+                 (lane & 3));
+    if (lane < 4) row_n = lookup(r0 + step + lane);
+    uint4* dst = reinterpret_cast<uint4*>(a.stage + static_cast<int64_t>(r0) * kLatent) + lane;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // unit lane + 32 (k & 1): scale byte lane / 4 + 8 (k & 1) of the row
+      const uint32_t w = __shfl_sync(0xffffffffu, sc, 4 * (k >> 1) + 2 * (k & 1) + (lane >> 4));
+      const uint32_t d = e4m3_scale_f16x2((w >> (8 * ((lane >> 2) & 3))) & 0xFFu);
+      uint4 o;
+      e4m3x4_to_f16x4(v[k].x, d, o.x, o.y);
+      e4m3x4_to_f16x4(v[k].y, d, o.z, o.w);
+      dst[32 * k] = o;
+    }
+  }
+}
+
 int clusters() { return max(1, device_sm_count() / 2); }
 
+// Workspace: partials, their sums, the clusters' records (all multiples of 16
+// bytes), then the staging.
+size_t partial_bytes() {
+  const size_t rows = static_cast<size_t>(2 * clusters()) * kRows;
+  return rows * kLatent * sizeof(float) + rows * 2 * sizeof(float) + clusters() * sizeof(Rec);
+}
+
 template <bool kE4m3>
-cudaError_t launch_one(const CUtensorMap& tm, const CUtensorMap& tr, const TcArgs& a, cudaStream_t stream) {
+cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const TcArgs& a, cudaStream_t stream) {
   auto kern = paged_attn_kernel<kE4m3>;
   static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
   int dev = 0;
@@ -1097,44 +1252,9 @@ cudaError_t launch_one(const CUtensorMap& tm, const CUtensorMap& tr, const TcArg
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  kern<<<dim3(2 * clusters()), threads(kE4m3), kSmem, stream>>>(tm, tr, a);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-size_t paged_attn_workspace_bytes() {
-  const size_t rows = static_cast<size_t>(2 * clusters()) * kRows;
-  return rows * kLatent * sizeof(float) + rows * 2 * sizeof(float) + clusters() * sizeof(Rec);
-}
-
-cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   const int G = clusters();
-  const size_t rows = static_cast<size_t>(2 * G) * kRows;
-  TcArgs a = {};
-  a.p = p;
-  a.ws_o = static_cast<float*>(p.workspace);
-  a.ws_ml = a.ws_o + rows * kLatent;
-  a.rec = reinterpret_cast<Rec*>(a.ws_ml + rows * 2);
-  a.n_slots = static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
-  a.n_rows = p.c.n_pages << p.c.page_shift;
-  // The latent parts of fp16 pages, and the RoPE parts of either type (fp16).
-  CUtensorMap tm, tr;
-  memset(&tm, 0, sizeof(tm));
-  const uint32_t box = static_cast<uint32_t>(min(kBK, 1 << p.c.page_shift));
-  const uint64_t n = static_cast<uint64_t>(a.n_rows);
-  cudaError_t e;
-  if (p.c.e4m3) {
-    e = make_tmap_3d(&tr, p.c.pages + kE4m3RopeOff, false, kRope, n, 1, kRowE4m3, n * kRowE4m3, kRopeHalf, box, 1, 64);
-    if (e != cudaSuccess) return e;
-    e = launch_one<true>(tm, tr, a, stream);
-  } else {
-    e = make_tmap_3d(&tm, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, 64, box, 1);
-    if (e != cudaSuccess) return e;
-    e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
-    if (e != cudaSuccess) return e;
-    e = launch_one<false>(tm, tr, a, stream);
-  }
+  kern<<<dim3(2 * G), threads(kE4m3), kSmem, stream>>>(tm, tr, a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(G), kRows / kCombRows);
@@ -1146,6 +1266,58 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, paged_combine_kernel, a, G);
+}
+
+}  // namespace
+
+size_t paged_attn_workspace_bytes() {
+  return partial_bytes() + kStageSeqs * sizeof(int32_t) + static_cast<size_t>(kStageRows) * kLatent * 2;
+}
+
+cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
+  const int G = clusters();
+  const size_t rows = static_cast<size_t>(2 * G) * kRows;
+  TcArgs a = {};
+  a.p = p;
+  a.ws_o = static_cast<float*>(p.workspace);
+  a.ws_ml = a.ws_o + rows * kLatent;
+  a.rec = reinterpret_cast<Rec*>(a.ws_ml + rows * 2);
+  int32_t* stage_base = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(p.workspace) + partial_bytes());
+  a.stage = reinterpret_cast<uint16_t*>(stage_base + kStageSeqs);
+  a.n_slots = static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
+  a.n_rows = p.c.n_pages << p.c.page_shift;
+  // The latents of fp16 pages or of staged rows, and the RoPE parts (fp16 in
+  // either row type).
+  CUtensorMap tm, tr;
+  memset(&tm, 0, sizeof(tm));
+  const uint32_t box = static_cast<uint32_t>(min(kBK, 1 << p.c.page_shift));
+  const uint64_t n = static_cast<uint64_t>(a.n_rows);
+  cudaError_t e;
+  if (!p.c.e4m3) {
+    e = make_tmap_3d(&tm, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, 64, box, 1);
+    if (e != cudaSuccess) return e;
+    e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
+    if (e != cudaSuccess) return e;
+    return launch_pair<false>(tm, tr, a, stream);
+  }
+  e = make_tmap_3d(&tr, p.c.pages + kE4m3RopeOff, false, kRope, n, 1, kRowE4m3, n * kRowE4m3, kRopeHalf, box, 1, 64);
+  if (e != cudaSuccess) return e;
+  // A batch of single tokens (T <= B) has no sequence of several blocks, bar one
+  // with empty sequences beside it.
+  if (p.T > p.B && p.B <= kStageSeqs && static_cast<int64_t>(p.T) * p.H > (kStageBlocks - 1) * kRows) {
+    a.stage_base = stage_base;
+    e = make_tmap_3d(&tm, a.stage, false, kLatent, kStageRows, 1, kLatent * 2,
+                     static_cast<uint64_t>(kStageRows) * kLatent * 2, 64, kBK, 1);
+    if (e != cudaSuccess) return e;
+    paged_stage_kernel<<<device_sm_count() * 4, 256, 0, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    a.take = kTakeStaged;
+    e = launch_pair<false>(tm, tr, a, stream);
+    if (e != cudaSuccess) return e;
+    a.take = kTakeUnstaged;
+  }
+  return launch_pair<true>(tm, tr, a, stream);
 }
 
 }  // namespace mla

@@ -226,6 +226,36 @@ def test_attention_split_over_the_keys(e4m3):
     check(b, run(b))
 
 
+def test_e4m3_chunks_beyond_the_staging():
+    """Two chunks whose rows are staged and a third that no longer fits, on a few pages named many times."""
+    ps, H, lens, news = 64, 16, [70001, 50000, 30001], [24, 33, 24]
+    rng = np.random.default_rng(8)
+    raw = PO.pack_rows(bf16(rng.standard_normal((8 * ps, 512))), bf16(rng.standard_normal((8 * ps, 64))), True)
+    pages = torch.from_numpy(raw).cuda().reshape(8, ps, 656)
+    vals = torch.from_numpy(PO.row_values(raw, True)).cuda()
+    table = torch.from_numpy(rng.integers(0, 8, (3, -(-max(lens) // ps))).astype(np.int32)).cuda()
+    T = sum(news)
+    q_lat = torch.from_numpy(rng.standard_normal((T, H, 512)).astype(np.float16)).cuda()
+    q_pe = torch.from_numpy(bf16(rng.standard_normal((T, H, 64)))).bfloat16().cuda()
+    out = torch.full((T, H, 512), float("nan"), dtype=torch.float16, device="cuda")
+    mla.mla_attn_paged(q_lat, q_pe, pages, table, i32(np.concatenate([[0], np.cumsum(news)])), i32(lens), out,
+                       scale=SCALE)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    at = 0
+    for b in range(3):
+        p = torch.arange(lens[b], device="cuda")
+        rows = vals[table[b].long()[p // ps] * ps + p % ps]
+        for i in (0, news[b] - 1):
+            n = lens[b] - news[b] + i + 1
+            q = torch.cat([q_lat[at + i].double(), q_pe[at + i].double()], -1)
+            w = ((q @ rows[:n].T) * SCALE).softmax(-1)
+            ref, mag = w @ rows[:n, :512], w @ rows[:n, :512].abs()
+            tol = (2.0 ** -11 + 2.0 ** -12) * mag + 2.0 ** -11 * ref.abs() + 2.0 ** -24
+            assert ((out[at + i].double() - ref).abs() <= tol).all()
+        at += news[b]
+
+
 def test_sharp_and_flat_scores():
     # nearly one key for each row; all keys alike (their mean); and all rows the same row
     for kw in (dict(std=6.0), dict(std=1e-3), dict(same=True)):

@@ -88,8 +88,8 @@ __host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 72 : 96; }
 constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
 
-constexpr int kPieceCost = 5;                // start-up of a piece, in tiles
-constexpr int kMinCost = 12;                 // least cost worth a cluster of its own
+constexpr int kPieceCost = 4;                // start-up of a piece, in tiles
+constexpr int kMinCost = 3;                  // least cost worth a cluster of its own
 
 struct Rec {                                 // what cluster c left unfinished
   int32_t open_g;     // slot of the block that starts in c and ends in a later cluster (-1: none)
@@ -102,9 +102,10 @@ struct Rec {                                 // what cluster c left unfinished
 
 // Staging of e4m3 latents as fp16 (rows of 512): up to kStageRows rows of the
 // sequences with at least kStageBlocks blocks, in batches of at most kStageSeqs.
-// Per row and visit of a block the conversion costs ~0.16 ns of the GPU's time,
-// staging a row ~0.3 ns once.
-constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 3;
+// Measured with and without, one sequence of 128 heads: 8 queries at 33K 112 and
+// 115 us, 152 queries 1161 and 1707 us, but 4 queries 85 and 74 us, and 8 queries
+// at 2000 rows 53 and 43 us (the staging and a second launch cost ~12 us).
+constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 12;
 
 // Which sequences a launch takes.
 enum Take : int32_t { kTakeAll, kTakeStaged, kTakeUnstaged };
@@ -204,6 +205,7 @@ struct Start {
   int64_t lo, hi;     // the cluster's range in the run of costs
   int64_t S;          // where slot g's cost starts in it
   int32_t g;          // first slot that ends after lo (n_slots: none)
+  int32_t b;          // and its sequence
 };
 
 // This cluster's pieces in order; every role walks the same sequence.
@@ -216,7 +218,8 @@ struct Iter {
     hi = st.hi;
     S = st.S;
     g = st.g;
-    if (g < a.n_slots) w.init(a, g);
+    w.b = st.b;
+    if (g < a.n_slots) w.load(a);
   }
   MLA_DEVINL bool next(const TcArgs& a, Item& it) {
     while (g < a.n_slots && S < hi) {
@@ -234,6 +237,14 @@ struct Iter {
     return false;
   }
 };
+
+// A piece's queries on their way into L2, by one thread of each CTA.
+MLA_DEVINL void prefetch_q(const TcArgs& a, const Item& it, uint32_t rank) {
+  if (rank == 0)
+    tc::prefetch_l2(a.p.q_lat + it.qrow0 * kLatent, static_cast<uint32_t>(it.nvalid) * kLatent * 2);
+  else
+    tc::prefetch_l2(a.p.q_pe + it.qrow0 * kRope, static_cast<uint32_t>(it.nvalid) * kRope * 2);
+}
 
 // Walks the tiles across pieces.
 struct Cursor {
@@ -337,6 +348,16 @@ MLA_DEVINL void tmem_ld16x2_16(uint32_t taddr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+
+// 32 TMEM lanes, 16 columns (lane = row).
+MLA_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // Arrive on `bar` of both CTAs of the pair when every MMA issued so far has
@@ -463,37 +484,37 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   constexpr int NT = threads(kE4m3);
 
   // ---- setup ---------------------------------------------------------------
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kLatStages; ++i) {
-      mbar_init(&B.lat_full[i], kE4m3 ? kProducerWarps : 1);
-      mbar_init(&B.lat_empty[i], 1);
-    }
-    for (int i = 0; i < kRopeStages; ++i) {
-      mbar_init(&B.rope_full[i], 1);
-      mbar_init(&B.rope_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.s_free[i], 12);
-      mbar_init(&B.x_full[i], 1);
-      mbar_init(&B.x_empty[i], 8);
-      mbar_init(&B.p_full[i], 9);
-      mbar_init(&B.pv_done[i], 2);
-    }
-    mbar_init(&B.q_ready, 4);
-    mbar_init(&B.o_ready, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&B.l_full[i], 5);
-    mbar_init(&B.cmd_full, 1);
-    mbar_init(&B.cmd_done, 4);
+  if (warp == kPvWarp) {
+    // a lane per barrier: how many arrivals complete a phase
+    auto init = [&](int l, uint64_t* bars, int n, uint32_t count) {
+      if (lane >= l && lane < l + n) mbar_init(bars + lane - l, count);
+    };
+    static_assert(kLatStages == 4 && kRopeStages == 2, "lanes below");
+    init(0, B.lat_full, 4, kE4m3 ? kProducerWarps : 1);
+    init(4, B.lat_empty, 4, 1);
+    init(8, B.rope_full, 2, 1);
+    init(10, B.rope_empty, 2, 1);
+    init(12, B.s_full, 2, 1);
+    init(14, B.s_free, 2, 12);
+    init(16, B.x_full, 2, 1);
+    init(18, B.x_empty, 2, 8);
+    init(20, B.p_full, 2, 9);
+    init(22, B.pv_done, 2, 2);
+    init(24, &B.q_ready, 1, 4);
+    init(25, &B.o_ready, 1, 1);
+    init(26, B.l_full, 4, 5);
+    init(30, &B.cmd_full, 1, 1);
+    init(31, &B.cmd_done, 1, 4);
     tc::fence_mbar_init();
     // what the peer sends for the first use of each buffer
-    for (int i = 0; i < 2; ++i) {
-      mbar_arrive_expect_tx(&B.x_full[i], kXBytes);
-      mbar_arrive_expect_tx(&B.p_full[i], kPTx);
-    }
-    for (int i = 0; i < 4; ++i) mbar_arrive_expect_tx(&B.l_full[i], kOwn * 4);
+    if (lane >= 16 && lane < 18) mbar_arrive_expect_tx(&B.x_full[lane - 16], kXBytes);
+    if (lane >= 20 && lane < 22) mbar_arrive_expect_tx(&B.p_full[lane - 20], kPTx);
+    if (lane >= 26 && lane < 30) mbar_arrive_expect_tx(&B.l_full[lane - 26], kOwn * 4);
+  }
+  if (threadIdx.x == 0) {
     B.st.g = a.n_slots;
     B.st.lo = B.st.hi = B.st.S = 0;
+    B.st.b = 0;
   }
   if (warp == kQkWarp) {
     tc::tmem_alloc(&B.tmem, 512);
@@ -501,9 +522,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   }
   if (blockIdx.x == 0) record_bad_seqs(a.p.cu, a.p.seq_len, a.p.B, a.p.T, a.p.c.max_rows(), a.p.err);
   {
-    // The run of all blocks' costs: each thread sums a share of the slots, a
-    // scan over the block gives its start, and the thread whose share holds
-    // this cluster's first unit finds the slot.
+    // The run of all blocks' costs: each thread sums a share of the slots (one
+    // slot, as a rule), a scan over the block gives its start, and the thread
+    // whose share holds this cluster's first unit finds the slot.
     long long* red = reinterpret_cast<long long*>(sStg);
     const int per = (a.n_slots + NT - 1) / NT;
     const int g0 = min(a.n_slots, static_cast<int>(threadIdx.x) * per), g1 = min(a.n_slots, g0 + per);
@@ -512,10 +533,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     long long sum = 0;
     if (g0 < g1) {
       w.init(a, g0);
-      for (int g = g0; g < g1; ++g) {
+      int g = g0;
+      do {
         const int n = w.block(a, g, it);
         sum += n > 0 ? n + kPieceCost : 0;
-      }
+      } while (++g < g1);
     }
     long long incl = sum;
 #pragma unroll
@@ -526,30 +548,41 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     if (lane == 31) red[warp] = incl;
     __syncthreads();
     long long before = 0, total = 0;
+#pragma unroll 1
     for (int i = 0; i < NT / 32; ++i) {
       if (i < warp) before += red[i];
       total += red[i];
     }
     const long long S0 = before + incl - sum;
-    const int ge = static_cast<int>(min(static_cast<long long>(G), max(1ll, total / kMinCost)));
-    if (c < ge && sum > 0) {
-      const long long lo = total * c / ge, hi = total * (c + 1) / ge;
-      if (S0 <= lo && lo < S0 + sum) {
-        long long S = S0;
+    // Cluster x of ge takes [total x / ge, total (x + 1) / ge).
+    const int ge = total < static_cast<long long>(G) * kMinCost
+                       ? max(1, static_cast<int>(static_cast<uint32_t>(total) / kMinCost)) : G;
+    long long lo, hi;
+    if (total < (1 << 24)) {             // 32-bit divisions: the 64-bit ones are slow code, run once
+      lo = static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ge);
+      hi = static_cast<uint32_t>(total) * static_cast<uint32_t>(c + 1) / static_cast<uint32_t>(ge);
+    } else {
+      lo = total * c / ge;
+      hi = total * (c + 1) / ge;
+    }
+    if (c < ge && sum > 0 && S0 <= lo && lo < S0 + sum) {
+      long long S = S0;
+      int g = g0;
+      if (per > 1) {                     // else `w` and `it` are the slot's
         w.init(a, g0);
-        for (int g = g0; g < g1; ++g) {
+        for (; g < g1; ++g) {
           const int n = w.block(a, g, it);
           const long long e = S + (n > 0 ? n + kPieceCost : 0);
-          if (lo < e) {
-            B.st.lo = lo;
-            B.st.hi = hi;
-            B.st.S = S;
-            B.st.g = g;
-            break;
-          }
+          if (lo < e) break;
           S = e;
         }
       }
+      B.st.lo = lo;
+      B.st.hi = hi;
+      B.st.S = S;
+      B.st.g = g;
+      B.st.b = w.b;
+      prefetch_q(a, it, rank);           // its load is the longest step before the first tile
     }
   }
   tc::fence_before_sync();
@@ -724,7 +757,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const int lrow = 16 * q4 + (lane & 15);
     const uint32_t lanes = static_cast<uint32_t>(32 * q4 + 16 * peer) << 16;     // the peer's rows
     const uint32_t peer_x = tc::mapa(smem_u32(sX), peer), peer_xfull = tc::mapa(smem_u32(&B.x_full[0]), peer);
-    const int i = 32 * q4 + lane;                                                // Q row of this thread
     uint32_t qrun = 0;
     int u = 0;
 #pragma unroll 1
@@ -732,29 +764,58 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       // Q of the piece.  The last score product of the previous piece is
       // complete: this warp has read its result.
       {
-        const bool rvalid = i < it.nvalid;
-        const int64_t qrow = it.qrow0 + i;
-        const uint4* src = reinterpret_cast<const uint4*>(a.p.q_lat + qrow * kLatent + 256 * rank);
-        const uint4* qp = reinterpret_cast<const uint4*>(a.p.q_pe + qrow * kRope) + 4 * rank;
-#pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t r[32];
+        // This warp's 32 rows, 32 dims (64 bytes) at a time, two in flight: a load
+        // instruction reads 8 rows x 64 contiguous bytes, and the warp's slice of
+        // the RoPE query tile turns them into a row per lane.
+        uint8_t* slice = sQr + q4 * 2048;
+        const int rr = lane >> 2, part = lane & 3;
+        const uint4* src = reinterpret_cast<const uint4*>(a.p.q_lat + (it.qrow0 + 32 * q4 + rr) * kLatent + 256 * rank) + part;
+        const uint4* qp = reinterpret_cast<const uint4*>(a.p.q_pe + (it.qrow0 + 32 * q4 + rr) * kRope) + 4 * rank + part;
+        const int nrows = it.nvalid - 32 * q4;
+        auto fetch = [&](uint4 (&v)[4], int cc) {            // cc == 8: the RoPE half
 #pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            const uint4 x = rvalid ? __ldg(src + cc * 8 + v) : make_uint4(0, 0, 0, 0);
-            r[4 * v] = x.x; r[4 * v + 1] = x.y; r[4 * v + 2] = x.z; r[4 * v + 3] = x.w;
+          for (int m = 0; m < 4; ++m) {
+            const uint4* x = cc < 8 ? src + 4 * cc + m * 8 * (kLatent / 8) : qp + m * 8 * (kRope / 8);
+            v[m] = rr + 8 * m < nrows ? __ldg(x) : make_uint4(0, 0, 0, 0);
           }
-          tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ + 32 * cc, r);
-        }
-        uint4 qpe[4];
+        };
+        auto place = [&](const uint4 (&v)[4], int cc) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) qpe[v] = rvalid ? __ldg(qp + v) : make_uint4(0, 0, 0, 0);
+          for (int m = 0; m < 4; ++m) *reinterpret_cast<uint4*>(slice + unit64(rr + 8 * m, part)) = v[m];
+          __syncwarp();
+          uint32_t r[16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 x = *reinterpret_cast<const uint4*>(slice + unit64(lane, q));
+            r[4 * q] = x.x; r[4 * q + 1] = x.y; r[4 * q + 2] = x.z; r[4 * q + 3] = x.w;
+          }
+          tmem_st16(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ + 16 * cc, r);
+          __syncwarp();
+        };
+        uint4 v0[4];
+        fetch(v0, 0);
+        if constexpr (kE4m3) {           // (no registers for a second set)
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            place(v0, cc);
+            fetch(v0, cc + 1);
+          }
+        } else {
+          uint4 v1[4];
+#pragma unroll 1
+          for (int cc = 0; cc < 8; cc += 2) {
+            fetch(v1, cc + 1);
+            place(v0, cc);
+            fetch(v0, cc + 2);
+            place(v1, cc + 1);
+          }
+        }
         tc::tmem_st_wait();
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          qrun = bf16x2_absmax(bf16x2_absmax(qrun, qpe[v].x), qpe[v].y);
-          qrun = bf16x2_absmax(bf16x2_absmax(qrun, qpe[v].z), qpe[v].w);
-          *reinterpret_cast<uint4*>(sQr + unit64(i, v)) = bf16x8_to_f16x8(qpe[v]);
+        for (int m = 0; m < 4; ++m) {
+          qrun = bf16x2_absmax(bf16x2_absmax(qrun, v0[m].x), v0[m].y);
+          qrun = bf16x2_absmax(bf16x2_absmax(qrun, v0[m].z), v0[m].w);
+          *reinterpret_cast<uint4*>(slice + unit64(rr + 8 * m, part)) = bf16x8_to_f16x8(v0[m]);
         }
         tc::fence_proxy_async();
         tc::fence_before_sync();
@@ -1000,6 +1061,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll 1
     while (ok && items.next(a, it)) {
       const int32_t base = staged ? __ldg(a.stage_base + it.b) : 0;
+      if (u > 0 && lane == 0) prefetch_q(a, it, rank);     // some tiles before the senders load it
       int row_n = lookup(0);
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
@@ -1062,14 +1124,16 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 
 // ---------------------------------------------------------------------------
 // Merge the partials of every block that a cluster boundary cut: block (x =
-// cluster in which it starts, y = group of 8 rows), a warp per row, 16 of the
-// 512 columns a lane.  Launched as a programmatic dependent of the attention.
+// cluster in which it starts, y = group of 4 rows), four warps a row, 4 columns
+// a lane, the loads of eight partials in flight.  (One warp a row, 16 columns a
+// lane, took 20 us longer for a row cut into 76 pieces.)  Launched as a
+// programmatic dependent of the attention.
 // ---------------------------------------------------------------------------
-constexpr int kCombRows = 8;
+constexpr int kCombRows = 4;
 
-__global__ void __launch_bounds__(32 * kCombRows) paged_combine_kernel(const TcArgs a, int G) {
+__global__ void __launch_bounds__(128 * kCombRows) paged_combine_kernel(const TcArgs a, int G) {
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kCombRows + warp;
+  const int row = blockIdx.y * kCombRows + (warp >> 2), col = 128 * (warp & 3) + 4 * lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Rec* rec = a.rec;
   const int g = rec[c].open_g;
@@ -1088,42 +1152,33 @@ __global__ void __launch_bounds__(32 * kCombRows) paged_combine_kernel(const TcA
   for (int s = lane; s < n; s += 32) M = fmaxf(M, a.ws_ml[2 * slot(s)]);
   M = warp_max(M);
   float L = 0.f;
-  float4 acc[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += 4) {
-    float4 v[4][4];
-    float w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[j] = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s0 + j < n) {
-        const int64_t q = slot(s0 + j);
-        const float4* src = reinterpret_cast<const float4*>(a.ws_o + q * kLatent) + lane;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[j][k] = src[32 * k];
-        w[j] = exp2f(a.ws_ml[2 * q] - M) * a.ws_ml[2 * q + 1];
-      }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    float w = 0.f;                               // lane: partial s0 + lane's weight
+    if (s0 + lane < n) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + 2 * slot(s0 + lane));
+      w = exp2f(ml.x - M) * ml.y;
     }
+    L += w;
+    for (int j0 = 0; j0 < min(32, n - s0); j0 += 8) {
+      float4 v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      L += w[j];
+      for (int j = 0; j < 8; ++j)
+        v[j] = s0 + j0 + j < n ? *reinterpret_cast<const float4*>(a.ws_o + slot(s0 + j0 + j) * kLatent + col)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[k].x = fmaf(w[j], v[j][k].x, acc[k].x);
-        acc[k].y = fmaf(w[j], v[j][k].y, acc[k].y);
-        acc[k].z = fmaf(w[j], v[j][k].z, acc[k].z);
-        acc[k].w = fmaf(w[j], v[j][k].w, acc[k].w);
+      for (int j = 0; j < 8; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j0 + j);
+        acc.x = fmaf(wj, v[j].x, acc.x);
+        acc.y = fmaf(wj, v[j].y, acc.y);
+        acc.z = fmaf(wj, v[j].z, acc.z);
+        acc.w = fmaf(wj, v[j].w, acc.w);
       }
     }
   }
-  const float inv = 1.f / L;
-  uint2* out = reinterpret_cast<uint2*>(a.p.o_lat + (rec[c].qrow0 + row) * kLatent) + lane;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    out[32 * k] = make_uint2(pack_f16x2(acc[k].x * inv, acc[k].y * inv), pack_f16x2(acc[k].z * inv, acc[k].w * inv));
+  const float inv = 1.f / warp_sum(L);
+  *reinterpret_cast<uint2*>(a.p.o_lat + (rec[c].qrow0 + row) * kLatent + col) =
+      make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
 }
 
 // ---------------------------------------------------------------------------
@@ -1258,7 +1313,7 @@ cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const TcAr
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(G), kRows / kCombRows);
-  cfg.blockDim = dim3(32 * kCombRows);
+  cfg.blockDim = dim3(128 * kCombRows);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -228,7 +228,7 @@ def test_attention_split_over_the_keys(e4m3):
 
 def test_e4m3_chunks_beyond_the_staging():
     """Two chunks whose rows are staged and a third that no longer fits, on a few pages named many times."""
-    ps, H, lens, news = 64, 16, [70001, 50000, 30001], [24, 33, 24]
+    ps, H, lens, news = 64, 16, [70001, 50000, 30001], [100, 128, 100]
     rng = np.random.default_rng(8)
     raw = PO.pack_rows(bf16(rng.standard_normal((8 * ps, 512))), bf16(rng.standard_normal((8 * ps, 64))), True)
     pages = torch.from_numpy(raw).cuda().reshape(8, ps, 656)

@@ -143,6 +143,7 @@ struct Item {
   uint32_t row0;              // first row within the sequence's new rows
   int64_t qrow0;              // first row in the token array
   bool open;                  // the block goes on past this piece
+  bool once;                  // the sequence has one or two blocks
   MLA_DEVINL bool whole() const { return t_lo == 0 && !open; }
   MLA_DEVINL int key_tile(int t) const {
     const int x = t_lo + t;
@@ -190,6 +191,7 @@ struct Walker {
     it.b = b;
     it.g = static_cast<int32_t>(g);
     it.nvalid = static_cast<int32_t>(r1 - r0);
+    it.once = rows <= 2 * kRows;
     it.row0 = r0;
     it.qrow0 = static_cast<int64_t>(seq.q0) * a.H + r0;
     it.pos0 = seq.len - seq.n;
@@ -370,6 +372,35 @@ MLA_DEVINL void mma_commit_pair_warp(uint64_t* bar) {
           smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+
+// Two fp32 in one register pair: packed adds and multiply-adds are one
+// instruction, and three-input maxima save a third (the softmax is bound by its
+// instruction stream).
+MLA_DEVINL uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MLA_DEVINL float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+MLA_DEVINL uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MLA_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MLA_DEVINL float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // 64 bytes of each of a warp's 32 rows (lane = row) to dst_row0 + row * stride,
@@ -627,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int sb = u & 1;
         const uint32_t ph = (u >> 1) & 1;
         const int base = it.key_tile(t) * kBK, k0 = base + col;
-        float s[16];
+        uint64_t s[8];                           // the scores, in pairs
         float mrow = -INFINITY;
         // Barriers are tested ahead of their use, so that their latencies
         // overlap; one that is not complete yet is waited for there.
@@ -643,30 +674,34 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           if (lane == 0) mbar_arrive(&B.s_free[sb]);
           if (!__all_sync(0xffffffffu, x_test)) dead = !wait_cl(&B.x_full[sb], ph, a);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(r[e]);
+          for (int e = 0; e < 8; ++e) s[e] = pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
         }
         if (!dead) {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const float4 x = *reinterpret_cast<const float4*>(sX + sb * kXBytes + ((col / 4 + g) * kOwn + lrow) * 16);
-            s[4 * g] += x.x;
-            s[4 * g + 1] += x.y;
-            s[4 * g + 2] += x.z;
-            s[4 * g + 3] += x.w;
+            const ulonglong2 x =
+                *reinterpret_cast<const ulonglong2*>(sX + sb * kXBytes + ((col / 4 + g) * kOwn + lrow) * 16);
+            s[2 * g] = add2(s[2 * g], x.x);
+            s[2 * g + 1] = add2(s[2 * g + 1], x.y);
           }
           if (k0 + 15 > lim || (k0 < wl && k0 + 15 >= a.p.n_sink)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (k0 + e > lim || (k0 + e < wl && k0 + e >= a.p.n_sink)) s[e] = -INFINITY;
+            for (int e = 0; e < 8; ++e) {
+              float2 v = unpack2(s[e]);
+              const int k = k0 + 2 * e;
+              if (k > lim || (k < wl && k >= a.p.n_sink)) v.x = -INFINITY;
+              if (k + 1 > lim || (k + 1 < wl && k + 1 >= a.p.n_sink)) v.y = -INFINITY;
+              s[e] = pack2(v.x, v.y);
+            }
           }
-          float mx[8];
+          float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mx[e] = fmaxf(s[2 * e], s[2 * e + 1]);
-#pragma unroll
-          for (int w = 4; w >= 1; w >>= 1)
-#pragma unroll
-            for (int e = 0; e < w; ++e) mx[e] = fmaxf(mx[e], mx[e + w]);
-          const float mown = mx[0] * c2;
+          for (int e = 0; e < 8; e += 2) {
+            const float2 v = unpack2(s[e]), w = unpack2(s[e + 1]);
+            mx = max3(mx, v.x, v.y);
+            my = max3(my, w.x, w.y);
+          }
+          const float mown = fmaxf(mx, my) * c2;
           mrow = fmaxf(mown, __shfl_xor_sync(0xffffffffu, mown, 16));
           if (hh == 0) sM[(2 * sb + half) * kOwn + lrow] = mrow;
         }
@@ -688,14 +723,17 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           }
           const float mb = m_run == -INFINITY ? 0.f : m_run;
           uint32_t pk[8];
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t cc = pack2(c2, c2), mm = pack2(-mb, -mb);
+          uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float p0 = tc::exp2_approx(fmaf(s[2 * e], c2, -mb)), p1 = tc::exp2_approx(fmaf(s[2 * e + 1], c2, -mb));
-            ls[e & 3] += p0 + p1;
+            const float2 x = unpack2(fma2(s[e], cc, mm));
+            const float p0 = tc::exp2_approx(x.x), p1 = tc::exp2_approx(x.y);
+            ls[e & 1] = add2(ls[e & 1], pack2(p0, p1));
             pk[e] = pack_f16x2(p0, p1);
           }
-          l_h += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          const float2 lsum = unpack2(add2(ls[0], ls[1]));
+          l_h += lsum.x + lsum.y;
           // The P buffer and the factors of tile u - 2 have been used in both CTAs.
           if (!__all_sync(0xffffffffu, p_test)) dead = !wait_cl(&B.pv_done[sb], ((u >> 1) - 1) & 1, a);
           if (!dead) {
@@ -1068,6 +1106,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int ls = u % kLatStages, rs = u % kRopeStages, row = row_n;
         if (t + 1 < it.n_tiles) row_n = lookup(t + 1);
         if (kE4m3 && ahead.more) prefetch();
+        // Rows that few blocks read come from HBM: each CTA has half of the next
+        // tile's rows on their way into L2 (32 tokens at 4K-32K rows: 177 -> 169
+        // us; for chunks, whose rows L2 holds, it costs 2-5%).
+        if (!kE4m3 && it.once && !staged && ch == 4 && row_n < a.n_rows)
+          tc::prefetch_l2(a.p.c.pages + (static_cast<int64_t>(row_n) + (rank ? box / 2 : 0)) * kRowF16,
+                          static_cast<uint32_t>(box / 2 * kRowF16));
         if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);

@@ -26,6 +26,10 @@
 //     share a tile's softmax (16 keys of a row per thread), and a warp's P goes to
 //     the peer as one bulk copy.
 //   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
+//   * A piece's queries come through the ring of cache tiles too, as two stages
+//     before its first tile, so that they are there when the piece before has
+//     issued its last score product.  (Loaded by the sender warps themselves they
+//     took 9-11k cycles a piece.)
 //   * fp16 pages come in by TMA as they are, and so do the RoPE parts of e4m3
 //     pages; their codes are read, turned into fp16 (code x scale, exact) and
 //     stored in the same layout by producer warps.  A sequence whose chunk has
@@ -90,6 +94,11 @@ constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp
 
 constexpr int kPieceCost = 4;                // start-up of a piece, in tiles
 constexpr int kMinCost = 3;                  // least cost worth a cluster of its own
+
+// Ring stages that a piece's queries take before its first tile (the e4m3 kernel,
+// whose ring its producers fill, loads them without it).  Tile u (counted over
+// all pieces) of piece k has ring position u + (k + 1) q_slots.
+__host__ __device__ constexpr int q_slots(bool e4m3) { return e4m3 ? 0 : 2; }
 
 struct Rec {                                 // what cluster c left unfinished
   int32_t open_g;     // slot of the block that starts in c and ends in a later cluster (-1: none)
@@ -292,7 +301,7 @@ MLA_DEVINL int32_t staged_row(const TcArgs& a, const Item& it, int32_t base, int
 // Barriers (u counts this cluster's tiles, k its pieces).
 struct Bars {
   uint64_t lat_full[kLatStages];    // tile in its stage
-  uint64_t lat_empty[kLatStages];   // P V has read it
+  uint64_t lat_empty[kLatStages];   // P V has read it (or the senders, queries)
   uint64_t rope_full[kRopeStages];
   uint64_t rope_empty[kRopeStages];
   uint64_t s_full[2];               // partial scores in TMEM
@@ -495,7 +504,7 @@ struct Producer {
 template <bool kE4m3>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
-                      const __grid_constant__ TcArgs a) {
+                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ TcArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQr = sm;
@@ -513,6 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = static_cast<int>(blockIdx.x >> 1), G = static_cast<int>(gridDim.x >> 1);
   constexpr int NT = threads(kE4m3);
+  constexpr int QS = q_slots(kE4m3);
 
   // ---- setup ---------------------------------------------------------------
   if (warp == kPvWarp) {
@@ -613,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       B.st.S = S;
       B.st.g = g;
       B.st.b = w.b;
-      prefetch_q(a, it, rank);           // its load is the longest step before the first tile
+      if (kE4m3) prefetch_q(a, it, rank);
     }
   }
   tc::fence_before_sync();
@@ -750,7 +760,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             // A tile with keys that no row of the block sees: their values must
             // not enter P V (0 x NaN).  The score product has read the tile.
             if (!kE4m3 && (base + kBK > it.kend || (base < it.wlo && base + kBK > a.p.n_sink))) {
-              uint8_t* stage = sLat + (u % kLatStages) * kLatStage;
+              uint8_t* stage = sLat + ((u + QS * (k + 1)) % kLatStages) * kLatStage;
               for (int q = threadIdx.x; q < kBK * 32; q += 256)
                 if (!key_visible(a, it, base + (q >> 5)))
                   *reinterpret_cast<uint4*>(stage + ((q >> 3) & 3) * kChunk + (q >> 5) * 128 + (q & 7) * 16) =
@@ -796,64 +806,80 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const uint32_t lanes = static_cast<uint32_t>(32 * q4 + 16 * peer) << 16;     // the peer's rows
     const uint32_t peer_x = tc::mapa(smem_u32(sX), peer), peer_xfull = tc::mapa(smem_u32(&B.x_full[0]), peer);
     uint32_t qrun = 0;
-    int u = 0;
+    int u = 0, k = 0;
 #pragma unroll 1
     while (ok && items.next(a, it)) {
       // Q of the piece.  The last score product of the previous piece is
       // complete: this warp has read its result.
       {
-        // This warp's 32 rows, 32 dims (64 bytes) at a time, two in flight: a load
-        // instruction reads 8 rows x 64 contiguous bytes, and the warp's slice of
-        // the RoPE query tile turns them into a row per lane.
         uint8_t* slice = sQr + q4 * 2048;
-        const int rr = lane >> 2, part = lane & 3;
-        const uint4* src = reinterpret_cast<const uint4*>(a.p.q_lat + (it.qrow0 + 32 * q4 + rr) * kLatent + 256 * rank) + part;
+        const int rr = lane >> 2, part = lane & 3, nrows = it.nvalid - 32 * q4;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ;
         const uint4* qp = reinterpret_cast<const uint4*>(a.p.q_pe + (it.qrow0 + 32 * q4 + rr) * kRope) + 4 * rank + part;
-        const int nrows = it.nvalid - 32 * q4;
-        auto fetch = [&](uint4 (&v)[4], int cc) {            // cc == 8: the RoPE half
+        uint4 pe[4];
+        auto fetch_pe = [&] {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint4* x = cc < 8 ? src + 4 * cc + m * 8 * (kLatent / 8) : qp + m * 8 * (kRope / 8);
-            v[m] = rr + 8 * m < nrows ? __ldg(x) : make_uint4(0, 0, 0, 0);
-          }
+          for (int m = 0; m < 4; ++m)
+            pe[m] = rr + 8 * m < nrows ? __ldg(qp + m * 8 * (kRope / 8)) : make_uint4(0, 0, 0, 0);
         };
-        auto place = [&](const uint4 (&v)[4], int cc) {
+        if constexpr (!kE4m3) {
+          fetch_pe();
+          // From the two ring stages (128 rows x 64 dims twice each), a row per
+          // lane.  Rows past the block's are zero.
+#pragma unroll 1
+          for (int q = 0; q < QS && ok; ++q) {
+            const int r0 = u + QS * k + q, ls = r0 % kLatStages;
+            ok = wait_all(&B.lat_full[ls], (r0 / kLatStages) & 1, a);
+            if (!ok) break;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              const uint8_t* src = sLat + ls * kLatStage + h * (kLatStage / 2);
+              uint32_t r[32];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) *reinterpret_cast<uint4*>(slice + unit64(rr + 8 * m, part)) = v[m];
-          __syncwarp();
-          uint32_t r[16];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 x = *reinterpret_cast<const uint4*>(slice + unit64(lane, q));
-            r[4 * q] = x.x; r[4 * q + 1] = x.y; r[4 * q + 2] = x.z; r[4 * q + 3] = x.w;
+              for (int w = 0; w < 8; ++w) {
+                const uint4 x = lane < nrows ? *reinterpret_cast<const uint4*>(src + unit128(32 * q4 + lane, w))
+                                             : make_uint4(0, 0, 0, 0);
+                r[4 * w] = x.x; r[4 * w + 1] = x.y; r[4 * w + 2] = x.z; r[4 * w + 3] = x.w;
+              }
+              tc::tmem_st32(tq + 64 * q + 32 * h, r);
+            }
           }
-          tmem_st16(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ + 16 * cc, r);
-          __syncwarp();
-        };
-        uint4 v0[4];
-        fetch(v0, 0);
-        if constexpr (kE4m3) {           // (no registers for a second set)
+          if (!ok) break;
+        } else {
+          // 32 dims (64 bytes) at a time: a load instruction reads 8 rows x 64
+          // contiguous bytes, and the warp's slice of the RoPE query tile turns
+          // them into a row per lane.
+          const uint4* src = reinterpret_cast<const uint4*>(a.p.q_lat + (it.qrow0 + 32 * q4 + rr) * kLatent + 256 * rank) + part;
+          uint4 v[4];
+          auto fetch = [&](int cc) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              v[m] = rr + 8 * m < nrows ? __ldg(src + 4 * cc + m * 8 * (kLatent / 8)) : make_uint4(0, 0, 0, 0);
+          };
+          fetch(0);
 #pragma unroll 1
           for (int cc = 0; cc < 8; ++cc) {
-            place(v0, cc);
-            fetch(v0, cc + 1);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) *reinterpret_cast<uint4*>(slice + unit64(rr + 8 * m, part)) = v[m];
+            __syncwarp();
+            if (cc < 7) fetch(cc + 1);
+            uint32_t r[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint4 x = *reinterpret_cast<const uint4*>(slice + unit64(lane, q));
+              r[4 * q] = x.x; r[4 * q + 1] = x.y; r[4 * q + 2] = x.z; r[4 * q + 3] = x.w;
+            }
+            tmem_st16(tq + 16 * cc, r);
+            __syncwarp();
           }
-        } else {
-          uint4 v1[4];
-#pragma unroll 1
-          for (int cc = 0; cc < 8; cc += 2) {
-            fetch(v1, cc + 1);
-            place(v0, cc);
-            fetch(v0, cc + 2);
-            place(v1, cc + 1);
-          }
+          fetch_pe();
         }
         tc::tmem_st_wait();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          qrun = bf16x2_absmax(bf16x2_absmax(qrun, v0[m].x), v0[m].y);
-          qrun = bf16x2_absmax(bf16x2_absmax(qrun, v0[m].z), v0[m].w);
-          *reinterpret_cast<uint4*>(slice + unit64(rr + 8 * m, part)) = bf16x8_to_f16x8(v0[m]);
+          qrun = bf16x2_absmax(bf16x2_absmax(qrun, pe[m].x), pe[m].y);
+          qrun = bf16x2_absmax(bf16x2_absmax(qrun, pe[m].z), pe[m].w);
+          *reinterpret_cast<uint4*>(slice + unit64(rr + 8 * m, part)) = bf16x8_to_f16x8(pe[m]);
         }
         tc::fence_proxy_async();
         tc::fence_before_sync();
@@ -880,6 +906,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           tc::st_async_v4(peer_x + sb * kXBytes + ((8 * hh + g) * kOwn + lrow) * 16,
                           make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]), peer_xfull + sb * 8);
       }
+      ++k;
     }
     if (bf16x2_absmax_overflows(qrun)) record_error(a.p.err, MLA_ERR_RANGE);
   } else if (warp < kQkWarp) {
@@ -981,16 +1008,18 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         rec.nvalid = it.nvalid;
         rec.qrow0 = it.qrow0;
       }
-      ok = wait_all(&B.q_ready, k++ & 1, a);
+      ok = wait_all(&B.q_ready, k & 1, a);
       tc::fence_after_sync();
+      if (ok && lane < QS) mbar_arrive(&B.lat_empty[(u + QS * k + lane) % kLatStages]);   // the queries have left the ring
+      ++k;
 #pragma unroll 1
       for (int t = 0; ok && t < it.n_tiles; ++t, ++u) {
-        const int ls = u % kLatStages, rs = u % kRopeStages, sb = u & 1;
+        const int r = u + QS * k, ls = r % kLatStages, rs = u % kRopeStages, sb = u & 1;
         // The last to complete is the tile, as a rule: the others are tested
         // while it is awaited.
         const bool r_test = mbar_test(&B.rope_full[rs], (u / kRopeStages) & 1);
         const bool s_test = u < 2 || mbar_test(&B.s_free[sb], ((u >> 1) - 1) & 1);
-        ok = wait_all(&B.lat_full[ls], (u / kLatStages) & 1, a);
+        ok = wait_all(&B.lat_full[ls], (r / kLatStages) & 1, a);
         if (!__all_sync(0xffffffffu, r_test)) ok = ok && wait_all(&B.rope_full[rs], (u / kRopeStages) & 1, a);
         if (!__all_sync(0xffffffffu, s_test)) ok = ok && wait_all(&B.s_free[sb], ((u >> 1) - 1) & 1, a);
         if (!ok) break;
@@ -1013,7 +1042,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   } else if (warp == kPvWarp) {
     // =============================== P V MMAs ==================================
     constexpr uint32_t idesc = tc::idesc_f16(128, 256, false, false, true);
-    int u = 0, n = 0;                  // tiles, requests posted to the output warps
+    int u = 0, k = 0, n = 0;           // tiles, pieces, requests posted to the output warps
     auto post = [&](int cmd) {
       if (n > 0) ok = ok && wait_all(&B.cmd_done, (n - 1) & 1, a);
       if (!ok) return;
@@ -1027,7 +1056,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     while (ok && items.next(a, it)) {
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
-        const int ls = u % kLatStages, sb = u & 1;
+        const int ls = (u + QS * (k + 1)) % kLatStages, sb = u & 1;
         ok = wait_cl(&B.p_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
         if (lane == 0) {               // tile u + 2's P, and its scores: this tile's have been read
@@ -1057,6 +1086,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       if (!ok) break;
       tc::mma_commit_warp(&B.o_ready);
       post(-1);
+      ++k;
     }
     if (ok) post(-2);
   } else if (warp == kLoadWarp) {
@@ -1095,15 +1125,28 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       ahead.init(a, B.st);
       for (int d = 0; d < kPrefetchTiles && ahead.more; ++d) prefetch();
     }
-    int u = 0;
+    int u = 0, k = 0;
 #pragma unroll 1
     while (ok && items.next(a, it)) {
+#pragma unroll 1
+      for (int q = 0; q < QS; ++q) {           // the queries: 128 rows x 64 dims twice a stage
+        const int r = u + QS * k + q, ls = r % kLatStages;
+        if (r >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((r / kLatStages) - 1) & 1, a);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
+        __syncwarp();
+        if (lane < 2)
+          tc::tma_load_3d(sLat + ls * kLatStage + lane * (kLatStage / 2), &tm_q, &B.lat_full[ls],
+                          256 * static_cast<int>(rank) + 128 * q + 64 * lane, static_cast<int>(it.qrow0), 0);
+      }
+      if (!ok) break;
+      ++k;
       const int32_t base = staged ? __ldg(a.stage_base + it.b) : 0;
-      if (u > 0 && lane == 0) prefetch_q(a, it, rank);     // some tiles before the senders load it
+      if (kE4m3 && u > 0 && lane == 0) prefetch_q(a, it, rank);     // some tiles before the senders load it
       int row_n = lookup(0);
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
-        const int ls = u % kLatStages, rs = u % kRopeStages, row = row_n;
+        const int r = u + QS * k, ls = r % kLatStages, rs = u % kRopeStages, row = row_n;
         if (t + 1 < it.n_tiles) row_n = lookup(t + 1);
         if (kE4m3 && ahead.more) prefetch();
         // Rows that few blocks read come from HBM: each CTA has half of the next
@@ -1119,7 +1162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         if (mine && ch == 4)
           tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs], rope_x, row, 0);
         if (kE4m3) continue;
-        if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
+        if (r >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((r / kLatStages) - 1) & 1, a);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
         __syncwarp();
@@ -1339,7 +1382,7 @@ size_t partial_bytes() {
 }
 
 template <bool kE4m3>
-cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const TcArgs& a, cudaStream_t stream) {
+cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const TcArgs& a, cudaStream_t stream) {
   auto kern = paged_attn_kernel<kE4m3>;
   static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
   int dev = 0;
@@ -1352,7 +1395,7 @@ cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const TcAr
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   const int G = clusters();
-  kern<<<dim3(2 * G), threads(kE4m3), kSmem, stream>>>(tm, tr, a);
+  kern<<<dim3(2 * G), threads(kE4m3), kSmem, stream>>>(tm, tr, tq, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1387,17 +1430,24 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   a.n_rows = p.c.n_pages << p.c.page_shift;
   // The latents of fp16 pages or of staged rows, and the RoPE parts (fp16 in
   // either row type).
-  CUtensorMap tm, tr;
+  CUtensorMap tm, tr, tq;
   memset(&tm, 0, sizeof(tm));
+  memset(&tq, 0, sizeof(tq));
   const uint32_t box = static_cast<uint32_t>(min(kBK, 1 << p.c.page_shift));
   const uint64_t n = static_cast<uint64_t>(a.n_rows);
   cudaError_t e;
+  const uint64_t qrows = static_cast<uint64_t>(p.T) * static_cast<uint64_t>(p.H);
+  auto map_q = [&] {
+    return make_tmap_3d(&tq, p.q_lat, false, kLatent, qrows, 1, kLatent * 2, qrows * kLatent * 2, 64, kRows, 1);
+  };
   if (!p.c.e4m3) {
+    e = map_q();
+    if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tm, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, 64, box, 1);
     if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
     if (e != cudaSuccess) return e;
-    return launch_pair<false>(tm, tr, a, stream);
+    return launch_pair<false>(tm, tr, tq, a, stream);
   }
   e = make_tmap_3d(&tr, p.c.pages + kE4m3RopeOff, false, kRope, n, 1, kRowE4m3, n * kRowE4m3, kRopeHalf, box, 1, 64);
   if (e != cudaSuccess) return e;
@@ -1411,12 +1461,14 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     paged_stage_kernel<<<device_sm_count() * 4, 256, 0, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    e = map_q();
+    if (e != cudaSuccess) return e;
     a.take = kTakeStaged;
-    e = launch_pair<false>(tm, tr, a, stream);
+    e = launch_pair<false>(tm, tr, tq, a, stream);
     if (e != cudaSuccess) return e;
     a.take = kTakeUnstaged;
   }
-  return launch_pair<true>(tm, tr, a, stream);
+  return launch_pair<true>(tm, tr, tq, a, stream);
 }
 
 }  // namespace mla

@@ -1094,9 +1094,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     // Lane 5 j + c: chunk c (four of 64 latent dims, then the RoPE half) of box
     // j, the part of the tile that lies in one page, looked up a tile ahead.  A
     // box without a visible row is loaded from behind the last row, which reads
-    // as zero.  Staged latents come as one box, on lanes 0-3.  (The e4m3 kernel's
-    // loader brings the RoPE boxes, and keeps the rows of the tiles kPrefetchTiles
-    // ahead on their way into L2.)
+    // as zero.  Pages of 64 rows and more, and staged latents, take one load for
+    // the four chunks (with 16-row pages the 20 loads of a tile make a chunk 1.25x
+    // slower).  The e4m3 kernel's loader brings the RoPE boxes, and keeps the rows
+    // of the tiles kPrefetchTiles ahead on their way into L2.
     const int shift = min(6, a.p.c.page_shift), box = 1 << shift, nb = kBK >> shift;
     const int j = lane / 5, ch = lane % 5;
     const bool mine = j < nb, staged = !kE4m3 && a.p.c.e4m3;
@@ -1135,9 +1136,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
         __syncwarp();
-        if (lane < 2)
-          tc::tma_load_3d(sLat + ls * kLatStage + lane * (kLatStage / 2), &tm_q, &B.lat_full[ls],
-                          256 * static_cast<int>(rank) + 128 * q + 64 * lane, static_cast<int>(it.qrow0), 0);
+        if (lane == 0)
+          tc::tma_load_3d(sLat + ls * kLatStage, &tm_q, &B.lat_full[ls], 0, static_cast<int>(it.qrow0),
+                          4 * static_cast<int>(rank) + 2 * q);
       }
       if (!ok) break;
       ++k;
@@ -1167,13 +1168,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
         __syncwarp();
         uint8_t* dst = sLat + ls * kLatStage;
-        const int x0 = 256 * static_cast<int>(rank);
-        if (staged) {
-          if (lane < 4)
-            tc::tma_load_3d(dst + lane * kChunk, &tm_lat, &B.lat_full[ls], x0 + 64 * lane,
-                            staged_row(a, it, base, it.key_tile(t)), 0);
+        const int c0 = 4 * static_cast<int>(rank);
+        if (staged || nb == 1) {               // all four chunks in one load
+          if (lane == 0)
+            tc::tma_load_3d(dst, &tm_lat, &B.lat_full[ls], 0, staged ? staged_row(a, it, base, it.key_tile(t)) : row, c0);
         } else if (mine && ch < 4) {
-          tc::tma_load_3d(dst + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls], x0 + 64 * ch, row, 0);
+          tc::tma_load_3d(dst + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls], 0, row, c0 + ch);
         }
       }
     }
@@ -1428,8 +1428,10 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   a.stage = reinterpret_cast<uint16_t*>(stage_base + kStageSeqs);
   a.n_slots = static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
   a.n_rows = p.c.n_pages << p.c.page_shift;
-  // The latents of fp16 pages or of staged rows, and the RoPE parts (fp16 in
-  // either row type).
+  // The latents of fp16 pages or of staged rows and the queries, as 64-dim chunks
+  // (dims, rows, chunks): one load brings all of a CTA's chunks of a tile, chunk
+  // after chunk, where the tile lies in one page.  The RoPE parts are fp16 in
+  // either row type.
   CUtensorMap tm, tr, tq;
   memset(&tm, 0, sizeof(tm));
   memset(&tq, 0, sizeof(tq));
@@ -1438,12 +1440,12 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   cudaError_t e;
   const uint64_t qrows = static_cast<uint64_t>(p.T) * static_cast<uint64_t>(p.H);
   auto map_q = [&] {
-    return make_tmap_3d(&tq, p.q_lat, false, kLatent, qrows, 1, kLatent * 2, qrows * kLatent * 2, 64, kRows, 1);
+    return make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kLatent / 64, kLatent * 2, 128, 64, kRows, 2);
   };
   if (!p.c.e4m3) {
     e = map_q();
     if (e != cudaSuccess) return e;
-    e = make_tmap_3d(&tm, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, 64, box, 1);
+    e = make_tmap_3d(&tm, p.c.pages, false, 64, n, kRow / 64, kRowF16, 128, 64, box, box == kBK ? 4 : 1);
     if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
     if (e != cudaSuccess) return e;
@@ -1455,8 +1457,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   // with empty sequences beside it.
   if (p.T > p.B && p.B <= kStageSeqs && static_cast<int64_t>(p.T) * p.H > (kStageBlocks - 1) * kRows) {
     a.stage_base = stage_base;
-    e = make_tmap_3d(&tm, a.stage, false, kLatent, kStageRows, 1, kLatent * 2,
-                     static_cast<uint64_t>(kStageRows) * kLatent * 2, 64, kBK, 1);
+    e = make_tmap_3d(&tm, a.stage, false, 64, kStageRows, kLatent / 64, kLatent * 2, 128, 64, kBK, 4);
     if (e != cudaSuccess) return e;
     paged_stage_kernel<<<device_sm_count() * 4, 256, 0, stream>>>(a);
     e = cudaGetLastError();

@@ -31,8 +31,10 @@
 //     issued its last score product.  (Loaded by the sender warps themselves they
 //     took 9-11k cycles a piece.)
 //   * fp16 pages come in by TMA as they are, and so do the RoPE parts of e4m3
-//     pages; their codes are read, turned into fp16 (code x scale, exact) and
-//     stored in the same layout by producer warps.  A sequence whose chunk has
+//     pages; their codes come into a ring of their own, from which producer warps
+//     turn them into fp16 tiles (code x scale, exact).  (Read by the producers
+//     from global memory instead, with a fourth tile stage in the ring's place,
+//     the e4m3 attention was slower than the fp16 one.)  A sequence whose chunk has
 //     several blocks would have its codes converted once per block: its visible
 //     rows are converted once, before, into the workspace, and the kernel for fp16
 //     pages takes it, the e4m3 kernel the other sequences of the batch.
@@ -57,7 +59,11 @@ constexpr int kBK = 64;                      // keys per tile
 constexpr int kOwn = kRows / 2;              // rows whose softmax a CTA computes
 constexpr int kChunk = kBK * 128;            // 8 KB: 64 keys x 64 fp16
 constexpr int kLatStage = 4 * kChunk;        // 32 KB: 64 keys x this CTA's 256 latent dims
-constexpr int kLatStages = 4;
+__host__ __device__ constexpr int lat_stages(bool e4m3) { return e4m3 ? 3 : 4; }
+// e4m3 ring: 64 keys x 256 codes (this CTA's half), then the rows' 16 scale bytes.
+constexpr int kRawCodes = kBK * 256, kRawStage = kRawCodes + kBK * 16, kRawStages = 2;
+constexpr int kRingBytes = lat_stages(true) * kLatStage + kRawStages * kRawStage;   // the larger of the two kernels'
+static_assert(kRingBytes >= lat_stages(false) * kLatStage, "tile ring");
 constexpr int kRopeStages = 2;               // a RoPE tile is done with after its score product
 constexpr int kRopeHalf = 32;
 constexpr int kRopeChunk = kBK * kRopeHalf * 2;     // 4 KB
@@ -66,7 +72,8 @@ constexpr int kPBytes = kRows * 128;         // 16 KB: two halves of 128 rows x 
 constexpr int kXBytes = kOwn * kBK * 4;      // 16 KB: 64 rows x 64 keys fp32
 constexpr int kPTx = kOwn * kBK * 2 + kOwn * 4;     // bytes a CTA gets per tile: the other's P rows and factors
 constexpr int kOffLat = kQRopeBytes;
-constexpr int kOffRope = kOffLat + kLatStages * kLatStage;
+constexpr int kOffRaw = kOffLat + lat_stages(true) * kLatStage;      // (e4m3)
+constexpr int kOffRope = kOffLat + kRingBytes;
 constexpr int kOffP = kOffRope + kRopeStages * kRopeChunk;
 constexpr int kOffX = kOffP + 2 * kPBytes;
 constexpr int kOffStg = kOffX + 2 * kXBytes;         // epilogue staging, 2 KB per warp
@@ -84,7 +91,6 @@ static_assert(kSmem <= 232448, "shared memory");
 constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18, kProdWarp = 19;
 constexpr int kBarMax = 1;                   // + q, named: the row maxima (sums) of warps q and q + 4 are in sM
 constexpr int kProducerWarps = 8;
-constexpr int kPrefetchTiles = 8;            // e4m3: rows on their way into L2 ahead of the producers
 __host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kProdWarp + (e4m3 ? kProducerWarps : 0)); }
 // 19 warps: 5 per sub-partition, 96 registers a thread; 27 warps: 7, 72.
 __host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 72 : 96; }
@@ -257,24 +263,6 @@ MLA_DEVINL void prefetch_q(const TcArgs& a, const Item& it, uint32_t rank) {
     tc::prefetch_l2(a.p.q_pe + it.qrow0 * kRope, static_cast<uint32_t>(it.nvalid) * kRope * 2);
 }
 
-// Walks the tiles across pieces.
-struct Cursor {
-  Iter iter;
-  Item it;
-  int t;
-  bool more;
-  MLA_DEVINL void init(const TcArgs& a, const Start& st) {
-    iter.init(a, st);
-    t = 0;
-    more = iter.next(a, it);
-  }
-  MLA_DEVINL void next(const TcArgs& a) {
-    if (++t < it.n_tiles) return;
-    t = 0;
-    more = iter.next(a, it);
-  }
-};
-
 // Keys [k, k + n) hold one that some row of the block sees.
 MLA_DEVINL bool any_visible(const TcArgs& a, const Item& it, int k, int n) {
   return k < it.kend && (k + n > it.wlo || k < a.p.n_sink);
@@ -300,8 +288,10 @@ MLA_DEVINL int32_t staged_row(const TcArgs& a, const Item& it, int32_t base, int
 
 // Barriers (u counts this cluster's tiles, k its pieces).
 struct Bars {
-  uint64_t lat_full[kLatStages];    // tile in its stage
-  uint64_t lat_empty[kLatStages];   // P V has read it (or the senders, queries)
+  uint64_t lat_full[4];             // tile in its stage
+  uint64_t lat_empty[4];   // P V has read it (or the senders, queries)
+  uint64_t raw_full[kRawStages];    // e4m3: codes and scales of the tile in their stage
+  uint64_t raw_empty[kRawStages];   // all producer warps have read them
   uint64_t rope_full[kRopeStages];
   uint64_t rope_empty[kRopeStages];
   uint64_t s_full[2];               // partial scores in TMEM
@@ -439,41 +429,24 @@ MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
 }
 
 // ---------------------------------------------------------------------------
-// e4m3 producer: this CTA's 256 codes of a tile's 64 rows into its stage, as
-// fp16.  Thread pt (of 8 kKeys) takes 16 codes of key pt / 8 + kKeys j, at 16 (pt
-// % 8) + 128 h, for h < 2: a warp's load reads 4 keys x 128 contiguous codes, and
-// all offsets but the row's are constants.  The 8 scale bytes of the row's half
-// come in one load.  Keys 16 g .. 16 g + 15 lie in one page (pages hold at least
-// 16 rows); lane g < 4 of each warp looks up their first pool row, a tile ahead.
-// Rows that no row of the block sees are not read and become zero.
+// e4m3 producer: this CTA's 256 codes of a tile's 64 rows from their ring stage
+// into a tile stage, as fp16.  Thread pt (of 256) takes 16 codes of key pt / 8 +
+// 32 j, at 16 (pt % 8) + 128 h, for j, h < 2: a warp reads 4 keys x 128
+// contiguous codes, and all offsets are constants of the thread.
 // ---------------------------------------------------------------------------
 struct Producer {
   static constexpr int kKeys = 4 * kProducerWarps, J = kBK / kKeys;
   uint4 v[2 * J];
   uint2 d[J];
 
-  MLA_DEVINL static int32_t lookup(const TcArgs& a, const Item& it, int kt, int lane) {
-    int32_t row = -1;
-    if (lane < 4 && any_visible(a, it, kt * kBK + 16 * lane, 16)) {
-      row = static_cast<int32_t>(a.p.c.row_of(it.b, kt * kBK + 16 * lane));
-      if (row < 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
-    }
-    return row;
-  }
-
-  MLA_DEVINL void load(const TcArgs& a, const Item& it, int kt, int32_t row, int rank, int pt) {
+  MLA_DEVINL void load(const uint8_t* raw, int rank, int pt) {
     const int k0 = pt >> 3, c0 = pt & 7;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int32_t r = __shfl_sync(0xffffffffu, row, (k0 + kKeys * j) >> 4);
-      const uint8_t* p = a.p.c.pages + static_cast<int64_t>(r + (k0 & 15)) * kRowE4m3 + 256 * rank + 16 * c0;
-      v[2 * j] = v[2 * j + 1] = make_uint4(0, 0, 0, 0);
-      d[j] = make_uint2(0x70707070u, 0x70707070u);
-      if (r >= 0 && key_visible(a, it, kt * kBK + kKeys * j + k0)) {
-        v[2 * j] = __ldg(reinterpret_cast<const uint4*>(p));
-        v[2 * j + 1] = __ldg(reinterpret_cast<const uint4*>(p + 128));
-        d[j] = __ldg(reinterpret_cast<const uint2*>(p + (kE4m3ScaleOff - 248 * rank - 16 * c0)));
-      }
+      const int key = k0 + kKeys * j;
+      v[2 * j] = *reinterpret_cast<const uint4*>(raw + key * 256 + 16 * c0);
+      v[2 * j + 1] = *reinterpret_cast<const uint4*>(raw + key * 256 + 16 * c0 + 128);
+      d[j] = *reinterpret_cast<const uint2*>(raw + kRawCodes + key * 16 + 8 * rank);
     }
   }
 
@@ -485,7 +458,7 @@ struct Producer {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint4 x = v[2 * j + h];
-        const uint32_t s = e4m3_scale_f16x2(((h ? d[j].y : d[j].x) >> (8 * (c0 >> 1))) & 0xFFu);
+        const uint32_t s = e4m3_scale_f16x2(__byte_perm(h ? d[j].y : d[j].x, 0u, 0x4440 + (c0 >> 1)));
         uint4 lo, hi;
         e4m3x4_to_f16x4(x.x, s, lo.x, lo.y);
         e4m3x4_to_f16x4(x.y, s, lo.z, lo.w);
@@ -509,6 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQr = sm;
   uint8_t* sLat = sm + kOffLat;
+  uint8_t* sRaw = sm + kOffRaw;
   uint8_t* sRope = sm + kOffRope;
   uint8_t* sP = sm + kOffP;
   uint8_t* sX = sm + kOffX;
@@ -522,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = static_cast<int>(blockIdx.x >> 1), G = static_cast<int>(gridDim.x >> 1);
   constexpr int NT = threads(kE4m3);
-  constexpr int QS = q_slots(kE4m3);
+  constexpr int QS = q_slots(kE4m3), LS = lat_stages(kE4m3);
 
   // ---- setup ---------------------------------------------------------------
   if (warp == kPvWarp) {
@@ -530,7 +504,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     auto init = [&](int l, uint64_t* bars, int n, uint32_t count) {
       if (lane >= l && lane < l + n) mbar_init(bars + lane - l, count);
     };
-    static_assert(kLatStages == 4 && kRopeStages == 2, "lanes below");
+    static_assert(kRawStages == 2 && kRopeStages == 2, "lanes below");
+    init(0, B.raw_full, 2, 1);
+    init(2, B.raw_empty, 2, kProducerWarps);
     init(0, B.lat_full, 4, kE4m3 ? kProducerWarps : 1);
     init(4, B.lat_empty, 4, 1);
     init(8, B.rope_full, 2, 1);
@@ -759,8 +735,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             }
             // A tile with keys that no row of the block sees: their values must
             // not enter P V (0 x NaN).  The score product has read the tile.
-            if (!kE4m3 && (base + kBK > it.kend || (base < it.wlo && base + kBK > a.p.n_sink))) {
-              uint8_t* stage = sLat + ((u + QS * (k + 1)) % kLatStages) * kLatStage;
+            if (base + kBK > it.kend || (base < it.wlo && base + kBK > a.p.n_sink)) {
+              uint8_t* stage = sLat + ((u + QS * (k + 1)) % LS) * kLatStage;
               for (int q = threadIdx.x; q < kBK * 32; q += 256)
                 if (!key_visible(a, it, base + (q >> 5)))
                   *reinterpret_cast<uint4*>(stage + ((q >> 3) & 3) * kChunk + (q >> 5) * 128 + (q & 7) * 16) =
@@ -828,8 +804,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           // lane.  Rows past the block's are zero.
 #pragma unroll 1
           for (int q = 0; q < QS && ok; ++q) {
-            const int r0 = u + QS * k + q, ls = r0 % kLatStages;
-            ok = wait_all(&B.lat_full[ls], (r0 / kLatStages) & 1, a);
+            const int r0 = u + QS * k + q, ls = r0 % LS;
+            ok = wait_all(&B.lat_full[ls], (r0 / LS) & 1, a);
             if (!ok) break;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
@@ -1010,16 +986,16 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       }
       ok = wait_all(&B.q_ready, k & 1, a);
       tc::fence_after_sync();
-      if (ok && lane < QS) mbar_arrive(&B.lat_empty[(u + QS * k + lane) % kLatStages]);   // the queries have left the ring
+      if (ok && lane < QS) mbar_arrive(&B.lat_empty[(u + QS * k + lane) % LS]);   // the queries have left the ring
       ++k;
 #pragma unroll 1
       for (int t = 0; ok && t < it.n_tiles; ++t, ++u) {
-        const int r = u + QS * k, ls = r % kLatStages, rs = u % kRopeStages, sb = u & 1;
+        const int r = u + QS * k, ls = r % LS, rs = u % kRopeStages, sb = u & 1;
         // The last to complete is the tile, as a rule: the others are tested
         // while it is awaited.
         const bool r_test = mbar_test(&B.rope_full[rs], (u / kRopeStages) & 1);
         const bool s_test = u < 2 || mbar_test(&B.s_free[sb], ((u >> 1) - 1) & 1);
-        ok = wait_all(&B.lat_full[ls], (r / kLatStages) & 1, a);
+        ok = wait_all(&B.lat_full[ls], (r / LS) & 1, a);
         if (!__all_sync(0xffffffffu, r_test)) ok = ok && wait_all(&B.rope_full[rs], (u / kRopeStages) & 1, a);
         if (!__all_sync(0xffffffffu, s_test)) ok = ok && wait_all(&B.s_free[sb], ((u >> 1) - 1) & 1, a);
         if (!ok) break;
@@ -1056,7 +1032,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     while (ok && items.next(a, it)) {
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
-        const int ls = (u + QS * (k + 1)) % kLatStages, sb = u & 1;
+        const int ls = (u + QS * (k + 1)) % LS, sb = u & 1;
         ok = wait_cl(&B.p_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
         if (lane == 0) {               // tile u + 2's P, and its scores: this tile's have been read
@@ -1096,8 +1072,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     // box without a visible row is loaded from behind the last row, which reads
     // as zero.  Pages of 64 rows and more, and staged latents, take one load for
     // the four chunks (with 16-row pages the 20 loads of a tile make a chunk 1.25x
-    // slower).  The e4m3 kernel's loader brings the RoPE boxes, and keeps the rows
-    // of the tiles kPrefetchTiles ahead on their way into L2.
+    // slower).  The e4m3 kernel's loader brings the codes (lane 5 j) and the scales
+    // (lane 5 j + 1) of box j instead.
     const int shift = min(6, a.p.c.page_shift), box = 1 << shift, nb = kBK >> shift;
     const int j = lane / 5, ch = lane % 5;
     const bool mine = j < nb, staged = !kE4m3 && a.p.c.e4m3;
@@ -1109,30 +1085,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       if (x < 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
       return x >= 0 ? static_cast<int>(x) : a.n_rows;
     };
-    Cursor ahead;
-    auto prefetch = [&] {
-      if (rank == 0 && lane < nb) {
-        const int key = ahead.it.key_tile(ahead.t) * kBK + lane * box;
-        if (any_visible(a, ahead.it, key, box)) {
-          const int64_t x = a.p.c.row_of(ahead.it.b, key);
-          if (x >= 0)
-            tc::prefetch_l2(a.p.c.pages + x * kRowE4m3,
-                            static_cast<uint32_t>(min(box, ahead.it.kend - key)) * kRowE4m3);
-        }
-      }
-      ahead.next(a);
-    };
-    if (kE4m3) {
-      ahead.init(a, B.st);
-      for (int d = 0; d < kPrefetchTiles && ahead.more; ++d) prefetch();
-    }
     int u = 0, k = 0;
 #pragma unroll 1
     while (ok && items.next(a, it)) {
 #pragma unroll 1
       for (int q = 0; q < QS; ++q) {           // the queries: 128 rows x 64 dims twice a stage
-        const int r = u + QS * k + q, ls = r % kLatStages;
-        if (r >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((r / kLatStages) - 1) & 1, a);
+        const int r = u + QS * k + q, ls = r % LS;
+        if (r >= LS) ok = wait_all(&B.lat_empty[ls], ((r / LS) - 1) & 1, a);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
         __syncwarp();
@@ -1147,15 +1106,26 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       int row_n = lookup(0);
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
-        const int r = u + QS * k, ls = r % kLatStages, rs = u % kRopeStages, row = row_n;
+        const int rs = u % kRopeStages, row = row_n;
         if (t + 1 < it.n_tiles) row_n = lookup(t + 1);
-        if (kE4m3 && ahead.more) prefetch();
         // Rows that few blocks read come from HBM: each CTA has half of the next
         // tile's rows on their way into L2 (32 tokens at 4K-32K rows: 177 -> 169
         // us; for chunks, whose rows L2 holds, it costs 2-5%).
         if (!kE4m3 && it.once && !staged && ch == 4 && row_n < a.n_rows)
           tc::prefetch_l2(a.p.c.pages + (static_cast<int64_t>(row_n) + (rank ? box / 2 : 0)) * kRowF16,
                           static_cast<uint32_t>(box / 2 * kRowF16));
+        if (kE4m3) {
+          const int ws = u % kRawStages;
+          if (u >= kRawStages) ok = wait_all(&B.raw_empty[ws], ((u / kRawStages) - 1) & 1, a);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&B.raw_full[ws], kRawStage);
+          __syncwarp();
+          uint8_t* dst = sRaw + ws * kRawStage;
+          if (mine && ch == 0)
+            tc::tma_load_3d(dst + j * box * 256, &tm_lat, &B.raw_full[ws], 128 * static_cast<int>(rank), row, 0);
+          else if (mine && ch == 1)
+            tc::tma_load_3d(dst + kRawCodes + j * box * 16, &tm_q, &B.raw_full[ws], kE4m3ScaleOff / 2, row, 0);
+        }
         if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
@@ -1163,7 +1133,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         if (mine && ch == 4)
           tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs], rope_x, row, 0);
         if (kE4m3) continue;
-        if (r >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((r / kLatStages) - 1) & 1, a);
+        const int r = u + QS * k, ls = r % LS;
+        if (r >= LS) ok = wait_all(&B.lat_empty[ls], ((r / LS) - 1) & 1, a);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
         __syncwarp();
@@ -1184,18 +1155,21 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     int u = 0;
 #pragma unroll 1
     while (ok && items.next(a, it)) {
-      int32_t row = Producer::lookup(a, it, it.key_tile(0), lane);
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
-        const int ls = u % kLatStages;
-        x.load(a, it, it.key_tile(t), row, static_cast<int>(rank), pt);
-        if (t + 1 < it.n_tiles) row = Producer::lookup(a, it, it.key_tile(t + 1), lane);
-        if (u >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((u / kLatStages) - 1) & 1, a);
+        const int ls = u % LS, ws = u % kRawStages;
+        ok = wait_all(&B.raw_full[ws], (u / kRawStages) & 1, a);
+        if (!ok) break;
+        x.load(sRaw + ws * kRawStage, static_cast<int>(rank), pt);
+        if (u >= LS) ok = wait_all(&B.lat_empty[ls], ((u / LS) - 1) & 1, a);
         if (!ok) break;
         x.store(sLat + ls * kLatStage, pt);
         tc::fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.lat_full[ls]);
+        if (lane == 0) {
+          mbar_arrive(&B.lat_full[ls]);
+          mbar_arrive(&B.raw_empty[ws]);
+        }
       }
     }
   }
@@ -1451,6 +1425,13 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     return launch_pair<false>(tm, tr, tq, a, stream);
   }
+  // The e4m3 kernel's own, in elements of two bytes, as the rows are: a CTA's 256
+  // codes, and in the queries' place the 16 scales.
+  CUtensorMap tcodes, tscales;
+  e = make_tmap_3d(&tcodes, p.c.pages, false, kRowE4m3 / 2, n, 1, kRowE4m3, n * kRowE4m3, 128, box, 1, 0);
+  if (e != cudaSuccess) return e;
+  e = make_tmap_3d(&tscales, p.c.pages, false, kRowE4m3 / 2, n, 1, kRowE4m3, n * kRowE4m3, 8, box, 1, 0);
+  if (e != cudaSuccess) return e;
   e = make_tmap_3d(&tr, p.c.pages + kE4m3RopeOff, false, kRope, n, 1, kRowE4m3, n * kRowE4m3, kRopeHalf, box, 1, 64);
   if (e != cudaSuccess) return e;
   // A batch of single tokens (T <= B) has no sequence of several blocks, bar one
@@ -1469,7 +1450,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     a.take = kTakeUnstaged;
   }
-  return launch_pair<true>(tm, tr, tq, a, stream);
+  return launch_pair<true>(tcodes, tr, tscales, a, stream);
 }
 
 }  // namespace mla

@@ -87,13 +87,13 @@ static_assert(kSmem <= 232448, "shared memory");
 
 // Warp roles: softmax 0-3 (keys 0-31 of a tile) and 4-7 (keys 32-63), senders
 // (and Q loads) 8-11, output 12-15, score MMAs 16, P V MMAs 17, TMA loads 18, and
-// for e4m3 pages the producers 19-26.
+// for e4m3 pages the producers 19-22.
 constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18, kProdWarp = 19;
 constexpr int kBarMax = 1;                   // + q, named: the row maxima (sums) of warps q and q + 4 are in sM
-constexpr int kProducerWarps = 8;
+constexpr int kProducerWarps = 4;
 __host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kProdWarp + (e4m3 ? kProducerWarps : 0)); }
-// 19 warps: 5 per sub-partition, 96 registers a thread; 27 warps: 7, 72.
-__host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 72 : 96; }
+// 19 warps: 5 per sub-partition, 96 registers a thread; 23 warps: 6, 80.
+__host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 80 : 96; }
 
 constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
@@ -430,46 +430,33 @@ MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
 
 // ---------------------------------------------------------------------------
 // e4m3 producer: this CTA's 256 codes of a tile's 64 rows from their ring stage
-// into a tile stage, as fp16.  Thread pt (of 256) takes 16 codes of key pt / 8 +
-// 32 j, at 16 (pt % 8) + 128 h, for j, h < 2: a warp reads 4 keys x 128
-// contiguous codes, and all offsets are constants of the thread.
+// into a tile stage, as fp16.  Step j of thread pt (of 128) takes 16 codes each
+// at 16 (pt % 8) + 128 h, h < 2, of key pt / 8 + 16 j: a warp reads 4 keys x 128
+// contiguous codes, and all offsets are constants of the thread.  Four warps, a
+// step at a time: with eight warps, or all of a thread's codes loaded first, the
+// larger hot code made the kernel 2-6% slower (8 tokens at 98304 rows, 248 us).
 // ---------------------------------------------------------------------------
-struct Producer {
-  static constexpr int kKeys = 4 * kProducerWarps, J = kBK / kKeys;
-  uint4 v[2 * J];
-  uint2 d[J];
+constexpr int kProdKeys = 4 * kProducerWarps;
 
-  MLA_DEVINL void load(const uint8_t* raw, int rank, int pt) {
-    const int k0 = pt >> 3, c0 = pt & 7;
+MLA_DEVINL void produce(const uint8_t* raw, uint8_t* lat, int rank, int pt, int j) {
+  const int k0 = pt >> 3, c0 = pt & 7, key = k0 + kProdKeys * j;
+  const uint32_t dst = (c0 >> 2) * kChunk + unit128(k0, 2 * (c0 & 3));
+  const uint8_t* src = raw + key * 256 + 16 * c0;
+  const uint4 v[2] = {*reinterpret_cast<const uint4*>(src), *reinterpret_cast<const uint4*>(src + 128)};
+  const uint2 d = *reinterpret_cast<const uint2*>(raw + kRawCodes + key * 16 + 8 * rank);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int key = k0 + kKeys * j;
-      v[2 * j] = *reinterpret_cast<const uint4*>(raw + key * 256 + 16 * c0);
-      v[2 * j + 1] = *reinterpret_cast<const uint4*>(raw + key * 256 + 16 * c0 + 128);
-      d[j] = *reinterpret_cast<const uint2*>(raw + kRawCodes + key * 16 + 8 * rank);
-    }
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t s = e4m3_scale_f16x2(__byte_perm(h ? d.y : d.x, 0u, 0x4440 + (c0 >> 1)));
+    uint4 lo, hi;
+    e4m3x4_to_f16x4(v[h].x, s, lo.x, lo.y);
+    e4m3x4_to_f16x4(v[h].y, s, lo.z, lo.w);
+    e4m3x4_to_f16x4(v[h].z, s, hi.x, hi.y);
+    e4m3x4_to_f16x4(v[h].w, s, hi.z, hi.w);
+    uint8_t* q = lat + 2 * kChunk * h + kProdKeys * 128 * j;
+    *reinterpret_cast<uint4*>(q + dst) = lo;
+    *reinterpret_cast<uint4*>(q + (dst ^ 16u)) = hi;
   }
-
-  MLA_DEVINL void store(uint8_t* lat, int pt) const {
-    const int k0 = pt >> 3, c0 = pt & 7;
-    const uint32_t dst = (c0 >> 2) * kChunk + unit128(k0, 2 * (c0 & 3));
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 x = v[2 * j + h];
-        const uint32_t s = e4m3_scale_f16x2(__byte_perm(h ? d[j].y : d[j].x, 0u, 0x4440 + (c0 >> 1)));
-        uint4 lo, hi;
-        e4m3x4_to_f16x4(x.x, s, lo.x, lo.y);
-        e4m3x4_to_f16x4(x.y, s, lo.z, lo.w);
-        e4m3x4_to_f16x4(x.z, s, hi.x, hi.y);
-        e4m3x4_to_f16x4(x.w, s, hi.z, hi.w);
-        uint8_t* q = lat + 2 * kChunk * h + kKeys * 128 * j;
-        *reinterpret_cast<uint4*>(q + dst) = lo;
-        *reinterpret_cast<uint4*>(q + (dst ^ 16u)) = hi;
-      }
-  }
-};
+}
 
 // ---------------------------------------------------------------------------
 // The kernel
@@ -1151,7 +1138,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   } else if constexpr (kE4m3) {
     // ============================ e4m3 producers ===============================
     const int pt = static_cast<int>(threadIdx.x) - kProdWarp * 32;
-    Producer x;
     int u = 0;
 #pragma unroll 1
     while (ok && items.next(a, it)) {
@@ -1160,10 +1146,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int ls = u % LS, ws = u % kRawStages;
         ok = wait_all(&B.raw_full[ws], (u / kRawStages) & 1, a);
         if (!ok) break;
-        x.load(sRaw + ws * kRawStage, static_cast<int>(rank), pt);
         if (u >= LS) ok = wait_all(&B.lat_empty[ls], ((u / LS) - 1) & 1, a);
         if (!ok) break;
-        x.store(sLat + ls * kLatStage, pt);
+#pragma unroll 1
+        for (int j = 0; j < kBK / kProdKeys; ++j)
+          produce(sRaw + ws * kRawStage, sLat + ls * kLatStage, static_cast<int>(rank), pt, j);
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0) {

@@ -136,6 +136,24 @@ MLA_DEVINL void e4m3x4_to_f16x4(uint32_t c, uint32_t d, uint32_t& lo, uint32_t& 
   hi = *reinterpret_cast<const uint32_t*>(&r1);
 }
 
+// A launch that may begin while the kernel before it in the stream finishes (the
+// kernel waits with griddepcontrol.wait before its first access to global memory).
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, bool out_f16, cudaStream_t stream);
 size_t paged_attn_workspace_bytes();

@@ -524,6 +524,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     tc::tmem_alloc(&B.tmem, 512);
     tc::tmem_relinquish();
   }
+  if (warp == kLoadWarp && lane == 0) {
+    tc::prefetch_tmap(&tm_lat);
+    tc::prefetch_tmap(&tm_rope);
+    tc::prefetch_tmap(&tm_q);
+  }
+  // All above may run while the kernel before finishes (programmatic launch).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0) record_bad_seqs(a.p.cu, a.p.seq_len, a.p.B, a.p.T, a.p.c.max_rows(), a.p.err);
   {
     // The run of all blocks' costs: each thread sums a share of the slots (one
@@ -551,12 +558,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     }
     if (lane == 31) red[warp] = incl;
     __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll 1
-    for (int i = 0; i < NT / 32; ++i) {
-      if (i < warp) before += red[i];
-      total += red[i];
-    }
+    const long long part = lane < NT / 32 ? red[lane] : 0;
+    const long long total = warp_sum_i64(part), before = warp_sum_i64(lane < warp ? part : 0);
     const long long S0 = before + incl - sum;
     // Cluster x of ge takes [total x / ge, total (x + 1) / ge).
     const int ge = total < static_cast<long long>(G) * kMinCost
@@ -988,7 +991,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t k0 = smem_u32(sLat + ls * kLatStage), d = tmem + kTmS + sb * 64;
-#pragma unroll
+#pragma unroll 8
         for (int ks = 0; ks < 16; ++ks)        // latent half: A = Q from TMEM
           tc::mma_ts_warp(d, tmem + kTmQ + ks * 8, tc::sdesc_sw128(k0 + (ks >> 2) * kChunk + (ks & 3) * 32, 16, 1024),
                           idesc, ks > 0 ? 1u : 0u);
@@ -1183,6 +1186,7 @@ __global__ void __launch_bounds__(128 * kCombRows) paged_combine_kernel(const Tc
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y * kCombRows + (warp >> 2), col = 128 * (warp & 3) + 4 * lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Rec* rec = a.rec;
   const int g = rec[c].open_g;
   if (g < 0 || row >= rec[c].nvalid) return;
@@ -1240,6 +1244,8 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
   __shared__ long long s_warp[8];
   __shared__ int32_t s_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   long long sum = 0;
   int32_t rows[kStageSeqs / 256];
 #pragma unroll
@@ -1356,19 +1362,10 @@ cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUte
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   const int G = clusters();
-  kern<<<dim3(2 * G), threads(kE4m3), kSmem, stream>>>(tm, tr, tq, a);
-  e = cudaGetLastError();
+  e = launch_dependent(kern, dim3(2 * G), dim3(threads(kE4m3)), kSmem, stream, tm, tr, tq, a);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(G), kRows / kCombRows);
-  cfg.blockDim = dim3(128 * kCombRows);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel, a, G);
+  return launch_dependent(paged_combine_kernel, dim3(static_cast<unsigned>(G), kRows / kCombRows),
+                          dim3(128 * kCombRows), 0, stream, a, G);
 }
 
 }  // namespace
@@ -1427,8 +1424,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     a.stage_base = stage_base;
     e = make_tmap_3d(&tm, a.stage, false, 64, kStageRows, kLatent / 64, kLatent * 2, 128, 64, kBK, 4);
     if (e != cudaSuccess) return e;
-    paged_stage_kernel<<<device_sm_count() * 4, 256, 0, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_dependent(paged_stage_kernel, dim3(device_sm_count() * 4), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
     e = map_q();
     if (e != cudaSuccess) return e;

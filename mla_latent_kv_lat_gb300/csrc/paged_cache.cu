@@ -75,6 +75,8 @@ MLA_DEVINL int32_t token_row(const PagedAppendArgs& a, int64_t j, int32_t& pos, 
 // HBM-bound: 1152 bytes in and 1152 (fp16) or 656 (e4m3) out per token.
 template <bool kE4m3>
 __global__ void __launch_bounds__(256, 4) paged_append_kernel(PagedAppendArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) record_bad_seqs(a.cu, a.seq_len, a.B, a.T, a.c.max_rows(), a.err);
   const int lane = threadIdx.x & 31;
   const int64_t step = kGroup * static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -168,6 +170,8 @@ MLA_DEVINL uint4 out8(uint4 v) {
 // HBM-bound: 1152 (fp16) or 656 (e4m3) bytes in and 1152 out per row.
 template <bool kE4m3, bool kOutF16>
 __global__ void __launch_bounds__(256, 4) paged_gather_kernel(PagedGatherArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t step = kGroup * static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   constexpr int kUnits = kRow / 8;                            // 16-byte units of an output row
@@ -241,15 +245,13 @@ unsigned row_blocks(int64_t n) {
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   auto kern = a.c.e4m3 ? paged_append_kernel<true> : paged_append_kernel<false>;
-  kern<<<row_blocks(a.T), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(row_blocks(a.T)), dim3(256), 0, stream, a);
 }
 
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, bool out_f16, cudaStream_t stream) {
   auto kern = a.c.e4m3 ? (out_f16 ? paged_gather_kernel<true, true> : paged_gather_kernel<true, false>)
                        : (out_f16 ? paged_gather_kernel<false, true> : paged_gather_kernel<false, false>);
-  kern<<<row_blocks(a.R), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(row_blocks(a.R)), dim3(256), 0, stream, a);
 }
 
 }  // namespace mla

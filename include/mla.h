@@ -354,12 +354,17 @@ int mla_rope_append(const void* c_kv, const void* k_pe, const int32_t* pos, cons
  * decreasing); seq_len[b] (device int32) counts its cache rows INCLUDING the
  * new tokens, which are its last ones: token i of n sits at position
  * seq_len[b] - n + i.  Rows of the token array outside [cu[0], cu[B]) are
- * padding: not read, and their outputs stay as they were.  A sequence whose
- * new tokens leave [0, T), number more than seq_len[b], or whose seq_len[b]
- * exceeds max_pages x page_size is skipped and recorded as MLA_ERR_INVALID_ARG
- * in the device error word; so is a needed table entry outside [0, n_pages)
- * (see each call).  The others are computed as usual.  These arrays are read
- * on the device only, so a captured call follows their contents.              */
+ * padding: their values are not used, and their outputs stay as they were.  A
+ * sequence whose new tokens leave [0, T), number more than seq_len[b], or whose
+ * seq_len[b] is negative or exceeds max_pages x page_size (or 2^31 - 4097) is
+ * skipped and recorded as MLA_ERR_INVALID_ARG in the device error word; so is a
+ * needed table entry outside [0, n_pages) (see each call).  The others are
+ * computed as usual.  (A decreasing cu is recorded too, but leaves all outputs
+ * of the call undefined.)  These arrays are read on the device only, so a
+ * captured call follows their contents.
+ * The kernels of these calls are launched as programmatic dependents: they may
+ * be scheduled while the stream's previous kernel finishes, and wait for its
+ * completion before they touch memory.                                        */
 typedef enum mla_page_type { MLA_PAGE_F16 = 0, MLA_PAGE_E4M3 = 1 } mla_page_type;
 
 typedef struct mla_paged_cache {
@@ -378,8 +383,8 @@ typedef struct mla_paged_cache {
  * c_kv device bf16 [T][512]; k_pe device bf16 [T][64] (not yet rotated).
  * A token whose table entry is bad is skipped and recorded.  Values the row
  * type cannot hold record MLA_ERR_RANGE: latents past fp16 (MLA_PAGE_F16) or
- * past 57344 = 448 x 2^7 in magnitude (MLA_PAGE_E4M3; stored as the largest),
- * RoPE values past fp16.  Two tokens of one call must not name the same row.
+ * past 57344 = 448 x 2^7 in magnitude (MLA_PAGE_E4M3; stored as the largest, a
+ * NaN as a NaN code), RoPE values past fp16.  Two tokens of one call must not name the same row.
  * freq_base, freq_scale and host errors as in mla_rope_append.                */
 int mla_paged_append(const mla_paged_cache* cache, const void* c_kv, const void* k_pe,
                      const int32_t* cu_new, const int32_t* seq_len, int32_t B, int32_t T,
@@ -396,8 +401,10 @@ int mla_paged_gather(const mla_paged_cache* cache, const int32_t* row0, const in
                      int32_t B, int32_t R, void* out, int32_t out_f16, void* stream);
 
 /* Bytes of device workspace mla_attn_paged needs on the current device: the
- * partial results of work split over the keys.  Depends on neither the batch
- * nor the lengths.  Returns 0 for invalid dims.                               */
+ * partial results of work split over the keys (40 MB on GB300), and room for
+ * 131072 rows of an e4m3 cache as fp16 (134 MB): a sequence with a chunk of new
+ * tokens has its visible rows converted there once.  Depends on neither the
+ * batch nor the lengths.  Returns 0 for invalid dims.                         */
 size_t mla_paged_workspace_size(const mla_dims* dims);
 
 /* Attention of the batch's new tokens over their pages (steps 2-4 of the
@@ -408,7 +415,7 @@ size_t mla_paged_workspace_size(const mla_dims* dims);
  * window > 0 keeps the last `window` positions (the token's own among them)
  * and the first n_sink (attention sinks); window == 0 keeps all.
  * q_lat device fp16 [T][H][512]; q_pe device bf16 [T][H][64] (rotated);
- * o_lat device fp16 [T][H][512].
+ * o_lat device fp16 [T][H][512], apart from q_lat (MLA_ERR_INVALID_ARG).
  * workspace device, ws_bytes >= mla_paged_workspace_size(dims): contents need
  * not be kept between calls; calls that may overlap on the GPU need one each.
  * Visible rows must hold finite values; rows that no new token of the call

@@ -373,6 +373,14 @@ def _stream_on(stream, dev: int):
     return _stream(stream)
 
 
+def stream_context(stream, dev: int):
+    """Allocations inside belong to ``stream`` (None: the current stream), so that a block which the allocator takes
+    back is not handed to another stream while ``stream``'s kernels still use it."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+    return torch.cuda.stream(stream)
+
+
 def _paged(pages, block_table, dev: int) -> MLAPagedCache:
     """The C description of a paged cache: pages fp16 [n_pages, page_size, 576] or uint8 [n_pages, page_size, 656],
     block_table int32 [B, max_pages] (rows may be further apart than max_pages)."""
@@ -449,7 +457,8 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
         raise ValueError(f"q_lat must have shape (T, H, {KV_LORA_RANK}), got {tuple(q_lat.shape)}")
     (T, H, _), Bn = q_lat.shape, block_table.shape[0]
     if workspace is None:
-        workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)
+        with stream_context(stream, dev):
+            workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)
     st = load_library().mla_attn_paged(
         make_dims(H, scale), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
         _arg(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE), dev), cache,

@@ -481,6 +481,10 @@ int mla_attn_paged(const mla_dims* dims, const void* q_lat, const void* q_pe, co
   if (s != MLA_OK) return s;
   if (T < 1 || window < 0 || n_sink < 0) return MLA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(T) * dims->n_head > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  // q_lat is read (by several clusters) while o_lat is written
+  const uintptr_t q = reinterpret_cast<uintptr_t>(q_lat), o = reinterpret_cast<uintptr_t>(o_lat);
+  const uintptr_t bytes = static_cast<uintptr_t>(T) * dims->n_head * kLatent * 2;
+  if (q < o + bytes && o < q + bytes) return MLA_ERR_INVALID_ARG;
   if (workspace == nullptr || ws_bytes < paged_attn_workspace_bytes()) return MLA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return MLA_ERR_MISALIGNED;
   a.q_lat = static_cast<const uint16_t*>(q_lat);

@@ -156,7 +156,8 @@ def mla_paged_step(q_nope, q_pe, c_kv, k_pe, wk_b, wv_b, pages, block_table, cu_
     the token arrays behind the last sequence are padding (their ``o`` follows from what ``bufs.o_lat`` held)."""
     T, H = q_nope.shape[0], q_nope.shape[1]
     if bufs is None:
-        bufs = paged_buffers(T, H, q_nope.device)
+        with B.stream_context(stream, q_nope.device.index):
+            bufs = paged_buffers(T, H, q_nope.device)
     B.mla_paged_append(c_kv, k_pe, pages, block_table, cu_q, seq_len, freq_base=freq_base, freq_scale=freq_scale,
                        stream=stream)
     B.mla_absorb_q(q_nope, wk_b, bufs.q_lat, scale=scale, stream=stream)

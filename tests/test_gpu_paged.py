@@ -290,6 +290,41 @@ def test_strided_table_offsets_and_order_of_the_batch():
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_behind_the_32_bit_offsets(e4m3):
+    """Pages whose rows lie more than 4 GiB into the pool: written, attended over and read back."""
+    b = Batch(20, e4m3, 16, 64, [3, 70], [200, 90])
+    d, extra = b.dev(), 60000 if not e4m3 else 105000
+    pages = torch.empty(extra + b.n_pages, 64, d["pages"].shape[2], dtype=d["pages"].dtype, device="cuda")
+    pages[:3].view(torch.uint8).fill_(0xFF)              # what a wrapped offset would read: NaN
+    pages[extra:] = d["pages"]
+    assert pages[extra:].data_ptr() - pages.data_ptr() > 1 << 32
+    d["pages"] = pages
+    d["block_table"] = torch.where((d["block_table"] >= 0) & (d["block_table"] < b.n_pages), d["block_table"] + extra,
+                                   d["block_table"])
+    check(b, run(b, d))
+    out = torch.empty(200, 576, dtype=torch.float16, device="cuda")
+    mla.mla_paged_gather(pages, d["block_table"][:1].contiguous(), None, i32([0, 200]), out)
+    assert np.array_equal(out.double().cpu().numpy(), b.rows[0])
+    c = torch.full((1, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+    mla.mla_paged_append(c, k, pages, d["block_table"][:1].contiguous(), i32([0, 1]), i32([150]))
+    mla.mla_paged_gather(pages, d["block_table"][:1].contiguous(), i32([149]), i32([0, 1]), out)
+    assert (out[0, :512] == 3).all() and (out[0, 512:] == 0).all()
+    assert mla.mla_get_device_error() == 0
+
+
+def test_a_decreasing_cu_is_reported_and_stays_in_bounds():
+    b = Batch(21, False, 16, 16, [4, 4, 4], [40, 30, 20])
+    d = b.dev()
+    d["cu_q"] = i32([0, 8, 2, 12])
+    out = run(b, d)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == INVALID
+    assert run(b).isfinite().all()                       # the next call is not affected
+    assert mla.mla_get_device_error() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_same_call_same_bits_on_two_streams(e4m3):
     b = Batch(18, e4m3, 128, 64, [1, 1, 5], [3000, 5000, 900])
     d = b.dev()

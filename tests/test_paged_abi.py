@@ -11,7 +11,7 @@ from oracle import paged_oracle as PO
 from tests.paged_util import Batch
 
 P = ctypes.c_void_p
-GOOD, ODD, ODD4 = 0x100000, 0x100008, 0x100002       # never dereferenced: the checks fail first
+GOOD, OUT, ODD, ODD4 = 0x100000, 0x90000000, 0x100008, 0x100002   # never dereferenced: the checks fail first
 
 
 @pytest.fixture(scope="module")
@@ -40,7 +40,7 @@ def test_bad_caches_are_refused(lib):
     for kw, want in BAD_CACHES:
         assert lib.mla_paged_append(cache(**kw), GOOD, GOOD, GOOD, GOOD, 2, 4, 1e4, 1.0, None) == want, kw
         assert lib.mla_paged_gather(cache(**kw), None, GOOD, 2, 4, GOOD, 0, None) == want, kw
-        assert lib.mla_attn_paged(d, GOOD, GOOD, cache(**kw), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, GOOD, None) == want, kw
+        assert lib.mla_attn_paged(d, GOOD, GOOD, cache(**kw), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, OUT, None) == want, kw
     assert lib.mla_paged_append(None, GOOD, GOOD, GOOD, GOOD, 2, 4, 1e4, 1.0, None) == -1
 
 
@@ -60,17 +60,20 @@ def test_bad_arguments_are_refused(lib):
     assert ga(cache(), None, GOOD, 2, 0, GOOD, 0, None) == -1
     d = ctypes.byref(binding.make_dims(16))
     ws = lib.mla_paged_workspace_size(d)
-    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, -1, 0, GOOD, ws, GOOD, None) == -1
-    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 8, -1, GOOD, ws, GOOD, None) == -1
-    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 0, 0, 0, GOOD, ws, GOOD, None) == -1
-    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 0, 4, 0, 0, GOOD, ws, GOOD, None) == -1
-    assert at(d, GOOD, None, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, GOOD, None) == -1
-    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, None, ws, GOOD, None) == -4
-    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws - 1, GOOD, None) == -4
-    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, ODD, ws, GOOD, None) == -3
-    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 1 << 28, 0, 0, GOOD, ws, GOOD, None) == -2
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, -1, 0, GOOD, ws, OUT, None) == -1
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 8, -1, GOOD, ws, OUT, None) == -1
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 0, 0, 0, GOOD, ws, OUT, None) == -1
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 0, 4, 0, 0, GOOD, ws, OUT, None) == -1
+    assert at(d, GOOD, None, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, OUT, None) == -1
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, None, ws, OUT, None) == -4
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws - 1, OUT, None) == -4
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, ODD, ws, OUT, None) == -3
+    assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 1 << 28, 0, 0, GOOD, ws, OUT, None) == -2
+    # q_lat and o_lat (4 tokens x 16 heads x 1024 bytes) must not overlap
+    for o in (GOOD, GOOD + 65536 - 16, GOOD - 65536 + 16):
+        assert at(d, GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, o, None) == -1
     bad = binding.make_dims(24)
-    assert at(ctypes.byref(bad), GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, GOOD, None) == -2
+    assert at(ctypes.byref(bad), GOOD, GOOD, cache(), GOOD, GOOD, 2, 4, 0, 0, GOOD, ws, OUT, None) == -2
     assert lib.mla_paged_workspace_size(ctypes.byref(bad)) == 0
 
 

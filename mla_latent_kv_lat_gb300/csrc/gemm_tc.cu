@@ -241,23 +241,36 @@ cudaError_t get_tmap_encoder(void** fn) {
 }
 
 // 3-D tiled tensor map, 16-bit elements, 128-byte (or 64-byte, or with 0 no) swizzle, zero fill outside.
-cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t d0, uint64_t d1, uint64_t d2,
-                         uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2,
-                         int swizzle_bytes) {
+static cudaError_t make_tmap(CUtensorMap* map, const void* base, bool bf16, uint32_t rank, const cuuint64_t* dims,
+                             const cuuint64_t* strides, const cuuint32_t* box, int swizzle_bytes) {
   void* fn = nullptr;
   cudaError_t e = get_tmap_encoder(&fn);
   if (e != cudaSuccess) return e;
-  const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
-  const cuuint32_t box[3] = {b0, b1, b2};
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
-      map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
+      map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base),
       dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
       swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                           : (swizzle_bytes == 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B),
       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t d0, uint64_t d1, uint64_t d2,
+                         uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2,
+                         int swizzle_bytes) {
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
+  const cuuint32_t box[3] = {b0, b1, b2};
+  return make_tmap(map, base, bf16, 3, dims, strides, box, swizzle_bytes);
+}
+
+cudaError_t make_tmap_row_groups(CUtensorMap* map, const void* base, uint64_t groups, uint64_t chunks,
+                                 uint64_t row_bytes, uint32_t box_groups, uint32_t box_chunks) {
+  const cuuint64_t dims[4] = {64, 8, chunks, groups};
+  const cuuint64_t strides[3] = {row_bytes, 128, 8 * row_bytes};
+  const cuuint32_t box[4] = {64, 8, box_chunks, box_groups};
+  return make_tmap(map, base, false, 4, dims, strides, box, 128);
 }
 
 int device_sm_count() {

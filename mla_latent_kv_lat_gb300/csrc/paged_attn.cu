@@ -57,8 +57,12 @@ namespace {
 constexpr int kRows = 128;                   // query rows of a block (MMA M)
 constexpr int kBK = 64;                      // keys per tile
 constexpr int kOwn = kRows / 2;              // rows whose softmax a CTA computes
-constexpr int kChunk = kBK * 128;            // 8 KB: 64 keys x 64 fp16
-constexpr int kLatStage = 4 * kChunk;        // 32 KB: 64 keys x this CTA's 256 latent dims
+// A tile of latents lies in groups of eight keys, a group in chunks of 64 dims:
+// 128-byte rows, evenly spaced groups, and the part of a tile that lies in one page
+// (16 rows at least) is one block, so that one load brings it whatever the page's size.
+constexpr int kChunk = 8 * 128;              // 1 KB: 8 keys x 64 fp16
+constexpr int kGroup = 4 * kChunk;           // 4 KB: 8 keys x this CTA's 256 latent dims
+constexpr int kLatStage = kBK / 8 * kGroup;  // 32 KB
 __host__ __device__ constexpr int lat_stages(bool e4m3) { return e4m3 ? 3 : 4; }
 // e4m3 ring: 64 keys x 256 codes (this CTA's half), then the rows' 16 scale bytes.
 constexpr int kRawCodes = kBK * 256, kRawStage = kRawCodes + kBK * 16, kRawStages = 2;
@@ -440,7 +444,7 @@ constexpr int kProdKeys = 4 * kProducerWarps;
 
 MLA_DEVINL void produce(const uint8_t* raw, uint8_t* lat, int rank, int pt, int j) {
   const int k0 = pt >> 3, c0 = pt & 7, key = k0 + kProdKeys * j;
-  const uint32_t dst = (c0 >> 2) * kChunk + unit128(k0, 2 * (c0 & 3));
+  const uint32_t dst = (k0 >> 3) * kGroup + (c0 >> 2) * kChunk + unit128(k0 & 7, 2 * (c0 & 3));
   const uint8_t* src = raw + key * 256 + 16 * c0;
   const uint4 v[2] = {*reinterpret_cast<const uint4*>(src), *reinterpret_cast<const uint4*>(src + 128)};
   const uint2 d = *reinterpret_cast<const uint2*>(raw + kRawCodes + key * 16 + 8 * rank);
@@ -452,7 +456,7 @@ MLA_DEVINL void produce(const uint8_t* raw, uint8_t* lat, int rank, int pt, int 
     e4m3x4_to_f16x4(v[h].y, s, lo.z, lo.w);
     e4m3x4_to_f16x4(v[h].z, s, hi.x, hi.y);
     e4m3x4_to_f16x4(v[h].w, s, hi.z, hi.w);
-    uint8_t* q = lat + 2 * kChunk * h + kProdKeys * 128 * j;
+    uint8_t* q = lat + 2 * kChunk * h + kProdKeys / 8 * kGroup * j;
     *reinterpret_cast<uint4*>(q + dst) = lo;
     *reinterpret_cast<uint4*>(q + (dst ^ 16u)) = hi;
   }
@@ -729,7 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
               uint8_t* stage = sLat + ((u + QS * (k + 1)) % LS) * kLatStage;
               for (int q = threadIdx.x; q < kBK * 32; q += 256)
                 if (!key_visible(a, it, base + (q >> 5)))
-                  *reinterpret_cast<uint4*>(stage + ((q >> 3) & 3) * kChunk + (q >> 5) * 128 + (q & 7) * 16) =
+                  *reinterpret_cast<uint4*>(stage + (q >> 8) * kGroup + ((q >> 3) & 3) * kChunk + ((q >> 5) & 7) * 128 + (q & 7) * 16) =
                       make_uint4(0, 0, 0, 0);
             }
             tc::fence_proxy_async();
@@ -993,7 +997,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const uint32_t k0 = smem_u32(sLat + ls * kLatStage), d = tmem + kTmS + sb * 64;
 #pragma unroll 8
         for (int ks = 0; ks < 16; ++ks)        // latent half: A = Q from TMEM
-          tc::mma_ts_warp(d, tmem + kTmQ + ks * 8, tc::sdesc_sw128(k0 + (ks >> 2) * kChunk + (ks & 3) * 32, 16, 1024),
+          tc::mma_ts_warp(d, tmem + kTmQ + ks * 8, tc::sdesc_sw128(k0 + (ks >> 2) * kChunk + (ks & 3) * 32, 16, kGroup),
                           idesc, ks > 0 ? 1u : 0u);
         const uint32_t q0 = smem_u32(sQr), r0 = smem_u32(sRope + rs * kRopeChunk);
 #pragma unroll
@@ -1045,7 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll
         for (int ks = 0; ks < kBK / 16; ++ks)
           tc::mma_ss_warp(tmem + kTmO, tc::sdesc_sw64(p0 + (ks >> 1) * (kPBytes / 2) + (ks & 1) * 32),
-                          tc::sdesc_sw128(v0 + ks * 2048, kChunk, 1024), idesc, (t > 0 || ks > 0) ? 1u : 0u);
+                          tc::sdesc_sw128(v0 + ks * 2 * kGroup, kChunk, kGroup), idesc, (t > 0 || ks > 0) ? 1u : 0u);
         tc::mma_commit_warp(&B.lat_empty[ls]);
         mma_commit_pair_warp(&B.pv_done[sb]);
       }
@@ -1057,15 +1061,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     if (ok) post(-2);
   } else if (warp == kLoadWarp) {
     // ============================== TMA loader =================================
-    // Lane 5 j + c: chunk c (four of 64 latent dims, then the RoPE half) of box
-    // j, the part of the tile that lies in one page, looked up a tile ahead.  A
-    // box without a visible row is loaded from behind the last row, which reads
-    // as zero.  Pages of 64 rows and more, and staged latents, take one load for
-    // the four chunks (with 16-row pages the 20 loads of a tile make a chunk 1.25x
-    // slower).  The e4m3 kernel's loader brings the codes (lane 5 j) and the scales
-    // (lane 5 j + 1) of box j instead.
+    // Lane 3 j + c: box j, the part of the tile that lies in one page, looked up a
+    // tile ahead: its RoPE half (c = 0), its latents or e4m3 codes (1), their scales
+    // (2).  A box without a visible row is loaded from behind the last row, which
+    // reads as zero.
     const int shift = min(6, a.p.c.page_shift), box = 1 << shift, nb = kBK >> shift;
-    const int j = lane / 5, ch = lane % 5;
+    const int j = lane / 3, ch = lane % 3;
     const bool mine = j < nb, staged = !kE4m3 && a.p.c.e4m3;
     const int rope_x = (a.p.c.e4m3 ? 0 : kLatent) + kRopeHalf * static_cast<int>(rank);
     auto lookup = [&](int t) -> int {
@@ -1101,7 +1102,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         // Rows that few blocks read come from HBM: each CTA has half of the next
         // tile's rows on their way into L2 (32 tokens at 4K-32K rows: 177 -> 169
         // us; for chunks, whose rows L2 holds, it costs 2-5%).
-        if (!kE4m3 && it.once && !staged && ch == 4 && row_n < a.n_rows)
+        if (!kE4m3 && it.once && !staged && ch == 0 && row_n < a.n_rows)
           tc::prefetch_l2(a.p.c.pages + (static_cast<int64_t>(row_n) + (rank ? box / 2 : 0)) * kRowF16,
                           static_cast<uint32_t>(box / 2 * kRowF16));
         if (kE4m3) {
@@ -1111,16 +1112,16 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           if (lane == 0) mbar_arrive_expect_tx(&B.raw_full[ws], kRawStage);
           __syncwarp();
           uint8_t* dst = sRaw + ws * kRawStage;
-          if (mine && ch == 0)
+          if (mine && ch == 1)
             tc::tma_load_3d(dst + j * box * 256, &tm_lat, &B.raw_full[ws], 128 * static_cast<int>(rank), row, 0);
-          else if (mine && ch == 1)
+          else if (mine && ch == 2)
             tc::tma_load_3d(dst + kRawCodes + j * box * 16, &tm_q, &B.raw_full[ws], kE4m3ScaleOff / 2, row, 0);
         }
         if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
         __syncwarp();
-        if (mine && ch == 4)
+        if (mine && ch == 0)
           tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs], rope_x, row, 0);
         if (kE4m3) continue;
         const int r = u + QS * k, ls = r % LS;
@@ -1130,11 +1131,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         __syncwarp();
         uint8_t* dst = sLat + ls * kLatStage;
         const int c0 = 4 * static_cast<int>(rank);
-        if (staged || nb == 1) {               // all four chunks in one load
+        if (staged) {
           if (lane == 0)
-            tc::tma_load_3d(dst, &tm_lat, &B.lat_full[ls], 0, staged ? staged_row(a, it, base, it.key_tile(t)) : row, c0);
-        } else if (mine && ch < 4) {
-          tc::tma_load_3d(dst + ch * kChunk + j * box * 128, &tm_lat, &B.lat_full[ls], 0, row, c0 + ch);
+            tc::tma_load_4d(dst, &tm_lat, &B.lat_full[ls], 0, 0, c0, staged_row(a, it, base, it.key_tile(t)) / 8);
+        } else if (mine && ch == 1) {
+          tc::tma_load_4d(dst + j * box / 8 * kGroup, &tm_lat, &B.lat_full[ls], 0, 0, c0, row / 8);
         }
       }
     }
@@ -1386,9 +1387,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   a.stage = reinterpret_cast<uint16_t*>(stage_base + kStageSeqs);
   a.n_slots = static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
   a.n_rows = p.c.n_pages << p.c.page_shift;
-  // The latents of fp16 pages or of staged rows and the queries, as 64-dim chunks
-  // (dims, rows, chunks): one load brings all of a CTA's chunks of a tile, chunk
-  // after chunk, where the tile lies in one page.  The RoPE parts are fp16 in
+  // The latents of fp16 pages or of staged rows, in groups of eight rows; the
+  // queries, as 64-dim chunks (dims, rows, chunks).  The RoPE parts are fp16 in
   // either row type.
   CUtensorMap tm, tr, tq;
   memset(&tm, 0, sizeof(tm));
@@ -1403,7 +1403,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   if (!p.c.e4m3) {
     e = map_q();
     if (e != cudaSuccess) return e;
-    e = make_tmap_3d(&tm, p.c.pages, false, 64, n, kRow / 64, kRowF16, 128, 64, box, box == kBK ? 4 : 1);
+    e = make_tmap_row_groups(&tm, p.c.pages, n / 8, kRow / 64, kRowF16, box / 8, 4);
     if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
     if (e != cudaSuccess) return e;
@@ -1422,7 +1422,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   // with empty sequences beside it.
   if (p.T > p.B && p.B <= kStageSeqs && static_cast<int64_t>(p.T) * p.H > (kStageBlocks - 1) * kRows) {
     a.stage_base = stage_base;
-    e = make_tmap_3d(&tm, a.stage, false, 64, kStageRows, kLatent / 64, kLatent * 2, 128, 64, kBK, 4);
+    e = make_tmap_row_groups(&tm, a.stage, kStageRows / 8, kLatent / 64, kLatent * 2, kBK / 8, 4);
     if (e != cudaSuccess) return e;
     e = launch_dependent(paged_stage_kernel, dim3(device_sm_count() * 4), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;

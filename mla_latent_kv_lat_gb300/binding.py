@@ -386,21 +386,24 @@ def _paged(pages, block_table, dev: int) -> MLAPagedCache:
     block_table int32 [B, max_pages] (rows may be further apart than max_pages)."""
     if not isinstance(pages, torch.Tensor) or pages.dtype not in (torch.float16, torch.uint8):
         raise TypeError("pages must be a torch.float16 or torch.uint8 tensor")
-    f16 = pages.dtype is torch.float16
+    f16, shape = pages.dtype is torch.float16, pages.shape
     row = ROW if f16 else ROW_E4M3
-    if pages.dim() != 3 or pages.shape[2] != row:
-        raise ValueError(f"pages must have shape (n_pages, page_size, {row}), got {tuple(pages.shape)}")
+    if len(shape) != 3 or shape[2] != row:
+        raise ValueError(f"pages must have shape (n_pages, page_size, {row}), got {tuple(shape)}")
+    if pages.get_device() != dev or not pages.is_contiguous():
+        _arg(pages, "pages", pages.dtype, shape, dev)
     if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32:
         raise TypeError("block_table must be a torch.int32 tensor")
-    if block_table.dim() != 2 or block_table.shape[0] < 1 or block_table.shape[1] < 1:
+    tshape = block_table.shape
+    if len(tshape) != 2 or tshape[0] < 1 or tshape[1] < 1:
         raise ValueError("block_table must have shape (B, max_pages)")
-    width, (stride, inner) = block_table.shape[1], block_table.stride()
-    if width > 1 and inner != 1:
+    stride, inner = block_table.stride()
+    if inner != 1 and tshape[1] > 1:
         raise ValueError("block_table's rows must be contiguous")
     if block_table.get_device() != dev:
         raise ValueError(f"block_table is on {block_table.device}, another tensor on cuda:{dev}")
-    return MLAPagedCache(_arg(pages, "pages", pages.dtype, pages.shape, dev), block_table.data_ptr(), stride, width,
-                         pages.shape[0], pages.shape[1], PAGE_F16 if f16 else PAGE_E4M3)
+    return MLAPagedCache(pages.data_ptr(), block_table.data_ptr(), stride, tshape[1], shape[0], shape[1],
+                         PAGE_F16 if f16 else PAGE_E4M3)
 
 
 def mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base: float = 10000.0,

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <math.h>
+#include <string.h>
 
 #include <mutex>
 
@@ -220,16 +221,24 @@ int check_i32(std::initializer_list<const int32_t*> ps) {
 }
 
 // turns per position of pair i, frac(t_i) as 0.64 fixed point: two exact
-// 32-bit halves of the double's fraction
+// 32-bit halves of the double's fraction.  A thread keeps the table of its last
+// frequencies: a model has one, and its powers are a fifth of an append's C call.
 void rope_turns(float freq_base, float freq_scale, uint64_t* turn) {
-  const double kTwoPi = 6.283185307179586;
-  for (int i = 0; i < kRope / 2; ++i) {
-    double t = static_cast<double>(freq_scale) * pow(static_cast<double>(freq_base), -2.0 * i / kRope) / kTwoPi;
-    t -= floor(t);
-    const double hi = floor(ldexp(t, 32));
-    const double lo = nearbyint(ldexp(ldexp(t, 32) - hi, 32));
-    turn[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo);
+  static thread_local uint64_t table[kRope / 2];
+  static thread_local float base = 0.f, scale = 0.f;           // no call has these: none is in the table yet
+  if (base != freq_base || scale != freq_scale) {
+    const double kTwoPi = 6.283185307179586;
+    for (int i = 0; i < kRope / 2; ++i) {
+      double t = static_cast<double>(freq_scale) * pow(static_cast<double>(freq_base), -2.0 * i / kRope) / kTwoPi;
+      t -= floor(t);
+      const double hi = floor(ldexp(t, 32));
+      const double lo = nearbyint(ldexp(ldexp(t, 32) - hi, 32));
+      table[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo);
+    }
+    base = freq_base;
+    scale = freq_scale;
   }
+  memcpy(turn, table, sizeof(table));
 }
 
 }  // namespace

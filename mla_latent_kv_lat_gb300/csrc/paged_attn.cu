@@ -1029,10 +1029,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int ls = (u + QS * (k + 1)) % LS, sb = u & 1;
         ok = wait_cl(&B.p_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
-        if (lane == 0) {               // tile u + 2's P, and its scores: this tile's have been read
-          mbar_arrive_expect_tx(&B.p_full[sb], kPTx);
-          mbar_arrive_expect_tx(&B.x_full[sb], kXBytes);
-        }
         if (t == 0) {
           if (n > 0) ok = wait_all(&B.cmd_done, (n - 1) & 1, a);          // the previous output has left O
         } else {
@@ -1043,7 +1039,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           }
         }
         if (!ok) break;
-        tc::fence_proxy_async();       // the peer's P rows, written by st.async, for the MMA
         tc::fence_after_sync();
         const uint32_t v0 = smem_u32(sLat + ls * kLatStage), p0 = smem_u32(sP + sb * kPBytes);
 #pragma unroll
@@ -1052,6 +1047,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
                           tc::sdesc_sw128(v0 + ks * 2 * kGroup, kChunk, kGroup), idesc, (t > 0 || ks > 0) ? 1u : 0u);
         tc::mma_commit_warp(&B.lat_empty[ls]);
         mma_commit_pair_warp(&B.pv_done[sb]);
+        if (lane == 0) {               // tile u + 2's P, and its scores: this tile's have been read
+          mbar_arrive_expect_tx(&B.p_full[sb], kPTx);
+          mbar_arrive_expect_tx(&B.x_full[sb], kXBytes);
+        }
       }
       if (!ok) break;
       tc::mma_commit_warp(&B.o_ready);

@@ -14,7 +14,9 @@
 //     the contraction, for all 128 rows.
 //   * The partial scores are reduced between the CTAs by rows: CTA r owns rows
 //     with (row / 16) % 2 == r.  Four sender warps pass the other CTA's 64 rows
-//     on to it in fp32 (st.async into distributed shared memory); softmax warps
+//     on to it in fp32, 4 KB a warp and tile as one bulk copy (stored to its shared
+//     memory 16 bytes a thread, they kept the SM's way out busy for 1000 of a
+//     tile's 2200 cycles: chunks over 16-row pages 268 us, not 255); softmax warps
 //     add what arrives to their own half, so scores are full fp32 sums and each
 //     row's softmax is computed once in the pair.  P (fp16) of the owned rows is
 //     stored to both CTAs, with the factor by which the row's earlier output has
@@ -80,7 +82,8 @@ constexpr int kOffRaw = kOffLat + lat_stages(true) * kLatStage;      // (e4m3)
 constexpr int kOffRope = kOffLat + kRingBytes;
 constexpr int kOffP = kOffRope + kRopeStages * kRopeChunk;
 constexpr int kOffX = kOffP + 2 * kPBytes;
-constexpr int kOffStg = kOffX + 2 * kXBytes;         // epilogue staging, 2 KB per warp
+constexpr int kOffXs = kOffX + kXBytes;               // what goes to the other CTA
+constexpr int kOffStg = kOffXs + kXBytes;         // epilogue staging, 2 KB per warp
 constexpr int kOffAlpha = kOffStg + 4 * 2048;        // [2][128] output factors
 constexpr int kOffL = kOffAlpha + 2 * kRows * 4;     // [4][128] row sums
 constexpr int kOffM = kOffL + 4 * kRows * 4;         // [2][2][64] row maxima of the key halves, by tile parity
@@ -300,8 +303,8 @@ struct Bars {
   uint64_t rope_empty[kRopeStages];
   uint64_t s_full[2];               // partial scores in TMEM
   uint64_t s_free[2];               // both the softmax and the sender warps have read them
-  uint64_t x_full[2];               // the other CTA's partials of the owned rows have arrived
-  uint64_t x_empty[2];              // the other CTA has read what this one sent
+  uint64_t x_full[4];               // the other CTA's partials of warp q's 16 owned rows have arrived
+  uint64_t x_empty[4];              // the other CTA has read what this one's sender warp q sent
   uint64_t p_full[2];               // P and factors of all 128 rows
   uint64_t pv_done[2];              // P V done in both CTAs: P buffer, factors and O of that tile
   uint64_t q_ready;                 // piece k's queries in TMEM and shared memory
@@ -330,10 +333,6 @@ MLA_DEVINL void st_async_b32(uint32_t remote_addr, uint32_t v, uint32_t remote_b
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(remote_addr), "r"(v),
                "r"(remote_bar)
                : "memory");
-}
-
-MLA_DEVINL void named_bar_arrive(int id, int nthreads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
 // `bytes` of this CTA's shared memory to the peer's, counted on its barrier.
@@ -477,6 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   uint8_t* sRope = sm + kOffRope;
   uint8_t* sP = sm + kOffP;
   uint8_t* sX = sm + kOffX;
+  uint8_t* sXs = sm + kOffXs;
   uint8_t* sStg = sm + kOffStg;
   float* sAlpha = reinterpret_cast<float*>(sm + kOffAlpha);
   float* sL = reinterpret_cast<float*>(sm + kOffL);
@@ -504,8 +504,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     init(10, B.rope_empty, 2, 1);
     init(12, B.s_full, 2, 1);
     init(14, B.s_free, 2, 12);
-    init(16, B.x_full, 2, 1);
-    init(18, B.x_empty, 2, 8);
+    init(16, B.x_full, 4, 1);
+    init(16, B.x_empty, 4, 1);
     init(20, B.p_full, 2, 9);
     init(22, B.pv_done, 2, 2);
     init(24, &B.q_ready, 1, 4);
@@ -515,7 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     init(31, &B.cmd_done, 1, 4);
     tc::fence_mbar_init();
     // what the peer sends for the first use of each buffer
-    if (lane >= 16 && lane < 18) mbar_arrive_expect_tx(&B.x_full[lane - 16], kXBytes);
+    if (lane >= 16 && lane < 20) mbar_arrive_expect_tx(&B.x_full[lane - 16], kXBytes / 4);
     if (lane >= 20 && lane < 22) mbar_arrive_expect_tx(&B.p_full[lane - 20], kPTx);
     if (lane >= 26 && lane < 30) mbar_arrive_expect_tx(&B.l_full[lane - 26], kOwn * 4);
   }
@@ -623,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const uint32_t peer_p = tc::mapa(smem_u32(sP), peer), peer_pfull = tc::mapa(smem_u32(&B.p_full[0]), peer);
     const uint32_t peer_alpha = tc::mapa(smem_u32(sAlpha), peer), peer_l = tc::mapa(smem_u32(sL), peer);
     const uint32_t peer_lfull = tc::mapa(smem_u32(&B.l_full[0]), peer);
-    const uint32_t peer_xempty = tc::mapa(smem_u32(&B.x_empty[0]), peer);
+    const uint32_t peer_xempty = tc::mapa(smem_u32(&B.x_empty[q4]), peer);
     bool dead = false;
     int u = 0, k = 0;
 #pragma unroll 1
@@ -642,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         float mrow = -INFINITY;
         // Barriers are tested ahead of their use, so that their latencies
         // overlap; one that is not complete yet is waited for there.
-        const bool s_test = mbar_test(&B.s_full[sb], ph), x_test = tc::mbar_test_cluster(&B.x_full[sb], ph);
+        const bool s_test = mbar_test(&B.s_full[sb], ph), x_test = tc::mbar_test_cluster(&B.x_full[q4], u & 1);
         if (!dead && !__all_sync(0xffffffffu, s_test)) dead = !wait_all(&B.s_full[sb], ph, a);
         if (!dead) {
           tc::fence_after_sync();
@@ -652,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&B.s_free[sb]);
-          if (!__all_sync(0xffffffffu, x_test)) dead = !wait_cl(&B.x_full[sb], ph, a);
+          if (!__all_sync(0xffffffffu, x_test)) dead = !wait_cl(&B.x_full[q4], u & 1, a);
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[e] = pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
         }
@@ -660,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const ulonglong2 x =
-                *reinterpret_cast<const ulonglong2*>(sX + sb * kXBytes + ((col / 4 + g) * kOwn + lrow) * 16);
+                *reinterpret_cast<const ulonglong2*>(sX + q4 * (kXBytes / 4) + (col / 4 + g) * 256 + (lane & 15) * 16);
             s[2 * g] = add2(s[2 * g], x.x);
             s[2 * g + 1] = add2(s[2 * g + 1], x.y);
           }
@@ -688,9 +688,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const bool p_test = u < 2 || tc::mbar_test_cluster(&B.pv_done[sb], ((u >> 1) - 1) & 1);
         tc::named_bar_sync(kBarMax + q4, 64);
         if (!dead) {
-          // Every value read from the exchange buffer went into the maximum, so
-          // the peer may refill it (and a relaxed arrival suffices).
-          if (lane == 0) tc::mbar_arrive_remote_relaxed(peer_xempty + sb * 8);
+          // Every value that the two warps read from the exchange buffer went into
+          // their maxima, so the peer may refill it (and a relaxed arrival suffices).
+          if (half == 0 && lane == 0) {
+            mbar_arrive_expect_tx(&B.x_full[q4], kXBytes / 4);
+            tc::mbar_arrive_remote_relaxed(peer_xempty);
+          }
           mrow = fmaxf(mrow, sM[(2 * sb + (half ^ 1)) * kOwn + lrow]);
           // Lazy rescale: only when the row maximum grew by more than the
           // threshold.  A row may see none of the tile's keys (or none so far):
@@ -772,9 +775,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   } else if (warp < kOutWarp) {
     // ===================== queries, and the peer's partial scores ==============
     const int q4 = warp - kSendWarp, hh = lane >> 4;
-    const int lrow = 16 * q4 + (lane & 15);
     const uint32_t lanes = static_cast<uint32_t>(32 * q4 + 16 * peer) << 16;     // the peer's rows
-    const uint32_t peer_x = tc::mapa(smem_u32(sX), peer), peer_xfull = tc::mapa(smem_u32(&B.x_full[0]), peer);
+    uint8_t* xs = sXs + q4 * (kXBytes / 4);      // [keys / 4][16 rows][4 keys]
+    const uint32_t peer_x = tc::mapa(smem_u32(sX), peer) + q4 * (kXBytes / 4);
+    const uint32_t peer_xfull = tc::mapa(smem_u32(&B.x_full[q4]), peer);
     uint32_t qrun = 0;
     int u = 0, k = 0;
 #pragma unroll 1
@@ -859,7 +863,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int sb = u & 1;
-        const bool x_test = u < 2 || tc::mbar_test_cluster(&B.x_empty[sb], ((u >> 1) - 1) & 1);
+        const bool x_test = u < 1 || tc::mbar_test_cluster(&B.x_empty[q4], (u - 1) & 1);
         ok = wait_all(&B.s_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
         tc::fence_after_sync();
@@ -869,12 +873,16 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.s_free[sb]);
-        if (!__all_sync(0xffffffffu, x_test)) ok = wait_cl(&B.x_empty[sb], ((u >> 1) - 1) & 1, a);
+        // (read there means that the copy below has left its source, too)
+        if (!__all_sync(0xffffffffu, x_test)) ok = wait_cl(&B.x_empty[q4], (u - 1) & 1, a);
         if (!ok) break;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
-          tc::st_async_v4(peer_x + sb * kXBytes + ((8 * hh + g) * kOwn + lrow) * 16,
-                          make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]), peer_xfull + sb * 8);
+          *reinterpret_cast<uint4*>(xs + (8 * hh + g) * 256 + (lane & 15) * 16) =
+              make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) bulk_to_peer(peer_x, smem_u32(xs), kXBytes / 4, peer_xfull);
       }
       ++k;
     }
@@ -1047,10 +1055,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
                           tc::sdesc_sw128(v0 + ks * 2 * kGroup, kChunk, kGroup), idesc, (t > 0 || ks > 0) ? 1u : 0u);
         tc::mma_commit_warp(&B.lat_empty[ls]);
         mma_commit_pair_warp(&B.pv_done[sb]);
-        if (lane == 0) {               // tile u + 2's P, and its scores: this tile's have been read
-          mbar_arrive_expect_tx(&B.p_full[sb], kPTx);
-          mbar_arrive_expect_tx(&B.x_full[sb], kXBytes);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(&B.p_full[sb], kPTx);     // tile u + 2's P
       }
       if (!ok) break;
       tc::mma_commit_warp(&B.o_ready);

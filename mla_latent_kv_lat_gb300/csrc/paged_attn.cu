@@ -23,10 +23,15 @@
 //     to shrink if its running maximum grew.  (Exchanging all partial scores in
 //     fp16 and computing every softmax twice takes the same bytes on the wire,
 //     twice the exponentials, and rounds the scores.)
-//   * A tile stays in its stage from its load to its P V, so the chain of steps
-//     between them, not any unit's throughput, bounds the pace: eight warps
-//     share a tile's softmax (16 keys of a row per thread), and a warp's P goes to
-//     the peer as one bulk copy.
+//   * What bounds it: the shared memory, through which a tile moves 216 KB (its
+//     load 36, operands of the products 92, partial scores 64, P 24), 1700 cycles
+//     at 128 bytes a cycle of the 2050 that a tile takes; the tensor pipe is busy
+//     for 1080, the way to the other CTA for 1330.  A tile stays in its stage from
+//     its load to its P V, ~8500 cycles, so the four stages allow no less than 2100
+//     either.  Eight warps share a tile's softmax (16 keys of a row per thread);
+//     two sets of four that take the tiles in turn were 1-2% slower, and so were
+//     16 warps.  512 queries of 128 heads at 33K rows: 3.57 ms, 1320 TFLOP/s, 69%
+//     of the measured rate; 32 tokens at 4K to 32K rows: 157 us, 4.4 TB/s.
 //   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
 //   * A piece's queries come through the ring of cache tiles too, as two stages
 //     before its first tile, so that they are there when the piece before has
@@ -105,7 +110,7 @@ __host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 80 : 96; }
 constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
 
-constexpr int kPieceCost = 4;                // start-up of a piece, in tiles
+constexpr int kPieceCost = 3;                // start-up of a piece (5-6k cycles) in tiles
 constexpr int kMinCost = 3;                  // least cost worth a cluster of its own
 
 // Ring stages that a piece's queries take before its first tile (the e4m3 kernel,
@@ -124,9 +129,10 @@ struct Rec {                                 // what cluster c left unfinished
 
 // Staging of e4m3 latents as fp16 (rows of 512): up to kStageRows rows of the
 // sequences with at least kStageBlocks blocks, in batches of at most kStageSeqs.
-// Measured with and without, one sequence of 128 heads: 8 queries at 33K 112 and
-// 115 us, 152 queries 1161 and 1707 us, but 4 queries 85 and 74 us, and 8 queries
-// at 2000 rows 53 and 43 us (the staging and a second launch cost ~12 us).
+// Measured with and without, one sequence of 128 heads (a query is a block) at 33K
+// rows: 4 queries 70 and 62 us, 8 97 and 97, 12 122 and 134, 152 1066 and 1453; the
+// staging and a second launch cost ~10 us, so at 2000 rows 16 queries take 41 and 32
+// us, 64 69 and 67.
 constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 12;
 
 // Which sequences a launch takes.
@@ -437,7 +443,9 @@ MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
 // at 16 (pt % 8) + 128 h, h < 2, of key pt / 8 + 16 j: a warp reads 4 keys x 128
 // contiguous codes, and all offsets are constants of the thread.  Four warps, a
 // step at a time: with eight warps, or all of a thread's codes loaded first, the
-// larger hot code made the kernel 2-6% slower (8 tokens at 98304 rows, 248 us).
+// larger hot code made the kernel 2-6% slower.  (8 tokens at 98304 rows: 246 us; the
+// codes loaded into the tile's own stage and converted in place, which leaves room
+// for a fourth stage: 254 us.)
 // ---------------------------------------------------------------------------
 constexpr int kProdKeys = 4 * kProducerWarps;
 
@@ -736,8 +744,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
               uint8_t* stage = sLat + ((u + QS * (k + 1)) % LS) * kLatStage;
               for (int q = threadIdx.x; q < kBK * 32; q += 256)
                 if (!key_visible(a, it, base + (q >> 5)))
-                  *reinterpret_cast<uint4*>(stage + (q >> 8) * kGroup + ((q >> 3) & 3) * kChunk + ((q >> 5) & 7) * 128 + (q & 7) * 16) =
-                      make_uint4(0, 0, 0, 0);
+                  *reinterpret_cast<uint4*>(stage + (q >> 8) * kGroup + ((q >> 3) & 3) * kChunk + ((q >> 5) & 7) * 128 +
+                                            (q & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             tc::fence_proxy_async();
             __syncwarp();
@@ -1104,8 +1112,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int rs = u % kRopeStages, row = row_n;
         if (t + 1 < it.n_tiles) row_n = lookup(t + 1);
         // Rows that few blocks read come from HBM: each CTA has half of the next
-        // tile's rows on their way into L2 (32 tokens at 4K-32K rows: 177 -> 169
-        // us; for chunks, whose rows L2 holds, it costs 2-5%).
+        // tile's rows on their way into L2 (32 tokens at 4K-32K rows: 175 -> 157
+        // us; for chunks, whose rows L2 holds, it costs 3-4%, and for e4m3 pages,
+        // which the ring loads further ahead, it changes nothing).
         if (!kE4m3 && it.once && !staged && ch == 0 && row_n < a.n_rows)
           tc::prefetch_l2(a.p.c.pages + (static_cast<int64_t>(row_n) + (rank ? box / 2 : 0)) * kRowF16,
                           static_cast<uint32_t>(box / 2 * kRowF16));

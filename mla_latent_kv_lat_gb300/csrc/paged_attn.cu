@@ -111,7 +111,7 @@ constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, t
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
 
 constexpr int kPieceCost = 3;                // start-up of a piece (5-6k cycles) in tiles
-constexpr int kMinCost = 3;                  // least cost worth a cluster of its own
+constexpr float kCutCost = 4.f;               // of a share (see there)
 
 // Ring stages that a piece's queries take before its first tile (the e4m3 kernel,
 // whose ring its producers fill, loads them without it).  Tile u (counted over
@@ -574,8 +574,17 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const long long total = warp_sum_i64(part), before = warp_sum_i64(lane < warp ? part : 0);
     const long long S0 = before + incl - sum;
     // Cluster x of ge takes [total x / ge, total (x + 1) / ge).
-    const int ge = total < static_cast<long long>(G) * kMinCost
-                       ? max(1, static_cast<int>(static_cast<uint32_t>(total) / kMinCost)) : G;
+    // With less work than that, all of it takes fewer clusters: a shorter piece saves
+    // its tiles' time, another piece of the block costs the merge.  The sum is least
+    // near share = sqrt(cost of a block / kCutCost); blocks of up to two tiles are
+    // not cut.  (One token at 257 rows, 16 heads: shares of 1, 2, 3 take 14.2, 14.9,
+    // 17.0 us; 128 heads at 4000 rows 27.6, 21.8, 21.0, at 16000 shares of 3.3 and 8
+    // 33.6 and 28.5.)
+    const float units = static_cast<float>(total);
+    const float blocks = fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H / kRows);   // about
+    const float share = units <= blocks * (kPieceCost + 2) ? kPieceCost + 2
+                                                           : fmaxf(1.f, rintf(sqrtf(units / (blocks * kCutCost))));
+    const int ge = max(1, static_cast<int>(fminf(static_cast<float>(G), ceilf(units / share))));
     long long lo, hi;
     if (total < (1 << 24)) {             // 32-bit divisions: the 64-bit ones are slow code, run once
       lo = static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ge);

@@ -173,6 +173,15 @@ struct Item {
   bool open;                  // the block goes on past this piece
   bool once;                  // the sequence has one or two blocks
   MLA_DEVINL bool whole() const { return t_lo == 0 && !open; }
+  // The piece in [lo, hi) of the run of costs, in which the block's n tiles start at r0.
+  MLA_DEVINL bool cut(int64_t lo, int64_t hi, int64_t r0, int n) {
+    const int64_t p_lo = max(lo, r0), p_hi = min(hi, r0 + n);
+    if (p_lo >= p_hi) return false;
+    t_lo = static_cast<int32_t>(p_lo - r0);
+    n_tiles = static_cast<int32_t>(p_hi - p_lo);
+    open = p_hi < r0 + n;
+    return true;
+  }
   MLA_DEVINL int key_tile(int t) const {
     const int x = t_lo + t;
     return x < sink_tiles ? x : first + x - sink_tiles;
@@ -233,36 +242,42 @@ struct Walker {
 
 struct Start {
   int64_t lo, hi;     // the cluster's range in the run of costs
-  int64_t S;          // where slot g's cost starts in it
+  int64_t S;          // where slot g's cost starts in it (ends, if it has the first piece)
   int32_t g;          // first slot that ends after lo (n_slots: none)
   int32_t b;          // and its sequence
+  Item it;            // the cluster's first piece, in slot g (n_tiles 0: none there)
 };
 
 // This cluster's pieces in order; every role walks the same sequence.
 struct Iter {
   Walker w;
+  const Start* st;
   int64_t lo, hi, S;
   int32_t g;
-  MLA_DEVINL void init(const TcArgs& a, const Start& st) {
-    lo = st.lo;
-    hi = st.hi;
-    S = st.S;
-    g = st.g;
-    w.b = st.b;
-    if (g < a.n_slots) w.load(a);
+  bool first;                  // the next piece is st->it
+  MLA_DEVINL void init(const Start& start) {
+    st = &start;
+    lo = start.lo;
+    hi = start.hi;
+    S = start.S;
+    g = start.g;
+    w.b = start.b - 1;         // loaded by the first block asked for
+    w.s1 = -1;
+    first = start.it.n_tiles > 0;
+    if (first) ++g;
   }
   MLA_DEVINL bool next(const TcArgs& a, Item& it) {
+    if (first) {
+      first = false;
+      it = st->it;
+      return true;
+    }
     while (g < a.n_slots && S < hi) {
       const int n = w.block(a, g++, it);
       if (n == 0) continue;
-      const int64_t r0 = S + kPieceCost;         // where the block's tiles start
+      const int64_t r0 = S + kPieceCost;
       S = r0 + n;
-      const int64_t p_lo = max(lo, r0), p_hi = min(hi, S);
-      if (p_lo >= p_hi) continue;
-      it.t_lo = static_cast<int32_t>(p_lo - r0);
-      it.n_tiles = static_cast<int32_t>(p_hi - p_lo);
-      it.open = p_hi < S;
-      return true;
+      if (it.cut(lo, hi, r0, n)) return true;
     }
     return false;
   }
@@ -334,6 +349,13 @@ MLA_DEVINL bool wait_cl(uint64_t* bar, uint32_t parity, const TcArgs& a) {
 // in a 64-byte-swizzled one (rows of 32 halves).
 MLA_DEVINL uint32_t unit128(int row, int u) { return static_cast<uint32_t>(row * 128 + ((u ^ (row & 7)) << 4)); }
 MLA_DEVINL uint32_t unit64(int row, int u) { return static_cast<uint32_t>(row * 64 + ((u ^ ((row >> 1) & 3)) << 4)); }
+
+// Sum of 0 <= x < 2^52 over the warp: two reductions of 26 bits.
+MLA_DEVINL long long warp_sum_wide(long long x) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x) & 0x3FFFFFFu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x >> 26));
+  return (static_cast<long long>(hi) << 26) + lo;
+}
 
 MLA_DEVINL void st_async_b32(uint32_t remote_addr, uint32_t v, uint32_t remote_bar) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(remote_addr), "r"(v),
@@ -531,6 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     B.st.g = a.n_slots;
     B.st.lo = B.st.hi = B.st.S = 0;
     B.st.b = 0;
+    B.st.it.n_tiles = 0;
   }
   if (warp == kQkWarp) {
     tc::tmem_alloc(&B.tmem, 512);
@@ -541,6 +564,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     tc::prefetch_tmap(&tm_rope);
     tc::prefetch_tmap(&tm_q);
   }
+  // The peer's barriers are ready once its threads have come here: waited for below.
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   // All above may run while the kernel before finishes (programmatic launch).
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0) record_bad_seqs(a.p.cu, a.p.seq_len, a.p.B, a.p.T, a.p.c.max_rows(), a.p.err);
@@ -571,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     if (lane == 31) red[warp] = incl;
     __syncthreads();
     const long long part = lane < NT / 32 ? red[lane] : 0;
-    const long long total = warp_sum_i64(part), before = warp_sum_i64(lane < warp ? part : 0);
+    const long long total = warp_sum_wide(part), before = warp_sum_wide(lane < warp ? part : 0);
     const long long S0 = before + incl - sum;
     // Cluster x of ge takes [total x / ge, total (x + 1) / ge).
     // With less work than that, all of it takes fewer clusters: a shorter piece saves
@@ -580,48 +605,54 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     // not cut.  (One token at 257 rows, 16 heads: shares of 1, 2, 3 take 14.2, 14.9,
     // 17.0 us; 128 heads at 4000 rows 27.6, 21.8, 21.0, at 16000 shares of 3.3 and 8
     // 33.6 and 28.5.)
-    const float units = static_cast<float>(total);
-    const float blocks = fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H / kRows);   // about
-    const float share = units <= blocks * (kPieceCost + 2) ? kPieceCost + 2
-                                                           : fmaxf(1.f, rintf(sqrtf(units / (blocks * kCutCost))));
-    const int ge = max(1, static_cast<int>(fminf(static_cast<float>(G), ceilf(units / share))));
+    int ge = G;
     long long lo, hi;
-    if (total < (1 << 24)) {             // 32-bit divisions: the 64-bit ones are slow code, run once
-      lo = static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ge);
-      hi = static_cast<uint32_t>(total) * static_cast<uint32_t>(c + 1) / static_cast<uint32_t>(ge);
+    if (total < (1 << 24)) {             // (so its divisions have 32 bits: the 64-bit ones are slow code, run once)
+      const uint32_t units = static_cast<uint32_t>(total);
+      const float blocks = fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H * (1.f / kRows));   // about
+      uint32_t share = kPieceCost + 2;
+      if (units > blocks * share) {
+        const float x = __fdividef(static_cast<float>(units), blocks * kCutCost);
+        share = max(1u, static_cast<uint32_t>(x * rsqrtf(x) + 0.5f));
+      }
+      if (units < static_cast<uint32_t>(G) * share) ge = max(1, static_cast<int>((units + share - 1) / share));
+      lo = units * static_cast<uint32_t>(c) / static_cast<uint32_t>(ge);
+      hi = units * static_cast<uint32_t>(c + 1) / static_cast<uint32_t>(ge);
     } else {
       lo = total * c / ge;
       hi = total * (c + 1) / ge;
     }
     if (c < ge && sum > 0 && S0 <= lo && lo < S0 + sum) {
       long long S = S0;
-      int g = g0;
-      if (per > 1) {                     // else `w` and `it` are the slot's
+      int g = g0, n = static_cast<int>(sum) - kPieceCost;
+      if (per > 1) {                     // else `it` and n are the slot's
         w.init(a, g0);
         for (; g < g1; ++g) {
-          const int n = w.block(a, g, it);
+          n = w.block(a, g, it);
           const long long e = S + (n > 0 ? n + kPieceCost : 0);
           if (lo < e) break;
           S = e;
         }
       }
+      const bool piece = it.cut(lo, hi, S + kPieceCost, n);
       B.st.lo = lo;
       B.st.hi = hi;
-      B.st.S = S;
+      B.st.S = piece ? S + kPieceCost + n : S;
       B.st.g = g;
       B.st.b = w.b;
+      if (piece) B.st.it = it;
       if (kE4m3) prefetch_q(a, it, rank);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  tc::cluster_sync();                 // the peer's barriers are ready before any remote arrival
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   tc::fence_after_sync();
   const uint32_t tmem = B.tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   Iter items;
-  items.init(a, B.st);
+  items.init(B.st);
   Item it;
   bool ok = true;
 

@@ -153,7 +153,8 @@ def mla_paged_step(q_nope, q_pe, c_kv, k_pe, wk_b, wv_b, pages, block_table, cu_
                    bufs: Optional[PagedBuffers] = None, scale=None, stream=None) -> PagedBuffers:
     """One step of a batch on a paged cache: the new tokens' rows into their pages, then absorb -> attention over
     the pages -> late decompression.  A sequence may bring one token (decode), a chunk (prefill) or none; rows of
-    the token arrays behind the last sequence are padding (their ``o`` follows from what ``bufs.o_lat`` held)."""
+    the token arrays behind the last sequence are padding, finite (absorption checks all rows' range); their ``o``
+    follows from what ``bufs.o_lat`` held."""
     T, H = q_nope.shape[0], q_nope.shape[1]
     if bufs is None:
         with B.stream_context(stream, q_nope.device.index):

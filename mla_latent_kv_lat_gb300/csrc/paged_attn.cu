@@ -598,16 +598,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const long long part = lane < NT / 32 ? red[lane] : 0;
     const long long total = warp_sum_wide(part), before = warp_sum_wide(lane < warp ? part : 0);
     const long long S0 = before + incl - sum;
-    // Cluster x of ge takes [total x / ge, total (x + 1) / ge).
-    // With less work than that, all of it takes fewer clusters: a shorter piece saves
+    // Cluster x of G takes [total x / G, total (x + 1) / G).  Short work takes fewer
+    // clusters, with an equal share each: a shorter piece saves
     // its tiles' time, another piece of the block costs the merge.  The sum is least
     // near share = sqrt(cost of a block / kCutCost); blocks of up to two tiles are
     // not cut.  (One token at 257 rows, 16 heads: shares of 1, 2, 3 take 14.2, 14.9,
     // 17.0 us; 128 heads at 4000 rows 27.6, 21.8, 21.0, at 16000 shares of 3.3 and 8
     // 33.6 and 28.5.)
-    int ge = G;
     long long lo, hi;
-    if (total < (1 << 24)) {             // (so its divisions have 32 bits: the 64-bit ones are slow code, run once)
+    if (total < (1 << 24)) {
       const uint32_t units = static_cast<uint32_t>(total);
       const float blocks = fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H * (1.f / kRows));   // about
       uint32_t share = kPieceCost + 2;
@@ -615,14 +614,18 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const float x = __fdividef(static_cast<float>(units), blocks * kCutCost);
         share = max(1u, static_cast<uint32_t>(x * rsqrtf(x) + 0.5f));
       }
-      if (units < static_cast<uint32_t>(G) * share) ge = max(1, static_cast<int>((units + share - 1) / share));
-      lo = units * static_cast<uint32_t>(c) / static_cast<uint32_t>(ge);
-      hi = units * static_cast<uint32_t>(c + 1) / static_cast<uint32_t>(ge);
+      if (units <= static_cast<uint32_t>(G) * share) {
+        lo = min(units, static_cast<uint32_t>(c) * share);
+        hi = min(units, static_cast<uint32_t>(c + 1) * share);
+      } else {                           // (32-bit divisions: the 64-bit ones are slow code, run once)
+        lo = units * static_cast<uint32_t>(c) / static_cast<uint32_t>(G);
+        hi = units * static_cast<uint32_t>(c + 1) / static_cast<uint32_t>(G);
+      }
     } else {
-      lo = total * c / ge;
-      hi = total * (c + 1) / ge;
+      lo = total * c / G;
+      hi = total * (c + 1) / G;
     }
-    if (c < ge && sum > 0 && S0 <= lo && lo < S0 + sum) {
+    if (lo < hi && sum > 0 && S0 <= lo && lo < S0 + sum) {
       long long S = S0;
       int g = g0, n = static_cast<int>(sum) - kPieceCost;
       if (per > 1) {                     // else `it` and n are the slot's
@@ -1121,16 +1124,23 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const int j = lane / 3, ch = lane % 3;
     const bool mine = j < nb, staged = !kE4m3 && a.p.c.e4m3;
     const int rope_x = (a.p.c.e4m3 ? 0 : kLatent) + kRopeHalf * static_cast<int>(rank);
-    auto lookup = [&](int t) -> int {
+    // A box's table entry, and its row given the entry.
+    auto entry = [&](int t) -> int32_t {
+      const int key = it.key_tile(t) * kBK + j * box;
+      return mine && any_visible(a, it, key, box)
+                 ? __ldg(a.p.c.table + it.b * a.p.c.table_stride + (key >> a.p.c.page_shift)) : 0;
+    };
+    auto row_at = [&](int t, int32_t id) -> int {
       const int key = it.key_tile(t) * kBK + j * box;
       if (!mine || !any_visible(a, it, key, box)) return a.n_rows;
-      const int64_t x = a.p.c.row_of(it.b, key);
-      if (x < 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
-      return x >= 0 ? static_cast<int>(x) : a.n_rows;
+      if (id >= 0 && id < a.p.c.n_pages) return (id << a.p.c.page_shift) + (key & ((1 << a.p.c.page_shift) - 1));
+      record_error(a.p.err, MLA_ERR_INVALID_ARG);
+      return a.n_rows;
     };
     int u = 0, k = 0;
 #pragma unroll 1
     while (ok && items.next(a, it)) {
+      const int32_t id0 = entry(0);            // (on its way while the queries are asked for)
 #pragma unroll 1
       for (int q = 0; q < QS; ++q) {           // the queries: 128 rows x 64 dims twice a stage
         const int r = u + QS * k + q, ls = r % LS;
@@ -1146,11 +1156,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       ++k;
       const int32_t base = staged ? __ldg(a.stage_base + it.b) : 0;
       if (kE4m3 && u > 0 && lane == 0) prefetch_q(a, it, rank);     // some tiles before the senders load it
-      int row_n = lookup(0);
+      int row_n = row_at(0, id0);
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int rs = u % kRopeStages, row = row_n;
-        if (t + 1 < it.n_tiles) row_n = lookup(t + 1);
+        if (t + 1 < it.n_tiles) row_n = row_at(t + 1, entry(t + 1));
         // Rows that few blocks read come from HBM: each CTA has half of the next
         // tile's rows on their way into L2 (32 tokens at 4K-32K rows: 175 -> 157
         // us; for chunks, whose rows L2 holds, it costs 3-4%, and for e4m3 pages,

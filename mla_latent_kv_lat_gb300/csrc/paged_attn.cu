@@ -118,13 +118,20 @@ constexpr float kCutCost = 4.f;               // of a share (see there)
 // all pieces) of piece k has ring position u + (k + 1) q_slots.
 __host__ __device__ constexpr int q_slots(bool e4m3) { return e4m3 ? 0 : 2; }
 
-struct Rec {                                 // what cluster c left unfinished
-  int32_t open_g;     // slot of the block that starts in c and ends in a later cluster (-1: none)
-  int32_t nvalid;     // its rows
+struct __align__(16) Rec {     // the block that starts in cluster c and ends in a later one
+  int64_t end;        // where it ends in the run of costs
+  int64_t total;      // the run's length
   int64_t qrow0;      // its first (token, head) row
-  int32_t cont_g;     // slot of the block that c continues from an earlier cluster (-1: none)
-  int32_t cont_open;  // and that goes on past c
-  int64_t pad;
+  int32_t nvalid;     // its rows (0: no such block)
+  int32_t share;      // of every cluster; 0: all have total / G
+  // Clusters whose range starts before `end`.
+  MLA_DEVINL int clusters(int G) const {
+    if (share > 0) return static_cast<int>((static_cast<uint32_t>(end) + share - 1) / share);
+    if (total < (1 << 24))
+      return static_cast<int>((static_cast<uint32_t>(end) * G + static_cast<uint32_t>(total) - 1) /
+                              static_cast<uint32_t>(total));
+    return static_cast<int>((end * G + total - 1) / total);
+  }
 };
 
 // Staging of e4m3 latents as fp16 (rows of 512): up to kStageRows rows of the
@@ -162,7 +169,7 @@ MLA_DEVINL int64_t slot_of_seq(const PagedAttnArgs& a, int b) {
 }
 
 struct Item {
-  int32_t b, g;               // sequence, slot
+  int32_t b;                  // sequence
   int32_t kend, wlo;          // keys some row of the block sees: [0, n_sink) and [wlo, kend)
   int32_t first, sink_tiles;  // tile t of the block is t < sink_tiles ? t : first + t - sink_tiles
   int32_t t_lo, n_tiles;      // this piece: tiles [t_lo, t_lo + n_tiles)
@@ -226,7 +233,6 @@ struct Walker {
     const uint32_t H = static_cast<uint32_t>(a.H), r0 = static_cast<uint32_t>(i) * kRows;
     const uint32_t r1 = min(r0 + kRows, rows);
     it.b = b;
-    it.g = static_cast<int32_t>(g);
     it.nvalid = static_cast<int32_t>(r1 - r0);
     it.once = rows <= 2 * kRows;
     it.row0 = r0;
@@ -245,6 +251,8 @@ struct Start {
   int64_t S;          // where slot g's cost starts in it (ends, if it has the first piece)
   int32_t g;          // first slot that ends after lo (n_slots: none)
   int32_t b;          // and its sequence
+  int32_t share;      // of every cluster (the last one's may be less); 0: all have total / G
+  int64_t total;
   Item it;            // the cluster's first piece, in slot g (n_tiles 0: none there)
 };
 
@@ -602,14 +610,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     // clusters, with an equal share each: a shorter piece saves
     // its tiles' time, another piece of the block costs the merge.  The sum is least
     // near share = sqrt(cost of a block / kCutCost); blocks of up to two tiles are
-    // not cut.  (One token at 257 rows, 16 heads: shares of 1, 2, 3 take 14.2, 14.9,
-    // 17.0 us; 128 heads at 4000 rows 27.6, 21.8, 21.0, at 16000 shares of 3.3 and 8
-    // 33.6 and 28.5.)
+    // not cut.  (Measured when a call took 2 us longer than now: one token at 257 rows,
+    // 16 heads, shares of 1, 2, 3 14.2, 14.9, 17.0 us; 128 heads at 4000 rows 27.6,
+    // 21.8, 21.0, at 16000 shares of 3.3 and 8 33.6 and 28.5.)
     long long lo, hi;
+    uint32_t share = 0;
     if (total < (1 << 24)) {
       const uint32_t units = static_cast<uint32_t>(total);
       const float blocks = fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H * (1.f / kRows));   // about
-      uint32_t share = kPieceCost + 2;
+      share = kPieceCost + 2;
       if (units > blocks * share) {
         const float x = __fdividef(static_cast<float>(units), blocks * kCutCost);
         share = max(1u, static_cast<uint32_t>(x * rsqrtf(x) + 0.5f));
@@ -618,6 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         lo = min(units, static_cast<uint32_t>(c) * share);
         hi = min(units, static_cast<uint32_t>(c + 1) * share);
       } else {                           // (32-bit divisions: the 64-bit ones are slow code, run once)
+        share = 0;
         lo = units * static_cast<uint32_t>(c) / static_cast<uint32_t>(G);
         hi = units * static_cast<uint32_t>(c + 1) / static_cast<uint32_t>(G);
       }
@@ -638,6 +648,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         }
       }
       const bool piece = it.cut(lo, hi, S + kPieceCost, n);
+      B.st.share = static_cast<int32_t>(share);
+      B.st.total = total;
       B.st.lo = lo;
       B.st.hi = hi;
       B.st.S = piece ? S + kPieceCost + n : S;
@@ -1025,18 +1037,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   } else if (warp == kQkWarp) {
     // ============================== score MMAs =================================
     constexpr uint32_t idesc = tc::idesc_f16(128, kBK, false, false, false);
-    Rec rec = {-1, 0, 0, -1, 0, 0};
+    Rec rec = {0, 0, 0, 0, 0};
     int u = 0, k = 0;
 #pragma unroll 1
     while (ok && items.next(a, it)) {
-      if (it.t_lo > 0) {
-        rec.cont_g = it.g;
-        rec.cont_open = it.open ? 1 : 0;
-      } else if (it.open) {
-        rec.open_g = it.g;
-        rec.nvalid = it.nvalid;
-        rec.qrow0 = it.qrow0;
-      }
+      if (it.t_lo == 0 && it.open) rec = {items.S, items.st->total, it.qrow0, it.nvalid, items.st->share};
       ok = wait_all(&B.q_ready, k & 1, a);
       tc::fence_after_sync();
       if (ok && lane < QS) mbar_arrive(&B.lat_empty[(u + QS * k + lane) % LS]);   // the queries have left the ring
@@ -1066,7 +1071,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         tc::mma_commit_warp(&B.s_full[sb]);
       }
     }
-    if (!ok) rec.open_g = rec.cont_g = -1;
+    if (!ok) rec.nvalid = 0;
     if (rank == 0 && lane == 0) a.rec[c] = rec;
   } else if (warp == kPvWarp) {
     // =============================== P V MMAs ==================================
@@ -1238,50 +1243,67 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 }
 
 // ---------------------------------------------------------------------------
-// Merge the partials of every block that a cluster boundary cut: block (x =
-// cluster in which it starts, y = group of 4 rows), four warps a row, 4 columns
-// a lane, the loads of eight partials in flight.  (One warp a row, 16 columns a
-// lane, took 20 us longer for a row cut into 76 pieces.)  Launched as a
-// programmatic dependent of the attention.
+// Merge the partials of every block that a cluster boundary cut: four warps a row,
+// 4 columns a lane.  (One warp a row, 16 columns a lane, took 20 us longer for a row
+// cut into 76 pieces.)  Grid: x = the cluster in which the block starts, y = group of
+// 4 rows; with few blocks (kFew) x = which of the cut blocks, so that one token does
+// not start 2432 blocks for a few that have work, and eight partials are under way
+// with the statistics, in twice the registers.  (With and without: one token at 257
+// rows, 16 heads, 12.6 and 13.0 us, 128 heads at 100 rows 12.0 and 14.1, 8 tokens at
+// 1000 rows 18.8 and 19.5; but 16 tokens 22.0 and 21.8, 32 tokens 31.7 and 29.4.)  Launched as a programmatic dependent of the
+// attention.
 // ---------------------------------------------------------------------------
-constexpr int kCombRows = 4;
+constexpr int kCombRows = 4, kMaxClusters = 128;
 
-__global__ void __launch_bounds__(128 * kCombRows) paged_combine_kernel(const TcArgs a, int G) {
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <bool kFew>
+__global__ void __launch_bounds__(128 * kCombRows, kFew ? 2 : 4) paged_combine_kernel(const TcArgs a, int G) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y * kCombRows + (warp >> 2), col = 128 * (warp & 3) + 4 * lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Rec* rec = a.rec;
-  const int g = rec[c].open_g;
-  if (g < 0 || row >= rec[c].nvalid) return;
-  // the clusters after c that continue block g
-  int n = 1;
-  for (int x0 = c + 1; x0 < G; x0 += 32) {
-    const int x = x0 + lane;
-    const bool cont = x < G && rec[x].cont_g == g;
-    const unsigned stop = ~__ballot_sync(0xffffffffu, cont);
-    n += stop ? __ffs(stop) - 1 : 32;
-    if (stop) break;
+  int c = static_cast<int>(blockIdx.x);
+  if constexpr (kFew) {
+    int cut[kMaxClusters / 32], before = 0;
+#pragma unroll
+    for (int q = 0; q < kMaxClusters / 32; ++q) cut[q] = 32 * q + lane < G ? a.rec[32 * q + lane].nvalid : 0;
+    c = -1;
+#pragma unroll
+    for (int q = 0; q < kMaxClusters / 32; ++q) {
+      const uint32_t some = __ballot_sync(0xffffffffu, cut[q] > 0);
+      const int rank = before + __popc(some & ((1u << lane) - 1));
+      const uint32_t mine = __ballot_sync(0xffffffffu, cut[q] > 0 && rank == static_cast<int>(blockIdx.x));
+      if (mine) c = 32 * q + __ffs(mine) - 1;
+      before += __popc(some);
+    }
+    if (c < 0) return;
   }
+  const Rec r = a.rec[c];
+  if (row >= r.nvalid) return;
+  const int n = r.clusters(G) - c;               // pieces: one in each of these clusters
   auto slot = [&](int s) { return (2 * static_cast<int64_t>(c + s) + (s == 0 ? 1 : 0)) * kRows + row; };
-  float M = -INFINITY;
-  for (int s = lane; s < n; s += 32) M = fmaxf(M, a.ws_ml[2 * slot(s)]);
+  auto stat = [&](int s) {
+    return s < n ? *reinterpret_cast<const float2*>(a.ws_ml + 2 * slot(s)) : make_float2(-INFINITY, 0.f);
+  };
+  float4 v[8];
+  auto fetch = [&](int s0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = s0 + j < n ? *reinterpret_cast<const float4*>(a.ws_o + slot(s0 + j) * kLatent + col)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  if (kFew) fetch(0);
+  float2 ml = stat(lane);
+  float M = ml.x;
+  for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, a.ws_ml[2 * slot(s)]);
   M = warp_max(M);
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < n; s0 += 32) {
-    float w = 0.f;                               // lane: partial s0 + lane's weight
-    if (s0 + lane < n) {
-      const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + 2 * slot(s0 + lane));
-      w = exp2f(ml.x - M) * ml.y;
-    }
+    if (s0 > 0) ml = stat(s0 + lane);
+    const float w = s0 + lane < n ? exp2f(ml.x - M) * ml.y : 0.f;      // lane: partial s0 + lane's weight
     L += w;
     for (int j0 = 0; j0 < min(32, n - s0); j0 += 8) {
-      float4 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = s0 + j0 + j < n ? *reinterpret_cast<const float4*>(a.ws_o + slot(s0 + j0 + j) * kLatent + col)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!kFew || s0 + j0 > 0) fetch(s0 + j0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float wj = __shfl_sync(0xffffffffu, w, j0 + j);
@@ -1293,7 +1315,7 @@ __global__ void __launch_bounds__(128 * kCombRows) paged_combine_kernel(const Tc
     }
   }
   const float inv = 1.f / warp_sum(L);
-  *reinterpret_cast<uint2*>(a.p.o_lat + (rec[c].qrow0 + row) * kLatent + col) =
+  *reinterpret_cast<uint2*>(a.p.o_lat + (r.qrow0 + row) * kLatent + col) =
       make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
 }
 
@@ -1403,7 +1425,7 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
   }
 }
 
-int clusters() { return max(1, device_sm_count() / 2); }
+int clusters() { return max(1, min(kMaxClusters, device_sm_count() / 2)); }
 
 // Workspace: partials, their sums, the clusters' records (all multiples of 16
 // bytes), then the staging.
@@ -1428,7 +1450,12 @@ cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUte
   const int G = clusters();
   e = launch_dependent(kern, dim3(2 * G), dim3(threads(kE4m3)), kSmem, stream, tm, tr, tq, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_combine_kernel, dim3(static_cast<unsigned>(G), kRows / kCombRows),
+  // at most n_slots blocks, of at most T x H rows
+  const int64_t rows = min(static_cast<int64_t>(kRows), static_cast<int64_t>(a.p.T) * a.p.H);
+  const int groups = static_cast<int>((rows + kCombRows - 1) / kCombRows);
+  const bool few = a.n_slots < G && a.n_slots * groups <= 10 * G;
+  return launch_dependent(few ? paged_combine_kernel<true> : paged_combine_kernel<false>,
+                          dim3(static_cast<unsigned>(few ? a.n_slots : G), static_cast<unsigned>(groups)),
                           dim3(128 * kCombRows), 0, stream, a, G);
 }
 

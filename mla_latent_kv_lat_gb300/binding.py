@@ -9,6 +9,7 @@ of libmla; if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -364,6 +365,7 @@ def _paged_device(t, name: str) -> int:
     return t.get_device()
 
 
+_dims = functools.lru_cache(maxsize=64)(make_dims)   # (the calls only read it)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object around it
 
 
@@ -463,7 +465,7 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
         with stream_context(stream, dev):
             workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)
     st = load_library().mla_attn_paged(
-        make_dims(H, scale), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
+        _dims(H, scale), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
         _arg(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE), dev), cache,
         _arg(cu_q, "cu_q", torch.int32, (Bn + 1,), dev), _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn, T,
         window, n_sink, _arg(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(),

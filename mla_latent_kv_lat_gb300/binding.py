@@ -465,7 +465,7 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
         with stream_context(stream, dev):
             workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)
     st = load_library().mla_attn_paged(
-        _dims(H, scale), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
+        _dims(H, scale if scale is None else float(scale)), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
         _arg(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE), dev), cache,
         _arg(cu_q, "cu_q", torch.int32, (Bn + 1,), dev), _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn, T,
         window, n_sink, _arg(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(),

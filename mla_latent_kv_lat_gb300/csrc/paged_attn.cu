@@ -469,18 +469,21 @@ MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
 
 // ---------------------------------------------------------------------------
 // e4m3 producer: this CTA's 256 codes of a tile's 64 rows from their ring stage
-// into a tile stage, as fp16.  Step j of thread pt (of 128) takes 16 codes each
-// at 16 (pt % 8) + 128 h, h < 2, of key pt / 8 + 16 j: a warp reads 4 keys x 128
-// contiguous codes, and all offsets are constants of the thread.  Four warps, a
-// step at a time: with eight warps, or all of a thread's codes loaded first, the
-// larger hot code made the kernel 2-6% slower.  (8 tokens at 98304 rows: 246 us; the
-// codes loaded into the tile's own stage and converted in place, which leaves room
-// for a fourth stage: 254 us.)
+// into a tile stage, as fp16.  Step j of thread pt (of 128) takes 16 codes each at
+// 16 c0 + 128 h, h < 2, of key k0 + 16 j; all offsets are constants of the thread.
+// Eight consecutive lanes take half of the units of two adjacent keys, the one's
+// lower and the other's upper half: their loads and stores then lie in eight
+// different 16-byte columns of the banks (a key's eight units, 4 chunk-0 and 4
+// chunk-1 stores in the same columns, 240 us for 8 tokens at 98304 rows; so 233).
+// Four warps, a step at a time: with eight warps, or all of a thread's codes loaded
+// first, the larger hot code made the kernel 2-6% slower; the codes loaded into the
+// tile's own stage and converted in place, which leaves room for a fourth stage, 3%.
 // ---------------------------------------------------------------------------
 constexpr int kProdKeys = 4 * kProducerWarps;
 
 MLA_DEVINL void produce(const uint8_t* raw, uint8_t* lat, int rank, int pt, int j) {
-  const int k0 = pt >> 3, c0 = pt & 7, key = k0 + kProdKeys * j;
+  const int k0 = 2 * (pt >> 4) + ((pt >> 2) & 1), c0 = (pt & 3) | (((pt >> 2) ^ (pt >> 3)) & 1) << 2;
+  const int key = k0 + kProdKeys * j;
   const uint32_t dst = (k0 >> 3) * kGroup + (c0 >> 2) * kChunk + unit128(k0 & 7, 2 * (c0 & 3));
   const uint8_t* src = raw + key * 256 + 16 * c0;
   const uint4 v[2] = {*reinterpret_cast<const uint4*>(src), *reinterpret_cast<const uint4*>(src + 128)};

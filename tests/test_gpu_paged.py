@@ -226,6 +226,19 @@ def test_attention_split_over_the_keys(e4m3):
     check(b, run(b))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,H,top", [(5, 128, 128), (24, 16, 900), (30, 128, 500), (90, 128, 200), (700, 16, 90)])
+def test_batches_from_few_blocks_to_many(B, H, top, e4m3):
+    """Blocks that are not cut, equal shares, a run shared by all clusters, more sequences than threads; some
+    sequences bring two tokens, some none."""
+    rng = np.random.default_rng(B)
+    news = [int(n) for n in rng.choice((0, 1, 1, 1, 1, 2), B)]
+    lens = [max(n, int(x)) for n, x in zip(news, rng.integers(1, top + 1, B))]
+    news[0], lens[0] = 1, top
+    b = Batch(22, e4m3, H, 16, news, lens, pad=3)
+    check(b, run(b))
+
+
 def test_e4m3_chunks_beyond_the_staging():
     """Two chunks whose rows are staged and a third that no longer fits, on a few pages named many times."""
     ps, H, lens, news = 64, 16, [70001, 50000, 30001], [100, 128, 100]
@@ -254,6 +267,29 @@ def test_e4m3_chunks_beyond_the_staging():
             tol = (2.0 ** -11 + 2.0 ** -12) * mag + 2.0 ** -11 * ref.abs() + 2.0 ** -24
             assert ((out[at + i].double() - ref).abs() <= tol).all()
         at += news[b]
+
+
+def test_a_chunk_of_more_than_2_to_the_24_tiles():
+    """8600 tokens of 128 heads at the end of 131500 rows, on a few pages named many times."""
+    ps, H, T, L = 64, 128, 8600, 131500
+    g = torch.Generator(device="cuda").manual_seed(9)
+    pages = torch.randn(8, ps, 576, device="cuda", generator=g).half()
+    table = torch.randint(0, 8, (1, -(-L // ps)), dtype=torch.int32, device="cuda", generator=g)
+    q_lat = torch.randn(T, H, 512, device="cuda", generator=g, dtype=torch.float16)
+    q_pe = torch.randn(T, H, 64, device="cuda", generator=g, dtype=torch.bfloat16)
+    out = torch.full((T, H, 512), float("nan"), dtype=torch.float16, device="cuda")
+    mla.mla_attn_paged(q_lat, q_pe, pages, table, i32([0, T]), i32([L]), out, scale=SCALE)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    assert torch.isfinite(out).all()
+    p = torch.arange(L, device="cuda")
+    rows = pages.reshape(-1, 576)[table[0].long()[p // ps] * ps + p % ps].double()
+    for i in (0, 4321, T - 1):
+        n = L - T + i + 1
+        w = ((torch.cat([q_lat[i].double(), q_pe[i].double()], -1) @ rows[:n].T) * SCALE).softmax(-1)
+        ref, mag = w @ rows[:n, :512], w @ rows[:n, :512].abs()
+        tol = (2.0 ** -11 + 2.0 ** -12) * mag + 2.0 ** -11 * ref.abs() + 2.0 ** -24
+        assert ((out[i].double() - ref).abs() <= tol).all()
 
 
 def test_sharp_and_flat_scores():

@@ -38,13 +38,12 @@
 //     issued its last score product.  (Loaded by the sender warps themselves they
 //     took 9-11k cycles a piece.)
 //   * fp16 pages come in by TMA as they are, and so do the RoPE parts of e4m3
-//     pages; their codes come into a ring of their own, from which producer warps
-//     turn them into fp16 tiles (code x scale, exact).  (Read by the producers
-//     from global memory instead, with a fourth tile stage in the ring's place,
-//     the e4m3 attention was slower than the fp16 one.)  A sequence whose chunk has
-//     several blocks would have its codes converted once per block: its visible
-//     rows are converted once, before, into the workspace, and the kernel for fp16
-//     pages takes it, the e4m3 kernel the other sequences of the batch.
+//     pages; their codes come into the second half of the tile's stage, where
+//     producer warps turn them into the fp16 tile (code x scale, exact).  (With a
+//     ring of their own for the codes there is room for three stages: 3% slower.)
+//     A sequence whose chunk has several blocks would have its codes converted once
+//     per block: its visible rows are converted once, before, into the workspace,
+//     and the kernel for fp16 pages takes it, the e4m3 kernel the other sequences.
 // Work split: a block costs its tiles plus `kPieceCost`; the costs of all
 // blocks form one run, which the clusters share evenly.  A cluster's piece that
 // is a whole block writes o_lat; a block cut by a cluster boundary leaves fp32
@@ -70,11 +69,10 @@ constexpr int kOwn = kRows / 2;              // rows whose softmax a CTA compute
 constexpr int kChunk = 8 * 128;              // 1 KB: 8 keys x 64 fp16
 constexpr int kGroup = 4 * kChunk;           // 4 KB: 8 keys x this CTA's 256 latent dims
 constexpr int kLatStage = kBK / 8 * kGroup;  // 32 KB
-__host__ __device__ constexpr int lat_stages(bool e4m3) { return e4m3 ? 3 : 4; }
-// e4m3 ring: 64 keys x 256 codes (this CTA's half), then the rows' 16 scale bytes.
-constexpr int kRawCodes = kBK * 256, kRawStage = kRawCodes + kBK * 16, kRawStages = 2;
-constexpr int kRingBytes = lat_stages(true) * kLatStage + kRawStages * kRawStage;   // the larger of the two kernels'
-static_assert(kRingBytes >= lat_stages(false) * kLatStage, "tile ring");
+constexpr int LS = 4;                        // tile stages
+// e4m3: a tile's codes (64 keys x 256, this CTA's half) arrive in the second half of
+// its stage, their rows' 16 scale bytes beside it.
+constexpr int kRawOff = kLatStage / 2, kRawScale = kBK * 16, kRawBytes = kBK * 256 + kRawScale;
 constexpr int kRopeStages = 2;               // a RoPE tile is done with after its score product
 constexpr int kRopeHalf = 32;
 constexpr int kRopeChunk = kBK * kRopeHalf * 2;     // 4 KB
@@ -83,8 +81,8 @@ constexpr int kPBytes = kRows * 128;         // 16 KB: two halves of 128 rows x 
 constexpr int kXBytes = kOwn * kBK * 4;      // 16 KB: 64 rows x 64 keys fp32
 constexpr int kPTx = kOwn * kBK * 2 + kOwn * 4;     // bytes a CTA gets per tile: the other's P rows and factors
 constexpr int kOffLat = kQRopeBytes;
-constexpr int kOffRaw = kOffLat + lat_stages(true) * kLatStage;      // (e4m3)
-constexpr int kOffRope = kOffLat + kRingBytes;
+constexpr int kOffScale = kOffLat + LS * kLatStage;  // (e4m3)
+constexpr int kOffRope = kOffScale + LS * kRawScale;
 constexpr int kOffP = kOffRope + kRopeStages * kRopeChunk;
 constexpr int kOffX = kOffP + 2 * kPBytes;
 constexpr int kOffXs = kOffX + kXBytes;               // what goes to the other CTA
@@ -102,6 +100,7 @@ static_assert(kSmem <= 232448, "shared memory");
 // for e4m3 pages the producers 19-22.
 constexpr int kSendWarp = 8, kOutWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18, kProdWarp = 19;
 constexpr int kBarMax = 1;                   // + q, named: the row maxima (sums) of warps q and q + 4 are in sM
+constexpr int kBarProd = 5;                  // the producers
 constexpr int kProducerWarps = 4;
 __host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kProdWarp + (e4m3 ? kProducerWarps : 0)); }
 // 19 warps: 5 per sub-partition, 96 registers a thread; 23 warps: 6, 80.
@@ -113,10 +112,9 @@ constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp
 constexpr int kPieceCost = 3;                // start-up of a piece (5-6k cycles) in tiles
 constexpr float kCutCost = 4.f;               // of a share (see there)
 
-// Ring stages that a piece's queries take before its first tile (the e4m3 kernel,
-// whose ring its producers fill, loads them without it).  Tile u (counted over
-// all pieces) of piece k has ring position u + (k + 1) q_slots.
-__host__ __device__ constexpr int q_slots(bool e4m3) { return e4m3 ? 0 : 2; }
+// Ring stages that a piece's queries take before its first tile.  Tile u (counted
+// over all pieces) of piece k has ring position u + (k + 1) QS.
+constexpr int QS = 2;
 
 struct __align__(16) Rec {     // the block that starts in cluster c and ends in a later one
   int64_t end;        // where it ends in the run of costs
@@ -291,14 +289,6 @@ struct Iter {
   }
 };
 
-// A piece's queries on their way into L2, by one thread of each CTA.
-MLA_DEVINL void prefetch_q(const TcArgs& a, const Item& it, uint32_t rank) {
-  if (rank == 0)
-    tc::prefetch_l2(a.p.q_lat + it.qrow0 * kLatent, static_cast<uint32_t>(it.nvalid) * kLatent * 2);
-  else
-    tc::prefetch_l2(a.p.q_pe + it.qrow0 * kRope, static_cast<uint32_t>(it.nvalid) * kRope * 2);
-}
-
 // Keys [k, k + n) hold one that some row of the block sees.
 MLA_DEVINL bool any_visible(const TcArgs& a, const Item& it, int k, int n) {
   return k < it.kend && (k + n > it.wlo || k < a.p.n_sink);
@@ -326,8 +316,7 @@ MLA_DEVINL int32_t staged_row(const TcArgs& a, const Item& it, int32_t base, int
 struct Bars {
   uint64_t lat_full[4];             // tile in its stage
   uint64_t lat_empty[4];   // P V has read it (or the senders, queries)
-  uint64_t raw_full[kRawStages];    // e4m3: codes and scales of the tile in their stage
-  uint64_t raw_empty[kRawStages];   // all producer warps have read them
+  uint64_t raw_full[4];             // e4m3: its codes and scales
   uint64_t rope_full[kRopeStages];
   uint64_t rope_empty[kRopeStages];
   uint64_t s_full[2];               // partial scores in TMEM
@@ -388,16 +377,6 @@ MLA_DEVINL void tmem_ld16x2_16(uint32_t taddr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-
-// 32 TMEM lanes, 16 columns (lane = row).
-MLA_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 
 // Arrive on `bar` of both CTAs of the pair when every MMA issued so far has
@@ -468,34 +447,45 @@ MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
 }
 
 // ---------------------------------------------------------------------------
-// e4m3 producer: this CTA's 256 codes of a tile's 64 rows from their ring stage
-// into a tile stage, as fp16.  Step j of thread pt (of 128) takes 16 codes each at
-// 16 c0 + 128 h, h < 2, of key k0 + 16 j; all offsets are constants of the thread.
-// Eight consecutive lanes take half of the units of two adjacent keys, the one's
-// lower and the other's upper half: their loads and stores then lie in eight
-// different 16-byte columns of the banks (a key's eight units, 4 chunk-0 and 4
-// chunk-1 stores in the same columns, 240 us for 8 tokens at 98304 rows; so 233).
-// Four warps, a step at a time: with eight warps, or all of a thread's codes loaded
-// first, the larger hot code made the kernel 2-6% slower; the codes loaded into the
-// tile's own stage and converted in place, which leaves room for a fourth stage, 3%.
+// e4m3 producer: this CTA's 256 codes of a tile's 64 rows into fp16, in place: the
+// codes lie in the second half of the tile's stage.  Step j of thread pt (of 128)
+// takes 16 codes each at 16 c0 + 128 h, h < 2, of key k0 + 16 j; all offsets are
+// constants of the thread.  Steps 2 and 3 overwrite codes: those of steps 0 and 1,
+// and of 2 and 3.  Eight consecutive lanes take half of the units of two adjacent
+// keys, the one's lower and the other's upper half: their loads and stores then lie
+// in eight different 16-byte columns of the banks (one key's eight units, whose
+// stores meet in four, took 3% longer).  Four warps, a step at a time: eight warps, or
+// codes loaded a step ahead, make the hot code larger and the kernel 2-6% slower.
+// 8 tokens at 98304 rows: 225 us.
 // ---------------------------------------------------------------------------
 constexpr int kProdKeys = 4 * kProducerWarps;
+static_assert(kBK / kProdKeys == 4, "steps");
 
-MLA_DEVINL void produce(const uint8_t* raw, uint8_t* lat, int rank, int pt, int j) {
-  const int k0 = 2 * (pt >> 4) + ((pt >> 2) & 1), c0 = (pt & 3) | (((pt >> 2) ^ (pt >> 3)) & 1) << 2;
-  const int key = k0 + kProdKeys * j;
+MLA_DEVINL int prod_key(int pt) { return 2 * (pt >> 4) + ((pt >> 2) & 1); }
+MLA_DEVINL int prod_unit(int pt) { return (pt & 3) | (((pt >> 2) ^ (pt >> 3)) & 1) << 2; }
+
+struct Codes {
+  uint4 v[2];
+  uint2 d;                                     // the key's scale bytes of this CTA
+};
+MLA_DEVINL void load_codes(Codes& c, const uint8_t* lat, const uint8_t* scale, int rank, int pt, int j) {
+  const int key = prod_key(pt) + kProdKeys * j;
+  const uint8_t* src = lat + kRawOff + key * 256 + 16 * prod_unit(pt);
+  c.v[0] = *reinterpret_cast<const uint4*>(src);
+  c.v[1] = *reinterpret_cast<const uint4*>(src + 128);
+  c.d = *reinterpret_cast<const uint2*>(scale + key * 16 + 8 * rank);
+}
+MLA_DEVINL void store_f16(const Codes& c, uint8_t* lat, int pt, int j) {
+  const int k0 = prod_key(pt), c0 = prod_unit(pt);
   const uint32_t dst = (k0 >> 3) * kGroup + (c0 >> 2) * kChunk + unit128(k0 & 7, 2 * (c0 & 3));
-  const uint8_t* src = raw + key * 256 + 16 * c0;
-  const uint4 v[2] = {*reinterpret_cast<const uint4*>(src), *reinterpret_cast<const uint4*>(src + 128)};
-  const uint2 d = *reinterpret_cast<const uint2*>(raw + kRawCodes + key * 16 + 8 * rank);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t s = e4m3_scale_f16x2(__byte_perm(h ? d.y : d.x, 0u, 0x4440 + (c0 >> 1)));
+    const uint32_t s = e4m3_scale_f16x2(__byte_perm(h ? c.d.y : c.d.x, 0u, 0x4440 + (c0 >> 1)));
     uint4 lo, hi;
-    e4m3x4_to_f16x4(v[h].x, s, lo.x, lo.y);
-    e4m3x4_to_f16x4(v[h].y, s, lo.z, lo.w);
-    e4m3x4_to_f16x4(v[h].z, s, hi.x, hi.y);
-    e4m3x4_to_f16x4(v[h].w, s, hi.z, hi.w);
+    e4m3x4_to_f16x4(c.v[h].x, s, lo.x, lo.y);
+    e4m3x4_to_f16x4(c.v[h].y, s, lo.z, lo.w);
+    e4m3x4_to_f16x4(c.v[h].z, s, hi.x, hi.y);
+    e4m3x4_to_f16x4(c.v[h].w, s, hi.z, hi.w);
     uint8_t* q = lat + 2 * kChunk * h + kProdKeys / 8 * kGroup * j;
     *reinterpret_cast<uint4*>(q + dst) = lo;
     *reinterpret_cast<uint4*>(q + (dst ^ 16u)) = hi;
@@ -508,12 +498,13 @@ MLA_DEVINL void produce(const uint8_t* raw, uint8_t* lat, int rank, int pt, int 
 template <bool kE4m3>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
-                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ TcArgs a) {
+                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_scale,
+                      const __grid_constant__ TcArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQr = sm;
   uint8_t* sLat = sm + kOffLat;
-  uint8_t* sRaw = sm + kOffRaw;
+  uint8_t* sScale = sm + kOffScale;
   uint8_t* sRope = sm + kOffRope;
   uint8_t* sP = sm + kOffP;
   uint8_t* sX = sm + kOffX;
@@ -528,7 +519,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = static_cast<int>(blockIdx.x >> 1), G = static_cast<int>(gridDim.x >> 1);
   constexpr int NT = threads(kE4m3);
-  constexpr int QS = q_slots(kE4m3), LS = lat_stages(kE4m3);
 
   // ---- setup ---------------------------------------------------------------
   if (warp == kPvWarp) {
@@ -536,9 +526,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     auto init = [&](int l, uint64_t* bars, int n, uint32_t count) {
       if (lane >= l && lane < l + n) mbar_init(bars + lane - l, count);
     };
-    static_assert(kRawStages == 2 && kRopeStages == 2, "lanes below");
-    init(0, B.raw_full, 2, 1);
-    init(2, B.raw_empty, 2, kProducerWarps);
+    static_assert(LS == 4 && kRopeStages == 2, "lanes below");
+    init(0, B.raw_full, 4, 1);
     init(0, B.lat_full, 4, kE4m3 ? kProducerWarps : 1);
     init(4, B.lat_empty, 4, 1);
     init(8, B.rope_full, 2, 1);
@@ -574,6 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     tc::prefetch_tmap(&tm_lat);
     tc::prefetch_tmap(&tm_rope);
     tc::prefetch_tmap(&tm_q);
+    if (kE4m3) tc::prefetch_tmap(&tm_scale);
   }
   // The peer's barriers are ready once its threads have come here: waited for below.
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -659,7 +649,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       B.st.g = g;
       B.st.b = w.b;
       if (piece) B.st.it = it;
-      if (kE4m3) prefetch_q(a, it, rank);
     }
   }
   tc::fence_before_sync();
@@ -857,63 +846,30 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const uint32_t tq = tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmQ;
         const uint4* qp = reinterpret_cast<const uint4*>(a.p.q_pe + (it.qrow0 + 32 * q4 + rr) * kRope) + 4 * rank + part;
         uint4 pe[4];
-        auto fetch_pe = [&] {
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            pe[m] = rr + 8 * m < nrows ? __ldg(qp + m * 8 * (kRope / 8)) : make_uint4(0, 0, 0, 0);
-        };
-        if constexpr (!kE4m3) {
-          fetch_pe();
-          // From the two ring stages (128 rows x 64 dims twice each), a row per
-          // lane.  Rows past the block's are zero.
+        for (int m = 0; m < 4; ++m)
+          pe[m] = rr + 8 * m < nrows ? __ldg(qp + m * 8 * (kRope / 8)) : make_uint4(0, 0, 0, 0);
+        // From the two ring stages (128 rows x 64 dims twice each), a row per
+        // lane.  Rows past the block's are zero.
 #pragma unroll 1
-          for (int q = 0; q < QS && ok; ++q) {
-            const int r0 = u + QS * k + q, ls = r0 % LS;
-            ok = wait_all(&B.lat_full[ls], (r0 / LS) & 1, a);
-            if (!ok) break;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              const uint8_t* src = sLat + ls * kLatStage + h * (kLatStage / 2);
-              uint32_t r[32];
-#pragma unroll
-              for (int w = 0; w < 8; ++w) {
-                const uint4 x = lane < nrows ? *reinterpret_cast<const uint4*>(src + unit128(32 * q4 + lane, w))
-                                             : make_uint4(0, 0, 0, 0);
-                r[4 * w] = x.x; r[4 * w + 1] = x.y; r[4 * w + 2] = x.z; r[4 * w + 3] = x.w;
-              }
-              tc::tmem_st32(tq + 64 * q + 32 * h, r);
-            }
-          }
+        for (int q = 0; q < QS && ok; ++q) {
+          const int r0 = u + QS * k + q, ls = r0 % LS;
+          ok = wait_all(kE4m3 ? &B.raw_full[ls] : &B.lat_full[ls], (r0 / LS) & 1, a);
           if (!ok) break;
-        } else {
-          // 32 dims (64 bytes) at a time: a load instruction reads 8 rows x 64
-          // contiguous bytes, and the warp's slice of the RoPE query tile turns
-          // them into a row per lane.
-          const uint4* src = reinterpret_cast<const uint4*>(a.p.q_lat + (it.qrow0 + 32 * q4 + rr) * kLatent + 256 * rank) + part;
-          uint4 v[4];
-          auto fetch = [&](int cc) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              v[m] = rr + 8 * m < nrows ? __ldg(src + 4 * cc + m * 8 * (kLatent / 8)) : make_uint4(0, 0, 0, 0);
-          };
-          fetch(0);
 #pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* src = sLat + ls * kLatStage + h * (kLatStage / 2);
+            uint32_t r[32];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) *reinterpret_cast<uint4*>(slice + unit64(rr + 8 * m, part)) = v[m];
-            __syncwarp();
-            if (cc < 7) fetch(cc + 1);
-            uint32_t r[16];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint4 x = *reinterpret_cast<const uint4*>(slice + unit64(lane, q));
-              r[4 * q] = x.x; r[4 * q + 1] = x.y; r[4 * q + 2] = x.z; r[4 * q + 3] = x.w;
+            for (int w = 0; w < 8; ++w) {
+              const uint4 x = lane < nrows ? *reinterpret_cast<const uint4*>(src + unit128(32 * q4 + lane, w))
+                                           : make_uint4(0, 0, 0, 0);
+              r[4 * w] = x.x; r[4 * w + 1] = x.y; r[4 * w + 2] = x.z; r[4 * w + 3] = x.w;
             }
-            tmem_st16(tq + 16 * cc, r);
-            __syncwarp();
+            tc::tmem_st32(tq + 64 * q + 32 * h, r);
           }
-          fetch_pe();
         }
+        if (!ok) break;
         tc::tmem_st_wait();
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -1154,16 +1110,16 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const int r = u + QS * k + q, ls = r % LS;
         if (r >= LS) ok = wait_all(&B.lat_empty[ls], ((r / LS) - 1) & 1, a);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
+        uint64_t* full = kE4m3 ? &B.raw_full[ls] : &B.lat_full[ls];
+        if (lane == 0) mbar_arrive_expect_tx(full, kLatStage);
         __syncwarp();
         if (lane == 0)
-          tc::tma_load_3d(sLat + ls * kLatStage, &tm_q, &B.lat_full[ls], 0, static_cast<int>(it.qrow0),
+          tc::tma_load_3d(sLat + ls * kLatStage, &tm_q, full, 0, static_cast<int>(it.qrow0),
                           4 * static_cast<int>(rank) + 2 * q);
       }
       if (!ok) break;
       ++k;
       const int32_t base = staged ? __ldg(a.stage_base + it.b) : 0;
-      if (kE4m3 && u > 0 && lane == 0) prefetch_q(a, it, rank);     // some tiles before the senders load it
       int row_n = row_at(0, id0);
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
@@ -1173,65 +1129,75 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         // tile's rows on their way into L2 (32 tokens at 4K-32K rows: 175 -> 157
         // us; for chunks, whose rows L2 holds, it costs 3-4%, and for e4m3 pages,
         // which the ring loads further ahead, it changes nothing).
-        if (!kE4m3 && it.once && !staged && ch == 0 && row_n < a.n_rows)
-          tc::prefetch_l2(a.p.c.pages + (static_cast<int64_t>(row_n) + (rank ? box / 2 : 0)) * kRowF16,
-                          static_cast<uint32_t>(box / 2 * kRowF16));
-        if (kE4m3) {
-          const int ws = u % kRawStages;
-          if (u >= kRawStages) ok = wait_all(&B.raw_empty[ws], ((u / kRawStages) - 1) & 1, a);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&B.raw_full[ws], kRawStage);
+        constexpr int kRowBytes = kE4m3 ? kRowE4m3 : kRowF16;
+        if (it.once && !staged && ch == 0 && row_n < a.n_rows)
+          tc::prefetch_l2(a.p.c.pages + (static_cast<int64_t>(row_n) + (rank ? box / 2 : 0)) * kRowBytes,
+                          static_cast<uint32_t>(box / 2 * kRowBytes));
+        auto load_rope = [&] {
+          if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
           __syncwarp();
-          uint8_t* dst = sRaw + ws * kRawStage;
-          if (mine && ch == 1)
-            tc::tma_load_3d(dst + j * box * 256, &tm_lat, &B.raw_full[ws], 128 * static_cast<int>(rank), row, 0);
-          else if (mine && ch == 2)
-            tc::tma_load_3d(dst + kRawCodes + j * box * 16, &tm_q, &B.raw_full[ws], kE4m3ScaleOff / 2, row, 0);
-        }
-        if (u >= kRopeStages) ok = wait_all(&B.rope_empty[rs], ((u / kRopeStages) - 1) & 1, a);
+          if (mine && ch == 0)
+            tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs], rope_x, row, 0);
+        };
+        // Codes go first: they are still to be converted, and the RoPE part's stage
+        // waits for a score product that comes late (8 tokens at 98304 rows 225 us,
+        // after it 246).
+        if (!kE4m3) load_rope();
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&B.rope_full[rs], kRopeChunk);
-        __syncwarp();
-        if (mine && ch == 0)
-          tc::tma_load_3d(sRope + rs * kRopeChunk + j * box * 64, &tm_rope, &B.rope_full[rs], rope_x, row, 0);
-        if (kE4m3) continue;
         const int r = u + QS * k, ls = r % LS;
         if (r >= LS) ok = wait_all(&B.lat_empty[ls], ((r / LS) - 1) & 1, a);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&B.lat_full[ls], kLatStage);
+        uint64_t* full = kE4m3 ? &B.raw_full[ls] : &B.lat_full[ls];
+        if (lane == 0) mbar_arrive_expect_tx(full, kE4m3 ? kRawBytes : kLatStage);
         __syncwarp();
         uint8_t* dst = sLat + ls * kLatStage;
         const int c0 = 4 * static_cast<int>(rank);
-        if (staged) {
+        if (kE4m3) {
+          if (mine && ch == 1)
+            tc::tma_load_3d(dst + kRawOff + j * box * 256, &tm_lat, full, 128 * static_cast<int>(rank), row, 0);
+          else if (mine && ch == 2)
+            tc::tma_load_3d(sScale + ls * kRawScale + j * box * 16, &tm_scale, full, kE4m3ScaleOff / 2, row, 0);
+        } else if (staged) {
           if (lane == 0)
-            tc::tma_load_4d(dst, &tm_lat, &B.lat_full[ls], 0, 0, c0, staged_row(a, it, base, it.key_tile(t)) / 8);
+            tc::tma_load_4d(dst, &tm_lat, full, 0, 0, c0, staged_row(a, it, base, it.key_tile(t)) / 8);
         } else if (mine && ch == 1) {
-          tc::tma_load_4d(dst + j * box / 8 * kGroup, &tm_lat, &B.lat_full[ls], 0, 0, c0, row / 8);
+          tc::tma_load_4d(dst + j * box / 8 * kGroup, &tm_lat, full, 0, 0, c0, row / 8);
         }
+        if (kE4m3) load_rope();
+        if (!ok) break;
       }
     }
   } else if constexpr (kE4m3) {
     // ============================ e4m3 producers ===============================
+    // (a warp whose wait gave up goes on with nothing but the named barriers)
     const int pt = static_cast<int>(threadIdx.x) - kProdWarp * 32;
-    int u = 0;
+    bool dead = false;
+    int r = 0;                         // ring position
 #pragma unroll 1
-    while (ok && items.next(a, it)) {
+    while (items.next(a, it)) {
 #pragma unroll 1
-      for (int t = 0; t < it.n_tiles; ++t, ++u) {
-        const int ls = u % LS, ws = u % kRawStages;
-        ok = wait_all(&B.raw_full[ws], (u / kRawStages) & 1, a);
-        if (!ok) break;
-        if (u >= LS) ok = wait_all(&B.lat_empty[ls], ((u / LS) - 1) & 1, a);
-        if (!ok) break;
+      for (int q = 0; q < QS; ++q, ++r) {      // the queries: a phase like the tiles'
+        if (!dead) dead = !wait_all(&B.raw_full[r % LS], (r / LS) & 1, a);
+        if (!dead && lane == 0) mbar_arrive(&B.lat_full[r % LS]);
+      }
 #pragma unroll 1
-        for (int j = 0; j < kBK / kProdKeys; ++j)
-          produce(sRaw + ws * kRawStage, sLat + ls * kLatStage, static_cast<int>(rank), pt, j);
+      for (int t = 0; t < it.n_tiles; ++t, ++r) {
+        const int ls = r % LS;
+        uint8_t* lat = sLat + ls * kLatStage;
+        if (!dead) dead = !wait_all(&B.raw_full[ls], (r / LS) & 1, a);
+#pragma unroll 1
+        for (int j = 0; j < kBK / kProdKeys; ++j) {
+          Codes c;
+          if (!dead) load_codes(c, lat, sScale + ls * kRawScale, static_cast<int>(rank), pt, j);
+          if (j >= 2) tc::named_bar_sync(kBarProd, 32 * kProducerWarps);
+          if (!dead) store_f16(c, lat, pt, j);
+        }
+        if (dead) continue;
         tc::fence_proxy_async();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&B.lat_full[ls]);
-          mbar_arrive(&B.raw_empty[ws]);
-        }
+        if (lane == 0) mbar_arrive(&B.lat_full[ls]);
       }
     }
   }
@@ -1438,7 +1404,8 @@ size_t partial_bytes() {
 }
 
 template <bool kE4m3>
-cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const TcArgs& a, cudaStream_t stream) {
+cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const CUtensorMap& ts,
+                        const TcArgs& a, cudaStream_t stream) {
   auto kern = paged_attn_kernel<kE4m3>;
   static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
   int dev = 0;
@@ -1451,7 +1418,7 @@ cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUte
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   const int G = clusters();
-  e = launch_dependent(kern, dim3(2 * G), dim3(threads(kE4m3)), kSmem, stream, tm, tr, tq, a);
+  e = launch_dependent(kern, dim3(2 * G), dim3(threads(kE4m3)), kSmem, stream, tm, tr, tq, ts, a);
   if (e != cudaSuccess) return e;
   // at most n_slots blocks, of at most T x H rows
   const int64_t rows = min(static_cast<int64_t>(kRows), static_cast<int64_t>(a.p.T) * a.p.H);
@@ -1484,26 +1451,20 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   // queries, as 64-dim chunks (dims, rows, chunks).  The RoPE parts are fp16 in
   // either row type.
   CUtensorMap tm, tr, tq;
-  memset(&tm, 0, sizeof(tm));
-  memset(&tq, 0, sizeof(tq));
   const uint32_t box = static_cast<uint32_t>(min(kBK, 1 << p.c.page_shift));
   const uint64_t n = static_cast<uint64_t>(a.n_rows);
   cudaError_t e;
   const uint64_t qrows = static_cast<uint64_t>(p.T) * static_cast<uint64_t>(p.H);
-  auto map_q = [&] {
-    return make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kLatent / 64, kLatent * 2, 128, 64, kRows, 2);
-  };
+  e = make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kLatent / 64, kLatent * 2, 128, 64, kRows, 2);
+  if (e != cudaSuccess) return e;
   if (!p.c.e4m3) {
-    e = map_q();
-    if (e != cudaSuccess) return e;
     e = make_tmap_row_groups(&tm, p.c.pages, n / 8, kRow / 64, kRowF16, box / 8, 4);
     if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
     if (e != cudaSuccess) return e;
-    return launch_pair<false>(tm, tr, tq, a, stream);
+    return launch_pair<false>(tm, tr, tq, tq, a, stream);
   }
-  // The e4m3 kernel's own, in elements of two bytes, as the rows are: a CTA's 256
-  // codes, and in the queries' place the 16 scales.
+  // In elements of two bytes, as the rows are: a CTA's 256 codes, and the 16 scales.
   CUtensorMap tcodes, tscales;
   e = make_tmap_3d(&tcodes, p.c.pages, false, kRowE4m3 / 2, n, 1, kRowE4m3, n * kRowE4m3, 128, box, 1, 0);
   if (e != cudaSuccess) return e;
@@ -1519,14 +1480,12 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_dependent(paged_stage_kernel, dim3(device_sm_count() * 4), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
-    e = map_q();
-    if (e != cudaSuccess) return e;
     a.take = kTakeStaged;
-    e = launch_pair<false>(tm, tr, tq, a, stream);
+    e = launch_pair<false>(tm, tr, tq, tq, a, stream);
     if (e != cudaSuccess) return e;
     a.take = kTakeUnstaged;
   }
-  return launch_pair<true>(tcodes, tr, tscales, a, stream);
+  return launch_pair<true>(tcodes, tr, tq, tscales, a, stream);
 }
 
 }  // namespace mla

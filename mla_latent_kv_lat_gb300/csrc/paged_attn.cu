@@ -135,10 +135,10 @@ struct __align__(16) Rec {     // the block that starts in cluster c and ends in
 // Staging of e4m3 latents as fp16 (rows of 512): up to kStageRows rows of the
 // sequences with at least kStageBlocks blocks, in batches of at most kStageSeqs.
 // Measured with and without, one sequence of 128 heads (a query is a block) at 33K
-// rows: 4 queries 70 and 62 us, 8 97 and 97, 12 122 and 134, 152 1066 and 1453; the
-// staging and a second launch cost ~10 us, so at 2000 rows 16 queries take 41 and 32
-// us, 64 69 and 67.
-constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 12;
+// rows: 8 queries 93 and 85 us, 12 120 and 119, 16 149 and 154, 152 1055 and 1315;
+// the staging and a second launch cost ~10 us, so at 2000 rows 16 queries take 36 and
+// 27 us, 64 66 and 60, 256 149 and 162.
+constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 16;
 
 // Which sequences a launch takes.
 enum Take : int32_t { kTakeAll, kTakeStaged, kTakeUnstaged };

@@ -239,9 +239,11 @@ def test_batches_from_few_blocks_to_many(B, H, top, e4m3):
     check(b, run(b))
 
 
-def test_e4m3_chunks_beyond_the_staging():
-    """Two chunks whose rows are staged and a third that no longer fits, on a few pages named many times."""
-    ps, H, lens, news = 64, 16, [70001, 50000, 30001], [100, 128, 100]
+@pytest.mark.parametrize("news", [[100, 128, 100], [160, 200, 160]], ids=str)
+def test_e4m3_chunks_beyond_the_staging(news):
+    """Chunks of too few blocks to be staged; two that are staged and a third that no longer fits.  On a few pages
+    named many times."""
+    ps, H, lens = 64, 16, [70001, 50000, 30001]
     rng = np.random.default_rng(8)
     raw = PO.pack_rows(bf16(rng.standard_normal((8 * ps, 512))), bf16(rng.standard_normal((8 * ps, 64))), True)
     pages = torch.from_numpy(raw).cuda().reshape(8, ps, 656)

@@ -495,7 +495,12 @@ MLA_DEVINL void store_f16(const Codes& c, uint8_t* lat, int pt, int j) {
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
-template <bool kE4m3>
+// kFewRows: blocks of fewer rows than 128, as single tokens of few heads are: warps
+// whose rows all lie behind a block's do no softmax, and their scores stay where they
+// are (32 tokens at 4K-32K rows, 16 heads: 136 us, without it 146; 64 heads 140 and
+// 148, 96 heads 146 and 151).  Its own instantiation, because the tests make full
+// blocks 2% slower; for e4m3 pages it gains nothing.
+template <bool kE4m3, bool kFewRows>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                       const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_scale,
@@ -666,7 +671,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   if (warp < kSendWarp) {
     // ================================ softmax ==================================
     // Four threads per owned row: warps q and q + 4, lanes l and l + 16, 16 keys
-    // of every tile each.  A wait that gave up makes the warp `dead`: it goes on
+    // of every tile each.  A warp whose 16 rows all lie behind the block's (kFewRows)
+    // leaves their P as it is: no output takes it.  A wait that gave up makes the warp `dead`: it goes on
     // through the tiles with nothing but the named barriers, on which its partner
     // waits without a limit.
     const int half = warp >> 2, q4 = warp & 3, hh = lane >> 4;
@@ -680,10 +686,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const uint32_t peer_lfull = tc::mapa(smem_u32(&B.l_full[0]), peer);
     const uint32_t peer_xempty = tc::mapa(smem_u32(&B.x_empty[q4]), peer);
     bool dead = false;
-    int u = 0, k = 0;
+    int u = 0, k = 0, xu = 0;          // tiles, pieces, tiles of pieces in which some row is this warp's
 #pragma unroll 1
     while (items.next(a, it)) {
       const bool rvalid = i < it.nvalid;
+      const bool mine = !kFewRows || 32 * q4 + 16 * static_cast<int>(rank) < it.nvalid;
       // keys [wl, lim] and the sinks are visible to this row
       const int lim = rvalid ? it.pos0 + static_cast<int>((it.row0 + i) / static_cast<uint32_t>(a.p.H)) : it.kend - 1;
       const int wl = a.p.window > 0 ? max(0, lim - a.p.window + 1) : 0;
@@ -691,15 +698,16 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int sb = u & 1;
-        const uint32_t ph = (u >> 1) & 1;
+        const uint32_t ph = (u >> 1) & 1, xph = (kFewRows ? xu : u) & 1;
         const int base = it.key_tile(t) * kBK, k0 = base + col;
         uint64_t s[8];                           // the scores, in pairs
         float mrow = -INFINITY;
         // Barriers are tested ahead of their use, so that their latencies
         // overlap; one that is not complete yet is waited for there.
-        const bool s_test = mbar_test(&B.s_full[sb], ph), x_test = tc::mbar_test_cluster(&B.x_full[q4], u & 1);
+        const bool s_test = mbar_test(&B.s_full[sb], ph), x_test = tc::mbar_test_cluster(&B.x_full[q4], xph);
         if (!dead && !__all_sync(0xffffffffu, s_test)) dead = !wait_all(&B.s_full[sb], ph, a);
-        if (!dead) {
+        if (!dead && !mine && lane == 0) mbar_arrive(&B.s_free[sb]);
+        if (!dead && mine) {
           tc::fence_after_sync();
           uint32_t r[16];
           tmem_ld16x2_16(tmem + lanes + kTmS + sb * 64 + 32 * half, r);
@@ -707,11 +715,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&B.s_free[sb]);
-          if (!__all_sync(0xffffffffu, x_test)) dead = !wait_cl(&B.x_full[q4], u & 1, a);
+          if (!__all_sync(0xffffffffu, x_test)) dead = !wait_cl(&B.x_full[q4], xph, a);
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[e] = pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
         }
-        if (!dead) {
+        if (!dead && mine) {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const ulonglong2 x =
@@ -742,7 +750,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         }
         const bool p_test = u < 2 || tc::mbar_test_cluster(&B.pv_done[sb], ((u >> 1) - 1) & 1);
         tc::named_bar_sync(kBarMax + q4, 64);
-        if (!dead) {
+        float alpha = 1.f;
+        uint32_t pk[8];
+        if (!dead && mine) {
+          ++xu;
           // Every value that the two warps read from the exchange buffer went into
           // their maxima, so the peer may refill it (and a relaxed arrival suffices).
           if (half == 0 && lane == 0) {
@@ -753,14 +764,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           // Lazy rescale: only when the row maximum grew by more than the
           // threshold.  A row may see none of the tile's keys (or none so far):
           // its maximum stays -inf, its P zero.
-          float alpha = 1.f;
           if (mrow > m_run + kRescaleThreshold) {
             alpha = tc::exp2_approx(m_run - mrow);
             m_run = mrow;
             l_h *= alpha;
           }
           const float mb = m_run == -INFINITY ? 0.f : m_run;
-          uint32_t pk[8];
           const uint64_t cc = pack2(c2, c2), mm = pack2(-mb, -mb);
           uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
@@ -772,14 +781,18 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           }
           const float2 lsum = unpack2(add2(ls[0], ls[1]));
           l_h += lsum.x + lsum.y;
+        }
+        if (!dead) {
           // The P buffer and the factors of tile u - 2 have been used in both CTAs.
           if (!__all_sync(0xffffffffu, p_test)) dead = !wait_cl(&B.pv_done[sb], ((u >> 1) - 1) & 1, a);
           if (!dead) {
             uint8_t* pt = sP + sb * kPBytes + half * (kPBytes / 2);
+            if (mine) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
-              *reinterpret_cast<uint4*>(pt + unit64(i, 2 * hh + g)) =
-                  make_uint4(pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
+              for (int g = 0; g < 2; ++g)
+                *reinterpret_cast<uint4*>(pt + unit64(i, 2 * hh + g)) =
+                    make_uint4(pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
+            }
             if (half == 0 && hh == 0) {
               const float f = t == 0 ? 1.f : alpha;      // the piece's first P V overwrites O
               st_async_b32(peer_alpha + (sb * kRows + i) * 4, __float_as_uint(f), peer_pfull + sb * 8);
@@ -835,7 +848,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const uint32_t peer_x = tc::mapa(smem_u32(sX), peer) + q4 * (kXBytes / 4);
     const uint32_t peer_xfull = tc::mapa(smem_u32(&B.x_full[q4]), peer);
     uint32_t qrun = 0;
-    int u = 0, k = 0;
+    int u = 0, k = 0, xu = 0;          // tiles, pieces, tiles with something to send
 #pragma unroll 1
     while (ok && items.next(a, it)) {
       // Q of the piece.  The last score product of the previous piece is
@@ -882,12 +895,18 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.q_ready);
       }
+      const bool theirs = !kFewRows || 32 * q4 + 16 * static_cast<int>(peer) < it.nvalid;
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int sb = u & 1;
-        const bool x_test = u < 1 || tc::mbar_test_cluster(&B.x_empty[q4], (u - 1) & 1);
+        const int xc = kFewRows ? xu : u;
+        const bool x_test = xc < 1 || tc::mbar_test_cluster(&B.x_empty[q4], (xc - 1) & 1);
         ok = wait_all(&B.s_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
+        if (!theirs) {
+          if (lane == 0) mbar_arrive(&B.s_free[sb]);
+          continue;
+        }
         tc::fence_after_sync();
         uint32_t r[32];
         tc::tmem_ld16x2<32>(tmem + lanes + kTmS + sb * 64, r);
@@ -896,7 +915,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.s_free[sb]);
         // (read there means that the copy below has left its source, too)
-        if (!__all_sync(0xffffffffu, x_test)) ok = wait_cl(&B.x_empty[q4], (u - 1) & 1, a);
+        if (!__all_sync(0xffffffffu, x_test)) ok = wait_cl(&B.x_empty[q4], (xc - 1) & 1, a);
         if (!ok) break;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
@@ -905,6 +924,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0) bulk_to_peer(peer_x, smem_u32(xs), kXBytes / 4, peer_xfull);
+        ++xu;
       }
       ++k;
     }
@@ -949,7 +969,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const float l = sL[(k & 3) * kRows + i];
         const float inv = l > 0.f ? 1.f / l : 0.f;     // a row that sees no key of this piece
         const int nrows = it.nvalid - 32 * q4;
-        if (it.whole()) {
+        if (kFewRows && nrows <= 0) {
+          // none of the block's rows
+        } else if (it.whole()) {
           uint8_t* dst = reinterpret_cast<uint8_t*>(a.p.o_lat + (it.qrow0 + 32 * q4) * kLatent + 256 * rank);
 #pragma unroll 1
           for (int cc = 0; cc < 8; ++cc) {
@@ -1403,10 +1425,10 @@ size_t partial_bytes() {
   return rows * kLatent * sizeof(float) + rows * 2 * sizeof(float) + clusters() * sizeof(Rec);
 }
 
-template <bool kE4m3>
+template <bool kE4m3, bool kFewRows>
 cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const CUtensorMap& ts,
                         const TcArgs& a, cudaStream_t stream) {
-  auto kern = paged_attn_kernel<kE4m3>;
+  auto kern = paged_attn_kernel<kE4m3, kFewRows>;
   static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1462,7 +1484,9 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
     if (e != cudaSuccess) return e;
-    return launch_pair<false>(tm, tr, tq, tq, a, stream);
+    // a block of single tokens has H rows
+    return p.T <= p.B && p.H <= kRows - 16 ? launch_pair<false, true>(tm, tr, tq, tq, a, stream)
+                                   : launch_pair<false, false>(tm, tr, tq, tq, a, stream);
   }
   // In elements of two bytes, as the rows are: a CTA's 256 codes, and the 16 scales.
   CUtensorMap tcodes, tscales;
@@ -1481,11 +1505,11 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     e = launch_dependent(paged_stage_kernel, dim3(device_sm_count() * 4), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
     a.take = kTakeStaged;
-    e = launch_pair<false>(tm, tr, tq, tq, a, stream);
+    e = launch_pair<false, false>(tm, tr, tq, tq, a, stream);
     if (e != cudaSuccess) return e;
     a.take = kTakeUnstaged;
   }
-  return launch_pair<true>(tcodes, tr, tq, tscales, a, stream);
+  return launch_pair<true, false>(tcodes, tr, tq, tscales, a, stream);
 }
 
 }  // namespace mla

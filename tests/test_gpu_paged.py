@@ -239,6 +239,18 @@ def test_batches_from_few_blocks_to_many(B, H, top, e4m3):
     check(b, run(b))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H,news", [(16, [1, 8, 0, 0, 0, 0, 0, 0, 0, 1]), (48, [4, 0, 1, 0, 0, 0]), (112, [1, 2, 1, 0]),
+                                    (80, [1] * 100), (32, [0, 3, 0, 1])], ids=str)
+def test_blocks_of_few_rows_beside_full_ones(H, news, e4m3):
+    """No more tokens than sequences, few heads: warps without rows, blocks of one and of all rows in turn."""
+    lens = [50 + 97 * (i * 7 % 10) for i in range(len(news))]
+    b = Batch(23, e4m3, H, 64, news, lens, pad=1)
+    b.T = min(b.T, len(news))                            # at most a token per sequence in the token array
+    b.q_lat, b.q_pe = b.q_lat[:b.T], b.q_pe[:b.T]
+    check(b, run(b))
+
+
 @pytest.mark.parametrize("news", [[100, 128, 100], [160, 200, 160]], ids=str)
 def test_e4m3_chunks_beyond_the_staging(news):
     """Chunks of too few blocks to be staged; two that are staged and a third that no longer fits.  On a few pages

@@ -31,7 +31,7 @@
 //     either.  Eight warps share a tile's softmax (16 keys of a row per thread);
 //     two sets of four that take the tiles in turn were 1-2% slower, and so were
 //     16 warps.  512 queries of 128 heads at 33K rows: 3.57 ms, 1320 TFLOP/s, 69%
-//     of the measured rate; 32 tokens at 4K to 32K rows: 157 us, 4.4 TB/s.
+//     of the measured rate; 32 tokens at 4K to 32K rows: 155 us, 4.5 TB/s.
 //   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
 //   * A piece's queries come through the ring of cache tiles too, as two stages
 //     before its first tile, so that they are there when the piece before has
@@ -48,7 +48,8 @@
 // blocks form one run, which the clusters share evenly.  A cluster's piece that
 // is a whole block writes o_lat; a block cut by a cluster boundary leaves fp32
 // partials (at most two per cluster) that paged_combine_kernel merges.
-// Every wait on a barrier is bounded.
+// Every wait on an mbarrier is bounded; a warp that gave one up still comes to the
+// named barriers.
 #include <string.h>
 
 #include <atomic>
@@ -69,7 +70,7 @@ constexpr int kOwn = kRows / 2;              // rows whose softmax a CTA compute
 constexpr int kChunk = 8 * 128;              // 1 KB: 8 keys x 64 fp16
 constexpr int kGroup = 4 * kChunk;           // 4 KB: 8 keys x this CTA's 256 latent dims
 constexpr int kLatStage = kBK / 8 * kGroup;  // 32 KB
-constexpr int LS = 4;                        // tile stages
+constexpr int kLatStages = 4;                // tile stages
 // e4m3: a tile's codes (64 keys x 256, this CTA's half) arrive in the second half of
 // its stage, their rows' 16 scale bytes beside it.
 constexpr int kRawOff = kLatStage / 2, kRawScale = kBK * 16, kRawBytes = kBK * 256 + kRawScale;
@@ -81,12 +82,12 @@ constexpr int kPBytes = kRows * 128;         // 16 KB: two halves of 128 rows x 
 constexpr int kXBytes = kOwn * kBK * 4;      // 16 KB: 64 rows x 64 keys fp32
 constexpr int kPTx = kOwn * kBK * 2 + kOwn * 4;     // bytes a CTA gets per tile: the other's P rows and factors
 constexpr int kOffLat = kQRopeBytes;
-constexpr int kOffScale = kOffLat + LS * kLatStage;  // (e4m3)
-constexpr int kOffRope = kOffScale + LS * kRawScale;
+constexpr int kOffScale = kOffLat + kLatStages * kLatStage;  // (e4m3)
+constexpr int kOffRope = kOffScale + kLatStages * kRawScale;
 constexpr int kOffP = kOffRope + kRopeStages * kRopeChunk;
 constexpr int kOffX = kOffP + 2 * kPBytes;
-constexpr int kOffXs = kOffX + kXBytes;               // what goes to the other CTA
-constexpr int kOffStg = kOffXs + kXBytes;         // epilogue staging, 2 KB per warp
+constexpr int kOffXs = kOffX + kXBytes;              // what goes to the other CTA
+constexpr int kOffStg = kOffXs + kXBytes;            // epilogue staging, 2 KB per warp
 constexpr int kOffAlpha = kOffStg + 4 * 2048;        // [2][128] output factors
 constexpr int kOffL = kOffAlpha + 2 * kRows * 4;     // [4][128] row sums
 constexpr int kOffM = kOffL + 4 * kRows * 4;         // [2][2][64] row maxima of the key halves, by tile parity
@@ -110,11 +111,11 @@ constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, t
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
 
 constexpr int kPieceCost = 3;                // start-up of a piece (5-6k cycles) in tiles
-constexpr float kCutCost = 4.f;               // of a share (see there)
+constexpr float kCutCost = 4.f;              // of a share (see there)
 
 // Ring stages that a piece's queries take before its first tile.  Tile u (counted
-// over all pieces) of piece k has ring position u + (k + 1) QS.
-constexpr int QS = 2;
+// over all pieces) of piece k has ring position u + (k + 1) kQSlots.
+constexpr int kQSlots = 2;
 
 struct __align__(16) Rec {     // the block that starts in cluster c and ends in a later one
   int64_t end;        // where it ends in the run of costs
@@ -315,8 +316,8 @@ MLA_DEVINL int32_t staged_row(const TcArgs& a, const Item& it, int32_t base, int
 // Barriers (u counts this cluster's tiles, k its pieces).
 struct Bars {
   uint64_t lat_full[4];             // tile in its stage
-  uint64_t lat_empty[4];   // P V has read it (or the senders, queries)
-  uint64_t raw_full[4];             // e4m3: its codes and scales
+  uint64_t lat_empty[4];            // P V has read it (or the senders, queries)
+  uint64_t raw_full[4];             // e4m3: its codes and scales (or queries)
   uint64_t rope_full[kRopeStages];
   uint64_t rope_empty[kRopeStages];
   uint64_t s_full[2];               // partial scores in TMEM
@@ -531,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     auto init = [&](int l, uint64_t* bars, int n, uint32_t count) {
       if (lane >= l && lane < l + n) mbar_init(bars + lane - l, count);
     };
-    static_assert(LS == 4 && kRopeStages == 2, "lanes below");
+    static_assert(kLatStages == 4 && kRopeStages == 2, "lanes below");
     init(0, B.raw_full, 4, 1);
     init(0, B.lat_full, 4, kE4m3 ? kProducerWarps : 1);
     init(4, B.lat_empty, 4, 1);
@@ -605,9 +606,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const long long total = warp_sum_wide(part), before = warp_sum_wide(lane < warp ? part : 0);
     const long long S0 = before + incl - sum;
     // Cluster x of G takes [total x / G, total (x + 1) / G).  Short work takes fewer
-    // clusters, with an equal share each: a shorter piece saves
-    // its tiles' time, another piece of the block costs the merge.  The sum is least
-    // near share = sqrt(cost of a block / kCutCost); blocks of up to two tiles are
+    // clusters, with an equal share each: a shorter piece saves its tiles' time, another
+    // piece of the block costs the merge.  The sum is least near share = sqrt(cost of a block / kCutCost); blocks of up to two tiles are
     // not cut.  (Measured when a call took 2 us longer than now: one token at 257 rows,
     // 16 heads, shares of 1, 2, 3 14.2, 14.9, 17.0 us; 128 heads at 4000 rows 27.6,
     // 21.8, 21.0, at 16000 shares of 3.3 and 8 33.6 and 28.5.)
@@ -615,7 +615,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     uint32_t share = 0;
     if (total < (1 << 24)) {
       const uint32_t units = static_cast<uint32_t>(total);
-      const float blocks = fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H * (1.f / kRows));   // about
+      const float blocks =                                        // about
+          fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H * (1.f / kRows));
       share = kPieceCost + 2;
       if (units > blocks * share) {
         const float x = __fdividef(static_cast<float>(units), blocks * kCutCost);
@@ -801,7 +802,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             // A tile with keys that no row of the block sees: their values must
             // not enter P V (0 x NaN).  The score product has read the tile.
             if (base + kBK > it.kend || (base < it.wlo && base + kBK > a.p.n_sink)) {
-              uint8_t* stage = sLat + ((u + QS * (k + 1)) % LS) * kLatStage;
+              uint8_t* stage = sLat + ((u + kQSlots * (k + 1)) % kLatStages) * kLatStage;
               for (int q = threadIdx.x; q < kBK * 32; q += 256)
                 if (!key_visible(a, it, base + (q >> 5)))
                   *reinterpret_cast<uint4*>(stage + (q >> 8) * kGroup + ((q >> 3) & 3) * kChunk + ((q >> 5) & 7) * 128 +
@@ -865,9 +866,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         // From the two ring stages (128 rows x 64 dims twice each), a row per
         // lane.  Rows past the block's are zero.
 #pragma unroll 1
-        for (int q = 0; q < QS && ok; ++q) {
-          const int r0 = u + QS * k + q, ls = r0 % LS;
-          ok = wait_all(kE4m3 ? &B.raw_full[ls] : &B.lat_full[ls], (r0 / LS) & 1, a);
+        for (int q = 0; q < kQSlots && ok; ++q) {
+          const int r0 = u + kQSlots * k + q, ls = r0 % kLatStages;
+          ok = wait_all(kE4m3 ? &B.raw_full[ls] : &B.lat_full[ls], (r0 / kLatStages) & 1, a);
           if (!ok) break;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -1025,16 +1026,17 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       if (it.t_lo == 0 && it.open) rec = {items.S, items.st->total, it.qrow0, it.nvalid, items.st->share};
       ok = wait_all(&B.q_ready, k & 1, a);
       tc::fence_after_sync();
-      if (ok && lane < QS) mbar_arrive(&B.lat_empty[(u + QS * k + lane) % LS]);   // the queries have left the ring
+      // the queries have left the ring
+      if (ok && lane < kQSlots) mbar_arrive(&B.lat_empty[(u + kQSlots * k + lane) % kLatStages]);
       ++k;
 #pragma unroll 1
       for (int t = 0; ok && t < it.n_tiles; ++t, ++u) {
-        const int r = u + QS * k, ls = r % LS, rs = u % kRopeStages, sb = u & 1;
+        const int r = u + kQSlots * k, ls = r % kLatStages, rs = u % kRopeStages, sb = u & 1;
         // The last to complete is the tile, as a rule: the others are tested
         // while it is awaited.
         const bool r_test = mbar_test(&B.rope_full[rs], (u / kRopeStages) & 1);
         const bool s_test = u < 2 || mbar_test(&B.s_free[sb], ((u >> 1) - 1) & 1);
-        ok = wait_all(&B.lat_full[ls], (r / LS) & 1, a);
+        ok = wait_all(&B.lat_full[ls], (r / kLatStages) & 1, a);
         if (!__all_sync(0xffffffffu, r_test)) ok = ok && wait_all(&B.rope_full[rs], (u / kRopeStages) & 1, a);
         if (!__all_sync(0xffffffffu, s_test)) ok = ok && wait_all(&B.s_free[sb], ((u >> 1) - 1) & 1, a);
         if (!ok) break;
@@ -1071,7 +1073,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     while (ok && items.next(a, it)) {
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
-        const int ls = (u + QS * (k + 1)) % LS, sb = u & 1;
+        const int ls = (u + kQSlots * (k + 1)) % kLatStages, sb = u & 1;
         ok = wait_cl(&B.p_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
         if (t == 0) {
@@ -1128,9 +1130,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     while (ok && items.next(a, it)) {
       const int32_t id0 = entry(0);            // (on its way while the queries are asked for)
 #pragma unroll 1
-      for (int q = 0; q < QS; ++q) {           // the queries: 128 rows x 64 dims twice a stage
-        const int r = u + QS * k + q, ls = r % LS;
-        if (r >= LS) ok = wait_all(&B.lat_empty[ls], ((r / LS) - 1) & 1, a);
+      for (int q = 0; q < kQSlots; ++q) {           // the queries: 128 rows x 64 dims twice a stage
+        const int r = u + kQSlots * k + q, ls = r % kLatStages;
+        if (r >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((r / kLatStages) - 1) & 1, a);
         if (!ok) break;
         uint64_t* full = kE4m3 ? &B.raw_full[ls] : &B.lat_full[ls];
         if (lane == 0) mbar_arrive_expect_tx(full, kLatStage);
@@ -1168,8 +1170,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         // after it 246).
         if (!kE4m3) load_rope();
         if (!ok) break;
-        const int r = u + QS * k, ls = r % LS;
-        if (r >= LS) ok = wait_all(&B.lat_empty[ls], ((r / LS) - 1) & 1, a);
+        const int r = u + kQSlots * k, ls = r % kLatStages;
+        if (r >= kLatStages) ok = wait_all(&B.lat_empty[ls], ((r / kLatStages) - 1) & 1, a);
         if (!ok) break;
         uint64_t* full = kE4m3 ? &B.raw_full[ls] : &B.lat_full[ls];
         if (lane == 0) mbar_arrive_expect_tx(full, kE4m3 ? kRawBytes : kLatStage);
@@ -1200,15 +1202,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll 1
     while (items.next(a, it)) {
 #pragma unroll 1
-      for (int q = 0; q < QS; ++q, ++r) {      // the queries: a phase like the tiles'
-        if (!dead) dead = !wait_all(&B.raw_full[r % LS], (r / LS) & 1, a);
-        if (!dead && lane == 0) mbar_arrive(&B.lat_full[r % LS]);
+      for (int q = 0; q < kQSlots; ++q, ++r) {      // the queries: a phase like the tiles'
+        if (!dead) dead = !wait_all(&B.raw_full[r % kLatStages], (r / kLatStages) & 1, a);
+        if (!dead && lane == 0) mbar_arrive(&B.lat_full[r % kLatStages]);
       }
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++r) {
-        const int ls = r % LS;
+        const int ls = r % kLatStages;
         uint8_t* lat = sLat + ls * kLatStage;
-        if (!dead) dead = !wait_all(&B.raw_full[ls], (r / LS) & 1, a);
+        if (!dead) dead = !wait_all(&B.raw_full[ls], (r / kLatStages) & 1, a);
 #pragma unroll 1
         for (int j = 0; j < kBK / kProdKeys; ++j) {
           Codes c;
@@ -1241,8 +1243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 // not start 2432 blocks for a few that have work, and eight partials are under way
 // with the statistics, in twice the registers.  (With and without: one token at 257
 // rows, 16 heads, 12.6 and 13.0 us, 128 heads at 100 rows 12.0 and 14.1, 8 tokens at
-// 1000 rows 18.8 and 19.5; but 16 tokens 22.0 and 21.8, 32 tokens 31.7 and 29.4.)  Launched as a programmatic dependent of the
-// attention.
+// 1000 rows 18.8 and 19.5; but 16 tokens 22.0 and 21.8, 32 tokens 31.7 and 29.4.)
+// Launched as a programmatic dependent of the attention.
 // ---------------------------------------------------------------------------
 constexpr int kCombRows = 4, kMaxClusters = 128;
 

@@ -316,7 +316,7 @@ MLA_DEVINL int32_t staged_row(const TcArgs& a, const Item& it, int32_t base, int
 // Barriers (u counts this cluster's tiles, k its pieces).
 struct Bars {
   uint64_t lat_full[4];             // tile in its stage
-  uint64_t lat_empty[4];            // P V has read it (or the senders, queries)
+  uint64_t lat_empty[4];            // P V has read it (or the senders, queries; e4m3: and the producers saw them)
   uint64_t raw_full[4];             // e4m3: its codes and scales (or queries)
   uint64_t rope_full[kRopeStages];
   uint64_t rope_empty[kRopeStages];
@@ -1025,6 +1025,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     while (ok && items.next(a, it)) {
       if (it.t_lo == 0 && it.open) rec = {items.S, items.st->total, it.qrow0, it.nvalid, items.st->share};
       ok = wait_all(&B.q_ready, k & 1, a);
+      // e4m3: the producers, too, must have seen the queries' loads.  One that looked only
+      // after the next load into the stage had landed would wait for a parity that has
+      // come and gone.
+      if constexpr (kE4m3) {
+        for (int r = u + kQSlots * k; ok && r < u + kQSlots * (k + 1); ++r)
+          ok = wait_all(&B.lat_full[r % kLatStages], (r / kLatStages) & 1, a);
+      }
       tc::fence_after_sync();
       // the queries have left the ring
       if (ok && lane < kQSlots) mbar_arrive(&B.lat_empty[(u + kQSlots * k + lane) % kLatStages]);

@@ -251,6 +251,16 @@ def test_blocks_of_few_rows_beside_full_ones(H, news, e4m3):
     check(b, run(b))
 
 
+@pytest.mark.parametrize("top", [64, 300])
+def test_many_short_blocks_in_the_e4m3_ring(top):
+    """Several pieces a cluster, of one tile each or of one to five: their queries and tiles follow one another
+    through the ring's stages (test_paged_ring.py has the order in which stages are released)."""
+    rng = np.random.default_rng(top)
+    lens = [int(x) for x in rng.integers(1, top + 1, 500)]
+    b = Batch(24, True, 128, 16, [1] * len(lens), lens)
+    check(b, run(b))
+
+
 @pytest.mark.parametrize("news", [[100, 128, 100], [160, 200, 160]], ids=str)
 def test_e4m3_chunks_beyond_the_staging(news):
     """Chunks of too few blocks to be staged; two that are staged and a third that no longer fits.  On a few pages

@@ -904,11 +904,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const bool x_test = xc < 1 || tc::mbar_test_cluster(&B.x_empty[q4], (xc - 1) & 1);
         ok = wait_all(&B.s_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
+        tc::fence_after_sync();        // also before the next piece's queries, where nothing is read here
         if (!theirs) {
           if (lane == 0) mbar_arrive(&B.s_free[sb]);
           continue;
         }
-        tc::fence_after_sync();
         uint32_t r[32];
         tc::tmem_ld16x2<32>(tmem + lanes + kTmS + sb * 64, r);
         tc::tmem_ld_wait();

@@ -251,6 +251,15 @@ def test_blocks_of_few_rows_beside_full_ones(H, news, e4m3):
     check(b, run(b))
 
 
+@pytest.mark.parametrize("H", [16, 48, 112])
+def test_queries_of_few_rows_follow_one_another(H):
+    """Several pieces a cluster, single tokens of few heads: warps that read no scores write the next queries."""
+    rng = np.random.default_rng(H)
+    lens = [int(x) for x in rng.integers(1, 200, 500)]
+    b = Batch(25, False, H, 16, [1] * len(lens), lens)
+    check(b, run(b))
+
+
 @pytest.mark.parametrize("top", [64, 300])
 def test_many_short_blocks_in_the_e4m3_ring(top):
     """Several pieces a cluster, of one tile each or of one to five: their queries and tiles follow one another

@@ -123,13 +123,16 @@ struct __align__(16) Rec {     // the block that starts in cluster c and ends in
   int64_t qrow0;      // its first (token, head) row
   int32_t nvalid;     // its rows (0: no such block)
   int32_t share;      // of every cluster; 0: all have total / G
-  // Clusters whose range starts before `end`.
+  // Clusters whose range starts before `end`.  No more than there are: with a cu that
+  // decreases, the cluster's walk and the total may disagree on the blocks, and `end`
+  // lie behind the total.
   MLA_DEVINL int clusters(int G) const {
-    if (share > 0) return static_cast<int>((static_cast<uint32_t>(end) + share - 1) / share);
-    if (total < (1 << 24))
-      return static_cast<int>((static_cast<uint32_t>(end) * G + static_cast<uint32_t>(total) - 1) /
-                              static_cast<uint32_t>(total));
-    return static_cast<int>((end * G + total - 1) / total);
+    int64_t n;
+    if (share > 0) n = (static_cast<uint32_t>(end) + share - 1) / share;
+    else if (total < (1 << 24))
+      n = (static_cast<uint32_t>(end) * G + static_cast<uint32_t>(total) - 1) / static_cast<uint32_t>(total);
+    else n = (end * G + total - 1) / total;
+    return static_cast<int>(min(n, static_cast<int64_t>(G)));
   }
 };
 

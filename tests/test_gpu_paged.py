@@ -393,6 +393,27 @@ def test_a_decreasing_cu_is_reported_and_stays_in_bounds():
     assert mla.mla_get_device_error() == 0
 
 
+@pytest.mark.parametrize("cu,lens", [
+    ([0, 23, 24, 21, 54, 13, 21, 60], [76, 163070, 119811, 60, 8312, 1783, 84]),
+    ([0, 13, 17, 13, 20, 8, 17, 9, 12, 11, 20], [682, 172736, 1706, 199, 814, 2440, 2384, 1866, 52, 40]),
+    ([0, 16, 2, 16, 5, 1, 9, 20, 20], [186009, 1445, 409, 94, 68, 1518, 795, 2423])], ids=str)
+def test_a_decreasing_cu_with_blocks_behind_the_total(cu, lens):
+    """Offsets with which the walk over the blocks meets long ones that the total does not count: a block's end then
+    lies up to eight times the total away, and the merge must not look for partials there."""
+    T, H = cu[-1], 128
+    g = torch.Generator(device="cuda").manual_seed(10)
+    pages = torch.randn(4, 64, 576, device="cuda", generator=g).half()
+    table = torch.randint(0, 4, (len(lens), -(-max(lens) // 64)), dtype=torch.int32, device="cuda", generator=g)
+    q_lat = torch.randn(T, H, 512, device="cuda", generator=g, dtype=torch.float16)
+    q_pe = torch.randn(T, H, 64, device="cuda", generator=g, dtype=torch.bfloat16)
+    out = torch.zeros(T, H, 512, dtype=torch.float16, device="cuda")
+    mla.mla_attn_paged(q_lat, q_pe, pages, table, i32(cu), i32(lens), out, scale=SCALE)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == INVALID
+    b = Batch(21, False, 16, 16, [4, 4, 4], [40, 30, 20])
+    check(b, run(b))
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_same_call_same_bits_on_two_streams(e4m3):
     b = Batch(18, e4m3, 128, 64, [1, 1, 5], [3000, 5000, 900])

@@ -110,6 +110,12 @@ __host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 80 : 96; }
 constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
 
+// What the P V warp asks of the output warps, besides a rescale of O (tile >= 0).  A
+// piece may be millions of tiles long and never need one, so that they would wait
+// through all of it, past the limit of a wait: every kBeat tiles (5 ms) they get a
+// request for nothing.
+constexpr int kCmdOutput = -1, kCmdStop = -2, kCmdNone = -3, kBeat = 4096;
+
 constexpr int kPieceCost = 3;                // start-up of a piece (5-6k cycles) in tiles
 constexpr float kCutCost = 4.f;              // of a share (see there)
 
@@ -334,7 +340,7 @@ struct Bars {
   uint64_t l_full[4];               // piece k's row sums (slot k % 4)
   uint64_t cmd_full, cmd_done;      // the P V warp's requests to the output warps
   uint32_t tmem;
-  int32_t cmd;                      // -2 stop, -1 write the piece's output, else rescale O by tile cmd's factors
+  int32_t cmd;                      // kCmd.., or a tile u: rescale O by its factors
   Start st;
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
@@ -935,8 +941,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     if (bf16x2_absmax_overflows(qrun)) record_error(a.p.err, MLA_ERR_RANGE);
   } else if (warp < kQkWarp) {
     // ================================= output ==================================
-    // Requests of the P V warp, in order: rescale O before a P V, or write a
-    // finished piece's output.
+    // Requests of the P V warp, in order: rescale O before a P V, write a
+    // finished piece's output, or nothing.
     const int q4 = warp - kOutWarp, i = 32 * q4 + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
     uint8_t* stg = sStg + q4 * 2048;
@@ -946,7 +952,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       ok = wait_all(&B.cmd_full, n & 1, a);
       if (!ok) break;
       const int u = *reinterpret_cast<volatile int32_t*>(&B.cmd);
-      if (u == -2) break;
+      if (u == kCmdStop) break;
       if (u >= 0) {
         const float f = sAlpha[(u & 1) * kRows + i];
         ok = wait_cl(&B.pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, a);
@@ -964,7 +970,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           }
           tc::tmem_st_wait();
         }
-      } else {
+      } else if (u == kCmdOutput) {
         if (!items.next(a, it)) break;
         ok = wait_all(&B.o_ready, k & 1, a) && wait_cl(&B.l_full[k & 3], (k >> 2) & 1, a);
         if (!ok) break;
@@ -1093,6 +1099,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f)) {
             post(u);
             if (ok) ok = wait_all(&B.cmd_done, (n - 1) & 1, a);
+          } else if (t % kBeat == 0) {
+            post(kCmdNone);
           }
         }
         if (!ok) break;
@@ -1108,10 +1116,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       }
       if (!ok) break;
       tc::mma_commit_warp(&B.o_ready);
-      post(-1);
+      post(kCmdOutput);
       ++k;
     }
-    if (ok) post(-2);
+    if (ok) post(kCmdStop);
   } else if (warp == kLoadWarp) {
     // ============================== TMA loader =================================
     // Lane 3 j + c: box j, the part of the tile that lies in one page, looked up a

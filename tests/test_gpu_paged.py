@@ -325,6 +325,31 @@ def test_a_chunk_of_more_than_2_to_the_24_tiles():
         assert ((out[i].double() - ref).abs() <= tol).all()
 
 
+def test_a_block_that_takes_longer_than_a_wait_may():
+    """80 sequences of 45 million rows, on two pages named many times: a cluster works on one block for more than half
+    a second, the limit of a wait.  All keys behind the first page score 200 below, so the output is the first
+    page's."""
+    ps, n, B, H = 4096, 11000, 80, 16
+    g = torch.Generator(device="cuda").manual_seed(12)
+    pages = torch.randn(2, ps, 576, device="cuda", generator=g).half()
+    pages[:, :, 512:] = 0
+    pages[1, :, 512] = -200.0
+    table = torch.ones(B, n, dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    q_lat = torch.randn(B, H, 512, device="cuda", generator=g, dtype=torch.float16)
+    q_pe = torch.zeros(B, H, 64, device="cuda", dtype=torch.bfloat16)
+    q_pe[:, :, 0] = 16.0                                 # x 200 x 0.072 = 231, below every score of the first page
+    out = torch.full((B, H, 512), float("nan"), dtype=torch.float16, device="cuda")
+    mla.mla_attn_paged(q_lat, q_pe, pages, table, i32(np.arange(B + 1)), i32([n * ps - 37] * B), out, scale=SCALE)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    rows = pages[0, :, :512].double()
+    w = ((q_lat.double() @ rows.T) * SCALE).softmax(-1)
+    ref, mag = w @ rows, w @ rows.abs()
+    tol = (2.0 ** -11 + 2.0 ** -12) * mag + 2.0 ** -11 * ref.abs() + 2.0 ** -24 + 2.0 ** -25 * ps * rows.abs().max()
+    assert ((out.double() - ref).abs() <= tol).all()
+
+
 def test_sharp_and_flat_scores():
     # nearly one key for each row; all keys alike (their mean); and all rows the same row
     for kw in (dict(std=6.0), dict(std=1e-3), dict(same=True)):

@@ -359,7 +359,7 @@ def _arg(t, name: str, dtype, shape, dev: int) -> int:
     raise ValueError(f"{name} is on {t.device}, another tensor on cuda:{dev}")
 
 
-def _paged_device(t, name: str) -> int:
+def paged_device(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.get_device()
@@ -412,7 +412,7 @@ def mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base:
                      freq_scale: float = 0.025, stream=None):
     """New tokens' rows into their pages: token i of sequence b's n new ones (rows cu_new[b].. of c_kv, k_pe) is
     written at position seq_len[b] - n + i, its RoPE part rotated by that position, in the pages' type."""
-    dev = _paged_device(c_kv, "c_kv")
+    dev = paged_device(c_kv, "c_kv")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base, freq_scale, stream)
@@ -427,7 +427,7 @@ def mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base:
 
 def mla_paged_gather(pages, block_table, row0, cu_rows, out, stream=None):
     """out [R, 576] (bf16 or fp16): rows cu_rows[b].. <- positions row0[b].. of sequence b (row0 None: from 0)."""
-    dev = _paged_device(out, "out")
+    dev = paged_device(out, "out")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return mla_paged_gather(pages, block_table, row0, cu_rows, out, stream)
@@ -452,7 +452,7 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
     """o_lat [T, H, 512]: attention of the batch's new tokens over their pages (one token a sequence or a chunk);
     window > 0 keeps each token's last ``window`` positions and the first ``n_sink``.  Without a workspace a fresh
     one is taken from PyTorch's allocator."""
-    dev = _paged_device(q_lat, "q_lat")
+    dev = paged_device(q_lat, "q_lat")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window, n_sink, workspace,

@@ -155,10 +155,20 @@ def mla_paged_step(q_nope, q_pe, c_kv, k_pe, wk_b, wv_b, pages, block_table, cu_
     the pages -> late decompression.  A sequence may bring one token (decode), a chunk (prefill) or none; rows of
     the token arrays behind the last sequence are padding, finite (absorption checks all rows' range); their ``o``
     follows from what ``bufs.o_lat`` held."""
+    dev = B.paged_device(q_nope, "q_nope")
+    if dev != torch.cuda.current_device():   # all four calls on the tensors' device and one of its streams
+        with torch.cuda.device(dev):
+            return mla_paged_step(q_nope, q_pe, c_kv, k_pe, wk_b, wv_b, pages, block_table, cu_q, seq_len, window=window,
+                                  n_sink=n_sink, freq_base=freq_base, freq_scale=freq_scale, bufs=bufs, scale=scale,
+                                  stream=stream)
     T, H = q_nope.shape[0], q_nope.shape[1]
     if bufs is None:
-        with B.stream_context(stream, q_nope.device.index):
+        with B.stream_context(stream, dev):
             bufs = paged_buffers(T, H, q_nope.device)
+    # (the cache calls check their other tensors)
+    for name, t in (("c_kv", c_kv), ("wk_b", wk_b), ("wv_b", wv_b), ("bufs.q_lat", bufs.q_lat), ("bufs.o", bufs.o)):
+        if B.paged_device(t, name) != dev:
+            raise ValueError(f"{name} is on {t.device}, q_nope on cuda:{dev}")
     B.mla_paged_append(c_kv, k_pe, pages, block_table, cu_q, seq_len, freq_base=freq_base, freq_scale=freq_scale,
                        stream=stream)
     B.mla_absorb_q(q_nope, wk_b, bufs.q_lat, scale=scale, stream=stream)

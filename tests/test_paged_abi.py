@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import mla_latent_kv_lat_gb300 as mla
-from mla_latent_kv_lat_gb300 import binding, build
+from mla_latent_kv_lat_gb300 import binding, build, pipeline
 from oracle import paged_oracle as PO
 from tests.paged_util import Batch
 
@@ -93,6 +93,77 @@ def test_the_binding_refuses_what_the_library_cannot_see():
         binding._paged(pages, table[0], -1)
     with pytest.raises(ValueError, match="contiguous"):
         binding._paged(pages, torch.zeros(4, 3, dtype=torch.int32).t(), -1)
+
+
+class OnDevice1(torch.Tensor):
+    """A host tensor that says that it lies on CUDA device 1."""
+    is_cuda, device = True, torch.device("cuda", 1)
+
+    def get_device(self):
+        return 1
+
+
+class OnDevice0(OnDevice1):
+    device = torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
+
+
+def test_a_step_on_another_device_runs_all_its_calls_there(monkeypatch):
+    """A stand-in for the library notes the current device and the stream of each call."""
+    current, calls = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    class Lib:
+        def __getattr__(self, name):
+            def call(*args):
+                stream = args[-1].value if isinstance(args[-1], ctypes.c_void_p) else args[-1]
+                calls.append((name, current[0], stream))
+                return 0
+            return call
+
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(100 + current[0]))
+    monkeypatch.setattr(binding, "_raw_stream", lambda dev: 100 + dev)
+    monkeypatch.setattr(binding, "load_library", Lib)
+
+    def on1(*shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice1)
+
+    H, i32 = 16, torch.int32
+    bufs = pipeline.PagedBuffers(on1(2, H, 512, dtype=torch.float16), on1(2, H, 512, dtype=torch.float16),
+                                 on1(2, H, 128, dtype=torch.float32), on1(64, dtype=torch.uint8))
+    args = dict(q_nope=on1(2, H, 128), q_pe=on1(2, H, 64), c_kv=on1(2, 512), k_pe=on1(2, 64), wk_b=on1(H, 128, 512),
+                wv_b=on1(H, 512, 128), pages=on1(3, 16, 576, dtype=torch.float16), block_table=on1(1, 2, dtype=i32),
+                cu_q=on1(2, dtype=i32), seq_len=on1(1, dtype=i32))
+    pipeline.mla_paged_step(**args, bufs=bufs)
+    assert [c[0] for c in calls] == ["mla_paged_append", "mla_absorb_q", "mla_attn_paged", "mla_late_decompress"]
+    assert all(c[1:] == (1, 101) for c in calls), calls
+    assert current[0] == 0
+    # and none of them runs when the tensors lie on two devices
+    del calls[:]
+    for name in ("c_kv", "wk_b", "wv_b"):
+        with pytest.raises(ValueError, match=name):
+            pipeline.mla_paged_step(**dict(args, **{name: args[name].as_subclass(OnDevice0)}), bufs=bufs)
+    bufs.o = bufs.o.as_subclass(OnDevice0)
+    with pytest.raises(ValueError, match="bufs.o"):
+        pipeline.mla_paged_step(**args, bufs=bufs)
+    assert not calls
 
 
 def test_oracle_rows():

@@ -111,10 +111,11 @@ constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, t
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
 
 // What the P V warp asks of the output warps, besides a rescale of O (tile >= 0).  A
-// piece may be millions of tiles long and never need one, so that they would wait
-// through all of it, past the limit of a wait: every kBeat tiles (5 ms) they get a
-// request for nothing.
-constexpr int kCmdOutput = -1, kCmdStop = -2, kCmdNone = -3, kBeat = 4096;
+// piece may be millions of tiles long and never need one, so the limit of their wait
+// grows by kTileUs with every tile of the cluster (one takes ~1.1 us).  (A request for
+// nothing every 4096 tiles instead made the P V warp's loop 0.5% slower.)
+constexpr int kCmdOutput = -1, kCmdStop = -2;
+constexpr int64_t kTileUs = 16;
 
 constexpr int kPieceCost = 3;                // start-up of a piece (5-6k cycles) in tiles
 constexpr float kCutCost = 4.f;              // of a share (see there)
@@ -941,15 +942,17 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     if (bf16x2_absmax_overflows(qrun)) record_error(a.p.err, MLA_ERR_RANGE);
   } else if (warp < kQkWarp) {
     // ================================= output ==================================
-    // Requests of the P V warp, in order: rescale O before a P V, write a
-    // finished piece's output, or nothing.
+    // Requests of the P V warp, in order: rescale O before a P V, or write a
+    // finished piece's output.
     const int q4 = warp - kOutWarp, i = 32 * q4 + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
     uint8_t* stg = sStg + q4 * 2048;
+    const uint32_t limit_us = static_cast<uint32_t>(
+        min(a.p.wait_us + kTileUs * (B.st.hi - B.st.lo), static_cast<int64_t>(UINT32_MAX)));
     int k = 0;
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
-      ok = wait_all(&B.cmd_full, n & 1, a);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&B.cmd_full, n & 1, limit_us, a.p.err));
       if (!ok) break;
       const int u = *reinterpret_cast<volatile int32_t*>(&B.cmd);
       if (u == kCmdStop) break;
@@ -970,7 +973,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           }
           tc::tmem_st_wait();
         }
-      } else if (u == kCmdOutput) {
+      } else {
         if (!items.next(a, it)) break;
         ok = wait_all(&B.o_ready, k & 1, a) && wait_cl(&B.l_full[k & 3], (k >> 2) & 1, a);
         if (!ok) break;
@@ -1099,8 +1102,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f)) {
             post(u);
             if (ok) ok = wait_all(&B.cmd_done, (n - 1) & 1, a);
-          } else if (t % kBeat == 0) {
-            post(kCmdNone);
           }
         }
         if (!ok) break;

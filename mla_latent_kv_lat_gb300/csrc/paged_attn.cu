@@ -108,7 +108,13 @@ __host__ __device__ constexpr int threads(bool e4m3) { return 32 * (kProdWarp + 
 __host__ __device__ constexpr int max_regs(bool e4m3) { return e4m3 ? 80 : 96; }
 
 constexpr uint32_t kTmQ = 0, kTmS = 128, kTmO = 256;   // TMEM columns: Q 128, two score buffers of 64, O 256
-constexpr float kRescaleThreshold = 8.0f;    // log2 units: P stays <= 256 in fp16
+// P in fp16 is exp2(score - m + kPShift), m the running maximum, which lags behind the
+// largest score by at most kRescaleThreshold: P stays <= 2^15.  The factor is in the row
+// sums and the partials' weights too, and cancels.  A probability keeps fp16's 11 bits
+// down to 2^-21 of the largest and counts down to 2^-32 of it (without the shift 2^-14
+// and 2^-25: of 98304 rows, all 16 below one key in score, 6% were lost).
+constexpr float kRescaleThreshold = 8.0f;    // log2 units
+constexpr float kPShift = 7.0f;
 
 // What the P V warp asks of the output warps, besides a rescale of O (tile >= 0).  A
 // piece may be millions of tiles long and never need one, so the limit of their wait
@@ -158,7 +164,7 @@ struct TcArgs {
   PagedAttnArgs p;
   Take take;
   float* ws_o;        // fp32 [2 G][128][512] partials, normalised by their own sums
-  float* ws_ml;       // fp32 [2 G][128][2] running maximum (log2 units) and sum
+  float* ws_ml;       // fp32 [2 G][128][2] running maximum (log2 units, less kPShift) and sum
   Rec* rec;           // [G]
   int32_t* stage_base;   // [B] a sequence's first staged row, -1: not staged (unless take is kTakeAll)
   uint16_t* stage;       // fp16 [kStageRows][512]
@@ -705,7 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       // keys [wl, lim] and the sinks are visible to this row
       const int lim = rvalid ? it.pos0 + static_cast<int>((it.row0 + i) / static_cast<uint32_t>(a.p.H)) : it.kend - 1;
       const int wl = a.p.window > 0 ? max(0, lim - a.p.window + 1) : 0;
-      float m_run = -INFINITY, l_h = 0.f;
+      float m_run = -INFINITY, l_h = 0.f;      // the running maximum, less kPShift; the sum
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int sb = u & 1;
@@ -775,9 +781,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           // Lazy rescale: only when the row maximum grew by more than the
           // threshold.  A row may see none of the tile's keys (or none so far):
           // its maximum stays -inf, its P zero.
-          if (mrow > m_run + kRescaleThreshold) {
-            alpha = tc::exp2_approx(m_run - mrow);
-            m_run = mrow;
+          if (mrow > m_run + (kRescaleThreshold + kPShift)) {
+            alpha = tc::exp2_approx(m_run - (mrow - kPShift));
+            m_run = mrow - kPShift;
             l_h *= alpha;
           }
           const float mb = m_run == -INFINITY ? 0.f : m_run;

@@ -439,6 +439,41 @@ def test_a_decreasing_cu_with_blocks_behind_the_total(cu, lens):
     check(b, run(b))
 
 
+@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("gap", [8.0, 14.0, 16.0, 18.0])
+def test_a_leading_key_of_small_values(gap, where, H):
+    """One key, with values of zero, whose score leads all 98304 others by `gap` (an attention sink): the output is the
+    others' small share.  As many sequences as leave their blocks whole."""
+    ps, L, B = 64, 98305, 152
+    g = torch.Generator(device="cuda").manual_seed(13)
+    pages = (torch.randn(-(-L // ps), ps, 576, device="cuda", generator=g) + 1.0).half()
+    pages[:, :, 512:] = 0
+    lead = 0 if where == "first" else L - 1
+    pages.view(-1, 576)[lead] = 0
+    pages.view(-1, 576)[lead, 512] = 1.0
+    table = torch.arange(len(pages), dtype=torch.int32, device="cuda").repeat(B, 1)
+    q_lat = torch.zeros(B, H, 512, dtype=torch.float16, device="cuda")
+    q_pe = torch.zeros(B, H, 64, dtype=torch.bfloat16, device="cuda")
+    q_pe[:, :, 0] = 128.0
+    scale = gap / 128.0                                  # exact: scores of 0 and of gap
+    out = torch.full((B, H, 512), float("nan"), dtype=torch.float16, device="cuda")
+    mla.mla_attn_paged(q_lat, q_pe, pages, table, i32(np.arange(B + 1)), i32([L] * B), out, scale=scale)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    rows = pages.view(-1, 576)[:L, :512].double()
+    w = float(np.exp(-gap))
+    total = 1.0 + (L - 1) * w
+    ref, mag = rows.sum(0) * w / total, rows.abs().sum(0) * w / total
+    # P to fp16: 2^-11 of itself, or below fp16's normal range 2^-25 where the largest is 2^7 at least; its exponent
+    # in fp32 (three roundings at up to 33, the exponential's own 2^-22): 2^-18; sums in fp32 of 16 products a step, a
+    # last place each; row sums in fp32, half of one a tile; the output to fp16
+    tol = ((2.0 ** -11 + 2.0 ** -18 + L / 16 * 2.0 ** -23) * mag + 2.0 ** -32 * L * rows.abs().mean(0)
+           + (2.0 ** -11 + (L / 64 + 1) * 2.0 ** -24) * ref.abs() + 2.0 ** -25)
+    off = ((out.double() - ref).abs() / tol).max().item()
+    assert off <= 1.0, off
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_same_call_same_bits_on_two_streams(e4m3):
     b = Batch(18, e4m3, 128, 64, [1, 1, 5], [3000, 5000, 900])

@@ -788,13 +788,19 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           }
           const float mb = m_run == -INFINITY ? 0.f : m_run;
           const uint64_t cc = pack2(c2, c2), mm = pack2(-mb, -mb);
+          // The row sum adds the probabilities as P V takes them, rounded: the weights
+          // of the values then sum to one, and a leading key's rounding cancels.  (The
+          // conversions back cost 0.3% of 32 tokens' time, 1.4% over e4m3 pages; with
+          // scores six times as large the error falls from 2.4e-4 to 2.1e-4 of the
+          // norm, the largest from 6.6e-4 to 3.9e-4.)
           uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 x = unpack2(fma2(s[e], cc, mm));
             const float p0 = tc::exp2_approx(x.x), p1 = tc::exp2_approx(x.y);
-            ls[e & 1] = add2(ls[e & 1], pack2(p0, p1));
             pk[e] = pack_f16x2(p0, p1);
+            const float2 pr = f16x2_to_f32(pk[e]);
+            ls[e & 1] = add2(ls[e & 1], pack2(pr.x, pr.y));
           }
           const float2 lsum = unpack2(add2(ls[0], ls[1]));
           l_h += lsum.x + lsum.y;

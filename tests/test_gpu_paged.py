@@ -475,6 +475,32 @@ def test_a_leading_key_of_small_values(gap, where, H):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H,L", [(16, 66), (128, 200), (64, 20000)])
+def test_weights_sum_to_one(H, L, e4m3):
+    """Rows of equal latents with different RoPE keys: whatever the weights, the output is that latent, to the bit (the
+    sums' fp32 roundings are far below half an fp16 step).  The first key scores 0, one of the second tile 2^7 (1 +
+    0.98 x 2^-11) times as much: less than lets the running maximum move, and almost half a step from an fp16 value, so
+    that the output would be 1.8 half steps off if the row sum did not have the same rounding."""
+    ps = 64
+    lat = torch.full((-(-L // ps) * ps, 512), 1.875)
+    rope = torch.zeros(len(lat), 64)
+    rope[1:, 0] = -1000.0
+    rope[65, 0] = 100.0
+    raw = torch.from_numpy(PO.pack_rows(lat.numpy(), rope.numpy(), e4m3)).cuda()
+    pages = (raw if e4m3 else raw.view(torch.float16)).reshape(len(lat) // ps, ps, -1)
+    table = torch.arange(len(pages), dtype=torch.int32, device="cuda")[None]
+    q_lat = torch.zeros(1, H, 512, dtype=torch.float16, device="cuda")
+    q_pe = torch.zeros(1, H, 64, dtype=torch.bfloat16, device="cuda")
+    q_pe[:, :, 0] = 1.0
+    scale = (7.0 + np.log2(1.0 + 0.98 * 2.0 ** -11)) / 100.0 * np.log(2.0)
+    out = torch.full((1, H, 512), float("nan"), dtype=torch.float16, device="cuda")
+    mla.mla_attn_paged(q_lat, q_pe, pages, table, i32([0, 1]), i32([L]), out, scale=scale)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    assert (out == 1.875).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_same_call_same_bits_on_two_streams(e4m3):
     b = Batch(18, e4m3, 128, 64, [1, 1, 5], [3000, 5000, 900])
     d = b.dev()

@@ -396,7 +396,10 @@ int mla_paged_append(const mla_paged_cache* cache, const void* c_kv, const void*
  * row0 device int32 [B] or NULL (zero); cu_rows device int32 [B + 1];
  * out device bf16 [R][576], or fp16 with out_f16 != 0 (then exact).
  * A row whose position is outside the table row, or whose table entry is bad,
- * is left as it was and recorded.                                             */
+ * is left as it was and recorded.  A sequence whose rows leave [0, R) is
+ * recorded as MLA_ERR_INVALID_ARG: rows at R and behind have no place and are
+ * not written, with cu_rows[b] < 0 none of its rows is.  Decreasing cu_rows are
+ * recorded, too; which rows they leave unwritten is undefined.               */
 int mla_paged_gather(const mla_paged_cache* cache, const int32_t* row0, const int32_t* cu_rows,
                      int32_t B, int32_t R, void* out, int32_t out_f16, void* stream);
 

@@ -232,6 +232,13 @@ __global__ void __launch_bounds__(256, 4) paged_gather_kernel(PagedGatherArgs a)
       if (row_p >= 0) dst[(lane >> 3) * kUnits + kLatent / 8 + (lane & 7)] = out8<kOutF16>(pe);
     }
   }
+  if (blockIdx.x == 0) {
+    // sequences whose rows leave the output (here, cu is in the cache)
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+      const int32_t c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
+      bad = bad || c0 < 0 || c1 < c0 || c1 > a.R;
+    }
+  }
   if (bad) record_error(a.err, MLA_ERR_INVALID_ARG);
 }
 

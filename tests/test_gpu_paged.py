@@ -191,6 +191,22 @@ def test_bad_sequences_and_pages_are_skipped_and_reported():
     assert mla.mla_get_device_error() == INVALID
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("cu,whole", [([0, 4, 8, 13], 8), ([0, 4, 40, 40], 4), ([0, 8, 4, 12], 0), ([-2, 4, 8, 12], 0),
+                                      ([12, 12, 12, 12], 0), ([0, 4, 8, 12], 12)], ids=str)
+def test_read_back_reports_rows_outside_the_output(cu, whole, e4m3):
+    """`whole`: rows of the output in front that the call defines, whatever it reports."""
+    b = Batch(27, e4m3, 16, 16, [40, 33, 20], [40, 33, 20])
+    d = b.dev()
+    out = torch.full((12, 576), 7.0, dtype=torch.float16, device="cuda")
+    mla.mla_paged_gather(d["pages"], d["block_table"], None, i32(cu), out)
+    torch.cuda.synchronize()
+    good = cu[0] >= 0 and all(x <= y for x, y in zip(cu, cu[1:])) and cu[-1] <= 12
+    assert mla.mla_get_device_error() == (0 if good else INVALID)
+    want = np.concatenate([b.rows[s][:max(0, cu[s + 1] - cu[s])] for s in range(3)]) if whole else np.zeros((0, 576))
+    assert np.array_equal(out[:whole].double().cpu().numpy(), want[:whole])
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------

@@ -379,7 +379,9 @@ def stream_context(stream, dev: int):
     """Allocations inside belong to ``stream`` (None: the current stream), so that a block which the allocator takes
     back is not handed to another stream while ``stream``'s kernels still use it."""
     if stream is not None and not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+        handle = int(getattr(stream, "cuda_stream", stream))
+        # The handles 0 and 1 (cudaStreamLegacy) are the default stream; ExternalStream takes 0 for "a new one".
+        stream = torch.cuda.default_stream(dev) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=dev)
     return torch.cuda.stream(stream)
 
 

@@ -597,6 +597,26 @@ def test_captured_step_follows_its_arrays(e4m3):
             assert np.isfinite(got).all()
 
 
+@pytest.mark.parametrize("stream", [0, 1])
+def test_a_step_on_the_default_stream_by_its_handle(stream, monkeypatch):
+    """Its buffers come from that stream, and so does the zero fill of o_lat."""
+    H, seen = 16, []
+    make = P.paged_buffers
+    monkeypatch.setattr(P, "paged_buffers", lambda *a: (seen.append(torch.cuda.current_stream()), make(*a))[1])
+    g = torch.Generator(device="cuda").manual_seed(14)
+    bf = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()             # noqa: E731
+    args = (bf(2, H, 128), bf(2, H, 64), bf(2, 512), bf(2, 64), bf(H, 128, 512), bf(H, 512, 128) / 22)
+    table, cu, lens = torch.tensor([[0]], dtype=torch.int32, device="cuda"), i32([0, 2]), i32([2])
+    outs = []
+    for s in (None, stream):
+        pages = P.paged_pages(1, 16)
+        outs.append(P.mla_paged_step(*args, pages, table, cu, lens, stream=s).o.clone())
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    assert seen == [torch.cuda.default_stream()] * 2
+    assert torch.equal(*outs) and outs[0].abs().max() > 0
+
+
 def test_read_back_feeds_the_flat_prefill():
     """A prefix in pages, read back as flat rows, gives the flat prefill the same answer as the pages give."""
     b = Batch(19, False, 16, 64, [40], [200])

@@ -166,6 +166,22 @@ def test_a_step_on_another_device_runs_all_its_calls_there(monkeypatch):
     assert not calls
 
 
+def test_allocations_belong_to_the_stream_that_a_handle_names(monkeypatch):
+    """Handles 0 and 1 are the default stream's; others are wrapped; Stream objects and None pass."""
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda dev: ("default", dev))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device: ("external", h, device))
+
+    class Foreign:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    for h in (0, 1):
+        assert binding.stream_context(h, 1) == binding.stream_context(Foreign(h), 1) == ("default", 1)
+    assert binding.stream_context(0x7f00, 0) == binding.stream_context(Foreign(0x7f00), 0) == ("external", 0x7f00, 0)
+    assert binding.stream_context(None, 0) is None
+
+
 def test_oracle_rows():
     v = PO.e4m3_values()
     assert v[0x7E] == 448 and v[1] == 2.0 ** -9 and v[8] == 2.0 ** -6 and v[0x38] == 1.0 and v[0xB8] == -1.0

@@ -362,6 +362,8 @@ int mla_rope_append(const void* c_kv, const void* k_pe, const int32_t* pos, cons
  * computed as usual.  (A decreasing cu is recorded too, but leaves all outputs
  * of the call undefined.)  These arrays are read on the device only, so a
  * captured call follows their contents.
+ * What a call writes (append: the pages; gather: out; attention: o_lat and the
+ * workspace) must not overlap anything else that it is given: MLA_ERR_INVALID_ARG.
  * The kernels of these calls are launched as programmatic dependents: they may
  * be scheduled while the stream's previous kernel finishes, and wait for its
  * completion before they touch memory.                                        */
@@ -418,7 +420,7 @@ size_t mla_paged_workspace_size(const mla_dims* dims);
  * window > 0 keeps the last `window` positions (the token's own among them)
  * and the first n_sink (attention sinks); window == 0 keeps all.
  * q_lat device fp16 [T][H][512]; q_pe device bf16 [T][H][64] (rotated);
- * o_lat device fp16 [T][H][512], apart from q_lat (MLA_ERR_INVALID_ARG).
+ * o_lat device fp16 [T][H][512].
  * workspace device, ws_bytes >= mla_paged_workspace_size(dims): contents need
  * not be kept between calls; calls that may overlap on the GPU need one each.
  * Visible rows must hold finite values; rows that no new token of the call

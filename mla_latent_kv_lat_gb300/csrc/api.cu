@@ -220,6 +220,25 @@ int check_i32(std::initializer_list<const int32_t*> ps) {
   return MLA_OK;
 }
 
+// Memory that a call writes must lie apart from all that it reads.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool overlap(Span written, std::initializer_list<Span> others) {
+  const uintptr_t w = reinterpret_cast<uintptr_t>(written.p);
+  for (const Span& o : others) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(o.p);
+    if (p != 0 && p < w + written.bytes && w < p + o.bytes) return true;
+  }
+  return false;
+}
+Span i32_span(const int32_t* p, int64_t n) { return {p, 4 * n}; }
+Span pages_span(const PagedCache& c) {
+  return {c.pages, (static_cast<int64_t>(c.n_pages) << c.page_shift) * (c.e4m3 ? kRowE4m3 : kRowF16)};
+}
+Span table_span(const PagedCache& c, int32_t B) { return i32_span(c.table, (B - 1) * c.table_stride + c.max_pages); }
+
 // turns per position of pair i, frac(t_i) as 0.64 fixed point: two exact
 // 32-bit halves of the double's fraction.  A thread keeps the table of its last
 // frequencies: a model has one, and its powers are a fifth of an append's C call.
@@ -440,6 +459,9 @@ int mla_paged_append(const mla_paged_cache* cache, const void* c_kv, const void*
   if (T < 1) return MLA_ERR_INVALID_ARG;
   if (!(freq_base > 1.f) || !(freq_scale > 0.f) || !isfinite(freq_base) || !isfinite(freq_scale))
     return MLA_ERR_INVALID_ARG;
+  if (overlap(pages_span(a.c), {{c_kv, int64_t{T} * kLatent * 2}, {k_pe, int64_t{T} * kRope * 2}, table_span(a.c, B),
+                                i32_span(cu_new, int64_t{B} + 1), i32_span(seq_len, B)}))
+    return MLA_ERR_INVALID_ARG;
   a.c_kv = static_cast<const uint16_t*>(c_kv);
   a.k_pe = static_cast<const uint16_t*>(k_pe);
   a.cu = cu_new;
@@ -462,6 +484,9 @@ int mla_paged_gather(const mla_paged_cache* cache, const int32_t* row0, const in
   if (s != MLA_OK) return s;
   if (row0 != nullptr && (reinterpret_cast<uintptr_t>(row0) & 3u)) return MLA_ERR_MISALIGNED;
   if (R < 1) return MLA_ERR_INVALID_ARG;
+  if (overlap({out, int64_t{R} * kRow * 2},
+              {pages_span(a.c), table_span(a.c, B), i32_span(cu_rows, int64_t{B} + 1), i32_span(row0, B)}))
+    return MLA_ERR_INVALID_ARG;
   a.row0 = row0;
   a.cu = cu_rows;
   a.B = B;
@@ -490,12 +515,18 @@ int mla_attn_paged(const mla_dims* dims, const void* q_lat, const void* q_pe, co
   if (s != MLA_OK) return s;
   if (T < 1 || window < 0 || n_sink < 0) return MLA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(T) * dims->n_head > INT32_MAX) return MLA_ERR_UNSUPPORTED;
-  // q_lat is read (by several clusters) while o_lat is written
-  const uintptr_t q = reinterpret_cast<uintptr_t>(q_lat), o = reinterpret_cast<uintptr_t>(o_lat);
-  const uintptr_t bytes = static_cast<uintptr_t>(T) * dims->n_head * kLatent * 2;
-  if (q < o + bytes && o < q + bytes) return MLA_ERR_INVALID_ARG;
+  // what the clusters read while others of them write
+  const int64_t rows = int64_t{T} * dims->n_head;
+  const Span o = {o_lat, rows * kLatent * 2}, q = {q_lat, rows * kLatent * 2};
+  if (overlap(o, {q})) return MLA_ERR_INVALID_ARG;
   if (workspace == nullptr || ws_bytes < paged_attn_workspace_bytes()) return MLA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return MLA_ERR_MISALIGNED;
+  const Span ws = {workspace, static_cast<int64_t>(paged_attn_workspace_bytes())};
+  for (const Span& w : {o, ws})
+    if (overlap(w, {{q_pe, rows * kRope * 2}, pages_span(a.c), table_span(a.c, B), i32_span(cu_q, int64_t{B} + 1),
+                    i32_span(seq_len, B)}))
+      return MLA_ERR_INVALID_ARG;
+  if (overlap(ws, {o, q})) return MLA_ERR_INVALID_ARG;
   a.q_lat = static_cast<const uint16_t*>(q_lat);
   a.q_pe = static_cast<const uint16_t*>(q_pe);
   a.cu = cu_q;

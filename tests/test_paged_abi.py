@@ -77,6 +77,39 @@ def test_bad_arguments_are_refused(lib):
     assert lib.mla_paged_workspace_size(ctypes.byref(bad)) == 0
 
 
+def test_overlapping_memory_is_refused(lib):
+    """What a call writes, laid over the first and the last 16 (or 4) bytes of each thing that it reads."""
+    B, T, H, far = 3, 5, 16, 0x400000000
+    d = ctypes.byref(binding.make_dims(H))
+    ws = lib.mla_paged_workspace_size(d)
+    for type_, row in ((0, 1152), (1, 656)):
+        pool, table = 100 * 64 * row, ((B - 1) * 9 + 8) * 4
+        # every span at a place of its own, 4 GB apart
+        sizes = dict(pages=pool, table=table, cu=4 * (B + 1), len=4 * B, a=T * 1024, b=T * 128, ql=T * H * 1024,
+                     qp=T * H * 128, o=T * H * 1024, ws=ws, out=T * 1152, row0=4 * B)
+        place = {k: far * (i + 1) for i, k in enumerate(sizes)}
+
+        def calls(at):
+            c = cache(pages=at["pages"], block_table=at["table"], table_stride=9, type=type_)
+            return dict(
+                append=lambda: lib.mla_paged_append(c, at["a"], at["b"], at["cu"], at["len"], B, T, 1e4, 1.0, None),
+                gather=lambda: lib.mla_paged_gather(c, at["row0"], at["cu"], B, T, at["out"], 0, None),
+                attn=lambda: lib.mla_attn_paged(d, at["ql"], at["qp"], c, at["cu"], at["len"], B, T, 0, 0, at["ws"], ws,
+                                                at["o"], None))
+        reads = dict(append=("a", "b", "table", "cu", "len"), gather=("pages", "table", "cu", "row0"),
+                     attn=("ql", "qp", "pages", "table", "cu", "len"))
+        writes = dict(append=("pages",), gather=("out",), attn=("o", "ws"))
+        for call in reads:
+            for w in writes[call]:
+                for r in reads[call] + tuple(x for x in writes[call] if x != w):
+                    first, last = place[r] - sizes[w] + 16, place[r] + (sizes[r] - 1) // 16 * 16
+                    for to in (first + (-first) % 16, last):
+                        assert calls(dict(place, **{w: to}))[call]() == -1, (call, w, r, to - place[r])
+                    if not torch.cuda.is_available():        # side by side they pass the checks, and then find no device
+                        for to in (place[r] - sizes[w], place[r] + sizes[r] + (-sizes[r]) % 16):
+                            assert calls(dict(place, **{w: to // 16 * 16}))[call]() == -5, (call, w, r)
+
+
 def test_the_binding_refuses_what_the_library_cannot_see():
     pages, table = torch.zeros(2, 16, 576, dtype=torch.float16), torch.zeros(1, 2, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):

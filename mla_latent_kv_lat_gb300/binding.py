@@ -470,7 +470,8 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
         _dims(H, scale if scale is None else float(scale)), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
         _arg(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE), dev), cache,
         _arg(cu_q, "cu_q", torch.int32, (Bn + 1,), dev), _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn, T,
-        window, n_sink, _arg(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(),
+        window, n_sink, _arg(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev),
+        workspace.numel(),
         _arg(o_lat, "o_lat", torch.float16, (T, H, KV_LORA_RANK), dev), _stream_on(stream, dev))
     _check("mla_attn_paged", st)
 

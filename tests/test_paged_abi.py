@@ -199,6 +199,26 @@ def test_a_step_on_another_device_runs_all_its_calls_there(monkeypatch):
     assert not calls
 
 
+def test_a_workspace_that_is_no_tensor_is_refused_by_name(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+
+    class Lib:
+        mla_attn_paged = None
+
+    monkeypatch.setattr(binding, "load_library", Lib)
+
+    def on1(*shape, dtype=torch.int32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice1)
+
+    f16 = torch.float16
+    for bad, error in ((1 << 20, TypeError), (bytearray(64), TypeError), (on1(64), TypeError),
+                       (torch.zeros(64, dtype=torch.uint8), ValueError)):
+        with pytest.raises(error, match="workspace"):
+            mla.mla_attn_paged(on1(2, 16, 512, dtype=f16), on1(2, 16, 64, dtype=torch.bfloat16),
+                               on1(3, 16, 576, dtype=f16), on1(1, 2), on1(2), on1(1), on1(2, 16, 512, dtype=f16),
+                               workspace=bad)
+
+
 def test_allocations_belong_to_the_stream_that_a_handle_names(monkeypatch):
     """Handles 0 and 1 are the default stream's; others are wrapped; Stream objects and None pass."""
     monkeypatch.setattr(torch.cuda, "stream", lambda s: s)

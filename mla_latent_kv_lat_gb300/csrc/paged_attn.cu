@@ -49,7 +49,7 @@
 // is a whole block writes o_lat; a block cut by a cluster boundary leaves fp32
 // partials (at most two per cluster) that paged_combine_kernel merges.
 // Every wait on an mbarrier is bounded; a warp that gave one up still comes to the
-// named barriers.
+// named barriers, and its CTA leaves when what it had under way has ended.
 #include <string.h>
 
 #include <atomic>
@@ -122,6 +122,7 @@ constexpr float kPShift = 7.0f;
 // nothing every 4096 tiles instead made the P V warp's loop 0.5% slower.)
 constexpr int kCmdOutput = -1, kCmdStop = -2;
 constexpr int64_t kTileUs = 16;
+constexpr uint64_t kGaveUpNs = 200000;       // from a wait that ran out to the CTA's end
 
 constexpr int kPieceCost = 3;                // start-up of a piece (5-6k cycles) in tiles
 constexpr float kCutCost = 4.f;              // of a share (see there)
@@ -863,6 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       tc::named_bar_sync(kBarMax + q4, 64);
       ++k;
     }
+    ok = !dead;
   } else if (warp < kOutWarp) {
     // ===================== queries, and the peer's partial scores ==============
     const int q4 = warp - kSendWarp, hh = lane >> 4;
@@ -1255,10 +1257,16 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         if (lane == 0) mbar_arrive(&B.lat_full[ls]);
       }
     }
+    ok = !dead;
   }
 
   tc::fence_before_sync();
-  __syncthreads();
+  if (__syncthreads_or(!ok)) {
+    // A wait ran out.  Loads, copies to the other CTA and products may be under way that
+    // nobody waits for any more: they take a few microseconds.
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < kGaveUpNs) __nanosleep(1000);
+  }
   tc::cluster_sync();                 // nothing may be sent to a CTA that has left
   if (warp == kQkWarp) {
     tc::fence_after_sync();

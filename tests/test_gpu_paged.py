@@ -517,6 +517,20 @@ def test_weights_sum_to_one(H, L, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+def test_calls_behind_a_recorded_timeout_end_and_leave_the_next_one_right(e4m3):
+    """While the error word holds a timeout, waits that do not complete at once give up: every role of the kernel then
+    leaves early, with loads and products under way."""
+    few, many = Batch(28, e4m3, 16, 16, [1, 5], [300, 90]), Batch(29, e4m3, 128, 64, [1] * 90, [777] * 90)
+    d = [(b, b.dev()) for b in (few, many)]
+    mla.mla_selftest_wait_timeout(1000)
+    for b, x in d:
+        run(b, x)                                        # undefined outputs
+    assert mla.mla_get_device_error() == -6
+    for b, x in d:
+        check(b, run(b, x))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_same_call_same_bits_on_two_streams(e4m3):
     b = Batch(18, e4m3, 128, 64, [1, 1, 5], [3000, 5000, 900])
     d = b.dev()

@@ -463,6 +463,8 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
     if q_lat.dim() != 3:
         raise ValueError(f"q_lat must have shape (T, H, {KV_LORA_RANK}), got {tuple(q_lat.shape)}")
     (T, H, _), Bn = q_lat.shape, block_table.shape[0]
+    if max(window, n_sink) >= 1 << 31 or min(window, n_sink) < -1 << 31:     # ctypes would take their low 32 bits
+        raise ValueError(f"window ({window}) and n_sink ({n_sink}) must be int32")
     if workspace is None:
         with stream_context(stream, dev):
             workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)

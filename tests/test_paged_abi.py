@@ -199,6 +199,26 @@ def test_a_step_on_another_device_runs_all_its_calls_there(monkeypatch):
     assert not calls
 
 
+@pytest.mark.parametrize("kw", [dict(window=1 << 31), dict(window=(1 << 32) + 5), dict(n_sink=1 << 40),
+                                dict(window=5 - (1 << 32))], ids=str)
+def test_windows_past_32_bits_are_refused(monkeypatch, kw):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+
+    class Lib:
+        mla_attn_paged = None
+
+    monkeypatch.setattr(binding, "load_library", Lib)
+
+    def on1(*shape, dtype=torch.int32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice1)
+
+    f16 = torch.float16
+    with pytest.raises(ValueError, match="window"):
+        mla.mla_attn_paged(on1(2, 16, 512, dtype=f16), on1(2, 16, 64, dtype=torch.bfloat16),
+                           on1(3, 16, 576, dtype=f16), on1(1, 2), on1(2), on1(1), on1(2, 16, 512, dtype=f16),
+                           workspace=on1(64, dtype=torch.uint8), **kw)
+
+
 def test_a_workspace_that_is_no_tensor_is_refused_by_name(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
 

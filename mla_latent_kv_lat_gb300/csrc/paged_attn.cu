@@ -432,6 +432,11 @@ MLA_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+// a and b plus the halves of w (fp16), added in fp32.
+MLA_DEVINL void add_f16x2(float& a, float& b, uint32_t w) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}"
+      : "+f"(a), "+f"(b) : "r"(w));
+}
 MLA_DEVINL float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -790,21 +795,19 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
           const float mb = m_run == -INFINITY ? 0.f : m_run;
           const uint64_t cc = pack2(c2, c2), mm = pack2(-mb, -mb);
           // The row sum adds the probabilities as P V takes them, rounded: the weights
-          // of the values then sum to one, and a leading key's rounding cancels.  (The
-          // conversions back cost 0.3% of 32 tokens' time, 1.4% over e4m3 pages; with
+          // of the values then sum to one, and a leading key's rounding cancels.  (With
           // scores six times as large the error falls from 2.4e-4 to 2.1e-4 of the
-          // norm, the largest from 6.6e-4 to 3.9e-4.)
-          uint64_t ls[2] = {0ull, 0ull};
+          // norm, the largest from 6.6e-4 to 3.9e-4.  Converted back and added in pairs
+          // they took 0.3% longer for 32 tokens and 1.8% over e4m3 pages.)
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 x = unpack2(fma2(s[e], cc, mm));
             const float p0 = tc::exp2_approx(x.x), p1 = tc::exp2_approx(x.y);
             pk[e] = pack_f16x2(p0, p1);
-            const float2 pr = f16x2_to_f32(pk[e]);
-            ls[e & 1] = add2(ls[e & 1], pack2(pr.x, pr.y));
+            add_f16x2(ls[2 * (e & 1)], ls[2 * (e & 1) + 1], pk[e]);
           }
-          const float2 lsum = unpack2(add2(ls[0], ls[1]));
-          l_h += lsum.x + lsum.y;
+          l_h += (ls[0] + ls[2]) + (ls[1] + ls[3]);
         }
         if (!dead) {
           // The P buffer and the factors of tile u - 2 have been used in both CTAs.

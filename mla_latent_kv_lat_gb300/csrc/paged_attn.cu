@@ -121,6 +121,14 @@ constexpr float kPShift = 7.0f;
 // grows by kTileUs with every tile of the cluster (one takes ~1.1 us).  (A request for
 // nothing every 4096 tiles instead made the P V warp's loop 0.5% slower.)
 constexpr int kCmdOutput = -1, kCmdStop = -2;
+// A request kCmdMove - u moves what O holds before tile u's P V to the piece's partial in
+// the workspace; O starts anew.  The tensor cores' fp32 sums are not rounded but cut
+// off: with every 16 keys O loses 2^-24 of itself on average, and over a million rows
+// 0.65% were missing.  Every kMoveTiles tiles (65536 rows, 2.4e-4) O is therefore added
+// to the partial, rounded to nearest: 152 tokens at a million rows 33.4 -> 34.1 ms.  Its
+// code makes shorter calls 1% slower (32 tokens 156.6 -> 158.2 us), so it is an
+// instantiation of its own (kLong), for calls in which a block can have as many tiles.
+constexpr int kCmdMove = -3, kMoveTiles = 1024;
 constexpr int64_t kTileUs = 16;
 constexpr uint64_t kGaveUpNs = 200000;       // from a wait that ran out to the CTA's end
 
@@ -348,7 +356,7 @@ struct Bars {
   uint64_t l_full[4];               // piece k's row sums (slot k % 4)
   uint64_t cmd_full, cmd_done;      // the P V warp's requests to the output warps
   uint32_t tmem;
-  int32_t cmd;                      // kCmd.., or a tile u: rescale O by its factors
+  int32_t cmd;                      // kCmd.. (kCmdMove - u), or a tile u: rescale O by its factors
   Start st;
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
@@ -459,6 +467,51 @@ MLA_DEVINL void store_rows(uint8_t* stg, int lane, const uint4 (&w)[4], uint8_t*
   __syncwarp();
 }
 
+// 32 rows (lane = row) x 256 columns of O, plus g times what `part` holds of them (`add`),
+// times f: as fp32 to `part`, or as fp16 to `out`.
+__device__ __noinline__ void move_o(uint32_t taddr, uint8_t* stg, uint8_t* part, int nrows, bool add, float g, float f,
+                                    uint8_t* out) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int cc = 0; cc < 16; ++cc) {
+    uint32_t r[16];
+    tc::tmem_ld16(taddr + 16 * cc, r);
+    tc::tmem_ld_wait();
+    float o[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(r[e]);
+    if (add && lane < nrows) {
+      const float4* p = reinterpret_cast<const float4*>(part + lane * (kLatent * 4) + cc * 64);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float4 x = p[v];
+        o[4 * v] = fmaf(x.x, g, o[4 * v]);
+        o[4 * v + 1] = fmaf(x.y, g, o[4 * v + 1]);
+        o[4 * v + 2] = fmaf(x.z, g, o[4 * v + 2]);
+        o[4 * v + 3] = fmaf(x.w, g, o[4 * v + 3]);
+      }
+    }
+    __syncwarp();
+    if (out != nullptr) {
+      if (lane < nrows) {
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = pack_f16x2(o[2 * e] * f, o[2 * e + 1] * f);
+        uint4* q = reinterpret_cast<uint4*>(out + lane * (kLatent * 2) + cc * 32);
+        q[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        q[1] = make_uint4(h[4], h[5], h[6], h[7]);
+      }
+    } else {
+      uint4 w[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        w[v] = make_uint4(__float_as_uint(o[4 * v] * f), __float_as_uint(o[4 * v + 1] * f),
+                          __float_as_uint(o[4 * v + 2] * f), __float_as_uint(o[4 * v + 3] * f));
+      store_rows(stg, lane, w, part + cc * 64, kLatent * 4, nrows);
+    }
+  }
+}
+
 MLA_DEVINL uint4 bf16x8_to_f16x8(uint4 v) {
   uint4 o;
   float2 f;
@@ -523,7 +576,7 @@ MLA_DEVINL void store_f16(const Codes& c, uint8_t* lat, int pt, int j) {
 // are (32 tokens at 4K-32K rows, 16 heads: 136 us, without it 146; 64 heads 140 and
 // 148, 96 heads 146 and 151).  Its own instantiation, because the tests make full
 // blocks 2% slower; for e4m3 pages it gains nothing.
-template <bool kE4m3, bool kFewRows>
+template <bool kE4m3, bool kFewRows, bool kLong>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                       const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_scale,
@@ -959,25 +1012,42 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     if (bf16x2_absmax_overflows(qrun)) record_error(a.p.err, MLA_ERR_RANGE);
   } else if (warp < kQkWarp) {
     // ================================= output ==================================
-    // Requests of the P V warp, in order: rescale O before a P V, or write a
-    // finished piece's output.
+    // Requests of the P V warp, in order: rescale O before a P V, move it, or write
+    // a finished piece's output.
     const int q4 = warp - kOutWarp, i = 32 * q4 + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
     uint8_t* stg = sStg + q4 * 2048;
     const uint32_t limit_us = static_cast<uint32_t>(
         min(a.p.wait_us + kTileUs * (B.st.hi - B.st.lo), static_cast<int64_t>(UINT32_MAX)));
     int k = 0;
+    bool moved = false;                // some of the piece under way is in its partial,
+    float g = 1.f;                     // which this row's factor since then has yet to shrink
+    auto partial = [&](const Item& x) {  // this warp's rows in it
+      const int64_t slot = 2 * static_cast<int64_t>(c) + (x.t_lo > 0 ? 0 : 1);
+      return reinterpret_cast<uint8_t*>(a.ws_o + (slot * kRows + 32 * q4) * kLatent + 256 * rank);
+    };
 #pragma unroll 1
     for (int n = 0; ok; ++n) {
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&B.cmd_full, n & 1, limit_us, a.p.err));
       if (!ok) break;
       const int u = *reinterpret_cast<volatile int32_t*>(&B.cmd);
       if (u == kCmdStop) break;
-      if (u >= 0) {
+      if (kLong && u <= kCmdMove) {
+        const int m = kCmdMove - u;
+        ok = wait_cl(&B.pv_done[(m - 1) & 1], ((m - 1) >> 1) & 1, a);
+        if (!ok) break;
+        tc::fence_after_sync();
+        Iter ahead = items;            // (the output looks the piece up again)
+        if (!ahead.next(a, it)) break;
+        move_o(tmem + lanes + kTmO, stg, partial(it), it.nvalid - 32 * q4, moved, g, 1.f, nullptr);
+        moved = true;
+        g = sAlpha[(m & 1) * kRows + i];
+      } else if (u >= 0) {
         const float f = sAlpha[(u & 1) * kRows + i];
         ok = wait_cl(&B.pv_done[(u - 1) & 1], ((u - 1) >> 1) & 1, a);
         if (!ok) break;
         tc::fence_after_sync();
+        if (kLong) g *= f;
         if (__any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
           for (int cc = 0; cc < 8; ++cc) {
@@ -999,7 +1069,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         const float l = sL[(k & 3) * kRows + i];
         const float inv = l > 0.f ? 1.f / l : 0.f;     // a row that sees no key of this piece
         const int nrows = it.nvalid - 32 * q4;
-        if (kFewRows && nrows <= 0) {
+        if (kLong && moved) {
+          uint16_t* out = a.p.o_lat + (it.qrow0 + 32 * q4) * kLatent + 256 * rank;
+          move_o(tmem + lanes + kTmO, stg, partial(it), nrows, true, g, inv,
+                 it.whole() ? reinterpret_cast<uint8_t*>(out) : nullptr);
+          moved = false;
+        } else if (kFewRows && nrows <= 0) {
           // none of the block's rows
         } else if (it.whole()) {
           uint8_t* dst = reinterpret_cast<uint8_t*>(a.p.o_lat + (it.qrow0 + 32 * q4) * kLatent + 256 * rank);
@@ -1019,8 +1094,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             store_rows(stg, lane, w, dst + cc * 64, kLatent * 2, nrows);
           }
         } else {
-          const int64_t slot = 2 * static_cast<int64_t>(c) + (it.t_lo > 0 ? 0 : 1);
-          uint8_t* dst = reinterpret_cast<uint8_t*>(a.ws_o + (slot * kRows + 32 * q4) * kLatent + 256 * rank);
+          uint8_t* dst = partial(it);
 #pragma unroll 1
           for (int cc = 0; cc < 8; ++cc) {
             uint32_t o[32];
@@ -1110,14 +1184,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int ls = (u + kQSlots * (k + 1)) % kLatStages, sb = u & 1;
+        const bool move = kLong && t > 0 && t % kMoveTiles == 0;
         ok = wait_cl(&B.p_full[sb], (u >> 1) & 1, a);
         if (!ok) break;
         if (t == 0) {
           if (n > 0) ok = wait_all(&B.cmd_done, (n - 1) & 1, a);          // the previous output has left O
         } else {
           const float4 f = *reinterpret_cast<const float4*>(sAlpha + sb * kRows + 4 * lane);
-          if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f)) {
-            post(u);
+          if (move || __any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f || f.z != 1.f || f.w != 1.f)) {
+            post(move ? kCmdMove - u : u);
             if (ok) ok = wait_all(&B.cmd_done, (n - 1) & 1, a);
           }
         }
@@ -1127,7 +1202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 #pragma unroll
         for (int ks = 0; ks < kBK / 16; ++ks)
           tc::mma_ss_warp(tmem + kTmO, tc::sdesc_sw64(p0 + (ks >> 1) * (kPBytes / 2) + (ks & 1) * 32),
-                          tc::sdesc_sw128(v0 + ks * 2 * kGroup, kChunk, kGroup), idesc, (t > 0 || ks > 0) ? 1u : 0u);
+                          tc::sdesc_sw128(v0 + ks * 2 * kGroup, kChunk, kGroup), idesc,
+                          ((t > 0 && !move) || ks > 0) ? 1u : 0u);
         tc::mma_commit_warp(&B.lat_empty[ls]);
         mma_commit_pair_warp(&B.pv_done[sb]);
         if (lane == 0) mbar_arrive_expect_tx(&B.p_full[sb], kPTx);     // tile u + 2's P
@@ -1469,10 +1545,10 @@ size_t partial_bytes() {
   return rows * kLatent * sizeof(float) + rows * 2 * sizeof(float) + clusters() * sizeof(Rec);
 }
 
-template <bool kE4m3, bool kFewRows>
+template <bool kE4m3, bool kFewRows, bool kLong>
 cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const CUtensorMap& ts,
                         const TcArgs& a, cudaStream_t stream) {
-  auto kern = paged_attn_kernel<kE4m3, kFewRows>;
+  auto kern = paged_attn_kernel<kE4m3, kFewRows, kLong>;
   static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1493,6 +1569,22 @@ cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUte
   return launch_dependent(few ? paged_combine_kernel<true> : paged_combine_kernel<false>,
                           dim3(static_cast<unsigned>(few ? a.n_slots : G), static_cast<unsigned>(groups)),
                           dim3(128 * kCombRows), 0, stream, a, G);
+}
+
+// kLong: a block of the call can have more than kMoveTiles tiles.  Its keys are at most a
+// table row's, or those of a window over its tokens (128 / 16 and two, at most) and the
+// sinks, with the tiles that these cut at both ends.
+bool any_long(const PagedAttnArgs& p) {
+  int64_t rows = min(static_cast<int64_t>(p.c.max_pages) << p.c.page_shift, static_cast<int64_t>(INT32_MAX));
+  if (p.window > 0) rows = min(rows, static_cast<int64_t>(p.window) + p.n_sink + kRows / 16 + 2 + 4 * kBK);
+  return rows > kMoveTiles * kBK;
+}
+
+template <bool kE4m3, bool kFewRows>
+cudaError_t launch_for(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const CUtensorMap& ts,
+                       const TcArgs& a, cudaStream_t stream) {
+  return any_long(a.p) ? launch_pair<kE4m3, kFewRows, true>(tm, tr, tq, ts, a, stream)
+                       : launch_pair<kE4m3, kFewRows, false>(tm, tr, tq, ts, a, stream);
 }
 
 }  // namespace
@@ -1529,8 +1621,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
     if (e != cudaSuccess) return e;
     // a block of single tokens has H rows
-    return p.T <= p.B && p.H <= kRows - 16 ? launch_pair<false, true>(tm, tr, tq, tq, a, stream)
-                                   : launch_pair<false, false>(tm, tr, tq, tq, a, stream);
+    return p.T <= p.B && p.H <= kRows - 16 ? launch_for<false, true>(tm, tr, tq, tq, a, stream)
+                                           : launch_for<false, false>(tm, tr, tq, tq, a, stream);
   }
   // In elements of two bytes, as the rows are: a CTA's 256 codes, and the 16 scales.
   CUtensorMap tcodes, tscales;
@@ -1549,11 +1641,11 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     e = launch_dependent(paged_stage_kernel, dim3(device_sm_count() * 4), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
     a.take = kTakeStaged;
-    e = launch_pair<false, false>(tm, tr, tq, tq, a, stream);
+    e = launch_for<false, false>(tm, tr, tq, tq, a, stream);
     if (e != cudaSuccess) return e;
     a.take = kTakeUnstaged;
   }
-  return launch_pair<true, false>(tcodes, tr, tq, tscales, a, stream);
+  return launch_for<true, false>(tcodes, tr, tq, tscales, a, stream);
 }
 
 }  // namespace mla

@@ -531,6 +531,42 @@ def test_calls_behind_a_recorded_timeout_end_and_leave_the_next_one_right(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,H,lead", [(152, 128, 15), (152, 16, 16), (152, 16, 17), (20, 48, 100), (3, 128, 16)])
+def test_sums_over_a_million_rows(B, H, lead, e4m3):
+    """Values of one sign, over rows that all count, in whole blocks (152 sequences), in blocks that are cut, and with
+    one page whose scores move the running maximum around the place (65536 rows) where sums are moved on."""
+    ps, L = 4096, (1 << 20) - 77
+    rng = np.random.default_rng(15)
+    lat, rope = np.zeros((8 * ps, 512), np.float32), np.zeros((8 * ps, 64), np.float32)
+    lat[:] = bf16(rng.uniform(1.0, 2.0, lat.shape))
+    rope[7 * ps:, 0] = 1.0                               # the leading page
+    raw = torch.from_numpy(PO.pack_rows(lat, rope, e4m3)).cuda()
+    pages = (raw if e4m3 else raw.view(torch.float16)).reshape(8, ps, -1)
+    table = rng.integers(0, 7, (1, 256))
+    table[0, lead] = 7
+    q_lat = torch.zeros(B, H, 512, dtype=torch.float16, device="cuda")
+    q_pe = torch.zeros(B, H, 64, dtype=torch.bfloat16, device="cuda")
+    q_pe[:, :, 0] = 1.0
+    gap = 5.875                                          # 8.5 in log2: the running maximum moves
+    out = torch.full((B, H, 512), float("nan"), dtype=torch.float16, device="cuda")
+    mla.mla_attn_paged(q_lat, q_pe, pages, i32(np.repeat(table, B, 0)), i32(np.arange(B + 1)), i32([L] * B), out,
+                       scale=gap)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    rows = PO.row_values(raw.cpu().numpy(), e4m3)[:, :512].reshape(8, ps, 512)
+    n = np.full(256, ps)
+    n[-1] = L - 255 * ps
+    w = np.where(table[0] == 7, np.exp(gap), 1.0)
+    total = (w * n).sum()
+    ref = sum(w[i] * rows[table[0, i], :n[i]].sum(0) for i in range(256)) / total
+    # relative, all values being positive: P to fp16 and the output to fp16 2^-11 each; the products' sums a last place
+    # (2^-23) for each 16 keys of 65536 rows, 2^-11; the row sum half of one a tile, 16384 x 2^-24; the exponent 2^-18
+    tol = 3 * 2.0 ** -11 + 2.0 ** -10 + 2.0 ** -18
+    off = np.abs(out.double().cpu().numpy() / ref - 1.0).max()
+    assert off <= tol, f"{off:.2e} of {tol:.2e}"
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_same_call_same_bits_on_two_streams(e4m3):
     b = Batch(18, e4m3, 128, 64, [1, 1, 5], [3000, 5000, 900])
     d = b.dev()

@@ -349,7 +349,7 @@ int mla_rope_append(const void* c_kv, const void* k_pe, const int32_t* pos, cons
  * B > 1).  Only entries of pages that hold a row the call needs are used; the
  * others may hold anything.
  *
- * Batches: B sequences (at most 65535) in one token array of T rows.  Sequence
+ * Batches: B >= 1 sequences (at most 65535) in one token array of T >= 1 rows.  Sequence
  * b's new tokens are rows cu[b] .. cu[b + 1] - 1 (cu: device int32 [B + 1], not
  * decreasing); seq_len[b] (device int32) counts its cache rows INCLUDING the
  * new tokens, which are its last ones: token i of n sits at position
@@ -395,7 +395,7 @@ int mla_paged_append(const mla_paged_cache* cache, const void* c_kv, const void*
 /* Read rows back into the flat layout of this header (the rows a flat prefill
  * or a copy to another cache takes): out row cu_rows[b] + i <- the values of
  * position row0[b] + i of sequence b, for cu_rows[b] + i < cu_rows[b + 1].
- * row0 device int32 [B] or NULL (zero); cu_rows device int32 [B + 1];
+ * row0 device int32 [B] or NULL (zero); cu_rows device int32 [B + 1]; R >= 1;
  * out device bf16 [R][576], or fp16 with out_f16 != 0 (then exact).
  * A row whose position is outside the table row, or whose table entry is bad,
  * is left as it was and recorded.  A sequence whose rows leave [0, R) is
@@ -427,6 +427,11 @@ size_t mla_paged_workspace_size(const mla_dims* dims);
  * sees may hold anything, and a page that holds only such rows needs no valid
  * table entry.  A needed table entry outside [0, n_pages) is recorded as
  * MLA_ERR_INVALID_ARG and leaves that sequence's outputs undefined.
+ * Roundings: q_pe becomes fp16 (exact from 2^-14 to 65504 in magnitude; below,
+ * to a multiple of 2^-24; above, MLA_ERR_RANGE).  Scores, their maxima and all
+ * sums are fp32.  A probability enters the sum over the values and its row's
+ * total as fp16, to within 2^-11 of itself, or 2^-32 of the row's largest if
+ * that is more.  o_lat is rounded once.
  * The order of the sums depends on the arguments and the batch alone: the same
  * call gives the same bits.                                                   */
 int mla_attn_paged(const mla_dims* dims, const void* q_lat, const void* q_pe,

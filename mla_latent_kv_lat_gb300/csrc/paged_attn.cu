@@ -16,7 +16,7 @@
 //     with (row / 16) % 2 == r.  Four sender warps pass the other CTA's 64 rows
 //     on to it in fp32, 4 KB a warp and tile as one bulk copy (stored to its shared
 //     memory 16 bytes a thread, they kept the SM's way out busy for 1000 of a
-//     tile's 2200 cycles: chunks over 16-row pages 268 us, not 255); softmax warps
+//     tile's 2200 cycles: chunks over 16-row pages took 268 us, then 255); softmax warps
 //     add what arrives to their own half, so scores are full fp32 sums and each
 //     row's softmax is computed once in the pair.  P (fp16) of the owned rows is
 //     stored to both CTAs, with the factor by which the row's earlier output has
@@ -30,8 +30,9 @@
 //     its load to its P V, ~8500 cycles, so the four stages allow no less than 2100
 //     either.  Eight warps share a tile's softmax (16 keys of a row per thread);
 //     two sets of four that take the tiles in turn were 1-2% slower, and so were
-//     16 warps.  512 queries of 128 heads at 33K rows: 3.57 ms, 1320 TFLOP/s, 69%
-//     of the measured rate; 32 tokens at 4K to 32K rows: 155 us, 4.5 TB/s.
+//     16 warps.  512 queries of 128 heads at 33K rows: 3.61 ms, 1305 TFLOP/s, 68%
+//     of the measured rate; 32 tokens at 4K to 32K rows: 156 us, 4.4 TB/s (one set of
+//     pages again and again; new ones each time 3.67 ms and 166 us).
 //   * O += P V on tcgen05, V read in place from the cache tile (N-major view).
 //   * A piece's queries come through the ring of cache tiles too, as two stages
 //     before its first tile, so that they are there when the piece before has
@@ -161,9 +162,9 @@ struct __align__(16) Rec {     // the block that starts in cluster c and ends in
 // Staging of e4m3 latents as fp16 (rows of 512): up to kStageRows rows of the
 // sequences with at least kStageBlocks blocks, in batches of at most kStageSeqs.
 // Measured with and without, one sequence of 128 heads (a query is a block) at 33K
-// rows: 8 queries 93 and 85 us, 12 120 and 119, 16 149 and 154, 152 1055 and 1315;
-// the staging and a second launch cost ~10 us, so at 2000 rows 16 queries take 36 and
-// 27 us, 64 66 and 60, 256 149 and 162.
+// rows: 8 queries 93 and 86 us, 12 121 and 121, 16 150 and 156, 152 1071 and 1333;
+// the staging and a second launch cost ~10 us, so at 2000 rows 16 queries take 37 and
+// 28 us, 64 66 and 60, 256 153 and 164.
 constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 16;
 
 // Which sequences a launch takes.
@@ -573,8 +574,8 @@ MLA_DEVINL void store_f16(const Codes& c, uint8_t* lat, int pt, int j) {
 // ---------------------------------------------------------------------------
 // kFewRows: blocks of fewer rows than 128, as single tokens of few heads are: warps
 // whose rows all lie behind a block's do no softmax, and their scores stay where they
-// are (32 tokens at 4K-32K rows, 16 heads: 136 us, without it 146; 64 heads 140 and
-// 148, 96 heads 146 and 151).  Its own instantiation, because the tests make full
+// are (32 tokens at 4K-32K rows, 16 heads: 138 us, without it 147; 64 heads 143 and
+// 149, 96 heads 149 and 152).  Its own instantiation, because the tests make full
 // blocks 2% slower; for e4m3 pages it gains nothing.
 template <bool kE4m3, bool kFewRows, bool kLong>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
@@ -682,10 +683,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     const long long S0 = before + incl - sum;
     // Cluster x of G takes [total x / G, total (x + 1) / G).  Short work takes fewer
     // clusters, with an equal share each: a shorter piece saves its tiles' time, another
-    // piece of the block costs the merge.  The sum is least near share = sqrt(cost of a block / kCutCost); blocks of up to two tiles are
-    // not cut.  (Measured when a call took 2 us longer than now: one token at 257 rows,
-    // 16 heads, shares of 1, 2, 3 14.2, 14.9, 17.0 us; 128 heads at 4000 rows 27.6,
-    // 21.8, 21.0, at 16000 shares of 3.3 and 8 33.6 and 28.5.)
+    // piece of the block costs the merge.  The sum is least near share = sqrt(cost of a
+    // block / kCutCost); blocks of up to two tiles are not cut.  (One token at 257 rows,
+    // 16 heads, shares of 1, 2, 3, 8: 12.5, 12.8, 13.2, 14.3 us; 128 heads at 4000 rows
+    // 26.6, 20.4, 19.1, 22.2, the rule 19.8; at 16000 shares of 3.3 and 8 31.5 and 26.5.)
     long long lo, hi;
     uint32_t share = 0;
     if (total < (1 << 24)) {
@@ -1359,9 +1360,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
 // cut into 76 pieces.)  Grid: x = the cluster in which the block starts, y = group of
 // 4 rows; with few blocks (kFew) x = which of the cut blocks, so that one token does
 // not start 2432 blocks for a few that have work, and eight partials are under way
-// with the statistics, in twice the registers.  (With and without: one token at 257
-// rows, 16 heads, 12.6 and 13.0 us, 128 heads at 100 rows 12.0 and 14.1, 8 tokens at
-// 1000 rows 18.8 and 19.5; but 16 tokens 22.0 and 21.8, 32 tokens 31.7 and 29.4.)
+// with the statistics, in twice the registers.  (With and without: 128 heads, one
+// token at 100 rows 11.9 and 14.0 us, 4 tokens at 2000 rows 18.9 and 19.5, 8 tokens at
+// 1000 rows 18.9 and 19.1, but 16 heads at 257 rows 12.6 and 12.2; past the rule's
+// bound it loses: 32 tokens took 31.7 and 29.4.)
 // Launched as a programmatic dependent of the attention.
 // ---------------------------------------------------------------------------
 constexpr int kCombRows = 4, kMaxClusters = 128;

@@ -13,6 +13,7 @@
 #include <cudaTypedefs.h>
 
 #include "kernels.cuh"
+#include "paged.cuh"
 #include "tc.cuh"
 
 namespace mla {

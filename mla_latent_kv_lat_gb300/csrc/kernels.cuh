@@ -92,10 +92,6 @@ struct AttnTcArgs {
 cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t d0, uint64_t d1, uint64_t d2,
                          uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2,
                          int swizzle_bytes = 128);
-// Rows of 16-bit elements in groups of eight, in chunks of 64 elements (dims:
-// element, row of the group, chunk, group), with 128-byte swizzle.
-cudaError_t make_tmap_row_groups(CUtensorMap* map, const void* base, uint64_t groups, uint64_t chunks,
-                                 uint64_t row_bytes, uint32_t box_groups, uint32_t box_chunks);
 
 // Prefill: n_items row tiles of 128.  Decode: n_items = number of clusters G
 // (the pieces are found on the device).

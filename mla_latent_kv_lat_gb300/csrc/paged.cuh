@@ -154,6 +154,11 @@ cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Rows of 16-bit elements in groups of eight, in chunks of 64 elements (dims:
+// element, row of the group, chunk, group), with 128-byte swizzle.
+cudaError_t make_tmap_row_groups(CUtensorMap* map, const void* base, uint64_t groups, uint64_t chunks,
+                                 uint64_t row_bytes, uint32_t box_groups, uint32_t box_chunks);
+
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, bool out_f16, cudaStream_t stream);
 size_t paged_attn_workspace_bytes();

@@ -387,6 +387,14 @@ MLA_DEVINL void st_async_b32(uint32_t remote_addr, uint32_t v, uint32_t remote_b
                : "memory");
 }
 
+MLA_DEVINL void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // `bytes` of this CTA's shared memory to the peer's, counted on its barrier.
 MLA_DEVINL void bulk_to_peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -1298,9 +1306,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             tc::tma_load_3d(sScale + ls * kRawScale + j * box * 16, &tm_scale, full, kE4m3ScaleOff / 2, row, 0);
         } else if (staged) {
           if (lane == 0)
-            tc::tma_load_4d(dst, &tm_lat, full, 0, 0, c0, staged_row(a, it, base, it.key_tile(t)) / 8);
+            tma_load_4d(dst, &tm_lat, full, 0, 0, c0, staged_row(a, it, base, it.key_tile(t)) / 8);
         } else if (mine && ch == 1) {
-          tc::tma_load_4d(dst + j * box / 8 * kGroup, &tm_lat, full, 0, 0, c0, row / 8);
+          tma_load_4d(dst + j * box / 8 * kGroup, &tm_lat, full, 0, 0, c0, row / 8);
         }
         if (kE4m3) load_rope();
         if (!ok) break;

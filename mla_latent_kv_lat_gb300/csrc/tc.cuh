@@ -214,14 +214,6 @@ MLA_DEVINL void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, in
       : "memory");
 }
 
-MLA_DEVINL void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Bring `bytes` (multiple of 16) of global memory at `p` (16-byte aligned)
 // into L2 without waiting.
 MLA_DEVINL void prefetch_l2(const void* p, uint32_t bytes) {

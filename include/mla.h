@@ -439,6 +439,107 @@ int mla_attn_paged(const mla_dims* dims, const void* q_lat, const void* q_pe,
                    int32_t B, int32_t T, int32_t window, int32_t n_sink, void* workspace,
                    size_t ws_bytes, void* o_lat, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Normed append, and attention over chosen blocks of a paged cache
+ * ---------------------------------------------------------------------------
+ * Build choices for serving, as the paged cache.  The first call makes a
+ * step's queries and cache rows out of the projections' outputs; the others
+ * let each token attend to a few blocks of 64 positions instead of its whole
+ * context: a mean row for each complete block, a score of each block from it,
+ * the choice, and the attention over what was chosen (or over any other list).
+ * Block j of a sequence holds its positions 64 j .. 64 j + 63 and lies in one
+ * page: the block calls want page_size >= 64 (MLA_ERR_UNSUPPORTED).  Batches,
+ * padding, invalid sequences and overlapping memory as above: what a call
+ * writes (marked "out") must not overlap what it reads nor its other outputs.
+ * The order of every sum depends on the arguments and the batch alone.        */
+
+/* Queries and keys of the batch's new tokens, normed and rotated, the keys
+ * into their pages, in one pass:
+ *   q[t][h]  = [nope 128 | rope 64]; with q_weight, x = q * rsqrt(mean(q^2) + eps)
+ *              * q_weight over its 192 values, else x = q;
+ *              q_nope[t][h] <- x[0..127], q_pe[t][h] <- RoPE(x[128..191], position)
+ *   kv[t]    = [latent 512 | rope 64]; row of token t <- [latent * rsqrt(mean(latent^2)
+ *              + eps) * kv_weight | RoPE(rope, position)]
+ * Rows, positions and RoPE as in mla_paged_append; what it feeds next are
+ * mla_absorb_q (q_nope) and the paged attentions (q_pe).
+ * q  device bf16: head h of token t at q + t * q_token_stride + h * q_head_stride
+ *    (elements; multiples of 8, else MLA_ERR_MISALIGNED), its 192 values
+ *    contiguous; kv device bf16, token t at kv + t * kv_token_stride, 576
+ *    contiguous.  A slice of a wider projection will do; strides may be 0.
+ * q_weight device bf16 [192] or NULL; kv_weight device bf16 [512].
+ * out: q_nope device bf16 [T][H][128]; q_pe device bf16 [T][H][64]; the pages.
+ * Sums of squares, products and rotations are fp32; every value is rounded
+ * once, to bf16 or to the page's type (e4m3: scales and codes are of the fp32
+ * latents).  Values that a row cannot hold record MLA_ERR_RANGE, as there.
+ * A token whose table entry is bad gets no row, and is recorded; its queries
+ * are written.  Two tokens of one call must not name the same row.
+ * Host errors: eps not finite and > 0, frequencies as in mla_rope_append.     */
+int mla_paged_norm_append(const mla_dims* dims, const void* q, int64_t q_token_stride,
+                          int64_t q_head_stride, const void* kv, int64_t kv_token_stride,
+                          const void* q_weight, const void* kv_weight, const mla_paged_cache* cache,
+                          const int32_t* cu_new, const int32_t* seq_len, int32_t B, int32_t T,
+                          float eps, float freq_base, float freq_scale, void* q_nope, void* q_pe,
+                          void* stream);
+
+/* Entries of a token's list of blocks, at most. */
+#define MLA_MAX_BLOCKS 1024
+
+/* Mean rows of the blocks that the batch's new tokens complete (whose last
+ * position is one of theirs): the mean of a block's 64 rows as the pages hold
+ * them, summed in fp32, rounded once to fp16.  Call it after the append.
+ * block_keys, out: device fp16 [n_pages][page_size / 64][576]: they lie as the
+ * pages do, so that sequences that share a page share its mean rows.
+ * T bounds the new tokens, as the token arrays of the other calls do.  A block
+ * whose table entry is bad is skipped and recorded.                           */
+int mla_paged_block_keys(const mla_paged_cache* cache, const int32_t* cu_new, const int32_t* seq_len,
+                         int32_t B, int32_t T, void* block_keys, void* stream);
+
+/* Scores of the blocks before each new token's own: for a token at position p
+ *   scores[t][j] = scale * max over heads h of
+ *                  (q_lat[t][h] . block_keys[j][0..511] + q_pe[t][h] . block_keys[j][512..575])
+ * for j < p / 64 (block j of the token's sequence), -inf for p / 64 <= j < n_scores.
+ * q_lat, q_pe as in mla_attn_paged.  cache: its table and sizes; its pages and
+ * type are not looked at.  The mean rows of these blocks must be there and finite.
+ * scores, out: device fp32, row t at scores + t * score_stride, n_scores of
+ * each row (score_stride >= n_scores).  A token at a position of 64 * (n_scores + 1) or
+ * behind has blocks without a score: recorded as MLA_ERR_INVALID_ARG.
+ * q_pe becomes fp16 (as in mla_attn_paged); products and sums are fp32.       */
+int mla_paged_block_scores(const mla_dims* dims, const void* q_lat, const void* q_pe,
+                           const mla_paged_cache* cache, const void* block_keys, const int32_t* cu_q,
+                           const int32_t* seq_len, int32_t B, int32_t T, float* scores,
+                           int64_t score_stride, int32_t n_scores, void* stream);
+
+/* The choice: a token at position p takes its own block p / 64, the n_local - 1
+ * before it and the first n_sink, and of the others before its own those with
+ * the largest scores, up to K blocks in all (all, if there are no more).
+ * Equal scores: the lower block first; a NaN ranks below -inf.
+ * out: blocks device int32 [T][K], a token's in ascending order, -1 behind
+ * them; counts device int32 [T].
+ * scores as mla_paged_block_scores leaves them (those of the first, the last and later
+ * blocks are not looked at).  1 <= K <= MLA_MAX_BLOCKS, n_sink >= 0, n_local >= 1,
+ * n_sink + n_local <= K.  A token whose own block is not below n_scores gets no
+ * block, and is recorded as MLA_ERR_INVALID_ARG.                              */
+int mla_paged_select_blocks(const float* scores, int64_t score_stride, int32_t n_scores,
+                            const int32_t* cu_q, const int32_t* seq_len, int32_t B, int32_t T,
+                            int32_t n_sink, int32_t n_local, int32_t* blocks, int32_t* counts,
+                            int32_t K, void* stream);
+
+/* mla_attn_paged over listed blocks: a token at position p sees key j iff
+ * j <= p and one of blocks[t][0 .. counts[t] - 1] is j / 64.  In any order; a block
+ * listed twice counts twice.  A token that sees no key (counts[t] == 0) gets
+ * zeros.
+ * blocks device int32 [T][K], 1 <= K <= MLA_MAX_BLOCKS; counts device int32 [T].
+ * An entry below 0 or above p / 64 adds nothing and is recorded as
+ * MLA_ERR_INVALID_ARG; a count outside [0, K] is recorded and taken as the
+ * nearer of the two.
+ * Only pages with a listed block need a valid table entry, and only the rows
+ * that some token sees need finite values.  Everything else as there: types, workspace,
+ * roundings, errors.                                                          */
+int mla_attn_paged_blocks(const mla_dims* dims, const void* q_lat, const void* q_pe,
+                          const mla_paged_cache* cache, const int32_t* cu_q, const int32_t* seq_len,
+                          int32_t B, int32_t T, const int32_t* blocks, const int32_t* counts,
+                          int32_t K, void* workspace, size_t ws_bytes, void* o_lat, void* stream);
+
 /* Synchronise `stream`, then return and clear the current device's error
  * word: MLA_OK, or the first device-side error recorded since the last call
  * (MLA_ERR_TIMEOUT from a bounded wait, MLA_ERR_INVALID_ARG from the slot

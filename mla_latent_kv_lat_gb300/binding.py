@@ -22,6 +22,7 @@ KV_LORA_RANK, QK_ROPE, QK_NOPE, V_HEAD, ROW = 512, 64, 128, 128, 576
 Q8_BLOCKS = 18
 ROW_E4M3 = 656                    # bytes of a paged e4m3 row: 512 codes, 64 fp16, 16 scales
 PAGE_F16, PAGE_E4M3 = 0, 1
+BLOCK = 64                        # positions of a block that block-sparse attention chooses
 
 STATUS = {0: "MLA_OK", -1: "MLA_ERR_INVALID_ARG", -2: "MLA_ERR_UNSUPPORTED", -3: "MLA_ERR_MISALIGNED",
           -4: "MLA_ERR_WORKSPACE", -5: "MLA_ERR_CUDA", -6: "MLA_ERR_TIMEOUT", -7: "MLA_ERR_RANGE"}
@@ -80,6 +81,12 @@ _SIGS = {
     "mla_paged_gather": ([_C, _P, _P, _I32, _I32, _P, _I32, _P], ctypes.c_int),
     "mla_paged_workspace_size": ([_D], _SZ),
     "mla_attn_paged": ([_D, _P, _P, _C, _P, _P, _I32, _I32, _I32, _I32, _P, _SZ, _P, _P], ctypes.c_int),
+    "mla_paged_norm_append": ([_D, _P, _I64, _I64, _P, _I64, _P, _P, _C, _P, _P, _I32, _I32, ctypes.c_float, ctypes.c_float,
+                               ctypes.c_float, _P, _P, _P], ctypes.c_int),
+    "mla_paged_block_keys": ([_C, _P, _P, _I32, _I32, _P, _P], ctypes.c_int),
+    "mla_paged_block_scores": ([_D, _P, _P, _C, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _P], ctypes.c_int),
+    "mla_paged_select_blocks": ([_P, _I64, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _I32, _P], ctypes.c_int),
+    "mla_attn_paged_blocks": ([_D, _P, _P, _C, _P, _P, _I32, _I32, _P, _P, _I32, _P, _SZ, _P, _P], ctypes.c_int),
     "mla_get_device_error": ([_P], ctypes.c_int),
     "mla_selftest_wait_timeout": ([_I32, _P], ctypes.c_int),
     "mla_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -476,6 +483,154 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
         workspace.numel(),
         _arg(o_lat, "o_lat", torch.float16, (T, H, KV_LORA_RANK), dev), _stream_on(stream, dev))
     _check("mla_attn_paged", st)
+
+
+def _fit(value: int, name: str) -> int:
+    """A Python integer that the C call takes as int32 (ctypes would take its low 32 bits)."""
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name} ({value}) must be int32")
+    return value
+
+
+def _strided(t, name: str, dtype, shape, dev: int) -> int:
+    """Device address of a tensor of this type and shape on CUDA device ``dev``, contiguous in its last dimension."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, another tensor on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr()
+
+
+def mla_paged_norm_append(q, kv, q_weight, kv_weight, pages, block_table, cu_new, seq_len, q_nope, q_pe, eps: float = 1e-6,
+                          freq_base: float = 10000.0, freq_scale: float = 0.025, stream=None):
+    """The projections' outputs of new tokens made ready: q [T, H, 192] (RMS-normed over each head if ``q_weight`` [192]
+    is given) into q_nope [T, H, 128] and the rotated q_pe [T, H, 64]; kv [T, 576] into the tokens' rows, its latent
+    RMS-normed with ``kv_weight`` [512], its RoPE part rotated.  q and kv may be slices of wider tensors (last
+    dimension contiguous, other strides multiples of 8)."""
+    dev = paged_device(q, "q")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return mla_paged_norm_append(q, kv, q_weight, kv_weight, pages, block_table, cu_new, seq_len, q_nope, q_pe, eps,
+                                         freq_base, freq_scale, stream)
+    cache = _paged(pages, block_table, dev)
+    if q.dim() != 3:
+        raise ValueError(f"q must have shape (T, H, {QK_NOPE + QK_ROPE}), got {tuple(q.shape)}")
+    (T, H, _), Bn, bf16 = q.shape, block_table.shape[0], torch.bfloat16
+    qp, kvp = _strided(q, "q", bf16, (T, H, QK_NOPE + QK_ROPE), dev), _strided(kv, "kv", bf16, (T, ROW), dev)
+    # (the stride of a dimension of one counts for nothing, and may be anything)
+    qt, kt, qh = q.stride(0) if T > 1 else 0, kv.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0
+    st = load_library().mla_paged_norm_append(
+        _dims(H, None), qp, qt, qh, kvp, kt,
+        _arg(q_weight, "q_weight", bf16, (QK_NOPE + QK_ROPE,), dev) if q_weight is not None else None,
+        _arg(kv_weight, "kv_weight", bf16, (KV_LORA_RANK,), dev), cache, _arg(cu_new, "cu_new", torch.int32, (Bn + 1,), dev),
+        _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn, T, eps, freq_base, freq_scale,
+        _arg(q_nope, "q_nope", bf16, (T, H, QK_NOPE), dev), _arg(q_pe, "q_pe", bf16, (T, H, QK_ROPE), dev),
+        _stream_on(stream, dev))
+    _check("mla_paged_norm_append", st)
+
+
+def _block_keys(block_keys, n_pages: int, page_size: int, dev: int) -> int:
+    return _arg(block_keys, "block_keys", torch.float16, (n_pages, page_size // BLOCK, ROW), dev)
+
+
+def mla_paged_block_keys(pages, block_table, cu_new, seq_len, block_keys, T: int, stream=None):
+    """Mean rows of the blocks of 64 positions that the batch's new tokens (at most T, their rows appended) complete,
+    into block_keys fp16 [n_pages, page_size / 64, 576]."""
+    dev = paged_device(pages, "pages")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return mla_paged_block_keys(pages, block_table, cu_new, seq_len, block_keys, T, stream)
+    cache, Bn = _paged(pages, block_table, dev), block_table.shape[0]
+    st = load_library().mla_paged_block_keys(
+        cache, _arg(cu_new, "cu_new", torch.int32, (Bn + 1,), dev), _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn,
+        _fit(T, "T"), _block_keys(block_keys, pages.shape[0], pages.shape[1], dev), _stream_on(stream, dev))
+    _check("mla_paged_block_keys", st)
+
+
+def _rows_f32(scores, T, dev: int):
+    """(address, row stride, width) of fp32 scores [T, n_scores] whose rows may be further apart."""
+    if not isinstance(scores, torch.Tensor) or scores.dim() != 2 or scores.shape[0] != T or scores.shape[1] < 1:
+        raise ValueError(f"scores must have shape ({T}, n_scores)")
+    return _strided(scores, "scores", torch.float32, scores.shape, dev), scores.stride(0), scores.shape[1]
+
+
+def mla_paged_block_scores(q_lat, q_pe, block_keys, block_table, cu_q, seq_len, scores, scale=None, stream=None):
+    """scores fp32 [T, n_scores]: for each new token and each block j before its own, scale times the largest head's
+    product with the block's mean row (block_keys); -inf from its own block on."""
+    dev = paged_device(q_lat, "q_lat")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return mla_paged_block_scores(q_lat, q_pe, block_keys, block_table, cu_q, seq_len, scores, scale, stream)
+    if q_lat.dim() != 3:
+        raise ValueError(f"q_lat must have shape (T, H, {KV_LORA_RANK}), got {tuple(q_lat.shape)}")
+    if not isinstance(block_keys, torch.Tensor) or block_keys.dim() != 3 or block_keys.shape[2] != ROW:
+        raise ValueError(f"block_keys must have shape (n_pages, page_size / {BLOCK}, {ROW})")
+    if block_keys.dtype is not torch.float16:
+        raise TypeError(f"block_keys must be torch.float16, got {block_keys.dtype}")
+    (T, H, _), Bn = q_lat.shape, block_table.shape[0]
+    n_pages, page_size = block_keys.shape[0], BLOCK * block_keys.shape[1]
+    cache = _paged(block_keys, block_table, dev)         # (its pages are not read)
+    cache.page_size = page_size
+    sp, stride, width = _rows_f32(scores, T, dev)
+    st = load_library().mla_paged_block_scores(
+        _dims(H, scale if scale is None else float(scale)), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
+        _arg(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE), dev), cache, _block_keys(block_keys, n_pages, page_size, dev),
+        _arg(cu_q, "cu_q", torch.int32, (Bn + 1,), dev), _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn, T, sp,
+        stride, width, _stream_on(stream, dev))
+    _check("mla_paged_block_scores", st)
+
+
+def mla_paged_select_blocks(scores, cu_q, seq_len, blocks, counts, n_sink: int = 1, n_local: int = 1, stream=None):
+    """blocks int32 [T, K] and counts int32 [T]: each new token's own block, the n_local - 1 before it, the first
+    n_sink, and the best-scored others up to K; ascending, -1 behind."""
+    dev = paged_device(scores, "scores")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return mla_paged_select_blocks(scores, cu_q, seq_len, blocks, counts, n_sink, n_local, stream)
+    if not isinstance(blocks, torch.Tensor) or blocks.dim() != 2:
+        raise ValueError("blocks must have shape (T, K)")
+    (T, K), Bn = blocks.shape, seq_len.shape[0]
+    sp, stride, width = _rows_f32(scores, T, dev)
+    st = load_library().mla_paged_select_blocks(
+        sp, stride, width, _arg(cu_q, "cu_q", torch.int32, (Bn + 1,), dev), _arg(seq_len, "seq_len", torch.int32, (Bn,), dev),
+        Bn, T, _fit(n_sink, "n_sink"), _fit(n_local, "n_local"), _arg(blocks, "blocks", torch.int32, (T, K), dev),
+        _arg(counts, "counts", torch.int32, (T,), dev), K, _stream_on(stream, dev))
+    _check("mla_paged_select_blocks", st)
+
+
+def mla_attn_paged_blocks(q_lat, q_pe, pages, block_table, cu_q, seq_len, blocks, counts, o_lat, workspace=None, scale=None,
+                          stream=None):
+    """o_lat [T, H, 512]: mla_attn_paged over the rows of each token's listed blocks (blocks int32 [T, K], of which the
+    first counts[t] of row t count).  Without a workspace a fresh one is taken from PyTorch's allocator."""
+    dev = paged_device(q_lat, "q_lat")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return mla_attn_paged_blocks(q_lat, q_pe, pages, block_table, cu_q, seq_len, blocks, counts, o_lat, workspace,
+                                         scale, stream)
+    cache = _paged(pages, block_table, dev)
+    if q_lat.dim() != 3:
+        raise ValueError(f"q_lat must have shape (T, H, {KV_LORA_RANK}), got {tuple(q_lat.shape)}")
+    (T, H, _), Bn = q_lat.shape, block_table.shape[0]
+    if not isinstance(blocks, torch.Tensor) or blocks.dim() != 2:
+        raise ValueError(f"blocks must have shape ({T}, K)")
+    K = blocks.shape[1]
+    if workspace is None:
+        with stream_context(stream, dev):
+            workspace = torch.empty(mla_paged_workspace_size(H, scale), dtype=torch.uint8, device=q_lat.device)
+    st = load_library().mla_attn_paged_blocks(
+        _dims(H, scale if scale is None else float(scale)), _arg(q_lat, "q_lat", torch.float16, (T, H, KV_LORA_RANK), dev),
+        _arg(q_pe, "q_pe", torch.bfloat16, (T, H, QK_ROPE), dev), cache, _arg(cu_q, "cu_q", torch.int32, (Bn + 1,), dev),
+        _arg(seq_len, "seq_len", torch.int32, (Bn,), dev), Bn, T, _arg(blocks, "blocks", torch.int32, (T, K), dev),
+        _arg(counts, "counts", torch.int32, (T,), dev), K,
+        _arg(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev), workspace.numel(),
+        _arg(o_lat, "o_lat", torch.float16, (T, H, KV_LORA_RANK), dev), _stream_on(stream, dev))
+    _check("mla_attn_paged_blocks", st)
 
 
 def mla_get_device_error(stream=None) -> int:

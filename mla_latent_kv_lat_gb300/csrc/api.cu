@@ -260,6 +260,66 @@ void rope_turns(float freq_base, float freq_scale, uint64_t* turn) {
   memcpy(turn, table, sizeof(table));
 }
 
+Span keys_span(const PagedCache& c, const void* keys) {
+  return {keys, (static_cast<int64_t>(c.n_pages) << c.page_shift) / kBlockRows * kRow * 2};
+}
+
+// What a call with blocks of positions needs of its cache and lists.
+int check_blocks(const mla_paged_cache* cache, std::initializer_list<const int32_t*> lists, int32_t K) {
+  if (cache == nullptr || K < 1) return MLA_ERR_INVALID_ARG;
+  int s = check_i32(lists);
+  if (s != MLA_OK) return s;
+  return cache->page_size < kBlockRows || K > MLA_MAX_BLOCKS ? MLA_ERR_UNSUPPORTED : MLA_OK;
+}
+
+// Attention over pages: blocks null for all (or a window's) rows, else the blocks listed for each token.
+int attn_paged(const mla_dims* dims, const void* q_lat, const void* q_pe, const mla_paged_cache* cache,
+               const int32_t* cu_q, const int32_t* seq_len, int32_t B, int32_t T, int32_t window, int32_t n_sink,
+               const int32_t* blocks, const int32_t* counts, int32_t K, void* workspace, size_t ws_bytes, void* o_lat,
+               void* stream) {
+  int s = check_dims(dims);
+  if (s != MLA_OK) return s;
+  PagedAttnArgs a = {};
+  s = check_paged(cache, B, &a.c);
+  if (s != MLA_OK) return s;
+  s = check_ptrs({q_lat, q_pe, o_lat});
+  if (s != MLA_OK) return s;
+  s = check_i32({cu_q, seq_len});
+  if (s != MLA_OK) return s;
+  if (T < 1 || window < 0 || n_sink < 0) return MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) * dims->n_head > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  // what the clusters read while others of them write
+  const int64_t rows = int64_t{T} * dims->n_head;
+  const Span o = {o_lat, rows * kLatent * 2}, q = {q_lat, rows * kLatent * 2};
+  if (overlap(o, {q})) return MLA_ERR_INVALID_ARG;
+  if (workspace == nullptr || ws_bytes < paged_attn_workspace_bytes()) return MLA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MLA_ERR_MISALIGNED;
+  const Span ws = {workspace, static_cast<int64_t>(paged_attn_workspace_bytes())};
+  for (const Span& w : {o, ws})
+    if (overlap(w, {{q_pe, rows * kRope * 2}, pages_span(a.c), table_span(a.c, B), i32_span(cu_q, int64_t{B} + 1),
+                    i32_span(seq_len, B), i32_span(blocks, int64_t{T} * K), i32_span(counts, blocks ? T : 0)}))
+      return MLA_ERR_INVALID_ARG;
+  if (overlap(ws, {o, q})) return MLA_ERR_INVALID_ARG;
+  a.q_lat = static_cast<const uint16_t*>(q_lat);
+  a.q_pe = static_cast<const uint16_t*>(q_pe);
+  a.cu = cu_q;
+  a.seq_len = seq_len;
+  a.B = B;
+  a.T = T;
+  a.H = dims->n_head;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.blocks = blocks;
+  a.counts = counts;
+  a.K = K;
+  a.scale_log2 = dims->scale * kLog2eF;
+  a.o_lat = static_cast<uint16_t*>(o_lat);
+  a.workspace = workspace;
+  a.wait_us = kDefaultWaitUs;
+  if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
+  return to_status(launch_paged_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace mla
 
@@ -504,44 +564,150 @@ size_t mla_paged_workspace_size(const mla_dims* dims) {
 int mla_attn_paged(const mla_dims* dims, const void* q_lat, const void* q_pe, const mla_paged_cache* cache,
                    const int32_t* cu_q, const int32_t* seq_len, int32_t B, int32_t T, int32_t window, int32_t n_sink,
                    void* workspace, size_t ws_bytes, void* o_lat, void* stream) {
+  return attn_paged(dims, q_lat, q_pe, cache, cu_q, seq_len, B, T, window, n_sink, nullptr, nullptr, 0, workspace, ws_bytes,
+                    o_lat, stream);
+}
+
+int mla_attn_paged_blocks(const mla_dims* dims, const void* q_lat, const void* q_pe, const mla_paged_cache* cache,
+                          const int32_t* cu_q, const int32_t* seq_len, int32_t B, int32_t T, const int32_t* blocks,
+                          const int32_t* counts, int32_t K, void* workspace, size_t ws_bytes, void* o_lat, void* stream) {
+  int s = check_blocks(cache, {blocks, counts}, K);
+  if (s != MLA_OK) return s;
+  return attn_paged(dims, q_lat, q_pe, cache, cu_q, seq_len, B, T, 0, 0, blocks, counts, K, workspace, ws_bytes, o_lat,
+                    stream);
+}
+
+int mla_paged_norm_append(const mla_dims* dims, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                          const void* kv, int64_t kv_token_stride, const void* q_weight, const void* kv_weight,
+                          const mla_paged_cache* cache, const int32_t* cu_new, const int32_t* seq_len, int32_t B, int32_t T,
+                          float eps, float freq_base, float freq_scale, void* q_nope, void* q_pe, void* stream) {
   int s = check_dims(dims);
   if (s != MLA_OK) return s;
-  PagedAttnArgs a = {};
+  NormAppendArgs a = {};
   s = check_paged(cache, B, &a.c);
   if (s != MLA_OK) return s;
-  s = check_ptrs({q_lat, q_pe, o_lat});
+  s = check_ptrs({q, kv, kv_weight, q_nope, q_pe});
   if (s != MLA_OK) return s;
-  s = check_i32({cu_q, seq_len});
+  if (q_weight != nullptr && !aligned16(q_weight)) return MLA_ERR_MISALIGNED;
+  s = check_i32({cu_new, seq_len});
   if (s != MLA_OK) return s;
-  if (T < 1 || window < 0 || n_sink < 0) return MLA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(T) * dims->n_head > INT32_MAX) return MLA_ERR_UNSUPPORTED;
-  // what the clusters read while others of them write
-  const int64_t rows = int64_t{T} * dims->n_head;
-  const Span o = {o_lat, rows * kLatent * 2}, q = {q_lat, rows * kLatent * 2};
-  if (overlap(o, {q})) return MLA_ERR_INVALID_ARG;
-  if (workspace == nullptr || ws_bytes < paged_attn_workspace_bytes()) return MLA_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return MLA_ERR_MISALIGNED;
-  const Span ws = {workspace, static_cast<int64_t>(paged_attn_workspace_bytes())};
-  for (const Span& w : {o, ws})
-    if (overlap(w, {{q_pe, rows * kRope * 2}, pages_span(a.c), table_span(a.c, B), i32_span(cu_q, int64_t{B} + 1),
-                    i32_span(seq_len, B)}))
+  if (T < 1 || q_token_stride < 0 || q_head_stride < 0 || kv_token_stride < 0) return MLA_ERR_INVALID_ARG;
+  if (q_token_stride % 8 != 0 || q_head_stride % 8 != 0 || kv_token_stride % 8 != 0) return MLA_ERR_MISALIGNED;
+  if (!(eps > 0.f) || !isfinite(eps)) return MLA_ERR_INVALID_ARG;
+  if (!(freq_base > 1.f) || !(freq_scale > 0.f) || !isfinite(freq_base) || !isfinite(freq_scale))
+    return MLA_ERR_INVALID_ARG;
+  const int64_t H = dims->n_head, rows = int64_t{T} * H;
+  if (rows > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  const int64_t most = int64_t{1} << 40;      // elements: no span below overflows
+  if (q_token_stride > most / T || q_head_stride > most / H || kv_token_stride > most / T) return MLA_ERR_UNSUPPORTED;
+  const Span in_q = {q, 2 * ((T - 1) * q_token_stride + (H - 1) * q_head_stride + kNope + kRope)};
+  const Span in_kv = {kv, 2 * ((T - 1) * kv_token_stride + kRow)};
+  const Span out[3] = {{q_nope, rows * kNope * 2}, {q_pe, rows * kRope * 2}, pages_span(a.c)};
+  for (int i = 0; i < 3; ++i)
+    if (overlap(out[i], {in_q, in_kv, {q_weight, q_weight ? 2 * (kNope + kRope) : 0}, {kv_weight, 2 * kLatent},
+                         table_span(a.c, B), i32_span(cu_new, int64_t{B} + 1), i32_span(seq_len, B), out[(i + 1) % 3]}))
       return MLA_ERR_INVALID_ARG;
-  if (overlap(ws, {o, q})) return MLA_ERR_INVALID_ARG;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.kv = static_cast<const uint16_t*>(kv);
+  a.kv_token = kv_token_stride;
+  a.q_weight = static_cast<const uint16_t*>(q_weight);
+  a.kv_weight = static_cast<const uint16_t*>(kv_weight);
+  a.cu = cu_new;
+  a.seq_len = seq_len;
+  a.B = B;
+  a.T = T;
+  a.H = dims->n_head;
+  a.eps = eps;
+  a.q_nope = static_cast<uint16_t*>(q_nope);
+  a.q_pe = static_cast<uint16_t*>(q_pe);
+  if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
+  rope_turns(freq_base, freq_scale, a.turn);
+  return to_status(launch_norm_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_paged_block_keys(const mla_paged_cache* cache, const int32_t* cu_new, const int32_t* seq_len, int32_t B,
+                         int32_t T, void* block_keys, void* stream) {
+  BlockKeysArgs a = {};
+  int s = check_paged(cache, B, &a.c);
+  if (s != MLA_OK) return s;
+  if (cache->page_size < kBlockRows) return MLA_ERR_UNSUPPORTED;
+  s = check_ptrs({block_keys});
+  if (s != MLA_OK) return s;
+  s = check_i32({cu_new, seq_len});
+  if (s != MLA_OK) return s;
+  if (T < 1) return MLA_ERR_INVALID_ARG;
+  if (overlap(keys_span(a.c, block_keys), {pages_span(a.c), table_span(a.c, B), i32_span(cu_new, int64_t{B} + 1),
+                                           i32_span(seq_len, B)}))
+    return MLA_ERR_INVALID_ARG;
+  a.cu = cu_new;
+  a.seq_len = seq_len;
+  a.B = B;
+  a.T = T;
+  a.keys = static_cast<uint16_t*>(block_keys);
+  if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
+  return to_status(launch_block_keys(a, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_paged_block_scores(const mla_dims* dims, const void* q_lat, const void* q_pe, const mla_paged_cache* cache,
+                           const void* block_keys, const int32_t* cu_q, const int32_t* seq_len, int32_t B, int32_t T,
+                           float* scores, int64_t score_stride, int32_t n_scores, void* stream) {
+  int s = check_dims(dims);
+  if (s != MLA_OK) return s;
+  BlockScoresArgs a = {};
+  s = check_ptrs({q_lat, q_pe, block_keys});
+  if (s != MLA_OK) return s;
+  if (cache == nullptr) return MLA_ERR_INVALID_ARG;
+  mla_paged_cache c = *cache;                // (its pages are not read)
+  c.pages = const_cast<void*>(block_keys);
+  c.type = MLA_PAGE_F16;
+  s = check_paged(&c, B, &a.c);
+  if (s != MLA_OK) return s;
+  if (c.page_size < kBlockRows) return MLA_ERR_UNSUPPORTED;
+  s = check_i32({cu_q, seq_len, reinterpret_cast<const int32_t*>(scores)});
+  if (s != MLA_OK) return s;
+  if (T < 1 || n_scores < 1 || score_stride < 0 || (T > 1 && score_stride < n_scores)) return MLA_ERR_INVALID_ARG;
+  const int64_t rows = int64_t{T} * dims->n_head;
+  if (rows > INT32_MAX || score_stride > (int64_t{1} << 40) / T) return MLA_ERR_UNSUPPORTED;
+  if (overlap({scores, 4 * ((T - 1) * score_stride + n_scores)},
+              {{q_lat, rows * kLatent * 2}, {q_pe, rows * kRope * 2}, keys_span(a.c, block_keys), table_span(a.c, B),
+               i32_span(cu_q, int64_t{B} + 1), i32_span(seq_len, B)}))
+    return MLA_ERR_INVALID_ARG;
   a.q_lat = static_cast<const uint16_t*>(q_lat);
   a.q_pe = static_cast<const uint16_t*>(q_pe);
+  a.keys = static_cast<const uint16_t*>(block_keys);
   a.cu = cu_q;
   a.seq_len = seq_len;
   a.B = B;
   a.T = T;
   a.H = dims->n_head;
-  a.window = window;
-  a.n_sink = n_sink;
-  a.scale_log2 = dims->scale * kLog2eF;
-  a.o_lat = static_cast<uint16_t*>(o_lat);
-  a.workspace = workspace;
+  a.W = n_scores;
+  a.scale = dims->scale;
+  a.scores = scores;
+  a.stride = score_stride;
   a.wait_us = kDefaultWaitUs;
   if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
-  return to_status(launch_paged_attn(a, static_cast<cudaStream_t>(stream)));
+  return to_status(launch_block_scores(a, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_paged_select_blocks(const float* scores, int64_t score_stride, int32_t n_scores, const int32_t* cu_q,
+                            const int32_t* seq_len, int32_t B, int32_t T, int32_t n_sink, int32_t n_local, int32_t* blocks,
+                            int32_t* counts, int32_t K, void* stream) {
+  int s = check_i32({reinterpret_cast<const int32_t*>(scores), cu_q, seq_len, blocks, counts});
+  if (s != MLA_OK) return s;
+  if (B < 1 || T < 1 || n_scores < 1 || K < 1 || n_sink < 0 || n_local < 1) return MLA_ERR_INVALID_ARG;
+  if (score_stride < 0 || (T > 1 && score_stride < n_scores)) return MLA_ERR_INVALID_ARG;
+  if (int64_t{n_sink} + n_local > K) return MLA_ERR_INVALID_ARG;
+  if (B > 65535 || K > MLA_MAX_BLOCKS || score_stride > (int64_t{1} << 40) / T) return MLA_ERR_UNSUPPORTED;
+  const Span out[2] = {i32_span(blocks, int64_t{T} * K), i32_span(counts, T)};
+  for (int i = 0; i < 2; ++i)
+    if (overlap(out[i], {{scores, 4 * ((T - 1) * score_stride + n_scores)}, i32_span(cu_q, int64_t{B} + 1),
+                         i32_span(seq_len, B), out[1 - i]}))
+      return MLA_ERR_INVALID_ARG;
+  SelectBlocksArgs a = {scores, score_stride, cu_q, seq_len, B, T, n_scores, K, n_sink, n_local, blocks, counts, nullptr};
+  if (error_word(&a.err) != cudaSuccess) return MLA_ERR_CUDA;
+  return to_status(launch_select_blocks(a, static_cast<cudaStream_t>(stream)));
 }
 
 int mla_get_device_error(void* stream) {

@@ -1,0 +1,440 @@
+// The cheap score by which block-sparse attention chooses: for a token at position p
+// and each block j < p / 64 of 64 positions before its own
+//
+//   score[t][j] = scale * max_h (q_lat[t][h] . kbar[j][0..511] + q_pe[t][h] . kbar[j][512..575])
+//
+// with kbar[j] the block's mean row; -inf for the others.
+//
+// On the 5th-generation tensor cores with the blocks as rows (M = 128) and the
+// queries of `gt` tokens, H each, as columns (N = gt H <= 128): the largest head of a
+// block then is a maximum over one thread's registers, with no exchange.
+//   * A work item is 128 blocks of one sequence and a run of its new tokens.  The mean
+//     rows' latent part stays in tensor memory (256 columns), the RoPE part in shared
+//     memory; queries stream through a ring of 16 KB stages by TMA.  (With the rows in
+//     shared memory, both operands of each product would come from there: 128 bytes a
+//     cycle, all it has.)
+//   * Mean rows lie with their pages: four warps gather them with 16-byte asynchronous
+//     copies, 64 dims at a time, and move them into tensor memory.  The same warps turn
+//     q_pe (bf16) into fp16, the type of the mean rows.
+//   * Two accumulators of 128 columns: four warps reduce one while the next is filled.
+#include <atomic>
+
+#include "kernels.cuh"
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kTile = 128;                   // blocks of an item (MMA M)
+constexpr int kMaxN = 128;                   // (token, head) columns
+constexpr int kChunk = 128 * 128;            // 128 rows x 64 fp16
+constexpr int kChunks = kLatent / 64;
+constexpr int kStages = 8, kFeed = 4;
+constexpr int kOffKr = 0;                                    // the mean rows' RoPE part
+constexpr int kOffFeed = kOffKr + kChunk;                    // mean rows on their way; two of them hold q_pe, too
+constexpr int kOffRing = kOffFeed + kFeed * kChunk;
+constexpr int kOffBar = kOffRing + kStages * kChunk;
+constexpr int kSmem = 1024 + kOffBar + 256;
+static_assert(kSmem <= 232448, "shared memory");
+
+constexpr int kFeedWarp = 4, kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
+constexpr int kBarFeed = 1;
+constexpr uint32_t kTmK = 0, kTmS = 256;
+constexpr uint64_t kGaveUpNs = 200000;       // from a wait that ran out to the CTA's end
+
+struct Args {
+  BlockScoresArgs p;
+  int32_t gt;          // tokens of a group
+  int32_t tiles;       // of a row of scores
+  int32_t n_slots;     // groups, at most
+  int32_t per;         // of them a CTA takes
+};
+
+struct Bars {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t k_full, k_free;             // the item's mean rows are there; its last product is done
+  uint64_t qr_full[2], qr_empty[2];
+  uint64_t s_full[2], s_empty[2];
+  uint32_t tmem;
+};
+static_assert(sizeof(Bars) <= 256, "barriers");
+
+// Sequence b's groups get slots cu[b] / gt + b, ... (their ranges do not overlap).
+MLA_DEVINL int32_t slot_of_seq(const Args& a, int b) {
+  return max(0, min(a.p.T, __ldg(a.p.cu + b))) / a.gt + b;
+}
+
+struct Group {
+  int32_t b, t0, nt;                   // tokens [t0, t0 + nt)
+  int32_t pos;                         // of the first
+  bool live;                           // some token has a block in the tile
+  bool fresh;                          // the first live one of its sequence here: mean rows are loaded
+};
+
+// This CTA's groups in order; every role walks the same ones.  Whole warps.
+struct Walk {
+  int32_t g, g1, b, s0, s1, tile, last;
+  PagedSeq seq;
+  MLA_DEVINL void load(const Args& a) {
+    s0 = slot_of_seq(a, b);
+    s1 = b + 1 < a.p.B ? slot_of_seq(a, b + 1) : INT32_MAX;
+    bool bad;
+    seq = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
+  }
+  MLA_DEVINL void init(const Args& a) {
+    tile = static_cast<int32_t>(blockIdx.x % static_cast<unsigned>(a.tiles));
+    g = static_cast<int32_t>(blockIdx.x / static_cast<unsigned>(a.tiles)) * a.per;
+    g1 = min(a.n_slots, g + a.per);
+    last = -1;
+    // the largest b with slot_of_seq(b) <= g, 32 at a time
+    int lo = 0, n = a.p.B;
+    const int lane = threadIdx.x & 31;
+    while (n > 1) {
+      const int step = (n + 31) / 32, m = lo + lane * step;
+      const uint32_t le = __ballot_sync(0xffffffffu, lane == 0 || (m < lo + n && slot_of_seq(a, m) <= g));
+      const int k = 31 - __clz(le);
+      n = min(step, lo + n - (lo + k * step));
+      lo += k * step;
+    }
+    b = lo;
+    load(a);
+  }
+  MLA_DEVINL bool next(const Args& a, Group& r) {
+    for (; g < g1; ++g) {
+      while (g >= s1) {
+        ++b;
+        load(a);
+      }
+      const int64_t t = static_cast<int64_t>(g - s0) * a.gt;
+      if (g < s0 || t >= seq.n) continue;
+      r.b = b;
+      r.t0 = seq.q0 + static_cast<int32_t>(t);
+      r.nt = min(a.gt, seq.n - static_cast<int32_t>(t));
+      r.pos = seq.len - seq.n + static_cast<int32_t>(t);
+      r.live = (r.pos + r.nt - 1) >> kBlockShift > tile * kTile;
+      r.fresh = r.live && b != last;
+      if (r.live) last = b;
+      ++g;
+      return true;
+    }
+    return false;
+  }
+};
+
+MLA_DEVINL bool wait_all(uint64_t* bar, uint32_t parity, const Args& a) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.p.wait_us, a.p.err));
+}
+
+MLA_DEVINL void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+MLA_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+MLA_DEVINL void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+MLA_DEVINL float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    block_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sKr = sm + kOffKr;
+  uint8_t* sFeed = sm + kOffFeed;
+  uint8_t* sRing = sm + kOffRing;
+  Bars& B = *reinterpret_cast<Bars*>(sm + kOffBar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == kLoadWarp && lane == 0) {
+    tc::prefetch_tmap(&tm_q);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&B.full[i], 1);
+      mbar_init(&B.empty[i], 1);
+    }
+    mbar_init(&B.k_full, 4);
+    mbar_init(&B.k_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.qr_full[i], 4);
+      mbar_init(&B.qr_empty[i], 1);
+      mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.s_empty[i], 4);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&B.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = B.tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0) record_bad_seqs(a.p.cu, a.p.seq_len, a.p.B, a.p.T, a.p.c.max_rows(), a.p.err);
+
+  const int H = a.p.H, N = a.gt * H;
+  Walk walk;
+  walk.init(a);
+  Group r;
+  const int j0 = walk.tile * kTile;
+  bool ok = true;
+
+  if (warp < kFeedWarp) {
+    // ============================== maxima, output ==============================
+    const int j = j0 + 32 * warp + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+    int u = 0;
+    while (ok && walk.next(a, r)) {
+      float* out = a.p.scores + static_cast<int64_t>(r.t0) * a.p.stride + j;
+      if (walk.tile == 0 && lane == 0 && (r.pos + r.nt - 1) >> kBlockShift > a.p.W) record_error(a.p.err, MLA_ERR_INVALID_ARG);
+      if (!r.live) {
+        if (j < a.p.W)
+          for (int t = 0; t < r.nt; ++t) out[t * a.p.stride] = -INFINITY;
+        continue;
+      }
+      const int sb = u & 1;
+      ok = wait_all(&B.s_full[sb], (u >> 1) & 1, a);
+      if (!ok) break;
+      tc::fence_after_sync();
+      float m = -INFINITY;
+      int t = 0, c = 0;                  // token of the group, columns of it seen
+#pragma unroll 1
+      for (int c0 = 0; c0 < r.nt * H; c0 += 32) {
+        uint32_t x[32];
+        tc::tmem_ld32(tmem + lanes + kTmS + sb * kMaxN + c0, x);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (t >= r.nt) break;          // (half of the last 32 may lie behind the group)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) m = max3(m, __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
+          c += 16;
+          if (c == H) {
+            if (j < a.p.W) *out = j < (r.pos + t) >> kBlockShift ? m * a.p.scale : -INFINITY;
+            out += a.p.stride;
+            m = -INFINITY;
+            c = 0;
+            ++t;
+          }
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.s_empty[sb]);
+      ++u;
+    }
+  } else if (warp < kLoadWarp) {
+    // ======================== mean rows, RoPE parts of queries ==================
+    // (a warp whose wait gave up goes on with nothing but the named barriers)
+    const int ft = threadIdx.x - 32 * kFeedWarp, q4 = warp - kFeedWarp, un = ft & 7;
+    const int per_shift = a.p.c.page_shift - kBlockShift;
+    const int64_t qrows = static_cast<int64_t>(a.p.T) * H;
+    uint32_t qrun = 0;
+    bool dead = false;
+    int u = 0, k = 0;
+    while (walk.next(a, r)) {
+      if (!r.live) continue;
+      if (r.fresh) {
+        // Unit ft + 128 i of a chunk: row ft / 8 + 16 i.  The sequence's blocks before
+        // its last token's own are there; the others are zero.
+        const int n_there = (walk.seq.len - 1) >> kBlockShift;
+        int64_t src[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = j0 + (ft >> 3) + 16 * i;
+          src[i] = -1;
+          if (j < n_there) {
+            const int32_t id = __ldg(a.p.c.table + r.b * a.p.c.table_stride + (j >> per_shift));
+            if (id >= 0 && id < a.p.c.n_pages) src[i] = (static_cast<int64_t>(id) << per_shift) + (j & ((1 << per_shift) - 1));
+            else if (un == 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
+          }
+        }
+        // The last products of the item before have read its rows (and q_pe of all groups).
+        if (k > 0 && !dead) dead = !wait_all(&B.k_free, (k - 1) & 1, a);
+        auto fetch = [&](uint8_t* to, int c) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = (ft >> 3) + 16 * i;
+            cp_async16(smem_u32(to) + row * 128 + ((un ^ (row & 7)) << 4),
+                       a.p.keys + (src[i] < 0 ? 0 : src[i] * kRow) + 64 * c + 8 * un, src[i] >= 0);
+          }
+          cp_async_commit();
+        };
+        if (!dead) {
+          fetch(sKr, kChunks);
+          for (int c = 0; c < kFeed; ++c) fetch(sFeed + c * kChunk, c);
+        }
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+          if (!dead) cp_async_wait<kFeed - 1>();
+          tc::named_bar_sync(kBarFeed, 128);
+          if (!dead) {
+            const uint8_t* from = sFeed + (c % kFeed) * kChunk;
+            const int row = 32 * q4 + lane;
+            uint32_t x[32];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const uint4 v = *reinterpret_cast<const uint4*>(from + row * 128 + ((w ^ (row & 7)) << 4));
+              x[4 * w] = v.x; x[4 * w + 1] = v.y; x[4 * w + 2] = v.z; x[4 * w + 3] = v.w;
+            }
+            tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmK + 32 * c, x);
+          }
+          tc::named_bar_sync(kBarFeed, 128);
+          if (!dead) {
+            if (c + kFeed < kChunks) fetch(sFeed + (c % kFeed) * kChunk, c + kFeed);
+            else cp_async_commit();      // (an empty group keeps the count)
+          }
+        }
+        if (!dead) {
+          tc::tmem_st_wait();
+          tc::fence_proxy_async();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.k_full);
+        }
+        ++k;
+      }
+      // q_pe of the group: N rows x 64, eight 16-byte units a thread
+      if (dead) continue;
+      const int64_t row0 = static_cast<int64_t>(r.t0) * H;
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = (ft >> 3) + 16 * i;
+        v[i] = row < r.nt * H && row0 + row < qrows
+                   ? __ldg(reinterpret_cast<const uint4*>(a.p.q_pe + (row0 + row) * kRope) + un) : make_uint4(0, 0, 0, 0);
+      }
+      if (u >= 2) dead = !wait_all(&B.qr_empty[u & 1], ((u >> 1) - 1) & 1, a);
+      if (dead) continue;
+      uint8_t* to = sFeed + (u & 1) * kChunk;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = (ft >> 3) + 16 * i;
+        qrun = bf16x2_absmax(bf16x2_absmax(qrun, v[i].x), v[i].y);
+        qrun = bf16x2_absmax(bf16x2_absmax(qrun, v[i].z), v[i].w);
+        uint4 o;
+        float2 f;
+        f = bf16x2_to_f32(v[i].x); o.x = pack_f16x2(f.x, f.y);
+        f = bf16x2_to_f32(v[i].y); o.y = pack_f16x2(f.x, f.y);
+        f = bf16x2_to_f32(v[i].z); o.z = pack_f16x2(f.x, f.y);
+        f = bf16x2_to_f32(v[i].w); o.w = pack_f16x2(f.x, f.y);
+        *reinterpret_cast<uint4*>(to + row * 128 + ((un ^ (row & 7)) << 4)) = o;
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.qr_full[u & 1]);
+      ++u;
+    }
+    if (bf16x2_absmax_overflows(qrun)) record_error(a.p.err, MLA_ERR_RANGE);
+    ok = !dead;
+  } else if (warp == kLoadWarp) {
+    // ============================== queries (TMA) ===============================
+    int s = 0;                           // stages filled
+    while (ok && walk.next(a, r)) {
+      if (!r.live) continue;
+      for (int c = 0; c < kChunks; ++c, ++s) {
+        const int st = s % kStages;
+        if (s >= kStages) ok = wait_all(&B.empty[st], ((s / kStages) - 1) & 1, a);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&B.full[st], static_cast<uint32_t>(N) * 128);
+          tc::tma_load_3d(sRing + st * kChunk, &tm_q, &B.full[st], 0, r.t0 * H, c);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    // ================================== MMAs ====================================
+    const uint32_t idesc = tc::idesc_f16(128, N, false, false, false);
+    int s = 0, u = 0, k = 0;
+    while (ok && walk.next(a, r)) {
+      if (!r.live) continue;
+      if (r.fresh) {
+        // the item before is done with its mean rows when its products are
+        if (k > 0) tc::mma_commit_warp(&B.k_free);
+        ok = wait_all(&B.k_full, k & 1, a);
+        if (!ok) break;
+        ++k;
+      }
+      const int sb = u & 1;
+      if (u >= 2) ok = wait_all(&B.s_empty[sb], ((u >> 1) - 1) & 1, a);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t d = tmem + kTmS + sb * kMaxN;
+      for (int c = 0; ok && c < kChunks; ++c, ++s) {
+        const int st = s % kStages;
+        ok = wait_all(&B.full[st], (s / kStages) & 1, a);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t q0 = smem_u32(sRing + st * kChunk);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc::mma_ts_warp(d, tmem + kTmK + 32 * c + 8 * ks, tc::sdesc_sw128(q0 + 32 * ks, 16, 1024), idesc, (c | ks) != 0);
+        tc::mma_commit_warp(&B.empty[st]);
+      }
+      if (!ok) break;
+      ok = wait_all(&B.qr_full[sb], (u >> 1) & 1, a);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t k0 = smem_u32(sKr), q0 = smem_u32(sFeed + sb * kChunk);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        tc::mma_ss_warp(d, tc::sdesc_sw128(k0 + 32 * ks, 16, 1024), tc::sdesc_sw128(q0 + 32 * ks, 16, 1024), idesc, 1u);
+      tc::mma_commit_warp(&B.qr_empty[sb]);
+      tc::mma_commit_warp(&B.s_full[sb]);
+      ++u;
+    }
+  }
+
+  tc::fence_before_sync();
+  if (__syncthreads_or(!ok)) {
+    // A wait ran out: loads and products may be under way that nobody waits for any more.
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < kGaveUpNs) __nanosleep(1000);
+  }
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_block_scores(const BlockScoresArgs& p, cudaStream_t stream) {
+  Args a = {};
+  a.p = p;
+  // Tokens of a group are of one sequence: with single tokens there is one.
+  a.gt = p.T > p.B ? kMaxN / p.H : 1;
+  a.tiles = (p.W + kTile - 1) / kTile;
+  a.n_slots = p.T / a.gt + p.B;
+  const int64_t units = static_cast<int64_t>(a.n_slots) * a.tiles, sms = device_sm_count();
+  // Single tokens have mean rows of their own each, so there is nothing to keep; a
+  // chunk's tokens share theirs: about one run of groups for each SM.
+  a.per = p.T > p.B ? static_cast<int32_t>((units + sms - 1) / sms) : 1;
+  const int64_t grid = static_cast<int64_t>(a.tiles) * ((a.n_slots + a.per - 1) / a.per);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  CUtensorMap tq;
+  const uint64_t qrows = static_cast<uint64_t>(p.T) * static_cast<uint64_t>(p.H);
+  cudaError_t e = make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kChunks, kLatent * 2, 128, 64,
+                               static_cast<uint32_t>(a.gt * p.H), 1);
+  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || (set.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(block_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_dependent(block_scores_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, stream, tq, a);
+}
+
+}  // namespace mla

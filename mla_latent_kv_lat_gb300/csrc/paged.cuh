@@ -1,5 +1,5 @@
 // The paged latent cache: row formats, the sequence table, page lookup, and
-// the launchers of the paged operators (append, gather, attention).
+// the launchers of the paged operators.
 #pragma once
 
 #include "common.cuh"
@@ -79,6 +79,9 @@ MLA_DEVINL void record_bad_seqs(const int32_t* cu, const int32_t* seq_len, int B
   }
 }
 
+// Blocks of positions that block-sparse attention chooses among.
+constexpr int kBlockRows = 64, kBlockShift = 6;
+
 struct PagedAppendArgs {
   PagedCache c;
   const uint16_t* c_kv;      // bf16 [T][512]
@@ -108,11 +111,70 @@ struct PagedAttnArgs {
   int32_t B, T, H;
   int32_t window;            // 0: the whole context
   int32_t n_sink;
+  const int32_t* blocks;     // [T][K] blocks of 64 positions that a token attends to (null: as window says)
+  const int32_t* counts;     // [T] entries of a token's list
+  int32_t K;
   float scale_log2;          // softmax scale * log2(e)
   uint16_t* o_lat;           // fp16 [T][H][512]
   void* workspace;           // paged_attn_workspace_bytes()
   int* err;
   uint32_t wait_us;
+};
+
+struct NormAppendArgs {
+  PagedCache c;
+  const uint16_t* q;         // bf16, head h of token t at t * q_token + h * q_head: 128 values, then 64 to rotate
+  int64_t q_token, q_head;   // elements
+  const uint16_t* kv;        // bf16, token t at t * kv_token: the latent (512), then 64 to rotate
+  int64_t kv_token;
+  const uint16_t* q_weight;  // bf16 [192] or null: queries are not normed
+  const uint16_t* kv_weight; // bf16 [512]
+  const int32_t* cu;         // [B + 1]
+  const int32_t* seq_len;    // [B]
+  int32_t B, T, H;
+  int32_t iters;             // set by the launcher: groups of four heads that a warp takes
+  float eps;
+  uint16_t* q_nope;          // bf16 [T][H][128]
+  uint16_t* q_pe;            // bf16 [T][H][64]
+  int* err;
+  uint64_t turn[kRope / 2];  // as in PagedAppendArgs
+};
+
+struct BlockKeysArgs {
+  PagedCache c;
+  const int32_t* cu;         // [B + 1]
+  const int32_t* seq_len;    // [B]
+  int32_t B, T;
+  uint16_t* keys;            // fp16 [n_pages][page_size / 64][576]
+  int* err;
+};
+
+struct BlockScoresArgs {
+  PagedCache c;              // (pages are not read)
+  const uint16_t* q_lat;     // fp16 [T][H][512]
+  const uint16_t* q_pe;      // bf16 [T][H][64]
+  const uint16_t* keys;      // fp16 [n_pages][page_size / 64][576]
+  const int32_t* cu;         // [B + 1]
+  const int32_t* seq_len;    // [B]
+  int32_t B, T, H;
+  int32_t W;                 // scores of a row
+  float scale;
+  float* scores;             // [T][stride]
+  int64_t stride;
+  int* err;
+  uint32_t wait_us;
+};
+
+struct SelectBlocksArgs {
+  const float* scores;       // [T][stride], W of a row are there
+  int64_t stride;
+  const int32_t* cu;         // [B + 1]
+  const int32_t* seq_len;    // [B]
+  int32_t B, T, W, K;
+  int32_t n_sink, n_local;   // blocks
+  int32_t* blocks;           // [T][K]
+  int32_t* counts;           // [T]
+  int* err;
 };
 
 // 2^(s - 127) for a scale byte s in [112, 134] as fp16, in both halves (2^-15, s =
@@ -134,6 +196,22 @@ MLA_DEVINL void e4m3x4_to_f16x4(uint32_t c, uint32_t d, uint32_t& lo, uint32_t& 
   const __half2 r1 = __hmul2(*reinterpret_cast<const __half2*>(&x1), s);
   lo = *reinterpret_cast<const uint32_t*>(&r0);
   hi = *reinterpret_cast<const uint32_t*>(&r1);
+}
+
+// Exponent e of the smallest scale 2^e in [2^-15, 2^7] with amax <= 448 * 2^e.
+// 448 = 1.75 * 2^8, so with amax = m * 2^k (m in [1, 2)) it is k - 8 for
+// m <= 1.75 and k - 7 otherwise.  (A subnormal amax clamps to -15.)
+MLA_DEVINL int e4m3_scale_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return max(kE4m3MinExp, min(kE4m3MaxExp, e));
+}
+
+// Two fp32 values to two e4m3 codes (nearest even, saturating).
+MLA_DEVINL uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // A launch that may begin while the kernel before it in the stream finishes (the
@@ -161,6 +239,10 @@ cudaError_t make_tmap_row_groups(CUtensorMap* map, const void* base, uint64_t gr
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, bool out_f16, cudaStream_t stream);
+cudaError_t launch_norm_append(const NormAppendArgs& a, cudaStream_t stream);
+cudaError_t launch_block_keys(const BlockKeysArgs& a, cudaStream_t stream);
+cudaError_t launch_block_scores(const BlockScoresArgs& a, cudaStream_t stream);
+cudaError_t launch_select_blocks(const SelectBlocksArgs& a, cudaStream_t stream);
 size_t paged_attn_workspace_bytes();
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
 

@@ -165,7 +165,15 @@ struct __align__(16) Rec {     // the block that starts in cluster c and ends in
 // rows: 8 queries 93 and 86 us, 12 121 and 121, 16 150 and 156, 152 1071 and 1333;
 // the staging and a second launch cost ~10 us, so at 2000 rows 16 queries take 37 and
 // 28 us, 64 66 and 60, 256 153 and 164.
-constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 16;
+constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 16, kStageReads = 8;
+
+// With listed blocks every token converts its own: staging pays when the batch's lists
+// name a row kStageReads times on average.
+MLA_DEVINL bool worth_staging(const PagedAttnArgs& a, const PagedSeq& s) {
+  if (a.blocks != nullptr)
+    return s.n >= kStageBlocks && static_cast<int64_t>(s.n) * a.K * kBK >= static_cast<int64_t>(kStageReads) * s.len;
+  return static_cast<int64_t>(s.n) * a.H > (kStageBlocks - 1) * kRows;
+}
 
 // Which sequences a launch takes.
 enum Take : int32_t { kTakeAll, kTakeStaged, kTakeUnstaged };
@@ -188,15 +196,19 @@ struct TcArgs {
 // floor(cu[b] H / 128) + b), so a slot's sequence is found by a search in cu
 // alone, with no prefix sums over the batch.  Slots without a block cost 0.
 // ---------------------------------------------------------------------------
+// With listed blocks (kListed) a block is the H rows of one token, whose list its
+// tiles are, and its slot is the token.
+template <bool kListed>
 MLA_DEVINL int64_t slot_of_seq(const PagedAttnArgs& a, int b) {
   const int32_t c = max(0, min(a.T, __ldg(a.cu + b)));
-  return static_cast<int64_t>(c) * a.H / kRows + b;
+  return kListed ? c : static_cast<int64_t>(c) * a.H / kRows + b;
 }
 
 struct Item {
   int32_t b;                  // sequence
   int32_t kend, wlo;          // keys some row of the block sees: [0, n_sink) and [wlo, kend)
   int32_t first, sink_tiles;  // tile t of the block is t < sink_tiles ? t : first + t - sink_tiles
+                              // (kListed: entry t of the token's list, which has `first` entries)
   int32_t t_lo, n_tiles;      // this piece: tiles [t_lo, t_lo + n_tiles)
   int32_t nvalid;             // rows
   int32_t pos0;               // position of the sequence's first new token
@@ -221,6 +233,7 @@ struct Item {
 };
 
 // Walks the slots in order.
+template <bool kListed>
 struct Walker {
   int b;                // sequence of the last slot asked for
   int64_t s0, s1;       // its first slot, and the next sequence's
@@ -229,8 +242,8 @@ struct Walker {
 
   MLA_DEVINL void load(const TcArgs& t) {
     const PagedAttnArgs& a = t.p;
-    s0 = slot_of_seq(a, b);
-    s1 = b + 1 < a.B ? slot_of_seq(a, b + 1) : INT64_MAX;
+    s0 = slot_of_seq<kListed>(a, b);
+    s1 = b + 1 < a.B ? slot_of_seq<kListed>(a, b + 1) : INT64_MAX;
     bool bad;
     seq = paged_seq(a.cu, a.seq_len, b, a.T, a.c.max_rows(), bad);
     rows = static_cast<uint32_t>(seq.n) * static_cast<uint32_t>(a.H);
@@ -241,7 +254,7 @@ struct Walker {
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int m = (lo + hi) >> 1;
-      if (slot_of_seq(a, m) <= g) lo = m; else hi = m;
+      if (slot_of_seq<kListed>(a, m) <= g) lo = m; else hi = m;
     }
     b = lo;
     load(t);
@@ -254,6 +267,21 @@ struct Walker {
       load(t);
     }
     const int64_t i = g - s0;
+    if constexpr (kListed) {
+      if (i < 0 || i * a.H >= rows) return 0;
+      const int32_t listed = __ldg(a.counts + g);
+      if (listed < 0 || listed > a.K) record_error(a.err, MLA_ERR_INVALID_ARG);
+      it.b = b;
+      it.nvalid = a.H;
+      it.once = seq.n <= 2;
+      it.row0 = static_cast<uint32_t>(i) * static_cast<uint32_t>(a.H);
+      it.qrow0 = g * a.H;
+      it.pos0 = seq.len - seq.n;
+      it.kend = it.pos0 + static_cast<int32_t>(i) + 1;
+      it.wlo = it.sink_tiles = 0;
+      it.first = max(0, min(listed, a.K));
+      return max(1, it.first);         // a token with no block goes through one tile of nothing: its output is zero
+    }
     if (i < 0 || i * kRows >= rows) return 0;
     const uint32_t H = static_cast<uint32_t>(a.H), r0 = static_cast<uint32_t>(i) * kRows;
     const uint32_t r1 = min(r0 + kRows, rows);
@@ -282,8 +310,9 @@ struct Start {
 };
 
 // This cluster's pieces in order; every role walks the same sequence.
+template <bool kListed>
 struct Iter {
-  Walker w;
+  Walker<kListed> w;
   const Start* st;
   int64_t lo, hi, S;
   int32_t g;
@@ -315,6 +344,17 @@ struct Iter {
     return false;
   }
 };
+
+// kListed: a warp holds 32 entries of the piece's list at a time, tile t's in lane t % 32.
+MLA_DEVINL int32_t list_entry(const TcArgs& a, const Item& it, int t) {
+  const int x = it.t_lo + t;
+  return t < it.n_tiles && x < it.first ? __ldg(a.p.blocks + it.qrow0 / a.p.H * a.p.K + x) : -1;
+}
+// First key of the tile that a list's entry names: of a block behind the token's own, or
+// of none, keys that no row sees.
+MLA_DEVINL int entry_key(const Item& it, int32_t e) {
+  return e >= 0 && e <= (it.kend - 1) / kBK ? e * kBK : (it.kend + kBK - 1) / kBK * kBK;
+}
 
 // Keys [k, k + n) hold one that some row of the block sees.
 MLA_DEVINL bool any_visible(const TcArgs& a, const Item& it, int k, int n) {
@@ -585,7 +625,8 @@ MLA_DEVINL void store_f16(const Codes& c, uint8_t* lat, int pt, int j) {
 // are (32 tokens at 4K-32K rows, 16 heads: 138 us, without it 147; 64 heads 143 and
 // 149, 96 heads 149 and 152).  Its own instantiation, because the tests make full
 // blocks 2% slower; for e4m3 pages it gains nothing.
-template <bool kE4m3, bool kFewRows, bool kLong>
+// kListed: each token has its own tiles (mla_attn_paged_blocks).
+template <bool kE4m3, bool kFewRows, bool kLong, bool kListed>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                       const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_scale,
@@ -667,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     long long* red = reinterpret_cast<long long*>(sStg);
     const int per = (a.n_slots + NT - 1) / NT;
     const int g0 = min(a.n_slots, static_cast<int>(threadIdx.x) * per), g1 = min(a.n_slots, g0 + per);
-    Walker w;
+    Walker<kListed> w;
     Item it;
     long long sum = 0;
     if (g0 < g1) {
@@ -700,7 +741,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     if (total < (1 << 24)) {
       const uint32_t units = static_cast<uint32_t>(total);
       const float blocks =                                        // about
-          fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H * (1.f / kRows));
+          kListed ? static_cast<float>(a.p.T)
+                  : fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H * (1.f / kRows));
       share = kPieceCost + 2;
       if (units > blocks * share) {
         const float x = __fdividef(static_cast<float>(units), blocks * kCutCost);
@@ -748,7 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   const uint32_t tmem = B.tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  Iter items;
+  Iter<kListed> items;
   items.init(B.st);
   Item it;
   bool ok = true;
@@ -777,14 +819,23 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       const bool rvalid = i < it.nvalid;
       const bool mine = !kFewRows || 32 * q4 + 16 * static_cast<int>(rank) < it.nvalid;
       // keys [wl, lim] and the sinks are visible to this row
-      const int lim = rvalid ? it.pos0 + static_cast<int>((it.row0 + i) / static_cast<uint32_t>(a.p.H)) : it.kend - 1;
-      const int wl = a.p.window > 0 ? max(0, lim - a.p.window + 1) : 0;
+      const int lim = rvalid && !kListed ? it.pos0 + static_cast<int>((it.row0 + i) / static_cast<uint32_t>(a.p.H))
+                                         : it.kend - 1;
+      const int wl = !kListed && a.p.window > 0 ? max(0, lim - a.p.window + 1) : 0;
+      int32_t entries = -1;
       float m_run = -INFINITY, l_h = 0.f;      // the running maximum, less kPShift; the sum
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int sb = u & 1;
         const uint32_t ph = (u >> 1) & 1, xph = (kFewRows ? xu : u) & 1;
-        const int base = it.key_tile(t) * kBK, k0 = base + col;
+        int base;
+        if constexpr (kListed) {
+          if ((t & 31) == 0) entries = list_entry(a, it, t + lane);
+          base = entry_key(it, __shfl_sync(0xffffffffu, entries, t & 31));
+        } else {
+          base = it.key_tile(t) * kBK;
+        }
+        const int k0 = base + col;
         uint64_t s[8];                           // the scores, in pairs
         float mrow = -INFINITY;
         // Barriers are tested ahead of their use, so that their latencies
@@ -812,7 +863,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             s[2 * g] = add2(s[2 * g], x.x);
             s[2 * g + 1] = add2(s[2 * g + 1], x.y);
           }
-          if (k0 + 15 > lim || (k0 < wl && k0 + 15 >= a.p.n_sink)) {
+          if (k0 + 15 > lim || (!kListed && k0 < wl && k0 + 15 >= a.p.n_sink)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               float2 v = unpack2(s[e]);
@@ -889,7 +940,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             }
             // A tile with keys that no row of the block sees: their values must
             // not enter P V (0 x NaN).  The score product has read the tile.
-            if (base + kBK > it.kend || (base < it.wlo && base + kBK > a.p.n_sink)) {
+            if (base + kBK > it.kend || (!kListed && base < it.wlo && base + kBK > a.p.n_sink)) {
               uint8_t* stage = sLat + ((u + kQSlots * (k + 1)) % kLatStages) * kLatStage;
               for (int q = threadIdx.x; q < kBK * 32; q += 256)
                 if (!key_visible(a, it, base + (q >> 5)))
@@ -1046,7 +1097,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         ok = wait_cl(&B.pv_done[(m - 1) & 1], ((m - 1) >> 1) & 1, a);
         if (!ok) break;
         tc::fence_after_sync();
-        Iter ahead = items;            // (the output looks the piece up again)
+        Iter<kListed> ahead = items;            // (the output looks the piece up again)
         if (!ahead.next(a, it)) break;
         move_o(tmem + lanes + kTmO, stg, partial(it), it.nvalid - 32 * q4, moved, g, 1.f, nullptr);
         moved = true;
@@ -1246,10 +1297,29 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       record_error(a.p.err, MLA_ERR_INVALID_ARG);
       return a.n_rows;
     };
+    // kListed: lane l looks tile t + l's row up (and its staged row), 32 tiles at a time.
+    auto listed_rows = [&](int t, int32_t base, int& srow) -> int {
+      srow = kStageRows;
+      const int x = it.t_lo + t + lane;
+      if (t + lane >= it.n_tiles || x >= it.first) return a.n_rows;
+      const int32_t e = list_entry(a, it, t + lane);
+      if (e >= 0 && e <= (it.kend - 1) / kBK) {
+        const int key = e * kBK;
+        const int32_t id = __ldg(a.p.c.table + it.b * a.p.c.table_stride + (key >> a.p.c.page_shift));
+        srow = base + key;
+        if (id >= 0 && id < a.p.c.n_pages) return (id << a.p.c.page_shift) + (key & ((1 << a.p.c.page_shift) - 1));
+      }
+      record_error(a.p.err, MLA_ERR_INVALID_ARG);
+      return a.n_rows;
+    };
     int u = 0, k = 0;
 #pragma unroll 1
     while (ok && items.next(a, it)) {
-      const int32_t id0 = entry(0);            // (on its way while the queries are asked for)
+      const int32_t base = staged ? __ldg(a.stage_base + it.b) : 0;
+      int srows = 0, rows = 0;
+      int32_t id0 = 0;                         // (on its way while the queries are asked for)
+      if constexpr (kListed) rows = listed_rows(0, base, srows);
+      else id0 = entry(0);
 #pragma unroll 1
       for (int q = 0; q < kQSlots; ++q) {           // the queries: 128 rows x 64 dims twice a stage
         const int r = u + kQSlots * k + q, ls = r % kLatStages;
@@ -1264,12 +1334,20 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       }
       if (!ok) break;
       ++k;
-      const int32_t base = staged ? __ldg(a.stage_base + it.b) : 0;
-      int row_n = row_at(0, id0);
+      int row_n = kListed ? 0 : row_at(0, id0);
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
-        const int rs = u % kRopeStages, row = row_n;
-        if (t + 1 < it.n_tiles) row_n = row_at(t + 1, entry(t + 1));
+        const int rs = u % kRopeStages;
+        int row, srow = 0;
+        if constexpr (kListed) {
+          if ((t & 31) == 0 && t > 0) rows = listed_rows(t, base, srows);
+          row = __shfl_sync(0xffffffffu, rows, t & 31);
+          srow = __shfl_sync(0xffffffffu, srows, t & 31);
+          row_n = __shfl_sync(0xffffffffu, rows, (t + 1) & 31);      // (the last of 32 asks for one that is there)
+        } else {
+          row = row_n;
+          if (t + 1 < it.n_tiles) row_n = row_at(t + 1, entry(t + 1));
+        }
         // Rows that few blocks read come from HBM: each CTA has half of the next
         // tile's rows on their way into L2 (32 tokens at 4K-32K rows: 175 -> 157
         // us; for chunks, whose rows L2 holds, it costs 3-4%, and for e4m3 pages,
@@ -1306,7 +1384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             tc::tma_load_3d(sScale + ls * kRawScale + j * box * 16, &tm_scale, full, kE4m3ScaleOff / 2, row, 0);
         } else if (staged) {
           if (lane == 0)
-            tma_load_4d(dst, &tm_lat, full, 0, 0, c0, staged_row(a, it, base, it.key_tile(t)) / 8);
+            tma_load_4d(dst, &tm_lat, full, 0, 0, c0, (kListed ? srow : staged_row(a, it, base, it.key_tile(t))) / 8);
         } else if (mine && ch == 1) {
           tma_load_4d(dst + j * box / 8 * kGroup, &tm_lat, full, 0, 0, c0, row / 8);
         }
@@ -1421,7 +1499,8 @@ __global__ void __launch_bounds__(128 * kCombRows, kFew ? 2 : 4) paged_combine_k
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < n; s0 += 32) {
     if (s0 > 0) ml = stat(s0 + lane);
-    const float w = s0 + lane < n ? exp2f(ml.x - M) * ml.y : 0.f;      // lane: partial s0 + lane's weight
+    // lane: partial s0 + lane's weight (a piece that sees no key has none, and may be all there is)
+    const float w = s0 + lane < n && ml.y > 0.f ? exp2f(ml.x - M) * ml.y : 0.f;
     L += w;
     for (int j0 = 0; j0 < min(32, n - s0); j0 += 8) {
       if (!kFew || s0 + j0 > 0) fetch(s0 + j0);
@@ -1435,7 +1514,8 @@ __global__ void __launch_bounds__(128 * kCombRows, kFew ? 2 : 4) paged_combine_k
       }
     }
   }
-  const float inv = 1.f / warp_sum(L);
+  L = warp_sum(L);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
   *reinterpret_cast<uint2*>(a.p.o_lat + (r.qrow0 + row) * kLatent + col) =
       make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
 }
@@ -1462,7 +1542,7 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
     if (b < a.p.B) {
       bool bad;
       const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
-      if (static_cast<int64_t>(s.n) * a.p.H > (kStageBlocks - 1) * kRows) {
+      if (worth_staging(a.p, s)) {
         int32_t sink;
         const int32_t first = seq_first_tile(a.p, s.len - s.n, sink);
         const int64_t r = static_cast<int64_t>(sink + (s.len + kBK - 1) / kBK - first) * kBK;
@@ -1555,10 +1635,10 @@ size_t partial_bytes() {
   return rows * kLatent * sizeof(float) + rows * 2 * sizeof(float) + clusters() * sizeof(Rec);
 }
 
-template <bool kE4m3, bool kFewRows, bool kLong>
+template <bool kE4m3, bool kFewRows, bool kLong, bool kListed>
 cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const CUtensorMap& ts,
                         const TcArgs& a, cudaStream_t stream) {
-  auto kern = paged_attn_kernel<kE4m3, kFewRows, kLong>;
+  auto kern = paged_attn_kernel<kE4m3, kFewRows, kLong, kListed>;
   static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1593,8 +1673,9 @@ bool any_long(const PagedAttnArgs& p) {
 template <bool kE4m3, bool kFewRows>
 cudaError_t launch_for(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const CUtensorMap& ts,
                        const TcArgs& a, cudaStream_t stream) {
-  return any_long(a.p) ? launch_pair<kE4m3, kFewRows, true>(tm, tr, tq, ts, a, stream)
-                       : launch_pair<kE4m3, kFewRows, false>(tm, tr, tq, ts, a, stream);
+  if (a.p.blocks != nullptr) return launch_pair<kE4m3, kFewRows, false, true>(tm, tr, tq, ts, a, stream);
+  return any_long(a.p) ? launch_pair<kE4m3, kFewRows, true, false>(tm, tr, tq, ts, a, stream)
+                       : launch_pair<kE4m3, kFewRows, false, false>(tm, tr, tq, ts, a, stream);
 }
 
 }  // namespace
@@ -1613,7 +1694,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   a.rec = reinterpret_cast<Rec*>(a.ws_ml + rows * 2);
   int32_t* stage_base = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(p.workspace) + partial_bytes());
   a.stage = reinterpret_cast<uint16_t*>(stage_base + kStageSeqs);
-  a.n_slots = static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
+  a.n_slots = p.blocks != nullptr ? p.T : static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
   a.n_rows = p.c.n_pages << p.c.page_shift;
   // The latents of fp16 pages or of staged rows, in groups of eight rows; the
   // queries, as 64-dim chunks (dims, rows, chunks).  The RoPE parts are fp16 in
@@ -1630,8 +1711,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
     if (e != cudaSuccess) return e;
-    // a block of single tokens has H rows
-    return p.T <= p.B && p.H <= kRows - 16 ? launch_for<false, true>(tm, tr, tq, tq, a, stream)
+    // a block of single tokens has H rows, and so has one of listed blocks
+    return (p.T <= p.B || p.blocks != nullptr) && p.H <= kRows - 16 ? launch_for<false, true>(tm, tr, tq, tq, a, stream)
                                            : launch_for<false, false>(tm, tr, tq, tq, a, stream);
   }
   // In elements of two bytes, as the rows are: a CTA's 256 codes, and the 16 scales.
@@ -1644,7 +1725,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // A batch of single tokens (T <= B) has no sequence of several blocks, bar one
   // with empty sequences beside it.
-  if (p.T > p.B && p.B <= kStageSeqs && static_cast<int64_t>(p.T) * p.H > (kStageBlocks - 1) * kRows) {
+  if (p.T > p.B && p.B <= kStageSeqs &&
+      (p.blocks != nullptr ? p.T >= kStageBlocks : static_cast<int64_t>(p.T) * p.H > (kStageBlocks - 1) * kRows)) {
     a.stage_base = stage_base;
     e = make_tmap_row_groups(&tm, a.stage, kStageRows / 8, kLatent / 64, kLatent * 2, kBK / 8, 4);
     if (e != cudaSuccess) return e;

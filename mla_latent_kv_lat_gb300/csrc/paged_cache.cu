@@ -34,22 +34,6 @@ MLA_DEVINL uint4 bf16x8_to_f16(uint4 v) {
   return o;
 }
 
-// Exponent e of the smallest scale 2^e in [2^-15, 2^7] with amax <= 448 * 2^e.
-// 448 = 1.75 * 2^8, so with amax = m * 2^k (m in [1, 2)) it is k - 8 for
-// m <= 1.75 and k - 7 otherwise.  (A subnormal amax clamps to -15.)
-MLA_DEVINL int e4m3_scale_exp(float amax) {
-  const uint32_t u = __float_as_uint(amax);
-  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return max(kE4m3MinExp, min(kE4m3MaxExp, e));
-}
-
-// Two fp32 values to two e4m3 codes (nearest even, saturating).
-MLA_DEVINL uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Both kernels: a warp takes four consecutive rows of the call's array at a time.
 // Lane k < 4 looks up row k's place in the pages, one group ahead, so that the
 // chain cu -> seq_len -> table -> row is off the path of the data; all loads of a

@@ -178,6 +178,74 @@ def mla_paged_step(q_nope, q_pe, c_kv, k_pe, wk_b, wv_b, pages, block_table, cu_
     return bufs
 
 
+def paged_block_keys(pages: torch.Tensor) -> torch.Tensor:
+    """The mean rows' pool of a page pool: fp16 [n_pages, page_size / 64, 576]."""
+    return torch.empty(pages.shape[0], pages.shape[1] // B.BLOCK, B.ROW, dtype=torch.float16, device=pages.device)
+
+
+@dataclass
+class SparseBuffers:
+    q_nope: torch.Tensor     # bf16 [T, H, 128]
+    q_pe: torch.Tensor       # bf16 [T, H, 64], rotated
+    q_lat: torch.Tensor      # fp16 [T, H, 512]
+    scores: torch.Tensor     # fp32 [T, n_scores], a score for each block of the longest context
+    blocks: torch.Tensor     # int32 [T, K]
+    counts: torch.Tensor     # int32 [T]
+    o_lat: torch.Tensor      # fp16 [T, H, 512]
+    o: torch.Tensor          # fp32 [T, H, 128]
+    workspace: torch.Tensor  # uint8, mla_paged_workspace_size(H)
+
+
+def sparse_buffers(T: int, H: int, n_scores: int, K: int, device="cuda") -> SparseBuffers:
+    i32 = dict(dtype=torch.int32, device=device)
+    return SparseBuffers(
+        torch.zeros(T, H, B.QK_NOPE, dtype=torch.bfloat16, device=device),
+        torch.empty(T, H, B.QK_ROPE, dtype=torch.bfloat16, device=device),
+        torch.empty(T, H, B.KV_LORA_RANK, dtype=torch.float16, device=device),
+        torch.empty(T, n_scores, dtype=torch.float32, device=device), torch.empty(T, K, **i32), torch.empty(T, **i32),
+        torch.zeros(T, H, B.KV_LORA_RANK, dtype=torch.float16, device=device),
+        torch.empty(T, H, B.V_HEAD, dtype=torch.float32, device=device),
+        torch.empty(B.mla_paged_workspace_size(H), dtype=torch.uint8, device=device))
+
+
+def mla_paged_sparse_step(q, kv, q_weight, kv_weight, wk_b, wv_b, pages, block_keys, block_table, cu_q, seq_len, *,
+                          n_blocks: int = 32, n_sink: int = 1, n_local: int = 2, eps: float = 1e-6,
+                          freq_base: float = 10000.0, freq_scale: float = 0.025, bufs: Optional[SparseBuffers] = None,
+                          scale=None, stream=None) -> SparseBuffers:
+    """One step of a batch on a paged cache in which each token attends to at most ``n_blocks`` blocks of 64
+    positions, from the projections' outputs on: norms, rotations and the new rows into their pages; the mean rows of
+    completed blocks; absorption; scores and choice of the blocks; attention over them; late decompression.
+    ``block_keys`` (paged_block_keys) goes with the pages from step to step.  Batches and padding as in
+    mla_paged_step; buffers (with as many scores a row as the longest context has blocks, and n_blocks entries a list)
+    as sparse_buffers makes them."""
+    dev = B.paged_device(q, "q")
+    if dev != torch.cuda.current_device():   # all calls on the tensors' device and one of its streams
+        with torch.cuda.device(dev):
+            return mla_paged_sparse_step(q, kv, q_weight, kv_weight, wk_b, wv_b, pages, block_keys, block_table, cu_q, seq_len,
+                                         n_blocks=n_blocks, n_sink=n_sink, n_local=n_local, eps=eps, freq_base=freq_base,
+                                         freq_scale=freq_scale, bufs=bufs, scale=scale, stream=stream)
+    T, H = q.shape[0], q.shape[1]
+    if bufs is None:
+        with B.stream_context(stream, dev):
+            bufs = sparse_buffers(T, H, max(1, block_table.shape[1] * pages.shape[1] // B.BLOCK), n_blocks, q.device)
+    # (the cache calls check their other tensors)
+    for name, t in (("wk_b", wk_b), ("wv_b", wv_b), ("bufs.q_lat", bufs.q_lat), ("bufs.o", bufs.o)):
+        if B.paged_device(t, name) != dev:
+            raise ValueError(f"{name} is on {t.device}, q on cuda:{dev}")
+    B.mla_paged_norm_append(q, kv, q_weight, kv_weight, pages, block_table, cu_q, seq_len, bufs.q_nope, bufs.q_pe, eps=eps,
+                            freq_base=freq_base, freq_scale=freq_scale, stream=stream)
+    B.mla_paged_block_keys(pages, block_table, cu_q, seq_len, block_keys, T, stream=stream)
+    B.mla_absorb_q(bufs.q_nope, wk_b, bufs.q_lat, scale=scale, stream=stream)
+    B.mla_paged_block_scores(bufs.q_lat, bufs.q_pe, block_keys, block_table, cu_q, seq_len, bufs.scores, scale=scale,
+                             stream=stream)
+    B.mla_paged_select_blocks(bufs.scores, cu_q, seq_len, bufs.blocks, bufs.counts, n_sink=n_sink, n_local=n_local,
+                              stream=stream)
+    B.mla_attn_paged_blocks(bufs.q_lat, bufs.q_pe, pages, block_table, cu_q, seq_len, bufs.blocks, bufs.counts, bufs.o_lat,
+                            workspace=bufs.workspace, scale=scale, stream=stream)
+    B.mla_late_decompress(bufs.o_lat, wv_b, bufs.o, scale=scale, stream=stream)
+    return bufs
+
+
 def mla_prefill_host(host: dict, q_pos0: int, dev: dict, bufs: PrefillBuffers, out_host: torch.Tensor,
                      stream=None) -> torch.Tensor:
     """Host-buffer prefill: copy each pinned host input into its device buffer,

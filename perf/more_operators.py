@@ -326,7 +326,9 @@ def run(s):
             mla.mla_paged_gather(s["pages"], s["table"], s["row0"], s["cu"], s["rows"])
             return [s["q_nope"], s["q_pe"], s["rows"]]
         if kind == "keys":
-            mla.mla_paged_block_keys(s["pages"], s["table"], s["cu"], s["len"], s["keys"], _tokens(s))
+            if "T" not in s:                # a program knows how many tokens its batch has
+                s["T"] = _tokens(s)
+            mla.mla_paged_block_keys(s["pages"], s["table"], s["cu"], s["len"], s["keys"], s["T"])
             return s["keys"]
         if kind == "scores":
             mla.mla_paged_block_scores(s["q_lat"], s["q_pe"], s["keys"], s["table"], s["cu"], s["len"], s["scores"], scale=SCALE)

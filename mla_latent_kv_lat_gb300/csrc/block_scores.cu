@@ -8,7 +8,7 @@
 // On the 5th-generation tensor cores with the blocks as rows (M = 128) and the
 // queries of `gt` tokens, H each, as columns (N = gt H <= 128): the largest head of a
 // block then is a maximum over one thread's registers, with no exchange.
-//   * A work item is 128 blocks of one sequence and a run of its new tokens.  The mean
+//   * A run is 128 blocks of one sequence and consecutive new tokens of it.  The mean
 //     rows' latent part stays in tensor memory (256 columns), the RoPE part in shared
 //     memory; queries stream through a ring of 16 KB stages by TMA.  (With the rows in
 //     shared memory, both operands of each product would come from there: 128 bytes a
@@ -26,7 +26,7 @@
 namespace mla {
 namespace {
 
-constexpr int kTile = 128;                   // blocks of an item (MMA M)
+constexpr int kTile = 128;                   // blocks of a tile (MMA M)
 constexpr int kMaxN = 128;                   // (token, head) columns
 constexpr int kChunk = 128 * 128;            // 128 rows x 64 fp16
 constexpr int kChunks = kLatent / 64;
@@ -35,7 +35,8 @@ constexpr int kOffKr = 0;                                    // the mean rows' R
 constexpr int kOffFeed = kOffKr + kChunk;                    // mean rows on their way; two of them hold q_pe, too
 constexpr int kOffRing = kOffFeed + kFeed * kChunk;
 constexpr int kOffBar = kOffRing + kStages * kChunk;
-constexpr int kSmem = 1024 + kOffBar + 256;
+constexpr int kBarBytes = 512;
+constexpr int kSmem = 1024 + kOffBar + kBarBytes;
 static_assert(kSmem <= 232448, "shared memory");
 
 constexpr int kFeedWarp = 4, kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
@@ -45,80 +46,105 @@ constexpr uint64_t kGaveUpNs = 200000;       // from a wait that ran out to the 
 
 struct Args {
   BlockScoresArgs p;
-  int32_t gt;          // tokens of a group
+  int32_t gt_shift;    // log2 of the tokens of a group
   int32_t tiles;       // of a row of scores
-  int32_t n_slots;     // groups, at most
-  int32_t per;         // of them a CTA takes
+};
+
+// Where a CTA's share of the work begins.  Work: for each sequence and each tile that
+// some new token has a block in, the groups with such a token (the last ones, since
+// positions grow), plus kRunCost for the run's start: one run of costs over all
+// sequences, which the CTAs share evenly.
+constexpr int kRunCost = 3;            // mean rows' load, in groups
+struct Start {
+  int64_t lo, hi;      // this CTA's range in the run of costs
+  int64_t S;           // where sequence b's cost starts in it
+  int32_t b;           // the sequence that holds lo (B: nothing to do)
 };
 
 struct Bars {
   uint64_t full[kStages], empty[kStages];
-  uint64_t k_full, k_free;             // the item's mean rows are there; its last product is done
+  uint64_t k_full, k_free;             // the run's mean rows are there; its last product is done
   uint64_t qr_full[2], qr_empty[2];
   uint64_t s_full[2], s_empty[2];
   uint32_t tmem;
+  Start st;
+  long long red[kThreads / 32];
 };
-static_assert(sizeof(Bars) <= 256, "barriers");
-
-// Sequence b's groups get slots cu[b] / gt + b, ... (their ranges do not overlap).
-MLA_DEVINL int32_t slot_of_seq(const Args& a, int b) {
-  return max(0, min(a.p.T, __ldg(a.p.cu + b))) / a.gt + b;
-}
+static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 
 struct Group {
-  int32_t b, t0, nt;                   // tokens [t0, t0 + nt)
+  int32_t t0, nt;                      // tokens [t0, t0 + nt)
   int32_t pos;                         // of the first
-  bool live;                           // some token has a block in the tile
-  bool fresh;                          // the first live one of its sequence here: mean rows are loaded
+  bool fresh;                          // the first of its run: mean rows are loaded
 };
 
-// This CTA's groups in order; every role walks the same ones.  Whole warps.
-struct Walk {
-  int32_t g, g1, b, s0, s1, tile, last;
-  PagedSeq seq;
-  MLA_DEVINL void load(const Args& a) {
-    s0 = slot_of_seq(a, b);
-    s1 = b + 1 < a.p.B ? slot_of_seq(a, b + 1) : INT32_MAX;
+// A sequence's tiles and groups.
+struct Seq {
+  PagedSeq s;
+  MLA_DEVINL void load(const Args& a, int b) {
     bool bad;
-    seq = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
+    s = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
   }
-  MLA_DEVINL void init(const Args& a) {
-    tile = static_cast<int32_t>(blockIdx.x % static_cast<unsigned>(a.tiles));
-    g = static_cast<int32_t>(blockIdx.x / static_cast<unsigned>(a.tiles)) * a.per;
-    g1 = min(a.n_slots, g + a.per);
-    last = -1;
-    // the largest b with slot_of_seq(b) <= g, 32 at a time
-    int lo = 0, n = a.p.B;
-    const int lane = threadIdx.x & 31;
-    while (n > 1) {
-      const int step = (n + 31) / 32, m = lo + lane * step;
-      const uint32_t le = __ballot_sync(0xffffffffu, lane == 0 || (m < lo + n && slot_of_seq(a, m) <= g));
-      const int k = 31 - __clz(le);
-      n = min(step, lo + n - (lo + k * step));
-      lo += k * step;
+  MLA_DEVINL int tiles(const Args& a) const {
+    return s.n > 0 ? min(a.tiles, (((s.len - 1) >> kBlockShift) + kTile - 1) / kTile) : 0;
+  }
+  MLA_DEVINL int groups(const Args& a) const { return (s.n + (1 << a.gt_shift) - 1) >> a.gt_shift; }
+  // The first group whose last token has a block in `tile` (< tiles()).
+  MLA_DEVINL int first(const Args& a, int tile) const {
+    const int64_t need = (static_cast<int64_t>(tile) * kTile + 1) * kBlockRows - (s.len - s.n);   // tokens before one that has
+    return need <= 0 ? 0 : static_cast<int>(need >> a.gt_shift);
+  }
+  MLA_DEVINL int64_t cost(const Args& a) const {
+    int64_t c = 0;
+    for (int tile = tiles(a) - 1; tile >= 0; --tile) c += kRunCost + groups(a) - first(a, tile);
+    return c;
+  }
+};
+
+// This CTA's groups in order; every role walks the same ones.
+struct Walk {
+  int64_t lo, hi, S;
+  int32_t b, tile, tiles, i, i1;
+  Seq q;
+  MLA_DEVINL void init(const Args& a, const Start& st) {
+    lo = st.lo;
+    hi = st.hi;
+    S = st.S;
+    b = st.b;
+    tile = -1;
+    i = i1 = 0;
+    tiles = 0;
+    if (b < a.p.B) {
+      q.load(a, b);
+      tiles = q.tiles(a);
     }
-    b = lo;
-    load(a);
   }
   MLA_DEVINL bool next(const Args& a, Group& r) {
-    for (; g < g1; ++g) {
-      while (g >= s1) {
-        ++b;
-        load(a);
+    r.fresh = false;
+    while (i >= i1) {                  // the next run
+      ++tile;
+      while (tile >= tiles) {
+        if (++b >= a.p.B || S >= hi) return false;
+        q.load(a, b);
+        tiles = q.tiles(a);
+        tile = 0;
       }
-      const int64_t t = static_cast<int64_t>(g - s0) * a.gt;
-      if (g < s0 || t >= seq.n) continue;
-      r.b = b;
-      r.t0 = seq.q0 + static_cast<int32_t>(t);
-      r.nt = min(a.gt, seq.n - static_cast<int32_t>(t));
-      r.pos = seq.len - seq.n + static_cast<int32_t>(t);
-      r.live = (r.pos + r.nt - 1) >> kBlockShift > tile * kTile;
-      r.fresh = r.live && b != last;
-      if (r.live) last = b;
-      ++g;
-      return true;
+      if (S >= hi) return false;
+      const int first = q.first(a, tile), n = q.groups(a) - first;
+      const int64_t r0 = S + kRunCost;
+      S = r0 + n;
+      const int64_t p_lo = max(lo, r0), p_hi = min(hi, S);
+      if (p_lo >= p_hi) continue;
+      i = first + static_cast<int32_t>(p_lo - r0);
+      i1 = first + static_cast<int32_t>(p_hi - r0);
+      r.fresh = true;
     }
-    return false;
+    const int t = i << a.gt_shift;
+    r.t0 = q.s.q0 + t;
+    r.nt = min(1 << a.gt_shift, q.s.n - t);
+    r.pos = q.s.len - q.s.n + t;
+    ++i;
+    return true;
   }
 };
 
@@ -178,26 +204,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) record_bad_seqs(a.p.cu, a.p.seq_len, a.p.B, a.p.T, a.p.c.max_rows(), a.p.err);
 
-  const int H = a.p.H, N = a.gt * H;
+  {
+    // The run of all sequences' costs: each thread sums a share of the sequences, a scan
+    // gives its start, and the thread whose share holds the CTA's first unit finds the sequence.
+    const int per = (a.p.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.p.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.p.B, b0 + per);
+    Seq q;
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      q.load(a, b);
+      sum += q.cost(a);
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) B.red[warp] = incl;
+    if (threadIdx.x == 0) B.st = {0, 0, 0, a.p.B};
+    __syncthreads();
+    int64_t total = 0, S = incl - sum;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      total += B.red[w];
+      if (w < warp) S += B.red[w];
+    }
+    const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    if (lo < hi && sum > 0 && S <= lo && lo < S + sum) {
+      int b = b0;
+      for (; b < b1; ++b) {
+        q.load(a, b);
+        const int64_t c = q.cost(a);
+        if (lo < S + c) break;
+        S += c;
+      }
+      B.st = {lo, hi, S, b};
+    }
+    __syncthreads();
+  }
+  const int H = a.p.H, N = H << a.gt_shift;
   Walk walk;
-  walk.init(a);
+  walk.init(a, B.st);
   Group r;
-  const int j0 = walk.tile * kTile;
   bool ok = true;
 
   if (warp < kFeedWarp) {
     // ============================== maxima, output ==============================
-    const int j = j0 + 32 * warp + lane;
+    // First what needs no product: of each token, the scores behind its last tile.
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kFeedWarp + warp; t < a.p.T; t += static_cast<int64_t>(gridDim.x) * kFeedWarp) {
+      Seq q;
+      q.load(a, find_seq_warp(a.p.cu, a.p.B, static_cast<int32_t>(t)));
+      if (t < q.s.q0 || t >= q.s.q0 + q.s.n) continue;
+      // (the tiles of its group are computed whole)
+      const int last = min(q.s.n, ((static_cast<int>(t - q.s.q0) >> a.gt_shift) + 1) << a.gt_shift) - 1;
+      const int own = (q.s.len - q.s.n + last) >> kBlockShift;
+      if (own > a.p.W && lane == 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
+      for (int j = min((own + kTile - 1) / kTile, a.tiles) * kTile + lane; j < a.p.W; j += 32)
+        a.p.scores[t * a.p.stride + j] = -INFINITY;
+    }
     const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
     int u = 0;
     while (ok && walk.next(a, r)) {
+      const int j = walk.tile * kTile + 32 * warp + lane;
       float* out = a.p.scores + static_cast<int64_t>(r.t0) * a.p.stride + j;
-      if (walk.tile == 0 && lane == 0 && (r.pos + r.nt - 1) >> kBlockShift > a.p.W) record_error(a.p.err, MLA_ERR_INVALID_ARG);
-      if (!r.live) {
-        if (j < a.p.W)
-          for (int t = 0; t < r.nt; ++t) out[t * a.p.stride] = -INFINITY;
-        continue;
-      }
       const int sb = u & 1;
       ok = wait_all(&B.s_full[sb], (u >> 1) & 1, a);
       if (!ok) break;
@@ -239,23 +309,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool dead = false;
     int u = 0, k = 0;
     while (walk.next(a, r)) {
-      if (!r.live) continue;
       if (r.fresh) {
         // Unit ft + 128 i of a chunk: row ft / 8 + 16 i.  The sequence's blocks before
         // its last token's own are there; the others are zero.
-        const int n_there = (walk.seq.len - 1) >> kBlockShift;
+        const int n_there = (walk.q.s.len - 1) >> kBlockShift, j0 = walk.tile * kTile;
         int64_t src[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int j = j0 + (ft >> 3) + 16 * i;
           src[i] = -1;
           if (j < n_there) {
-            const int32_t id = __ldg(a.p.c.table + r.b * a.p.c.table_stride + (j >> per_shift));
+            const int32_t id = __ldg(a.p.c.table + walk.b * a.p.c.table_stride + (j >> per_shift));
             if (id >= 0 && id < a.p.c.n_pages) src[i] = (static_cast<int64_t>(id) << per_shift) + (j & ((1 << per_shift) - 1));
             else if (un == 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
           }
         }
-        // The last products of the item before have read its rows (and q_pe of all groups).
+        // The last products of the run before have read its rows (and q_pe of all groups).
         if (k > 0 && !dead) dead = !wait_all(&B.k_free, (k - 1) & 1, a);
         auto fetch = [&](uint8_t* to, int c) {
 #pragma unroll
@@ -337,7 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================== queries (TMA) ===============================
     int s = 0;                           // stages filled
     while (ok && walk.next(a, r)) {
-      if (!r.live) continue;
       for (int c = 0; c < kChunks; ++c, ++s) {
         const int st = s % kStages;
         if (s >= kStages) ok = wait_all(&B.empty[st], ((s / kStages) - 1) & 1, a);
@@ -354,9 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = tc::idesc_f16(128, N, false, false, false);
     int s = 0, u = 0, k = 0;
     while (ok && walk.next(a, r)) {
-      if (!r.live) continue;
       if (r.fresh) {
-        // the item before is done with its mean rows when its products are
+        // the run before is done with its mean rows when its products are
         if (k > 0) tc::mma_commit_warp(&B.k_free);
         ok = wait_all(&B.k_full, k & 1, a);
         if (!ok) break;
@@ -410,19 +477,13 @@ cudaError_t launch_block_scores(const BlockScoresArgs& p, cudaStream_t stream) {
   Args a = {};
   a.p = p;
   // Tokens of a group are of one sequence: with single tokens there is one.
-  a.gt = p.T > p.B ? kMaxN / p.H : 1;
+  if (p.T > p.B)
+    while ((2 * p.H << a.gt_shift) <= kMaxN) ++a.gt_shift;
   a.tiles = (p.W + kTile - 1) / kTile;
-  a.n_slots = p.T / a.gt + p.B;
-  const int64_t units = static_cast<int64_t>(a.n_slots) * a.tiles, sms = device_sm_count();
-  // Single tokens have mean rows of their own each, so there is nothing to keep; a
-  // chunk's tokens share theirs: about one run of groups for each SM.
-  a.per = p.T > p.B ? static_cast<int32_t>((units + sms - 1) / sms) : 1;
-  const int64_t grid = static_cast<int64_t>(a.tiles) * ((a.n_slots + a.per - 1) / a.per);
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
   CUtensorMap tq;
   const uint64_t qrows = static_cast<uint64_t>(p.T) * static_cast<uint64_t>(p.H);
   cudaError_t e = make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kChunks, kLatent * 2, 128, 64,
-                               static_cast<uint32_t>(a.gt * p.H), 1);
+                               static_cast<uint32_t>(p.H << a.gt_shift), 1);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
   int dev = 0;
@@ -434,7 +495,8 @@ cudaError_t launch_block_scores(const BlockScoresArgs& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_dependent(block_scores_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, stream, tq, a);
+  return launch_dependent(block_scores_kernel, dim3(static_cast<unsigned>(device_sm_count())), dim3(kThreads), kSmem, stream,
+                          tq, a);
 }
 
 }  // namespace mla

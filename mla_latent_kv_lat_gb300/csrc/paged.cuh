@@ -69,6 +69,20 @@ MLA_DEVINL int find_seq(const int32_t* cu, int B, int32_t j) {
   return lo;
 }
 
+// The same by a whole warp, 32 sequences a step: two chained loads for a batch of 1024 instead of ten.
+MLA_DEVINL int find_seq_warp(const int32_t* cu, int B, int32_t j) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, m = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane == 0 || (m < lo + n && __ldg(cu + m) <= j));
+    const int k = 31 - __clz(le);
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
 // Record the batch's invalid sequences (one block of a launch calls it).
 MLA_DEVINL void record_bad_seqs(const int32_t* cu, const int32_t* seq_len, int B, int32_t T, int64_t max_rows,
                                 int* err) {

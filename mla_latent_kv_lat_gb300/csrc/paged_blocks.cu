@@ -20,6 +20,8 @@ struct KeyCfg {
   static constexpr int kGroups = kE4m3 ? 8 : 4;         // row groups
   static constexpr int kThreads = kUnits * kGroups;     // 320, 288
   static constexpr int kRowsEach = kBlockRows / kGroups;
+  static constexpr int kAtOnce = 8;                     // loads of a thread under way
+  static_assert(!kE4m3 || kRowsEach == kAtOnce, "one pass");
 };
 
 MLA_DEVINL int64_t key_slot(const BlockKeysArgs& a, int b) {
@@ -27,7 +29,7 @@ MLA_DEVINL int64_t key_slot(const BlockKeysArgs& a, int b) {
 }
 
 template <bool kE4m3>
-__global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads) block_keys_kernel(const BlockKeysArgs a) {
+__global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads, kE4m3 ? 2 : 4) block_keys_kernel(const BlockKeysArgs a) {
   using C = KeyCfg<kE4m3>;
   __shared__ float part[C::kGroups][kRow];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -53,19 +55,22 @@ __global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads) block_keys_kernel(con
     constexpr int kBytes = kE4m3 ? kRowE4m3 : kRowF16;
     const uint8_t* src = a.c.pages + row0 * kBytes;
     if constexpr (!kE4m3) {
-      uint4 v[C::kRowsEach];
-#pragma unroll
-      for (int r = 0; r < C::kRowsEach; ++r)
-        v[r] = __ldg(reinterpret_cast<const uint4*>(src + (grp + C::kGroups * r) * kBytes) + unit);
       float x[8] = {};
+#pragma unroll 1
+      for (int r0 = 0; r0 < C::kRowsEach; r0 += C::kAtOnce) {
+        uint4 v[C::kAtOnce];
 #pragma unroll
-      for (int r = 0; r < C::kRowsEach; ++r) {
-        const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+        for (int r = 0; r < C::kAtOnce; ++r)
+          v[r] = __ldg(reinterpret_cast<const uint4*>(src + (grp + C::kGroups * (r0 + r)) * kBytes) + unit);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 f = f16x2_to_f32(w[q]);
-          x[2 * q] += f.x;
-          x[2 * q + 1] += f.y;
+        for (int r = 0; r < C::kAtOnce; ++r) {
+          const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 f = f16x2_to_f32(w[q]);
+            x[2 * q] += f.x;
+            x[2 * q + 1] += f.y;
+          }
         }
       }
 #pragma unroll
@@ -73,17 +78,17 @@ __global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads) block_keys_kernel(con
         *reinterpret_cast<float4*>(&part[grp][8 * unit + e]) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
     } else {
       // units 0-31: 16 codes each, half of a scale's block; 32-39: eight RoPE values
-      uint4 v[C::kRowsEach];
-      uint32_t d[C::kRowsEach];
+      uint4 v[C::kAtOnce];
+      uint32_t d[C::kAtOnce];
 #pragma unroll
-      for (int r = 0; r < C::kRowsEach; ++r) {
+      for (int r = 0; r < C::kAtOnce; ++r) {
         const uint8_t* row = src + (grp + C::kGroups * r) * kBytes;
         v[r] = __ldg(reinterpret_cast<const uint4*>(row) + unit);
         d[r] = unit < 32 ? __ldg(row + kE4m3ScaleOff + unit / 2) : 0u;
       }
       float x[16] = {};
 #pragma unroll
-      for (int r = 0; r < C::kRowsEach; ++r) {
+      for (int r = 0; r < C::kAtOnce; ++r) {
         const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
         if (unit < 32) {
           const uint32_t sc = e4m3_scale_f16x2(d[r]);
@@ -133,123 +138,211 @@ __global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads) block_keys_kernel(con
 // all; equal scores go to the lower block.  Written in ascending order, -1 behind.
 //
 // A score becomes a key that orders as its value (larger is better; -0 as 0; a NaN
-// below everything).  The key of the last one taken is found bit by bit: the largest
-// x with at least R candidates of keys >= x.  One block of threads a token; its keys
-// stay in registers (up to kHeld a thread; for longer rows they are read again in
-// each step).  Latency-bound: 32 counts over the block, ~60 cycles each.
+// below everything).  The key of the last one taken is found bit by bit, the largest x
+// with at least R candidates of keys >= x, or until some x has exactly R.  A block of
+// kWarps warps takes a token, with kPer keys in each thread's registers: a warp alone
+// counts with no barrier, and with many tokens that is what it is bound by
+// (instructions, two a key and bit); more warps are quicker for one token.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32, kHeld = 16;
-
 MLA_DEVINL uint32_t score_key(float s) {
   const uint32_t u = __float_as_uint(s + 0.f);            // (-0 + 0 = 0)
   if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 1u;         // NaN; -inf is 0x007FFFFF
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-template <bool kHold>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectBlocksArgs a) {
-  __shared__ int s_cnt[2][kSelWarps];
-  __shared__ int2 s_wave[kSelWarps];
+// A token's part of the choice.
+struct Choice {
+  int own;            // its block
+  int c0, n;          // candidates [c0, c0 + n); the others up to `own` are taken as they are
+  int R;              // candidates to take
+};
+// False: the token gets nothing (padding, or recorded).
+MLA_DEVINL bool choice_of(const SelectBlocksArgs& a, int64_t t, int nthreads, Choice& c) {
+  const int b = find_seq_warp(a.cu, a.B, static_cast<int32_t>(t));
+  bool bad;
+  const PagedSeq s = paged_seq(a.cu, a.seq_len, b, a.T, INT32_MAX - 4096, bad);
+  if (t < s.q0 || t >= s.q0 + s.n) return false;
+  c.own = (s.len - s.n + static_cast<int>(t - s.q0)) >> kBlockShift;
+  if (c.own >= a.W) {                    // its blocks have no scores
+    if (threadIdx.x == 0) {
+      record_error(a.err, MLA_ERR_INVALID_ARG);
+      a.counts[t] = 0;
+    }
+    for (int i = threadIdx.x; i < a.K; i += nthreads) a.blocks[t * a.K + i] = -1;
+    return false;
+  }
+  const int c1 = max(0, c.own - a.n_local + 1);
+  c.c0 = min(a.n_sink, c1);
+  c.n = c1 - c.c0;
+  c.R = min(c.n, a.K - (c.own + 1 - c.n));
+  return true;
+}
+// What needs no scores: the first blocks, the last, what lies behind them, the count;
+// with R == n all.
+MLA_DEVINL void write_sure(const SelectBlocksArgs& a, int64_t t, int nthreads, const Choice& c) {
+  int32_t* out = a.blocks + t * a.K;
+  const int total = c.own + 1 - c.n + c.R, head = c.R == c.n ? total : c.c0;
+  for (int i = threadIdx.x; i < a.K; i += nthreads) {
+    if (i < head) out[i] = i;
+    else if (i >= c.c0 + c.R) out[i] = i < total ? c.own - (total - 1 - i) : -1;
+  }
+  if (threadIdx.x == 0) a.counts[t] = total;
+}
+
+template <int kWarps, int kPer>
+__global__ void __launch_bounds__(32 * kWarps) select_blocks_kernel(const SelectBlocksArgs a) {
+  constexpr int kN = 32 * kWarps, kWaves = kPer * kWarps, kEach = (kWaves + 31) / 32;
+  __shared__ int s_cnt[2][kWarps];
+  __shared__ uint32_t s_wave[32 * kEach];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) record_bad_seqs(a.cu, a.seq_len, a.B, a.T, INT32_MAX - 4096, a.err);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t t = blockIdx.x;
-  const int b = find_seq(a.cu, a.B, static_cast<int32_t>(t));
-  bool bad;
-  const PagedSeq s = paged_seq(a.cu, a.seq_len, b, a.T, INT32_MAX - 4096, bad);
-  if (t < s.q0 || t >= s.q0 + s.n) return;
-  const int own = (s.len - s.n + static_cast<int>(t - s.q0)) >> kBlockShift;
-  int32_t* out = a.blocks + t * a.K;
-  if (own >= a.W) {                      // its blocks have no scores
-    if (tid == 0) {
-      record_error(a.err, MLA_ERR_INVALID_ARG);
-      a.counts[t] = 0;
-    }
-    for (int i = tid; i < a.K; i += kSelThreads) out[i] = -1;
-    return;
-  }
-  // candidates: [c0, c1); the others up to `own` are taken as they are
-  const int c1 = max(0, own - a.n_local + 1), c0 = min(a.n_sink, c1), n = c1 - c0;
-  const int forced = own + 1 - n, R = min(n, a.K - forced), total = forced + R;
-  const float* src = a.scores + t * a.stride + c0;
-  uint32_t held[kHold ? kHeld : 1];
-  if constexpr (kHold) {
+  Choice c;
+  if (!choice_of(a, t, kN, c)) return;
+  const float* src = a.scores + t * a.stride + c.c0;
+  uint32_t key[kPer];                    // of candidates tid + k kN (0: there is none)
+  if (c.R > 0 && c.R < c.n) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const int i = tid + k * kSelThreads;
-      held[k] = i < n && R < n ? score_key(__ldg(src + i)) : 0u;
-    }
+    for (int k = 0; k < kPer; ++k) key[k] = tid + k * kN < c.n ? score_key(__ldg(src + tid + k * kN)) : 0u;
   }
-  auto key = [&](int k) -> uint32_t {    // of candidate tid + k kSelThreads (0: there is none)
-    if constexpr (kHold) return held[k];
-    const int i = tid + k * kSelThreads;
-    return i < n ? score_key(__ldg(src + i)) : 0u;
-  };
-  const int steps = (n + kSelThreads - 1) / kSelThreads;
-  // the largest x with at least R keys >= x, and how many keys are larger
-  uint32_t x = 0;
-  int above = 0;
-  if (R > 0 && R < n) {
-    int buf = 0;
-    auto count = [&](uint32_t y) -> int {
-      int c = 0;
-      if constexpr (kHold) {
+  write_sure(a, t, kN, c);
+  if (c.R == 0 || c.R == c.n) return;
+  int buf = 0;
+  auto count = [&](uint32_t y) -> int {
+    int n = 0;
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) c += held[k] >= y;
-      } else {
-        for (int k = 0; k < steps; ++k) c += key(k) >= y;
-      }
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0) s_cnt[buf][warp] = c;
+    for (int k = 0; k < kPer; ++k) n += key[k] >= y;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if constexpr (kWarps > 1) {
+      if (lane == 0) s_cnt[buf][warp] = n;
       __syncthreads();
-      c = 0;
+      n = 0;
 #pragma unroll
-      for (int w = 0; w < kSelWarps; ++w) c += s_cnt[buf][w];
+      for (int w = 0; w < kWarps; ++w) n += s_cnt[buf][w];
       buf ^= 1;
-      return c;
-    };
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t y = x | (1u << bit);
-      if (count(y) >= R) x = y;
     }
-    above = x == 0xFFFFFFFFu ? 0 : count(x + 1);
+    return n;
+  };
+  uint32_t x = 0;
+  int least = c.n;                       // keys >= x
+  for (int bit = 31; bit >= 0 && least != c.R; --bit) {
+    const uint32_t y = x | (1u << bit);
+    const int n = count(y);
+    if (n >= c.R) {
+      x = y;
+      least = n;
+    }
   }
-  // written in ascending order: a wave of kSelThreads blocks at a time
-  const int ties = R < n ? R - above : 0;      // of the keys equal to x, the first ones
-  int taken = 0, equal = 0;                    // before this wave
-  for (int i0 = 0; i0 <= own; i0 += kSelThreads) {
-    const int i = i0 + tid;                    // block
-    const int c = i - c0;                      // candidate
-    uint32_t kx = 0;
-    const bool cand = c >= 0 && c < n;
-    if (cand && R < n) kx = score_key(__ldg(src + c));
-    const bool sure = i <= own && (!cand || R == n || (R > 0 && kx > x));
-    const bool tie = cand && R < n && R > 0 && kx == x;
-    const uint32_t tie_w = __ballot_sync(0xffffffffu, tie), sure_w = __ballot_sync(0xffffffffu, sure);
-    if (lane == 0) s_wave[warp] = make_int2(__popc(sure_w), __popc(tie_w));
-    __syncthreads();
-    int sure_b = 0, tie_b = 0, sure_all = 0, tie_all = 0;
+  // Keys > x are taken, and of those equal to it the first `ties`.
+  const int ties = least == c.R ? c.R : c.R - (x == 0xFFFFFFFFu ? 0 : count(x + 1));
+  // Wave k of warp w, in this order, holds kWaves x 32 candidates in order.
+  uint32_t wave[kPer];                   // larger ones in the low half, equal ones in the high
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-      const int2 v = s_wave[w];
-      if (w < warp) { sure_b += v.x; tie_b += v.y; }
-      sure_all += v.x;
-      tie_all += v.y;
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t gt = __ballot_sync(0xffffffffu, key[k] > x), eq = __ballot_sync(0xffffffffu, key[k] == x);
+    wave[k] = __popc(gt) | __popc(eq) << 16;
+    if (lane == 0) s_wave[k * kWarps + warp] = wave[k];
+  }
+  if constexpr (kWarps > 1) __syncthreads();
+  else __syncwarp();
+  uint32_t mine[kEach], sum = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int w = lane * kEach + e;
+    mine[e] = sum;
+    sum += w < kWaves ? s_wave[w] : 0u;
+  }
+  uint32_t before = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  before -= sum;
+  int32_t* out = a.blocks + t * a.K + c.c0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t gt = __ballot_sync(0xffffffffu, key[k] > x), eq = __ballot_sync(0xffffffffu, key[k] == x);
+    const int w = k * kWarps + warp;
+    uint32_t p = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const uint32_t v = __shfl_sync(0xffffffffu, before + mine[e], w / kEach);
+      if (w % kEach == e) p = v;
     }
     const uint32_t below = (1u << lane) - 1;
-    const int sure_r = taken + sure_b + __popc(sure_w & below);          // sure ones before block i
-    const int tie_r = equal + tie_b + __popc(tie_w & below);             // ties before block i
-    if (sure || (tie && tie_r < ties)) {
-      const int at = sure_r + min(tie_r, ties);
-      if (at < a.K) out[at] = i;
+    const int gt_r = static_cast<int>(p & 0xFFFFu) + __popc(gt & below), eq_r = static_cast<int>(p >> 16) + __popc(eq & below);
+    if (key[k] > x || (key[k] == x && eq_r < ties)) out[gt_r + min(eq_r, ties)] = c.c0 + tid + k * kN;
+  }
+}
+
+// Rows of any length: the keys are read again for each bit.
+constexpr int kLongWarps = 8, kLongThreads = 32 * kLongWarps;
+
+__global__ void __launch_bounds__(kLongThreads) select_long_kernel(const SelectBlocksArgs a) {
+  __shared__ int s_cnt[2][kLongWarps];
+  __shared__ int2 s_wave[kLongWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0) record_bad_seqs(a.cu, a.seq_len, a.B, a.T, INT32_MAX - 4096, a.err);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t t = blockIdx.x;
+  Choice c;
+  if (!choice_of(a, t, kLongThreads, c)) return;
+  write_sure(a, t, kLongThreads, c);
+  if (c.R == 0 || c.R == c.n) return;
+  const float* src = a.scores + t * a.stride + c.c0;
+  int buf = 0;
+  auto count = [&](uint32_t y) -> int {
+    int n = 0;
+#pragma unroll 4
+    for (int i = tid; i < c.n; i += kLongThreads) n += score_key(__ldg(src + i)) >= y;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) s_cnt[buf][warp] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kLongWarps; ++w) n += s_cnt[buf][w];
+    buf ^= 1;
+    return n;
+  };
+  uint32_t x = 0;
+  int least = c.n;
+  for (int bit = 31; bit >= 0 && least != c.R; --bit) {
+    const uint32_t y = x | (1u << bit);
+    const int n = count(y);
+    if (n >= c.R) {
+      x = y;
+      least = n;
     }
-    taken += sure_all;
-    equal += tie_all;
+  }
+  const int ties = least == c.R ? c.R : c.R - (x == 0xFFFFFFFFu ? 0 : count(x + 1));
+  int32_t* out = a.blocks + t * a.K + c.c0;
+  int larger = 0, equal = 0;                   // before this wave
+  for (int i0 = 0; i0 < c.n; i0 += kLongThreads) {
+    const uint32_t key = i0 + tid < c.n ? score_key(__ldg(src + i0 + tid)) : 0u;
+    const uint32_t gt = __ballot_sync(0xffffffffu, key > x), eq = __ballot_sync(0xffffffffu, key == x);
+    if (lane == 0) s_wave[warp] = make_int2(__popc(gt), __popc(eq));
+    __syncthreads();
+    const uint32_t below = (1u << lane) - 1;
+    int gt_r = larger + __popc(gt & below), eq_r = equal + __popc(eq & below);
+#pragma unroll
+    for (int w = 0; w < kLongWarps; ++w) {
+      const int2 v = s_wave[w];
+      if (w < warp) { gt_r += v.x; eq_r += v.y; }
+      larger += v.x;
+      equal += v.y;
+    }
+    if (key > x || (key == x && eq_r < ties)) out[gt_r + min(eq_r, ties)] = c.c0 + i0 + tid;
     __syncthreads();
   }
-  for (int i = total + tid; i < a.K; i += kSelThreads) out[i] = -1;
-  if (tid == 0) a.counts[t] = total;
+}
+
+template <int kWarps, int kPer>
+cudaError_t launch_select(const SelectBlocksArgs& a, cudaStream_t stream) {
+  return launch_dependent(select_blocks_kernel<kWarps, kPer>, dim3(static_cast<unsigned>(a.T)), dim3(32 * kWarps), 0, stream, a);
 }
 
 }  // namespace
@@ -265,8 +358,12 @@ cudaError_t launch_block_keys(const BlockKeysArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_select_blocks(const SelectBlocksArgs& a, cudaStream_t stream) {
-  return launch_dependent(a.W <= kSelThreads * kHeld ? select_blocks_kernel<true> : select_blocks_kernel<false>,
-                          dim3(static_cast<unsigned>(a.T)), dim3(kSelThreads), 0, stream, a);
+  // More tokens than the SMs hold blocks of few warps: as few warps as the row's keys fit.
+  const bool many = a.T > 8 * device_sm_count();
+  if (a.W <= 1024) return many ? launch_select<1, 32>(a, stream) : launch_select<4, 8>(a, stream);
+  if (a.W <= 2048) return many ? launch_select<2, 32>(a, stream) : launch_select<8, 8>(a, stream);
+  if (a.W <= 8192) return launch_select<8, 32>(a, stream);
+  return launch_dependent(select_long_kernel, dim3(static_cast<unsigned>(a.T)), dim3(kLongThreads), 0, stream, a);
 }
 
 }  // namespace mla

@@ -167,13 +167,10 @@ struct __align__(16) Rec {     // the block that starts in cluster c and ends in
 // 28 us, 64 66 and 60, 256 153 and 164.
 constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 16, kStageReads = 8;
 
-// With listed blocks every token converts its own: staging pays when the batch's lists
-// name a row kStageReads times on average.
-MLA_DEVINL bool worth_staging(const PagedAttnArgs& a, const PagedSeq& s) {
-  if (a.blocks != nullptr)
-    return s.n >= kStageBlocks && static_cast<int64_t>(s.n) * a.K * kBK >= static_cast<int64_t>(kStageReads) * s.len;
-  return static_cast<int64_t>(s.n) * a.H > (kStageBlocks - 1) * kRows;
-}
+// The lists of blocks that a launch goes by.
+enum Lists { kNoLists, kTokenLists, kGroupLists };
+// Of tokens in groups: room for as many entries.
+constexpr int64_t kGroupEntries = int64_t{1} << 21;
 
 // Which sequences a launch takes.
 enum Take : int32_t { kTakeAll, kTakeStaged, kTakeUnstaged };
@@ -184,11 +181,26 @@ struct TcArgs {
   float* ws_o;        // fp32 [2 G][128][512] partials, normalised by their own sums
   float* ws_ml;       // fp32 [2 G][128][2] running maximum (log2 units, less kPShift) and sum
   Rec* rec;           // [G]
-  int32_t* stage_base;   // [B] a sequence's first staged row, -1: not staged (unless take is kTakeAll)
+  int32_t* stage_base;   // [B] a sequence's first staged row, -1: not staged (unless take is kTakeAll);
+                         // [kStageSeqs]: whether some sequence with new tokens is not
   uint16_t* stage;       // fp16 [kStageRows][512]
   int32_t n_slots;
   int32_t n_rows;     // rows of the page pool
+  // kGroupLists: 2^gt_shift tokens share a block; a slot's entries (the tiles that some
+  // token of it lists: first key, tokens), 2^gt_shift K apart, and their number
+  int32_t gt_shift;
+  uint2* group_lists;
+  int32_t* group_counts;
 };
+
+// With lists every block converts its own tiles: staging pays when the batch's lists name
+// a row kStageReads times on average (a group's tokens name each about twice).
+MLA_DEVINL bool worth_staging(const TcArgs& t, const PagedSeq& s) {
+  const PagedAttnArgs& a = t.p;
+  if (a.blocks == nullptr) return static_cast<int64_t>(s.n) * a.H > (kStageBlocks - 1) * kRows;
+  const int shift = max(0, t.gt_shift - 1);
+  return s.n >= kStageBlocks && static_cast<int64_t>(s.n >> shift) * a.K * kBK >= static_cast<int64_t>(kStageReads) * s.len;
+}
 
 // ---------------------------------------------------------------------------
 // Blocks.  Sequence b's blocks get slots cu[b] H / 128 + b, ...: these ranges
@@ -196,23 +208,26 @@ struct TcArgs {
 // floor(cu[b] H / 128) + b), so a slot's sequence is found by a search in cu
 // alone, with no prefix sums over the batch.  Slots without a block cost 0.
 // ---------------------------------------------------------------------------
-// With listed blocks (kListed) a block is the H rows of one token, whose list its
-// tiles are, and its slot is the token.
-template <bool kListed>
-MLA_DEVINL int64_t slot_of_seq(const PagedAttnArgs& a, int b) {
-  const int32_t c = max(0, min(a.T, __ldg(a.cu + b)));
-  return kListed ? c : static_cast<int64_t>(c) * a.H / kRows + b;
+// With lists (kLists) a block is the H rows of one token, its tiles are the token's
+// list and its slot the token; or, in groups, the rows of 2^gt_shift tokens, their
+// lists' union and a slot as above.
+template <int kLists>
+MLA_DEVINL int64_t slot_of_seq(const TcArgs& t, int b) {
+  const int32_t c = max(0, min(t.p.T, __ldg(t.p.cu + b)));
+  if (kLists == kGroupLists) return (c >> t.gt_shift) + b;
+  return kLists == kTokenLists ? c : static_cast<int64_t>(c) * t.p.H / kRows + b;
 }
 
 struct Item {
   int32_t b;                  // sequence
   int32_t kend, wlo;          // keys some row of the block sees: [0, n_sink) and [wlo, kend)
   int32_t first, sink_tiles;  // tile t of the block is t < sink_tiles ? t : first + t - sink_tiles
-                              // (kListed: entry t of the token's list, which has `first` entries)
+                              // (kLists: entry t of the list, which has `first` entries)
   int32_t t_lo, n_tiles;      // this piece: tiles [t_lo, t_lo + n_tiles)
   int32_t nvalid;             // rows
   int32_t pos0;               // position of the sequence's first new token
   uint32_t row0;              // first row within the sequence's new rows
+  int32_t slot;               // (kLists)
   int64_t qrow0;              // first row in the token array
   bool open;                  // the block goes on past this piece
   bool once;                  // the sequence has one or two blocks
@@ -233,7 +248,7 @@ struct Item {
 };
 
 // Walks the slots in order.
-template <bool kListed>
+template <int kLists>
 struct Walker {
   int b;                // sequence of the last slot asked for
   int64_t s0, s1;       // its first slot, and the next sequence's
@@ -242,8 +257,8 @@ struct Walker {
 
   MLA_DEVINL void load(const TcArgs& t) {
     const PagedAttnArgs& a = t.p;
-    s0 = slot_of_seq<kListed>(a, b);
-    s1 = b + 1 < a.B ? slot_of_seq<kListed>(a, b + 1) : INT64_MAX;
+    s0 = slot_of_seq<kLists>(t, b);
+    s1 = b + 1 < a.B ? slot_of_seq<kLists>(t, b + 1) : INT64_MAX;
     bool bad;
     seq = paged_seq(a.cu, a.seq_len, b, a.T, a.c.max_rows(), bad);
     rows = static_cast<uint32_t>(seq.n) * static_cast<uint32_t>(a.H);
@@ -254,7 +269,7 @@ struct Walker {
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int m = (lo + hi) >> 1;
-      if (slot_of_seq<kListed>(a, m) <= g) lo = m; else hi = m;
+      if (slot_of_seq<kLists>(t, m) <= g) lo = m; else hi = m;
     }
     b = lo;
     load(t);
@@ -267,20 +282,26 @@ struct Walker {
       load(t);
     }
     const int64_t i = g - s0;
-    if constexpr (kListed) {
-      if (i < 0 || i * a.H >= rows) return 0;
-      const int32_t listed = __ldg(a.counts + g);
-      if (listed < 0 || listed > a.K) record_error(a.err, MLA_ERR_INVALID_ARG);
+    if constexpr (kLists != kNoLists) {
+      const int gt = kLists == kGroupLists ? 1 << t.gt_shift : 1;
+      if (i < 0 || i * gt * a.H >= rows) return 0;
+      const int32_t tok = static_cast<int32_t>(i) * gt, nt = min(gt, seq.n - tok);
+      int32_t listed = __ldg((kLists == kGroupLists ? t.group_counts : a.counts) + g);
+      if (kLists == kTokenLists && (listed < 0 || listed > a.K)) {
+        record_error(a.err, MLA_ERR_INVALID_ARG);
+        listed = max(0, min(listed, a.K));
+      }
       it.b = b;
-      it.nvalid = a.H;
+      it.nvalid = nt * a.H;
       it.once = seq.n <= 2;
-      it.row0 = static_cast<uint32_t>(i) * static_cast<uint32_t>(a.H);
-      it.qrow0 = g * a.H;
+      it.row0 = static_cast<uint32_t>(tok) * static_cast<uint32_t>(a.H);
+      it.slot = static_cast<int32_t>(g);
+      it.qrow0 = static_cast<int64_t>(seq.q0 + tok) * a.H;
       it.pos0 = seq.len - seq.n;
-      it.kend = it.pos0 + static_cast<int32_t>(i) + 1;
+      it.kend = it.pos0 + tok + nt;
       it.wlo = it.sink_tiles = 0;
-      it.first = max(0, min(listed, a.K));
-      return max(1, it.first);         // a token with no block goes through one tile of nothing: its output is zero
+      it.first = listed;
+      return max(1, listed);           // tokens with no block go through one tile of nothing: their output is zero
     }
     if (i < 0 || i * kRows >= rows) return 0;
     const uint32_t H = static_cast<uint32_t>(a.H), r0 = static_cast<uint32_t>(i) * kRows;
@@ -310,9 +331,9 @@ struct Start {
 };
 
 // This cluster's pieces in order; every role walks the same sequence.
-template <bool kListed>
+template <int kLists>
 struct Iter {
-  Walker<kListed> w;
+  Walker<kLists> w;
   const Start* st;
   int64_t lo, hi, S;
   int32_t g;
@@ -345,15 +366,24 @@ struct Iter {
   }
 };
 
-// kListed: a warp holds 32 entries of the piece's list at a time, tile t's in lane t % 32.
-MLA_DEVINL int32_t list_entry(const TcArgs& a, const Item& it, int t) {
+// kLists: a warp holds 32 entries of the piece's list at a time, tile t's in lane t % 32:
+// the tile's first key, and the tokens of the group that list it.  What names no block
+// before or with a token's own, or nothing, becomes keys that no row sees.
+struct Entry {
+  int32_t key;
+  uint32_t tokens;
+};
+template <int kLists>
+MLA_DEVINL Entry list_entry(const TcArgs& a, const Item& it, int t) {
+  const Entry none = {(it.kend + kBK - 1) / kBK * kBK, 0u};
   const int x = it.t_lo + t;
-  return t < it.n_tiles && x < it.first ? __ldg(a.p.blocks + it.qrow0 / a.p.H * a.p.K + x) : -1;
-}
-// First key of the tile that a list's entry names: of a block behind the token's own, or
-// of none, keys that no row sees.
-MLA_DEVINL int entry_key(const Item& it, int32_t e) {
-  return e >= 0 && e <= (it.kend - 1) / kBK ? e * kBK : (it.kend + kBK - 1) / kBK * kBK;
+  if (t >= it.n_tiles || x >= it.first) return none;
+  if constexpr (kLists == kGroupLists) {
+    const uint2 e = __ldg(a.group_lists + ((static_cast<int64_t>(it.slot) << a.gt_shift) * a.p.K + x));
+    return {static_cast<int32_t>(e.x), e.y};
+  }
+  const int32_t e = __ldg(a.p.blocks + static_cast<int64_t>(it.slot) * a.p.K + x);
+  return e >= 0 && e <= (it.kend - 1) / kBK ? Entry{e * kBK, 1u} : none;
 }
 
 // Keys [k, k + n) hold one that some row of the block sees.
@@ -625,8 +655,8 @@ MLA_DEVINL void store_f16(const Codes& c, uint8_t* lat, int pt, int j) {
 // are (32 tokens at 4K-32K rows, 16 heads: 138 us, without it 147; 64 heads 143 and
 // 149, 96 heads 149 and 152).  Its own instantiation, because the tests make full
 // blocks 2% slower; for e4m3 pages it gains nothing.
-// kListed: each token has its own tiles (mla_attn_paged_blocks).
-template <bool kE4m3, bool kFewRows, bool kLong, bool kListed>
+// kLists: tiles are listed (mla_attn_paged_blocks).
+template <bool kE4m3, bool kFewRows, bool kLong, int kLists>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                       const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_scale,
@@ -651,6 +681,17 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   const int c = static_cast<int>(blockIdx.x >> 1), G = static_cast<int>(gridDim.x >> 1);
   constexpr int NT = threads(kE4m3);
 
+  // Every sequence is staged: the kernel for fp16 pages has taken them all.
+  if constexpr (kE4m3) {
+    if (a.take == kTakeUnstaged) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (a.stage_base[kStageSeqs] == 0) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (rank == 0 && threadIdx.x == 0) a.rec[c].nvalid = 0;
+        return;
+      }
+    }
+  }
   // ---- setup ---------------------------------------------------------------
   if (warp == kPvWarp) {
     // a lane per barrier: how many arrivals complete a phase
@@ -708,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     long long* red = reinterpret_cast<long long*>(sStg);
     const int per = (a.n_slots + NT - 1) / NT;
     const int g0 = min(a.n_slots, static_cast<int>(threadIdx.x) * per), g1 = min(a.n_slots, g0 + per);
-    Walker<kListed> w;
+    Walker<kLists> w;
     Item it;
     long long sum = 0;
     if (g0 < g1) {
@@ -741,7 +782,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     if (total < (1 << 24)) {
       const uint32_t units = static_cast<uint32_t>(total);
       const float blocks =                                        // about
-          kListed ? static_cast<float>(a.p.T)
+          kLists == kTokenLists ? static_cast<float>(a.p.T)
                   : fmaxf(static_cast<float>(a.p.B), static_cast<float>(a.p.T) * a.p.H * (1.f / kRows));
       share = kPieceCost + 2;
       if (units > blocks * share) {
@@ -790,7 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   const uint32_t tmem = B.tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  Iter<kListed> items;
+  Iter<kLists> items;
   items.init(B.st);
   Item it;
   bool ok = true;
@@ -819,19 +860,25 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       const bool rvalid = i < it.nvalid;
       const bool mine = !kFewRows || 32 * q4 + 16 * static_cast<int>(rank) < it.nvalid;
       // keys [wl, lim] and the sinks are visible to this row
-      const int lim = rvalid && !kListed ? it.pos0 + static_cast<int>((it.row0 + i) / static_cast<uint32_t>(a.p.H))
-                                         : it.kend - 1;
-      const int wl = !kListed && a.p.window > 0 ? max(0, lim - a.p.window + 1) : 0;
-      int32_t entries = -1;
+      const int lim_row = rvalid && kLists != kTokenLists
+                              ? it.pos0 + static_cast<int>((it.row0 + i) / static_cast<uint32_t>(a.p.H)) : it.kend - 1;
+      const int wl = kLists == kNoLists && a.p.window > 0 ? max(0, lim_row - a.p.window + 1) : 0;
+      const int pos_g = it.pos0 + static_cast<int>(it.row0 / static_cast<uint32_t>(a.p.H));   // of the first token
+      Entry entries = {0, 0u};
       float m_run = -INFINITY, l_h = 0.f;      // the running maximum, less kPShift; the sum
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int sb = u & 1;
         const uint32_t ph = (u >> 1) & 1, xph = (kFewRows ? xu : u) & 1;
-        int base;
-        if constexpr (kListed) {
-          if ((t & 31) == 0) entries = list_entry(a, it, t + lane);
-          base = entry_key(it, __shfl_sync(0xffffffffu, entries, t & 31));
+        int base, lim = lim_row, kend = it.kend;      // of the tile
+        if constexpr (kLists != kNoLists) {
+          if ((t & 31) == 0) entries = list_entry<kLists>(a, it, t + lane);
+          base = __shfl_sync(0xffffffffu, entries.key, t & 31);
+          if constexpr (kLists == kGroupLists) {
+            const uint32_t tokens = __shfl_sync(0xffffffffu, entries.tokens, t & 31);
+            if ((tokens >> (lim_row - pos_g) & 1) == 0) lim = -1;
+            kend = tokens ? pos_g + 32 - __clz(tokens) : 0;      // keys that the last of its tokens sees
+          }
         } else {
           base = it.key_tile(t) * kBK;
         }
@@ -863,7 +910,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             s[2 * g] = add2(s[2 * g], x.x);
             s[2 * g + 1] = add2(s[2 * g + 1], x.y);
           }
-          if (k0 + 15 > lim || (!kListed && k0 < wl && k0 + 15 >= a.p.n_sink)) {
+          if (k0 + 15 > lim || (kLists == kNoLists && k0 < wl && k0 + 15 >= a.p.n_sink)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               float2 v = unpack2(s[e]);
@@ -940,10 +987,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             }
             // A tile with keys that no row of the block sees: their values must
             // not enter P V (0 x NaN).  The score product has read the tile.
-            if (base + kBK > it.kend || (!kListed && base < it.wlo && base + kBK > a.p.n_sink)) {
+            if (base + kBK > kend || (kLists == kNoLists && base < it.wlo && base + kBK > a.p.n_sink)) {
               uint8_t* stage = sLat + ((u + kQSlots * (k + 1)) % kLatStages) * kLatStage;
               for (int q = threadIdx.x; q < kBK * 32; q += 256)
-                if (!key_visible(a, it, base + (q >> 5)))
+                if (kLists == kGroupLists ? base + (q >> 5) >= kend : !key_visible(a, it, base + (q >> 5)))
                   *reinterpret_cast<uint4*>(stage + (q >> 8) * kGroup + ((q >> 3) & 3) * kChunk + ((q >> 5) & 7) * 128 +
                                             (q & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
@@ -1097,7 +1144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
         ok = wait_cl(&B.pv_done[(m - 1) & 1], ((m - 1) >> 1) & 1, a);
         if (!ok) break;
         tc::fence_after_sync();
-        Iter<kListed> ahead = items;            // (the output looks the piece up again)
+        Iter<kLists> ahead = items;            // (the output looks the piece up again)
         if (!ahead.next(a, it)) break;
         move_o(tmem + lanes + kTmO, stg, partial(it), it.nvalid - 32 * q4, moved, g, 1.f, nullptr);
         moved = true;
@@ -1297,17 +1344,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       record_error(a.p.err, MLA_ERR_INVALID_ARG);
       return a.n_rows;
     };
-    // kListed: lane l looks tile t + l's row up (and its staged row), 32 tiles at a time.
+    // kLists: lane l looks tile t + l's row up (and its staged row), 32 tiles at a time.
     auto listed_rows = [&](int t, int32_t base, int& srow) -> int {
       srow = kStageRows;
-      const int x = it.t_lo + t + lane;
-      if (t + lane >= it.n_tiles || x >= it.first) return a.n_rows;
-      const int32_t e = list_entry(a, it, t + lane);
-      if (e >= 0 && e <= (it.kend - 1) / kBK) {
-        const int key = e * kBK;
-        const int32_t id = __ldg(a.p.c.table + it.b * a.p.c.table_stride + (key >> a.p.c.page_shift));
-        srow = base + key;
-        if (id >= 0 && id < a.p.c.n_pages) return (id << a.p.c.page_shift) + (key & ((1 << a.p.c.page_shift) - 1));
+      if (t + lane >= it.n_tiles || it.t_lo + t + lane >= it.first) return a.n_rows;
+      const Entry e = list_entry<kLists>(a, it, t + lane);
+      if (e.tokens != 0) {
+        const int32_t id = __ldg(a.p.c.table + it.b * a.p.c.table_stride + (e.key >> a.p.c.page_shift));
+        srow = base + e.key;
+        if (id >= 0 && id < a.p.c.n_pages) return (id << a.p.c.page_shift) + (e.key & ((1 << a.p.c.page_shift) - 1));
       }
       record_error(a.p.err, MLA_ERR_INVALID_ARG);
       return a.n_rows;
@@ -1318,7 +1363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       const int32_t base = staged ? __ldg(a.stage_base + it.b) : 0;
       int srows = 0, rows = 0;
       int32_t id0 = 0;                         // (on its way while the queries are asked for)
-      if constexpr (kListed) rows = listed_rows(0, base, srows);
+      if constexpr (kLists != kNoLists) rows = listed_rows(0, base, srows);
       else id0 = entry(0);
 #pragma unroll 1
       for (int q = 0; q < kQSlots; ++q) {           // the queries: 128 rows x 64 dims twice a stage
@@ -1334,12 +1379,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       }
       if (!ok) break;
       ++k;
-      int row_n = kListed ? 0 : row_at(0, id0);
+      int row_n = kLists != kNoLists ? 0 : row_at(0, id0);
 #pragma unroll 1
       for (int t = 0; t < it.n_tiles; ++t, ++u) {
         const int rs = u % kRopeStages;
         int row, srow = 0;
-        if constexpr (kListed) {
+        if constexpr (kLists != kNoLists) {
           if ((t & 31) == 0 && t > 0) rows = listed_rows(t, base, srows);
           row = __shfl_sync(0xffffffffu, rows, t & 31);
           srow = __shfl_sync(0xffffffffu, srows, t & 31);
@@ -1384,7 +1429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
             tc::tma_load_3d(sScale + ls * kRawScale + j * box * 16, &tm_scale, full, kE4m3ScaleOff / 2, row, 0);
         } else if (staged) {
           if (lane == 0)
-            tma_load_4d(dst, &tm_lat, full, 0, 0, c0, (kListed ? srow : staged_row(a, it, base, it.key_tile(t))) / 8);
+            tma_load_4d(dst, &tm_lat, full, 0, 0, c0, (kLists != kNoLists ? srow : staged_row(a, it, base, it.key_tile(t))) / 8);
         } else if (mine && ch == 1) {
           tma_load_4d(dst + j * box / 8 * kGroup, &tm_lat, full, 0, 0, c0, row / 8);
         }
@@ -1542,7 +1587,7 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
     if (b < a.p.B) {
       bool bad;
       const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
-      if (worth_staging(a.p, s)) {
+      if (worth_staging(a, s)) {
         int32_t sink;
         const int32_t first = seq_first_tile(a.p, s.len - s.n, sink);
         const int64_t r = static_cast<int64_t>(sink + (s.len + kBK - 1) / kBK - first) * kBK;
@@ -1563,6 +1608,7 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
   long long end = incl - sum;
   for (int w = 0; w < warp; ++w) end += s_warp[w];
   // The sequences before the first that does not fit are staged.
+  bool left = false;
 #pragma unroll
   for (int q = 0; q < kStageSeqs / 256; ++q) {
     const int b = tid * (kStageSeqs / 256) + q;
@@ -1570,10 +1616,15 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
     end += rows[q];
     s_end[b] = static_cast<int32_t>(min(end, static_cast<long long>(INT32_MAX)));
     if (end <= kStageRows) atomicMax(&s_total, static_cast<int32_t>(end));
-    if (blockIdx.x == 0 && b < a.p.B)
-      a.stage_base[b] = rows[q] > 0 && end <= kStageRows ? static_cast<int32_t>(base) : -1;
+    if (blockIdx.x == 0 && b < a.p.B) {
+      const bool staged = rows[q] > 0 && end <= kStageRows;
+      a.stage_base[b] = staged ? static_cast<int32_t>(base) : -1;
+      bool bad;
+      if (!staged && paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad).n > 0) left = true;
+    }
   }
-  __syncthreads();
+  if (__syncthreads_or(left) != 0) left = true;
+  if (blockIdx.x == 0 && tid == 0) a.stage_base[kStageSeqs] = left;
   const int32_t total = s_total;
   // Staged row r: the sequence, the position, the pool row (-1: zero).
   auto lookup = [&](int32_t r) -> int32_t {
@@ -1626,6 +1677,138 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Lists of groups.  A block has 128 rows, so with H <= 64 heads several tokens fit in
+// one; neighbouring tokens list much the same blocks, and a tile costs a block of 128
+// rows no more than one of H.  One block of threads a group: each token's entries as
+// bits of a map, then for every position of the maps' union an entry with the tokens
+// that have it, in ascending order.  A block that a token lists again gets entries of
+// their own behind (a rare path: each entry is looked for among the earlier ones).
+// ---------------------------------------------------------------------------
+constexpr int kMapWords = 512, kMapTokens = 8;         // positions of a map: 2^14 blocks at a time
+
+__global__ void __launch_bounds__(256) paged_lists_kernel(const TcArgs a) {
+  __shared__ uint32_t map[kMapTokens][kMapWords];
+  __shared__ uint32_t any[kMapWords];
+  __shared__ int32_t offs[kMapWords + 1];
+  __shared__ int32_t s_warp[8];
+  __shared__ int s_again;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Beside the staging, of which nothing is read here: it let this kernel start when what
+  // came before it had ended, and only its own end is waited for, below.
+  const bool beside = a.stage_base != nullptr;
+  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int g = static_cast<int>(blockIdx.x), K = a.p.K;
+  // the group's sequence: the largest b with a first slot <= g, 32 at a time
+  int b = 0;
+  for (int n = a.p.B; n > 1;) {
+    const int step = (n + 31) / 32, m = b + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane == 0 || (m < b + n && slot_of_seq<kGroupLists>(a, m) <= g));
+    const int k = 31 - __clz(le);
+    n = min(step, n - k * step);
+    b += k * step;
+  }
+  bool bad;
+  const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
+  const int64_t i = g - slot_of_seq<kGroupLists>(a, b);
+  if (i < 0 || (i << a.gt_shift) >= s.n) {
+    if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const int tok = static_cast<int>(i) << a.gt_shift, nt = min(1 << a.gt_shift, s.n - tok);
+  const int pos = s.len - s.n + tok;                   // of the first token
+  const int32_t* lists = a.p.blocks + static_cast<int64_t>(s.q0 + tok) * K;
+  const int32_t* counts = a.p.counts + s.q0 + tok;
+  // Entry x of the group's nt K, or -1 (behind its list's end, or naming no block).
+  auto entry = [&](int x, int& t, bool report) -> int32_t {
+    t = x / K;
+    if (t >= nt) return -1;
+    const int32_t n = __ldg(counts + t);
+    if (x - t * K >= n) return -1;
+    const int32_t e = __ldg(lists + x);
+    if (e >= 0 && e <= (pos + t) / kBK) return e;
+    if (report) record_error(a.p.err, MLA_ERR_INVALID_ARG);
+    return -1;
+  };
+  if (tid < nt) {
+    const int32_t n = __ldg(counts + tid);
+    if (n < 0 || n > K) record_error(a.p.err, MLA_ERR_INVALID_ARG);
+  }
+  if (tid == 0) s_again = 0;
+  uint2* out = a.group_lists + (static_cast<int64_t>(g) << a.gt_shift) * K;
+  const int nb = (pos + nt - 1) / kBK + 1;             // blocks that there are
+  int total = 0;
+  for (int w0 = 0; w0 < nb; w0 += kMapWords * 32) {
+    const int n = min(kMapWords * 32, nb - w0), words = (n + 31) / 32;
+    for (int x = tid; x < nt * words; x += 256) map[x / words][x % words] = 0;
+    __syncthreads();
+    for (int x = tid; x < nt * K; x += 256) {
+      int t;
+      const int32_t e = entry(x, t, w0 == 0) - w0;
+      if (e >= 0 && e < n && (atomicOr(&map[t][e >> 5], 1u << (e & 31)) >> (e & 31) & 1)) s_again = 1;
+    }
+    __syncthreads();
+    // the union, and how many positions lie before each of its words
+    int32_t mine[kMapWords / 256] = {}, sum = 0;
+#pragma unroll
+    for (int q = 0; q < kMapWords / 256; ++q) {
+      const int w = tid * (kMapWords / 256) + q;
+      uint32_t u = 0;
+      if (w < words)
+        for (int t = 0; t < nt; ++t) u |= map[t][w];
+      any[w] = u;
+      mine[q] = sum;
+      sum += __popc(u);
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int before = total + incl - sum, all = 0;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) before += s_warp[w];
+      all += s_warp[w];
+    }
+#pragma unroll
+    for (int q = 0; q < kMapWords / 256; ++q) offs[tid * (kMapWords / 256) + q] = before + mine[q];
+    __syncthreads();
+    for (int j = tid; j < n; j += 256) {
+      const uint32_t u = any[j >> 5];
+      if ((u >> (j & 31) & 1) == 0) continue;
+      uint32_t tokens = 0;
+      for (int t = 0; t < nt; ++t) tokens |= (map[t][j >> 5] >> (j & 31) & 1) << t;
+      out[offs[j >> 5] + __popc(u & ((1u << (j & 31)) - 1))] = make_uint2(static_cast<uint32_t>((w0 + j) * kBK), tokens);
+    }
+    total += all;
+    __syncthreads();
+  }
+  if (s_again) {
+    for (int x0 = 0; x0 < nt * K; x0 += 256) {
+      int t;
+      const int32_t e = entry(x0 + tid, t, false);
+      bool again = false;
+      for (int x = t * K; e >= 0 && !again && x < x0 + tid; ++x) again = __ldg(lists + x) == e;
+      const uint32_t m = __ballot_sync(0xffffffffu, again);
+      if (lane == 0) s_warp[warp] = __popc(m);
+      __syncthreads();
+      int at = total + __popc(m & ((1u << lane) - 1));
+      for (int w = 0; w < 8; ++w) {
+        if (w < warp) at += s_warp[w];
+        total += s_warp[w];
+      }
+      if (again) out[at] = make_uint2(static_cast<uint32_t>(e * kBK), 1u << t);
+      __syncthreads();
+    }
+  }
+  if (tid == 0) a.group_counts[g] = total;
+  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 int clusters() { return max(1, min(kMaxClusters, device_sm_count() / 2)); }
 
 // Workspace: partials, their sums, the clusters' records (all multiples of 16
@@ -1635,10 +1818,10 @@ size_t partial_bytes() {
   return rows * kLatent * sizeof(float) + rows * 2 * sizeof(float) + clusters() * sizeof(Rec);
 }
 
-template <bool kE4m3, bool kFewRows, bool kLong, bool kListed>
+template <bool kE4m3, bool kFewRows, bool kLong, int kLists>
 cudaError_t launch_pair(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const CUtensorMap& ts,
                         const TcArgs& a, cudaStream_t stream) {
-  auto kern = paged_attn_kernel<kE4m3, kFewRows, kLong, kListed>;
+  auto kern = paged_attn_kernel<kE4m3, kFewRows, kLong, kLists>;
   static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1673,15 +1856,31 @@ bool any_long(const PagedAttnArgs& p) {
 template <bool kE4m3, bool kFewRows>
 cudaError_t launch_for(const CUtensorMap& tm, const CUtensorMap& tr, const CUtensorMap& tq, const CUtensorMap& ts,
                        const TcArgs& a, cudaStream_t stream) {
-  if (a.p.blocks != nullptr) return launch_pair<kE4m3, kFewRows, false, true>(tm, tr, tq, ts, a, stream);
-  return any_long(a.p) ? launch_pair<kE4m3, kFewRows, true, false>(tm, tr, tq, ts, a, stream)
-                       : launch_pair<kE4m3, kFewRows, false, false>(tm, tr, tq, ts, a, stream);
+  if constexpr (!kFewRows)
+    if (a.group_lists != nullptr) return launch_pair<kE4m3, false, false, kGroupLists>(tm, tr, tq, ts, a, stream);
+  if (a.p.blocks != nullptr) return launch_pair<kE4m3, kFewRows, false, kTokenLists>(tm, tr, tq, ts, a, stream);
+  return any_long(a.p) ? launch_pair<kE4m3, kFewRows, true, kNoLists>(tm, tr, tq, ts, a, stream)
+                       : launch_pair<kE4m3, kFewRows, false, kNoLists>(tm, tr, tq, ts, a, stream);
 }
+
+// How the lists of a call are grouped: 2^shift tokens a block, the number of slots (0:
+// each token by itself).  Single tokens have no neighbours; with more than 64 heads no
+// two fit; and lists as long as the room does not hold stay as they are.
+int64_t group_slots(const PagedAttnArgs& p, int32_t& shift) {
+  shift = 0;
+  if (p.blocks == nullptr || p.T <= p.B || 2 * p.H > kRows) return 0;
+  while ((2 * p.H << shift) <= kRows) ++shift;
+  const int64_t slots = (static_cast<int64_t>(p.T) >> shift) + p.B;
+  return (slots << shift) * p.K <= kGroupEntries ? slots : 0;
+}
+
+// (16 bytes behind the sequences' entries: whether all are staged)
+size_t stage_bytes() { return (kStageSeqs + 4) * sizeof(int32_t) + static_cast<size_t>(kStageRows) * kLatent * 2; }
 
 }  // namespace
 
 size_t paged_attn_workspace_bytes() {
-  return partial_bytes() + kStageSeqs * sizeof(int32_t) + static_cast<size_t>(kStageRows) * kLatent * 2;
+  return partial_bytes() + stage_bytes() + kGroupEntries * sizeof(uint2) + kGroupEntries / 2 * sizeof(int32_t);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
@@ -1693,9 +1892,15 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   a.ws_ml = a.ws_o + rows * kLatent;
   a.rec = reinterpret_cast<Rec*>(a.ws_ml + rows * 2);
   int32_t* stage_base = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(p.workspace) + partial_bytes());
-  a.stage = reinterpret_cast<uint16_t*>(stage_base + kStageSeqs);
+  a.stage = reinterpret_cast<uint16_t*>(stage_base + kStageSeqs + 4);
   a.n_slots = p.blocks != nullptr ? p.T : static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
   a.n_rows = p.c.n_pages << p.c.page_shift;
+  const int64_t groups = group_slots(p, a.gt_shift);
+  if (groups > 0) {
+    a.group_lists = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.workspace) + partial_bytes() + stage_bytes());
+    a.group_counts = reinterpret_cast<int32_t*>(a.group_lists + kGroupEntries);
+    a.n_slots = static_cast<int32_t>(groups);
+  }
   // The latents of fp16 pages or of staged rows, in groups of eight rows; the
   // queries, as 64-dim chunks (dims, rows, chunks).  The RoPE parts are fp16 in
   // either row type.
@@ -1706,14 +1911,21 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   const uint64_t qrows = static_cast<uint64_t>(p.T) * static_cast<uint64_t>(p.H);
   e = make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kLatent / 64, kLatent * 2, 128, 64, kRows, 2);
   if (e != cudaSuccess) return e;
+  auto lists = [&]() {
+    return groups > 0 ? launch_dependent(paged_lists_kernel, dim3(static_cast<unsigned>(groups)), dim3(256), 0, stream, a)
+                      : cudaSuccess;
+  };
   if (!p.c.e4m3) {
+    e = lists();
+    if (e != cudaSuccess) return e;
     e = make_tmap_row_groups(&tm, p.c.pages, n / 8, kRow / 64, kRowF16, box / 8, 4);
     if (e != cudaSuccess) return e;
     e = make_tmap_3d(&tr, p.c.pages, false, kRow, n, 1, kRowF16, n * kRowF16, kRopeHalf, box, 1, 64);
     if (e != cudaSuccess) return e;
-    // a block of single tokens has H rows, and so has one of listed blocks
-    return (p.T <= p.B || p.blocks != nullptr) && p.H <= kRows - 16 ? launch_for<false, true>(tm, tr, tq, tq, a, stream)
-                                           : launch_for<false, false>(tm, tr, tq, tq, a, stream);
+    // a block of single tokens has H rows, and so has one with a token's own list
+    return (p.T <= p.B || p.blocks != nullptr) && groups == 0 && p.H <= kRows - 16
+               ? launch_for<false, true>(tm, tr, tq, tq, a, stream)
+               : launch_for<false, false>(tm, tr, tq, tq, a, stream);
   }
   // In elements of two bytes, as the rows are: a CTA's 256 codes, and the 16 scales.
   CUtensorMap tcodes, tscales;
@@ -1732,10 +1944,15 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_dependent(paged_stage_kernel, dim3(device_sm_count() * 4), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
+    e = lists();
+    if (e != cudaSuccess) return e;
     a.take = kTakeStaged;
     e = launch_for<false, false>(tm, tr, tq, tq, a, stream);
     if (e != cudaSuccess) return e;
     a.take = kTakeUnstaged;
+  } else {
+    e = lists();
+    if (e != cudaSuccess) return e;
   }
   return launch_for<true, false>(tcodes, tr, tq, tscales, a, stream);
 }

@@ -459,6 +459,68 @@ def test_long_lists(e4m3, K, lens):
     assert (np.abs(host(out) - host(dense)) <= 2 * tol).all()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H", [16, 48, 64])
+def test_neighbours_with_lists_of_their_own(e4m3, H):
+    """Chunks in which tokens share blocks of 128 rows: lists that agree, differ, are empty, name a block again or no
+    block, and tiles whose later rows only tokens see that do not list them."""
+    lists = [[0], [1, 0], [], [0, 1], [1, 1, 0, 1], [0], [], [1], [0, 0], [1], [1, 0], [0]]
+    b = Listed(31, e4m3, H, 64, [12], [70], 5, lists=lists)           # positions 58 .. 69: up to 63, block 1 is ahead
+    check(b, attend(b), INVALID)
+    lists = [list(range(t % 5)) + [7 + t % 3] for t in range(60)]
+    b = Listed(32, e4m3, H, 128, [37, 2, 21], [700, 650, 900], 9, lists=lists, pad=1)
+    check(b, attend(b))
+    lists[10], lists[41] = [-1, 3, 1 << 25], [3, 50, 3, 3, 2]
+    b = Listed(33, e4m3, H, 128, [37, 2, 21], [700, 650, 900], 9, lists=lists, pad=1)
+    check(b, attend(b), INVALID)
+
+
+def test_counts_outside_the_lists_of_a_group_are_reported():
+    b = Listed(34, False, 16, 64, [5], [400], 3, lists=[[0, 1, 2], [3], [1], [], [0, 4]])
+    d = b.dev()
+    d["counts"] += torch.tensor([5, -9, 0, 0, 0], dtype=torch.int32, device="cuda")
+    out = attend(b, d)
+    b.counts[:] = [3, 0, 1, 0, 2]
+    check(b, out, INVALID)
+
+
+def test_more_lists_than_the_workspace_groups():
+    lists = [[(7 * t) % 30, 30 + t % 3][:1 + t % 2] for t in range(2100)]
+    b = Listed(35, False, 16, 64, [2100], [4100], 1024, lists=lists)
+    check(b, attend(b), INVALID)         # (block 32 is ahead of the first 48 tokens)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_contexts_past_a_million_rows(H):
+    """Two pages stand in for all of a context's."""
+    rng, L, n = np.random.default_rng(36), 1_100_003, 3
+    rows = rng.standard_normal((8192, 576)).astype(np.float16)
+    table = rng.integers(0, 2, (1, -(-L // 4096))).astype(np.int32)
+    lists = [[17000, 5, 16383, 17187], [16384, 5, 0], [17187, 16385, 5, 40]]
+    q_lat = rng.standard_normal((n, H, 512)).astype(np.float16)
+    q_pe = bf16(rng.standard_normal((n, H, 64)))
+    blocks = np.full((n, 4), -1, np.int32)
+    for t, x in enumerate(lists):
+        blocks[t, :len(x)] = x
+    out = torch.empty(n, H, 512, dtype=torch.float16, device="cuda")
+    mla.mla_attn_paged_blocks(torch.from_numpy(q_lat).cuda(), torch.from_numpy(q_pe).bfloat16().cuda(),
+                              torch.from_numpy(rows).cuda().view(2, 4096, 576), i32(table), i32([0, n]), i32([L]),
+                              i32(blocks), i32([len(x) for x in lists]), out, scale=SCALE)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    q = np.concatenate([q_lat, q_pe], -1).astype(np.float64)
+    for t, lst in enumerate(lists):
+        p = L - n + t
+        keys = np.concatenate([np.arange(64 * j, min(64 * j + 64, p + 1)) for j in lst])
+        r = rows[table[0, keys // 4096] * 4096 + keys % 4096].astype(np.float64)
+        s = SCALE * (q[t] @ r.T)
+        w = np.exp(s - s.max(-1, keepdims=True))
+        w /= w.sum(-1, keepdims=True)
+        want, a = w @ r[:, :512], w @ np.abs(r[:, :512])
+        tol = (2.0 ** -11 + 2.0 ** -12) * a + 2.0 ** -11 * np.abs(want) + 2.0 ** -24 + 2.0 ** -25 * len(keys) * np.abs(r).max()
+        assert (np.abs(host(out[t]) - want) <= tol).all()
+
+
 def test_rows_at_far_addresses():
     """A pool past 4 GB: pages at its end."""
     b = Listed(23, False, 16, 256, [1, 2], [900, 700], 3, "all")

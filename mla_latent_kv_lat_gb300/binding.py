@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 from typing import Optional
@@ -485,6 +486,26 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
     _check("mla_attn_paged", st)
 
 
+_calls = None
+
+
+def _fast():
+    """The compiled way to the calls below (csrc/calls.cpp): its functions return the call's status, or None for
+    arguments that are not plainly right.  Those take the way through Python, which says what is wrong with them."""
+    global _calls
+    if _calls is None:
+        load_library()
+        path = _build.calls_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{os.path.basename(path)} is not built; run __graft_entry__.build() first")
+        spec = importlib.util.spec_from_file_location("_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(_build.LIB)
+        _calls = module
+    return _calls
+
+
 def _fit(value: int, name: str) -> int:
     """A Python integer that the C call takes as int32 (ctypes would take its low 32 bits)."""
     if not -1 << 31 <= value < 1 << 31:
@@ -513,6 +534,10 @@ def mla_paged_norm_append(q, kv, q_weight, kv_weight, pages, block_table, cu_new
     is given) into q_nope [T, H, 128] and the rotated q_pe [T, H, 64]; kv [T, 576] into the tokens' rows, its latent
     RMS-normed with ``kv_weight`` [512], its RoPE part rotated.  q and kv may be slices of wider tensors (last
     dimension contiguous, other strides multiples of 8)."""
+    st = (_calls or _fast()).norm_append(q, kv, q_weight, kv_weight, pages, block_table, cu_new, seq_len, q_nope, q_pe, eps,
+                                         freq_base, freq_scale, stream)
+    if st is not None:
+        return _check("mla_paged_norm_append", st)
     dev = paged_device(q, "q")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -542,6 +567,9 @@ def _block_keys(block_keys, n_pages: int, page_size: int, dev: int) -> int:
 def mla_paged_block_keys(pages, block_table, cu_new, seq_len, block_keys, T: int, stream=None):
     """Mean rows of the blocks of 64 positions that the batch's new tokens (at most T, their rows appended) complete,
     into block_keys fp16 [n_pages, page_size / 64, 576]."""
+    st = (_calls or _fast()).block_keys(pages, block_table, cu_new, seq_len, block_keys, T, stream)
+    if st is not None:
+        return _check("mla_paged_block_keys", st)
     dev = paged_device(pages, "pages")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -563,6 +591,9 @@ def _rows_f32(scores, T, dev: int):
 def mla_paged_block_scores(q_lat, q_pe, block_keys, block_table, cu_q, seq_len, scores, scale=None, stream=None):
     """scores fp32 [T, n_scores]: for each new token and each block j before its own, scale times the largest head's
     product with the block's mean row (block_keys); -inf from its own block on."""
+    st = (_calls or _fast()).block_scores(q_lat, q_pe, block_keys, block_table, cu_q, seq_len, scores, scale, stream)
+    if st is not None:
+        return _check("mla_paged_block_scores", st)
     dev = paged_device(q_lat, "q_lat")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -589,6 +620,9 @@ def mla_paged_block_scores(q_lat, q_pe, block_keys, block_table, cu_q, seq_len, 
 def mla_paged_select_blocks(scores, cu_q, seq_len, blocks, counts, n_sink: int = 1, n_local: int = 1, stream=None):
     """blocks int32 [T, K] and counts int32 [T]: each new token's own block, the n_local - 1 before it, the first
     n_sink, and the best-scored others up to K; ascending, -1 behind."""
+    st = (_calls or _fast()).select_blocks(scores, cu_q, seq_len, blocks, counts, n_sink, n_local, stream)
+    if st is not None:
+        return _check("mla_paged_select_blocks", st)
     dev = paged_device(scores, "scores")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -608,6 +642,10 @@ def mla_attn_paged_blocks(q_lat, q_pe, pages, block_table, cu_q, seq_len, blocks
                           stream=None):
     """o_lat [T, H, 512]: mla_attn_paged over the rows of each token's listed blocks (blocks int32 [T, K], of which the
     first counts[t] of row t count).  Without a workspace a fresh one is taken from PyTorch's allocator."""
+    st = (_calls or _fast()).attn_blocks(q_lat, q_pe, pages, block_table, cu_q, seq_len, blocks, counts, o_lat, workspace,
+                                         scale, stream)
+    if st is not None:
+        return _check("mla_attn_paged_blocks", st)
     dev = paged_device(q_lat, "q_lat")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):

@@ -1,4 +1,5 @@
-"""Build libmla.so in-tree from csrc/*.cu with nvcc for sm_103a (GB300).
+"""Build libmla.so in-tree from csrc/*.cu with nvcc for sm_103a (GB300), and beside it the module that
+takes the paged calls from Python to it (csrc/calls.cpp, against the installed PyTorch).
 
 Usage: ``python -m mla_latent_kv_lat_gb300.build [--force]``.  Translation
 units compile in parallel; the library links against the shared CUDA runtime
@@ -8,10 +9,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -31,19 +34,43 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libmla")
 
 
+def calls_path() -> str:
+    """The module of csrc/calls.cpp for this Python and PyTorch."""
+    import torch
+    version = "".join(c if c.isalnum() else "_" for c in torch.__version__)
+    return os.path.join(PKG, f"_calls_{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _build_calls() -> str:
+    root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    out = calls_path()
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "calls.cpp"), "-o", out + ".tmp"]
+    for i in inc:
+        cmd += ["-isystem" if i != INCLUDE else "-I", i]
+    cmd += ["-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+    return out
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
 def _deps():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + glob.glob(os.path.join(INCLUDE, "*.h")))
+                  + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(calls_path()):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(calls_path()))
     return all(os.path.getmtime(p) <= t for p in _deps() + [os.path.abspath(__file__)])
 
 
@@ -61,8 +88,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_build_calls)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "shared"]
     r = subprocess.run(cmd, capture_output=True, text=True)

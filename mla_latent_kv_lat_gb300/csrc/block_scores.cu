@@ -18,6 +18,7 @@
 //     q_pe (bf16) into fp16, the type of the mean rows.
 //   * Two accumulators of 128 columns: four warps reduce one while the next is filled.
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.cuh"
 #include "paged.cuh"
@@ -29,19 +30,26 @@ namespace {
 constexpr int kTile = 128;                   // blocks of a tile (MMA M)
 constexpr int kMaxN = 128;                   // (token, head) columns
 constexpr int kChunk = 128 * 128;            // 128 rows x 64 fp16
-constexpr int kChunks = kLatent / 64;
-constexpr int kStages = 8, kFeed = 4;
-constexpr int kOffKr = 0;                                    // the mean rows' RoPE part
-constexpr int kOffFeed = kOffKr + kChunk;                    // mean rows on their way; two of them hold q_pe, too
-constexpr int kOffRing = kOffFeed + kFeed * kChunk;
-constexpr int kOffBar = kOffRing + kStages * kChunk;
-constexpr int kBarBytes = 512;
-constexpr int kSmem = 1024 + kOffBar + kBarBytes;
-static_assert(kSmem <= 232448, "shared memory");
-
+constexpr int kStage = 2 * kChunk;
+constexpr int kChunks = kLatent / 64, kGroupStages = kChunks / 2;
+constexpr int kBarBytes = 1024;
+// kKeep: a run has many groups, and its mean rows stay in tensor memory; they come
+// through three chunks, of which two hold q_pe afterwards.  Else they stay in shared memory.
+template <bool kKeep>
+struct Cfg {
+  static constexpr int kStages = kKeep ? 5 : 2;                // of queries, two chunks each
+  static constexpr int kFeed = kKeep ? 3 : 1;                  // q_pe (and mean rows on their way)
+  static constexpr int kQr = kKeep ? 2 : 1;                    // q_pe
+  static constexpr int kRowChunks = kKeep ? 1 : kChunks + 1;   // mean rows: the RoPE part, or all
+  static constexpr int kOffFeed = kRowChunks * kChunk;
+  static constexpr int kOffRing = kOffFeed + kFeed * kChunk;
+  static constexpr int kOffBar = kOffRing + kStages * kStage;
+  static constexpr int kSmem = 1024 + kOffBar + kBarBytes;
+};
+static_assert(Cfg<true>::kSmem <= 232448 && Cfg<false>::kSmem <= 232448, "shared memory");
 constexpr int kFeedWarp = 4, kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
 constexpr int kBarFeed = 1;
-constexpr uint32_t kTmK = 0, kTmS = 256;
+constexpr uint32_t kTmS = 0, kTmK = 256;
 constexpr uint64_t kGaveUpNs = 200000;       // from a wait that ran out to the CTA's end
 
 struct Args {
@@ -62,13 +70,15 @@ struct Start {
 };
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t k_full, k_free;             // the run's mean rows are there; its last product is done
+  uint64_t full[5], empty[5];
+  uint64_t k_full[kChunks + 1];        // the run's mean rows are there (kKeep: [0] all of them)
+  uint64_t k_free;                     // its last product is done
   uint64_t qr_full[2], qr_empty[2];
   uint64_t s_full[2], s_empty[2];
   uint32_t tmem;
   Start st;
   long long red[kThreads / 32];
+  int32_t row[kTile];                  // the run's mean rows in the pool, -1: none
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 
@@ -166,14 +176,17 @@ MLA_DEVINL float max3(float a, float b, float c) {
   return r;
 }
 
+template <bool kKeep>
 __global__ void __launch_bounds__(kThreads, 1)
     block_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sKr = sm + kOffKr;
-  uint8_t* sFeed = sm + kOffFeed;
-  uint8_t* sRing = sm + kOffRing;
-  Bars& B = *reinterpret_cast<Bars*>(sm + kOffBar);
+  using C = Cfg<kKeep>;
+  constexpr int kStages = C::kStages, kFeed = C::kFeed, kQr = C::kQr;
+  uint8_t* sK = sm;
+  uint8_t* sFeed = sm + C::kOffFeed;
+  uint8_t* sRing = sm + C::kOffRing;
+  Bars& B = *reinterpret_cast<Bars*>(sm + C::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == kLoadWarp && lane == 0) {
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.full[i], 1);
       mbar_init(&B.empty[i], 1);
     }
-    mbar_init(&B.k_full, 4);
+    for (int i = 0; i <= kChunks; ++i) mbar_init(&B.k_full[i], 4);
     mbar_init(&B.k_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.qr_full[i], 4);
@@ -193,13 +206,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tc::tmem_alloc(&B.tmem, 512);
+    tc::tmem_alloc(&B.tmem, kKeep ? 512 : 256);
     tc::tmem_relinquish();
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = B.tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) record_bad_seqs(a.p.cu, a.p.seq_len, a.p.B, a.p.T, a.p.c.max_rows(), a.p.err);
@@ -223,7 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) B.red[warp] = incl;
     if (threadIdx.x == 0) B.st = {0, 0, 0, a.p.B};
-    __syncthreads();
+    tc::fence_before_sync();
+    __syncthreads();                   // (the barriers and tensor memory are ready, too)
+    tc::fence_after_sync();
     int64_t total = 0, S = incl - sum;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
@@ -243,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
+  const uint32_t tmem = B.tmem;
   const int H = a.p.H, N = H << a.gt_shift;
   Walk walk;
   walk.init(a, B.st);
@@ -309,68 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool dead = false;
     int u = 0, k = 0;
     while (walk.next(a, r)) {
-      if (r.fresh) {
-        // Unit ft + 128 i of a chunk: row ft / 8 + 16 i.  The sequence's blocks before
-        // its last token's own are there; the others are zero.
-        const int n_there = (walk.q.s.len - 1) >> kBlockShift, j0 = walk.tile * kTile;
-        int64_t src[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = j0 + (ft >> 3) + 16 * i;
-          src[i] = -1;
-          if (j < n_there) {
-            const int32_t id = __ldg(a.p.c.table + walk.b * a.p.c.table_stride + (j >> per_shift));
-            if (id >= 0 && id < a.p.c.n_pages) src[i] = (static_cast<int64_t>(id) << per_shift) + (j & ((1 << per_shift) - 1));
-            else if (un == 0) record_error(a.p.err, MLA_ERR_INVALID_ARG);
-          }
-        }
-        // The last products of the run before have read its rows (and q_pe of all groups).
-        if (k > 0 && !dead) dead = !wait_all(&B.k_free, (k - 1) & 1, a);
-        auto fetch = [&](uint8_t* to, int c) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = (ft >> 3) + 16 * i;
-            cp_async16(smem_u32(to) + row * 128 + ((un ^ (row & 7)) << 4),
-                       a.p.keys + (src[i] < 0 ? 0 : src[i] * kRow) + 64 * c + 8 * un, src[i] >= 0);
-          }
-          cp_async_commit();
-        };
-        if (!dead) {
-          fetch(sKr, kChunks);
-          for (int c = 0; c < kFeed; ++c) fetch(sFeed + c * kChunk, c);
-        }
-#pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
-          if (!dead) cp_async_wait<kFeed - 1>();
-          tc::named_bar_sync(kBarFeed, 128);
-          if (!dead) {
-            const uint8_t* from = sFeed + (c % kFeed) * kChunk;
-            const int row = 32 * q4 + lane;
-            uint32_t x[32];
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-              const uint4 v = *reinterpret_cast<const uint4*>(from + row * 128 + ((w ^ (row & 7)) << 4));
-              x[4 * w] = v.x; x[4 * w + 1] = v.y; x[4 * w + 2] = v.z; x[4 * w + 3] = v.w;
-            }
-            tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmK + 32 * c, x);
-          }
-          tc::named_bar_sync(kBarFeed, 128);
-          if (!dead) {
-            if (c + kFeed < kChunks) fetch(sFeed + (c % kFeed) * kChunk, c + kFeed);
-            else cp_async_commit();      // (an empty group keeps the count)
-          }
-        }
-        if (!dead) {
-          tc::tmem_st_wait();
-          tc::fence_proxy_async();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&B.k_full);
-        }
-        ++k;
-      }
       // q_pe of the group: N rows x 64, eight 16-byte units a thread
-      if (dead) continue;
       const int64_t row0 = static_cast<int64_t>(r.t0) * H;
       uint4 v[8];
 #pragma unroll
@@ -379,9 +330,99 @@ __global__ void __launch_bounds__(kThreads, 1)
         v[i] = row < r.nt * H && row0 + row < qrows
                    ? __ldg(reinterpret_cast<const uint4*>(a.p.q_pe + (row0 + row) * kRope) + un) : make_uint4(0, 0, 0, 0);
       }
-      if (u >= 2) dead = !wait_all(&B.qr_empty[u & 1], ((u >> 1) - 1) & 1, a);
+      if (r.fresh) {
+        // The sequence's blocks before its last token's own are there; the others are zero.
+        const int n_there = (walk.q.s.len - 1) >> kBlockShift;
+        const int j = walk.tile * kTile + ft;
+        int32_t mine = -1;
+        if (j < n_there) {
+          const int32_t id = __ldg(a.p.c.table + walk.b * a.p.c.table_stride + (j >> per_shift));
+          if (id >= 0 && id < a.p.c.n_pages) mine = (id << per_shift) + (j & ((1 << per_shift) - 1));
+          else record_error(a.p.err, MLA_ERR_INVALID_ARG);
+        }
+        B.row[ft] = mine;
+        __syncwarp();
+        // A warp brings its own 32 rows: unit lane + 32 i of its part of a chunk, row r0 + 4 i.
+        const int r0 = 32 * q4 + (lane >> 3);
+        const uint16_t* src[8];
+        uint32_t there = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t row = B.row[r0 + 4 * i];
+          src[i] = a.p.keys + static_cast<int64_t>(max(row, 0)) * kRow + 8 * un;
+          there |= row >= 0 ? 1u << i : 0u;
+        }
+        // The last products of the run before have read its rows (and q_pe of all groups).
+        if (k > 0 && !dead) dead = !wait_all(&B.k_free, (k - 1) & 1, a);
+        auto fetch = [&](uint8_t* to, int c) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = r0 + 4 * i;
+            cp_async16(smem_u32(to) + row * 128 + ((un ^ (row & 7)) << 4), src[i] + 64 * c, (there >> i & 1) != 0);
+          }
+          cp_async_commit();
+        };
+        if constexpr (kKeep) {
+          if (!dead) {
+            fetch(sK, kChunks);
+            for (int c = 0; c < kFeed; ++c) fetch(sFeed + c * kChunk, c);
+          }
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+            if (!dead) {
+              cp_async_wait<kFeed - 1>();
+              __syncwarp();
+              const uint8_t* from = sFeed + (c % kFeed) * kChunk;
+              const int row = 32 * q4 + lane;
+              uint32_t x[32];
+#pragma unroll
+              for (int w = 0; w < 8; ++w) {
+                const uint4 v = *reinterpret_cast<const uint4*>(from + row * 128 + ((w ^ (row & 7)) << 4));
+                x[4 * w] = v.x; x[4 * w + 1] = v.y; x[4 * w + 2] = v.z; x[4 * w + 3] = v.w;
+              }
+              tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmK + 32 * c, x);
+              __syncwarp();
+              if (c + kFeed < kChunks) fetch(sFeed + (c % kFeed) * kChunk, c + kFeed);
+              else cp_async_commit();      // (an empty group keeps the count)
+            }
+          }
+          if (!dead) {
+            tc::tmem_st_wait();
+            tc::fence_proxy_async();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.k_full[0]);
+          }
+          // (q_pe goes where other warps' rows were)
+          tc::named_bar_sync(kBarFeed, 128);
+        } else if (!dead) {
+          // all at once; a chunk is passed on when it has arrived, from the fifth on behind the next one's request
+          auto arrived = [&](int c) {
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.k_full[c]);
+          };
+#pragma unroll 1
+          for (int c = 0; c <= kChunks; ++c) {
+            fetch(sK + c * kChunk, c);
+            if (c >= 5) {
+              cp_async_wait<5>();
+              arrived(c - 5);
+            }
+          }
+          cp_async_wait<4>(); arrived(4);
+          cp_async_wait<3>(); arrived(5);
+          cp_async_wait<2>(); arrived(6);
+          cp_async_wait<1>(); arrived(7);
+          cp_async_wait<0>(); arrived(8);
+        }
+        ++k;
+      }
       if (dead) continue;
-      uint8_t* to = sFeed + (u & 1) * kChunk;
+      const int qb = u % kQr;
+      if (u >= kQr) dead = !wait_all(&B.qr_empty[qb], (u / kQr - 1) & 1, a);
+      if (dead) continue;
+      uint8_t* to = sFeed + qb * kChunk;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int row = (ft >> 3) + 16 * i;
@@ -397,64 +438,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&B.qr_full[u & 1]);
+      if (lane == 0) mbar_arrive(&B.qr_full[qb]);
       ++u;
     }
     if (bf16x2_absmax_overflows(qrun)) record_error(a.p.err, MLA_ERR_RANGE);
     ok = !dead;
   } else if (warp == kLoadWarp) {
     // ============================== queries (TMA) ===============================
-    int s = 0;                           // stages filled
+    int st = 0, use = 0;                 // the next stage, and how often the ring has been through
     while (ok && walk.next(a, r)) {
-      for (int c = 0; c < kChunks; ++c, ++s) {
-        const int st = s % kStages;
-        if (s >= kStages) ok = wait_all(&B.empty[st], ((s / kStages) - 1) & 1, a);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&B.full[st], static_cast<uint32_t>(N) * 128);
-          tc::tma_load_3d(sRing + st * kChunk, &tm_q, &B.full[st], 0, r.t0 * H, c);
+#pragma unroll 1
+      for (int c = 0; c < kGroupStages; ++c) {
+        if (use > 0) ok = ok && wait_all(&B.empty[st], (use - 1) & 1, a);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&B.full[st], static_cast<uint32_t>(N) * 256);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tc::tma_load_3d(sRing + st * kStage + h * kChunk, &tm_q, &B.full[st], 0, r.t0 * H, 2 * c + h);
         }
         __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          ++use;
+        }
       }
     }
   } else {
     // ================================== MMAs ====================================
     const uint32_t idesc = tc::idesc_f16(128, N, false, false, false);
-    int s = 0, u = 0, k = 0;
+    // Addresses are constants beside this one, which a reduction makes known to be the
+    // same in all lanes: held in lanes' registers, each product's operands would be moved
+    // over first, and the issue, not the tensor cores, would be the limit.
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+    const uint64_t ring = tc::sdesc_sw128(smem_u32(sRing), 16, 1024), rows = tc::sdesc_sw128(smem_u32(sK), 16, 1024),
+                   qpe = tc::sdesc_sw128(smem_u32(sFeed), 16, 1024);
+    auto at = [](uint64_t desc, int bytes) { return desc + static_cast<uint64_t>(bytes >> 4); };
+    int u = 0, k = 0, st = 0, use = 0;
     while (ok && walk.next(a, r)) {
-      if (r.fresh) {
+      const bool fresh = r.fresh;
+      if (fresh) {
         // the run before is done with its mean rows when its products are
         if (k > 0) tc::mma_commit_warp(&B.k_free);
-        ok = wait_all(&B.k_full, k & 1, a);
+        if (kKeep) ok = wait_all(&B.k_full[0], k & 1, a);
         if (!ok) break;
         ++k;
       }
-      const int sb = u & 1;
-      if (u >= 2) ok = wait_all(&B.s_empty[sb], ((u >> 1) - 1) & 1, a);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t d = tmem + kTmS + sb * kMaxN;
-      for (int c = 0; ok && c < kChunks; ++c, ++s) {
-        const int st = s % kStages;
-        ok = wait_all(&B.full[st], (s / kStages) & 1, a);
-        if (!ok) break;
+      auto group = [&](auto buf) {
+        constexpr int sb = decltype(buf)::value, qb = sb % kQr;
+        const uint32_t d = tm + kTmS + sb * kMaxN;
+        if (u >= 2) ok = wait_all(&B.s_empty[sb], ((u >> 1) - 1) & 1, a);
+        if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t q0 = smem_u32(sRing + st * kChunk);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc::mma_ts_warp(d, tmem + kTmK + 32 * c + 8 * ks, tc::sdesc_sw128(q0 + 32 * ks, 16, 1024), idesc, (c | ks) != 0);
-        tc::mma_commit_warp(&B.empty[st]);
-      }
-      if (!ok) break;
-      ok = wait_all(&B.qr_full[sb], (u >> 1) & 1, a);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t k0 = smem_u32(sKr), q0 = smem_u32(sFeed + sb * kChunk);
+        for (int c = 0; c < kGroupStages; ++c) {
+          ok = ok && wait_all(&B.full[st], use & 1, a);
+          if (!kKeep && fresh) ok = ok && wait_all(&B.k_full[2 * c], (k - 1) & 1, a) && wait_all(&B.k_full[2 * c + 1], (k - 1) & 1, a);
+          if (!ok) return;
+          tc::fence_after_sync();
+          const uint32_t stage = __reduce_max_sync(0xffffffffu, st * (kStage >> 4));
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        tc::mma_ss_warp(d, tc::sdesc_sw128(k0 + 32 * ks, 16, 1024), tc::sdesc_sw128(q0 + 32 * ks, 16, 1024), idesc, 1u);
-      tc::mma_commit_warp(&B.qr_empty[sb]);
-      tc::mma_commit_warp(&B.s_full[sb]);
+          for (int h = 0; h < 8; ++h) {
+            const uint64_t qd = at(ring + stage, (h >> 2) * kChunk + 32 * (h & 3));
+            if constexpr (kKeep) tc::mma_ts_warp(d, tm + kTmK + 64 * c + 8 * h, qd, idesc, (c | h) != 0);
+            else tc::mma_ss_warp(d, at(rows, (2 * c + (h >> 2)) * kChunk + 32 * (h & 3)), qd, idesc, (c | h) != 0);
+          }
+          tc::mma_commit_warp(&B.empty[st]);
+          if (++st == kStages) {
+            st = 0;
+            ++use;
+          }
+        }
+        ok = wait_all(&B.qr_full[qb], (u / kQr) & 1, a);
+        if (!kKeep && fresh) ok = ok && wait_all(&B.k_full[kChunks], (k - 1) & 1, a);
+        if (!ok) return;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          tc::mma_ss_warp(d, at(rows, (C::kRowChunks - 1) * kChunk + 32 * h), at(qpe, qb * kChunk + 32 * h), idesc, 1u);
+        tc::mma_commit_warp(&B.qr_empty[qb]);
+        tc::mma_commit_warp(&B.s_full[sb]);
+      };
+      if (u & 1) group(std::integral_constant<int, 1>());
+      else group(std::integral_constant<int, 0>());
       ++u;
     }
   }
@@ -467,8 +532,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(tmem, kKeep ? 512 : 256);
   }
+}
+
+template <bool kKeep>
+cudaError_t launch(const CUtensorMap& tq, const Args& a, cudaStream_t stream) {
+  auto kern = block_scores_kernel<kKeep>;
+  static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev > 63 || (set.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<kKeep>::kSmem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int64_t sms = device_sm_count();
+  // a run of single tokens is one group: no more CTAs than there can be runs
+  const int64_t grid = kKeep ? sms : min(sms, static_cast<int64_t>(a.p.T) * a.tiles);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), Cfg<kKeep>::kSmem, stream, tq, a);
 }
 
 }  // namespace
@@ -485,18 +569,7 @@ cudaError_t launch_block_scores(const BlockScoresArgs& p, cudaStream_t stream) {
   cudaError_t e = make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kChunks, kLatent * 2, 128, 64,
                                static_cast<uint32_t>(p.H << a.gt_shift), 1);
   if (e != cudaSuccess) return e;
-  static std::atomic<uint64_t> set{0};         // devices on which the attribute is set
-  int dev = 0;
-  e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev > 63 || (set.load(std::memory_order_relaxed) & bit) == 0) {
-    e = cudaFuncSetAttribute(block_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    set.fetch_or(bit, std::memory_order_relaxed);
-  }
-  return launch_dependent(block_scores_kernel, dim3(static_cast<unsigned>(device_sm_count())), dim3(kThreads), kSmem, stream,
-                          tq, a);
+  return p.T > p.B ? launch<true>(tq, a, stream) : launch<false>(tq, a, stream);
 }
 
 }  // namespace mla

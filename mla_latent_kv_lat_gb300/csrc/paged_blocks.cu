@@ -157,18 +157,18 @@ struct Choice {
   int R;              // candidates to take
 };
 // False: the token gets nothing (padding, or recorded).
-MLA_DEVINL bool choice_of(const SelectBlocksArgs& a, int64_t t, int nthreads, Choice& c) {
+MLA_DEVINL bool choice_of(const SelectBlocksArgs& a, int64_t t, int tid, int nthreads, Choice& c) {
   const int b = find_seq_warp(a.cu, a.B, static_cast<int32_t>(t));
   bool bad;
   const PagedSeq s = paged_seq(a.cu, a.seq_len, b, a.T, INT32_MAX - 4096, bad);
   if (t < s.q0 || t >= s.q0 + s.n) return false;
   c.own = (s.len - s.n + static_cast<int>(t - s.q0)) >> kBlockShift;
   if (c.own >= a.W) {                    // its blocks have no scores
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       record_error(a.err, MLA_ERR_INVALID_ARG);
       a.counts[t] = 0;
     }
-    for (int i = threadIdx.x; i < a.K; i += nthreads) a.blocks[t * a.K + i] = -1;
+    for (int i = tid; i < a.K; i += nthreads) a.blocks[t * a.K + i] = -1;
     return false;
   }
   const int c1 = max(0, c.own - a.n_local + 1);
@@ -179,36 +179,114 @@ MLA_DEVINL bool choice_of(const SelectBlocksArgs& a, int64_t t, int nthreads, Ch
 }
 // What needs no scores: the first blocks, the last, what lies behind them, the count;
 // with R == n all.
-MLA_DEVINL void write_sure(const SelectBlocksArgs& a, int64_t t, int nthreads, const Choice& c) {
+MLA_DEVINL void write_sure(const SelectBlocksArgs& a, int64_t t, int tid, int nthreads, const Choice& c) {
   int32_t* out = a.blocks + t * a.K;
   const int total = c.own + 1 - c.n + c.R, head = c.R == c.n ? total : c.c0;
-  for (int i = threadIdx.x; i < a.K; i += nthreads) {
+  for (int i = tid; i < a.K; i += nthreads) {
     if (i < head) out[i] = i;
     else if (i >= c.c0 + c.R) out[i] = i < total ? c.own - (total - 1 - i) : -1;
   }
-  if (threadIdx.x == 0) a.counts[t] = total;
+  if (tid == 0) a.counts[t] = total;
 }
 
+constexpr int kClose = 8;      // keys of a lane in the closer search
+
+// A block of threads takes one token; of those that are a warp's, kSingles.
+constexpr int kSingles = 4;
+
 template <int kWarps, int kPer>
-__global__ void __launch_bounds__(32 * kWarps) select_blocks_kernel(const SelectBlocksArgs a) {
-  constexpr int kN = 32 * kWarps, kWaves = kPer * kWarps, kEach = (kWaves + 31) / 32;
+__global__ void __launch_bounds__(kWarps == 1 ? 32 * kSingles : 32 * kWarps, kWarps > 1 ? 1 : kPer == 32 ? 8 : 5)
+    select_blocks_kernel(const SelectBlocksArgs a) {
+  constexpr int kN = 32 * kWarps, kWaves = kPer * kWarps, kEach = (kWaves + 31) / 32, kTok = kWarps == 1 ? kSingles : 1;
   __shared__ int s_cnt[2][kWarps];
-  __shared__ uint32_t s_wave[32 * kEach];
+  __shared__ uint32_t s_waves[kTok][32 * kEach];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0) record_bad_seqs(a.cu, a.seq_len, a.B, a.T, INT32_MAX - 4096, a.err);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = kWarps == 1 ? 0 : static_cast<int>(threadIdx.x >> 5);
+  const int tok = kWarps == 1 ? static_cast<int>(threadIdx.x >> 5) : 0, tid = kWarps == 1 ? lane : static_cast<int>(threadIdx.x);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTok + tok;
+  if (t >= a.T) return;
+  uint32_t* s_wave = s_waves[tok];
   Choice c;
-  if (!choice_of(a, t, kN, c)) return;
+  if (!choice_of(a, t, tid, kN, c)) return;
   const float* src = a.scores + t * a.stride + c.c0;
   uint32_t key[kPer];                    // of candidates tid + k kN (0: there is none)
   if (c.R > 0 && c.R < c.n) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) key[k] = tid + k * kN < c.n ? score_key(__ldg(src + tid + k * kN)) : 0u;
   }
-  write_sure(a, t, kN, c);
+  write_sure(a, t, tid, kN, c);
   if (c.R == 0 || c.R == c.n) return;
+  int32_t* out = a.blocks + t * a.K + c.c0;
+  if constexpr (kWarps == 1) {
+    // Of up to 32 (64) to take none lies below the least of the lanes' largest (second
+    // largest) keys, for each lane has that one or better.  What is left, a quarter as a
+    // rule, is written closely, in order, and the search goes on in an eighth of the keys.
+    uint32_t m1 = 0, m2 = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      m2 = max(m2, min(m1, key[k]));
+      m1 = max(m1, key[k]);
+    }
+    const uint32_t least = max(1u, __reduce_min_sync(0xffffffffu, c.R <= 32 ? m1 : m2)), top = __reduce_max_sync(0xffffffffu, m1);
+    int left = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) left += key[k] >= least;
+    left = __reduce_add_sync(0xffffffffu, left);
+    if (c.R <= 64 && left <= 32 * kClose) {
+      __shared__ uint32_t s_keys[kTok][32 * kClose];
+      __shared__ uint16_t s_ats[kTok][32 * kClose];
+      uint32_t* s_key = s_keys[tok];
+      uint16_t* s_at = s_ats[tok];
+      const uint32_t below = (1u << lane) - 1;
+      int at = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const uint32_t m = __ballot_sync(0xffffffffu, key[k] >= least);
+        if (key[k] >= least) {
+          const int p = at + __popc(m & below);
+          s_key[p] = key[k];
+          s_at[p] = static_cast<uint16_t>(lane + 32 * k);
+        }
+        at += __popc(m);
+      }
+      __syncwarp();
+      uint32_t close[kClose];
+#pragma unroll
+      for (int k = 0; k < kClose; ++k) close[k] = lane + 32 * k < left ? s_key[lane + 32 * k] : 0u;
+      auto count = [&](uint32_t y) {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kClose; ++k) n += close[k] >= y;
+        return static_cast<int>(__reduce_add_sync(0xffffffffu, n));
+      };
+      // all keys left share the bits above `bits`
+      const int bits = 32 - __clz(top ^ least);
+      uint32_t x = bits < 32 ? top >> bits << bits : 0u;
+      int n_x = left;                      // keys >= x
+      for (int bit = bits - 1; bit >= 0 && n_x != c.R; --bit) {
+        const uint32_t y = x | (1u << bit);
+        const int n = count(y);
+        if (n >= c.R) {
+          x = y;
+          n_x = n;
+        }
+      }
+      const int ties = n_x == c.R ? c.R : c.R - (x == 0xFFFFFFFFu ? 0 : count(x + 1));
+      int larger = 0, equal = 0;           // before this wave
+#pragma unroll
+      for (int k = 0; k < kClose; ++k) {
+        const uint32_t gt = __ballot_sync(0xffffffffu, close[k] > x), eq = __ballot_sync(0xffffffffu, close[k] == x);
+        const int eq_r = equal + __popc(eq & below);
+        if (close[k] > x || (close[k] == x && eq_r < ties))
+          out[larger + __popc(gt & below) + min(eq_r, ties)] = c.c0 + s_at[lane + 32 * k];
+        larger += __popc(gt);
+        equal += __popc(eq);
+      }
+      return;
+    }
+  }
   int buf = 0;
   auto count = [&](uint32_t y) -> int {
     int n = 0;
@@ -261,7 +339,6 @@ __global__ void __launch_bounds__(32 * kWarps) select_blocks_kernel(const Select
     if (lane >= o) before += v;
   }
   before -= sum;
-  int32_t* out = a.blocks + t * a.K + c.c0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const uint32_t gt = __ballot_sync(0xffffffffu, key[k] > x), eq = __ballot_sync(0xffffffffu, key[k] == x);
@@ -290,8 +367,8 @@ __global__ void __launch_bounds__(kLongThreads) select_long_kernel(const SelectB
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t t = blockIdx.x;
   Choice c;
-  if (!choice_of(a, t, kLongThreads, c)) return;
-  write_sure(a, t, kLongThreads, c);
+  if (!choice_of(a, t, tid, kLongThreads, c)) return;
+  write_sure(a, t, tid, kLongThreads, c);
   if (c.R == 0 || c.R == c.n) return;
   const float* src = a.scores + t * a.stride + c.c0;
   int buf = 0;
@@ -342,7 +419,8 @@ __global__ void __launch_bounds__(kLongThreads) select_long_kernel(const SelectB
 
 template <int kWarps, int kPer>
 cudaError_t launch_select(const SelectBlocksArgs& a, cudaStream_t stream) {
-  return launch_dependent(select_blocks_kernel<kWarps, kPer>, dim3(static_cast<unsigned>(a.T)), dim3(32 * kWarps), 0, stream, a);
+  return launch_dependent(select_blocks_kernel<kWarps, kPer>, dim3(static_cast<unsigned>(kWarps == 1 ? (a.T - 1) / kSingles + 1 : a.T)),
+                          dim3(32 * (kWarps == 1 ? kSingles : kWarps)), 0, stream, a);
 }
 
 }  // namespace
@@ -361,7 +439,7 @@ cudaError_t launch_select_blocks(const SelectBlocksArgs& a, cudaStream_t stream)
   // More tokens than the SMs hold blocks of few warps: as few warps as the row's keys fit.
   const bool many = a.T > 8 * device_sm_count();
   if (a.W <= 1024) return many ? launch_select<1, 32>(a, stream) : launch_select<4, 8>(a, stream);
-  if (a.W <= 2048) return many ? launch_select<2, 32>(a, stream) : launch_select<8, 8>(a, stream);
+  if (a.W <= 2048) return many ? launch_select<1, 64>(a, stream) : launch_select<8, 8>(a, stream);
   if (a.W <= 8192) return launch_select<8, 32>(a, stream);
   return launch_dependent(select_long_kernel, dim3(static_cast<unsigned>(a.T)), dim3(kLongThreads), 0, stream, a);
 }

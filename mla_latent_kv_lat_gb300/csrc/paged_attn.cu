@@ -184,6 +184,7 @@ struct TcArgs {
   int32_t* stage_base;   // [B] a sequence's first staged row, -1: not staged (unless take is kTakeAll);
                          // [kStageSeqs]: whether some sequence with new tokens is not
   uint16_t* stage;       // fp16 [kStageRows][512]
+  int32_t stage_blocks;  // of threads that stage
   int32_t n_slots;
   int32_t n_rows;     // rows of the page pool
   // kGroupLists: 2^gt_shift tokens share a block; a slot's entries (the tiles that some
@@ -1566,118 +1567,6 @@ __global__ void __launch_bounds__(128 * kCombRows, kFew ? 2 : 4) paged_combine_k
 }
 
 // ---------------------------------------------------------------------------
-// Staging: the latents of chosen sequences' visible rows as fp16.  Each block
-// scans the batch for the sequences' first staged rows (those that still fit
-// are staged), then the warps take four rows at a time; rows that no new token
-// sees become zero.  HBM-bound: 656 bytes in (512 + 16 used), 1024 out a row.
-// ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
-  __shared__ int32_t s_end[kStageSeqs];        // staged rows up to and with sequence b
-  __shared__ long long s_warp[8];
-  __shared__ int32_t s_total;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  long long sum = 0;
-  int32_t rows[kStageSeqs / 256];
-#pragma unroll
-  for (int q = 0; q < kStageSeqs / 256; ++q) {
-    const int b = tid * (kStageSeqs / 256) + q;
-    rows[q] = 0;
-    if (b < a.p.B) {
-      bool bad;
-      const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
-      if (worth_staging(a, s)) {
-        int32_t sink;
-        const int32_t first = seq_first_tile(a.p, s.len - s.n, sink);
-        const int64_t r = static_cast<int64_t>(sink + (s.len + kBK - 1) / kBK - first) * kBK;
-        rows[q] = static_cast<int32_t>(min(r, static_cast<int64_t>(kStageRows + 1)));
-      }
-    }
-    sum += rows[q];
-  }
-  long long incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) s_warp[warp] = incl;
-  if (tid == 0) s_total = 0;
-  __syncthreads();
-  long long end = incl - sum;
-  for (int w = 0; w < warp; ++w) end += s_warp[w];
-  // The sequences before the first that does not fit are staged.
-  bool left = false;
-#pragma unroll
-  for (int q = 0; q < kStageSeqs / 256; ++q) {
-    const int b = tid * (kStageSeqs / 256) + q;
-    const long long base = end;
-    end += rows[q];
-    s_end[b] = static_cast<int32_t>(min(end, static_cast<long long>(INT32_MAX)));
-    if (end <= kStageRows) atomicMax(&s_total, static_cast<int32_t>(end));
-    if (blockIdx.x == 0 && b < a.p.B) {
-      const bool staged = rows[q] > 0 && end <= kStageRows;
-      a.stage_base[b] = staged ? static_cast<int32_t>(base) : -1;
-      bool bad;
-      if (!staged && paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad).n > 0) left = true;
-    }
-  }
-  if (__syncthreads_or(left) != 0) left = true;
-  if (blockIdx.x == 0 && tid == 0) a.stage_base[kStageSeqs] = left;
-  const int32_t total = s_total;
-  // Staged row r: the sequence, the position, the pool row (-1: zero).
-  auto lookup = [&](int32_t r) -> int32_t {
-    if (r >= total) return -1;
-    int lo = 0, hi = kStageSeqs - 1;           // the first sequence with s_end > r
-    while (lo < hi) {
-      const int m = (lo + hi) >> 1;
-      if (s_end[m] > r) hi = m; else lo = m + 1;
-    }
-    bool bad;
-    const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, lo, a.p.T, a.p.c.max_rows(), bad);
-    const int32_t pos0 = s.len - s.n, x = r - (lo > 0 ? s_end[lo - 1] : 0);
-    int32_t sink;
-    const int32_t first = seq_first_tile(a.p, pos0, sink);
-    const int32_t t = x / kBK, p = (t < sink ? t : t - sink + first) * kBK + x % kBK;
-    const int32_t wlo = a.p.window > 0 ? max(0, pos0 - a.p.window + 1) : 0;
-    if (p >= s.len || (p < wlo && p >= a.p.n_sink)) return -1;
-    return static_cast<int32_t>(a.p.c.row_of(lo, p));      // a bad page: recorded by the attention
-  };
-  const int32_t step = 4 * static_cast<int32_t>(gridDim.x) * 8;
-  int32_t r0 = 4 * (static_cast<int32_t>(blockIdx.x) * 8 + warp);
-  int32_t row_n = lane < 4 ? lookup(r0 + lane) : -1;
-  for (; r0 < total; r0 += step) {
-    const int32_t row_l = row_n;
-    uint2 v[8];
-    uint32_t sc = 0x70707070u;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int32_t row = __shfl_sync(0xffffffffu, row_l, k >> 1);
-      v[k] = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.p.c.pages + static_cast<int64_t>(row) * kRowE4m3) + lane +
-                              32 * (k & 1))
-                      : make_uint2(0, 0);
-    }
-    const int32_t row_s = __shfl_sync(0xffffffffu, row_l, (lane >> 2) & 3);
-    if (lane < 16 && row_s >= 0)
-      sc = __ldg(reinterpret_cast<const uint32_t*>(a.p.c.pages + static_cast<int64_t>(row_s) * kRowE4m3 + kE4m3ScaleOff) +
-                 (lane & 3));
-    if (lane < 4) row_n = lookup(r0 + step + lane);
-    uint4* dst = reinterpret_cast<uint4*>(a.stage + static_cast<int64_t>(r0) * kLatent) + lane;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // unit lane + 32 (k & 1): scale byte lane / 4 + 8 (k & 1) of the row
-      const uint32_t w = __shfl_sync(0xffffffffu, sc, 4 * (k >> 1) + 2 * (k & 1) + (lane >> 4));
-      const uint32_t d = e4m3_scale_f16x2((w >> (8 * ((lane >> 2) & 3))) & 0xFFu);
-      uint4 o;
-      e4m3x4_to_f16x4(v[k].x, d, o.x, o.y);
-      e4m3x4_to_f16x4(v[k].y, d, o.z, o.w);
-      dst[32 * k] = o;
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
 // Lists of groups.  A block has 128 rows, so with H <= 64 heads several tokens fit in
 // one; neighbouring tokens list much the same blocks, and a tile costs a block of 128
 // rows no more than one of H.  One block of threads a group: each token's entries as
@@ -1687,19 +1576,14 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kMapWords = 512, kMapTokens = 8;         // positions of a map: 2^14 blocks at a time
 
-__global__ void __launch_bounds__(256) paged_lists_kernel(const TcArgs a) {
+MLA_DEVINL void list_group(const TcArgs& a, int g) {
   __shared__ uint32_t map[kMapTokens][kMapWords];
   __shared__ uint32_t any[kMapWords];
   __shared__ int32_t offs[kMapWords + 1];
   __shared__ int32_t s_warp[8];
   __shared__ int s_again;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // Beside the staging, of which nothing is read here: it let this kernel start when what
-  // came before it had ended, and only its own end is waited for, below.
-  const bool beside = a.stage_base != nullptr;
-  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int g = static_cast<int>(blockIdx.x), K = a.p.K;
+  const int K = a.p.K;
   // the group's sequence: the largest b with a first slot <= g, 32 at a time
   int b = 0;
   for (int n = a.p.B; n > 1;) {
@@ -1712,10 +1596,7 @@ __global__ void __launch_bounds__(256) paged_lists_kernel(const TcArgs a) {
   bool bad;
   const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
   const int64_t i = g - slot_of_seq<kGroupLists>(a, b);
-  if (i < 0 || (i << a.gt_shift) >= s.n) {
-    if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
+  if (i < 0 || (i << a.gt_shift) >= s.n) return;
   const int tok = static_cast<int>(i) << a.gt_shift, nt = min(1 << a.gt_shift, s.n - tok);
   const int pos = s.len - s.n + tok;                   // of the first token
   const int32_t* lists = a.p.blocks + static_cast<int64_t>(s.q0 + tok) * K;
@@ -1806,7 +1687,129 @@ __global__ void __launch_bounds__(256) paged_lists_kernel(const TcArgs a) {
     }
   }
   if (tid == 0) a.group_counts[g] = total;
-  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(256) paged_lists_kernel(const TcArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  list_group(a, static_cast<int>(blockIdx.x));
+}
+
+// ---------------------------------------------------------------------------
+// Staging: the latents of chosen sequences' visible rows as fp16.  Each block
+// scans the batch for the sequences' first staged rows (those that still fit
+// are staged), then the warps take four rows at a time; rows that no new token
+// sees become zero.  HBM-bound: 656 bytes in (512 + 16 used), 1024 out a row.
+// The blocks behind the first stage_blocks list groups.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
+  __shared__ int32_t s_end[kStageSeqs];        // staged rows up to and with sequence b
+  __shared__ long long s_warp[8];
+  __shared__ int32_t s_total;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (static_cast<int>(blockIdx.x) >= a.stage_blocks) {
+    list_group(a, static_cast<int>(blockIdx.x) - a.stage_blocks);
+    return;
+  }
+  long long sum = 0;
+  int32_t rows[kStageSeqs / 256];
+#pragma unroll
+  for (int q = 0; q < kStageSeqs / 256; ++q) {
+    const int b = tid * (kStageSeqs / 256) + q;
+    rows[q] = 0;
+    if (b < a.p.B) {
+      bool bad;
+      const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad);
+      if (worth_staging(a, s)) {
+        int32_t sink;
+        const int32_t first = seq_first_tile(a.p, s.len - s.n, sink);
+        const int64_t r = static_cast<int64_t>(sink + (s.len + kBK - 1) / kBK - first) * kBK;
+        rows[q] = static_cast<int32_t>(min(r, static_cast<int64_t>(kStageRows + 1)));
+      }
+    }
+    sum += rows[q];
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  if (tid == 0) s_total = 0;
+  __syncthreads();
+  long long end = incl - sum;
+  for (int w = 0; w < warp; ++w) end += s_warp[w];
+  // The sequences before the first that does not fit are staged.
+  bool left = false;
+#pragma unroll
+  for (int q = 0; q < kStageSeqs / 256; ++q) {
+    const int b = tid * (kStageSeqs / 256) + q;
+    const long long base = end;
+    end += rows[q];
+    s_end[b] = static_cast<int32_t>(min(end, static_cast<long long>(INT32_MAX)));
+    if (end <= kStageRows) atomicMax(&s_total, static_cast<int32_t>(end));
+    if (blockIdx.x == 0 && b < a.p.B) {
+      const bool staged = rows[q] > 0 && end <= kStageRows;
+      a.stage_base[b] = staged ? static_cast<int32_t>(base) : -1;
+      bool bad;
+      if (!staged && paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad).n > 0) left = true;
+    }
+  }
+  if (__syncthreads_or(left) != 0) left = true;
+  if (blockIdx.x == 0 && tid == 0) a.stage_base[kStageSeqs] = left;
+  const int32_t total = s_total;
+  // Staged row r: the sequence, the position, the pool row (-1: zero).
+  auto lookup = [&](int32_t r) -> int32_t {
+    if (r >= total) return -1;
+    int lo = 0, hi = kStageSeqs - 1;           // the first sequence with s_end > r
+    while (lo < hi) {
+      const int m = (lo + hi) >> 1;
+      if (s_end[m] > r) hi = m; else lo = m + 1;
+    }
+    bool bad;
+    const PagedSeq s = paged_seq(a.p.cu, a.p.seq_len, lo, a.p.T, a.p.c.max_rows(), bad);
+    const int32_t pos0 = s.len - s.n, x = r - (lo > 0 ? s_end[lo - 1] : 0);
+    int32_t sink;
+    const int32_t first = seq_first_tile(a.p, pos0, sink);
+    const int32_t t = x / kBK, p = (t < sink ? t : t - sink + first) * kBK + x % kBK;
+    const int32_t wlo = a.p.window > 0 ? max(0, pos0 - a.p.window + 1) : 0;
+    if (p >= s.len || (p < wlo && p >= a.p.n_sink)) return -1;
+    return static_cast<int32_t>(a.p.c.row_of(lo, p));      // a bad page: recorded by the attention
+  };
+  const int32_t step = 4 * a.stage_blocks * 8;
+  int32_t r0 = 4 * (static_cast<int32_t>(blockIdx.x) * 8 + warp);
+  int32_t row_n = lane < 4 ? lookup(r0 + lane) : -1;
+  for (; r0 < total; r0 += step) {
+    const int32_t row_l = row_n;
+    uint2 v[8];
+    uint32_t sc = 0x70707070u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int32_t row = __shfl_sync(0xffffffffu, row_l, k >> 1);
+      v[k] = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.p.c.pages + static_cast<int64_t>(row) * kRowE4m3) + lane +
+                              32 * (k & 1))
+                      : make_uint2(0, 0);
+    }
+    const int32_t row_s = __shfl_sync(0xffffffffu, row_l, (lane >> 2) & 3);
+    if (lane < 16 && row_s >= 0)
+      sc = __ldg(reinterpret_cast<const uint32_t*>(a.p.c.pages + static_cast<int64_t>(row_s) * kRowE4m3 + kE4m3ScaleOff) +
+                 (lane & 3));
+    if (lane < 4) row_n = lookup(r0 + step + lane);
+    uint4* dst = reinterpret_cast<uint4*>(a.stage + static_cast<int64_t>(r0) * kLatent) + lane;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // unit lane + 32 (k & 1): scale byte lane / 4 + 8 (k & 1) of the row
+      const uint32_t w = __shfl_sync(0xffffffffu, sc, 4 * (k >> 1) + 2 * (k & 1) + (lane >> 4));
+      const uint32_t d = e4m3_scale_f16x2((w >> (8 * ((lane >> 2) & 3))) & 0xFFu);
+      uint4 o;
+      e4m3x4_to_f16x4(v[k].x, d, o.x, o.y);
+      e4m3x4_to_f16x4(v[k].y, d, o.z, o.w);
+      dst[32 * k] = o;
+    }
+  }
 }
 
 int clusters() { return max(1, min(kMaxClusters, device_sm_count() / 2)); }
@@ -1942,9 +1945,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     a.stage_base = stage_base;
     e = make_tmap_row_groups(&tm, a.stage, kStageRows / 8, kLatent / 64, kLatent * 2, kBK / 8, 4);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(paged_stage_kernel, dim3(device_sm_count() * 4), dim3(256), 0, stream, a);
-    if (e != cudaSuccess) return e;
-    e = lists();
+    a.stage_blocks = device_sm_count() * 4;
+    e = launch_dependent(paged_stage_kernel, dim3(static_cast<unsigned>(a.stage_blocks + groups)), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
     a.take = kTakeStaged;
     e = launch_for<false, false>(tm, tr, tq, tq, a, stream);

@@ -551,7 +551,7 @@ cudaError_t launch(const CUtensorMap& tq, const Args& a, cudaStream_t stream) {
   }
   const int64_t sms = device_sm_count();
   // a run of single tokens is one group: no more CTAs than there can be runs
-  const int64_t grid = kKeep ? sms : min(sms, static_cast<int64_t>(a.p.T) * a.tiles);
+  const int64_t grid = a.p.T > a.p.B ? sms : min(sms, static_cast<int64_t>(a.p.T) * a.tiles);
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), Cfg<kKeep>::kSmem, stream, tq, a);
 }
 
@@ -569,7 +569,11 @@ cudaError_t launch_block_scores(const BlockScoresArgs& p, cudaStream_t stream) {
   cudaError_t e = make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kChunks, kLatent * 2, 128, 64,
                                static_cast<uint32_t>(p.H << a.gt_shift), 1);
   if (e != cudaSuccess) return e;
-  return p.T > p.B ? launch<true>(tq, a, stream) : launch<false>(tq, a, stream);
+  // Mean rows are kept from 2.5 groups an SM on.  (From shared memory and kept, 3 tiles:
+  // 64 heads, 8 sequences of 32 tokens 12.7 and 12.7 us, of 64 22.3 and 20.7, 32 of 4 10.5
+  // and 10.9, of 32 39.7 and 32.3; one of 64 7.8 and 8.6.)
+  const bool keep = p.T > p.B && 2 * static_cast<int64_t>(p.T >> a.gt_shift) * a.tiles > 5 * device_sm_count();
+  return keep ? launch<true>(tq, a, stream) : launch<false>(tq, a, stream);
 }
 
 }  // namespace mla

@@ -1868,13 +1868,23 @@ cudaError_t launch_for(const CUtensorMap& tm, const CUtensorMap& tr, const CUten
 
 // How the lists of a call are grouped: 2^shift tokens a block, the number of slots (0:
 // each token by itself).  Single tokens have no neighbours; with more than 64 heads no
-// two fit; and lists as long as the room does not hold stay as they are.
+// two fit; and lists as long as the room does not hold stay as they are.  Making the
+// groups' lists takes 5 us, which few tiles do not give back.  (Each token by itself and
+// in groups, lists of 32 blocks of 20000 rows: 16 heads, 16 tokens 21 and 26 us, 64 43 and
+// 32, 8 x 4 30 and 30, 8 x 16 74 and 45, 32 x 16 255 and 111; 64 heads, 64 tokens 48 and
+// 48, 8 x 8 50 and 50, 32 x 4 86 and 81, 32 x 16 272 and 223.)
 int64_t group_slots(const PagedAttnArgs& p, int32_t& shift) {
   shift = 0;
   if (p.blocks == nullptr || p.T <= p.B || 2 * p.H > kRows) return 0;
   while ((2 * p.H << shift) <= kRows) ++shift;
+  if (static_cast<int64_t>(p.T) * p.K < (shift > 1 ? 16 : 28) * clusters()) {
+    shift = 0;
+    return 0;
+  }
   const int64_t slots = (static_cast<int64_t>(p.T) >> shift) + p.B;
-  return (slots << shift) * p.K <= kGroupEntries ? slots : 0;
+  if ((slots << shift) * p.K <= kGroupEntries) return slots;
+  shift = 0;
+  return 0;
 }
 
 // (16 bytes behind the sequences' entries: whether all are staged)
@@ -1939,9 +1949,12 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   e = make_tmap_3d(&tr, p.c.pages + kE4m3RopeOff, false, kRope, n, 1, kRowE4m3, n * kRowE4m3, kRopeHalf, box, 1, 64);
   if (e != cudaSuccess) return e;
   // A batch of single tokens (T <= B) has no sequence of several blocks, bar one
-  // with empty sequences beside it.
+  // with empty sequences beside it.  With lists, the staging and the second launch (14 us)
+  // are a fifth of the tiles' time at 64 tiles a cluster, and so is the conversion of
+  // every tile that they save.
   if (p.T > p.B && p.B <= kStageSeqs &&
-      (p.blocks != nullptr ? p.T >= kStageBlocks : static_cast<int64_t>(p.T) * p.H > (kStageBlocks - 1) * kRows)) {
+      (p.blocks != nullptr ? static_cast<int64_t>(p.T >> max(0, a.gt_shift - 1)) * p.K >= 64 * G
+                           : static_cast<int64_t>(p.T) * p.H > (kStageBlocks - 1) * kRows)) {
     a.stage_base = stage_base;
     e = make_tmap_row_groups(&tm, a.stage, kStageRows / 8, kLatent / 64, kLatent * 2, kBK / 8, 4);
     if (e != cudaSuccess) return e;

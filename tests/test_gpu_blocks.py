@@ -197,7 +197,8 @@ def test_block_keys_skips_bad_pages():
 @pytest.mark.parametrize("ps,news,lens,pad,width", [
     (64, [1], [1], 0, 1), (64, [1], [65], 0, 5), (128, [1, 0, 1, 1], [8300, 0, 63, 16385], 2, 257),
     (64, [70, 3, 1], [70, 400, 129], 1, 7), (256, [300], [8500], 0, 133), (4096, [9, 40], [20000, 16384 + 40], 0, 313),
-    (64, [1] * 40, [64 * k + 1 for k in range(40)], 0, 45)])
+    (64, [1] * 40, [64 * k + 1 for k in range(40)], 0, 45), (64, [0, 3, 0, 0], [0, 9000, 5, 0], 0, 150),
+    (128, [700, 1, 333], [30000, 20000, 400], 1, 480)])
 def test_block_scores(H, ps, news, lens, pad, width):
     b = Batch(10, False, H, ps, news, lens, pad=pad)
     rng = np.random.default_rng(11)
@@ -383,7 +384,7 @@ def check(b, out, status=0):
     (16, 64, [1], [1], 1, "all", 0), (16, 64, [1], [65], 4, "all", 0), (128, 64, [1], [5000], 40, "all", 0),
     (128, 128, [1, 0, 1, 1], [700, 0, 64, 2049], 5, "random", 2), (64, 64, [1] * 9, [300 + 67 * k for k in range(9)], 3, "all", 0),
     (32, 256, [70, 3, 1], [70, 400, 129], 4, "random", 1), (128, 64, [33], [3000], 17, "all", 0),
-    (48, 4096, [9, 40], [5000, 4136], 33, "random", 0), (112, 64, [130], [131], 3, "all", 3), (16, 64, [260], [700], 2, "random", 0)])
+    (48, 4096, [9, 40], [5000, 4136], 33, "random", 0), (32, 64, [0, 3, 0, 0], [0, 900, 5, 0], 4, "random", 0), (112, 64, [130], [131], 3, "all", 3), (16, 64, [260], [700], 2, "random", 0)])
 def test_attention_over_listed_blocks(e4m3, H, ps, news, lens, K, mode, pad):
     b = Listed(14, e4m3, H, ps, news, lens, K, mode, pad)
     check(b, attend(b))
@@ -465,22 +466,39 @@ def test_neighbours_with_lists_of_their_own(e4m3, H):
     """Chunks in which tokens share blocks of 128 rows: lists that agree, differ, are empty, name a block again or no
     block, and tiles whose later rows only tokens see that do not list them."""
     lists = [[0], [1, 0], [], [0, 1], [1, 1, 0, 1], [0], [], [1], [0, 0], [1], [1, 0], [0]]
-    b = Listed(31, e4m3, H, 64, [12], [70], 5, lists=lists)           # positions 58 .. 69: up to 63, block 1 is ahead
-    check(b, attend(b), INVALID)
+    for K in (5, 400):
+        b = Listed(31, e4m3, H, 64, [12], [70], K, lists=lists)       # positions 58 .. 69: up to 63, block 1 is ahead
+        check(b, attend(b), INVALID)
     lists = [list(range(t % 5)) + [7 + t % 3] for t in range(60)]
-    b = Listed(32, e4m3, H, 128, [37, 2, 21], [700, 650, 900], 9, lists=lists, pad=1)
-    check(b, attend(b))
+    for K in (9, 64):                    # (long rows of short lists: enough entries to go in groups)
+        b = Listed(32, e4m3, H, 128, [37, 2, 21], [700, 650, 900], K, lists=lists, pad=1)
+        check(b, attend(b))
     lists[10], lists[41] = [-1, 3, 1 << 25], [3, 50, 3, 3, 2]
-    b = Listed(33, e4m3, H, 128, [37, 2, 21], [700, 650, 900], 9, lists=lists, pad=1)
-    check(b, attend(b), INVALID)
+    for K in (9, 64):
+        b = Listed(33, e4m3, H, 128, [37, 2, 21], [700, 650, 900], K, lists=lists, pad=1)
+        check(b, attend(b), INVALID)
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("lens", [[600, 5000, 25000], [600, 640, 700], [30000, 26000, 25000]], ids=["some", "all", "none"])
+def test_e4m3_chunks_converted_beforehand_or_not(H, lens):
+    """Enough entries that sequences whose rows are read often are converted before the attention: some of them, all,
+    none."""
+    news = [80, 3 if lens[1] > 700 else 70, 40]
+    pos = [l - n + i for n, l in zip(news, lens) for i in range(n)]
+    lists = [sorted({(5 * t) % (p // 64 + 1), p // 64, 0, (t // 3) % (p // 64 + 1)}) for t, p in enumerate(pos)]
+    b = Listed(37, True, H, 128, news, lens, 64, lists=lists, pad=1)
+    check(b, attend(b))
 
 
 def test_counts_outside_the_lists_of_a_group_are_reported():
-    b = Listed(34, False, 16, 64, [5], [400], 3, lists=[[0, 1, 2], [3], [1], [], [0, 4]])
+    lists = [[t % 6] for t in range(600)]
+    lists[:5] = [[0, 1, 2], [3], [1], [], [0, 4]]
+    b = Listed(34, False, 16, 64, [600], [1000], 3, lists=lists)
     d = b.dev()
-    d["counts"] += torch.tensor([5, -9, 0, 0, 0], dtype=torch.int32, device="cuda")
+    d["counts"][:2] += torch.tensor([5, -9], dtype=torch.int32, device="cuda")
     out = attend(b, d)
-    b.counts[:] = [3, 0, 1, 0, 2]
+    b.counts[1] = 0
     check(b, out, INVALID)
 
 
@@ -490,16 +508,16 @@ def test_more_lists_than_the_workspace_groups():
     check(b, attend(b), INVALID)         # (block 32 is ahead of the first 48 tokens)
 
 
-@pytest.mark.parametrize("H", [16, 128])
-def test_contexts_past_a_million_rows(H):
-    """Two pages stand in for all of a context's."""
+@pytest.mark.parametrize("H,K", [(16, 4), (16, 1024), (128, 4)])
+def test_contexts_past_a_million_rows(H, K):
+    """Two pages stand in for all of a context's; lists of few entries, in rows that are short and long."""
     rng, L, n = np.random.default_rng(36), 1_100_003, 3
     rows = rng.standard_normal((8192, 576)).astype(np.float16)
     table = rng.integers(0, 2, (1, -(-L // 4096))).astype(np.int32)
     lists = [[17000, 5, 16383, 17187], [16384, 5, 0], [17187, 16385, 5, 40]]
     q_lat = rng.standard_normal((n, H, 512)).astype(np.float16)
     q_pe = bf16(rng.standard_normal((n, H, 64)))
-    blocks = np.full((n, 4), -1, np.int32)
+    blocks = np.full((n, K), -1, np.int32)
     for t, x in enumerate(lists):
         blocks[t, :len(x)] = x
     out = torch.empty(n, H, 512, dtype=torch.float16, device="cuda")

@@ -181,8 +181,7 @@ struct TcArgs {
   float* ws_o;        // fp32 [2 G][128][512] partials, normalised by their own sums
   float* ws_ml;       // fp32 [2 G][128][2] running maximum (log2 units, less kPShift) and sum
   Rec* rec;           // [G]
-  int32_t* stage_base;   // [B] a sequence's first staged row, -1: not staged (unless take is kTakeAll);
-                         // [kStageSeqs]: whether some sequence with new tokens is not
+  int32_t* stage_base;   // [B] a sequence's first staged row, -1: not staged (unless take is kTakeAll)
   uint16_t* stage;       // fp16 [kStageRows][512]
   int32_t stage_blocks;  // of threads that stage
   int32_t n_slots;
@@ -682,17 +681,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
   const int c = static_cast<int>(blockIdx.x >> 1), G = static_cast<int>(gridDim.x >> 1);
   constexpr int NT = threads(kE4m3);
 
-  // Every sequence is staged: the kernel for fp16 pages has taken them all.
-  if constexpr (kE4m3) {
-    if (a.take == kTakeUnstaged) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      if (a.stage_base[kStageSeqs] == 0) {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if (rank == 0 && threadIdx.x == 0) a.rec[c].nvalid = 0;
-        return;
-      }
-    }
-  }
   // ---- setup ---------------------------------------------------------------
   if (warp == kPvWarp) {
     // a lane per barrier: how many arrivals complete a phase
@@ -1700,8 +1688,9 @@ __global__ void __launch_bounds__(256) paged_lists_kernel(const TcArgs a) {
 // scans the batch for the sequences' first staged rows (those that still fit
 // are staged), then the warps take four rows at a time; rows that no new token
 // sees become zero.  HBM-bound: 656 bytes in (512 + 16 used), 1024 out a row.
-// The blocks behind the first stage_blocks list groups.
+// kGroups: the blocks behind the first stage_blocks list groups.
 // ---------------------------------------------------------------------------
+template <bool kGroups>
 __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
   __shared__ int32_t s_end[kStageSeqs];        // staged rows up to and with sequence b
   __shared__ long long s_warp[8];
@@ -1709,9 +1698,11 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (static_cast<int>(blockIdx.x) >= a.stage_blocks) {
-    list_group(a, static_cast<int>(blockIdx.x) - a.stage_blocks);
-    return;
+  if constexpr (kGroups) {
+    if (static_cast<int>(blockIdx.x) >= a.stage_blocks) {
+      list_group(a, static_cast<int>(blockIdx.x) - a.stage_blocks);
+      return;
+    }
   }
   long long sum = 0;
   int32_t rows[kStageSeqs / 256];
@@ -1743,7 +1734,6 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
   long long end = incl - sum;
   for (int w = 0; w < warp; ++w) end += s_warp[w];
   // The sequences before the first that does not fit are staged.
-  bool left = false;
 #pragma unroll
   for (int q = 0; q < kStageSeqs / 256; ++q) {
     const int b = tid * (kStageSeqs / 256) + q;
@@ -1751,15 +1741,10 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
     end += rows[q];
     s_end[b] = static_cast<int32_t>(min(end, static_cast<long long>(INT32_MAX)));
     if (end <= kStageRows) atomicMax(&s_total, static_cast<int32_t>(end));
-    if (blockIdx.x == 0 && b < a.p.B) {
-      const bool staged = rows[q] > 0 && end <= kStageRows;
-      a.stage_base[b] = staged ? static_cast<int32_t>(base) : -1;
-      bool bad;
-      if (!staged && paged_seq(a.p.cu, a.p.seq_len, b, a.p.T, a.p.c.max_rows(), bad).n > 0) left = true;
-    }
+    if (blockIdx.x == 0 && b < a.p.B)
+      a.stage_base[b] = rows[q] > 0 && end <= kStageRows ? static_cast<int32_t>(base) : -1;
   }
-  if (__syncthreads_or(left) != 0) left = true;
-  if (blockIdx.x == 0 && tid == 0) a.stage_base[kStageSeqs] = left;
+  __syncthreads();
   const int32_t total = s_total;
   // Staged row r: the sequence, the position, the pool row (-1: zero).
   auto lookup = [&](int32_t r) -> int32_t {
@@ -1779,7 +1764,7 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
     if (p >= s.len || (p < wlo && p >= a.p.n_sink)) return -1;
     return static_cast<int32_t>(a.p.c.row_of(lo, p));      // a bad page: recorded by the attention
   };
-  const int32_t step = 4 * a.stage_blocks * 8;
+  const int32_t step = 4 * (kGroups ? a.stage_blocks : static_cast<int32_t>(gridDim.x)) * 8;
   int32_t r0 = 4 * (static_cast<int32_t>(blockIdx.x) * 8 + warp);
   int32_t row_n = lane < 4 ? lookup(r0 + lane) : -1;
   for (; r0 < total; r0 += step) {
@@ -1887,8 +1872,7 @@ int64_t group_slots(const PagedAttnArgs& p, int32_t& shift) {
   return 0;
 }
 
-// (16 bytes behind the sequences' entries: whether all are staged)
-size_t stage_bytes() { return (kStageSeqs + 4) * sizeof(int32_t) + static_cast<size_t>(kStageRows) * kLatent * 2; }
+size_t stage_bytes() { return kStageSeqs * sizeof(int32_t) + static_cast<size_t>(kStageRows) * kLatent * 2; }
 
 }  // namespace
 
@@ -1905,7 +1889,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   a.ws_ml = a.ws_o + rows * kLatent;
   a.rec = reinterpret_cast<Rec*>(a.ws_ml + rows * 2);
   int32_t* stage_base = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(p.workspace) + partial_bytes());
-  a.stage = reinterpret_cast<uint16_t*>(stage_base + kStageSeqs + 4);
+  a.stage = reinterpret_cast<uint16_t*>(stage_base + kStageSeqs);
   a.n_slots = p.blocks != nullptr ? p.T : static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
   a.n_rows = p.c.n_pages << p.c.page_shift;
   const int64_t groups = group_slots(p, a.gt_shift);
@@ -1959,7 +1943,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
     e = make_tmap_row_groups(&tm, a.stage, kStageRows / 8, kLatent / 64, kLatent * 2, kBK / 8, 4);
     if (e != cudaSuccess) return e;
     a.stage_blocks = device_sm_count() * 4;
-    e = launch_dependent(paged_stage_kernel, dim3(static_cast<unsigned>(a.stage_blocks + groups)), dim3(256), 0, stream, a);
+    e = launch_dependent(groups > 0 ? paged_stage_kernel<true> : paged_stage_kernel<false>,
+                         dim3(static_cast<unsigned>(a.stage_blocks + groups)), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
     a.take = kTakeStaged;
     e = launch_for<false, false>(tm, tr, tq, tq, a, stream);

@@ -61,11 +61,13 @@ struct Args {
 // Where a CTA's share of the work begins.  Work: for each sequence and each tile that
 // some new token has a block in, the groups with such a token (the last ones, since
 // positions grow), plus kRunCost for the run's start: one run of costs over all
-// sequences, which the CTAs share evenly.
+// sequences, which the CTAs share evenly.  (Its length is at most (1 + kRunCost) T
+// tiles, and a row of scores has 128 values a tile: it passes 2^32 with more than 512 GB
+// of scores.)
 constexpr int kRunCost = 3;            // mean rows' load, in groups
 struct Start {
-  int64_t lo, hi;      // this CTA's range in the run of costs
-  int64_t S;           // where sequence b's cost starts in it
+  uint32_t lo, hi;     // this CTA's range in the run of costs
+  uint32_t S;          // where sequence b's cost starts in it
   int32_t b;           // the sequence that holds lo (B: nothing to do)
 };
 
@@ -77,7 +79,7 @@ struct Bars {
   uint64_t s_full[2], s_empty[2];
   uint32_t tmem;
   Start st;
-  long long red[kThreads / 32];
+  uint32_t red[kThreads / 32];
   int32_t row[kTile];                  // the run's mean rows in the pool, -1: none
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers");
@@ -101,11 +103,11 @@ struct Seq {
   MLA_DEVINL int groups(const Args& a) const { return (s.n + (1 << a.gt_shift) - 1) >> a.gt_shift; }
   // The first group whose last token has a block in `tile` (< tiles()).
   MLA_DEVINL int first(const Args& a, int tile) const {
-    const int64_t need = (static_cast<int64_t>(tile) * kTile + 1) * kBlockRows - (s.len - s.n);   // tokens before one that has
-    return need <= 0 ? 0 : static_cast<int>(need >> a.gt_shift);
+    const int need = (tile * kTile + 1) * kBlockRows - (s.len - s.n);       // tokens before one that has
+    return max(0, need) >> a.gt_shift;
   }
-  MLA_DEVINL int64_t cost(const Args& a) const {
-    int64_t c = 0;
+  MLA_DEVINL uint32_t cost(const Args& a) const {
+    uint32_t c = 0;
     for (int tile = tiles(a) - 1; tile >= 0; --tile) c += kRunCost + groups(a) - first(a, tile);
     return c;
   }
@@ -113,7 +115,7 @@ struct Seq {
 
 // This CTA's groups in order; every role walks the same ones.
 struct Walk {
-  int64_t lo, hi, S;
+  uint32_t lo, hi, S;
   int32_t b, tile, tiles, i, i1;
   Seq q;
   MLA_DEVINL void init(const Args& a, const Start& st) {
@@ -141,9 +143,9 @@ struct Walk {
       }
       if (S >= hi) return false;
       const int first = q.first(a, tile), n = q.groups(a) - first;
-      const int64_t r0 = S + kRunCost;
+      const uint32_t r0 = S + kRunCost;
       S = r0 + n;
-      const int64_t p_lo = max(lo, r0), p_hi = min(hi, S);
+      const uint32_t p_lo = max(lo, r0), p_hi = min(hi, S);
       if (p_lo >= p_hi) continue;
       i = first + static_cast<int32_t>(p_lo - r0);
       i1 = first + static_cast<int32_t>(p_hi - r0);
@@ -219,15 +221,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (a.p.B + kThreads - 1) / kThreads;
     const int b0 = min(a.p.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.p.B, b0 + per);
     Seq q;
-    int64_t sum = 0;
+    uint32_t sum = 0;
     for (int b = b0; b < b1; ++b) {
       q.load(a, b);
       sum += q.cost(a);
     }
-    long long incl = sum;
+    uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
     if (lane == 31) B.red[warp] = incl;
@@ -235,20 +237,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();                   // (the barriers and tensor memory are ready, too)
     tc::fence_after_sync();
-    int64_t total = 0, S = incl - sum;
+    uint32_t total = 0, S = incl - sum;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       total += B.red[w];
       if (w < warp) S += B.red[w];
     }
-    const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-    if (lo < hi && sum > 0 && S <= lo && lo < S + sum) {
+    const uint32_t share = total / gridDim.x, more = total % gridDim.x;    // the first `more` CTAs take one more
+    const uint32_t lo = share * blockIdx.x + min(blockIdx.x, more), hi = lo + share + (blockIdx.x < more ? 1 : 0);
+    if (lo < hi && S <= lo && lo < S + sum) {
       int b = b0;
-      for (; b < b1; ++b) {
-        q.load(a, b);
-        const int64_t c = q.cost(a);
-        if (lo < S + c) break;
-        S += c;
+      if (per > 1) {
+        for (; b < b1; ++b) {
+          q.load(a, b);
+          const uint32_t c = q.cost(a);
+          if (lo < S + c) break;
+          S += c;
+        }
       }
       B.st = {lo, hi, S, b};
     }

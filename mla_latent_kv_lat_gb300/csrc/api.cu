@@ -264,6 +264,9 @@ Span keys_span(const PagedCache& c, const void* keys) {
   return {keys, (static_cast<int64_t>(c.n_pages) << c.page_shift) / kBlockRows * kRow * 2};
 }
 
+// Scores of a row: no context has more blocks.
+constexpr int32_t kMaxScores = 1 << 25;
+
 // What a call with blocks of positions needs of its cache and lists.
 int check_blocks(const mla_paged_cache* cache, std::initializer_list<const int32_t*> lists, int32_t K) {
   if (cache == nullptr || K < 1) return MLA_ERR_INVALID_ARG;
@@ -669,7 +672,7 @@ int mla_paged_block_scores(const mla_dims* dims, const void* q_lat, const void* 
   if (s != MLA_OK) return s;
   if (T < 1 || n_scores < 1 || score_stride < 0 || (T > 1 && score_stride < n_scores)) return MLA_ERR_INVALID_ARG;
   const int64_t rows = int64_t{T} * dims->n_head;
-  if (rows > INT32_MAX || score_stride > (int64_t{1} << 40) / T) return MLA_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX || n_scores > kMaxScores || score_stride > (int64_t{1} << 40) / T) return MLA_ERR_UNSUPPORTED;
   if (overlap({scores, 4 * ((T - 1) * score_stride + n_scores)},
               {{q_lat, rows * kLatent * 2}, {q_pe, rows * kRope * 2}, keys_span(a.c, block_keys), table_span(a.c, B),
                i32_span(cu_q, int64_t{B} + 1), i32_span(seq_len, B)}))
@@ -699,7 +702,8 @@ int mla_paged_select_blocks(const float* scores, int64_t score_stride, int32_t n
   if (B < 1 || T < 1 || n_scores < 1 || K < 1 || n_sink < 0 || n_local < 1) return MLA_ERR_INVALID_ARG;
   if (score_stride < 0 || (T > 1 && score_stride < n_scores)) return MLA_ERR_INVALID_ARG;
   if (int64_t{n_sink} + n_local > K) return MLA_ERR_INVALID_ARG;
-  if (B > 65535 || K > MLA_MAX_BLOCKS || score_stride > (int64_t{1} << 40) / T) return MLA_ERR_UNSUPPORTED;
+  if (B > 65535 || K > MLA_MAX_BLOCKS || n_scores > kMaxScores || score_stride > (int64_t{1} << 40) / T)
+    return MLA_ERR_UNSUPPORTED;
   const Span out[2] = {i32_span(blocks, int64_t{T} * K), i32_span(counts, T)};
   for (int i = 0; i < 2; ++i)
     if (overlap(out[i], {{scores, 4 * ((T - 1) * score_stride + n_scores)}, i32_span(cu_q, int64_t{B} + 1),

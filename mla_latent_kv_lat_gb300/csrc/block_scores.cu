@@ -595,7 +595,7 @@ cudaError_t launch_block_scores(const BlockScoresArgs& p, cudaStream_t stream) {
   // Tokens of a group are of one sequence: with single tokens there is one.
   if (p.T > p.B)
     while ((2 * p.H << a.gt_shift) <= kMaxN) ++a.gt_shift;
-  a.tiles = (p.W + kTile - 1) / kTile;
+  a.tiles = (p.W - 1) / kTile + 1;
   CUtensorMap tq;
   const uint64_t qrows = static_cast<uint64_t>(p.T) * static_cast<uint64_t>(p.H);
   cudaError_t e = make_tmap_3d(&tq, p.q_lat, false, 64, qrows, kChunks, kLatent * 2, 128, 64,

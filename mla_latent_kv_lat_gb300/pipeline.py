@@ -228,6 +228,8 @@ def mla_paged_sparse_step(q, kv, q_weight, kv_weight, wk_b, wv_b, pages, block_k
     if bufs is None:
         with B.stream_context(stream, dev):
             bufs = sparse_buffers(T, H, max(1, block_table.shape[1] * pages.shape[1] // B.BLOCK), n_blocks, q.device)
+    elif bufs.blocks.shape[1] != n_blocks:
+        raise ValueError(f"bufs are for lists of {bufs.blocks.shape[1]} blocks, n_blocks is {n_blocks}")
     # (the cache calls check their other tensors)
     for name, t in (("wk_b", wk_b), ("wv_b", wv_b), ("bufs.q_lat", bufs.q_lat), ("bufs.o", bufs.o)):
         if B.paged_device(t, name) != dev:

@@ -98,7 +98,8 @@ BAD = [
     ("select", dict(T=0), -1), ("select", dict(B=0), -1), ("select", dict(n_scores=0), -1), ("select", dict(ss=8), -1),
     ("select", dict(n_sink=-1), -1), ("select", dict(n_local=0), -1), ("select", dict(K=0), -1), ("select", dict(n_sink=2, n_local=2), -1),
     ("select", dict(n_sink=2 ** 31 - 1, n_local=2 ** 31 - 1), -1), ("select", dict(K=1025), -2), ("select", dict(B=65536), -2),
-    ("select", dict(ss=1 << 40), -2),
+    ("select", dict(ss=1 << 40), -2), ("select", dict(ss=1 << 26, n_scores=1 << 26), -2),
+    ("scores", dict(ss=1 << 26, n_scores=1 << 26), -2), ("scores", dict(ss=2 ** 31 - 1, n_scores=2 ** 31 - 1), -2),
     ("attn", dict(blocks=None), -1), ("attn", dict(counts=None), -1), ("attn", dict(blocks=ODD4), -3), ("attn", dict(counts=ODD4), -3),
     ("attn", dict(K=0), -1), ("attn", dict(K=-1), -1), ("attn", dict(K=1025), -2), ("attn", dict(T=0), -1), ("attn", dict(B=0), -1),
     ("attn", dict(q_lat=None), -1), ("attn", dict(o=ODD), -3), ("attn", dict(ws=None), -4), ("attn", dict(ws_bytes=16), -4),
@@ -327,6 +328,7 @@ def test_a_step_on_another_device_runs_all_its_calls_there(monkeypatch, lib):
     args = dict(q=on1(2, H, 192, dtype=BF), kv=on1(2, 576, dtype=BF), q_weight=None, kv_weight=on1(512, dtype=BF),
                 wk_b=on1(H, 128, 512, dtype=BF), wv_b=on1(H, 512, 128, dtype=BF), pages=on1(3, 64, 576, dtype=F16),
                 block_keys=on1(3, 1, 576, dtype=F16), block_table=on1(1, 2), cu_q=on1(2), seq_len=on1(1))
+    args["n_blocks"] = 3
     pipeline.mla_paged_sparse_step(**args, bufs=bufs)
     assert [c[0] for c in seen] == ["mla_paged_norm_append", "mla_paged_block_keys", "mla_absorb_q", "mla_paged_block_scores",
                                     "mla_paged_select_blocks", "mla_attn_paged_blocks", "mla_late_decompress"]
@@ -339,6 +341,8 @@ def test_a_step_on_another_device_runs_all_its_calls_there(monkeypatch, lib):
     bufs.o = bufs.o.as_subclass(OnDevice0)
     with pytest.raises(ValueError, match="bufs.o"):
         pipeline.mla_paged_sparse_step(**args, bufs=bufs)
+    with pytest.raises(ValueError, match="n_blocks"):
+        pipeline.mla_paged_sparse_step(**dict(args, n_blocks=4), bufs=bufs)
     assert not seen
 
 

@@ -356,8 +356,37 @@ def mla_rope_append(c_kv, k_pe, pos, slot, kv=None, kv_q=None, kv_d=None, freq_b
     _check("mla_rope_append", st)
 
 
-# The paged calls are made once per layer of a decode step, where their own time on the host counts: they check
-# with single comparisons and go through _need's detailed messages only when one fails.
+_calls = None
+
+
+class _Unbuilt:
+    """No compiled way yet: the way through Python says that the library is missing."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _fast():
+    """The compiled way to the paged calls (csrc/calls.cpp): its functions return the call's status, or None for
+    arguments that are not plainly right.  Those take the way through Python, which says what is wrong with them."""
+    global _calls
+    if _calls is None:
+        path = _build.calls_path()
+        if not os.path.exists(_build.LIB):
+            return _Unbuilt()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{os.path.basename(path)} is not built; run __graft_entry__.build() first")
+        spec = importlib.util.spec_from_file_location("_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(_build.LIB)
+        _calls = module
+    return _calls
+
+
+# The paged calls are made once per layer of a decode step, where their own time on the host counts: they go through
+# the compiled module above, and what that leaves to them they check
+# with single comparisons, going through _need's detailed messages only when one fails.
 def _arg(t, name: str, dtype, shape, dev: int) -> int:
     """Device address of a contiguous tensor of this type and shape on CUDA device ``dev``."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
@@ -422,6 +451,9 @@ def mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base:
                      freq_scale: float = 0.025, stream=None):
     """New tokens' rows into their pages: token i of sequence b's n new ones (rows cu_new[b].. of c_kv, k_pe) is
     written at position seq_len[b] - n + i, its RoPE part rotated by that position, in the pages' type."""
+    st = (_calls or _fast()).append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base, freq_scale, stream)
+    if st is not None:
+        return _check("mla_paged_append", st)
     dev = paged_device(c_kv, "c_kv")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -437,6 +469,9 @@ def mla_paged_append(c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base:
 
 def mla_paged_gather(pages, block_table, row0, cu_rows, out, stream=None):
     """out [R, 576] (bf16 or fp16): rows cu_rows[b].. <- positions row0[b].. of sequence b (row0 None: from 0)."""
+    st = (_calls or _fast()).gather(pages, block_table, row0, cu_rows, out, stream)
+    if st is not None:
+        return _check("mla_paged_gather", st)
     dev = paged_device(out, "out")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -462,6 +497,10 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
     """o_lat [T, H, 512]: attention of the batch's new tokens over their pages (one token a sequence or a chunk);
     window > 0 keeps each token's last ``window`` positions and the first ``n_sink``.  Without a workspace a fresh
     one is taken from PyTorch's allocator."""
+    st = (_calls or _fast()).attn(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window, n_sink, workspace, scale,
+                                  stream)
+    if st is not None:
+        return _check("mla_attn_paged", st)
     dev = paged_device(q_lat, "q_lat")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -484,26 +523,6 @@ def mla_attn_paged(q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window
         workspace.numel(),
         _arg(o_lat, "o_lat", torch.float16, (T, H, KV_LORA_RANK), dev), _stream_on(stream, dev))
     _check("mla_attn_paged", st)
-
-
-_calls = None
-
-
-def _fast():
-    """The compiled way to the calls below (csrc/calls.cpp): its functions return the call's status, or None for
-    arguments that are not plainly right.  Those take the way through Python, which says what is wrong with them."""
-    global _calls
-    if _calls is None:
-        load_library()
-        path = _build.calls_path()
-        if not os.path.exists(path):
-            raise RuntimeError(f"{os.path.basename(path)} is not built; run __graft_entry__.build() first")
-        spec = importlib.util.spec_from_file_location("_calls", path)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        module.bind(_build.LIB)
-        _calls = module
-    return _calls
 
 
 def _fit(value: int, name: str) -> int:

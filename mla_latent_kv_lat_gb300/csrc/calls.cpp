@@ -23,6 +23,9 @@ namespace {
 constexpr int64_t kLatent = 512, kRope = 64, kNope = 128, kRow = 576, kRowE4m3 = 656, kBlock = 64;
 
 struct Lib {
+  decltype(&::mla_paged_append) append;
+  decltype(&::mla_paged_gather) gather;
+  decltype(&::mla_attn_paged) attn;
   decltype(&::mla_paged_norm_append) norm_append;
   decltype(&::mla_paged_block_keys) block_keys;
   decltype(&::mla_paged_block_scores) block_scores;
@@ -153,6 +156,36 @@ PyObject* norm_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// c_kv, k_pe, pages, block_table, cu_new, seq_len, freq_base, freq_scale, stream
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> int {
+    const at::Tensor& kv = tensor(a[0]);
+    const int dev = device_of(kv);
+    need(kv.dim() == 2);
+    const int64_t T = kv.size(0);
+    int32_t B;
+    const mla_paged_cache c = paged(a[2], a[3], dev, B);
+    return lib.append(&c, contiguous(a[0], at::kBFloat16, {T, kLatent}, dev), contiguous(a[1], at::kBFloat16, {T, kRope}, dev),
+                      i32(a[4], {int64_t{B} + 1}, dev), i32(a[5], {B}, dev), B, fit(T), number(a[6]), number(a[7]),
+                      stream(a[8], dev));
+  });
+}
+
+// pages, block_table, row0, cu_rows, out, stream
+PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> int {
+    const at::Tensor& out = tensor(a[4]);
+    const int dev = device_of(out);
+    const bool f16 = out.scalar_type() == at::kHalf;
+    need(out.dim() == 2);
+    const int64_t R = out.size(0);
+    int32_t B;
+    const mla_paged_cache c = paged(a[0], a[1], dev, B);
+    return lib.gather(&c, a[2] == Py_None ? nullptr : i32(a[2], {B}, dev), i32(a[3], {int64_t{B} + 1}, dev), B, fit(R),
+                      contiguous(a[4], f16 ? at::kHalf : at::kBFloat16, {R, kRow}, dev), f16, stream(a[5], dev));
+  });
+}
+
 // pages, block_table, cu_new, seq_len, block_keys, T, stream
 PyObject* block_keys(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 7, [&]() -> int {
@@ -218,6 +251,22 @@ PyObject* select_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// q_lat, q_pe, pages, block_table, cu_q, seq_len, o_lat, window, n_sink, workspace, scale, stream
+PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> int {
+    const Queries q(a[0]);
+    const mla_dims d = dims(q.H, a[10]);
+    int32_t B;
+    const mla_paged_cache c = paged(a[2], a[3], q.dev, B);
+    const at::Tensor& ws = tensor(a[9]);
+    need(ws.scalar_type() == at::kByte && ws.is_cuda() && ws.get_device() == q.dev && ws.is_contiguous());
+    return lib.attn(&d, q.t.data_ptr(), contiguous(a[1], at::kBFloat16, {q.T, q.H, kRope}, q.dev), &c,
+                    i32(a[4], {int64_t{B} + 1}, q.dev), i32(a[5], {B}, q.dev), B, fit(q.T), integer(a[7]), integer(a[8]),
+                    ws.data_ptr(), static_cast<size_t>(ws.numel()), contiguous(a[6], at::kHalf, {q.T, q.H, kLatent}, q.dev),
+                    stream(a[11], q.dev));
+  });
+}
+
 // q_lat, q_pe, pages, block_table, cu_q, seq_len, blocks, counts, o_lat, workspace, scale, stream
 PyObject* attn_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> int {
@@ -246,7 +295,8 @@ PyObject* bind(PyObject*, PyObject* path) {
     f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(dlsym(h, name));
     return f != nullptr;
   };
-  if (!find(lib.norm_append, "mla_paged_norm_append") || !find(lib.block_keys, "mla_paged_block_keys") ||
+  if (!find(lib.append, "mla_paged_append") || !find(lib.gather, "mla_paged_gather") || !find(lib.attn, "mla_attn_paged") ||
+      !find(lib.norm_append, "mla_paged_norm_append") || !find(lib.block_keys, "mla_paged_block_keys") ||
       !find(lib.block_scores, "mla_paged_block_scores") || !find(lib.select_blocks, "mla_paged_select_blocks") ||
       !find(lib.attn_blocks, "mla_attn_paged_blocks"))
     return PyErr_Format(PyExc_RuntimeError, "%s lacks a function", p);
@@ -255,6 +305,9 @@ PyObject* bind(PyObject*, PyObject* path) {
 
 #define MLA_FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
 PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
+                         {"append", MLA_FAST(append), METH_FASTCALL, nullptr},
+                         {"gather", MLA_FAST(gather), METH_FASTCALL, nullptr},
+                         {"attn", MLA_FAST(attn), METH_FASTCALL, nullptr},
                          {"norm_append", MLA_FAST(norm_append), METH_FASTCALL, nullptr},
                          {"block_keys", MLA_FAST(block_keys), METH_FASTCALL, nullptr},
                          {"block_scores", MLA_FAST(block_scores), METH_FASTCALL, nullptr},

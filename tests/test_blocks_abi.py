@@ -285,7 +285,7 @@ def test_the_compiled_way_leaves_what_is_not_plainly_right_to_the_binding(lib):
     """It returns None for tensors that are on no GPU, for no tensors, and for too few arguments."""
     fast = binding._fast()
     cpu = torch.zeros(2, 16, 512, dtype=F16)
-    for f, n in ((fast.norm_append, 14), (fast.block_keys, 7), (fast.block_scores, 9), (fast.select_blocks, 8), (fast.attn_blocks, 12)):
+    for f, n in ((fast.append, 9), (fast.gather, 6), (fast.attn, 12), (fast.norm_append, 14), (fast.block_keys, 7), (fast.block_scores, 9), (fast.select_blocks, 8), (fast.attn_blocks, 12)):
         assert f(*[cpu] * n) is None and f(*[None] * n) is None and f(*[3.5] * n) is None and f() is None
         assert f(*[cpu] * (n + 1)) is None
 

@@ -764,6 +764,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
       if (lane >= o) incl += x;
     }
     if (lane == 31) red[warp] = incl;
+    // kLists: blocks of this warp's slots, the costliest
+    int2* red_n = reinterpret_cast<int2*>(red + NT / 32);
+    const uint32_t some = kLists != kNoLists ? __ballot_sync(0xffffffffu, sum > 0) : 0u;
+    if constexpr (kLists != kNoLists) {
+      const int most = __reduce_max_sync(0xffffffffu, static_cast<int>(sum));
+      if (lane == 0) red_n[warp] = make_int2(__popc(some), most);
+    }
     __syncthreads();
     const long long part = lane < NT / 32 ? red[lane] : 0;
     const long long total = warp_sum_wide(part), before = warp_sum_wide(lane < warp ? part : 0);
@@ -797,6 +804,26 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(max_regs(kE4m3))
     } else {
       lo = total * c / G;
       hi = total * (c + 1) / G;
+    }
+    if constexpr (kLists != kNoLists) {
+      // Lists are short, and the partials of cut blocks may cost more than the equal share
+      // saves: then each block is a cluster's.  The partials' cost in tiles, with the blocks'
+      // rows, as measured with lists of 8 to 64 blocks (equal shares and a block a cluster,
+      // 128 heads: 16 tokens of 8 blocks 21.1 and 19.2 us, of 32 30.0 and 46.1, 32 of 16
+      // 33.4 and 31.8, of 32 40.7 and 47.4, 64 of 8 37.5 and 26.8, of 32 61.5 and 50.5, of
+      // 64 91.3 and 84.5; 16 heads: 64 of 8 26.4 and 23.3, of 64 74.5 and 78.1).
+      const int2 x = lane < NT / 32 ? red_n[lane] : make_int2(0, 0);
+      const int n_blocks = __reduce_add_sync(0xffffffffu, x.x), most = __reduce_max_sync(0xffffffffu, x.y);
+      const int rank = __reduce_add_sync(0xffffffffu, lane < warp ? x.x : 0) + __popc(some & ((1u << lane) - 1));
+      const float rows = min(1.f, static_cast<float>(a.p.H << a.gt_shift) * (1.f / kRows));
+      const float equal = share > 0 ? static_cast<float>(share) : static_cast<float>(total) / G;
+      const float pieces = share > 0 ? static_cast<float>(total) / share : static_cast<float>(G);
+      const float merge = (pieces + n_blocks) * (0.04f + 0.08f * rows) * (kE4m3 ? 0.85f : 1.f);   // (their tiles take longer)
+      if (per == 1 && n_blocks <= G && static_cast<float>(most) - equal < merge) {
+        lo = S0;
+        hi = sum > 0 && rank == c ? S0 + sum : S0;
+        share = 0;
+      }
     }
     if (lo < hi && sum > 0 && S0 <= lo && lo < S0 + sum) {
       long long S = S0;

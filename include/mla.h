@@ -500,8 +500,9 @@ int mla_paged_block_keys(const mla_paged_cache* cache, const int32_t* cu_new, co
  *   scores[t][j] = scale * max over heads h of
  *                  (q_lat[t][h] . block_keys[j][0..511] + q_pe[t][h] . block_keys[j][512..575])
  * for j < p / 64 (block j of the token's sequence), -inf for p / 64 <= j < n_scores.
- * q_lat, q_pe as in mla_attn_paged.  cache: its table and sizes; its pages and
- * type are not looked at.  The mean rows of these blocks must be there and finite.
+ * q_lat, q_pe as in mla_attn_paged, finite for the batch's tokens.  cache: its
+ * table and sizes; its pages and type are not looked at.  The mean rows of these
+ * blocks must be there and finite.
  * scores, out: device fp32, row t at scores + t * score_stride, n_scores of
  * each row (n_scores <= 2^25, score_stride >= n_scores).  A token at a position of 64 * (n_scores + 1) or
  * behind has blocks without a score: recorded as MLA_ERR_INVALID_ARG.

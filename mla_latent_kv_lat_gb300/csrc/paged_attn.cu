@@ -295,10 +295,9 @@ struct Walker {
       if (i < 0 || i * gt * a.H >= rows) return 0;
       const int32_t tok = static_cast<int32_t>(i) * gt, nt = min(gt, seq.n - tok);
       int32_t listed = __ldg((kLists == kGroupLists ? t.group_counts : a.counts) + g);
-      if (kLists == kTokenLists && (listed < 0 || listed > a.K)) {
-        record_error(a.err, MLA_ERR_INVALID_ARG);
-        listed = max(0, min(listed, a.K));
-      }
+      if (kLists == kTokenLists && (listed < 0 || listed > a.K)) record_error(a.err, MLA_ERR_INVALID_ARG);
+      // (With a cu that decreases, the groups' lists and this walk may disagree on the slots.)
+      listed = max(0, min(listed, gt * a.K));
       it.b = b;
       it.nvalid = nt * a.H;
       it.once = seq.n <= 2;
@@ -388,7 +387,7 @@ MLA_DEVINL Entry list_entry(const TcArgs& a, const Item& it, int t) {
   if (t >= it.n_tiles || x >= it.first) return none;
   if constexpr (kLists == kGroupLists) {
     const uint2 e = __ldg(a.group_lists + ((static_cast<int64_t>(it.slot) << a.gt_shift) * a.p.K + x));
-    return {static_cast<int32_t>(e.x), e.y};
+    return e.x < static_cast<uint32_t>(it.kend) ? Entry{static_cast<int32_t>(e.x), e.y} : none;
   }
   const int32_t e = __ldg(a.p.blocks + static_cast<int64_t>(it.slot) * a.p.K + x);
   return e >= 0 && e <= (it.kend - 1) / kBK ? Entry{e * kBK, 1u} : none;

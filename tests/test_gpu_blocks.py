@@ -122,6 +122,34 @@ def test_norm_append(e4m3, H, q_norm, packed, ps, news, lens, pad):
     assert (np.abs(vals[:, :512] - lat) <= (2.0 ** -4 + 2 * rel) * np.abs(lat) + 2.0 ** -10 * s).all()
 
 
+def test_norm_append_takes_broadcast_inputs_and_refuses_odd_places():
+    b = Batch(39, False, 16, 64, [5, 2], [70, 2])
+    H, T = 32, 7
+    one_q, one_kv = torch.randn(1, 1, 192, device="cuda").bfloat16(), torch.randn(1, 576, device="cuda").bfloat16()
+    w, qw = torch.ones(512, dtype=torch.bfloat16, device="cuda"), torch.ones(192, dtype=torch.bfloat16, device="cuda")
+
+    def go(q, kv):
+        pages = b.pages_dev().nan_to_num_(0.0)
+        outs = [torch.empty(T, H, n, dtype=torch.bfloat16, device="cuda") for n in (128, 64)]
+        mla.mla_paged_norm_append(q, kv, qw, w, pages, full_table(b), i32(b.cu), i32(b.lens), *outs)
+        torch.cuda.synchronize()
+        assert mla.mla_get_device_error() == 0
+        return outs + [pages]
+
+    q, kv = one_q.expand(T, H, 192), one_kv.expand(T, 576)               # strides of zero
+    for x, y in zip(go(q, kv), go(q.contiguous(), kv.contiguous())):
+        assert torch.equal(x, y)
+    heads_first = q.transpose(0, 1).contiguous().transpose(0, 1)          # [H, T, 192] in memory
+    assert torch.equal(go(heads_first, kv)[1], go(q, kv)[1])
+    odd = torch.zeros(T, 576 + 8, dtype=torch.bfloat16, device="cuda")
+    for bad in (odd[:, 4:580], torch.zeros(T, 580, dtype=torch.bfloat16, device="cuda")[:, :576]):
+        with pytest.raises(mla.MLAError) as e:
+            go(q, bad)
+        assert e.value.status == -3
+    with pytest.raises(ValueError, match="last dimension"):
+        go(q, torch.zeros(576, T, dtype=torch.bfloat16, device="cuda").t())
+
+
 def test_norm_append_reports_what_rows_cannot_hold_and_bad_pages():
     b = Batch(7, False, 16, 64, [2, 1], [80, 5])
     H, n = 16, 3
@@ -489,6 +517,28 @@ def test_e4m3_chunks_converted_beforehand_or_not(H, lens):
     lists = [sorted({(5 * t) % (p // 64 + 1), p // 64, 0, (t // 3) % (p // 64 + 1)}) for t, p in enumerate(pos)]
     b = Listed(37, True, H, 128, news, lens, 64, lists=lists, pad=1)
     check(b, attend(b))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H,n", [(16, 40), (64, 40), (128, 3), (16, 600)])
+def test_decreasing_offsets_are_reported(e4m3, H, n):
+    """Outputs are undefined then; the calls end, inside their memory, and the next ones are as ever."""
+    lists = [[t % 5, 7] for t in range(3 * n)]
+    b = Listed(38, e4m3, H, 64, [n, n, n], [1400, 1200, 1300], 96, lists=lists)
+    d = b.dev()
+    ws = torch.randint(0, 256, (mla.mla_paged_workspace_size(H),), dtype=torch.uint8, device="cuda")
+    scores, keys = torch.empty(b.T, 23, device="cuda"), torch.zeros(b.n_pages, 1, 576, dtype=torch.float16, device="cuda")
+    blocks, counts = torch.empty(b.T, 4, dtype=torch.int32, device="cuda"), torch.empty(b.T, dtype=torch.int32, device="cuda")
+    full = full_table(b)
+    for cu in ([0, 2 * n, n, 3 * n], [3 * n, 2 * n, n, 0], [0, -5, n, 2 * n], [n, 0, 3 * n, 3 * n], [0, n, 1 << 30, 3 * n]):
+        bad = dict(d, cu_q=i32(cu))
+        attend(b, bad, workspace=ws)
+        mla.mla_paged_block_scores(d["q_lat"], d["q_pe"], keys, full, i32(cu), d["seq_len"], scores, scale=SCALE)
+        mla.mla_paged_select_blocks(scores, i32(cu), d["seq_len"], blocks, counts, n_sink=1, n_local=1)
+        mla.mla_paged_block_keys(d["pages"], full, i32(cu), d["seq_len"], keys, b.T)
+        torch.cuda.synchronize()
+        assert mla.mla_get_device_error() == INVALID
+    check(b, attend(b, d, workspace=ws))
 
 
 def test_counts_outside_the_lists_of_a_group_are_reported():

@@ -2,6 +2,7 @@
 // 64 positions, and the choice of a token's blocks from their scores.
 #include "kernels.cuh"
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace mla {
 namespace {
@@ -13,9 +14,10 @@ namespace {
 // (n new tokens complete at most ceil(n / 64) blocks, so ranges do not overlap).
 // HBM-bound: a block of threads reads a block's 64 rows whole, each thread 16 bytes
 // of every kGroups-th row, eight of them under way at once (sixteen leave room for
-// half the blocks on an SM: 23.5 us instead of 19.6).  98304 fp16 rows: 19.6 us, 5.9 TB/s,
-// 88% of the copy rate; the one block that 64 single tokens complete, e4m3: 3.7 us, a
-// launch and the lookups.
+// half the blocks on an SM: 23.5 us instead of 19.5; a grid that stays, its next block
+// looked up beside the rows: 19.8, for e4m3 18.2 instead of 16.8).  98304 fp16 rows: 19.5 us,
+// 5.9 TB/s, 88% of the copy rate; e4m3 16.8 us; the one block that 64 single tokens complete:
+// 3.3 us, a launch and the lookups.
 // ---------------------------------------------------------------------------
 template <bool kE4m3>
 struct KeyCfg {
@@ -27,12 +29,18 @@ struct KeyCfg {
   static_assert(!kE4m3 || kRowsEach == kAtOnce, "one pass");
 };
 
+// The two halves of w (fp16) added to x[0], x[1] in fp32.
+MLA_DEVINL void add2(float* x, uint32_t w) {
+  x[0] = tc::add_f16lo_f32(w, x[0]);
+  x[1] = tc::add_f16hi_f32(w, x[1]);
+}
+
 MLA_DEVINL int64_t key_slot(const BlockKeysArgs& a, int b) {
   return (max(0, min(a.T, __ldg(a.cu + b))) >> kBlockShift) + b;
 }
 
 template <bool kE4m3>
-__global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads, kE4m3 ? 2 : 4) block_keys_kernel(const BlockKeysArgs a) {
+__global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads, kE4m3 ? 3 : 4) block_keys_kernel(const BlockKeysArgs a) {
   using C = KeyCfg<kE4m3>;
   __shared__ float part[C::kGroups][kRow];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -40,21 +48,28 @@ __global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads, kE4m3 ? 2 : 4) block_
   if (blockIdx.x == 0) record_bad_seqs(a.cu, a.seq_len, a.B, a.T, a.c.max_rows(), a.err);
   const int unit = threadIdx.x % C::kUnits, grp = threadIdx.x / C::kUnits;
   const int64_t slots = (a.T >> kBlockShift) + a.B;
-  for (int64_t g = blockIdx.x; g < slots; g += gridDim.x) {
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (key_slot(a, m) <= g) lo = m; else hi = m;
+  // First row of slot g's block, -1: none.
+  auto find = [&](int64_t g) -> int64_t {
+    int lo = 0, n = a.B;                       // the largest b with key_slot(b) <= g, 32 at a time
+    const int lane = threadIdx.x & 31;
+    while (n > 1) {
+      const int step = (n + 31) / 32, m = lo + lane * step;
+      const uint32_t le = __ballot_sync(0xffffffffu, lane == 0 || (m < lo + n && key_slot(a, m) <= g));
+      const int k = 31 - __clz(le);
+      n = min(step, n - k * step);
+      lo += k * step;
     }
     bool bad;
     const PagedSeq s = paged_seq(a.cu, a.seq_len, lo, a.T, a.c.max_rows(), bad);
-    const int64_t j = ((s.len - s.n) >> kBlockShift) + (g - key_slot(a, lo));     // the sequence's block
-    if (s.n == 0 || g < key_slot(a, lo) || j >= (s.len >> kBlockShift)) continue;
+    const int64_t g0 = key_slot(a, lo), j = ((s.len - s.n) >> kBlockShift) + (g - g0);     // the sequence's block
+    if (s.n == 0 || g < g0 || j >= (s.len >> kBlockShift)) return -1;
     const int64_t row0 = a.c.row_of(lo, j << kBlockShift);
-    if (row0 < 0) {
-      if (threadIdx.x == 0) record_error(a.err, MLA_ERR_INVALID_ARG);
-      continue;
-    }
+    if (row0 < 0 && threadIdx.x == 0) record_error(a.err, MLA_ERR_INVALID_ARG);
+    return row0;
+  };
+  for (int64_t g = blockIdx.x; g < slots; g += gridDim.x) {
+    const int64_t row0 = find(g);
+    if (row0 < 0) continue;
     constexpr int kBytes = kE4m3 ? kRowE4m3 : kRowF16;
     const uint8_t* src = a.c.pages + row0 * kBytes;
     if constexpr (!kE4m3) {
@@ -69,11 +84,7 @@ __global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads, kE4m3 ? 2 : 4) block_
         for (int r = 0; r < C::kAtOnce; ++r) {
           const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 f = f16x2_to_f32(w[q]);
-            x[2 * q] += f.x;
-            x[2 * q + 1] += f.y;
-          }
+          for (int q = 0; q < 4; ++q) add2(x + 2 * q, w[q]);
         }
       }
 #pragma unroll
@@ -99,19 +110,12 @@ __global__ void __launch_bounds__(KeyCfg<kE4m3>::kThreads, kE4m3 ? 2 : 4) block_
           for (int q = 0; q < 4; ++q) {
             uint32_t lo2, hi2;
             e4m3x4_to_f16x4(w[q], sc, lo2, hi2);
-            const float2 f = f16x2_to_f32(lo2), h = f16x2_to_f32(hi2);
-            x[4 * q] += f.x;
-            x[4 * q + 1] += f.y;
-            x[4 * q + 2] += h.x;
-            x[4 * q + 3] += h.y;
+            add2(x + 4 * q, lo2);
+            add2(x + 4 * q + 2, hi2);
           }
         } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 f = f16x2_to_f32(w[q]);
-            x[2 * q] += f.x;
-            x[2 * q + 1] += f.y;
-          }
+          for (int q = 0; q < 4; ++q) add2(x + 2 * q, w[q]);
         }
       }
       float* dst = &part[grp][unit < 32 ? 16 * unit : kLatent + 8 * (unit - 32)];

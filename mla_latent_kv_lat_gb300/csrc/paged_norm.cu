@@ -35,9 +35,9 @@ MLA_DEVINL void unpack8(uint4 v, float (&x)[8]) {
   }
 }
 
-// Position of token j, or -1 for padding and invalid sequences; b its sequence.
+// Position of token j (a warp's), or -1 for padding and invalid sequences; b its sequence.
 MLA_DEVINL int32_t token_pos(const NormAppendArgs& a, int32_t j, int& b) {
-  b = find_seq(a.cu, a.B, j);
+  b = find_seq_warp(a.cu, a.B, j);
   bool bad;
   const PagedSeq s = paged_seq(a.cu, a.seq_len, b, a.T, a.c.max_rows(), bad);
   return j >= s.q0 && j < s.q0 + s.n ? s.len - s.n + (j - s.q0) : -1;
@@ -48,7 +48,7 @@ MLA_DEVINL int32_t token_pos(const NormAppendArgs& a, int32_t j, int& b) {
 // so that a head's sum takes three exchanges and every access is 128 bytes wide.
 // The angles are computed once a task: a head's own would cost more than its loads.
 // HBM-bound: 8192 tokens of 128 heads into e4m3 rows 122 us, 6.7 TB/s; 64 tokens into
-// fp16 rows 3.5 us, a launch and the lookups.
+// fp16 rows 3.1 us, a launch and the lookups.
 template <bool kE4m3>
 __global__ void __launch_bounds__(256, 4) norm_append_kernel(const __grid_constant__ NormAppendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");

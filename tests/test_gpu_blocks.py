@@ -779,3 +779,51 @@ def test_calls_agree_with_the_plain_append():
     torch.cuda.synchronize()
     assert mla.mla_get_device_error() == 0
     assert torch.equal(pages[0], pages[1])
+
+
+def test_the_compiled_way_and_the_way_through_python_agree(monkeypatch):
+    """Every paged call by the compiled module, which has to take it, and by the binding alone: the same bits."""
+    from mla_latent_kv_lat_gb300 import binding as B
+    H, T = 16, 90
+    b = Listed(40, False, H, 64, [89, 1], [300, 500], 3, "all")
+    d, full = b.dev(), full_table(b)
+    rows = b.pages_dev().nan_to_num_(0.0)
+    g = lambda *s, dt=torch.bfloat16: torch.randn(*s, device="cuda").to(dt)  # noqa: E731
+    q, kv, qw, kw = g(T, H, 192), g(T, 576), g(192), g(512)
+    c_kv, k_pe, keys = g(T, 512), g(T, 64), torch.zeros(b.n_pages, 1, 576, dtype=torch.float16, device="cuda")
+    ws = torch.empty(mla.mla_paged_workspace_size(H), dtype=torch.uint8, device="cuda")
+    cu, ln = d["cu_q"], d["seq_len"]
+
+    def outs():
+        e = lambda *s, dt=torch.float16: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+        return dict(pages=rows.clone(), q_nope=e(T, H, 128, dt=torch.bfloat16), q_pe=e(T, H, 64, dt=torch.bfloat16),
+                    gathered=e(T, 576, dt=torch.bfloat16), keys=keys.clone(), scores=e(T, 8, dt=torch.float32),
+                    blocks=e(T, 3, dt=torch.int32), counts=e(T, dt=torch.int32), o=e(T, H, 512), whole=e(T, H, 512))
+
+    def calls(o, stream):
+        ws_blocks = (d["blocks"], d["counts"])
+        return [
+            ("append", mla.mla_paged_append, (c_kv, k_pe, o["pages"], full, cu, ln, 1e4, 0.025, stream)),
+            ("norm_append", mla.mla_paged_norm_append, (q, kv, qw, kw, o["pages"], full, cu, ln, o["q_nope"], o["q_pe"], 1e-6,
+                                                        1e4, 0.025, stream)),
+            ("gather", mla.mla_paged_gather, (o["pages"], full, ln - torch.diff(cu), cu, o["gathered"], stream)),
+            ("block_keys", mla.mla_paged_block_keys, (o["pages"], full, i32([0, 300, 800]), ln, o["keys"], 800, stream)),
+            ("block_scores", mla.mla_paged_block_scores, (d["q_lat"], d["q_pe"], o["keys"], full, cu, ln, o["scores"], SCALE,
+                                                          stream)),
+            ("select_blocks", mla.mla_paged_select_blocks, (o["scores"], cu, ln, o["blocks"], o["counts"], 1, 1, stream)),
+            ("attn_blocks", mla.mla_attn_paged_blocks, (d["q_lat"], d["q_pe"], o["pages"], full, cu, ln, *ws_blocks, o["o"], ws, SCALE,
+                                                        stream)),
+            ("attn", mla.mla_attn_paged, (d["q_lat"], d["q_pe"], o["pages"], full, cu, ln, o["whole"], 0, 0, ws, SCALE, stream))]
+
+    fast, slow, handle = outs(), outs(), outs()
+    for name, _, args in calls(fast, None):
+        assert getattr(B._fast(), name)(*args) == 0, name
+    for _, fn, args in calls(handle, torch.cuda.current_stream().cuda_stream):
+        fn(*args)
+    monkeypatch.setattr(B, "_calls", B._Unbuilt())
+    for _, fn, args in calls(slow, torch.cuda.current_stream()):
+        fn(*args)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    for k in fast:
+        assert torch.equal(fast[k], slow[k]) and torch.equal(fast[k], handle[k]), k

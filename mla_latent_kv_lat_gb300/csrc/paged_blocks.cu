@@ -271,9 +271,11 @@ __global__ void __launch_bounds__(kWarps == 1 ? 32 * kSingles : 32 * kWarps, kWa
         for (int k = 0; k < kClose; ++k) n += close[k] >= y;
         return static_cast<int>(__reduce_add_sync(0xffffffffu, n));
       };
-      // all keys left share the bits above `bits`
+      // All keys left share the bits above `bits`.  Where they are just the R to take there
+      // is nothing to search, and x is the least of them: those bits may all be 0, which
+      // the slots behind `left` hold.
       const int bits = 32 - __clz(top ^ least);
-      uint32_t x = bits < 32 ? top >> bits << bits : 0u;
+      uint32_t x = left == c.R ? least : bits < 32 ? top >> bits << bits : 0u;
       int n_x = left;                      // keys >= x
       for (int bit = bits - 1; bit >= 0 && n_x != c.R; --bit) {
         const uint32_t y = x | (1u << bit);

@@ -333,6 +333,71 @@ def test_select_blocks_reports_tokens_without_scores():
     assert counts[0] == 4 and blocks[0, 0] == 0 and blocks[0, 3] == 9
 
 
+def scores_of_kind(rng, kind, W, own, best):
+    """A row of W scores for a token whose own block is ``own``; in runs, ``best`` neighbours before it stand out."""
+    x = rng.standard_normal(W).astype(np.float32)
+    if kind == "ties":
+        x = np.round(2 * x)
+    elif kind == "special":
+        x[rng.random(W) < 0.3] = -np.inf
+        x[rng.random(W) < 0.02] = np.inf
+        x[rng.random(W) < 0.3] = np.nan
+    elif kind == "rising":                               # of either sign
+        x = np.linspace(-1, 1, W, dtype=np.float32)
+    elif kind == "falling":
+        x = np.linspace(-1, -5, W, dtype=np.float32)
+    elif kind in ("run", "passage"):                     # neighbours around 0 or -2 above the rest
+        n = min(best, own)
+        at = int(rng.integers(0, own - n + 1))
+        x = x - 20
+        x[at:at + n] = (0 if kind == "run" else -2) + rng.standard_normal(n)
+    elif kind == "same":
+        x[:] = -0.0 if rng.random() < 0.5 else 3.0
+    return x
+
+
+@pytest.mark.parametrize("R", [1, 29, 31, 32, 33, 61, 63, 64, 65, 300])
+@pytest.mark.parametrize("longest", [700, 1024, 1025, 2048])
+def test_select_blocks_of_many_tokens(R, longest):
+    """More tokens than a block of threads each is taken for: rows of each kind, long ones and such that have a few more
+    candidates than are taken; nothing else is written."""
+    kinds = ["random", "ties", "special", "rising", "falling", "run", "passage", "same"]
+    n_sink, n_local = 1, 2
+    K, many = R + n_sink + n_local, 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    # own blocks up to the row's last, around R candidates, and the first ones
+    news, lens = [many // 2, 0, many // 2, 64 * 4 + 9, 70], [64 * longest, 0, 64 * (longest * 3 // 4) + 5, 64 * (R + 5) + 1, 70]
+    lens = [min(n, 64 * longest) for n in lens]
+    cu, pad = np.concatenate([[0], np.cumsum(news)]), 3
+    T, W, rng = sum(news) + pad, longest, np.random.default_rng(41)
+    assert T > many
+    pos = np.concatenate([np.arange(l - n, l) for n, l in zip(news, lens)])
+    x = np.full((T, W + 5), 1e30, np.float32)
+    for t, p in enumerate(pos):
+        x[t, :W] = scores_of_kind(rng, kinds[t % len(kinds)], W, int(p) // 64, (32, 64, R)[t // len(kinds) % 3])
+    around = 4096
+    flat = torch.full((T * K + 2 * around,), -7, dtype=torch.int32, device="cuda")
+    cflat = torch.full((T + 2 * around,), -7, dtype=torch.int32, device="cuda")
+    blocks, counts = flat[around:-around].view(T, K), cflat[around:-around]
+    mla.mla_paged_select_blocks(torch.from_numpy(x).cuda()[:, :W], i32(cu), i32(lens), blocks, counts, n_sink=n_sink,
+                                n_local=n_local)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    for f in (flat, cflat):
+        assert (f[:around] == -7).all() and (f[-around:] == -7).all()
+    blocks, counts = blocks.cpu().numpy(), counts.cpu().numpy()
+    assert (blocks[len(pos):] == -7).all() and (counts[len(pos):] == -7).all()
+    for t, p in enumerate(pos):
+        own = int(p) // 64
+        forced = [j for j in range(own + 1) if j < n_sink or j > own - n_local]
+        rest = np.arange(n_sink, max(n_sink, own - n_local + 1))
+        rest = rest[np.argsort(-x[t, rest], kind="stable")]          # (NaN comes last)
+        want = np.sort(np.concatenate([forced, rest[:K - len(forced)]])).astype(np.int32)
+        if t % 97 == 0:
+            assert np.array_equal(want, BO.select(x[t, :W], int(p), K, n_sink, n_local))
+        assert counts[t] == len(want), t
+        assert np.array_equal(blocks[t, :len(want)], want) and (blocks[t, len(want):] == -1).all(), (t, kinds[t % len(kinds)])
+
+
 # ---------------------------------------------------------------------------
 # attention over listed blocks
 # ---------------------------------------------------------------------------

@@ -183,6 +183,48 @@ def test_norm_append_reports_what_rows_cannot_hold_and_bad_pages():
     assert same.all()                                     # (sequence 1's row is what it was: the same values again)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H,per,q_norm", [(16, 3, True), (80, 3, True), (80, 2, False), (128, 8, True)])
+def test_norm_append_of_many_tokens(e4m3, H, per, q_norm):
+    """Enough tokens that a warp takes ``per`` groups of four heads (and the last one of a token what is left): the bits
+    of calls with few tokens, each token's in a sample near the definition."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = -(-per * 64 * sms * 4 // H)
+    news = [n // 2, 3, n - n // 2]
+    b = Batch(42, e4m3, 16, 64, news, [n // 2, 700, n + 100], pad=1)
+    n, g = int(b.cu[-1]), torch.Generator(device="cuda").manual_seed(42)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, kv = (rnd(b.T, H, 192) * torch.exp(2 * rnd(b.T, H, 1))).bfloat16(), (rnd(b.T, 576) * torch.exp(2 * rnd(b.T, 1))).bfloat16()
+    qw, kw = (1 + 0.3 * rnd(192)).bfloat16() if q_norm else None, (1 + 0.3 * rnd(512)).bfloat16()
+    table = full_table(b)
+
+    def go(q, kv, pages, cu, lens):
+        outs = [torch.full((len(q), H, d), 7.0, dtype=torch.bfloat16, device="cuda") for d in (128, 64)]
+        mla.mla_paged_norm_append(q, kv, qw, kw, pages, table, i32(cu), i32(lens), *outs, eps=EPS, freq_base=FB, freq_scale=FS)
+        torch.cuda.synchronize()
+        assert mla.mla_get_device_error() == 0
+        return outs
+
+    pages = [b.pages_dev().view(torch.uint8).fill_(0).view(torch.uint8 if e4m3 else torch.float16) for _ in range(2)]
+    nope, pe = go(q, kv, pages[0], b.cu, b.lens)
+    assert (nope[n:] == 7).all() and (pe[n:] == 7).all()
+    few = 32 * sms // H                                   # half of what makes a warp take one group more
+    for lo in range(0, n, few):
+        hi = min(lo + few, n)
+        part = np.clip(b.cu, lo, hi)
+        lens = [l - n_new + int(np.clip(hi - c, 0, n_new)) for l, n_new, c in zip(b.lens, b.news, b.cu)]
+        x, y = go(q[lo:hi], kv[lo:hi], pages[1], part - lo, lens)
+        assert torch.equal(x, nope[lo:hi]) and torch.equal(y, pe[lo:hi]), lo
+    assert torch.equal(pages[0].view(torch.uint8), pages[1].view(torch.uint8))
+    some = np.unique(np.concatenate([np.arange(0, n, 41), [n - 1]]))
+    pos, at = positions(b)[some], torch.from_numpy(some).cuda()
+    rel = rel_norm(192) if q_norm else 0.0
+    x = BO.rms(host(q[at]), host(qw) if q_norm else None, EPS)
+    assert (np.abs(host(nope[at]) - x[..., :128]) <= (2.0 ** -8 + 2 * rel) * np.abs(x[..., :128])).all()
+    for h in range(H):
+        check_rotated(host(pe[at, h]), x[:, h, 128:], pos, 2.0 ** -8, 2 * rel)
+
+
 # ---------------------------------------------------------------------------
 # mean rows
 # ---------------------------------------------------------------------------
@@ -203,6 +245,44 @@ def test_block_keys(e4m3, ps, news, lens, pad):
     torch.cuda.synchronize()
     assert mla.mla_get_device_error() == 0
     assert (np.abs(host(keys).reshape(want.shape) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_block_keys_of_more_blocks_than_the_grid(e4m3):
+    """More completed blocks than blocks of threads, 16 an SM, so that these take several."""
+    ps, sms = 128, torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator(device="cuda").manual_seed(43)
+    news, lens = [64 * 25 * sms + 10, 0, 64 * 17 * sms, 1], [64 * 25 * sms + 10, 500, 64 * 17 * sms + 700, 640]
+    width = -(-max(lens) // ps)
+    n_pages = sum(-(-l // ps) for l in lens) + 1
+    order, table, at = np.random.default_rng(43).permutation(n_pages), np.full((4, width), -1, np.int32), 0
+    for s, l in enumerate(lens):
+        table[s, :-(-l // ps)] = order[at:at + -(-l // ps)]
+        at += -(-l // ps)
+    table, pages = i32(table), mla.paged_pages(n_pages, ps, e4m3)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    c_kv, k_pe = (torch.randn(int(cu[-1]), d, generator=g, device="cuda").bfloat16() for d in (512, 64))
+    mla.mla_paged_append(c_kv, k_pe, pages, table, i32(cu), i32(lens))
+    rows = torch.empty(int(cu[-1]), 576, dtype=torch.float16, device="cuda")
+    mla.mla_paged_gather(pages, table, None, i32(cu), rows)           # (exact)
+    keys = torch.full((n_pages, ps // 64, 576), 7.0, dtype=torch.float16, device="cuda")
+    new = np.concatenate([[0], np.cumsum(news)])
+    assert int(new[-1]) // 64 + 4 > 2 * 16 * sms
+    mla.mla_paged_block_keys(pages, table, i32(new), i32(lens), keys, int(new[-1]))
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0
+    flat, left = keys.view(-1, 576), torch.ones(n_pages * ps // 64, dtype=torch.bool, device="cuda")
+    for s, l in enumerate(lens):
+        lo, hi = (l - news[s]) // 64, l // 64
+        if lo >= hi:
+            continue
+        x = rows[int(cu[s]) + 64 * lo:int(cu[s]) + 64 * hi].double().view(-1, 64, 576)
+        j = torch.arange(lo, hi, device="cuda")
+        slot = table[s, j * 64 // ps].long() * (ps // 64) + j % (ps // 64)
+        tol = 64 * 2.0 ** -24 * x.abs().mean(1) + 2.0 ** -11 * x.mean(1).abs() + 2.0 ** -25     # as above
+        assert ((flat[slot].double() - x.mean(1)).abs() <= tol).all()
+        left[slot] = False
+    assert (flat[left] == 7).all() and int(left.sum()) > 0
 
 
 def test_block_keys_skips_bad_pages():

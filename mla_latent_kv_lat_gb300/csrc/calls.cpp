@@ -6,7 +6,9 @@
 // Each function takes the arguments of the binding's function of that name, in order,
 // checks what that function checks, and returns the C call's status; or None for
 // anything that is not plainly right (a wrong type, shape or device, another current
-// device): the binding then takes its own way, which says what is wrong.
+// device): the binding then takes its own way, which says what is wrong.  The C call
+// itself is made without the interpreter's lock, as ctypes makes it: a launch waits
+// where the queue is full, maybe for a host function that needs the lock.
 #include <Python.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -123,6 +125,15 @@ mla_paged_cache paged(PyObject* pages, PyObject* block_table, int dev, int32_t& 
   return c;
 }
 
+// f(args...) without the interpreter's lock; the arguments are made with it.
+template <typename F, typename... Args>
+int unlocked(F f, Args... args) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int status = f(args...);       // (a C entry: it throws nothing)
+  PyEval_RestoreThread(state);
+  return status;
+}
+
 template <typename Call>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, Call call) {
   try {
@@ -146,7 +157,7 @@ PyObject* norm_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t B;
     const mla_paged_cache c = paged(a[4], a[5], dev, B);
     // (the stride of a dimension of one counts for nothing, and may be anything)
-    return lib.norm_append(&d, q.data_ptr(), T > 1 ? q.stride(0) : 0, H > 1 ? q.stride(1) : 0, kv.data_ptr(),
+    return unlocked(lib.norm_append, &d, q.data_ptr(), T > 1 ? q.stride(0) : 0, H > 1 ? q.stride(1) : 0, kv.data_ptr(),
                            T > 1 ? kv.stride(0) : 0,
                            a[2] == Py_None ? nullptr : contiguous(a[2], at::kBFloat16, {kNope + kRope}, dev),
                            contiguous(a[3], at::kBFloat16, {kLatent}, dev), &c, i32(a[6], {int64_t{B} + 1}, dev),
@@ -165,7 +176,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t T = kv.size(0);
     int32_t B;
     const mla_paged_cache c = paged(a[2], a[3], dev, B);
-    return lib.append(&c, contiguous(a[0], at::kBFloat16, {T, kLatent}, dev), contiguous(a[1], at::kBFloat16, {T, kRope}, dev),
+    return unlocked(lib.append, &c, contiguous(a[0], at::kBFloat16, {T, kLatent}, dev), contiguous(a[1], at::kBFloat16, {T, kRope}, dev),
                       i32(a[4], {int64_t{B} + 1}, dev), i32(a[5], {B}, dev), B, fit(T), number(a[6]), number(a[7]),
                       stream(a[8], dev));
   });
@@ -181,7 +192,7 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t R = out.size(0);
     int32_t B;
     const mla_paged_cache c = paged(a[0], a[1], dev, B);
-    return lib.gather(&c, a[2] == Py_None ? nullptr : i32(a[2], {B}, dev), i32(a[3], {int64_t{B} + 1}, dev), B, fit(R),
+    return unlocked(lib.gather, &c, a[2] == Py_None ? nullptr : i32(a[2], {B}, dev), i32(a[3], {int64_t{B} + 1}, dev), B, fit(R),
                       contiguous(a[4], f16 ? at::kHalf : at::kBFloat16, {R, kRow}, dev), f16, stream(a[5], dev));
   });
 }
@@ -192,7 +203,7 @@ PyObject* block_keys(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dev = device_of(tensor(a[0]));
     int32_t B;
     const mla_paged_cache c = paged(a[0], a[1], dev, B);
-    return lib.block_keys(&c, i32(a[2], {int64_t{B} + 1}, dev), i32(a[3], {B}, dev), B, integer(a[5]),
+    return unlocked(lib.block_keys, &c, i32(a[2], {int64_t{B} + 1}, dev), i32(a[3], {B}, dev), B, integer(a[5]),
                           contiguous(a[4], at::kHalf, {c.n_pages, c.page_size / kBlock, kRow}, dev), stream(a[6], dev));
   });
 }
@@ -231,7 +242,7 @@ PyObject* block_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t B;
     table(c, a[3], q.dev, B);
     const Rows s(a[6], q.T, q.dev);
-    return lib.block_scores(&d, q.t.data_ptr(), contiguous(a[1], at::kBFloat16, {q.T, q.H, kRope}, q.dev), &c, k,
+    return unlocked(lib.block_scores, &d, q.t.data_ptr(), contiguous(a[1], at::kBFloat16, {q.T, q.H, kRope}, q.dev), &c, k,
                             i32(a[4], {int64_t{B} + 1}, q.dev), i32(a[5], {B}, q.dev), B, fit(q.T), s.data(), s.t.stride(0),
                             fit(s.t.size(1)), stream(a[8], q.dev));
   });
@@ -245,7 +256,7 @@ PyObject* select_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(blocks.dim() == 2 && len.dim() == 1);
     const int64_t T = blocks.size(0), K = blocks.size(1), B = len.size(0);
     const Rows s(a[0], T, dev);
-    return lib.select_blocks(s.data(), s.t.stride(0), fit(s.t.size(1)), i32(a[1], {B + 1}, dev), i32(a[2], {B}, dev), fit(B),
+    return unlocked(lib.select_blocks, s.data(), s.t.stride(0), fit(s.t.size(1)), i32(a[1], {B + 1}, dev), i32(a[2], {B}, dev), fit(B),
                              fit(T), integer(a[5]), integer(a[6]), const_cast<int32_t*>(i32(a[3], {T, K}, dev)),
                              const_cast<int32_t*>(i32(a[4], {T}, dev)), fit(K), stream(a[7], dev));
   });
@@ -260,7 +271,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const mla_paged_cache c = paged(a[2], a[3], q.dev, B);
     const at::Tensor& ws = tensor(a[9]);
     need(ws.scalar_type() == at::kByte && ws.is_cuda() && ws.get_device() == q.dev && ws.is_contiguous());
-    return lib.attn(&d, q.t.data_ptr(), contiguous(a[1], at::kBFloat16, {q.T, q.H, kRope}, q.dev), &c,
+    return unlocked(lib.attn, &d, q.t.data_ptr(), contiguous(a[1], at::kBFloat16, {q.T, q.H, kRope}, q.dev), &c,
                     i32(a[4], {int64_t{B} + 1}, q.dev), i32(a[5], {B}, q.dev), B, fit(q.T), integer(a[7]), integer(a[8]),
                     ws.data_ptr(), static_cast<size_t>(ws.numel()), contiguous(a[6], at::kHalf, {q.T, q.H, kLatent}, q.dev),
                     stream(a[11], q.dev));
@@ -278,7 +289,7 @@ PyObject* attn_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(blocks.dim() == 2 && blocks.size(0) == q.T);
     need(ws.scalar_type() == at::kByte && ws.is_cuda() && ws.get_device() == q.dev && ws.is_contiguous());
     const int64_t K = blocks.size(1);
-    return lib.attn_blocks(&d, q.t.data_ptr(), contiguous(a[1], at::kBFloat16, {q.T, q.H, kRope}, q.dev), &c,
+    return unlocked(lib.attn_blocks, &d, q.t.data_ptr(), contiguous(a[1], at::kBFloat16, {q.T, q.H, kRope}, q.dev), &c,
                            i32(a[4], {int64_t{B} + 1}, q.dev), i32(a[5], {B}, q.dev), B, fit(q.T), i32(a[6], {q.T, K}, q.dev),
                            i32(a[7], {q.T}, q.dev), fit(K), ws.data_ptr(), static_cast<size_t>(ws.numel()),
                            contiguous(a[8], at::kHalf, {q.T, q.H, kLatent}, q.dev), stream(a[11], q.dev));

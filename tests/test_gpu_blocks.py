@@ -972,3 +972,34 @@ def test_the_compiled_way_and_the_way_through_python_agree(monkeypatch):
     assert mla.mla_get_device_error() == 0
     for k in fast:
         assert torch.equal(fast[k], slow[k]) and torch.equal(fast[k], handle[k]), k
+
+
+def test_the_compiled_way_calls_the_library_without_the_interpreters_lock(tmp_path):
+    """A stand-in for the library says whether its caller holds the lock (1) or not (0)."""
+    import subprocess
+    from mla_latent_kv_lat_gb300 import binding as B
+    names = ("mla_paged_append", "mla_paged_gather", "mla_attn_paged", "mla_paged_norm_append", "mla_paged_block_keys",
+             "mla_paged_block_scores", "mla_paged_select_blocks", "mla_attn_paged_blocks")
+    src, lib = tmp_path / "stub.c", tmp_path / "stub.so"
+    src.write_text("int PyGILState_Check(void);\n" + "".join(f"int {n}() {{ return PyGILState_Check(); }}\n" for n in names))
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(lib), str(src)], check=True)
+    H, T, bf, f16, i4 = 16, 2, torch.bfloat16, torch.float16, torch.int32
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    pages, table, cu, ln = z(3, 64, 576, dt=f16), z(1, 2, dt=i4), z(2, dt=i4), z(1, dt=i4)
+    q_lat, q_pe, keys, scores = z(T, H, 512, dt=f16), z(T, H, 64), z(3, 1, 576, dt=f16), z(T, 5, dt=torch.float32)
+    blocks, counts, ws = z(T, 3, dt=i4), z(T, dt=i4), z(64, dt=torch.uint8)
+    fast = B._fast()
+    fast.bind(str(lib))
+    try:
+        got = [fast.append(z(T, 512), q_pe[:, 0].contiguous(), pages, table, cu, ln, 1e4, 0.025, None),
+               fast.gather(pages, table, None, cu, z(T, 576), None),
+               fast.attn(q_lat, q_pe, pages, table, cu, ln, q_lat.clone(), 0, 0, ws, None, None),
+               fast.norm_append(z(T, H, 192), z(T, 576), None, z(512), pages, table, cu, ln, z(T, H, 128), q_pe, 1e-6, 1e4, 0.025,
+                                None),
+               fast.block_keys(pages, table, cu, ln, keys, T, None),
+               fast.block_scores(q_lat, q_pe, keys, table, cu, ln, scores, None, None),
+               fast.select_blocks(scores, cu, ln, blocks, counts, 1, 1, None),
+               fast.attn_blocks(q_lat, q_pe, pages, table, cu, ln, blocks, counts, q_lat.clone(), ws, None, None)]
+    finally:
+        fast.bind(B._build.LIB)
+    assert got == [0] * len(names)

@@ -407,10 +407,10 @@ int mla_paged_gather(const mla_paged_cache* cache, const int32_t* row0, const in
 
 /* Bytes of device workspace mla_attn_paged and mla_attn_paged_blocks need on
  * the current device: the partial results of work split over the keys (40 MB on
- * GB300), room for 131072 rows of an e4m3 cache as fp16 (134 MB): a sequence
- * with a chunk of new tokens has its visible rows converted there once, and for
- * the lists that tokens of a chunk share (21 MB).  Depends on neither the
- * batch nor the lengths.  Returns 0 for invalid dims.                         */
+ * GB300), and room for 131072 rows of an e4m3 cache as fp16 (134 MB): a sequence
+ * with a chunk of new tokens has its visible rows converted there once.  (Lists
+ * that tokens of a chunk share lie at its end, in 21 MB at most.)  Depends on
+ * neither the batch nor the lengths.  Returns 0 for invalid dims.             */
 size_t mla_paged_workspace_size(const mla_dims* dims);
 
 /* Attention of the batch's new tokens over their pages (steps 2-4 of the

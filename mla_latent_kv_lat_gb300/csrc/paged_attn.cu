@@ -177,7 +177,7 @@ constexpr int kStageRows = 131072, kStageSeqs = 1024, kStageBlocks = 16, kStageR
 
 // The lists of blocks that a launch goes by.
 enum Lists { kNoLists, kTokenLists, kGroupLists };
-// Of tokens in groups: room for as many entries.
+// Of tokens in groups: as many entries at most (with their numbers 21 of the staging's 134 MB).
 constexpr int64_t kGroupEntries = int64_t{1} << 21;
 
 // Which sequences a launch takes.
@@ -190,12 +190,14 @@ struct TcArgs {
   float* ws_ml;       // fp32 [2 G][128][2] running maximum (log2 units, less kPShift) and sum
   Rec* rec;           // [G]
   int32_t* stage_base;   // [B] a sequence's first staged row, -1: not staged (unless take is kTakeAll)
-  uint16_t* stage;       // fp16 [kStageRows][512]
+  uint16_t* stage;       // fp16 [stage_rows][512]
+  int32_t stage_rows;    // kStageRows, less the room at their end that groups' lists take
   int32_t stage_blocks;  // of threads that stage
   int32_t n_slots;
   int32_t n_rows;     // rows of the page pool
   // kGroupLists: 2^gt_shift tokens share a block; a slot's entries (the tiles that some
-  // token of it lists: first key, tokens), 2^gt_shift K apart, and their number
+  // token of it lists: first key, tokens), 2^gt_shift K apart, and their number; behind
+  // the staged rows
   int32_t gt_shift;
   uint2* group_lists;
   int32_t* group_counts;
@@ -1751,7 +1753,7 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
         int32_t sink;
         const int32_t first = seq_first_tile(a.p, s.len - s.n, sink);
         const int64_t r = static_cast<int64_t>(sink + (s.len + kBK - 1) / kBK - first) * kBK;
-        rows[q] = static_cast<int32_t>(min(r, static_cast<int64_t>(kStageRows + 1)));
+        rows[q] = static_cast<int32_t>(min(r, static_cast<int64_t>(a.stage_rows + 1)));
       }
     }
     sum += rows[q];
@@ -1774,9 +1776,9 @@ __global__ void __launch_bounds__(256, 4) paged_stage_kernel(const TcArgs a) {
     const long long base = end;
     end += rows[q];
     s_end[b] = static_cast<int32_t>(min(end, static_cast<long long>(INT32_MAX)));
-    if (end <= kStageRows) atomicMax(&s_total, static_cast<int32_t>(end));
+    if (end <= a.stage_rows) atomicMax(&s_total, static_cast<int32_t>(end));
     if (blockIdx.x == 0 && b < a.p.B)
-      a.stage_base[b] = rows[q] > 0 && end <= kStageRows ? static_cast<int32_t>(base) : -1;
+      a.stage_base[b] = rows[q] > 0 && end <= a.stage_rows ? static_cast<int32_t>(base) : -1;
   }
   __syncthreads();
   const int32_t total = s_total;
@@ -1906,12 +1908,10 @@ int64_t group_slots(const PagedAttnArgs& p, int32_t& shift) {
   return 0;
 }
 
-size_t stage_bytes() { return kStageSeqs * sizeof(int32_t) + static_cast<size_t>(kStageRows) * kLatent * 2; }
-
 }  // namespace
 
 size_t paged_attn_workspace_bytes() {
-  return partial_bytes() + stage_bytes() + kGroupEntries * sizeof(uint2) + kGroupEntries / 2 * sizeof(int32_t);
+  return partial_bytes() + kStageSeqs * sizeof(int32_t) + static_cast<size_t>(kStageRows) * kLatent * 2;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
@@ -1927,9 +1927,14 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
   a.n_slots = p.blocks != nullptr ? p.T : static_cast<int32_t>(static_cast<int64_t>(p.T) * p.H / kRows + p.B);
   a.n_rows = p.c.n_pages << p.c.page_shift;
   const int64_t groups = group_slots(p, a.gt_shift);
+  a.stage_rows = kStageRows;
   if (groups > 0) {
-    a.group_lists = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.workspace) + partial_bytes() + stage_bytes());
-    a.group_counts = reinterpret_cast<int32_t*>(a.group_lists + kGroupEntries);
+    // Lists lie at the end of the staging's room, in as many (whole tiles of) rows as they need.
+    const int64_t entries = (groups << a.gt_shift) * p.K;
+    const int64_t bytes = entries * sizeof(uint2) + groups * sizeof(int32_t), tile = int64_t{kBK} * kLatent * 2;
+    a.stage_rows -= static_cast<int32_t>((bytes + tile - 1) / tile * kBK);
+    a.group_lists = reinterpret_cast<uint2*>(a.stage + static_cast<int64_t>(a.stage_rows) * kLatent);
+    a.group_counts = reinterpret_cast<int32_t*>(a.group_lists + entries);
     a.n_slots = static_cast<int32_t>(groups);
   }
   // The latents of fp16 pages or of staged rows, in groups of eight rows; the
@@ -1974,7 +1979,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& p, cudaStream_t stream) {
       (p.blocks != nullptr ? static_cast<int64_t>(p.T >> max(0, a.gt_shift - 1)) * p.K >= 64 * G
                            : static_cast<int64_t>(p.T) * p.H > (kStageBlocks - 1) * kRows)) {
     a.stage_base = stage_base;
-    e = make_tmap_row_groups(&tm, a.stage, kStageRows / 8, kLatent / 64, kLatent * 2, kBK / 8, 4);
+    e = make_tmap_row_groups(&tm, a.stage, static_cast<uint64_t>(a.stage_rows) / 8, kLatent / 64, kLatent * 2, kBK / 8, 4);
     if (e != cudaSuccess) return e;
     a.stage_blocks = device_sm_count() * 4;
     e = launch_dependent(groups > 0 ? paged_stage_kernel<true> : paged_stage_kernel<false>,

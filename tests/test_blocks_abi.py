@@ -63,6 +63,13 @@ def test_good_arguments_pass_the_checks(lib):
     assert calls(lib, T=1)["scores"][1](ss=0) == NO_DEVICE
 
 
+def test_lists_need_no_workspace_of_their_own(lib):
+    """Partials and records of each pair of SMs, and the staging with its table: what attention over whole contexts
+    needs.  A buffer of that size serves both calls."""
+    partials = lib.mla_paged_workspace_size(dims()) - (131072 * 1024 + 4096)
+    assert partials > 0 and partials % (2 * 128 * (512 + 2) * 4 + 32) == 0
+
+
 def test_bad_caches_are_refused(lib):
     for kw, want in BAD_CACHES + [(dict(page_size=32), -2), (dict(page_size=16), -2)]:
         for name, (_, call) in calls(lib).items():

@@ -664,6 +664,51 @@ def test_e4m3_chunks_converted_beforehand_or_not(H, lens):
     check(b, attend(b))
 
 
+@pytest.mark.parametrize("H,K,news,lens", [
+    (16, 256, [300, 300], [60000, 69500]),       # both converted, with a few tiles' room behind them for the lists
+    (16, 256, [300, 300], [60000, 71000]),       # the second one's rows and the lists do not fit
+    (64, 1024, [900, 120], [100000, 22700]), (64, 1024, [900, 120], [100000, 31000])], ids=str)
+def test_converted_rows_and_lists_share_the_workspace(H, K, news, lens):
+    """Pages that stand in for many of a context's; the room for converted rows full to the lists that lie behind them."""
+    rng, ps = np.random.default_rng(44), 4096
+    lat, rope = bf16(rng.standard_normal((2 * ps, 512))), bf16(rng.standard_normal((2 * ps, 64)))
+    raw = PO.pack_rows(lat, rope, True)
+    rows, T = PO.row_values(raw, True), sum(news)
+    table = rng.integers(0, 2, (2, -(-max(lens) // ps))).astype(np.int32)
+    cu = np.concatenate([[0], np.cumsum(news)])
+    g = torch.Generator(device="cuda").manual_seed(44)
+    q_lat = torch.randn(T, H, 512, generator=g, device="cuda").half()
+    q_pe = torch.randn(T, H, 64, generator=g, device="cuda").bfloat16()
+    blocks, counts = np.full((T, K), -1, np.int32), rng.integers(0, 6, T).astype(np.int32)
+    pos = np.concatenate([np.arange(l - n, l) for n, l in zip(news, lens)])
+    for t, p in enumerate(pos):
+        own = int(p) // 64
+        near = np.clip([own, own - 1 - t % 3, t % 7, own // 2, own // 3 + t % 2], 0, own)
+        blocks[t, :counts[t]] = near[:counts[t]]
+    out = torch.full((T, H, 512), float("nan"), dtype=torch.float16, device="cuda")
+    ws = torch.randint(0, 256, (mla.mla_paged_workspace_size(H) + 4096,), dtype=torch.uint8, device="cuda")
+    behind = ws[-4096:].clone()
+    mla.mla_attn_paged_blocks(q_lat, q_pe, torch.from_numpy(raw).cuda().view(2, ps, -1), i32(table), i32(cu), i32(lens),
+                              i32(blocks), i32(counts), out, workspace=ws[:-4096], scale=SCALE)
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0 and torch.equal(ws[-4096:], behind)
+    assert out.isfinite().all()
+    for t in range(0, T, 13):
+        lst, s, p = blocks[t, :counts[t]], int(t >= cu[1]), int(pos[t])
+        q = np.concatenate([host(q_lat[t]), host(q_pe[t])], -1)
+        if not len(lst):
+            assert (out[t] == 0).all()
+            continue
+        keys = np.concatenate([np.arange(64 * j, min(64 * j + 64, p + 1)) for j in lst])
+        r = rows[table[s, keys // ps] * ps + keys % ps]
+        x = SCALE * (q @ r.T)
+        w = np.exp(x - x.max(-1, keepdims=True))
+        w /= w.sum(-1, keepdims=True)
+        want, a = w @ r[:, :512], w @ np.abs(r[:, :512])
+        tol = (2.0 ** -11 + 2.0 ** -12) * a + 2.0 ** -11 * np.abs(want) + 2.0 ** -24 + 2.0 ** -25 * len(keys) * np.abs(r).max()
+        assert (np.abs(host(out[t]) - want) <= tol).all(), t
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("H,n", [(16, 40), (64, 40), (128, 3), (16, 600)])
 def test_decreasing_offsets_are_reported(e4m3, H, n):

@@ -1,5 +1,6 @@
 """Build libmla.so in-tree from csrc/*.cu with nvcc for sm_103a (GB300), and beside it the module that
-takes the paged calls from Python to it (csrc/calls.cpp, against the installed PyTorch).
+takes the paged calls from Python to it (csrc/calls.cpp, against the installed PyTorch; without g++ or a PyTorch with
+CUDA it is left out, and the binding makes these calls by itself).
 
 Usage: ``python -m mla_latent_kv_lat_gb300.build [--force]``.  Translation
 units compile in parallel; the library links against the shared CUDA runtime
@@ -41,8 +42,16 @@ def calls_path() -> str:
     return os.path.join(PKG, f"_calls_{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
+def _torch_root() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def can_build_calls() -> bool:
+    return shutil.which("g++") is not None and os.path.exists(os.path.join(_torch_root(), "lib", "libc10_cuda.so"))
+
+
 def _build_calls() -> str:
-    root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    root = _torch_root()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     out = calls_path()
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -68,9 +77,10 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(calls_path()):
+    made = [LIB] + ([calls_path()] if can_build_calls() else [])
+    if not all(os.path.exists(p) for p in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(calls_path()))
+    t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(p) <= t for p in _deps() + [os.path.abspath(__file__)])
 
 
@@ -89,9 +99,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        calls = ex.submit(_build_calls)
+        calls = ex.submit(_build_calls) if can_build_calls() else None
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        calls.result()
+        if calls is not None:
+            calls.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "shared"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,5 +1,6 @@
 """Refusals of the normed append and of the calls with blocks, on the host (no GPU needed), and their oracle."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -295,6 +296,40 @@ def test_the_compiled_way_leaves_what_is_not_plainly_right_to_the_binding(lib):
     for f, n in ((fast.append, 9), (fast.gather, 6), (fast.attn, 12), (fast.norm_append, 14), (fast.block_keys, 7), (fast.block_scores, 9), (fast.select_blocks, 8), (fast.attn_blocks, 12)):
         assert f(*[cpu] * n) is None and f(*[None] * n) is None and f(*[3.5] * n) is None and f() is None
         assert f(*[cpu] * (n + 1)) is None
+
+
+def test_without_the_compiled_module_the_calls_go_through_python(monkeypatch, device1, tmp_path):
+    monkeypatch.setattr(binding, "_calls", None)
+    monkeypatch.setattr(build, "calls_path", lambda: str(tmp_path / "_calls_of_another.so"))
+    with pytest.warns(UserWarning, match="_calls_of_another"):
+        binding._fast()
+    for name, (fn, kw) in good().items():
+        fn(**kw)
+        assert device1.pop() == fn.__name__, name
+
+
+def test_the_library_is_built_without_the_module_where_that_cannot_be(monkeypatch, tmp_path):
+    def calls():
+        raise AssertionError("no compiler")
+
+    made = []
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libmla.so"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "calls_path", lambda: str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build, "_build_calls", calls)
+    monkeypatch.setattr(build, "_compile", lambda src, extra: made.append(src) or src)
+    def link(cmd, **kw):
+        open(build.LIB + ".tmp", "w").close()
+        return types.SimpleNamespace(returncode=0)
+
+    monkeypatch.setattr(build.subprocess, "run", link)
+    monkeypatch.setattr(build, "can_build_calls", lambda: False)
+    assert not build.up_to_date()
+    assert build.build() == build.LIB and made and build.up_to_date()
+    monkeypatch.setattr(build, "can_build_calls", lambda: True)
+    assert not build.up_to_date()
+    with pytest.raises(AssertionError, match="no compiler"):
+        build.build()
 
 
 def test_a_step_on_another_device_runs_all_its_calls_there(monkeypatch, lib):

@@ -1048,3 +1048,77 @@ def test_the_compiled_way_calls_the_library_without_the_interpreters_lock(tmp_pa
     finally:
         fast.bind(B._build.LIB)
     assert got == [0] * len(names)
+
+
+def test_the_compiled_way_and_the_way_through_python_refuse_alike(monkeypatch):
+    """Every argument of every paged call replaced by what is not right: the same error by the same words, nothing written."""
+    from mla_latent_kv_lat_gb300 import binding as B
+    H, T, bf, f16, i4, f32, u8 = 16, 2, torch.bfloat16, torch.float16, torch.int32, torch.float32, torch.uint8
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    cache = dict(pages=z(3, 64, 576, dt=f16), block_table=z(1, 2, dt=i4))
+    batch = dict(cu_q=z(2, dt=i4), seq_len=z(1, dt=i4))
+    new = dict(cu_new=z(2, dt=i4), seq_len=z(1, dt=i4))
+    q = dict(q_lat=z(T, H, 512, dt=f16), q_pe=z(T, H, 64))
+    ws = z(mla.mla_paged_workspace_size(H), dt=u8)
+    calls = [
+        (mla.mla_paged_append, dict(c_kv=z(T, 512), k_pe=z(T, 64), **cache, **new, freq_base=1e4, freq_scale=0.025)),
+        (mla.mla_paged_gather, dict(**cache, row0=z(1, dt=i4), cu_rows=z(2, dt=i4), out=z(T, 576))),
+        (mla.mla_attn_paged, dict(**q, **cache, **batch, o_lat=z(T, H, 512, dt=f16), window=0, n_sink=0, workspace=ws)),
+        (mla.mla_paged_norm_append, dict(q=z(T, H, 192), kv=z(T, 576), q_weight=z(192), kv_weight=z(512), **cache, **new,
+                                         q_nope=z(T, H, 128), q_pe=z(T, H, 64), eps=1e-6, freq_base=1e4, freq_scale=0.025)),
+        (mla.mla_paged_block_keys, dict(**cache, **new, block_keys=z(3, 1, 576, dt=f16), T=T)),
+        (mla.mla_paged_block_scores, dict(**q, block_keys=z(3, 1, 576, dt=f16), block_table=cache["block_table"], **batch,
+                                          scores=z(T, 5, dt=f32), scale=SCALE)),
+        (mla.mla_paged_select_blocks, dict(scores=z(T, 5, dt=f32), **batch, blocks=z(T, 3, dt=i4), counts=z(T, dt=i4), n_sink=1,
+                                           n_local=1)),
+        (mla.mla_attn_paged_blocks, dict(**q, **cache, **batch, blocks=z(T, 3, dt=i4), counts=z(T, dt=i4),
+                                         o_lat=z(T, H, 512, dt=f16), workspace=ws, scale=SCALE))]
+
+    def wrong(name, t):
+        if isinstance(t, torch.Tensor):
+            other = f32 if t.dtype is not f32 else f16
+            yield "type", t.to(other)
+            yield "place", t.cpu()
+            yield "none", 3.5
+            if t is ws:
+                yield "small", t[:4096]
+                yield "odd", t[8:]
+                return
+            yield "more", torch.cat([t, t]) if t.dim() == 1 else torch.cat([t, t], -1)
+            yield "flat", t.flatten() if t.dim() > 1 else t[None]
+            if t.dim() > 1 and t.size(-1) > 1:
+                yield "gaps", torch.cat([t, t], -1)[..., ::2]
+            flat = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+            if t.dtype in (bf, f16):
+                yield "odd", flat[1:].view(t.shape)
+        elif name in ("window", "n_sink", "n_local", "T"):
+            yield "negative", -1
+            yield "far", 1 << 31
+        else:                                             # eps, frequencies, scale
+            yield "zero", 0.0
+            yield "negative", -1.0
+            yield "nan", float("nan")
+            yield "words", "1.5"
+
+    def outcome(fn, kw):
+        try:
+            fn(**kw)
+        except Exception as e:  # noqa: BLE001
+            return type(e), str(e)
+        return None
+
+    fast, seen = B._fast(), 0
+    assert not isinstance(fast, B._Unbuilt)
+    for fn, kw in calls:
+        assert outcome(fn, kw) is None, fn
+        for name, t in kw.items():
+            for what, bad in wrong(name, t):
+                monkeypatch.setattr(B, "_calls", fast)
+                got = outcome(fn, dict(kw, **{name: bad}))
+                monkeypatch.setattr(B, "_calls", B._Unbuilt())
+                want = outcome(fn, dict(kw, **{name: bad}))
+                monkeypatch.setattr(B, "_calls", fast)
+                assert got == want, (fn.__name__, name, what)
+                seen += want is not None
+    torch.cuda.synchronize()
+    assert mla.mla_get_device_error() == 0 and seen > 200

@@ -368,7 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           there |= row >= 0 ? 1u << i : 0u;
         }
         // The last products of the run before have read its rows (and q_pe of all groups).
-        if (k > 0 && !dead) dead = !wait_all(&B.k_free, (k - 1) & 1, a);
+        if (k > 0 && !dead) {
+          dead = !wait_all(&B.k_free, (k - 1) & 1, a);
+          tc::fence_after_sync();          // (tensor memory that they read is written next)
+        }
         auto fetch = [&](uint8_t* to, int c) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {

@@ -405,7 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c == kChunks / 2) cp_async_wait<0>();
                 __syncwarp();
                 keep(sRing + c * kChunk, c);
-                if ((c & 1) && lane == 0) mbar_arrive(&B.k_full[1 + c / 2]);
+                if (c & 1) {
+                  tc::fence_proxy_async();       // (bulk copies of queries go where these copies went)
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&B.k_full[1 + c / 2]);
+                }
               }
             }
           } else if (!dead) {

@@ -1122,3 +1122,26 @@ def test_the_compiled_way_and_the_way_through_python_refuse_alike(monkeypatch):
                 seen += want is not None
     torch.cuda.synchronize()
     assert mla.mla_get_device_error() == 0 and seen > 200
+
+
+@pytest.mark.parametrize("n_seqs", [400, 1500])
+def test_batches_of_many_sequences(n_seqs):
+    """More sequences than a block of threads has: every call against the definition, as above."""
+    rng = np.random.default_rng(45)
+    news = rng.choice([0, 1, 1, 1, 2, 5], n_seqs)
+    lens = news + rng.integers(0, 150, n_seqs) * (rng.random(n_seqs) < 0.8)
+    lens[::97] += 900
+    news, lens = [int(x) for x in news], [int(x) for x in lens]
+    test_block_scores(16, 64, news, lens, 3, 20)
+    test_block_keys(False, 64, news, lens, 2)
+    test_norm_append(True, 16, True, False, 64, news, lens, 1)
+    for H, e4m3, K in ((16, False, 2), (128, True, 3)):
+        b = Listed(46, e4m3, H, 64, news, lens, K, "random", 1)
+        check(b, attend(b))
+    K, W = 4, 20
+    scores = rng.standard_normal((sum(news), W)).astype(np.float32)
+    blocks, counts, cu = choose(torch.from_numpy(scores).cuda(), news, lens, K, 1, 1)
+    assert mla.mla_get_device_error() == 0
+    for t, p in enumerate(np.concatenate([np.arange(l - n, l) for n, l in zip(news, lens)])):
+        want = BO.select(scores[t], int(p), K, 1, 1)
+        assert counts[t] == len(want) and np.array_equal(blocks[t, :len(want)], want)

@@ -22,10 +22,10 @@
 // A chunk is bound by the queries' way into the SMs: a group of 128 columns and a tile take
 // 147 KB and 2300 cycles of the tensor cores, and 3300 in fact, 44 bytes a cycle and SM
 // (pairs of CTAs that load half each and multicast it were no faster).  512 tokens of 128
-// heads, 520 blocks: 38 us (queries of 75 MB in L2: 33), 1020 TFLOP/s, 53% of the measured
+// heads, 520 blocks: 38 us on the GPU (queries of 75 MB in L2: 34), 1020 TFLOP/s, 53% of the measured
 // rate; 48% of the tensor cores' cycles.  A single token is bound by the chain: lengths and
 // shares 2.5k cycles, table 1.2k, rows 1.5k, products 3k, maxima and end 1.5k.  32 tokens,
-// 4K to 98K rows: 12.9 us; one of 16 heads at 20001 rows: 5.7 us.
+// 4K to 98K rows: 12.8 us; one of 16 heads at 20001 rows: 5.6 us.
 #include <atomic>
 #include <type_traits>
 

@@ -49,10 +49,10 @@
 //     list's order; lists and table are looked up 32 tiles at a time, a lane each.  With
 //     up to 64 heads the tokens of a chunk share blocks of 128 rows, whose tiles are
 //     their lists' union and whose rows see a tile if their token lists it.  32 tokens of
-//     128 heads with 32 of up to 1536 blocks: 40 us, of which the cut blocks' partials
+//     128 heads with 32 of up to 1536 blocks: 40 us on the GPU, of which the cut blocks' partials
 //     (28 MB, written and read) and the start (8.5 us to the first score product) are
-//     half; 1024 tokens of one context: 505 us, 1160 TFLOP/s; 500 tokens of 64 heads over
-//     e4m3 pages: 146 us (each token by itself 195).
+//     half; 1024 tokens of one context: 507 us, 1150 TFLOP/s; 500 tokens of 64 heads over
+//     e4m3 pages: 148 us (each token by itself 195).
 // Work split: a block costs its tiles plus `kPieceCost`; the costs of all
 // blocks form one run, which the clusters share evenly.  A cluster's piece that
 // is a whole block writes o_lat; a block cut by a cluster boundary leaves fp32

@@ -389,7 +389,9 @@ MLA_DEVINL Entry list_entry(const TcArgs& a, const Item& it, int t) {
   if (t >= it.n_tiles || x >= it.first) return none;
   if constexpr (kLists == kGroupLists) {
     const uint2 e = __ldg(a.group_lists + ((static_cast<int64_t>(it.slot) << a.gt_shift) * a.p.K + x));
-    return e.x < static_cast<uint32_t>(it.kend) ? Entry{static_cast<int32_t>(e.x), e.y} : none;
+    // (Where a cu that decreases made the walk take a slot that has no list, this is what lay
+    // there: still a whole block, so that what is loaded and prefetched ends in its page.)
+    return e.x < static_cast<uint32_t>(it.kend) ? Entry{static_cast<int32_t>(e.x) & -kBK, e.y} : none;
   }
   const int32_t e = __ldg(a.p.blocks + static_cast<int64_t>(it.slot) * a.p.K + x);
   return e >= 0 && e <= (it.kend - 1) / kBK ? Entry{e * kBK, 1u} : none;

@@ -731,6 +731,25 @@ def test_decreasing_offsets_are_reported(e4m3, H, n):
     check(b, attend(b, d, workspace=ws))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("word", [1, 63, 161, 299])
+def test_decreasing_offsets_read_no_lists_of_their_own(e4m3, word):
+    """A workspace in which every entry that is not written names a key within a block, and sequences of two tokens whose
+    pages are all of the pool."""
+    n, L, K, H = 60, 300, 64, 16
+    lists = [[t % 5, 4] for t in range(2 * n)]
+    b = Listed(47, e4m3, H, 64, [2] * n, [L] * n, K, lists=lists)
+    d = b.dev()
+    full, raw = full_table(b), torch.zeros_like(d["pages"].view(torch.uint8))
+    ws = torch.full((mla.mla_paged_workspace_size(H) // 4,), word, dtype=torch.int32, device="cuda").view(torch.uint8)
+    up, down = list(range(0, 2 * n + 1, 2)), list(range(2 * n, -1, -2))
+    for cu in (down, up[:31][::-1] + up[31:], [x ^ 2 for x in up[:-1]] + up[-1:], [x ^ 1 for x in up]):
+        attend(b, dict(d, cu_q=i32(cu), block_table=full, pages=raw.view(d["pages"].dtype).view(d["pages"].shape)), workspace=ws)
+        torch.cuda.synchronize()
+        assert mla.mla_get_device_error() == INVALID
+    check(b, attend(b, d, workspace=ws))
+
+
 def test_counts_outside_the_lists_of_a_group_are_reported():
     lists = [[t % 6] for t in range(600)]
     lists[:5] = [[0, 1, 2], [3], [1], [], [0, 4]]
